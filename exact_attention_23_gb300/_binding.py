@@ -28,7 +28,8 @@ FA_BWD_NOALLOC_SCRATCH_BYTES = 33554432
 # Every symbol include/fa.h declares.
 EXPORTS = ("fa_fwd", "fa_fwd_ex", "fa_fwd_fp8", "fa_fwd_host_workspace_size", "fa_fwd_host", "fa_fwd_kv_workspace_size", "fa_fwd_kv",
            "fa_fwd_block_sparse", "fa_bwd_workspace_size", "fa_bwd", "fa_bwd_ex",
-           "fa_bwd_noalloc", "fa_strerror", "fa_version")
+           "fa_bwd_noalloc", "fa_visible_size", "fa_visible", "fa_fwd_mod", "fa_bwd_mod", "fa_rope",
+           "fa_rope_append", "fa_strerror", "fa_version")
 
 _lock = threading.Lock()
 _lib = None
@@ -77,6 +78,21 @@ def lib() -> ctypes.CDLL:
             L.fa_bwd_ex.restype = i
             L.fa_bwd_noalloc.argtypes = [vp] * 9 + [i, i, i, i, i, f, vp]
             L.fa_bwd_noalloc.restype = i
+            L.fa_visible_size.argtypes = [i, i]
+            L.fa_visible_size.restype = sz
+            L.fa_visible.argtypes = [vp, vp, i, i, vp, sz, i, i, vp]
+            L.fa_visible.restype = i
+            ull, ll = ctypes.c_ulonglong, ctypes.c_longlong
+            L.fa_fwd_mod.argtypes = [vp] * 6 + [i, f, vp, i, i, i, i, i, f, vp, ull, vp]
+            L.fa_fwd_mod.restype = i
+            L.fa_bwd_mod.argtypes = [vp] * 10 + [sz, vp, i, f, vp, i, i, i, i, i, f, vp, ull, vp]
+            L.fa_bwd_mod.restype = i
+            src = [vp, ll, ll, ll]
+            L.fa_rope.argtypes = src + [vp] + src + [vp, vp, i, vp, i, i, i, f, i, i, i, i, i, vp]
+            L.fa_rope.restype = i
+            L.fa_rope_append.argtypes = (src + [vp] + src + src + [vp, vp, vp, vp, i, vp, i, i, f]
+                                         + [i] * 6 + [vp])
+            L.fa_rope_append.restype = i
             L.fa_strerror.argtypes = [i]
             L.fa_strerror.restype = ctypes.c_char_p
             L.fa_version.argtypes = []
@@ -155,3 +171,43 @@ def fa_fwd_host(q, k, v, o, lse, B, H, T, d, causal, scale, heads_per_chunk, ws,
                 stream) -> int:
     return lib().fa_fwd_host(q, k, v, o, lse, B, H, T, d, int(bool(causal)), float(scale),
                              heads_per_chunk, ws, ws_bytes, stream)
+
+
+def fa_visible_size(B, T) -> int:
+    return int(lib().fa_visible_size(B, T))
+
+
+def fa_visible(doc_ids, prefix_len, prefix_per_token, causal, visible, visible_bytes, B, T,
+               stream) -> int:
+    return lib().fa_visible(doc_ids, prefix_len, int(prefix_per_token), int(bool(causal)), visible,
+                            int(visible_bytes), B, T, stream)
+
+
+def fa_fwd_mod(q, k, v, o, lse, visible, causal, softcap, slopes, B, H, Hkv, T, d, scale, status,
+               timeout_ns, stream) -> int:
+    return lib().fa_fwd_mod(q, k, v, o, lse, visible, int(bool(causal)), float(softcap), slopes, B,
+                            H, Hkv, T, d, float(scale), status, int(timeout_ns), stream)
+
+
+def fa_bwd_mod(q, k, v, o, dout, lse, dq, dk, dv, workspace, workspace_bytes, visible, causal,
+               softcap, slopes, B, H, Hkv, T, d, scale, status, timeout_ns, stream) -> int:
+    return lib().fa_bwd_mod(q, k, v, o, dout, lse, dq, dk, dv, workspace, int(workspace_bytes),
+                            visible, int(bool(causal)), float(softcap), slopes, B, H, Hkv, T, d,
+                            float(scale), status, int(timeout_ns), stream)
+
+
+def fa_rope(q, q_strides, q_out, k, k_strides, k_out, positions, positions_per_batch, inv_freq,
+            rot_dim, interleaved, inverse, mscale, B, H, Hkv, T, d, stream) -> int:
+    """q_strides and k_strides: (batch, head, token), in elements."""
+    return lib().fa_rope(q, *q_strides, q_out, k, *k_strides, k_out, positions,
+                         int(positions_per_batch), inv_freq, rot_dim, int(interleaved),
+                         int(inverse), float(mscale), B, H, Hkv, T, d, stream)
+
+
+def fa_rope_append(q, q_strides, q_out, k, k_strides, v, v_strides, k_cache, v_cache, ctx_len,
+                   positions, positions_per_batch, inv_freq, rot_dim, interleaved, mscale, B, H,
+                   Hkv, Tq, Tmax, d, stream) -> int:
+    return lib().fa_rope_append(q, *q_strides, q_out, k, *k_strides, v, *v_strides, k_cache,
+                                v_cache, ctx_len, positions, int(positions_per_batch), inv_freq,
+                                rot_dim, int(interleaved), float(mscale), B, H, Hkv, Tq, Tmax, d,
+                                stream)

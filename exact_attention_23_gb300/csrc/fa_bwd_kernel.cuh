@@ -49,6 +49,7 @@
 // [384,448) dQ, [448,512) Pᵀ (bf16 pairs).
 #pragma once
 
+#include "fa_mod.cuh"
 #include "sm103.cuh"
 
 // Timeline hooks: compiled out unless a tracing build defines FA_TRACE(tag, step).
@@ -63,7 +64,7 @@ namespace fa {
 // Query tiles have kBQ rows: 128 at d = 64; 64 at d = 128, where 128-column Sᵀ, dPᵀ, dV and
 // dK would already fill the 512 TMEM columns. With 64-query tiles every product keeps
 // M = 128: dQ is then made transposed, dQᵀ = Kᵀ·dSᵀ (head dims on TMEM lanes, N = 64).
-template <int D>
+template <int D, int MOD = 0>
 struct BwdCfg {
   static_assert(D == 64 || D == 128, "head dim");
   static constexpr int kBQ = (D == 64) ? 128 : 64;    // query rows per tile
@@ -91,7 +92,8 @@ struct BwdCfg {
   static constexpr int kStageBytes = 2 * kQTile;
   static constexpr int kDS = kStage0 + kStages * kStageBytes;  // dSᵀ: 2 buffers
   static constexpr int kDSBytes = 128 * kBQ * 2;      // [128 keys][kBQ queries] bf16, 64-col boxes
-  static constexpr int kVecBytes = 2 * kBQ * 4;       // per stage: −lse2[kBQ] then D[kBQ]
+  // per stage: −lse2[kBQ] then D[kBQ], and (MOD) the rows' visible intervals [lo, hi)
+  static constexpr int kVecBytes = (MOD ? 4 : 2) * kBQ * 4;
   static constexpr int kVec = kDS + 2 * kDSBytes;
   // Each dQ drain warp stages 16 of its TMEM columns for its 32 lanes (2 KB) for a bulk
   // reduce-add, two buffers per warp.
@@ -126,8 +128,23 @@ struct BwdBars {
   uint64_t grad_done;   // every MMA of the gradient issuer done: dK, dV final
   uint32_t tmem_base;
   uint32_t abort;
+  uint32_t whole[3];    // MOD: the stage's rows all see every key of this CTA's tile
 };
 static_assert(sizeof(BwdBars) <= 256, "barrier block");
+
+// Modified scores (MOD instantiations; see fa_mod.cuh). K, V, dK and dV then have one head for
+// every `group` query heads: the CTA of a key tile walks the query tiles of all of them, so a
+// shared head's gradient is summed in its accumulators, with no second pass.
+struct BwdModParams {
+  const int2* rows;     // [B][T_pad] visible key interval of each query row, or null
+  const int4* units;    // [B][n_kt] (key tile, first 128-row query tile, past the last, rows in use)
+  const int2* whole;    // [B][n_kt] (largest lo, smallest hi) over a 128-row query tile
+  const float* slopes;  // [H]
+  int Hkv;              // key heads
+  int group;            // query heads per key head
+  CapFactors cap;       // (CAP)
+  int causal;           // without rows
+};
 
 struct BwdParams {
   __nv_bfloat16* dk;
@@ -146,6 +163,7 @@ struct BwdParams {
   float scale_log2;    // scale · log2(e)
   uint64_t timeout_ns;
   uint32_t flags;
+  BwdModParams mod;    // MOD kernels only (BH then counts B·Hkv)
 };
 
 constexpr uint32_t kBwdFlagStarveQ = 1u;  // FA_FLAG_TEST_STARVE_Q
@@ -190,7 +208,9 @@ __host__ __device__ __forceinline__ size_t dq_acc_offset_t(int bh, int i, int n_
 // it in a packed fp32x2 FMA); zero the dQ accumulator.
 // D/8 consecutive lanes share a row, each reading 8 columns (16 bytes) of O and dO.
 // ------------------------------------------------------------------------------------
-template <int D>
+// MOD: a row that saw no key (lse = −∞) gets −∞ and D = 0, so that its P and dS are 0 whatever
+// its o and dO hold.
+template <int D, bool MOD = false>
 __global__ void __launch_bounds__(256) fa_bwd_prep_kernel(const __nv_bfloat16* __restrict__ o,
                                                           const __nv_bfloat16* __restrict__ dout,
                                                           const float* __restrict__ lse,
@@ -227,7 +247,14 @@ __global__ void __launch_bounds__(256) fa_bwd_prep_kernel(const __nv_bfloat16* _
     }
 #pragma unroll
     for (int w = L / 2; w > 0; w >>= 1) acc += __shfl_xor_sync(0xffffffffu, acc, w);
-    if (c == 0) {
+    if (MOD) {
+      if (c == 0) {
+        const float ls = (t < T) ? lse[(size_t)bh * T + t] : __int_as_float(0xff800000);
+        const bool none = ls == __int_as_float(0xff800000);
+        dvec[row] = none ? 0.f : acc;
+        lse2[row] = none ? ls : ls * -1.4426950408889634f;
+      }
+    } else if (c == 0) {
       dvec[row] = (t < T) ? acc : 0.f;
       lse2[row] = (t < T) ? lse[(size_t)bh * T + t] * -1.4426950408889634f : __int_as_float(0xff800000);
     }
@@ -315,12 +342,12 @@ __device__ __forceinline__ void st_row_chunk_sw128(uint32_t box, int r, int ch, 
                pack_bf16x2(x[6], x[7]));
 }
 
-template <int D, bool CAUSAL>
-__global__ void __launch_bounds__(BwdCfg<D>::kThreads, 1)
+template <int D, bool CAUSAL, int MOD = 0>
+__global__ void __launch_bounds__(BwdCfg<D, MOD>::kThreads, 1)
     fa_bwd_main_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
                        const __grid_constant__ CUtensorMap tm_v, const __grid_constant__ CUtensorMap tm_do,
                        const BwdParams p) {
-  using C = BwdCfg<D>;
+  using C = BwdCfg<D, MOD>;
   constexpr int NS = C::kStages;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* sm = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
@@ -334,10 +361,12 @@ __global__ void __launch_bounds__(BwdCfg<D>::kThreads, 1)
   const int grp = blockIdx.x / per_group;
   const int within = blockIdx.x - grp * per_group;
   const int gsize = min(p.head_group, p.BH - grp * p.head_group);
-  const int j = within / gsize;
-  const int bh = grp * p.head_group + within % gsize;
-  const int i0 = CAUSAL ? (j * 128) / C::kBQ : 0;
-  const int n = p.n_qt - i0;
+  int j = within / gsize;
+  const int bh = grp * p.head_group + within % gsize;  // (MOD: the key head's index)
+  int i0 = CAUSAL ? (j * 128) / C::kBQ : 0;
+  int n = p.n_qt - i0;
+  // MOD: the walk is the query tiles i0 … i0 + n_i − 1 of each of the key head's query heads
+  int n_i = n, used = p.T_pad, hk0 = 0;
 
   if (threadIdx.x == 0) {
     mbar_init(&bars->kv_full, 1);
@@ -374,6 +403,22 @@ __global__ void __launch_bounds__(BwdCfg<D>::kThreads, 1)
   // (No early trigger for the dQ conversion: letting it be scheduled during this grid's
   // last wave measured 5 % slower at d = 128.)
   pdl_wait();
+  if constexpr (MOD != 0) {
+    constexpr int kPer = 128 / C::kBQ;  // query tiles in 128 rows
+    const int b = bh / p.mod.Hkv;
+    hk0 = (bh - b * p.mod.Hkv) * p.mod.group;
+    if (p.mod.units) {
+      const int4 rec = __ldg(p.mod.units + (size_t)b * p.n_kt + j);
+      j = rec.x;
+      i0 = rec.y * kPer;
+      n_i = max(0, rec.z * kPer - i0);
+      used = rec.w;
+    } else if (p.mod.causal) {
+      i0 = j * kPer;
+      n_i = p.n_qt - i0;
+    }
+    n = n_i * p.mod.group;
+  }
   const uint32_t tmem = bars->tmem_base;
   const WaitCtl wc{&bars->abort, p.status, p.timeout_ns};
   const WaitCtl drain_wc = drain_ctl(p.timeout_ns);
@@ -428,18 +473,38 @@ __global__ void __launch_bounds__(BwdCfg<D>::kThreads, 1)
     for (int t = 0, st = 0, ph = 0; t < n && !starve; ++t) {
       if (t >= NS && !mbar_wait_warp_inl(&bars->q_empty[st], ph ^ 1, wc)) break;
       FA_TRACE(30, t);
+      int i = i0 + t, bq = bh;  // query tile and (b·h) of this step
+      if constexpr (MOD != 0) {
+        const int hg = t / n_i;
+        i = i0 + t - hg * n_i;
+        bq = bh * p.mod.group + hg;
+      }
       if (lane == 0) {
-        const int i = i0 + t;
         uint8_t* stage = sm + C::kStage0 + st * C::kStageBytes;
         float* vec = reinterpret_cast<float*>(sm + C::kVec + st * C::kVecBytes);
-        mbar_arrive_expect_tx(&bars->q_full[st], 2 * C::kQTile + C::kVecBytes);
+        if constexpr (MOD != 0) {
+          uint32_t vec_bytes = C::kVecBytes / 2;
+          if (p.mod.rows) {
+            const int b = bh / p.mod.Hkv;
+            const int2 w = __ldg(p.mod.whole + (size_t)b * p.n_kt + i * C::kBQ / 128);
+            bars->whole[st] = (w.x <= j * 128 && w.y >= j * 128 + 128) ? 1u : 0u;
+            vec_bytes = C::kVecBytes;
+          }
+          mbar_arrive_expect_tx(&bars->q_full[st], 2 * C::kQTile + vec_bytes);
+          if (p.mod.rows)
+            bulk_load(vec + 2 * C::kBQ,
+                      p.mod.rows + (size_t)(bh / p.mod.Hkv) * p.T_pad + (size_t)i * C::kBQ,
+                      C::kBQ * 8, &bars->q_full[st]);
+        } else {
+          mbar_arrive_expect_tx(&bars->q_full[st], 2 * C::kQTile + C::kVecBytes);
+        }
 #pragma unroll
         for (int b = 0; b < D / 64; ++b) {
-          tma_load_3d(stage + b * C::kQBox, &tm_q, &bars->q_full[st], b * 64, i * C::kBQ, bh);
+          tma_load_3d(stage + b * C::kQBox, &tm_q, &bars->q_full[st], b * 64, i * C::kBQ, bq);
           tma_load_3d(stage + C::kQTile + b * C::kQBox, &tm_do, &bars->q_full[st], b * 64,
-                      i * C::kBQ, bh);
+                      i * C::kBQ, bq);
         }
-        const size_t row0 = (size_t)bh * p.T_pad + (size_t)i * C::kBQ;
+        const size_t row0 = (size_t)bq * p.T_pad + (size_t)i * C::kBQ;
         bulk_load(vec, p.lse2 + row0, C::kBQ * 4, &bars->q_full[st]);
         bulk_load(vec + C::kBQ, p.dvec + row0, C::kBQ * 4, &bars->q_full[st]);
       }
@@ -457,10 +522,39 @@ __global__ void __launch_bounds__(BwdCfg<D>::kThreads, 1)
     constexpr uint32_t kIdS = idesc_bf16(128, C::kBQ, false);  // Sᵀ = K·Qᵀ, dPᵀ = V·dOᵀ
     const uint32_t k_s = sbase + C::kK, v_s = sbase + C::kV;
     bool ok = mbar_wait_warp_inl(&bars->kv_full, 0, wc);
+    // MOD: rows behind the last one in use (padding) may hold anything. Their P and dS are 0,
+    // but 0 · NaN must not reach a product: their K, V, Q and dO rows are zeroed here, before the
+    // first product that reads them (every other reader comes after it).
+    auto zero_rows = [&](uint32_t box, int first, int rows) {
+      for (int x = max(first, 0) * 8 + lane; x < rows * 8; x += 32) st_shared_v4(box + x * 16, 0u, 0u, 0u, 0u);
+    };
+    if constexpr (MOD != 0) {
+      if (ok && used < j * 128 + 128) {
+#pragma unroll
+        for (int b = 0; b < D / 64; ++b) {
+          zero_rows(k_s + b * C::kBox, used - j * 128, 128);
+          zero_rows(v_s + b * C::kBox, used - j * 128, 128);
+        }
+        fence_proxy_async_smem();
+        __syncwarp();
+      }
+    }
     for (int t = 0, st = 0, ph = 0; t < n && ok; ++t) {
       if (!(ok = mbar_wait_warp_inl(&bars->q_full[st], ph, wc))) break;
       if (t > 0 && !(ok = mbar_wait_warp_inl(&bars->s_free, (t - 1) & 1, wc))) break;
       FA_TRACE(1, t);
+      if constexpr (MOD != 0) {
+        const int i = i0 + t % n_i;
+        if (used < (i + 1) * C::kBQ) {
+#pragma unroll
+          for (int b = 0; b < D / 64; ++b) {
+            zero_rows(q_s(st) + b * C::kQBox, used - i * C::kBQ, C::kBQ);
+            zero_rows(do_s(st) + b * C::kQBox, used - i * C::kBQ, C::kBQ);
+          }
+          fence_proxy_async_smem();
+          __syncwarp();
+        }
+      }
       tc_fence_after_sync();
       if (lane == 0) {
 #pragma unroll
@@ -583,6 +677,12 @@ __global__ void __launch_bounds__(BwdCfg<D>::kThreads, 1)
     for (; t < n; ++t) {
       if (!(ok = mbar_wait_warp_inl(&bars->dq_full, t & 1, wc))) break;
       FA_TRACE(20, t);
+      int it = i0 + t, bq = bh;
+      if constexpr (MOD != 0) {
+        const int hg = t / n_i;
+        it = i0 + t - hg * n_i;
+        bq = bh * p.mod.group + hg;
+      }
       tc_fence_after_sync();
       // 32 columns at a time; the buffer is released once the last columns are in registers.
 #pragma unroll
@@ -614,8 +714,8 @@ __global__ void __launch_bounds__(BwdCfg<D>::kThreads, 1)
             if (lane == 0) {
               // TMEM columns 32h + 16k2 …: column group 8h + 4k2 of lanes 32·qd …
               const int cg = 8 * h + 4 * k2;
-              bulk_reduce_add_f32(p.dq_acc + ((D == 64) ? dq_acc_offset(bh, i0 + t, p.n_qt, cg, qd * 32, D)
-                                                        : dq_acc_offset_t(bh, i0 + t, p.n_qt, cg, qd * 32)),
+              bulk_reduce_add_f32(p.dq_acc + ((D == 64) ? dq_acc_offset(bq, it, p.n_qt, cg, qd * 32, D)
+                                                        : dq_acc_offset_t(bq, it, p.n_qt, cg, qd * 32)),
                                   buf, C::kDQChunk);
               bulk_commit_group();
             }
@@ -627,9 +727,14 @@ __global__ void __launch_bounds__(BwdCfg<D>::kThreads, 1)
       // Abandoned tiles: poison their dQ rows so that the failure cannot go unseen.
       const float nan = __int_as_float(0x7fc00000);
       for (; t < n; ++t) {
+        int it = i0 + t, bq = bh;
+        if constexpr (MOD != 0) {
+          it = i0 + t % n_i;
+          bq = bh * p.mod.group + t / n_i;
+        }
         for (int c4 = 0; c4 < 16; ++c4) {
-          float* dst = p.dq_acc + ((D == 64) ? dq_acc_offset(bh, i0 + t, p.n_qt, c4, r, D)
-                                             : dq_acc_offset_t(bh, i0 + t, p.n_qt, c4, r));
+          float* dst = p.dq_acc + ((D == 64) ? dq_acc_offset(bq, it, p.n_qt, c4, r, D)
+                                             : dq_acc_offset_t(bq, it, p.n_qt, c4, r));
           red_add_v4(dst, nan, nan, nan, nan);
         }
       }
@@ -648,8 +753,13 @@ __global__ void __launch_bounds__(BwdCfg<D>::kThreads, 1)
     // dSᵀ columns of this warpgroup: box (NC·g)/64, 16-byte chunks from ((NC·g) mod 64)/8
     const int ds_box_idx = (NC * g) / 64, ds_chunk0 = ((NC * g) % 64) / 8;
     bool ok = true;
+    int hg = 0, ti = 0;  // MOD: the step's query head within the group, and its tile within the walk
+    float nslope = 0.f;
     for (int t = 0, st = 0, ph = 0; t < n && ok; ++t) {
-      const int i = i0 + t;
+      const int i = MOD != 0 ? i0 + ti : i0 + t;
+      if constexpr ((MOD & kModBias) != 0) {
+        if (ti == 0) nslope = __ldg(p.mod.slopes + hk0 + hg) * -1.4426950408889634f;
+      }
       const float* vec = reinterpret_cast<const float*>(sm + C::kVec + st * C::kVecBytes);
       if (!(ok = mbar_wait_warp_inl(&bars->q_full[st], ph, wc))) break;
       if (!(ok = mbar_wait_warp_inl(&bars->s_full, t & 1, wc))) break;
@@ -663,8 +773,62 @@ __global__ void __launch_bounds__(BwdCfg<D>::kThreads, 1)
       // Pᵀ = exp2(S·scale·log2e − log2e·LSE_q), zero where the key comes after the query
       // (the argument on fp32 pairs; the workspace holds −log2e·LSE)
       float pr[NC];
+      uint32_t pkm[MOD != 0 ? NC / 2 : 1];  // MOD: Pᵀ's pairs, packed as they are made
       const float4* l4 = reinterpret_cast<const float4*>(vec + g * NC);
       const uint64_t c2 = f2_pack(p.scale_log2, p.scale_log2);
+      if constexpr (MOD != 0) {
+        // The modified scores' P, packed at once; pr keeps P · (1 − tanh²), what dS multiplies.
+        const int q0 = i * C::kBQ + g * NC, key = j * 128 + r;
+        bool part;  // some row of the stage does not see every key of the tile
+        if (p.mod.rows) part = bars->whole[st] == 0u;
+        else part = p.mod.causal && j * 128 + 127 > i * C::kBQ;
+        const bool left = j * 128 + qd * 32 + 31 <= q0;
+        const float dist0 = static_cast<float>(q0 - key);
+        const float base = nslope * dist0;
+        const float2* l2 = reinterpret_cast<const float2*>(vec + g * NC);
+        const int2* iv = reinterpret_cast<const int2*>(vec + 2 * C::kBQ) + g * NC;
+        bool far = false;
+        if constexpr ((MOD & kModCap) != 0) far = cap_far<NC>(s, p.mod.cap.limit);
+#pragma unroll
+        for (int c = 0; c < NC; c += 2) {
+          const float2 l = l2[c / 2];
+          uint64_t x2 = f2_pack(l.x, l.y), f2 = 0ull;
+          const uint64_t s2 = f2_pack(__uint_as_float(s[c]), __uint_as_float(s[c + 1]));
+          if constexpr ((MOD & kModBias) != 0) {
+            const float c0 = static_cast<float>(c), c1 = static_cast<float>(c + 1);
+            x2 = f2_add(x2, left ? f2_pack(fmaf(nslope, c0, base), fmaf(nslope, c1, base))
+                                 : f2_pack(nslope * fabsf(dist0 + c0), nslope * fabsf(dist0 + c1)));
+          }
+          if constexpr ((MOD & kModCap) != 0) {
+            const uint64_t th = cap_tanh2(__uint_as_float(s[c]), __uint_as_float(s[c + 1]), p.mod.cap, far);
+            x2 = f2_fma(th, f2_splat(p.mod.cap.out), x2);
+            f2 = f2_fma(f2_mul(th, f2_splat(-1.0f)), th, f2_splat(1.0f));
+          } else {
+            x2 = f2_fma(s2, c2, x2);
+          }
+          float x[2], f[2];
+          f2_unpack(x2, x[0], x[1]);
+          f2_unpack(f2, f[0], f[1]);
+          if (part) {
+            if (p.mod.rows) {
+              const int2 v0 = iv[c], v1 = iv[c + 1];
+              if (key < v0.x || key >= v0.y) x[0] = __int_as_float(0xff800000);
+              if (key < v1.x || key >= v1.y) x[1] = __int_as_float(0xff800000);
+            } else {
+              if (key > q0 + c) x[0] = __int_as_float(0xff800000);
+              if (key > q0 + c + 1) x[1] = __int_as_float(0xff800000);
+            }
+          }
+          const float p0 = ex2_approx(x[0]), p1 = ex2_approx(x[1]);
+          pkm[c / 2] = pack_bf16x2(p0, p1);
+          pr[c] = (MOD & kModCap) != 0 ? p0 * f[0] : p0;
+          pr[c + 1] = (MOD & kModCap) != 0 ? p1 * f[1] : p1;
+        }
+        if (++ti == n_i) {
+          ti = 0;
+          ++hg;
+        }
+      } else {
 #pragma unroll
       for (int c = 0; c < NC; c += 4) {
         const float4 l = l4[c / 4];
@@ -684,12 +848,13 @@ __global__ void __launch_bounds__(BwdCfg<D>::kThreads, 1)
         for (int c = 0; c < NC; ++c)
           if (rel > c) pr[c] = 0.f;
       }
+      }
       FA_TRACE(11, t);
       if (t >= 1 && !(ok = mbar_wait_warp_inl(&bars->p_free, (t - 1) & 1, wc))) break;
       FA_TRACE(12, t);
       uint32_t pk[NC / 2];
 #pragma unroll
-      for (int c = 0; c < NC / 2; ++c) pk[c] = pack_bf16x2(pr[2 * c], pr[2 * c + 1]);
+      for (int c = 0; c < NC / 2; ++c) pk[c] = MOD != 0 ? pkm[c % (MOD != 0 ? NC / 2 : 1)] : pack_bf16x2(pr[2 * c], pr[2 * c + 1]);
       tc_fence_after_sync();
       if constexpr (NC == 64) tmem_st32(tmem + lane_off + C::kColP + g * 32, pk);
       else if constexpr (NC == 32) tmem_st16(tmem + lane_off + C::kColP + g * 16, pk);
@@ -774,6 +939,10 @@ __global__ void __launch_bounds__(BwdCfg<D>::kThreads, 1)
           float y[8];
 #pragma unroll
           for (int e = 0; e < 8; ++e) y[e] = done ? __uint_as_float(x[c + e]) * mul : nan;
+          if (MOD != 0 && n == 0) {  // a key tile that no query sees
+#pragma unroll
+            for (int e = 0; e < 8; ++e) y[e] = 0.f;
+          }
           uint4 v;
           v.x = pack_bf16x2(y[0], y[1]);
           v.y = pack_bf16x2(y[2], y[3]);

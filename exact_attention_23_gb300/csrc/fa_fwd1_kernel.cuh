@@ -50,6 +50,7 @@
 #pragma once
 
 #include "fa_fwd_kernel.cuh"
+#include "fa_mod.cuh"
 
 // Timeline hooks: compiled out unless a tracing build defines FA1_TRACE(tag, step).
 #ifndef FA1_TRACE
@@ -115,7 +116,41 @@ struct Bars1 {
 };
 static_assert(sizeof(Bars1) <= 512, "barrier block");
 
-template <int D, bool CAUSAL, bool GEN = false>
+// The unit at position L of the list. MOD: a unit is (query head, query tile) with one contiguous
+// range of K tiles, from the visibility's records (heaviest tile first) or, without them, the
+// causal or full range, the last tile first.
+template <bool CAUSAL, bool GEN, int MOD>
+__device__ __forceinline__ Unit unit1_of(const FwdParams& p, int L) {
+  if constexpr (MOD != 0) {
+    Unit u;
+    const int pos = static_cast<int>(p.div_bh.div(static_cast<uint32_t>(L)));
+    u.bh = L - pos * p.BH;
+    u.split = 0;
+    if (p.mod.units) {
+      const int b = static_cast<int>(p.mod.div_h.div(static_cast<uint32_t>(u.bh)));
+      const int4 r = __ldg(p.mod.units + static_cast<size_t>(b) * p.n_qt + pos);
+      u.qt0 = r.x;
+      u.kb = r.y;
+      u.ke = r.z;
+      u.mh = r.w;
+    } else {
+      u.qt0 = p.n_qt - 1 - pos;
+      u.kb = 0;
+      u.ke = p.mod.causal ? u.qt0 + 1 : p.n_kv;
+      u.mh = p.n_kv * kBlockN;  // (rows past Tk are loaded as zeros)
+    }
+    u.n_steps = max(0, u.ke - u.kb);
+    u.nkv[0] = u.n_steps;
+    u.nkv[1] = 0;
+    u.last[0] = u.last[1] = 0;
+    return u;
+  } else {
+    return unit_of<CAUSAL, GEN>(p, L);
+  }
+}
+
+// MOD (bits kMod…): modified scores; always with GEN (rows may see no key) and CAUSAL false.
+template <int D, bool CAUSAL, bool GEN = false, int MOD = 0>
 __global__ void __launch_bounds__(Cfg1<D>::kThreads, 1)
     fa_fwd1_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
                    const __grid_constant__ CUtensorMap tm_v, const __grid_constant__ CUtensorMap tm_o,
@@ -188,7 +223,7 @@ __global__ void __launch_bounds__(Cfg1<D>::kThreads, 1)
     for (int r = 0; ok && r * grid < p.total_units; ++r) {
       const int L = unit_index(r, cta, grid);
       if (L >= p.total_units) continue;
-      const Unit u = unit_of<CAUSAL, GEN>(p, L);
+      const Unit u = unit1_of<CAUSAL, GEN, MOD>(p, L);
       const int qb = qn & 1;
       if (qn >= 2 && !mbar_wait_warp(&bars->q_empty[qb], ((qn >> 1) - 1) & 1, wc)) { ok = false; break; }
       const bool load = load_q && (later_q || qn == 0);
@@ -204,6 +239,8 @@ __global__ void __launch_bounds__(Cfg1<D>::kThreads, 1)
       ++qn;
       UnitSteps<CAUSAL, GEN> us;
       us.begin(p, u);
+      int kvh = u.bh;  // the key head this query head reads
+      if constexpr (MOD != 0) kvh = static_cast<int>(p.mod.div_g.div(static_cast<uint32_t>(u.bh)));
       for (int j = 0; j < u.n_steps; ++j, ++g) {
         us.next(u, j);
         const int kt = us.kt;
@@ -215,12 +252,12 @@ __global__ void __launch_bounds__(Cfg1<D>::kThreads, 1)
 #pragma unroll
           for (int s = 0; s < C::kSub; ++s)
             tma_load_3d_hint(smem + C::kKOff + st * C::kTileBytes + s * C::kSubBytes, &tm_k,
-                             &bars->k_full[st], s * 64, kt * kBlockN, u.bh, keep);
+                             &bars->k_full[st], s * 64, kt * kBlockN, kvh, keep);
           mbar_arrive_expect_tx(&bars->v_full[st], C::kTileBytes);
 #pragma unroll
           for (int s = 0; s < C::kSub; ++s)
             tma_load_3d_hint(smem + C::kVOff + st * C::kTileBytes + s * C::kSubBytes, &tm_v,
-                             &bars->v_full[st], s * 64, kt * kBlockN, u.bh, keep);
+                             &bars->v_full[st], s * 64, kt * kBlockN, kvh, keep);
         }
         __syncwarp();
       }
@@ -253,7 +290,7 @@ __global__ void __launch_bounds__(Cfg1<D>::kThreads, 1)
       for (int r = 0; ok && r * grid < p.total_units; ++r) {
         const int L = unit_index(r, cta, grid);
         if (L >= p.total_units) continue;
-        const Unit u = unit_of<CAUSAL, GEN>(p, L);
+        const Unit u = unit1_of<CAUSAL, GEN, MOD>(p, L);
         const int qb = qn & 1;
         if (!mbar_wait_warp(&bars->q_full[qb], (qn >> 1) & 1, wc)) { ok = false; break; }
         for (int j = 0; j < u.n_steps; ++j, ++g) {
@@ -295,7 +332,7 @@ __global__ void __launch_bounds__(Cfg1<D>::kThreads, 1)
       for (int r = 0; ok && r * grid < p.total_units; ++r) {
         const int L = unit_index(r, cta, grid);
         if (L >= p.total_units) continue;
-        const Unit u = unit_of<CAUSAL, GEN>(p, L);
+        const Unit u = unit1_of<CAUSAL, GEN, MOD>(p, L);
         for (int j = 0; j < u.n_steps; ++j, ++g) {
           const int st = g % C::kStages;
           const int b = g & 1;
@@ -309,6 +346,19 @@ __global__ void __launch_bounds__(Cfg1<D>::kThreads, 1)
             break;
           }
           tc_fence_after_sync();
+          if constexpr (MOD != 0) {
+            // Keys that no query of the sequence sees and that lie behind all that some query
+            // does may hold anything (padding): their P is 0, and 0 · NaN must not reach O.
+            const int used = u.mh - (u.kb + j) * kBlockN;
+            if (used < kBlockN) {
+              for (int x = used * 8 + lane; x < kBlockN * 8; x += 32)
+#pragma unroll
+                for (int s = 0; s < C::kSub; ++s)
+                  st_shared_v4(v_base + st * C::kTileBytes + s * C::kSubBytes + x * 16, 0u, 0u, 0u, 0u);
+              fence_proxy_async_smem();
+              __syncwarp();
+            }
+          }
           if (leader) {
             const uint32_t va = v_base + st * C::kTileBytes;
 #pragma unroll
@@ -541,7 +591,7 @@ __global__ void __launch_bounds__(Cfg1<D>::kThreads, 1)
     for (int r = 0; r * grid < p.total_units; ++r) {
       const int L = unit_index(r, cta, grid);
       if (L >= p.total_units) continue;
-      const Unit u = unit_of<CAUSAL, GEN>(p, L);
+      const Unit u = unit1_of<CAUSAL, GEN, MOD>(p, L);
       const int n = u.nkv[0];
       const int qt = u.qt0;
       const int q_row = qt * kBlockM + row;
@@ -556,6 +606,21 @@ __global__ void __launch_bounds__(Cfg1<D>::kThreads, 1)
         write_const_row(cur, 0u);
         write_lse(cur, -INFINITY);
         continue;
+      }
+      // MOD: this row's visible keys [lo, hi) and (BIAS) its head's slope in base 2, negated
+      int vlo = 0, vhi = 0;
+      float nslope = 0.0f;
+      if constexpr (MOD != 0) {
+        const int b = static_cast<int>(p.mod.div_h.div(static_cast<uint32_t>(u.bh)));
+        if (p.mod.rows) {
+          const int2 r = __ldg(p.mod.rows + static_cast<size_t>(b) * p.mod.T_pad + q_row);
+          vlo = r.x;
+          vhi = r.y;
+        } else {
+          vhi = p.mod.causal ? min(q_row + 1, p.Tk) : p.Tk;
+        }
+        if constexpr ((MOD & kModBias) != 0)
+          nslope = __ldg(p.mod.slopes + (u.bh - b * p.mod.H)) * -1.4426950408889634f;
       }
       float m_ref = -INFINITY;  // reference max (base-2 scaled units) shared by O_h and l
       float l = 0.0f;
@@ -583,7 +648,10 @@ __global__ void __launch_bounds__(Cfg1<D>::kThreads, 1)
         // form: after query + Tk − Tq).
         int lim;
         bool masked;
-        if constexpr (GEN) {
+        if constexpr (MOD != 0) {
+          lim = vhi - k0;
+          masked = lim < kC || vlo > k0;
+        } else if constexpr (GEN) {
           lim = (CAUSAL ? min(q_row + 1 + p.kv_off, p.Tk) : p.Tk) - k0;
           masked = lim < kC;
         } else {
@@ -602,7 +670,44 @@ __global__ void __launch_bounds__(Cfg1<D>::kThreads, 1)
         __syncwarp();
         if (lane == 0) mbar_arrive(&bars->s_free[b]);
         FA1_TRACE(20, j);
-        if (masked) {
+        if constexpr (MOD != 0) {
+          // Scores to base-2 exponents in place (fa_mod.cuh); the bias is linear in the key
+          // where every key of the step lies at or before the warp's first row.
+          const bool left = k0 + kC - 1 <= qt * kBlockM + quad * 32;
+          const float dist0 = static_cast<float>(q_row - k0);
+          const float base = nslope * dist0;
+          bool far = false;
+          if constexpr ((MOD & kModCap) != 0) far = cap_far<kC>(s, p.mod.cap.limit);
+          auto to_exponents = [&](bool far_) {
+#pragma unroll
+            for (int t = 0; t < kC; t += 2) {
+              uint64_t add = 0ull, x2;
+              if constexpr ((MOD & kModBias) != 0) {
+                const float t0 = static_cast<float>(t), t1 = static_cast<float>(t + 1);
+                add = left ? f2_pack(fmaf(-nslope, t0, base), fmaf(-nslope, t1, base))
+                           : f2_pack(nslope * fabsf(dist0 - t0), nslope * fabsf(dist0 - t1));
+              }
+              if constexpr ((MOD & kModCap) != 0)
+                x2 = f2_fma(cap_tanh2(u2f(s[t]), u2f(s[t + 1]), p.mod.cap, far_), f2_splat(p.mod.cap.out), add);
+              else if constexpr ((MOD & kModBias) != 0)
+                x2 = f2_fma(f2_pack(u2f(s[t]), u2f(s[t + 1])), f2_splat(c), add);
+              else
+                x2 = f2_mul(f2_pack(u2f(s[t]), u2f(s[t + 1])), f2_splat(c));
+              float x0, x1;
+              f2_unpack(x2, x0, x1);
+              s[t] = __float_as_uint(x0);
+              s[t + 1] = __float_as_uint(x1);
+            }
+          };
+          if (far) to_exponents(true);
+          else to_exponents(false);
+          if (masked) {
+            const int vl = vlo - k0;
+#pragma unroll
+            for (int t = 0; t < kC; ++t)
+              if (t >= lim || t < vl) s[t] = __float_as_uint(-INFINITY);
+          }
+        } else if (masked) {
 #pragma unroll
           for (int t = 0; t < kC; ++t)
             if (t >= lim) s[t] = __float_as_uint(-INFINITY);
@@ -615,7 +720,8 @@ __global__ void __launch_bounds__(Cfg1<D>::kThreads, 1)
 #pragma unroll
           for (int a = 0; a < 8; ++a) mx[a] = fmax3(mx[a], u2f(s[t + 2 * a]), u2f(s[t + 2 * a + 1]));
         const float m_tile =
-            fmax3(fmax3(mx[0], mx[1], mx[2]), fmax3(mx[3], mx[4], mx[5]), fmaxf(mx[6], mx[7])) * c;
+            fmax3(fmax3(mx[0], mx[1], mx[2]), fmax3(mx[3], mx[4], mx[5]), fmaxf(mx[6], mx[7])) *
+            (MOD != 0 ? 1.0f : c);  // (MOD: already base-2 exponents)
 
         float alpha = 1.0f;
         bool rescale = false;
@@ -640,7 +746,8 @@ __global__ void __launch_bounds__(Cfg1<D>::kThreads, 1)
         uint32_t pk[kC / 2];
 #pragma unroll
         for (int t = 0; t < kC / 2; ++t) {
-          const uint64_t x2 = f2_fma(f2_pack(u2f(s[2 * t]), u2f(s[2 * t + 1])), c2, nm2);
+          const uint64_t s2 = f2_pack(u2f(s[2 * t]), u2f(s[2 * t + 1]));
+          const uint64_t x2 = MOD != 0 ? f2_add(s2, nm2) : f2_fma(s2, c2, nm2);
           float x0, x1;
           f2_unpack(x2, x0, x1);
           const float p0 = ex2_approx(x0);

@@ -43,6 +43,7 @@
 // halves of the keys. (Both are described where they happen.)
 #pragma once
 
+#include "fa_mod.cuh"
 #include "sm103.cuh"
 
 // Timeline hooks: compiled out unless a tracing build defines FA_TRACE(tag, step).
@@ -140,6 +141,19 @@ struct FastDiv {
   }
 };
 
+// Modified scores (the one-tile kernel's MOD instantiations; see fa_mod.cuh).
+struct ModParams {
+  const int2* rows;     // [B][T_pad] visible key interval [lo, hi) of each query row, or null
+  const int4* units;    // [B][n_t] (query tile, first K tile, past the last, keys in use)
+  const float* slopes;  // [H] distance-bias slopes (BIAS)
+  int T_pad;            // ceil(T/128) · 128
+  int H;                // query heads
+  FastDiv div_h;        // bh / H = batch
+  FastDiv div_g;        // bh / (H / Hkv) = the key head's index
+  CapFactors cap;       // (CAP)
+  int causal;           // without rows: key j visible to query i iff j ≤ i (else every key)
+};
+
 struct FwdParams {
   __nv_bfloat16* o;
   float* lse;
@@ -167,6 +181,7 @@ struct FwdParams {
   int bmask_heads;    // 1 (shared) or BH
   float* o_part;      // n_splits > 1: [n_splits][BH][Tq][D] fp32 normalised partial O
   float* lse_part;    // n_splits > 1: [n_splits][BH][Tq] fp32 partial LSE (−∞: no key)
+  ModParams mod;      // MOD kernels only
 };
 
 __device__ __forceinline__ float u2f(uint32_t u) { return __uint_as_float(u); }

@@ -10,29 +10,9 @@
 #include "fa_fwd_kernel.cuh"
 #include "fa_fwd1_kernel.cuh"
 #include "fa_fwd_pair_kernel.cuh"
+#include "fa_pdl.h"
 
 namespace fa {
-
-constexpr int kMaxDevices = 64;
-
-// Launches kernel<<<grid, block, smem, stream>>>(args...) as a programmatic dependent of
-// the previous kernel on the stream: its launch and set-up overlap that kernel's tail, and
-// the kernel waits for it with pdl_wait() before touching global memory.
-template <typename... KArgs, typename... Args>
-cudaError_t launch_pdl(void (*kernel)(KArgs...), unsigned grid, unsigned block, size_t smem,
-                       cudaStream_t stream, Args&&... args) {
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(grid);
-  cfg.blockDim = dim3(block);
-  cfg.dynamicSmemBytes = smem;
-  cfg.stream = stream;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, kernel, static_cast<Args&&>(args)...);
-}
 
 struct FwdLaunch {
   CUtensorMap tm_q, tm_k, tm_v;
@@ -73,6 +53,10 @@ constexpr int kDecMultiMaxRows = 2;
 cudaError_t launch_decode_multi(const DecodeParams& p, int d, unsigned combine_grid,
                                 cudaStream_t stream);
 
+// Modified scores (fa_mod.cuh) on the one-tile kernel, mod the kMod… bits.
+cudaError_t launch_fwd_mod_d64(const FwdLaunch& a, int mod);
+cudaError_t launch_fwd_mod_d128(const FwdLaunch& a, int mod);
+
 struct BwdLaunch {
   CUtensorMap tm_q, tm_k, tm_v, tm_do;
   BwdParams p;
@@ -89,5 +73,8 @@ struct BwdLaunch {
 // Enqueues the three backward kernels (prep, main, dQ conversion) on a.stream.
 cudaError_t launch_bwd_d64(const BwdLaunch& a, bool causal);
 cudaError_t launch_bwd_d128(const BwdLaunch& a, bool causal);
+// The same with modified scores; a.p.BH counts key heads, q_heads = B·H.
+cudaError_t launch_bwd_mod_d64(const BwdLaunch& a, int mod, int q_heads);
+cudaError_t launch_bwd_mod_d128(const BwdLaunch& a, int mod, int q_heads);
 
 }  // namespace fa

@@ -1,0 +1,428 @@
+// Host side of attention with modified scores (include/fa.h: fa_visible, fa_fwd_mod, fa_bwd_mod)
+// and the kernel that makes a batch's visibility.
+#include <cuda.h>
+#include <cuda_runtime.h>
+#include <stddef.h>
+#include <stdint.h>
+
+#include <algorithm>
+#include <cmath>
+
+#include "fa.h"
+#include "fa_host.h"
+#include "fa_launch.h"
+
+using namespace fa::host;
+
+namespace fa {
+
+// What fa_visible writes (one buffer, sections on 256-byte boundaries):
+//   rows   int2 [B][T_pad]  visible keys [lo, hi) of each query row ((0, 0): none; padding too)
+//   fwd    int4 [B][n_t]    query tiles, most K tiles first: (tile, first K tile, past the last,
+//                           rows in use: one past the last row that sees or is seen)
+//   bwd    int4 [B][n_t]    key tiles, most query tiles first: (tile, first query tile, past the
+//                           last, rows in use)
+//   whole  int2 [B][n_t]    (largest lo, smallest hi) over a tile's rows
+//   span   int2 [B][n_t]    (smallest lo, largest hi) over the rows that see a key
+//   seen   int2 [B][n_t]    (first, past the last) query tile that sees a key tile
+struct VisibleLayout {
+  size_t rows, fwd, bwd, whole, span, seen, bytes;
+};
+
+static VisibleLayout visible_layout(int B, int T) {
+  auto up = [](size_t x) { return (x + 255u) / 256u * 256u; };
+  const size_t n_t = (static_cast<size_t>(T) + 127) / 128, b = static_cast<size_t>(B);
+  VisibleLayout l;
+  l.rows = 0;
+  l.fwd = up(b * n_t * 128 * 8);
+  l.bwd = l.fwd + up(b * n_t * 16);
+  l.whole = l.bwd + up(b * n_t * 16);
+  l.span = l.whole + up(b * n_t * 8);
+  l.seen = l.span + up(b * n_t * 8);
+  l.bytes = l.seen + up(b * n_t * 8);
+  return l;
+}
+
+struct VisibleParams {
+  const int* ids;     // [B][T] or null
+  const int* prefix;  // [B] or [B][T] or null
+  int prefix_per_token, causal, T, n_t;
+  int2* rows;
+  int4 *fwd, *bwd;
+  int2 *whole, *span, *seen;
+};
+
+constexpr int kVisThreads = 1024;
+
+// One block a sequence. A document is a maximal run of equal ids, so a row's document starts at
+// the last change of id at or before it and ends at the next one after it: a running maximum and
+// a running minimum, each thread taking one stretch of rows and the block joining the stretches.
+// Then a warp a tile: its rows' extremes, the query tiles that see it, and its place among the
+// tiles by the number it has to walk (a count of the tiles before it: n_t² comparisons, which at
+// 16384 tokens are 4 a lane and tile).
+__global__ void __launch_bounds__(kVisThreads) fa_visible_kernel(const VisibleParams p) {
+  __shared__ int s_last[kVisThreads / 32], s_first[kVisThreads / 32];
+  __shared__ int s_used;
+  pdl_wait();
+  pdl_launch_dependents();
+  const int b = blockIdx.x, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  constexpr int kWarps = kVisThreads / 32;
+  const int T = p.T, n_t = p.n_t;
+  const long long T_pad = static_cast<long long>(n_t) * 128;
+  const int* ids = p.ids ? p.ids + static_cast<size_t>(b) * T : nullptr;
+  int2* rows = p.rows + static_cast<size_t>(b) * T_pad;
+  if (tid == 0) s_used = 0;
+  const long long seg = (T_pad + kVisThreads - 1) / kVisThreads;
+  const int a0 = static_cast<int>(min(static_cast<long long>(T), tid * seg));
+  const int a1 = static_cast<int>(min(static_cast<long long>(T), (tid + 1) * seg));
+  int last = -1, first = T;  // this stretch's last and first document starts
+  for (int i = a0; i < a1; ++i) {
+    const bool st = i == 0 || (ids && ids[i] != ids[i - 1]);
+    if (st) {
+      last = i;
+      if (first == T) first = i;
+    }
+  }
+  // inclusive scans over the block's stretches: maximum from the left, minimum from the right
+  int mx = last, mn = first;
+#pragma unroll
+  for (int off = 1; off < 32; off <<= 1) {
+    const int a = __shfl_up_sync(0xffffffffu, mx, off), c = __shfl_down_sync(0xffffffffu, mn, off);
+    if (lane >= off) mx = max(mx, a);
+    if (lane + off < 32) mn = min(mn, c);
+  }
+  if (lane == 31) s_last[warp] = mx;
+  if (lane == 0) s_first[warp] = mn;
+  __syncthreads();
+  int before = __shfl_up_sync(0xffffffffu, mx, 1), after = __shfl_down_sync(0xffffffffu, mn, 1);
+  if (lane == 0) before = -1;
+  if (lane == 31) after = T;
+  for (int w = 0; w < warp; ++w) before = max(before, s_last[w]);
+  for (int w = warp + 1; w < kWarps; ++w) after = min(after, s_first[w]);
+  int cur = max(before, 0);
+  for (int i = a0; i < a1; ++i) {
+    if (ids && i > 0 && ids[i] != ids[i - 1]) cur = i;
+    rows[i].x = cur;
+  }
+  int end = after, used = 0;
+  for (int i = a1 - 1; i >= a0; --i) {
+    const int lo = rows[i].x;
+    int2 r = make_int2(lo, end);
+    if (ids && ids[i] < 0) {
+      r = make_int2(0, 0);
+    } else {
+      if (p.causal) {
+        const int pre = p.prefix ? max(0, p.prefix[p.prefix_per_token ? static_cast<size_t>(b) * T + i
+                                                                      : static_cast<size_t>(b)])
+                                 : 0;
+        r.y = max(i + 1, pre > end - lo ? end : lo + pre);
+      }
+      used = max(used, i + 1);
+    }
+    rows[i] = r;
+    if (lo == i) end = i;
+  }
+  for (long long i = T + tid; i < T_pad; i += kVisThreads) rows[i] = make_int2(0, 0);
+  atomicMax(&s_used, used);
+  __syncthreads();
+  const size_t t0 = static_cast<size_t>(b) * n_t;
+  for (int t = warp; t < n_t; t += kWarps) {
+    int lo_min = T, hi_max = 0, lo_max = 0, hi_min = T;
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const int i = t * 128 + lane + 32 * k;
+      if (i >= T) continue;
+      const int2 r = rows[i];
+      lo_max = max(lo_max, r.x);
+      hi_min = min(hi_min, r.y);
+      if (r.y > r.x) {
+        lo_min = min(lo_min, r.x);
+        hi_max = max(hi_max, r.y);
+      }
+    }
+    lo_min = __reduce_min_sync(0xffffffffu, lo_min);
+    hi_min = __reduce_min_sync(0xffffffffu, hi_min);
+    lo_max = __reduce_max_sync(0xffffffffu, lo_max);
+    hi_max = __reduce_max_sync(0xffffffffu, hi_max);
+    if (lane == 0) {
+      p.whole[t0 + t] = make_int2(lo_max, hi_min);
+      p.span[t0 + t] = hi_max > lo_min ? make_int2(lo_min, hi_max) : make_int2(0, 0);
+    }
+  }
+  __syncthreads();
+  used = s_used;
+  for (int t = warp; t < n_t; t += kWarps) {
+    // the query tiles whose rows see a key of this tile
+    int f = n_t, l = 0;
+    const int k0 = t * 128;
+    for (int q = lane; q < n_t; q += 32) {
+      const int2 s = p.span[t0 + q];
+      if (s.y > k0 && s.x < k0 + 128) {
+        f = min(f, q);
+        l = max(l, q + 1);
+      }
+    }
+    f = __reduce_min_sync(0xffffffffu, f);
+    l = __reduce_max_sync(0xffffffffu, l);
+    if (lane == 0) p.seen[t0 + t] = l > f ? make_int2(f, l) : make_int2(0, 0);
+  }
+  __syncthreads();
+  for (int t = warp; t < n_t; t += kWarps) {
+    const int2 s = p.span[t0 + t], k = p.seen[t0 + t];
+    const int kb = s.x >> 7, ke = (s.y + 127) >> 7;
+    int rf = 0, rb = 0;
+    for (int q = lane; q < n_t; q += 32) {
+      const int2 os = p.span[t0 + q], ok = p.seen[t0 + q];
+      const int on = ((os.y + 127) >> 7) - (os.x >> 7), on2 = ok.y - ok.x;
+      rf += on > ke - kb || (on == ke - kb && q < t);
+      rb += on2 > k.y - k.x || (on2 == k.y - k.x && q < t);
+    }
+    rf = __reduce_add_sync(0xffffffffu, rf);
+    rb = __reduce_add_sync(0xffffffffu, rb);
+    if (lane == 0) {
+      p.fwd[t0 + rf] = make_int4(t, kb, ke, used);
+      p.bwd[t0 + rb] = make_int4(t, k.x, k.y, used);
+    }
+  }
+}
+
+}  // namespace fa
+
+namespace {
+
+constexpr double kLog2e = 1.4426950408889634074;
+
+// The cap's factors; false when the arguments cannot be used.
+bool cap_factors(float scale, float softcap, fa::CapFactors* k) {
+  *k = fa::CapFactors{0.f, 0.f, 0.f, 0.f};
+  if (!std::isfinite(softcap) || softcap < 0.0f) return false;
+  if (softcap == 0.0f) return true;
+  const double u = static_cast<double>(scale) / softcap;
+  k->in = static_cast<float>(u);
+  k->in_exp = static_cast<float>(2.0 * kLog2e * u);
+  k->out = static_cast<float>(softcap * kLog2e);
+  k->limit = static_cast<float>(fa::kCapBend / std::fabs(u));
+  return std::isfinite(k->in_exp) && std::isfinite(k->out);
+}
+
+int mod_bits(float softcap, const float* slopes) {
+  return fa::kModOn | (softcap > 0.0f ? fa::kModCap : 0) | (slopes ? fa::kModBias : 0);
+}
+
+bool mod_sizes(int B, int H, int Hkv, int T, int d) {
+  if (B <= 0 || H <= 0 || Hkv <= 0 || T <= 0 || H % Hkv != 0 || (d != 64 && d != 128)) return false;
+  const long long BH = static_cast<long long>(B) * H, n_t = (static_cast<long long>(T) + 127) / 128;
+  // (the kernels keep tile · 128 in an int, and the unit lists count with one)
+  return BH <= INT32_MAX && n_t * 128 <= INT32_MAX && BH * n_t <= INT32_MAX &&
+         static_cast<long long>(T) * d * 2 < (1LL << 40) && BH * T * d < (1LL << 61);
+}
+
+bool any_misaligned(std::initializer_list<const void*> ps) {
+  for (const void* x : ps)
+    if (!aligned16(x)) return true;
+  return false;
+}
+
+}  // namespace
+
+extern "C" {
+
+size_t fa_visible_size(int B, int T) {
+  if (B <= 0 || T <= 0) return 0;
+  const long long n_t = (static_cast<long long>(T) + 127) / 128;
+  if (n_t * 128 > INT32_MAX || n_t * B > INT32_MAX) return 0;
+  return fa::visible_layout(B, T).bytes;
+}
+
+int fa_visible(const int* doc_ids, const int* prefix_len, int prefix_per_token, int causal,
+               void* visible, size_t visible_bytes, int B, int T, void* stream) {
+  if (!visible) return FA_ERR_INVALID_ARG;
+  const size_t need = fa_visible_size(B, T);
+  if (need == 0 || visible_bytes < need) return FA_ERR_INVALID_ARG;
+  if ((reinterpret_cast<uintptr_t>(visible) & 255u) || (reinterpret_cast<uintptr_t>(doc_ids) & 3u) ||
+      (reinterpret_cast<uintptr_t>(prefix_len) & 3u))
+    return FA_ERR_MISALIGNED;
+  const size_t bt = static_cast<size_t>(B) * T * 4;
+  if ((doc_ids && overlaps(visible, need, doc_ids, bt)) ||
+      (prefix_len && overlaps(visible, need, prefix_len, prefix_per_token ? bt : static_cast<size_t>(B) * 4)))
+    return FA_ERR_INVALID_ARG;
+  int dev = -1, sms = 0;
+  const int st = check_device(&dev, &sms);
+  if (st != FA_OK) return st;
+  const fa::VisibleLayout l = fa::visible_layout(B, T);
+  uint8_t* base = static_cast<uint8_t*>(visible);
+  fa::VisibleParams p{};
+  p.ids = doc_ids;
+  p.prefix = prefix_len;
+  p.prefix_per_token = prefix_per_token != 0;
+  p.causal = causal != 0;
+  p.T = T;
+  p.n_t = static_cast<int>((static_cast<long long>(T) + 127) / 128);
+  p.rows = reinterpret_cast<int2*>(base + l.rows);
+  p.fwd = reinterpret_cast<int4*>(base + l.fwd);
+  p.bwd = reinterpret_cast<int4*>(base + l.bwd);
+  p.whole = reinterpret_cast<int2*>(base + l.whole);
+  p.span = reinterpret_cast<int2*>(base + l.span);
+  p.seen = reinterpret_cast<int2*>(base + l.seen);
+  const cudaError_t e = fa::launch_pdl(fa::fa_visible_kernel, static_cast<unsigned>(B), fa::kVisThreads, 0,
+                                       static_cast<cudaStream_t>(stream), p);
+  return e == cudaSuccess ? FA_OK : FA_ERR_LAUNCH;
+}
+
+int fa_fwd_mod(const void* q, const void* k, const void* v, void* o, float* lse, const void* visible,
+               int causal, float softcap, const float* slopes, int B, int H, int Hkv, int T, int d,
+               float scale, int* status, unsigned long long timeout_ns, void* stream) {
+  if (!q || !k || !v || !o || !lse) return FA_ERR_INVALID_ARG;
+  fa::CapFactors cap;
+  if (!mod_sizes(B, H, Hkv, T, d) || !scale_ok(scale) || !cap_factors(scale, softcap, &cap))
+    return FA_ERR_INVALID_ARG;
+  if (any_misaligned({q, k, v, o, lse}) || (reinterpret_cast<uintptr_t>(visible) & 255u) ||
+      (reinterpret_cast<uintptr_t>(slopes) & 3u))
+    return FA_ERR_MISALIGNED;
+  const int BH = B * H;
+  const size_t qb = static_cast<size_t>(BH) * T * d * 2, kb = static_cast<size_t>(B) * Hkv * T * d * 2;
+  const size_t lb = static_cast<size_t>(BH) * T * 4;
+  const void* ins[5] = {q, k, v, visible, slopes};
+  const size_t in_bytes[5] = {qb, kb, kb, fa_visible_size(B, T), static_cast<size_t>(H) * 4};
+  for (int i = 0; i < 5; ++i)
+    if (ins[i] && (overlaps(o, qb, ins[i], in_bytes[i]) || overlaps(lse, lb, ins[i], in_bytes[i])))
+      return FA_ERR_INVALID_ARG;
+  if (overlaps(o, qb, lse, lb)) return FA_ERR_INVALID_ARG;
+  int dev = -1, sms = 0;
+  const int st = check_device(&dev, &sms);
+  if (st != FA_OK) return st;
+  EncodeTiledFn enc = encode_fn();
+  if (!enc) return FA_ERR_LAUNCH;
+  fa::FwdLaunch a;
+  a.p = fa::FwdParams{};
+  if (!encode_map(enc, &a.tm_q, q, T, d, BH) || !encode_map(enc, &a.tm_k, k, T, d, B * Hkv) ||
+      !encode_map(enc, &a.tm_v, v, T, d, B * Hkv) || !encode_map(enc, &a.tm_o, o, T, d, BH, 32))
+    return FA_ERR_INVALID_ARG;
+  const int n_t = (T + 127) / 128;
+  a.p.o = static_cast<__nv_bfloat16*>(o);
+  a.p.lse = lse;
+  a.p.status = status;
+  a.p.T = T;
+  a.p.BH = BH;
+  a.p.n_units = n_t;
+  a.p.total_units = n_t * BH;
+  a.p.n_kv = n_t;
+  a.p.tiles_per_cta = 1;
+  a.p.div_bh = fa::FastDiv::make(static_cast<uint32_t>(BH));
+  a.p.div_splits = fa::FastDiv::make(1u);
+  a.p.scale_log2 = static_cast<float>(static_cast<double>(scale) * kLog2e);
+  a.p.timeout_ns = timeout_ns ? timeout_ns : 2000000000ull;
+  a.p.Tk = T;
+  a.p.n_qt = n_t;
+  a.p.n_splits = 1;
+  a.p.kt_per_split = n_t;
+  a.p.bmask_heads = 1;
+  if (visible) {
+    const fa::VisibleLayout l = fa::visible_layout(B, T);
+    const uint8_t* base = static_cast<const uint8_t*>(visible);
+    a.p.mod.rows = reinterpret_cast<const int2*>(base + l.rows);
+    a.p.mod.units = reinterpret_cast<const int4*>(base + l.fwd);
+  }
+  a.p.mod.slopes = slopes;
+  a.p.mod.T_pad = n_t * 128;
+  a.p.mod.H = H;
+  a.p.mod.div_h = fa::FastDiv::make(static_cast<uint32_t>(H));
+  a.p.mod.div_g = fa::FastDiv::make(static_cast<uint32_t>(H / Hkv));
+  a.p.mod.cap = cap;
+  a.p.mod.causal = causal != 0;
+  a.grid = static_cast<unsigned>(std::min(a.p.total_units, sms));
+  a.stream = static_cast<cudaStream_t>(stream);
+  const int mod = mod_bits(softcap, slopes);
+  const cudaError_t e = (d == 64) ? fa::launch_fwd_mod_d64(a, mod) : fa::launch_fwd_mod_d128(a, mod);
+  return e == cudaSuccess ? FA_OK : FA_ERR_LAUNCH;
+}
+
+int fa_bwd_mod(const void* q, const void* k, const void* v, const void* o, const void* dout,
+               const float* lse, void* dq, void* dk, void* dv, void* workspace, size_t workspace_bytes,
+               const void* visible, int causal, float softcap, const float* slopes, int B, int H,
+               int Hkv, int T, int d, float scale, int* status, unsigned long long timeout_ns,
+               void* stream) {
+  if (!q || !k || !v || !o || !dout || !lse || !dq || !dk || !dv || !workspace)
+    return FA_ERR_INVALID_ARG;
+  fa::CapFactors cap;
+  if (!mod_sizes(B, H, Hkv, T, d) || !scale_ok(scale) || !cap_factors(scale, softcap, &cap))
+    return FA_ERR_INVALID_ARG;
+  const size_t need = fa_bwd_workspace_size(B, H, T, d);
+  if (need == 0 || workspace_bytes < need) return FA_ERR_INVALID_ARG;
+  if (any_misaligned({q, k, v, o, dout, lse, dq, dk, dv}) || (reinterpret_cast<uintptr_t>(workspace) & 255u) ||
+      (reinterpret_cast<uintptr_t>(visible) & 255u) || (reinterpret_cast<uintptr_t>(slopes) & 3u))
+    return FA_ERR_MISALIGNED;
+  const int BH = B * H, BHkv = B * Hkv;
+  const size_t qb = static_cast<size_t>(BH) * T * d * 2, kb = static_cast<size_t>(BHkv) * T * d * 2;
+  const void* ins[8] = {q, k, v, o, dout, lse, visible, slopes};
+  const size_t in_bytes[8] = {qb, kb, kb, qb, qb, static_cast<size_t>(BH) * T * 4, fa_visible_size(B, T),
+                              static_cast<size_t>(H) * 4};
+  const void* outs[4] = {dq, dk, dv, workspace};
+  const size_t out_bytes[4] = {qb, kb, kb, need};
+  for (int x = 0; x < 4; ++x) {
+    for (int y = 0; y < 8; ++y)
+      if (ins[y] && overlaps(outs[x], out_bytes[x], ins[y], in_bytes[y])) return FA_ERR_INVALID_ARG;
+    for (int y = x + 1; y < 4; ++y)
+      if (overlaps(outs[x], out_bytes[x], outs[y], out_bytes[y])) return FA_ERR_INVALID_ARG;
+  }
+  int dev = -1, sms = 0;
+  const int st = check_device(&dev, &sms);
+  if (st != FA_OK) return st;
+  EncodeTiledFn enc = encode_fn();
+  if (!enc) return FA_ERR_LAUNCH;
+  const int bq = (d == 64) ? 128 : 64;
+  fa::BwdLaunch a;
+  if (!encode_map(enc, &a.tm_q, q, T, d, BH, bq) || !encode_map(enc, &a.tm_k, k, T, d, BHkv) ||
+      !encode_map(enc, &a.tm_v, v, T, d, BHkv) || !encode_map(enc, &a.tm_do, dout, T, d, BH, bq))
+    return FA_ERR_INVALID_ARG;
+  const int n_t = (T + 127) / 128, T_pad = n_t * 128;
+  auto up = [](size_t x) { return (x + 255u) / 256u * 256u; };
+  const size_t rows = static_cast<size_t>(BH) * T_pad;
+  uint8_t* ws = static_cast<uint8_t*>(workspace);
+  a.p = fa::BwdParams{};
+  a.lse2 = reinterpret_cast<float*>(ws);
+  a.dvec = reinterpret_cast<float*>(ws + up(rows * 4));
+  a.p.dq_acc = reinterpret_cast<float*>(ws + 2 * up(rows * 4));
+  a.p.lse2 = a.lse2;
+  a.p.dvec = a.dvec;
+  a.p.dk = static_cast<__nv_bfloat16*>(dk);
+  a.p.dv = static_cast<__nv_bfloat16*>(dv);
+  a.p.status = status;
+  a.p.T = T;
+  a.p.T_pad = T_pad;
+  a.p.BH = BHkv;
+  a.p.n_qt = T_pad / bq;
+  a.p.n_kt = n_t;
+  // Key heads per group: their query heads' Q and dO (bf16) plus the fp32 dQ accumulator, about
+  // 64 MB (half the L2).
+  const long long per_head = 8LL * T_pad * d * (H / Hkv);
+  a.p.head_group = static_cast<int>(std::max<long long>(1, std::min<long long>(BHkv, (64LL << 20) / per_head)));
+  a.p.scale = scale;
+  a.p.scale_log2 = static_cast<float>(static_cast<double>(scale) * kLog2e);
+  a.p.timeout_ns = timeout_ns ? timeout_ns : 2000000000ull;
+  if (visible) {
+    const fa::VisibleLayout l = fa::visible_layout(B, T);
+    const uint8_t* base = static_cast<const uint8_t*>(visible);
+    a.p.mod.rows = reinterpret_cast<const int2*>(base + l.rows);
+    a.p.mod.units = reinterpret_cast<const int4*>(base + l.bwd);
+    a.p.mod.whole = reinterpret_cast<const int2*>(base + l.whole);
+  }
+  a.p.mod.slopes = slopes;
+  a.p.mod.Hkv = Hkv;
+  a.p.mod.group = H / Hkv;
+  a.p.mod.cap = cap;
+  a.p.mod.causal = causal != 0;
+  a.o = static_cast<const __nv_bfloat16*>(o);
+  a.dout = static_cast<const __nv_bfloat16*>(dout);
+  a.lse = lse;
+  a.dq = static_cast<__nv_bfloat16*>(dq);
+  a.grid_main = static_cast<unsigned>(static_cast<long long>(n_t) * BHkv);
+  a.grid_prep = static_cast<unsigned>(sms) * 8u;
+  a.grid_dq = static_cast<unsigned>(sms) * 8u;
+  a.stream = static_cast<cudaStream_t>(stream);
+  const int mod = mod_bits(softcap, slopes);
+  const cudaError_t e = (d == 64) ? fa::launch_bwd_mod_d64(a, mod, BH) : fa::launch_bwd_mod_d128(a, mod, BH);
+  return e == cudaSuccess ? FA_OK : FA_ERR_LAUNCH;
+}
+
+}  // extern "C"

@@ -1,0 +1,17 @@
+// Instantiations of the one-tile forward with modified scores for head dim 128: with and
+// without a tanh cap and a distance bias.
+#include "fa_mod_launch.cuh"
+
+namespace fa {
+
+cudaError_t launch_fwd_mod_d128(const FwdLaunch& a, int mod) {
+  switch (mod) {
+    case kModOn: return launch_fwd_mod<128, kModOn>(a);
+    case kModOn | kModCap: return launch_fwd_mod<128, kModOn | kModCap>(a);
+    case kModOn | kModBias: return launch_fwd_mod<128, kModOn | kModBias>(a);
+    case kModOn | kModCap | kModBias: return launch_fwd_mod<128, kModOn | kModCap | kModBias>(a);
+  }
+  return cudaErrorInvalidValue;
+}
+
+}  // namespace fa

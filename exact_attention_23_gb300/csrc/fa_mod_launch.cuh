@@ -1,0 +1,50 @@
+// Launches of the MOD kernels (modified scores), shared by their instantiation files. Internal.
+#pragma once
+
+#include <atomic>
+
+#include "fa_launch.h"
+
+namespace fa {
+
+// The shared-memory opt-in is a per-device attribute: set it once per device and kernel.
+template <typename Fn>
+cudaError_t smem_opt_in(Fn* fn, int smem, std::atomic<uint64_t>* done) {
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxDevices) return cudaErrorInvalidDevice;
+  const uint64_t bit = 1ull << (dev % 64);
+  if (done[dev / 64].load(std::memory_order_acquire) & bit) return cudaSuccess;
+  const cudaError_t e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  if (e == cudaSuccess) done[dev / 64].fetch_or(bit, std::memory_order_acq_rel);
+  return e;
+}
+
+template <int D, int MOD>
+cudaError_t launch_fwd_mod(const FwdLaunch& a) {
+  auto* fn = &fa_fwd1_kernel<D, false, true, MOD>;
+  static std::atomic<uint64_t> done[kMaxDevices / 64 + 1];
+  const int smem = Cfg1<D>::kSmemBytes;
+  const cudaError_t e = smem_opt_in(fn, smem, done);
+  if (e != cudaSuccess) return e;
+  return launch_pdl(fn, a.grid, Cfg1<D>::kThreads, smem, a.stream, a.tm_q, a.tm_k, a.tm_v, a.tm_o, a.p);
+}
+
+// a.p.BH counts key heads; q_heads = B·H.
+template <int D, int MOD>
+cudaError_t launch_bwd_mod(const BwdLaunch& a, int q_heads) {
+  using C = BwdCfg<D, MOD>;
+  auto* fn = &fa_bwd_main_kernel<D, false, MOD>;
+  static std::atomic<uint64_t> done[kMaxDevices / 64 + 1];
+  cudaError_t e = smem_opt_in(fn, C::kSmemBytes, done);
+  if (e != cudaSuccess) return e;
+  e = launch_pdl(fa_bwd_prep_kernel<D, true>, a.grid_prep, 256, 0, a.stream, a.o, a.dout, a.lse, a.lse2,
+                 a.dvec, a.p.dq_acc, a.p.T, a.p.T_pad, q_heads);
+  if (e != cudaSuccess) return e;
+  e = launch_pdl(fn, a.grid_main, C::kThreads, C::kSmemBytes, a.stream, a.tm_q, a.tm_k, a.tm_v, a.tm_do,
+                 a.p);
+  if (e != cudaSuccess) return e;
+  return launch_pdl(fa_bwd_dq_kernel<D>, a.grid_dq, 256, 0, a.stream, a.p.dq_acc, a.dq, a.p.T, a.p.n_qt,
+                    q_heads, a.p.scale);
+}
+
+}  // namespace fa

@@ -294,6 +294,118 @@ int fa_fwd_host(const void* q, const void* k, const void* v, void* o, float* lse
                 int T, int d, int causal, float scale, int heads_per_chunk, void* workspace,
                 size_t workspace_bytes, void* stream);
 
+/*
+ * ---------------------------------------------------------------------------------------
+ * Attention with modified scores, forward and backward.
+ *
+ *   z_ij = scale · q_i·k_j
+ *   z_ij = softcap · tanh(z_ij / softcap)          (softcap > 0; 0: no cap)
+ *   z_ij = z_ij − slopes[h] · |i − j|              (slopes given: a bias by distance)
+ *   O    = softmax over the visible keys of z_i · V,   LSE_i = ln Σ_visible exp(z_ij)
+ *
+ * Query head h reads key head h / (H / Hkv): q, o, dout, dq are [B, H, T, d] and k, v, dk, dv
+ * [B, Hkv, T, d], Hkv a divisor of H. Which keys a query sees is, for every mask here, one
+ * interval per query; fa_visible makes the intervals of a batch once, for every layer's calls.
+ * A row that sees no key gets O = 0, LSE = −∞ and no gradient. The forward takes its products on
+ * the tensor cores and everything else in fp32; P (and dS in the backward) are rounded to bf16
+ * as operands of their products.
+ * ---------------------------------------------------------------------------------------
+ */
+
+/*
+ * fa_visible — who sees whom in a batch of B sequences of T tokens.
+ *
+ *   doc_ids    : optional DEVICE int32 [B][T]. A document is a maximal run of equal ids; a
+ *                token sees its own document only. A negative id is padding: it sees nothing and
+ *                nothing sees it. NULL: each sequence is one document.
+ *   causal     : nonzero → key j is visible to query i when j ≤ i or j is one of the first
+ *                prefix_len tokens of their document; 0 → every key of the document (prefix_len
+ *                is then without effect).
+ *   prefix_len : optional DEVICE int32, [B] (prefix_per_token = 0: the same for every document
+ *                of the sequence) or [B][T] (each token holds its document's); ≤ 0 means none.
+ *   visible    : DEVICE buffer of at least fa_visible_size(B, T) bytes, 256-byte aligned,
+ *                written; opaque. It is read by fa_fwd_mod and fa_bwd_mod calls with the same
+ *                B and T, any number of them, on this stream or ordered after it.
+ */
+size_t fa_visible_size(int B, int T);
+int fa_visible(const int* doc_ids, const int* prefix_len, int prefix_per_token, int causal,
+               void* visible, size_t visible_bytes, int B, int T, void* stream);
+
+/*
+ * fa_fwd_mod — the forward with modified scores.
+ *
+ *   visible : a buffer filled by fa_visible for this B and T, or NULL: then `causal` alone says
+ *             who sees whom (with a buffer, `causal` is not looked at)
+ *   softcap : finite, ≥ 0
+ *   slopes  : optional DEVICE float [H], finite; no gradient is taken of them
+ *   status, timeout_ns : as for fa_fwd_ex
+ *
+ * Padding may hold anything: rows behind the last token that sees a key are never mixed into
+ * others' results, NaN included. Padding in front of or between documents must be finite.
+ */
+int fa_fwd_mod(const void* q, const void* k, const void* v, void* o, float* lse, const void* visible,
+               int causal, float softcap, const float* slopes, int B, int H, int Hkv, int T, int d,
+               float scale, int* status, unsigned long long timeout_ns, void* stream);
+
+/*
+ * fa_bwd_mod — its gradients, from the forward's o and lse and the upstream gradient dout:
+ * with P = exp(z − LSE) and dS = P ∘ (dO Vᵀ − D) ∘ (1 − tanh²), D = rowsum(dO ∘ O),
+ *   dQ = scale · dS K,   dK = scale · dSᵀ Q,   dV = Pᵀ dO,
+ * dK and dV summed over the query heads that share a key head. visible, causal, softcap, slopes
+ * and scale are those of the forward. workspace: fa_bwd_workspace_size(B, H, T, d) bytes,
+ * 256-byte aligned, as for fa_bwd. dQ is summed with atomic adds in an unspecified order (equal
+ * within fp32 rounding from call to call, as fa_bwd's); dK and dV are the same bits every time.
+ */
+int fa_bwd_mod(const void* q, const void* k, const void* v, const void* o, const void* dout,
+               const float* lse, void* dq, void* dk, void* dv, void* workspace, size_t workspace_bytes,
+               const void* visible, int causal, float softcap, const float* slopes, int B, int H,
+               int Hkv, int T, int d, float scale, int* status, unsigned long long timeout_ns,
+               void* stream);
+
+/*
+ * ---------------------------------------------------------------------------------------
+ * Rotary positions.
+ *
+ * The first rot_dim dimensions of a head are pairs, dimensions (i, i + rot_dim/2), or (2i,
+ * 2i + 1) when interleaved; pair i of the row at position n is turned by the angle
+ * n · inv_freq[i] and multiplied by mscale; the rest of the head is copied.
+ *
+ *   inv_freq  : DEVICE double [rot_dim/2], radians per position (scaled for long contexts by
+ *               whoever makes it); the angle keeps 2⁻⁶⁴ of a turn at every int32 position
+ *   rot_dim   : a multiple of 16, 16 … d
+ *   positions : DEVICE int32 [T], or [B][T] with positions_per_batch, or NULL (see each call)
+ *   sources   : bf16, any strides (*_sb, *_sh, *_st elements a batch, head, token; ≥ 0 and
+ *               multiples of 8; the d dimensions contiguous), so that a packed projection
+ *               [B, T, heads, d] is read in place
+ * ---------------------------------------------------------------------------------------
+ */
+
+/*
+ * fa_rope — q [B, H, T, d] and (Hkv > 0, else k and k_out NULL) k [B, Hkv, T, d] turned into
+ * contiguous q_out and k_out. inverse: turned back, which is the gradient (mscale included).
+ * positions NULL: token t is at position t. An output may be its own contiguous input;
+ * otherwise outputs overlap nothing.
+ */
+int fa_rope(const void* q, long long q_sb, long long q_sh, long long q_st, void* q_out,
+            const void* k, long long k_sb, long long k_sh, long long k_st, void* k_out,
+            const int* positions, int positions_per_batch, const double* inv_freq, int rot_dim,
+            int interleaved, int inverse, float mscale, int B, int H, int Hkv, int T, int d,
+            void* stream);
+
+/*
+ * fa_rope_append — a serving step's Tq new tokens: q is turned into the contiguous q_out
+ * [B, H, Tq, d]; k, turned, and v are written into rows ctx_len[b] … ctx_len[b] + Tq − 1 of the
+ * contiguous caches [B, Hkv, Tmax, d]. positions NULL: token t is at ctx_len[b] + t.
+ * ctx_len: DEVICE int32 [B]; a negative one marks an inactive sequence (its q_out is 0 and its
+ * cache is left as it is). Rows past Tmax are not written. Nothing else of the caches is touched.
+ */
+int fa_rope_append(const void* q, long long q_sb, long long q_sh, long long q_st, void* q_out,
+                   const void* k, long long k_sb, long long k_sh, long long k_st, const void* v,
+                   long long v_sb, long long v_sh, long long v_st, void* k_cache, void* v_cache,
+                   const int* ctx_len, const int* positions, int positions_per_batch,
+                   const double* inv_freq, int rot_dim, int interleaved, float mscale, int B, int H,
+                   int Hkv, int Tq, int Tmax, int d, void* stream);
+
 /* Static text for a status code (never NULL). */
 const char* fa_strerror(int status);
 
