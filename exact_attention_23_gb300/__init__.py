@@ -8,7 +8,8 @@ per-row natural-log logsumexp in fp32. ``fwd_kv`` attends Tq queries to Tk ≥ T
 ``bwd(q, k, v, o, lse, do, causal)`` returns the gradients (dq, dk, dv) (d = 64 or 128).
 ``fwd_mod`` and ``bwd_mod`` are attention with modified scores (a tanh cap, a bias by distance,
 documents and prefixes through ``visible``, key heads shared by query heads) and its gradients;
-``rope`` and ``rope_append`` turn queries and keys by their positions.
+``rope`` and ``rope_append`` turn queries and keys by their positions, and ``fwd_tree`` attends
+new tokens (one, a chain, a tree of drafts) to a cache of ragged contexts.
 The work is done by the CUDA kernels of ``libfa.so`` through its C ABI (include/fa.h);
 this module only allocates outputs and workspace with PyTorch and passes pointers and the
 current stream.
@@ -43,6 +44,8 @@ from ._binding import (  # noqa: F401
     fa_fwd_kv,
     fa_fwd_kv_workspace_size,
     fa_fwd_mod,
+    fa_fwd_tree,
+    fa_fwd_tree_workspace_size,
     fa_rope,
     fa_rope_append,
     fa_visible,
@@ -376,6 +379,16 @@ def visible(B: int, T: int, causal: bool = True, doc_ids=None, prefix_len=None, 
     return Visible(buffer, B, T, bool(causal))
 
 
+def _check_slopes(slopes, H, device):
+    import torch
+    if slopes is None:
+        return
+    if not isinstance(slopes, torch.Tensor) or slopes.dtype != torch.float32 \
+            or tuple(slopes.shape) != (H,) or not slopes.is_contiguous():
+        raise ValueError(f"slopes must be a contiguous float32 tensor of shape [{H}]")
+    _same_device(slopes, device, "slopes")
+
+
 def _check_mod(q, k, v, seen, causal, slopes):
     """Shapes, devices and masks of a modified-score call; the causal flag that holds."""
     import torch
@@ -386,11 +399,7 @@ def _check_mod(q, k, v, seen, causal, slopes):
     if k.shape != v.shape or k.shape[0] != B or k.shape[2:] != q.shape[2:] \
             or H % max(1, k.shape[1]) != 0:
         raise ValueError("q must be [B, H, T, d] and k, v [B, Hkv, T, d] with Hkv a divisor of H")
-    if slopes is not None:
-        if not isinstance(slopes, torch.Tensor) or slopes.dtype != torch.float32 \
-                or tuple(slopes.shape) != (H,) or not slopes.is_contiguous():
-            raise ValueError(f"slopes must be a contiguous float32 tensor of shape [{H}]")
-        _same_device(slopes, q.device, "slopes")
+    _check_slopes(slopes, H, q.device)
     if seen is None:
         return True if causal is None else bool(causal)
     if not isinstance(seen, Visible):
@@ -485,6 +494,80 @@ def bwd_mod(q, k, v, o, lse, do, visible=None, causal: bool | None = None, softc
     if rc != FA_OK:
         raise FAError(rc, "fa_bwd_mod")
     return dq, dk, dv
+
+
+def fwd_tree_workspace(B: int, H: int, Hkv: int, Tq: int, Tmax: int, d: int, device=None):
+    """A uint8 CUDA tensor large enough to serve as ``fwd_tree``'s workspace."""
+    import torch
+    dev = torch.device("cuda", torch.cuda.current_device()) if device is None \
+        else torch.device(device)
+    with torch.cuda.device(dev):
+        n = fa_fwd_tree_workspace_size(B, H, Hkv, Tq, Tmax, d)
+    if n == 0:
+        raise FAError(FA_ERR_INVALID_ARG, "fa_fwd_tree_workspace_size")
+    return torch.empty(n, dtype=torch.uint8, device=dev)
+
+
+def fwd_tree(q, k_cache, v_cache, ctx_len, tree=None, depths=None, softcap: float = 0.0,
+             slopes=None, scale: float | None = None, out=None, lse=None, workspace=None,
+             status=None, timeout_ns: int = 0):
+    """New tokens q [B, H, Tq, d] against caches [B, Hkv, Tmax, d] through fa_fwd_tree: sequence b
+    holds ``ctx_len[b]`` tokens (int32 [B]; negative: inactive) and behind them, already written
+    (``rope_append``), its Tq new ones.
+
+    A new token sees the whole context and, of the new tokens, those where ``tree`` (uint8 or bool
+    [Tq, Tq] or [B, Tq, Tq], nonzero = row t sees token s) says so; without it a chain: itself and
+    the ones before. ``softcap`` and ``slopes`` as for ``fwd_mod``, the bias measured between
+    positions ctx_len[b] + ``depths`` (int32 [Tq] or [B, Tq]; None: 0, 1, …). Returns (o, lse); a
+    token that sees nothing has o = 0 and lse = −inf. ``workspace``: see ``fwd_tree_workspace``.
+    """
+    import torch
+    for t, n in ((q, "q"), (k_cache, "k_cache"), (v_cache, "v_cache")):
+        _check(t, n)
+        _same_device(t, q.device, n)
+    B, H, Tq, d = q.shape
+    Hkv, Tmax = k_cache.shape[1], k_cache.shape[2]
+    if k_cache.shape != v_cache.shape or k_cache.shape[0] != B or k_cache.shape[3] != d \
+            or H % max(1, Hkv) != 0:
+        raise ValueError("q must be [B, H, Tq, d] and the caches [B, Hkv, Tmax, d] with Hkv a "
+                         "divisor of H")
+    _check_int32(ctx_len, ((B,),), q.device, "ctx_len")
+    if tree is not None:
+        if not isinstance(tree, torch.Tensor) or tree.dtype not in (torch.uint8, torch.bool) \
+                or not tree.is_contiguous() or tuple(tree.shape) not in ((Tq, Tq), (B, Tq, Tq)):
+            raise ValueError(f"tree must be a contiguous uint8 or bool tensor of shape "
+                             f"[{Tq}, {Tq}] or [{B}, {Tq}, {Tq}]")
+        _same_device(tree, q.device, "tree")
+    if depths is not None:
+        _check_int32(depths, ((Tq,), (B, Tq)), q.device, "depths")
+    _check_slopes(slopes, H, q.device)
+    if scale is None:
+        scale = 1.0 / math.sqrt(d)
+    if out is None:
+        out = torch.empty_like(q)
+    else:
+        _check_like(out, q, "out")
+    if lse is None:
+        lse = torch.empty((B, H, Tq), dtype=torch.float32, device=q.device)
+    else:
+        _check_lse(lse, (B, H, Tq), q.device)
+    if workspace is None:
+        workspace = fwd_tree_workspace(B, H, Hkv, Tq, Tmax, d, device=q.device)
+    _same_device(workspace, q.device, "workspace")
+    with torch.cuda.device(q.device):
+        rc = fa_fwd_tree(q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), out.data_ptr(),
+                         lse.data_ptr(), ctx_len.data_ptr(),
+                         None if tree is None else tree.data_ptr(),
+                         tree is not None and tree.dim() == 3,
+                         None if depths is None else depths.data_ptr(),
+                         depths is not None and depths.dim() == 2, softcap,
+                         None if slopes is None else slopes.data_ptr(), B, H, Hkv, Tq, Tmax, d,
+                         scale, workspace.data_ptr(), workspace.numel() * workspace.element_size(),
+                         None if status is None else status.data_ptr(), timeout_ns,
+                         torch.cuda.current_stream(q.device).cuda_stream)
+    if rc != FA_OK:
+        raise FAError(rc, "fa_fwd_tree")
+    return out, lse
 
 
 def rope_inv_freq(rot_dim: int, base: float = 10000.0, scaling: str | None = None,

@@ -29,7 +29,7 @@ FA_BWD_NOALLOC_SCRATCH_BYTES = 33554432
 EXPORTS = ("fa_fwd", "fa_fwd_ex", "fa_fwd_fp8", "fa_fwd_host_workspace_size", "fa_fwd_host", "fa_fwd_kv_workspace_size", "fa_fwd_kv",
            "fa_fwd_block_sparse", "fa_bwd_workspace_size", "fa_bwd", "fa_bwd_ex",
            "fa_bwd_noalloc", "fa_visible_size", "fa_visible", "fa_fwd_mod", "fa_bwd_mod", "fa_rope",
-           "fa_rope_append", "fa_strerror", "fa_version")
+           "fa_rope_append", "fa_fwd_tree_workspace_size", "fa_fwd_tree", "fa_strerror", "fa_version")
 
 _lock = threading.Lock()
 _lib = None
@@ -93,6 +93,10 @@ def lib() -> ctypes.CDLL:
             L.fa_rope_append.argtypes = (src + [vp] + src + src + [vp, vp, vp, vp, i, vp, i, i, f]
                                          + [i] * 6 + [vp])
             L.fa_rope_append.restype = i
+            L.fa_fwd_tree_workspace_size.argtypes = [i] * 6
+            L.fa_fwd_tree_workspace_size.restype = sz
+            L.fa_fwd_tree.argtypes = ([vp] * 7 + [i, vp, i, f, vp] + [i] * 6 + [f, vp, sz, vp, ull, vp])
+            L.fa_fwd_tree.restype = i
             L.fa_strerror.argtypes = [i]
             L.fa_strerror.restype = ctypes.c_char_p
             L.fa_version.argtypes = []
@@ -211,3 +215,16 @@ def fa_rope_append(q, q_strides, q_out, k, k_strides, v, v_strides, k_cache, v_c
                                 v_cache, ctx_len, positions, int(positions_per_batch), inv_freq,
                                 rot_dim, int(interleaved), float(mscale), B, H, Hkv, Tq, Tmax, d,
                                 stream)
+
+
+def fa_fwd_tree_workspace_size(B, H, Hkv, Tq, Tmax, d) -> int:
+    return int(lib().fa_fwd_tree_workspace_size(B, H, Hkv, Tq, Tmax, d))
+
+
+def fa_fwd_tree(q, k_cache, v_cache, o, lse, ctx_len, tree, tree_per_batch, depths,
+                depths_per_batch, softcap, slopes, B, H, Hkv, Tq, Tmax, d, scale, workspace,
+                workspace_bytes, status, timeout_ns, stream) -> int:
+    return lib().fa_fwd_tree(q, k_cache, v_cache, o, lse, ctx_len, tree, int(tree_per_batch), depths,
+                             int(depths_per_batch), float(softcap), slopes, B, H, Hkv, Tq, Tmax, d,
+                             float(scale), workspace, int(workspace_bytes), status, int(timeout_ns),
+                             stream)

@@ -11,6 +11,7 @@
 #include "fa.h"
 #include "fa_host.h"
 #include "fa_launch.h"
+#include "fa_mod_host.h"
 
 using namespace fa::host;
 
@@ -189,25 +190,6 @@ __global__ void __launch_bounds__(kVisThreads) fa_visible_kernel(const VisiblePa
 }  // namespace fa
 
 namespace {
-
-constexpr double kLog2e = 1.4426950408889634074;
-
-// The cap's factors; false when the arguments cannot be used.
-bool cap_factors(float scale, float softcap, fa::CapFactors* k) {
-  *k = fa::CapFactors{0.f, 0.f, 0.f, 0.f};
-  if (!std::isfinite(softcap) || softcap < 0.0f) return false;
-  if (softcap == 0.0f) return true;
-  const double u = static_cast<double>(scale) / softcap;
-  k->in = static_cast<float>(u);
-  k->in_exp = static_cast<float>(2.0 * kLog2e * u);
-  k->out = static_cast<float>(softcap * kLog2e);
-  k->limit = static_cast<float>(fa::kCapBend / std::fabs(u));
-  return std::isfinite(k->in_exp) && std::isfinite(k->out);
-}
-
-int mod_bits(float softcap, const float* slopes) {
-  return fa::kModOn | (softcap > 0.0f ? fa::kModCap : 0) | (slopes ? fa::kModBias : 0);
-}
 
 bool mod_sizes(int B, int H, int Hkv, int T, int d) {
   if (B <= 0 || H <= 0 || Hkv <= 0 || T <= 0 || H % Hkv != 0 || (d != 64 && d != 128)) return false;

@@ -4,20 +4,9 @@
 #include <atomic>
 
 #include "fa_launch.h"
+#include "fa_mod_host.h"
 
 namespace fa {
-
-// The shared-memory opt-in is a per-device attribute: set it once per device and kernel.
-template <typename Fn>
-cudaError_t smem_opt_in(Fn* fn, int smem, std::atomic<uint64_t>* done) {
-  int dev = 0;
-  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxDevices) return cudaErrorInvalidDevice;
-  const uint64_t bit = 1ull << (dev % 64);
-  if (done[dev / 64].load(std::memory_order_acquire) & bit) return cudaSuccess;
-  const cudaError_t e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
-  if (e == cudaSuccess) done[dev / 64].fetch_or(bit, std::memory_order_acq_rel);
-  return e;
-}
 
 template <int D, int MOD>
 cudaError_t launch_fwd_mod(const FwdLaunch& a) {

@@ -406,6 +406,39 @@ int fa_rope_append(const void* q, long long q_sb, long long q_sh, long long q_st
                    const double* inv_freq, int rot_dim, int interleaved, float mscale, int B, int H,
                    int Hkv, int Tq, int Tmax, int d, void* stream);
 
+/*
+ * ---------------------------------------------------------------------------------------
+ * fa_fwd_tree — new tokens against a cache: one decoded token a sequence, a chain of them (a
+ * chunk of a prompt), or the nodes of a tree of drafted tokens, each of which sees its ancestors.
+ *
+ * Sequence b holds ctx_len[b] tokens in rows 0 … ctx_len[b] − 1 of the caches [B, Hkv, Tmax, d],
+ * and its Tq new tokens' keys and values, already written (fa_rope_append), in the rows behind:
+ *
+ *   token t sees row j  iff  j < ctx_len[b],  or  j = ctx_len[b] + s < Tmax and tree[t][s] ≠ 0
+ *
+ * Scores are modified as in fa_fwd_mod, the bias measuring from position ctx_len[b] + depths[t]
+ * to j, or to ctx_len[b] + depths[s]. q, o: [B, H, Tq, d]; lse: [B, H, Tq]; query head h reads key
+ * head h / (H / Hkv). A token that sees no row gets O = 0 and LSE = −∞.
+ *
+ *   ctx_len : DEVICE int32 [B]; 0: no context; negative: an inactive sequence (O = 0, LSE = −∞).
+ *             The lengths are read on the device: work is shared out by them, not by Tmax.
+ *   tree    : optional DEVICE uint8 [Tq][Tq], or [B][Tq][Tq] with tree_per_batch; NULL: a chain
+ *             (tree[t][s] = s ≤ t)
+ *   depths  : optional DEVICE int32 [Tq], or [B][Tq] with depths_per_batch; NULL: 0, 1, 2, …;
+ *             used by the bias only
+ *   workspace : DEVICE memory of fa_fwd_tree_workspace_size(...) bytes (for the current device; 0:
+ *             unsupported sizes, or no usable device), 256-byte aligned, contents immaterial. Not
+ *             shared with a call that may run at the same time.
+ *
+ * Cache rows behind a sequence's last new token may hold anything, NaN included.
+ */
+size_t fa_fwd_tree_workspace_size(int B, int H, int Hkv, int Tq, int Tmax, int d);
+int fa_fwd_tree(const void* q, const void* k_cache, const void* v_cache, void* o, float* lse,
+                const int* ctx_len, const unsigned char* tree, int tree_per_batch, const int* depths,
+                int depths_per_batch, float softcap, const float* slopes, int B, int H, int Hkv, int Tq,
+                int Tmax, int d, float scale, void* workspace, size_t workspace_bytes, int* status,
+                unsigned long long timeout_ns, void* stream);
+
 /* Static text for a status code (never NULL). */
 const char* fa_strerror(int status);
 
