@@ -49,6 +49,8 @@
 // and a TMA store, and the LSE) is deferred into the first step of the next unit.
 #pragma once
 
+#include <type_traits>
+
 #include "fa_fwd_kernel.cuh"
 #include "fa_mod.cuh"
 
@@ -119,9 +121,31 @@ static_assert(sizeof(Bars1) <= 512, "barrier block");
 // The unit at position L of the list. MOD: a unit is (query head, query tile) with one contiguous
 // range of K tiles, from the visibility's records (heaviest tile first) or, without them, the
 // causal or full range, the last tile first.
-template <bool CAUSAL, bool GEN, int MOD>
-__device__ __forceinline__ Unit unit1_of(const FwdParams& p, int L) {
-  if constexpr (MOD != 0) {
+// TREE (with MOD): the CTA's stretch of all (sequence, key head, row block, key chunk) is walked
+// segment by segment instead of the list; a segment is a unit of 128 of a key head's R rows.
+struct NoSegments {
+  __device__ __forceinline__ void begin(const TreeList&) {}
+  __device__ __forceinline__ bool next(const TreeList&) { return false; }
+};
+template <int MOD>
+using SegmentsOf = std::conditional_t<(MOD & kModTree) != 0, TreeSegments, NoSegments>;
+
+template <bool CAUSAL, bool GEN, int MOD, typename Segments>
+__device__ __forceinline__ Unit unit1_of(const FwdParams& p, int L, const Segments& sg) {
+  if constexpr ((MOD & kModTree) != 0) {
+    Unit u;
+    u.bh = sg.b * p.mod.list.Hkv + sg.hk;
+    u.qt0 = sg.rb;
+    u.kb = sg.c0;
+    u.ke = sg.c1;
+    u.n_steps = u.nkv[0] = sg.c1 - sg.c0;
+    u.nkv[1] = 0;
+    u.split = sg.whole ? -1 : static_cast<int>(blockIdx.x) + sg.entry;  // the partial's slot
+    u.last[0] = sg.b;
+    u.last[1] = __ldg(p.mod.list.ctx_len + sg.b);
+    u.mh = tree_keys(p.mod.list, u.last[1]);
+    return u;
+  } else if constexpr (MOD != 0) {
     Unit u;
     const int pos = static_cast<int>(p.div_bh.div(static_cast<uint32_t>(L)));
     u.bh = L - pos * p.BH;
@@ -156,6 +180,7 @@ __global__ void __launch_bounds__(Cfg1<D>::kThreads, 1)
                    const __grid_constant__ CUtensorMap tm_v, const __grid_constant__ CUtensorMap tm_o,
                    const FwdParams p) {
   using C = Cfg1<D>;
+  constexpr bool kTree = (MOD & kModTree) != 0;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
   Bars1* bars = reinterpret_cast<Bars1*>(smem + C::kBarOff);
@@ -220,10 +245,13 @@ __global__ void __launch_bounds__(Cfg1<D>::kThreads, 1)
     const bool later_q = (p.flags & kFlagStarveLaterQ) == 0u;
     int g = 0, qn = 0, ql = 0;
     bool ok = true;
-    for (int r = 0; ok && r * grid < p.total_units; ++r) {
+    SegmentsOf<MOD> sg;
+    if constexpr (kTree) sg.begin(p.mod.list);
+    for (int r = 0; ok && (kTree || r * grid < p.total_units); ++r) {
       const int L = unit_index(r, cta, grid);
-      if (L >= p.total_units) continue;
-      const Unit u = unit1_of<CAUSAL, GEN, MOD>(p, L);
+      if (!kTree && L >= p.total_units) continue;
+      if (kTree && !sg.next(p.mod.list)) break;
+      const Unit u = unit1_of<CAUSAL, GEN, MOD>(p, L, sg);
       const int qb = qn & 1;
       if (qn >= 2 && !mbar_wait_warp(&bars->q_empty[qb], ((qn >> 1) - 1) & 1, wc)) { ok = false; break; }
       const bool load = load_q && (later_q || qn == 0);
@@ -287,10 +315,13 @@ __global__ void __launch_bounds__(Cfg1<D>::kThreads, 1)
       const uint32_t q_base = smem_u32(smem + C::kQOff);
       const uint32_t k_base = smem_u32(smem + C::kKOff);
       int g = 0, qn = 0;
-      for (int r = 0; ok && r * grid < p.total_units; ++r) {
+      SegmentsOf<MOD> sg;
+      if constexpr (kTree) sg.begin(p.mod.list);
+      for (int r = 0; ok && (kTree || r * grid < p.total_units); ++r) {
         const int L = unit_index(r, cta, grid);
-        if (L >= p.total_units) continue;
-        const Unit u = unit1_of<CAUSAL, GEN, MOD>(p, L);
+        if (!kTree && L >= p.total_units) continue;
+        if (kTree && !sg.next(p.mod.list)) break;
+        const Unit u = unit1_of<CAUSAL, GEN, MOD>(p, L, sg);
         const int qb = qn & 1;
         if (!mbar_wait_warp(&bars->q_full[qb], (qn >> 1) & 1, wc)) { ok = false; break; }
         for (int j = 0; j < u.n_steps; ++j, ++g) {
@@ -329,10 +360,13 @@ __global__ void __launch_bounds__(Cfg1<D>::kThreads, 1)
       const uint32_t idesc = idesc_bf16(kBlockM, D, true);
       const uint32_t v_base = smem_u32(smem + C::kVOff);
       int g = 0, nunits = 0;
-      for (int r = 0; ok && r * grid < p.total_units; ++r) {
+      SegmentsOf<MOD> sg;
+      if constexpr (kTree) sg.begin(p.mod.list);
+      for (int r = 0; ok && (kTree || r * grid < p.total_units); ++r) {
         const int L = unit_index(r, cta, grid);
-        if (L >= p.total_units) continue;
-        const Unit u = unit1_of<CAUSAL, GEN, MOD>(p, L);
+        if (!kTree && L >= p.total_units) continue;
+        if (kTree && !sg.next(p.mod.list)) break;
+        const Unit u = unit1_of<CAUSAL, GEN, MOD>(p, L, sg);
         for (int j = 0; j < u.n_steps; ++j, ++g) {
           const int st = g % C::kStages;
           const int b = g & 1;
@@ -404,6 +438,10 @@ __global__ void __launch_bounds__(Cfg1<D>::kThreads, 1)
     };
     auto row_out = [&](int bh, int split, int r0) {
       const int q_row = r0 + lane;
+      if constexpr (kTree)  // split: the partial's slot, or −1
+        return RowOut{static_cast<size_t>(bh) * static_cast<size_t>(p.T) + static_cast<size_t>(q_row),
+                      static_cast<size_t>(split) * kBlockM + static_cast<size_t>(row), r0, bh,
+                      q_row < p.T, split >= 0};
       return RowOut{static_cast<size_t>(bh) * static_cast<size_t>(p.T) + static_cast<size_t>(q_row),
                     (static_cast<size_t>(split) * p.BH + bh) * static_cast<size_t>(p.T) +
                         static_cast<size_t>(q_row),
@@ -560,12 +598,13 @@ __global__ void __launch_bounds__(Cfg1<D>::kThreads, 1)
     // thread's 16-byte record in shared memory, not in registers the step loop needs.
     bool pend = false;
     float4* const prec = reinterpret_cast<float4*>(smem + C::kPendOff) + half * kBlockM + row;
-    // (.w = bh + BH·split)
+    // (.w = bh + BH·split; TREE: bh, or −1 − slot)
     auto parked = [&](float& l, float& m) {
       const float4 v = *prec;
       l = v.x;
       m = v.y;
       const int r0 = __float_as_int(v.z), hs = __float_as_int(v.w);
+      if constexpr (kTree) return hs < 0 ? row_out(0, -1 - hs, r0) : row_out(hs, -1, r0);
       const int split = GEN ? hs / p.BH : 0;
       return row_out(hs - split * p.BH, split, r0);
     };
@@ -588,10 +627,13 @@ __global__ void __launch_bounds__(Cfg1<D>::kThreads, 1)
       }
     };
 
-    for (int r = 0; r * grid < p.total_units; ++r) {
+    SegmentsOf<MOD> sg;
+    if constexpr (kTree) sg.begin(p.mod.list);
+    for (int r = 0; kTree || r * grid < p.total_units; ++r) {
       const int L = unit_index(r, cta, grid);
-      if (L >= p.total_units) continue;
-      const Unit u = unit1_of<CAUSAL, GEN, MOD>(p, L);
+      if (!kTree && L >= p.total_units) continue;
+      if (kTree && !sg.next(p.mod.list)) break;
+      const Unit u = unit1_of<CAUSAL, GEN, MOD>(p, L, sg);
       const int n = u.nkv[0];
       const int qt = u.qt0;
       const int q_row = qt * kBlockM + row;
@@ -610,7 +652,22 @@ __global__ void __launch_bounds__(Cfg1<D>::kThreads, 1)
       // MOD: this row's visible keys [lo, hi) and (BIAS) its head's slope in base 2, negated
       int vlo = 0, vhi = 0;
       float nslope = 0.0f;
-      if constexpr (MOD != 0) {
+      // TREE: this row's token, its position, and its sequence's context
+      int tok = 0, ctx = 0;
+      float q_at = 0.0f;
+      if constexpr (kTree) {
+        const int r = min(q_row, p.T - 1);
+        const int hg = static_cast<int>(p.mod.mask.div_tq.div(static_cast<uint32_t>(r)));
+        const int Tq = p.mod.list.Tq;
+        tok = r - hg * Tq;
+        ctx = u.last[1];
+        vhi = min(ctx, u.mh);
+        if constexpr ((MOD & kModBias) != 0) {
+          const int hk = u.bh - u.last[0] * p.mod.list.Hkv;
+          q_at = static_cast<float>(ctx + (p.mod.mask.depths ? p.mod.mask.depths_of(u.last[0], Tq)[tok] : tok));
+          nslope = __ldg(p.mod.slopes + hk * (p.T / Tq) + hg) * -1.4426950408889634f;
+        }
+      } else if constexpr (MOD != 0) {
         const int b = static_cast<int>(p.mod.div_h.div(static_cast<uint32_t>(u.bh)));
         if (p.mod.rows) {
           const int2 r = __ldg(p.mod.rows + static_cast<size_t>(b) * p.mod.T_pad + q_row);
@@ -673,8 +730,8 @@ __global__ void __launch_bounds__(Cfg1<D>::kThreads, 1)
         if constexpr (MOD != 0) {
           // Scores to base-2 exponents in place (fa_mod.cuh); the bias is linear in the key
           // where every key of the step lies at or before the warp's first row.
-          const bool left = k0 + kC - 1 <= qt * kBlockM + quad * 32;
-          const float dist0 = static_cast<float>(q_row - k0);
+          const bool left = kTree ? k0 + kC - 1 <= ctx : k0 + kC - 1 <= qt * kBlockM + quad * 32;
+          const float dist0 = kTree ? q_at - static_cast<float>(k0) : static_cast<float>(q_row - k0);
           const float base = nslope * dist0;
           bool far = false;
           if constexpr ((MOD & kModCap) != 0) far = cap_far<kC>(s, p.mod.cap.limit);
@@ -701,7 +758,59 @@ __global__ void __launch_bounds__(Cfg1<D>::kThreads, 1)
           };
           if (far) to_exponents(true);
           else to_exponents(false);
-          if (masked) {
+          if constexpr (kTree) {
+            // A step that reaches the new tokens: the row's visible keys as bit words, made by a
+            // short loop (this code runs once a segment, so its size is fetch time), then applied.
+            if (masked) {
+              const int Tq = p.mod.list.Tq;
+              const int d0 = k0 - ctx;  // the step's first key as a new token
+              const uint8_t* flags = p.mod.mask.tree ? p.mod.mask.row(u.last[0], tok, Tq) : nullptr;
+              const int* depths = nullptr;
+              if constexpr ((MOD & kModBias) != 0) {
+                if (p.mod.mask.depths) depths = p.mod.mask.depths_of(u.last[0], Tq);
+              }
+              uint32_t bits[kC / 32];
+#pragma unroll
+              for (int w = 0; w < kC / 32; ++w) {
+                const int dw = d0 + w * 32;
+                // context keys, chain keys and rows of the cache: ranges
+                const int n_see = min(max(min(ctx, u.mh) - (k0 + w * 32), 0), 32);
+                uint32_t word = n_see >= 32 ? 0xFFFFFFFFu : (1u << n_see) - 1u;
+                if (flags) {
+#pragma unroll 1
+                  for (int t0 = max(0, -dw) & ~7; t0 < min(32, Tq - dw); t0 += 8) {
+                    uint32_t f[8];
+#pragma unroll
+                    for (int t = 0; t < 8; ++t) f[t] = flags[min(max(dw + t0 + t, 0), Tq - 1)];
+#pragma unroll
+                    for (int t = 0; t < 8; ++t) {
+                      const int dk = dw + t0 + t;
+                      if (dk >= 0 && dk < Tq && ctx + dk < u.mh && f[t] != 0u) word |= 1u << (t0 + t);
+                    }
+                  }
+                } else {
+                  const int n_chain = min(max(min(tok + 1, u.mh - ctx) - dw, 0), 32);
+                  if (dw > -32) word |= n_chain >= 32 ? 0xFFFFFFFFu : (1u << n_chain) - 1u;
+                }
+                bits[w] = word;
+                if constexpr ((MOD & kModBias) != 0) {
+                  if (depths) {  // from the keys' indices to their positions
+                    const int dk = dw + lane;
+                    const float place = static_cast<float>(ctx + (dk < 0 ? dk : depths[min(dk, Tq - 1)]));
+#pragma unroll
+                    for (int t = 0; t < 32; ++t) {
+                      const float at = __shfl_sync(0xffffffffu, place, t);
+                      const float was = fabsf(dist0 - static_cast<float>(w * 32 + t));
+                      s[w * 32 + t] = __float_as_uint(fmaf(nslope, fabsf(q_at - at) - was, u2f(s[w * 32 + t])));
+                    }
+                  }
+                }
+              }
+#pragma unroll
+              for (int t = 0; t < kC; ++t)
+                if (!((bits[t >> 5] >> (t & 31)) & 1u)) s[t] = __float_as_uint(-INFINITY);
+            }
+          } else if (masked) {
             const int vl = vlo - k0;
 #pragma unroll
             for (int t = 0; t < kC; ++t)
@@ -818,7 +927,8 @@ __global__ void __launch_bounds__(Cfg1<D>::kThreads, 1)
         fail_rows(cur);
         continue;
       }
-      *prec = make_float4(l, m_ref, __int_as_float(cur.r0), __int_as_float(cur.bh + p.BH * u.split));
+      *prec = make_float4(l, m_ref, __int_as_float(cur.r0), __int_as_float(kTree ? (u.split < 0 ? u.bh : -1 - u.split)
+                                                                                    : cur.bh + p.BH * u.split));
       pend = true;
     }
     if (pend) flush_pending();  // the last unit's epilogue (its last step is g − 1)

@@ -44,6 +44,7 @@
 #pragma once
 
 #include "fa_mod.cuh"
+#include "fa_tree_walk.cuh"
 #include "sm103.cuh"
 
 // Timeline hooks: compiled out unless a tracing build defines FA_TRACE(tag, step).
@@ -125,22 +126,6 @@ struct Bars {
 };
 static_assert(sizeof(Bars) <= 512, "barrier block");
 
-// Division of 32-bit unsigned numerators by a fixed divisor d ≥ 1 without a divide: with
-// m = ⌈2⁶⁴ / d⌉, ⌊n / d⌋ = ⌊m·n / 2⁶⁴⌋ for every n < 2³² (Lemire, Kaser and Kurz, "Faster
-// remainder by direct computation", 2019, theorem 1). d = 1 is taken apart (m would not fit).
-struct FastDiv {
-  uint64_t m;
-  uint32_t d;
-  static FastDiv make(uint32_t d) { return FastDiv{d > 1u ? ~0ull / d + 1ull : 0ull, d}; }
-  __host__ __device__ __forceinline__ uint32_t div(uint32_t n) const {
-#ifdef __CUDA_ARCH__
-    return d == 1u ? n : static_cast<uint32_t>(__umul64hi(m, n));
-#else
-    return d == 1u ? n : static_cast<uint32_t>((static_cast<unsigned __int128>(m) * n) >> 64);
-#endif
-  }
-};
-
 // Modified scores (the one-tile kernel's MOD instantiations; see fa_mod.cuh).
 struct ModParams {
   const int2* rows;     // [B][T_pad] visible key interval [lo, hi) of each query row, or null
@@ -152,6 +137,8 @@ struct ModParams {
   FastDiv div_g;        // bh / (H / Hkv) = the key head's index
   CapFactors cap;       // (CAP)
   int causal;           // without rows: key j visible to query i iff j ≤ i (else every key)
+  TreeList list;        // TREE: new tokens against a cache (fa_tree_walk.cuh); T above is then R,
+  TreeMask mask;        //   BH counts key heads, and o_part, lse_part are [slots][128][D], [slots][128]
 };
 
 struct FwdParams {

@@ -56,6 +56,9 @@ cudaError_t launch_decode_multi(const DecodeParams& p, int d, unsigned combine_g
 // Modified scores (fa_mod.cuh) on the one-tile kernel, mod the kMod… bits.
 cudaError_t launch_fwd_mod_d64(const FwdLaunch& a, int mod);
 cudaError_t launch_fwd_mod_d128(const FwdLaunch& a, int mod);
+// New tokens against a cache on the same kernel (a.p.T the rows a key head, a.grid the stretches).
+cudaError_t launch_fwd_tree_d64(const FwdLaunch& a, int mod);
+cudaError_t launch_fwd_tree_d128(const FwdLaunch& a, int mod);
 
 struct BwdLaunch {
   CUtensorMap tm_q, tm_k, tm_v, tm_do;

@@ -16,9 +16,26 @@
 
 namespace fa {
 
+// Division of 32-bit unsigned numerators by a fixed divisor d ≥ 1 without a divide: with
+// m = ⌈2⁶⁴ / d⌉, ⌊n / d⌋ = ⌊m·n / 2⁶⁴⌋ for every n < 2³² (Lemire, Kaser and Kurz, "Faster
+// remainder by direct computation", 2019, theorem 1). d = 1 is taken apart (m would not fit).
+struct FastDiv {
+  uint64_t m;
+  uint32_t d;
+  static FastDiv make(uint32_t d) { return FastDiv{d > 1u ? ~0ull / d + 1ull : 0ull, d}; }
+  __host__ __device__ __forceinline__ uint32_t div(uint32_t n) const {
+#ifdef __CUDA_ARCH__
+    return d == 1u ? n : static_cast<uint32_t>(__umul64hi(m, n));
+#else
+    return d == 1u ? n : static_cast<uint32_t>((static_cast<unsigned __int128>(m) * n) >> 64);
+#endif
+  }
+};
+
 constexpr int kModOn = 1;    // modified scores with row intervals
 constexpr int kModCap = 2;   // tanh cap
 constexpr int kModBias = 4;  // distance bias
+constexpr int kModTree = 8;  // new tokens against a cache (fa_tree_walk.cuh)
 
 // The cap. With u = z / cap, tanh(u) is
 //   |u| ≤ 0.8:  u · P(u²), P of degree 5, fitted to tanh(u)/u by iteratively reweighted least

@@ -8,12 +8,17 @@
 // The angle. A float product of a far position and a frequency loses the angle itself (at
 // position 10⁶ an fp32 step is 0.06 rad), so it is kept as a fixed-point fraction of a turn:
 // frequency / 2π in units of 2⁻⁶⁴ turns, multiplied by the integer position modulo 2⁶⁴, which
-// drops whole turns exactly. The top 32 bits, as a signed fraction of a turn, go to sincospif.
+// drops whole turns exactly. The top 32 bits are the angle within ±π, where __cosf and __sinf are
+// within 2⁻²¹ of the values: against the results' rounding to bf16, 2⁻⁹ of theirs, no choice of
+// the slower functions could show.
+// Each block makes the fixed-point frequencies once, in shared memory: five fp64 operations a
+// pair, of which an SM does two lanes a clock (every thread making its own took 13 of the 20 µs
+// of B4 H12+12 T1024 d64).
 //
 // The kernel moves bytes: each row is read and written once (2 + 2 bytes an element against
 // three multiply-adds a dimension). A thread owns 8 pairs (two 16-byte vectors) of one (batch,
-// position) and walks up to kHeads heads with them, so the angles' 64-bit products and eight
-// sincospif are paid once for all its heads; four heads' loads are in flight together. Reading
+// position) and walks several heads with them, so the angles' 64-bit products, sines and cosines
+// are paid once for all its heads; four heads' loads are in flight together. Reading
 // with the caller's strides lets a packed projection [B, T, heads, d] be turned straight into
 // the contiguous [B, H, T, d] that attention reads.
 #include <cuda_bf16.h>
@@ -49,7 +54,11 @@ struct RopeParams {
   float mscale, sign;
 };
 
-constexpr int kRopeThreads = 256;
+// 128 threads at 64 registers, eight blocks an SM: B1 H16+4 T16384 d128 (168 MB) 29.9 µs, 5.6 TB/s;
+// B4 H12+12 T1024 d64 (25 MB) 7.9. (256 threads at 72 registers 32.1 and 8.4; two heads in
+// flight at 48 registers 31.5 and 7.5; 42 registers, which spill, 40.7 and 10.3.)
+constexpr int kRopeThreads = 128;
+constexpr int kRopeBlocks = 8;
 constexpr int kRopeFlight = 4;  // heads whose loads a thread keeps in flight
 
 __device__ __forceinline__ void unpack8(const uint4& w, float* f) {
@@ -62,9 +71,15 @@ __device__ __forceinline__ void unpack8(const uint4& w, float* f) {
 }
 
 template <bool INTER, bool APPEND>
-__global__ void __launch_bounds__(kRopeThreads) fa_rope_kernel(const RopeParams p) {
+__global__ void __launch_bounds__(kRopeThreads, kRopeBlocks) fa_rope_kernel(const RopeParams p) {
+  __shared__ unsigned long long turns[64];  // turns a position, in 2⁻⁶⁴
   pdl_wait();
   pdl_launch_dependents();
+  if (threadIdx.x < 8 * p.rot_units) {
+    const double f = p.inv_freq[threadIdx.x] * 0.15915494309189533577;  // 1 / 2π
+    turns[threadIdx.x] = __double2ull_rn((f - floor(f)) * 18446744073709551616.0);
+  }
+  __syncthreads();
   const unsigned ch = blockIdx.x / p.n_blocks;
   const long long item = static_cast<long long>(blockIdx.x - ch * p.n_blocks) * kRopeThreads + threadIdx.x;
   if (item >= p.n_items) return;
@@ -92,13 +107,10 @@ __global__ void __launch_bounds__(kRopeThreads) fa_rope_kernel(const RopeParams 
     const int pos = p.positions ? p.positions[p.pos_per_batch ? row : t] : ctx + t;
 #pragma unroll
     for (int e = 0; e < 8; ++e) {
-      const double turns = p.inv_freq[u * 8 + e] * 0.15915494309189533577;  // 1 / 2π
-      const unsigned long long f = __double2ull_rn((turns - floor(turns)) * 18446744073709551616.0);
-      const unsigned long long a = f * static_cast<unsigned long long>(static_cast<long long>(pos));
-      const float half = static_cast<float>(static_cast<int>(a >> 32)) * 4.656612873077393e-10f;  // 2⁻³¹
-      sincospif(half, &sn[e], &cs[e]);
-      cs[e] *= p.mscale;
-      sn[e] *= p.mscale * p.sign;
+      const unsigned long long a = turns[u * 8 + e] * static_cast<unsigned long long>(static_cast<long long>(pos));
+      const float x = static_cast<float>(static_cast<int>(a >> 32)) * 1.4629180792671596e-9f;  // 2π·2⁻³²
+      cs[e] = __cosf(x) * p.mscale;
+      sn[e] = __sinf(x) * (p.mscale * p.sign);
     }
   }
   for (int hb = h0; hb < h1; hb += kRopeFlight) {
@@ -182,10 +194,10 @@ int rope_launch(RopeParams& p, bool append, int interleaved, int d, void* stream
   p.heads = p.H + p.Hkv * (append ? 2 : 1);
   p.n_items = static_cast<long long>(p.B) * p.T * p.d_units;
   const long long blocks = (p.n_items + kRopeThreads - 1) / kRopeThreads;
-  // Heads a thread walks: as many as leave every SM four blocks, so that the angles are shared
+  // Heads a thread walks: as many as leave every SM its eight blocks, so that the angles are shared
   // widely on long sequences and a short call spreads over the GPU.
   long long chunk = p.heads;
-  while (chunk > 1 && blocks * ((p.heads + chunk - 1) / chunk) < 4LL * sms) chunk = (chunk + 1) / 2;
+  while (chunk > 1 && blocks * ((p.heads + chunk - 1) / chunk) < static_cast<long long>(kRopeBlocks) * sms) chunk = (chunk + 1) / 2;
   p.chunk = static_cast<int>(chunk);
   const long long grid = blocks * ((p.heads + chunk - 1) / chunk);
   if (grid > INT32_MAX) return FA_ERR_INVALID_ARG;

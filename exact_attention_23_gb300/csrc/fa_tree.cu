@@ -11,6 +11,7 @@
 
 #include "fa.h"
 #include "fa_host.h"
+#include "fa_launch.h"
 #include "fa_mod_host.h"
 #include "fa_pdl.h"
 #include "fa_tree_kernel.cuh"
@@ -24,7 +25,7 @@ namespace {
 struct TreeLaunch {
   CUtensorMap tm_k, tm_v;
   TreeParams p;
-  unsigned grid, combine_grid;
+  unsigned grid;
   cudaStream_t stream;
 };
 
@@ -35,10 +36,7 @@ cudaError_t launch_tree(const TreeLaunch& a) {
   static std::atomic<uint64_t> done[kMaxDevices / 64 + 1];
   cudaError_t e = smem_opt_in(fn, smem, done);
   if (e != cudaSuccess) return e;
-  e = launch_pdl(fn, a.grid, kTreeBlock, smem, a.stream, a.tm_k, a.tm_v, a.p);
-  if (e != cudaSuccess) return e;
-  return launch_pdl(fa_tree_combine_kernel<D, RG * 16>, a.combine_grid, 256, 0, a.stream, a.p,
-                    static_cast<int>(a.grid));
+  return launch_pdl(fn, a.grid, kTreeBlock, smem, a.stream, a.tm_k, a.tm_v, a.p);
 }
 
 template <int D, int RG>
@@ -54,18 +52,21 @@ cudaError_t launch_tree_mod(const TreeLaunch& a, int mod) {
 template <int D>
 cudaError_t launch_tree_rows(const TreeLaunch& a, int rows, int mod) {
   return rows == 16 ? launch_tree_mod<D, 1>(a, mod)
-                    : rows == 32 ? launch_tree_mod<D, 2>(a, mod) : launch_tree_mod<D, 4>(a, mod);
+                    : launch_tree_mod<D, 2>(a, mod);
 }
 
-// Rows a block: the fewest of 16, 32, 64 that hold all R, so that the keys are read once; more
-// rows than 64 go in blocks of 64, whose later ones find the keys in L2.
-int block_rows(int R) { return R <= 16 ? 16 : R <= 32 ? 32 : 64; }
+// Up to 32 rows of a key head: the streaming kernel, in one block of 16 or 32 rows, so that the
+// keys are read once. More: blocks of 128 rows on the one-tile tensor-core kernel (B4 H16 Hkv4,
+// 16 tokens, 64 rows, 16384 keys, d = 128: SIDE_A against SIDE_B µs with 64 rows on mma.sync,
+// whose products then take longer than the keys' bytes).
+bool wide(int R) { return R > 32; }
+int block_rows_log2(int R) { return R <= 16 ? 4 : R <= 32 ? 5 : 7; }
 
-// Chunks a stretch has at least: under two the merge costs more than the parallelism gives.
-constexpr int kMinPer = 2;
+// Chunks a stretch has at least.
+constexpr int kMinPer = 2, kMinPerWide = 1;
 
 struct TreeSizes {
-  int R, rows, row_blocks;
+  int R, rows_log2, row_blocks, chunk_log2, min_per;
   long long entries, grid, slots;
   size_t lse_off, bytes;
 };
@@ -76,19 +77,22 @@ bool tree_sizes(int B, int H, int Hkv, int Tq, int Tmax, int d, int sms, TreeSiz
   const long long R = static_cast<long long>(H / Hkv) * Tq, BHkv = static_cast<long long>(B) * Hkv;
   if (static_cast<long long>(B) * H > INT32_MAX || R > (1 << 24) || Tmax > (1 << 30)) return false;
   z->R = static_cast<int>(R);
-  z->rows = block_rows(z->R);
-  z->row_blocks = (z->R + z->rows - 1) / z->rows;
+  z->rows_log2 = block_rows_log2(z->R);
+  z->row_blocks = (z->R + (1 << z->rows_log2) - 1) >> z->rows_log2;
+  z->chunk_log2 = wide(z->R) ? 7 : 6;
+  z->min_per = wide(z->R) ? kMinPerWide : kMinPer;
   z->entries = BHkv * z->row_blocks;
   if (z->entries > (1 << 28) || BHkv * R > (1LL << 40) || BHkv > (1LL << 60) / d / Tmax) return false;
-  const long long chunks = (static_cast<long long>(Tmax) + kTreeKeys - 1) / kTreeKeys;
-  if (z->entries * chunks > INT32_MAX - 64) return false;  // (the kernel numbers them with an int)
-  const long long most = (z->entries * chunks + kMinPer - 1) / kMinPer;
-  const long long fit = static_cast<long long>(sms) * (d == 64 ? TreeCfg<64>::kCtasPerSm : TreeCfg<128>::kCtasPerSm);
+  const long long chunks = (static_cast<long long>(Tmax) + (1 << z->chunk_log2) - 1) >> z->chunk_log2;
+  if (z->entries * chunks > INT32_MAX - 128) return false;  // (the kernels number them with an int)
+  const long long most = (z->entries * chunks + z->min_per - 1) / z->min_per;
+  const long long fit = static_cast<long long>(sms) *
+                        (wide(z->R) ? 1 : d == 64 ? TreeCfg<64>::kCtasPerSm : TreeCfg<128>::kCtasPerSm);
   z->grid = std::max<long long>(1, std::min(fit, most));
   z->slots = z->grid + z->entries;
   auto up = [](size_t x) { return (x + 255u) / 256u * 256u; };
-  z->lse_off = up(static_cast<size_t>(z->slots) * z->rows * d * 4);
-  z->bytes = z->lse_off + up(static_cast<size_t>(z->slots) * z->rows * 4);
+  z->lse_off = up((static_cast<size_t>(z->slots) << z->rows_log2) * d * 4);
+  z->bytes = z->lse_off + up((static_cast<size_t>(z->slots) << z->rows_log2) * 4);
   return true;
 }
 
@@ -142,41 +146,72 @@ int fa_fwd_tree(const void* q, const void* k_cache, const void* v_cache, void* o
   if (dst != FA_OK) return dst;
   EncodeTiledFn enc = encode_fn();
   if (!enc) return FA_ERR_LAUNCH;
-  fa::TreeLaunch a;
-  if (!encode_map(enc, &a.tm_k, k_cache, Tmax, d, B * Hkv, fa::kTreeKeys) ||
-      !encode_map(enc, &a.tm_v, v_cache, Tmax, d, B * Hkv, fa::kTreeKeys))
-    return FA_ERR_INVALID_ARG;
   uint8_t* ws = static_cast<uint8_t*>(workspace);
+  fa::TreeLaunch a;
   a.p = fa::TreeParams{};
   a.p.q = static_cast<const __nv_bfloat16*>(q);
   a.p.o = static_cast<__nv_bfloat16*>(o);
   a.p.lse = lse;
   a.p.o_part = reinterpret_cast<float*>(ws);
   a.p.lse_part = reinterpret_cast<float*>(ws + z.lse_off);
-  a.p.ctx_len = ctx_len;
-  a.p.tree = tree;
-  a.p.depths = depths;
   a.p.slopes = slopes;
   a.p.status = status;
   a.p.timeout_ns = timeout_ns ? timeout_ns : 2000000000ull;
-  a.p.div_tq = fa::FastDiv::make(static_cast<uint32_t>(Tq));
+  a.p.list = fa::TreeList{ctx_len, B, Hkv, Tq, Tmax, z.row_blocks, z.min_per, z.chunk_log2};
+  a.p.mask = fa::TreeMask{tree, depths, fa::FastDiv::make(static_cast<uint32_t>(Tq)), tree_per_batch != 0,
+                          depths_per_batch != 0};
   a.p.cap = cap;
   a.p.scale_log2 = static_cast<float>(static_cast<double>(scale) * kLog2e);
-  a.p.tree_per_batch = tree_per_batch != 0;
-  a.p.depths_per_batch = depths_per_batch != 0;
-  a.p.B = B;
-  a.p.Hkv = Hkv;
   a.p.R = z.R;
-  a.p.Tq = Tq;
-  a.p.Tmax = Tmax;
-  a.p.row_blocks = z.row_blocks;
-  a.p.min_per = fa::kMinPer;
   a.grid = static_cast<unsigned>(z.grid);
-  const long long rows = static_cast<long long>(B) * Hkv * z.R;
-  a.combine_grid = static_cast<unsigned>(std::min<long long>((rows + 7) / 8, static_cast<long long>(sms) * 8));
   a.stream = static_cast<cudaStream_t>(stream);
-  const int mod = mod_bits(softcap, slopes);
-  const cudaError_t e = (d == 64) ? fa::launch_tree_rows<64>(a, z.rows, mod) : fa::launch_tree_rows<128>(a, z.rows, mod);
+  const int mod = mod_bits(softcap, slopes), BHkv = B * Hkv;
+  const int box = 1 << z.chunk_log2;
+  if (!encode_map(enc, &a.tm_k, k_cache, Tmax, d, BHkv, box) || !encode_map(enc, &a.tm_v, v_cache, Tmax, d, BHkv, box))
+    return FA_ERR_INVALID_ARG;
+  cudaError_t e;
+  if (fa::wide(z.R)) {
+    fa::FwdLaunch f;
+    f.p = fa::FwdParams{};
+    f.tm_k = a.tm_k;
+    f.tm_v = a.tm_v;
+    if (!encode_map(enc, &f.tm_q, q, z.R, d, BHkv) || !encode_map(enc, &f.tm_o, o, z.R, d, BHkv, 32))
+      return FA_ERR_INVALID_ARG;
+    f.p.o = a.p.o;
+    f.p.lse = lse;
+    f.p.o_part = a.p.o_part;
+    f.p.lse_part = a.p.lse_part;
+    f.p.status = status;
+    f.p.timeout_ns = a.p.timeout_ns;
+    f.p.T = z.R;
+    f.p.BH = BHkv;
+    f.p.tiles_per_cta = 1;
+    f.p.div_bh = fa::FastDiv::make(1u);
+    f.p.div_splits = fa::FastDiv::make(1u);
+    f.p.scale_log2 = a.p.scale_log2;
+    f.p.Tk = Tmax;
+    f.p.n_qt = z.row_blocks;
+    f.p.n_kv = (Tmax + 127) / 128;
+    f.p.n_splits = 1;
+    f.p.bmask_heads = 1;
+    f.p.mod.slopes = slopes;
+    f.p.mod.H = H;
+    f.p.mod.div_h = fa::FastDiv::make(1u);
+    f.p.mod.div_g = fa::FastDiv::make(1u);
+    f.p.mod.cap = cap;
+    f.p.mod.list = a.p.list;
+    f.p.mod.mask = a.p.mask;
+    f.grid = a.grid;
+    f.stream = a.stream;
+    e = (d == 64) ? fa::launch_fwd_tree_d64(f, mod) : fa::launch_fwd_tree_d128(f, mod);
+  } else {
+    e = (d == 64) ? fa::launch_tree_rows<64>(a, 1 << z.rows_log2, mod) : fa::launch_tree_rows<128>(a, 1 << z.rows_log2, mod);
+  }
+  if (e != cudaSuccess) return FA_ERR_LAUNCH;
+  const long long rows = static_cast<long long>(BHkv) * z.R;
+  const unsigned cg = static_cast<unsigned>(std::min<long long>((rows + 7) / 8, static_cast<long long>(sms) * 8));
+  auto* combine = d == 64 ? &fa::fa_tree_combine_kernel<64> : &fa::fa_tree_combine_kernel<128>;
+  e = fa::launch_pdl(combine, cg, 256, 0, a.stream, a.p, z.rows_log2, static_cast<int>(a.grid));
   return e == cudaSuccess ? FA_OK : FA_ERR_LAUNCH;
 }
 

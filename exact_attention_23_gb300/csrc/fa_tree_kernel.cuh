@@ -21,17 +21,11 @@
 // quarter (half, all) of each chunk with a running maximum, sum and O of its own, merged once per
 // segment through shared memory. K is read as B fragments by ldmatrix, V by ldmatrix.trans, both
 // conflict-free out of the 128-byte-swizzled boxes that TMA writes.
-//
-// Work is cut by keys, not by sequences: all chunks of all (sequence, key head, row block) are
-// numbered in a row, and CTA c takes the c-th of equal stretches, whatever the lengths are (they
-// live on the device). A stretch crosses sequences in segments; a sequence that lies in several
-// stretches leaves one partial (normalised fp32 rows and LSE) per stretch for
-// fa_tree_combine_kernel. Stretch c's segment of list entry e has slot c + e: from one segment to
-// the next c or e grows, so slots never meet.
 #pragma once
 
 #include "fa_fwd_kernel.cuh"
 #include "fa_mod.cuh"
+#include "fa_tree_walk.cuh"
 #include "sm103.cuh"
 
 namespace fa {
@@ -42,19 +36,14 @@ struct TreeParams {
   float* lse;              // [BHkv][R]
   float* o_part;           // [slots][rows][D]
   float* lse_part;         // [slots][rows]
-  const int* ctx_len;      // [B], < 0: inactive
-  const uint8_t* tree;     // [Tq][Tq] or [B][Tq][Tq], or null (chain)
-  const int* depths;       // [Tq] or [B][Tq], or null (0, 1, 2, …); BIAS
   const float* slopes;     // [H]; BIAS
   int* status;
   uint64_t timeout_ns;
-  FastDiv div_tq;
+  TreeList list;
+  TreeMask mask;
   CapFactors cap;
   float scale_log2;
-  int tree_per_batch, depths_per_batch;
-  int B, Hkv, R, Tq, Tmax;
-  int row_blocks;          // ceil(R / rows)
-  int min_per;             // chunks a stretch has at least
+  int R;                   // query rows a key head: (H / Hkv) · Tq
 };
 
 constexpr int kTreeKeys = 64;        // keys per chunk
@@ -73,91 +62,6 @@ struct TreeCfg {
   static constexpr int kSmemBytes = kMergeOff + 3 * 16 * D * 4 + 1024;  // + alignment slack
 };
 
-// Where a position of the list of all chunks lies.
-struct TreePlace {
-  int b, chunks;     // sequence, its chunks
-  int entry0;        // list entry of the sequence's first (key head, row block)
-  int start;         // position of its first chunk
-};
-
-__device__ __forceinline__ int tree_chunks(const TreeParams& p, int b) {
-  const int ctx = p.ctx_len[b];
-  if (ctx < 0) return 0;
-  const long long keys = static_cast<long long>(ctx) + p.Tq;
-  return static_cast<int>((min(keys, static_cast<long long>(p.Tmax)) + kTreeKeys - 1) / kTreeKeys);
-}
-
-// The list's length, and (x ≥ 0) the sequence that position x lies in; whole warp. (Positions fit
-// an int: the host refuses longer lists.)
-__device__ __forceinline__ int tree_locate(const TreeParams& p, int x, TreePlace* at) {
-  const int lane = threadIdx.x & 31;
-  const int entries = p.Hkv * p.row_blocks;
-  int run = 0;
-  for (int b0 = 0; b0 < p.B; b0 += 32) {
-    const int n = b0 + lane < p.B ? tree_chunks(p, b0 + lane) : 0;
-    int incl = n * entries;
-#pragma unroll
-    for (int off = 1; off < 32; off <<= 1) {
-      const int y = __shfl_up_sync(0xffffffffu, incl, off);
-      if (lane >= off) incl += y;
-    }
-    const int total = __shfl_sync(0xffffffffu, incl, 31);
-    if (x >= run && x < run + total) {
-      const int w = __ffs(__ballot_sync(0xffffffffu, run + incl > x)) - 1;
-      at->b = b0 + w;
-      at->chunks = __shfl_sync(0xffffffffu, n, w);
-      at->start = run + __shfl_sync(0xffffffffu, incl, w) - at->chunks * entries;
-      at->entry0 = at->b * entries;
-    }
-    run += total;
-  }
-  return run;
-}
-
-// Chunks of a stretch, of `stretches` over a list of `total`.
-__device__ __forceinline__ int tree_per(const TreeParams& p, int total, int stretches) {
-  return max((total + stretches - 1) / stretches, p.min_per);
-}
-
-// A stretch's segments in order.
-struct TreeSegments {
-  TreePlace at;
-  int pos, end;                  // next position, past the stretch's last
-  // the current segment
-  int b, hk, rb, entry, c0, c1;  // sequence, key head, row block, list entry, chunks [c0, c1)
-  bool whole;                    // it covers its entry
-  __device__ __forceinline__ void begin(const TreeParams& p) {
-    const int total = tree_locate(p, -1, &at);
-    const int per = tree_per(p, total, gridDim.x);
-    // (a list shorter than grid · min_per leaves later CTAs nothing)
-    pos = static_cast<int>(min(static_cast<long long>(per) * blockIdx.x, static_cast<long long>(total)));
-    end = min(total - pos, per) + pos;
-    if (pos < end) tree_locate(p, pos, &at);
-  }
-  __device__ __forceinline__ bool next(const TreeParams& p) {
-    if (pos >= end) return false;
-    const int entries = p.Hkv * p.row_blocks;
-    int y = pos - at.start;
-    while (y >= at.chunks * entries) {  // the next sequence with chunks
-      at.start += at.chunks * entries;
-      at.entry0 += entries;
-      y = pos - at.start;
-      ++at.b;
-      at.chunks = tree_chunks(p, at.b);
-    }
-    const int e = y / at.chunks;
-    b = at.b;
-    hk = e / p.row_blocks;
-    rb = e - hk * p.row_blocks;
-    entry = at.entry0 + e;
-    c0 = y - e * at.chunks;
-    c1 = min(at.chunks, c0 + (end - pos));
-    whole = c0 == 0 && c1 == at.chunks;
-    pos += c1 - c0;
-    return true;
-  }
-};
-
 __device__ __forceinline__ void ldsm4(uint32_t addr, uint32_t (&r)[4]) {
   asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
                : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(addr) : "memory");
@@ -167,8 +71,7 @@ __device__ __forceinline__ void ldsm4_t(uint32_t addr, uint32_t (&r)[4]) {
                : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(addr) : "memory");
 }
 __device__ __forceinline__ void mma16816(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
-  asm volatile(
-      "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
+  asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
       "{%0,%1,%2,%3};"
       : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
       : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
@@ -204,7 +107,7 @@ __global__ void __launch_bounds__(kTreeBlock, TreeCfg<D>::kCtasPerSm)
   pdl_launch_dependents();
   const WaitCtl wc{&abort_flag, p.status, p.timeout_ns};
   TreeSegments sg;
-  sg.begin(p);
+  sg.begin(p.list);
 
   if (warp == 4) {
     // ---------------------------------------------------------------- producer
@@ -214,8 +117,8 @@ __global__ void __launch_bounds__(kTreeBlock, TreeCfg<D>::kCtasPerSm)
     }
     int n = 0;
     bool ok = true;
-    while (ok && sg.next(p)) {
-      const int bh = sg.b * p.Hkv + sg.hk;
+    while (ok && sg.next(p.list)) {
+      const int bh = sg.b * p.list.Hkv + sg.hk;
       for (int u = 2 * sg.c0; ok && u < 2 * sg.c1; ++u, ++n) {  // K and V tiles in turn
         const int st = n % C::kStages;
         if (n >= C::kStages && !mbar_wait_warp(&empty[st], ((n / C::kStages) - 1) & 1, wc)) {
@@ -248,10 +151,10 @@ __global__ void __launch_bounds__(kTreeBlock, TreeCfg<D>::kCtasPerSm)
   const float nan = __uint_as_float(0x7FC00000u);
   int n = 0;
   bool ok = true;
-  while (sg.next(p)) {
-    const int bh = sg.b * p.Hkv + sg.hk;
-    const int ctx = p.ctx_len[sg.b];
-    const int keys = static_cast<int>(min(static_cast<long long>(ctx) + p.Tq, static_cast<long long>(p.Tmax)));
+  while (sg.next(p.list)) {
+    const int bh = sg.b * p.list.Hkv + sg.hk;
+    const int ctx = p.list.ctx_len[sg.b], Tq = p.list.Tq;
+    const int keys = tree_keys(p.list, ctx);
     const int r0 = sg.rb * kRows + rg * 16 + qr;    // this thread's rows: r0 and r0 + 8
     int tok[2];
     bool live[2];
@@ -260,13 +163,12 @@ __global__ void __launch_bounds__(kTreeBlock, TreeCfg<D>::kCtasPerSm)
     for (int i = 0; i < 2; ++i) {
       const int r = r0 + 8 * i;
       live[i] = r < p.R;
-      const int g = static_cast<int>(p.div_tq.div(static_cast<uint32_t>(live[i] ? r : 0)));
-      tok[i] = (live[i] ? r : 0) - g * p.Tq;
+      const int g = static_cast<int>(p.mask.div_tq.div(static_cast<uint32_t>(live[i] ? r : 0)));
+      tok[i] = (live[i] ? r : 0) - g * Tq;
       if constexpr ((MOD & kModBias) != 0) {
-        const int depth = p.depths ? p.depths[(p.depths_per_batch ? static_cast<size_t>(sg.b) * p.Tq : 0) + tok[i]]
-                                   : tok[i];
+        const int depth = p.mask.depths ? p.mask.depths_of(sg.b, Tq)[tok[i]] : tok[i];
         at[i] = static_cast<float>(ctx + depth);
-        nsl[i] = p.slopes[sg.hk * (p.R / p.Tq) + g] * -1.4426950408889634f;
+        nsl[i] = p.slopes[sg.hk * (p.R / Tq) + g] * -1.4426950408889634f;
       }
     }
     uint32_t qf[D / 16][4];
@@ -293,19 +195,24 @@ __global__ void __launch_bounds__(kTreeBlock, TreeCfg<D>::kCtasPerSm)
       const uint32_t kt = ring + stk * C::kTile, vt = ring + stv * C::kTile;
       const int key0 = c * kTreeKeys + kg * NK;    // this warp's first key
       // ---- S = Q·Kᵀ
+      // (32 dimensions of every key at a time: the fragments' loads stand together in front of
+      // products that do not wait for one another)
       float s[NT][4];
 #pragma unroll
-      for (int j = 0; j < NT; ++j) {
-        s[j][0] = s[j][1] = s[j][2] = s[j][3] = 0.f;
-        const int row = kg * NK + j * 8 + (lane & 7);
+      for (int j = 0; j < NT; ++j) s[j][0] = s[j][1] = s[j][2] = s[j][3] = 0.f;
 #pragma unroll
-        for (int k = 0; k < D / 32; ++k) {
-          uint32_t b[4];
-          const int ch = (k & 1) * 4 + (lane >> 3);
-          ldsm4(kt + (k >> 1) * C::kBoxBytes + row * 128 + ((ch ^ (row & 7)) << 4), b);
-          mma16816(s[j], qf[2 * k], b[0], b[1]);
-          mma16816(s[j], qf[2 * k + 1], b[2], b[3]);
+      for (int k = 0; k < D / 32; ++k) {
+        uint32_t b[NT][4];
+        const int ch = (k & 1) * 4 + (lane >> 3);
+#pragma unroll
+        for (int j = 0; j < NT; ++j) {
+          const int row = kg * NK + j * 8 + (lane & 7);
+          ldsm4(kt + (k >> 1) * C::kBoxBytes + row * 128 + ((ch ^ (row & 7)) << 4), b[j]);
         }
+#pragma unroll
+        for (int j = 0; j < NT; ++j) mma16816(s[j], qf[2 * k], b[j][0], b[j][1]);
+#pragma unroll
+        for (int j = 0; j < NT; ++j) mma16816(s[j], qf[2 * k + 1], b[j][2], b[j][3]);
       }
       __syncwarp();
       if (lane == 0) mbar_arrive(&empty[stk]);
@@ -338,36 +245,39 @@ __global__ void __launch_bounds__(kTreeBlock, TreeCfg<D>::kCtasPerSm)
       // ---- the new tokens' keys: the tree, and their depths in the bias
       const bool tail = key0 + NK > min(ctx, keys);  // (a context may fill the cache)
       if (tail) {
-#pragma unroll 1
-        for (int j = 0; j < NT; ++j)
+        // Flags and depths are loaded for a pair of tiles at once, from clamped places, so that no
+        // load waits for another.
 #pragma unroll
-          for (int i = 0; i < 2; ++i)
+        for (int j0 = 0; j0 < NT; j0 += 2) {
+          int see[2][2][2], dep[2][2];
+#pragma unroll
+          for (int j = 0; j < 2; ++j)
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
-              const int key = key0 + j * 8 + qc + e;
-              const int d = key - ctx;
-              float x = 0.f;  // (a dynamic j must not index s: select by comparing)
+              const int d = key0 + (j0 + j) * 8 + qc + e - ctx, dc = min(max(d, 0), Tq - 1);
 #pragma unroll
-              for (int jj = 0; jj < NT; ++jj)
-                if (jj == j) x = s[jj][2 * i + e];
-              if (d >= 0 || key >= keys) {
-                bool see = key < keys && d < p.Tq;
-                if (see)
-                  see = p.tree ? p.tree[((p.tree_per_batch ? static_cast<size_t>(sg.b) * p.Tq : 0) + tok[i]) * p.Tq + d] != 0
-                               : d <= tok[i];
-                if constexpr ((MOD & kModBias) != 0) {
-                  if (see && p.depths) {  // (without depths the key's index is its position)
-                    const float place = static_cast<float>(
-                        ctx + p.depths[(p.depths_per_batch ? static_cast<size_t>(sg.b) * p.Tq : 0) + d]);
-                    x += nsl[i] * (fabsf(at[i] - place) - fabsf(at[i] - static_cast<float>(key)));
-                  }
-                }
-                if (!see) x = -INFINITY;
-              }
-#pragma unroll
-              for (int jj = 0; jj < NT; ++jj)
-                if (jj == j) s[jj][2 * i + e] = x;
+              for (int i = 0; i < 2; ++i)
+                see[j][e][i] = p.mask.tree ? p.mask.row(sg.b, tok[i], Tq)[dc] : (d <= tok[i] ? 1 : 0);
+              if constexpr ((MOD & kModBias) != 0)
+                dep[j][e] = p.mask.depths ? p.mask.depths_of(sg.b, Tq)[dc] : dc;
             }
+#pragma unroll
+          for (int j = 0; j < 2; ++j)
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+              const int key = key0 + (j0 + j) * 8 + qc + e, d = key - ctx;
+#pragma unroll
+              for (int i = 0; i < 2; ++i) {
+                float& x = s[j0 + j][2 * i + e];
+                if constexpr ((MOD & kModBias) != 0) {  // from the key's index to its position
+                  if (d >= 0)
+                    x += nsl[i] * (fabsf(at[i] - static_cast<float>(ctx + dep[j][e])) -
+                                   fabsf(at[i] - static_cast<float>(key)));
+                }
+                if (key >= keys || (d >= 0 && see[j][e][i] == 0)) x = -INFINITY;
+              }
+            }
+        }
       }
       // ---- online softmax with a lazy reference: in the common step no row's maximum passes its
       // reference by more than τ, and no lane needs another's scores
@@ -423,18 +333,24 @@ __global__ void __launch_bounds__(kTreeBlock, TreeCfg<D>::kCtasPerSm)
           }
         }
 #pragma unroll
-        for (int x = 0; x < D / 16; ++x) {
-          uint32_t b[4];
-          const int ch = (x & 3) * 2 + (lane >> 4);
-          ldsm4_t(vt + (x >> 2) * C::kBoxBytes + row * 128 + ((ch ^ (row & 7)) << 4), b);
-          if (cut) {
-            b[0] &= keep[0];
-            b[1] &= keep[1];
-            b[2] &= keep[0];
-            b[3] &= keep[1];
+        for (int x0 = 0; x0 < D / 16; x0 += 4) {
+          uint32_t b[4][4];
+#pragma unroll
+          for (int x = 0; x < 4; ++x) {
+            const int ch = x * 2 + (lane >> 4);
+            ldsm4_t(vt + (x0 >> 2) * C::kBoxBytes + row * 128 + ((ch ^ (row & 7)) << 4), b[x]);
+            if (cut) {
+              b[x][0] &= keep[0];
+              b[x][1] &= keep[1];
+              b[x][2] &= keep[0];
+              b[x][3] &= keep[1];
+            }
           }
-          mma16816(o[2 * x], pf[k], b[0], b[1]);
-          mma16816(o[2 * x + 1], pf[k], b[2], b[3]);
+#pragma unroll
+          for (int x = 0; x < 4; ++x) {
+            mma16816(o[2 * (x0 + x)], pf[k], b[x][0], b[x][1]);
+            mma16816(o[2 * (x0 + x) + 1], pf[k], b[x][2], b[x][3]);
+          }
         }
       }
       __syncwarp();
@@ -528,23 +444,25 @@ __global__ void __launch_bounds__(kTreeBlock, TreeCfg<D>::kCtasPerSm)
 }
 
 // Joins the partials of the rows whose keys lie in several stretches (of `stretches`, the grid of
-// fa_tree_kernel), and writes the rows of sequences without keys. A warp a row.
-template <int D, int ROWS>
-__global__ void __launch_bounds__(256) fa_tree_combine_kernel(const TreeParams p, int stretches) {
+// the kernel before), and writes the rows of sequences without keys. A warp a row: its lanes read
+// the partials' LSEs side by side, and kFlight partial rows are loaded before the first is used.
+template <int D>
+__global__ void __launch_bounds__(256) fa_tree_combine_kernel(const TreeParams p, int rows_log2, int stretches) {
+  constexpr int kV = D / 32;  // columns a lane
+  constexpr int kFlight = 8;
   pdl_wait();
   pdl_launch_dependents();
   const int lane = threadIdx.x & 31;
-  constexpr int kV = D / 32;  // columns a lane
-  const int entries = p.Hkv * p.row_blocks;
-  const long long rows = static_cast<long long>(p.B) * p.Hkv * p.R;
-  const int total = tree_locate(p, -1, nullptr);
-  const int per = tree_per(p, total, stretches);
+  const int entries = p.list.Hkv * p.list.row_blocks;
+  const long long rows = static_cast<long long>(p.list.B) * p.list.Hkv * p.R;
+  const int total = tree_locate(p.list, -1, nullptr);
+  const int per = tree_per(p.list, total, stretches);
   for (long long row = static_cast<long long>(blockIdx.x) * 8 + (threadIdx.x >> 5); row < rows;
        row += static_cast<long long>(gridDim.x) * 8) {
     const int bh = static_cast<int>(row / p.R);
     const int r = static_cast<int>(row - static_cast<long long>(bh) * p.R);
-    const int b = bh / p.Hkv, hk = bh - b * p.Hkv, rb = r / ROWS;
-    const int chunks = tree_chunks(p, b);
+    const int b = bh / p.list.Hkv, hk = bh - b * p.list.Hkv, rb = r >> rows_log2;
+    const int chunks = tree_chunks(p.list, b);
     __nv_bfloat16* dst = p.o + row * D + lane * kV;
     if (chunks == 0) {
 #pragma unroll
@@ -553,35 +471,56 @@ __global__ void __launch_bounds__(256) fa_tree_combine_kernel(const TreeParams p
       continue;
     }
     int before = 0;  // chunks of the sequences in front
-    for (int x = lane; x < b; x += 32) before += tree_chunks(p, x);
-#pragma unroll
-    for (int off = 16; off > 0; off >>= 1) before += __shfl_xor_sync(0xffffffffu, before, off);
-    const int e = hk * p.row_blocks + rb;
+    for (int x = lane; x < b; x += 32) before += tree_chunks(p.list, x);
+    before = __reduce_add_sync(0xffffffffu, before);
+    const int e = hk * p.list.row_blocks + rb;
     const int s = before * entries + e * chunks;
-    const int c0 = s / per, c1 = (s + chunks - 1) / per;
-    if (c0 == c1) continue;
-    const size_t first = (static_cast<size_t>(c0) + static_cast<size_t>(b) * entries + e) * ROWS + (r - rb * ROWS);
-    float M = -INFINITY;
-    for (int c = lane; c <= c1 - c0; c += 32) M = fmaxf(M, p.lse_part[first + static_cast<size_t>(c) * ROWS]);
-#pragma unroll
-    for (int off = 16; off > 0; off >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, off));
-    const float mu = M == -INFINITY ? 0.f : M;
-    float L = 0.f, acc[kV];
+    const int c0 = s / per, n = (s + chunks - 1) / per - c0 + 1;
+    if (n == 1) continue;
+    const size_t first = ((static_cast<size_t>(c0) + static_cast<size_t>(b) * entries + e) << rows_log2) +
+                         (r - (rb << rows_log2));
+    float M = -INFINITY, L = 0.f, acc[kV];
 #pragma unroll
     for (int x = 0; x < kV; ++x) acc[x] = 0.f;
-#pragma unroll 4
-    for (int c = 0; c <= c1 - c0; ++c) {
-      const size_t at = first + static_cast<size_t>(c) * ROWS;
-      const float w = ex2_approx((p.lse_part[at] - mu) * 1.4426950408889634f);
-      L += w;
-      const float* src = p.o_part + at * D + lane * kV;
+    for (int c32 = 0; c32 < n; c32 += 32) {
+      const int end = min(n, c32 + 32);
+      const float ls = c32 + lane < n ? p.lse_part[first + (static_cast<size_t>(c32 + lane) << rows_log2)] : -INFINITY;
+      float w = 0.f;
+      for (int c = c32; c < end; c += kFlight) {
+        float2 y[kFlight][kV / 2];
 #pragma unroll
-      for (int x = 0; x < kV; x += 2) {
-        const float2 y = *reinterpret_cast<const float2*>(src + x);
-        acc[x] = fmaf(w, y.x, acc[x]);
-        acc[x + 1] = fmaf(w, y.y, acc[x + 1]);
+        for (int i = 0; i < kFlight; ++i) {
+          const float* src = p.o_part + (first + (static_cast<size_t>(min(c + i, n - 1)) << rows_log2)) * D + lane * kV;
+#pragma unroll
+          for (int x = 0; x < kV / 2; ++x) y[i][x] = *reinterpret_cast<const float2*>(src + 2 * x);
+        }
+        if (c == c32) {  // (the first rows are on their way while the weights are made)
+          float m = ls;
+#pragma unroll
+          for (int off = 16; off > 0; off >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, off));
+          m = fmaxf(m, M);
+          const float mu = m == -INFINITY ? 0.f : m;
+          const float f = ex2_approx((M - mu) * 1.4426950408889634f);  // 0 before the first
+          w = ex2_approx((ls - mu) * 1.4426950408889634f);
+          L *= f;
+#pragma unroll
+          for (int x = 0; x < kV; ++x) acc[x] *= f;
+          M = m;
+        }
+#pragma unroll
+        for (int i = 0; i < kFlight; ++i) {
+          const float wi = __shfl_sync(0xffffffffu, w, (c + i) & 31);
+          if (c + i >= n) continue;
+          L += wi;
+#pragma unroll
+          for (int x = 0; x < kV / 2; ++x) {
+            acc[2 * x] = fmaf(wi, y[i][x].x, acc[2 * x]);
+            acc[2 * x + 1] = fmaf(wi, y[i][x].y, acc[2 * x + 1]);
+          }
+        }
       }
     }
+    const float mu = M == -INFINITY ? 0.f : M;
     const float inv = L == 0.f ? 0.f : 1.f / L;
 #pragma unroll
     for (int x = 0; x < kV; x += 2)

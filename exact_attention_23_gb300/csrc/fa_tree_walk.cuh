@@ -1,0 +1,132 @@
+// How attention of new tokens against a cache (fa_fwd_tree) shares out its work, and its mask.
+//
+// The list: for each sequence b with keys, its Hkv key heads times row blocks (the query rows that
+// read the same keys, R = (H / Hkv)·Tq of them, in blocks), each entry with the chunks of the
+// sequence's min(ctx_b + Tq, Tmax) keys.
+//
+// Work is cut by keys, not by sequences: all chunks of all (sequence, key head, row block) are
+// numbered in a row, and CTA c takes the c-th of equal stretches, whatever the lengths are (they
+// live on the device). A stretch crosses sequences in segments; a sequence that lies in several
+// stretches leaves one partial (normalised fp32 rows and LSE) per stretch for
+// fa_tree_combine_kernel. Stretch c's segment of list entry e has slot c + e: from one segment to
+// the next c or e grows, so slots never meet.
+#pragma once
+
+#include "fa_mod.cuh"
+#include "sm103.cuh"
+
+namespace fa {
+
+struct TreeList {
+  const int* ctx_len;  // [B], < 0: inactive
+  int B, Hkv, Tq, Tmax;
+  int row_blocks;      // row blocks a key head
+  int min_per;         // chunks a stretch has at least
+  int chunk_log2;      // keys a chunk: 1 << chunk_log2
+};
+
+struct TreeMask {
+  const uint8_t* tree;  // [Tq][Tq] or [B][Tq][Tq], or null (chain)
+  const int* depths;    // [Tq] or [B][Tq], or null (0, 1, 2, …); BIAS
+  FastDiv div_tq;       // row / Tq = query head within the key head's group
+  int tree_per_batch, depths_per_batch;
+
+  // Row t's flags, and a sequence's depths.
+  __device__ __forceinline__ const uint8_t* row(int b, int t, int Tq) const {
+    return tree + ((tree_per_batch ? static_cast<size_t>(b) * Tq : 0) + t) * Tq;
+  }
+  __device__ __forceinline__ const int* depths_of(int b, int Tq) const {
+    return depths + (depths_per_batch ? static_cast<size_t>(b) * Tq : 0);
+  }
+};
+
+__device__ __forceinline__ int tree_keys(const TreeList& p, int ctx) {
+  return static_cast<int>(min(static_cast<long long>(ctx) + p.Tq, static_cast<long long>(p.Tmax)));
+}
+
+// Where a position of the list of all chunks lies.
+struct TreePlace {
+  int b, chunks;     // sequence, its chunks
+  int entry0;        // list entry of the sequence's first (key head, row block)
+  int start;         // position of its first chunk
+};
+
+__device__ __forceinline__ int tree_chunks(const TreeList& p, int b) {
+  const int ctx = p.ctx_len[b];
+  if (ctx < 0) return 0;
+  const long long keys = static_cast<long long>(ctx) + p.Tq;
+  return static_cast<int>((min(keys, static_cast<long long>(p.Tmax)) + (1 << p.chunk_log2) - 1) >> p.chunk_log2);
+}
+
+// The list's length, and (x ≥ 0) the sequence that position x lies in; whole warp. (Positions fit
+// an int: the host refuses longer lists.)
+__device__ __forceinline__ int tree_locate(const TreeList& p, int x, TreePlace* at) {
+  const int lane = threadIdx.x & 31;
+  const int entries = p.Hkv * p.row_blocks;
+  int run = 0;
+  for (int b0 = 0; b0 < p.B; b0 += 32) {
+    const int n = b0 + lane < p.B ? tree_chunks(p, b0 + lane) : 0;
+    int incl = n * entries;
+#pragma unroll
+    for (int off = 1; off < 32; off <<= 1) {
+      const int y = __shfl_up_sync(0xffffffffu, incl, off);
+      if (lane >= off) incl += y;
+    }
+    const int total = __shfl_sync(0xffffffffu, incl, 31);
+    if (x >= run && x < run + total) {
+      const int w = __ffs(__ballot_sync(0xffffffffu, run + incl > x)) - 1;
+      at->b = b0 + w;
+      at->chunks = __shfl_sync(0xffffffffu, n, w);
+      at->start = run + __shfl_sync(0xffffffffu, incl, w) - at->chunks * entries;
+      at->entry0 = at->b * entries;
+    }
+    run += total;
+  }
+  return run;
+}
+
+// Chunks of a stretch, of `stretches` over a list of `total`.
+__device__ __forceinline__ int tree_per(const TreeList& p, int total, int stretches) {
+  return max((total + stretches - 1) / stretches, p.min_per);
+}
+
+// A stretch's segments in order.
+struct TreeSegments {
+  TreePlace at;
+  int pos, end;                  // next position, past the stretch's last
+  // the current segment
+  int b, hk, rb, entry, c0, c1;  // sequence, key head, row block, list entry, chunks [c0, c1)
+  bool whole;                    // it covers its entry
+  __device__ __forceinline__ void begin(const TreeList& p) {
+    const int total = tree_locate(p, -1, &at);
+    const int per = tree_per(p, total, gridDim.x);
+    // (a list shorter than grid · min_per leaves later CTAs nothing)
+    pos = static_cast<int>(min(static_cast<long long>(per) * blockIdx.x, static_cast<long long>(total)));
+    end = min(total - pos, per) + pos;
+    if (pos < end) tree_locate(p, pos, &at);
+  }
+  __device__ __forceinline__ bool next(const TreeList& p) {
+    if (pos >= end) return false;
+    const int entries = p.Hkv * p.row_blocks;
+    int y = pos - at.start;
+    while (y >= at.chunks * entries) {  // the next sequence with chunks
+      at.start += at.chunks * entries;
+      at.entry0 += entries;
+      y = pos - at.start;
+      ++at.b;
+      at.chunks = tree_chunks(p, at.b);
+    }
+    const int e = y / at.chunks;
+    b = at.b;
+    hk = e / p.row_blocks;
+    rb = e - hk * p.row_blocks;
+    entry = at.entry0 + e;
+    c0 = y - e * at.chunks;
+    c1 = min(at.chunks, c0 + (end - pos));
+    whole = c0 == 0 && c1 == at.chunks;
+    pos += c1 - c0;
+    return true;
+  }
+};
+
+}  // namespace fa

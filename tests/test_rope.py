@@ -2,8 +2,8 @@
 64-bit reference written as complex products.
 
 Bound: the result's rounding to bf16, 2⁻⁸ of the value, and the fp32 arithmetic before it: cosine
-and sine within 2⁻²² (the angle's 2⁻²⁵ half turns, sincospif's 2 ulp, the magnitude's product) and
-three roundings, together at most 2⁻²⁰·m·(|a| + |b|)."""
+and sine within 2⁻²¹ (the functions' documented error in ±π) and 2⁻²² more (the angle's rounding to
+24 bits), and three roundings, together at most 2⁻²⁰·m·(|a| + |b|)."""
 
 import math
 
