@@ -27,7 +27,7 @@ SOURCES = ["fa_api.cu", "fa_fwd1.cu", "fa_fwd1_gen.cu", "fa_fwd_pair.cu", "fa_fw
            "fa_mod_bwd_d64.cu", "fa_mod_bwd_d128.cu", "fa_mod_api.cu", "fa_rope.cu", "fa_tree.cu",
            "fa_tree_wide_d64.cu", "fa_tree_wide_d128.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
-FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "-Xptxas", "-v",
+FLAGS = ["-O3", "-lineinfo", "-std=c++20", "-Xcompiler", "-fPIC", "-Xptxas", "-v",
          "-I", INCLUDE, "-I", CSRC]
 
 

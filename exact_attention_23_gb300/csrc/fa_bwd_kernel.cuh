@@ -470,14 +470,18 @@ __global__ void __launch_bounds__(BwdCfg<D, MOD>::kThreads, 1)
     }
     __syncwarp();
     const bool starve = (p.flags & kBwdFlagStarveQ) != 0u;
+    int ti = 0, hg = 0;  // MOD: the step's query tile within the walk, its head within the group
     for (int t = 0, st = 0, ph = 0; t < n && !starve; ++t) {
       if (t >= NS && !mbar_wait_warp_inl(&bars->q_empty[st], ph ^ 1, wc)) break;
       FA_TRACE(30, t);
       int i = i0 + t, bq = bh;  // query tile and (b·h) of this step
       if constexpr (MOD != 0) {
-        const int hg = t / n_i;
-        i = i0 + t - hg * n_i;
+        i = i0 + ti;
         bq = bh * p.mod.group + hg;
+        if (++ti == n_i) {
+          ti = 0;
+          ++hg;
+        }
       }
       if (lane == 0) {
         uint8_t* stage = sm + C::kStage0 + st * C::kStageBytes;
@@ -539,12 +543,14 @@ __global__ void __launch_bounds__(BwdCfg<D, MOD>::kThreads, 1)
         __syncwarp();
       }
     }
+    int ti = 0;  // MOD: the step's query tile within the walk
     for (int t = 0, st = 0, ph = 0; t < n && ok; ++t) {
       if (!(ok = mbar_wait_warp_inl(&bars->q_full[st], ph, wc))) break;
       if (t > 0 && !(ok = mbar_wait_warp_inl(&bars->s_free, (t - 1) & 1, wc))) break;
       FA_TRACE(1, t);
       if constexpr (MOD != 0) {
-        const int i = i0 + t % n_i;
+        const int i = i0 + ti;
+        if (++ti == n_i) ti = 0;
         if (used < (i + 1) * C::kBQ) {
 #pragma unroll
           for (int b = 0; b < D / 64; ++b) {
@@ -674,14 +680,18 @@ __global__ void __launch_bounds__(BwdCfg<D, MOD>::kThreads, 1)
     // earlier must have read it.
     const uint32_t stage0 = sbase + C::kDQStage + qd * 2 * C::kDQChunk;
     int nchunk = 0;
+    int ti = 0, hg = 0;  // MOD: as in the producer
     for (; t < n; ++t) {
       if (!(ok = mbar_wait_warp_inl(&bars->dq_full, t & 1, wc))) break;
       FA_TRACE(20, t);
       int it = i0 + t, bq = bh;
       if constexpr (MOD != 0) {
-        const int hg = t / n_i;
-        it = i0 + t - hg * n_i;
+        it = i0 + ti;
         bq = bh * p.mod.group + hg;
+        if (++ti == n_i) {
+          ti = 0;
+          ++hg;
+        }
       }
       tc_fence_after_sync();
       // 32 columns at a time; the buffer is released once the last columns are in registers.
@@ -787,43 +797,48 @@ __global__ void __launch_bounds__(BwdCfg<D, MOD>::kThreads, 1)
         const float base = nslope * dist0;
         const float2* l2 = reinterpret_cast<const float2*>(vec + g * NC);
         const int2* iv = reinterpret_cast<const int2*>(vec + 2 * C::kBQ) + g * NC;
+        auto probabilities = [&]<bool FAR, bool LEFT>() {
+#pragma unroll
+          for (int c = 0; c < NC; c += 2) {
+            const float2 l = l2[c / 2];
+            uint64_t x2 = f2_pack(l.x, l.y), bend = 0ull;
+            const uint64_t s2 = f2_pack(__uint_as_float(s[c]), __uint_as_float(s[c + 1]));
+            if constexpr ((MOD & kModBias) != 0) {
+              const float c0 = static_cast<float>(c), c1 = static_cast<float>(c + 1);
+              x2 = f2_add(x2, LEFT ? f2_pack(fmaf(nslope, c0, base), fmaf(nslope, c1, base))
+                                   : f2_pack(nslope * fabsf(dist0 + c0), nslope * fabsf(dist0 + c1)));
+            }
+            if constexpr ((MOD & kModCap) != 0) {
+              const uint64_t z2 = cap2<FAR>(s2, p.mod.cap);
+              x2 = f2_add(z2, x2);
+              bend = f2_fma(f2_mul(z2, z2), f2_splat(p.mod.cap.bend), f2_splat(1.0f));  // 1 − tanh²
+            } else {
+              x2 = f2_fma(s2, c2, x2);
+            }
+            float x[2];
+            f2_unpack(x2, x[0], x[1]);
+            if (part) {
+              if (p.mod.rows) {
+                const int2 v0 = iv[c], v1 = iv[c + 1];
+                if (key < v0.x || key >= v0.y) x[0] = __int_as_float(0xff800000);
+                if (key < v1.x || key >= v1.y) x[1] = __int_as_float(0xff800000);
+              } else {
+                if (key > q0 + c) x[0] = __int_as_float(0xff800000);
+                if (key > q0 + c + 1) x[1] = __int_as_float(0xff800000);
+              }
+            }
+            pr[c] = ex2_approx(x[0]);
+            pr[c + 1] = ex2_approx(x[1]);
+            pkm[c / 2] = pack_bf16x2(pr[c], pr[c + 1]);
+            if constexpr ((MOD & kModCap) != 0)
+              f2_unpack(f2_mul(f2_pack(pr[c], pr[c + 1]), bend), pr[c], pr[c + 1]);
+          }
+        };
         bool far = false;
         if constexpr ((MOD & kModCap) != 0) far = cap_far<NC>(s, p.mod.cap.limit);
-#pragma unroll
-        for (int c = 0; c < NC; c += 2) {
-          const float2 l = l2[c / 2];
-          uint64_t x2 = f2_pack(l.x, l.y), f2 = 0ull;
-          const uint64_t s2 = f2_pack(__uint_as_float(s[c]), __uint_as_float(s[c + 1]));
-          if constexpr ((MOD & kModBias) != 0) {
-            const float c0 = static_cast<float>(c), c1 = static_cast<float>(c + 1);
-            x2 = f2_add(x2, left ? f2_pack(fmaf(nslope, c0, base), fmaf(nslope, c1, base))
-                                 : f2_pack(nslope * fabsf(dist0 + c0), nslope * fabsf(dist0 + c1)));
-          }
-          if constexpr ((MOD & kModCap) != 0) {
-            const uint64_t th = cap_tanh2(__uint_as_float(s[c]), __uint_as_float(s[c + 1]), p.mod.cap, far);
-            x2 = f2_fma(th, f2_splat(p.mod.cap.out), x2);
-            f2 = f2_fma(f2_mul(th, f2_splat(-1.0f)), th, f2_splat(1.0f));
-          } else {
-            x2 = f2_fma(s2, c2, x2);
-          }
-          float x[2], f[2];
-          f2_unpack(x2, x[0], x[1]);
-          f2_unpack(f2, f[0], f[1]);
-          if (part) {
-            if (p.mod.rows) {
-              const int2 v0 = iv[c], v1 = iv[c + 1];
-              if (key < v0.x || key >= v0.y) x[0] = __int_as_float(0xff800000);
-              if (key < v1.x || key >= v1.y) x[1] = __int_as_float(0xff800000);
-            } else {
-              if (key > q0 + c) x[0] = __int_as_float(0xff800000);
-              if (key > q0 + c + 1) x[1] = __int_as_float(0xff800000);
-            }
-          }
-          const float p0 = ex2_approx(x[0]), p1 = ex2_approx(x[1]);
-          pkm[c / 2] = pack_bf16x2(p0, p1);
-          pr[c] = (MOD & kModCap) != 0 ? p0 * f[0] : p0;
-          pr[c + 1] = (MOD & kModCap) != 0 ? p1 * f[1] : p1;
-        }
+        if (far) probabilities.template operator()<true, false>();
+        else if ((MOD & kModBias) != 0 && !left) probabilities.template operator()<false, false>();
+        else probabilities.template operator()<false, true>();
         if (++ti == n_i) {
           ti = 0;
           ++hg;

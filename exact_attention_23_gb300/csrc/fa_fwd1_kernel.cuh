@@ -181,6 +181,7 @@ __global__ void __launch_bounds__(Cfg1<D>::kThreads, 1)
                    const FwdParams p) {
   using C = Cfg1<D>;
   constexpr bool kTree = (MOD & kModTree) != 0;
+  constexpr bool kXform = (MOD & (kModCap | kModBias)) != 0;  // scores are modified before the softmax
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
   Bars1* bars = reinterpret_cast<Bars1*>(smem + C::kBarOff);
@@ -728,36 +729,39 @@ __global__ void __launch_bounds__(Cfg1<D>::kThreads, 1)
         if (lane == 0) mbar_arrive(&bars->s_free[b]);
         FA1_TRACE(20, j);
         if constexpr (MOD != 0) {
-          // Scores to base-2 exponents in place (fa_mod.cuh); the bias is linear in the key
-          // where every key of the step lies at or before the warp's first row.
+          // Capped or biased scores to base-2 exponents in place (fa_mod.cuh); the bias is linear
+          // in the key where every key of the step lies at or before the warp's first row. (A far
+          // step, rare, takes the general bias.)
           const bool left = kTree ? k0 + kC - 1 <= ctx : k0 + kC - 1 <= qt * kBlockM + quad * 32;
           const float dist0 = kTree ? q_at - static_cast<float>(k0) : static_cast<float>(q_row - k0);
           const float base = nslope * dist0;
-          bool far = false;
-          if constexpr ((MOD & kModCap) != 0) far = cap_far<kC>(s, p.mod.cap.limit);
-          auto to_exponents = [&](bool far_) {
+          auto to_exponents = [&]<bool FAR, bool LEFT>() {
 #pragma unroll
             for (int t = 0; t < kC; t += 2) {
-              uint64_t add = 0ull, x2;
+              const uint64_t s2 = f2_pack(u2f(s[t]), u2f(s[t + 1]));
+              const float t0 = static_cast<float>(t), t1 = static_cast<float>(t + 1);
+              uint64_t x2;
               if constexpr ((MOD & kModBias) != 0) {
-                const float t0 = static_cast<float>(t), t1 = static_cast<float>(t + 1);
-                add = left ? f2_pack(fmaf(-nslope, t0, base), fmaf(-nslope, t1, base))
-                           : f2_pack(nslope * fabsf(dist0 - t0), nslope * fabsf(dist0 - t1));
+                const uint64_t add = LEFT ? f2_pack(fmaf(-nslope, t0, base), fmaf(-nslope, t1, base))
+                                          : f2_pack(nslope * fabsf(dist0 - t0), nslope * fabsf(dist0 - t1));
+                if constexpr ((MOD & kModCap) != 0) x2 = f2_add(cap2<FAR>(s2, p.mod.cap), add);
+                else x2 = f2_fma(s2, f2_splat(c), add);
+              } else {
+                x2 = cap2<FAR>(s2, p.mod.cap);
               }
-              if constexpr ((MOD & kModCap) != 0)
-                x2 = f2_fma(cap_tanh2(u2f(s[t]), u2f(s[t + 1]), p.mod.cap, far_), f2_splat(p.mod.cap.out), add);
-              else if constexpr ((MOD & kModBias) != 0)
-                x2 = f2_fma(f2_pack(u2f(s[t]), u2f(s[t + 1])), f2_splat(c), add);
-              else
-                x2 = f2_mul(f2_pack(u2f(s[t]), u2f(s[t + 1])), f2_splat(c));
               float x0, x1;
               f2_unpack(x2, x0, x1);
               s[t] = __float_as_uint(x0);
               s[t + 1] = __float_as_uint(x1);
             }
           };
-          if (far) to_exponents(true);
-          else to_exponents(false);
+          if constexpr (kXform) {
+            bool far = false;
+            if constexpr ((MOD & kModCap) != 0) far = cap_far<kC>(s, p.mod.cap.limit);
+            if (far) to_exponents.template operator()<true, false>();
+            else if ((MOD & kModBias) != 0 && !left) to_exponents.template operator()<false, false>();
+            else to_exponents.template operator()<false, true>();
+          }
           if constexpr (kTree) {
             // A step that reaches the new tokens: the row's visible keys as bit words, made by a
             // short loop (this code runs once a segment, so its size is fetch time), then applied.
@@ -830,7 +834,7 @@ __global__ void __launch_bounds__(Cfg1<D>::kThreads, 1)
           for (int a = 0; a < 8; ++a) mx[a] = fmax3(mx[a], u2f(s[t + 2 * a]), u2f(s[t + 2 * a + 1]));
         const float m_tile =
             fmax3(fmax3(mx[0], mx[1], mx[2]), fmax3(mx[3], mx[4], mx[5]), fmaxf(mx[6], mx[7])) *
-            (MOD != 0 ? 1.0f : c);  // (MOD: already base-2 exponents)
+            (kXform ? 1.0f : c);  // (capped or biased: already base-2 exponents)
 
         float alpha = 1.0f;
         bool rescale = false;
@@ -856,7 +860,7 @@ __global__ void __launch_bounds__(Cfg1<D>::kThreads, 1)
 #pragma unroll
         for (int t = 0; t < kC / 2; ++t) {
           const uint64_t s2 = f2_pack(u2f(s[2 * t]), u2f(s[2 * t + 1]));
-          const uint64_t x2 = MOD != 0 ? f2_add(s2, nm2) : f2_fma(s2, c2, nm2);
+          const uint64_t x2 = kXform ? f2_add(s2, nm2) : f2_fma(s2, c2, nm2);
           float x0, x1;
           f2_unpack(x2, x0, x1);
           const float p0 = ex2_approx(x0);

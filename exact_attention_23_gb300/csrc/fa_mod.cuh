@@ -37,40 +37,29 @@ constexpr int kModCap = 2;   // tanh cap
 constexpr int kModBias = 4;  // distance bias
 constexpr int kModTree = 8;  // new tokens against a cache (fa_tree_walk.cuh)
 
-// The cap. With u = z / cap, tanh(u) is
-//   |u| ≤ 0.8:  u · P(u²), P of degree 5, fitted to tanh(u)/u by iteratively reweighted least
-//               squares: relative error 6·10⁻⁸, so a large cap leaves small scores as they are
-//   beyond:     ±(1 − 2 / (1 + 2^(2·log2(e)·|u|))), which saturates by itself (2^y → ∞)
-// (tanh.approx.f32 has a relative error of 2⁻¹¹: 0.02 of a score at a cap of 50.) The
-// polynomial takes 3.5 issue slots a score on fp32 pairs and no MUFU operation; the exponential
-// form takes two MUFU operations beside the softmax's own, and MUFU bounds these kernels at
-// head dim 64. So a warp takes the second form only in a step where one of its scores needs it.
+// The cap. With u = z / cap = in · s (s the raw score), the capped score in base 2 is
+//   |u| ≤ 0.8:  s · (c0 + c1·s² + … + c4·s⁸): tanh(u)/u ≈ P(u²), P of degree 4 fitted by
+//               iteratively reweighted least squares to a relative error of 1.0·10⁻⁶, with
+//               scale·log2(e) and the powers of `in` multiplied into its coefficients on the host.
+//               A relative error, so a large cap leaves small scores as they are.
+//   beyond:     out · ±(1 − 2 / (1 + 2^(2·log2(e)·|u|))), which saturates by itself (2^y → ∞)
+// (tanh.approx.f32 has a relative error of 2⁻¹¹: 0.02 of a score at a cap of 50.) The polynomial
+// takes six packed operations a pair of scores and none of the MUFU's, which the softmax's own
+// exponentials fill (8 cycles a warp and score); the exponential form takes two MUFU operations a
+// score more. A warp takes it, for a whole step, only where one of its scores needs it.
 constexpr float kCapBend = 0.8f;
+constexpr double kCapPoly[5] = {0.9999989943572278, -0.3332537198003981, 0.1323056561802812,
+                                -0.04918014254491106, 0.012100138637293043};
 
 struct CapFactors {
-  float in;      // scale / cap: u per raw score
-  float in_exp;  // 2·log2(e)·scale / cap
-  float out;     // cap · log2(e)
-  float limit;   // raw scores up to this have |u| ≤ kCapBend
+  float c[5];      // kCapPoly[k] · in^2k · scale · log2(e)
+  float in_exp;    // 2·log2(e)·scale / cap
+  float out;       // cap · log2(e)
+  float bend;      // −1 / out²: 1 − tanh² = 1 + bend · (capped score)²
+  float limit;     // raw scores up to this are |u| ≤ kCapBend
 };
 
 __device__ __forceinline__ uint64_t f2_splat(float x) { return f2_pack(x, x); }
-
-// tanh(u)/u from w = u² on fp32 pairs.
-__device__ __forceinline__ uint64_t tanh_ratio2(uint64_t w) {
-  uint64_t r = f2_fma(f2_splat(-0.00435529975220561f), w, f2_splat(0.01909330114722252f));
-  r = f2_fma(r, w, f2_splat(-0.05311431735754013f));
-  r = f2_fma(r, w, f2_splat(0.13321048021316528f));
-  r = f2_fma(r, w, f2_splat(-0.3333267569541931f));
-  return f2_fma(r, w, f2_splat(0.9999999403953552f));
-}
-
-// tanh(u) for |u| > kCapBend, from y = 2·log2(e)·u.
-__device__ __forceinline__ float tanh_far(float y) {
-  float r;
-  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(1.0f + ex2_approx(fabsf(y))));
-  return copysignf(fmaf(-2.0f, r, 1.0f), y);
-}
 
 // Whether any of a warp's n raw scores lies beyond the polynomial's range (warp-uniform).
 template <int N>
@@ -82,18 +71,27 @@ __device__ __forceinline__ bool cap_far(const uint32_t* s, float limit) {
   return __any_sync(0xffffffffu, m > limit);
 }
 
-// tanh(u) of a pair of raw scores; `far` as cap_far.
-__device__ __forceinline__ uint64_t cap_tanh2(float s0, float s1, const CapFactors& k, bool far) {
-  const uint64_t u = f2_mul(f2_pack(s0, s1), f2_splat(k.in));
-  uint64_t t = f2_mul(u, tanh_ratio2(f2_mul(u, u)));
-  if (far) {
-    float t0, t1;
-    f2_unpack(t, t0, t1);
-    if (fabsf(s0) > k.limit) t0 = tanh_far(s0 * k.in_exp);
-    if (fabsf(s1) > k.limit) t1 = tanh_far(s1 * k.in_exp);
-    t = f2_pack(t0, t1);
+// A pair of raw scores to capped ones in base 2; `far` as cap_far.
+__device__ __forceinline__ float cap_exp(float s, const CapFactors& k) {
+  const float y = s * k.in_exp;
+  float r;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(1.0f + ex2_approx(fabsf(y))));
+  return copysignf(fmaf(-2.0f * k.out, r, k.out), y);
+}
+template <bool FAR>
+__device__ __forceinline__ uint64_t cap2(uint64_t s, const CapFactors& k) {
+  if constexpr (FAR) {
+    float s0, s1;
+    f2_unpack(s, s0, s1);
+    return f2_pack(cap_exp(s0, k), cap_exp(s1, k));
+  } else {
+    const uint64_t w = f2_mul(s, s);
+    uint64_t r = f2_fma(f2_splat(k.c[4]), w, f2_splat(k.c[3]));
+    r = f2_fma(r, w, f2_splat(k.c[2]));
+    r = f2_fma(r, w, f2_splat(k.c[1]));
+    r = f2_fma(r, w, f2_splat(k.c[0]));
+    return f2_mul(s, r);
   }
-  return t;
 }
 
 }  // namespace fa

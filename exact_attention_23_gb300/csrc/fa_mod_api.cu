@@ -292,7 +292,11 @@ int fa_fwd_mod(const void* q, const void* k, const void* v, void* o, float* lse,
   a.p.tiles_per_cta = 1;
   a.p.div_bh = fa::FastDiv::make(static_cast<uint32_t>(BH));
   a.p.div_splits = fa::FastDiv::make(1u);
-  a.p.scale_log2 = static_cast<float>(static_cast<double>(scale) * kLog2e);
+  const int mod = mod_bits(softcap, slopes);
+  // Unmodified scores take their maximum before the factor, as the dense kernels; others the
+  // plain factor.
+  a.p.scale_log2 = mod == fa::kModOn ? exponent_factor(static_cast<double>(scale) * kLog2e, &a.p.s_negate)
+                                     : static_cast<float>(static_cast<double>(scale) * kLog2e);
   a.p.timeout_ns = timeout_ns ? timeout_ns : 2000000000ull;
   a.p.Tk = T;
   a.p.n_qt = n_t;
@@ -314,7 +318,6 @@ int fa_fwd_mod(const void* q, const void* k, const void* v, void* o, float* lse,
   a.p.mod.causal = causal != 0;
   a.grid = static_cast<unsigned>(std::min(a.p.total_units, sms));
   a.stream = static_cast<cudaStream_t>(stream);
-  const int mod = mod_bits(softcap, slopes);
   const cudaError_t e = (d == 64) ? fa::launch_fwd_mod_d64(a, mod) : fa::launch_fwd_mod_d128(a, mod);
   return e == cudaSuccess ? FA_OK : FA_ERR_LAUNCH;
 }

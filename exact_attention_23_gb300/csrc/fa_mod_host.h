@@ -4,6 +4,7 @@
 #include <cuda_runtime.h>
 #include <stdint.h>
 
+#include <algorithm>
 #include <atomic>
 #include <cmath>
 
@@ -30,15 +31,20 @@ constexpr double kLog2e = 1.4426950408889634074;
 
 // The cap's factors; false when the arguments cannot be used.
 inline bool cap_factors(float scale, float softcap, fa::CapFactors* k) {
-  *k = fa::CapFactors{0.f, 0.f, 0.f, 0.f};
+  *k = fa::CapFactors{};
   if (!std::isfinite(softcap) || softcap < 0.0f) return false;
   if (softcap == 0.0f) return true;
   const double u = static_cast<double>(scale) / softcap;
-  k->in = static_cast<float>(u);
+  double power = static_cast<double>(scale) * kLog2e;
+  for (int i = 0; i < 5; ++i, power *= u * u) k->c[i] = static_cast<float>(fa::kCapPoly[i] * power);
   k->in_exp = static_cast<float>(2.0 * kLog2e * u);
   k->out = static_cast<float>(softcap * kLog2e);
-  k->limit = static_cast<float>(fa::kCapBend / std::fabs(u));
-  return std::isfinite(k->in_exp) && std::isfinite(k->out);
+  k->bend = static_cast<float>(-1.0 / (softcap * kLog2e * softcap * kLog2e));
+  // (squares of raw scores up to 10¹⁸ stay finite)
+  k->limit = static_cast<float>(std::min(fa::kCapBend / std::fabs(u), 1e18));
+  for (float c : k->c)
+    if (!std::isfinite(c)) return false;
+  return std::isfinite(k->in_exp) && std::isfinite(k->out) && std::isfinite(k->bend);
 }
 
 inline int mod_bits(float softcap, const float* slopes) {

@@ -188,7 +188,8 @@ int fa_fwd_tree(const void* q, const void* k_cache, const void* v_cache, void* o
     f.p.tiles_per_cta = 1;
     f.p.div_bh = fa::FastDiv::make(1u);
     f.p.div_splits = fa::FastDiv::make(1u);
-    f.p.scale_log2 = a.p.scale_log2;
+    f.p.scale_log2 = mod == fa::kModOn ? exponent_factor(static_cast<double>(scale) * kLog2e, &f.p.s_negate)
+                                       : a.p.scale_log2;
     f.p.Tk = Tmax;
     f.p.n_qt = z.row_blocks;
     f.p.n_kv = (Tmax + 127) / 128;

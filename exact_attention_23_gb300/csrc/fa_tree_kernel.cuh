@@ -217,6 +217,22 @@ __global__ void __launch_bounds__(kTreeBlock, TreeCfg<D>::kCtasPerSm)
       __syncwarp();
       if (lane == 0) mbar_arrive(&empty[stk]);
       // ---- scores to base-2 exponents
+      auto to_exponents = [&]<bool FAR>() {
+#pragma unroll
+        for (int j = 0; j < NT; ++j)
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
+            const uint64_t s2 = f2_pack(s[j][2 * i], s[j][2 * i + 1]);
+            uint64_t x2;
+            if constexpr ((MOD & kModCap) != 0) x2 = cap2<FAR>(s2, p.cap);
+            else x2 = f2_mul(s2, f2_splat(p.scale_log2));
+            if constexpr ((MOD & kModBias) != 0) {
+              const float d0 = at[i] - static_cast<float>(key0 + j * 8 + qc);
+              x2 = f2_add(x2, f2_pack(nsl[i] * fabsf(d0), nsl[i] * fabsf(d0 - 1.0f)));
+            }
+            f2_unpack(x2, s[j][2 * i], s[j][2 * i + 1]);
+          }
+      };
       bool far = false;
       if constexpr ((MOD & kModCap) != 0) {
         float a = 0.f;
@@ -225,23 +241,8 @@ __global__ void __launch_bounds__(kTreeBlock, TreeCfg<D>::kCtasPerSm)
           a = fmax3(fmax3(a, fabsf(s[j][0]), fabsf(s[j][1])), fabsf(s[j][2]), fabsf(s[j][3]));
         far = __any_sync(0xffffffffu, a > p.cap.limit);
       }
-#pragma unroll
-      for (int j = 0; j < NT; ++j)
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-          uint64_t add = 0ull, x2;
-          if constexpr ((MOD & kModBias) != 0) {
-            const float d0 = at[i] - static_cast<float>(key0 + j * 8 + qc);
-            add = f2_pack(nsl[i] * fabsf(d0), nsl[i] * fabsf(d0 - 1.0f));
-          }
-          if constexpr ((MOD & kModCap) != 0)
-            x2 = f2_fma(cap_tanh2(s[j][2 * i], s[j][2 * i + 1], p.cap, far), f2_splat(p.cap.out), add);
-          else if constexpr ((MOD & kModBias) != 0)
-            x2 = f2_fma(f2_pack(s[j][2 * i], s[j][2 * i + 1]), f2_splat(p.scale_log2), add);
-          else
-            x2 = f2_mul(f2_pack(s[j][2 * i], s[j][2 * i + 1]), f2_splat(p.scale_log2));
-          f2_unpack(x2, s[j][2 * i], s[j][2 * i + 1]);
-        }
+      if (far) to_exponents.template operator()<true>();
+      else to_exponents.template operator()<false>();
       // ---- the new tokens' keys: the tree, and their depths in the bias
       const bool tail = key0 + NK > min(ctx, keys);  // (a context may fill the cache)
       if (tail) {

@@ -5,8 +5,9 @@ the kernels.
 Bounds (u = 2⁻⁸, half a bf16 step relative to the value):
   o    the output's rounding, u·|o|, and P rounded to bf16 before its product: u·Σ_j p_j|v_j|
        (twice that, for the fp32 arithmetic in between)
-  lse  fp32: a dot product of d terms, d·2⁻²⁴·Σ|q_c k_c|·|scale|; the cap's absolute error, a few
-       2⁻²⁴ of the cap; the bias, 2⁻²¹ of its size; the sum of exponentials and its logarithm
+  lse  fp32: a dot product of d terms, d·2⁻²⁴·Σ|q_c k_c|·|scale|; the cap's error, at most
+       1.0e-6·tanh(0.8)·cap = 2⁻²⁰·⁵ of the cap where it is a polynomial (relative error 1.0e-6)
+       and 2⁻²¹ beyond, with three fp32 roundings at most 2⁻²⁰ in all; the bias, 2⁻²¹ of its size; the sum of exponentials and its logarithm
   dV   u·|dV| + 2u·Pᵀ|dO|
   dQ   u·|dQ| + 2u·|scale|·M|K|, dK likewise with Mᵀ|Q|, where M = P·(1 − tanh²)·(|dP − D| +
        Σ_c|dO_c O_c|) bounds dS's own rounding and D's error, made from the rounded o
@@ -78,7 +79,7 @@ def attention(q, k, v, ok, scale, softcap=0.0, slopes=None, do=None, query_at=No
     r = {"o": o, "lse": lse, "o_tol": U * o.abs() + 2 * U * (p @ vv.abs()) + 1e-7}
     zero = torch.zeros_like(mag)
     worst = torch.where(ok, mag, zero).amax(-1)
-    r["lse_tol"] = (d * 2.0 ** -24 + 2.0 ** -21) * worst + softcap * 2.0 ** -21 + 1e-5 \
+    r["lse_tol"] = (d * 2.0 ** -24 + 2.0 ** -21) * worst + softcap * 2.0 ** -20 + 1e-5 \
         + 2.0 ** -21 * torch.where(ok, dist.abs(), zero).amax(-1)
     if do is None:
         return r
