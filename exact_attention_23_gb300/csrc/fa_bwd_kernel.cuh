@@ -817,16 +817,6 @@ __global__ void __launch_bounds__(BwdCfg<D, MOD>::kThreads, 1)
             }
             float x[2];
             f2_unpack(x2, x[0], x[1]);
-            if (part) {
-              if (p.mod.rows) {
-                const int2 v0 = iv[c], v1 = iv[c + 1];
-                if (key < v0.x || key >= v0.y) x[0] = __int_as_float(0xff800000);
-                if (key < v1.x || key >= v1.y) x[1] = __int_as_float(0xff800000);
-              } else {
-                if (key > q0 + c) x[0] = __int_as_float(0xff800000);
-                if (key > q0 + c + 1) x[1] = __int_as_float(0xff800000);
-              }
-            }
             pr[c] = ex2_approx(x[0]);
             pr[c + 1] = ex2_approx(x[1]);
             pkm[c / 2] = pack_bf16x2(pr[c], pr[c + 1]);
@@ -839,6 +829,28 @@ __global__ void __launch_bounds__(BwdCfg<D, MOD>::kThreads, 1)
         if (far) probabilities.template operator()<true, false>();
         else if ((MOD & kModBias) != 0 && !left) probabilities.template operator()<false, false>();
         else probabilities.template operator()<false, true>();
+        if (part) {  // masked pairs to zero, whatever their exponentials were
+#pragma unroll
+          for (int c = 0; c < NC; c += 2) {
+            bool out0, out1;
+            if (p.mod.rows) {
+              const int2 v0 = iv[c], v1 = iv[c + 1];
+              out0 = key < v0.x || key >= v0.y;
+              out1 = key < v1.x || key >= v1.y;
+            } else {
+              out0 = key > q0 + c;
+              out1 = key > q0 + c + 1;
+            }
+            if (out0) {
+              pr[c] = 0.f;
+              pkm[c / 2] &= 0xFFFF0000u;
+            }
+            if (out1) {
+              pr[c + 1] = 0.f;
+              pkm[c / 2] &= 0x0000FFFFu;
+            }
+          }
+        }
         if (++ti == n_i) {
           ti = 0;
           ++hg;

@@ -181,6 +181,7 @@ __global__ void __launch_bounds__(Cfg1<D>::kThreads, 1)
                    const FwdParams p) {
   using C = Cfg1<D>;
   constexpr bool kTree = (MOD & kModTree) != 0;
+  constexpr bool kRef = (MOD & kModRef) != 0;  // the softmax is taken against 0
   constexpr bool kXform = (MOD & (kModCap | kModBias)) != 0;  // scores are modified before the softmax
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
@@ -680,7 +681,8 @@ __global__ void __launch_bounds__(Cfg1<D>::kThreads, 1)
         if constexpr ((MOD & kModBias) != 0)
           nslope = __ldg(p.mod.slopes + (u.bh - b * p.mod.H)) * -1.4426950408889634f;
       }
-      float m_ref = -INFINITY;  // reference max (base-2 scaled units) shared by O_h and l
+      // reference max (base-2 scaled units) shared by O_h and l
+      float m_ref = kRef ? 0.0f : -INFINITY;
       float l = 0.0f;
       // the tile's K tiles (GEN: its walk, the next position fetched a step ahead)
       Walk w{nullptr, 0};
@@ -728,6 +730,7 @@ __global__ void __launch_bounds__(Cfg1<D>::kThreads, 1)
         __syncwarp();
         if (lane == 0) mbar_arrive(&bars->s_free[b]);
         FA1_TRACE(20, j);
+        bool fused = false;  // kRef: a step without masks or far scores
         if constexpr (MOD != 0) {
           // Capped or biased scores to base-2 exponents in place (fa_mod.cuh); the bias is linear
           // in the key where every key of the step lies at or before the warp's first row. (A far
@@ -758,7 +761,10 @@ __global__ void __launch_bounds__(Cfg1<D>::kThreads, 1)
           if constexpr (kXform) {
             bool far = false;
             if constexpr ((MOD & kModCap) != 0) far = cap_far<kC>(s, p.mod.cap.limit);
-            if (far) to_exponents.template operator()<true, false>();
+            if constexpr (kRef) fused = !far && !__any_sync(0xffffffffu, masked);
+            if (kRef && fused) {
+              // capped where they are exponentiated, below
+            } else if (far) to_exponents.template operator()<true, false>();
             else if ((MOD & kModBias) != 0 && !left) to_exponents.template operator()<false, false>();
             else to_exponents.template operator()<false, true>();
           }
@@ -825,6 +831,9 @@ __global__ void __launch_bounds__(Cfg1<D>::kThreads, 1)
           for (int t = 0; t < kC; ++t)
             if (t >= lim) s[t] = __float_as_uint(-INFINITY);
         }
+        float alpha = 1.0f;
+        bool any_rescale = false;
+        if constexpr (!kRef) {
         float mx[8];
 #pragma unroll
         for (int a = 0; a < 8; ++a) mx[a] = fmaxf(u2f(s[2 * a]), u2f(s[2 * a + 1]));
@@ -836,7 +845,6 @@ __global__ void __launch_bounds__(Cfg1<D>::kThreads, 1)
             fmax3(fmax3(mx[0], mx[1], mx[2]), fmax3(mx[3], mx[4], mx[5]), fmaxf(mx[6], mx[7])) *
             (kXform ? 1.0f : c);  // (capped or biased: already base-2 exponents)
 
-        float alpha = 1.0f;
         bool rescale = false;
         if (j == 0) {
           m_ref = m_tile;
@@ -846,7 +854,8 @@ __global__ void __launch_bounds__(Cfg1<D>::kThreads, 1)
           l *= alpha;
           rescale = true;
         }
-        const bool any_rescale = __any_sync(0xffffffffu, rescale);
+        any_rescale = __any_sync(0xffffffffu, rescale);
+        }
         FA1_TRACE(40, j);
 
         // p = 2^(s·c − m_ref) on fp32 pairs; row sum in fp32; P kept as bf16 pairs. (A row
@@ -857,18 +866,25 @@ __global__ void __launch_bounds__(Cfg1<D>::kThreads, 1)
         const uint64_t nm2 = f2_pack(-m_use, -m_use);
         uint64_t acc0 = f2_pack(0.f, 0.f), acc1 = acc0;
         uint32_t pk[kC / 2];
+        auto exponentials = [&]<bool FUSED>() {
 #pragma unroll
-        for (int t = 0; t < kC / 2; ++t) {
-          const uint64_t s2 = f2_pack(u2f(s[2 * t]), u2f(s[2 * t + 1]));
-          const uint64_t x2 = kXform ? f2_add(s2, nm2) : f2_fma(s2, c2, nm2);
-          float x0, x1;
-          f2_unpack(x2, x0, x1);
-          const float p0 = ex2_approx(x0);
-          const float p1 = ex2_approx(x1);
-          if (t & 1) acc1 = f2_add(acc1, f2_pack(p0, p1));
-          else acc0 = f2_add(acc0, f2_pack(p0, p1));
-          pk[t] = pack_bf16x2(p0, p1);
-        }
+          for (int t = 0; t < kC / 2; ++t) {
+            const uint64_t s2 = f2_pack(u2f(s[2 * t]), u2f(s[2 * t + 1]));
+            uint64_t x2;
+            if constexpr (FUSED) x2 = cap2<false>(s2, p.mod.cap);
+            else if constexpr (kRef) x2 = s2;
+            else x2 = kXform ? f2_add(s2, nm2) : f2_fma(s2, c2, nm2);
+            float x0, x1;
+            f2_unpack(x2, x0, x1);
+            const float p0 = ex2_approx(x0);
+            const float p1 = ex2_approx(x1);
+            if (t & 1) acc1 = f2_add(acc1, f2_pack(p0, p1));
+            else acc0 = f2_add(acc0, f2_pack(p0, p1));
+            pk[t] = pack_bf16x2(p0, p1);
+          }
+        };
+        if (kRef && fused) exponentials.template operator()<kRef>();
+        else exponentials.template operator()<false>();
         FA1_TRACE(42, j);
         if (any_rescale) {
           // Rows whose max jumped bring their O_h to the new reference before this step's

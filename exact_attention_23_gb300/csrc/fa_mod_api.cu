@@ -292,7 +292,7 @@ int fa_fwd_mod(const void* q, const void* k, const void* v, void* o, float* lse,
   a.p.tiles_per_cta = 1;
   a.p.div_bh = fa::FastDiv::make(static_cast<uint32_t>(BH));
   a.p.div_splits = fa::FastDiv::make(1u);
-  const int mod = mod_bits(softcap, slopes);
+  const int mod = fwd_mod_bits(softcap, slopes);
   // Unmodified scores take their maximum before the factor, as the dense kernels; others the
   // plain factor.
   a.p.scale_log2 = mod == fa::kModOn ? exponent_factor(static_cast<double>(scale) * kLog2e, &a.p.s_negate)

@@ -51,5 +51,11 @@ inline int mod_bits(float softcap, const float* slopes) {
   return fa::kModOn | (softcap > 0.0f ? fa::kModCap : 0) | (slopes ? fa::kModBias : 0);
 }
 
+// The forward's: a small enough cap alone takes the softmax against 0.
+inline int fwd_mod_bits(float softcap, const float* slopes) {
+  const int mod = mod_bits(softcap, slopes);
+  return mod == (fa::kModOn | fa::kModCap) && softcap * kLog2e <= fa::kCapRef ? mod | fa::kModRef : mod;
+}
+
 }  // namespace host
 }  // namespace fa

@@ -8,6 +8,7 @@ cudaError_t launch_fwd_tree_d64(const FwdLaunch& a, int mod) {
   switch (mod) {
     case kModOn: return launch_fwd_mod<64, kModTree | kModOn>(a);
     case kModOn | kModCap: return launch_fwd_mod<64, kModTree | kModOn | kModCap>(a);
+    case kModOn | kModCap | kModRef: return launch_fwd_mod<64, kModTree | kModOn | kModCap | kModRef>(a);
     case kModOn | kModBias: return launch_fwd_mod<64, kModTree | kModOn | kModBias>(a);
     case kModOn | kModCap | kModBias: return launch_fwd_mod<64, kModTree | kModOn | kModCap | kModBias>(a);
   }
