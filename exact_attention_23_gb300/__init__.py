@@ -34,6 +34,7 @@ from ._binding import (  # noqa: F401
     fa_bwd,
     fa_bwd_ex,
     fa_bwd_mod,
+    fa_bwd_mod_workspace_size,
     fa_bwd_workspace_size,
     fa_fwd,
     fa_fwd_block_sparse,
@@ -313,7 +314,8 @@ def q_tiles(T: int, rows: int = 128) -> int:
 
 
 # The operators of ops.py, imported with torch on their first use.
-_OPS = ("Visible", "visible", "fwd_mod", "bwd_mod", "rope_inv_freq", "rope", "rope_append",
+_OPS = ("Visible", "visible", "fwd_mod", "bwd_mod_workspace", "bwd_mod",
+        "rope_inv_freq", "rope", "rope_append",
         "fwd_tree_workspace", "fwd_tree")
 
 

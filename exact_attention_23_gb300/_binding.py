@@ -28,7 +28,8 @@ FA_BWD_NOALLOC_SCRATCH_BYTES = 33554432
 # Every symbol include/fa.h declares.
 EXPORTS = ("fa_fwd", "fa_fwd_ex", "fa_fwd_fp8", "fa_fwd_host_workspace_size", "fa_fwd_host", "fa_fwd_kv_workspace_size", "fa_fwd_kv",
            "fa_fwd_block_sparse", "fa_bwd_workspace_size", "fa_bwd", "fa_bwd_ex",
-           "fa_bwd_noalloc", "fa_visible_size", "fa_visible", "fa_fwd_mod", "fa_bwd_mod", "fa_rope",
+           "fa_bwd_noalloc", "fa_visible_size", "fa_visible", "fa_fwd_mod", "fa_bwd_mod",
+           "fa_bwd_mod_workspace_size", "fa_rope",
            "fa_rope_append", "fa_fwd_tree_workspace_size", "fa_fwd_tree", "fa_strerror", "fa_version")
 
 _lock = threading.Lock()
@@ -87,6 +88,8 @@ def lib() -> ctypes.CDLL:
             L.fa_fwd_mod.restype = i
             L.fa_bwd_mod.argtypes = [vp] * 10 + [sz, vp, i, f, vp, i, i, i, i, i, f, vp, ull, vp]
             L.fa_bwd_mod.restype = i
+            L.fa_bwd_mod_workspace_size.argtypes = [i] * 5
+            L.fa_bwd_mod_workspace_size.restype = sz
             src = [vp, ll, ll, ll]
             L.fa_rope.argtypes = src + [vp] + src + [vp, vp, i, vp, i, i, i, f, i, i, i, i, i, vp]
             L.fa_rope.restype = i
@@ -198,6 +201,10 @@ def fa_bwd_mod(q, k, v, o, dout, lse, dq, dk, dv, workspace, workspace_bytes, vi
     return lib().fa_bwd_mod(q, k, v, o, dout, lse, dq, dk, dv, workspace, int(workspace_bytes),
                             visible, int(bool(causal)), float(softcap), slopes, B, H, Hkv, T, d,
                             float(scale), status, int(timeout_ns), stream)
+
+
+def fa_bwd_mod_workspace_size(B, H, Hkv, T, d) -> int:
+    return int(lib().fa_bwd_mod_workspace_size(B, H, Hkv, T, d))
 
 
 def fa_rope(q, q_strides, q_out, k, k_strides, k_out, positions, positions_per_batch, inv_freq,

@@ -134,14 +134,18 @@ static_assert(sizeof(BwdBars) <= 256, "barrier block");
 
 // Modified scores (MOD instantiations; see fa_mod.cuh). K, V, dK and dV then have one head for
 // every `group` query heads: the CTA of a key tile walks the query tiles of all of them, so a
-// shared head's gradient is summed in its accumulators, with no second pass.
+// shared head's gradient is summed in its accumulators, with no second pass. Where that leaves too
+// few CTAs to share out evenly, a group is cut into `parts`, each part's sum goes out in fp32, and
+// fa_bwd_sum_kernel adds the parts in order (no atomics: the same bits every time).
 struct BwdModParams {
   const int2* rows;     // [B][T_pad] visible key interval of each query row, or null
   const int4* units;    // [B][n_kt] (key tile, first 128-row query tile, past the last, rows in use)
   const int2* whole;    // [B][n_kt] (largest lo, smallest hi) over a 128-row query tile
   const float* slopes;  // [H]
+  float* part_out;      // parts > 1: [2][parts][B·Hkv][T][D], dK (scaled) then dV
   int Hkv;              // key heads
   int group;            // query heads per key head
+  int parts;            // parts of a group (BH then counts B·Hkv·parts)
   CapFactors cap;       // (CAP)
   int causal;           // without rows
 };
@@ -331,6 +335,32 @@ __global__ void __launch_bounds__(256) fa_bwd_dq_kernel(const float* __restrict_
   }
 }
 
+// dK and dV = the sums of their parts' fp32 rows, as bf16: part_out is [2][parts][n], 8 values a
+// thread and step.
+static __global__ void __launch_bounds__(256) fa_bwd_sum_kernel(const float* __restrict__ part_out,
+                                                                __nv_bfloat16* __restrict__ dk,
+                                                                __nv_bfloat16* __restrict__ dv, size_t n,
+                                                                int parts) {
+  pdl_wait();
+  pdl_launch_dependents();
+  const size_t stride = (size_t)gridDim.x * blockDim.x * 8;
+  for (size_t x = ((size_t)blockIdx.x * blockDim.x + threadIdx.x) * 8; x < 2 * n; x += stride) {
+    const bool is_dv = x >= n;
+    const size_t e = is_dv ? x - n : x;
+    const float* src = part_out + (is_dv ? (size_t)parts * n : 0) + e;
+    float4 a = make_float4(0.f, 0.f, 0.f, 0.f), b = a;
+#pragma unroll 4
+    for (int s = 0; s < parts; ++s) {
+      const float4 u = *reinterpret_cast<const float4*>(src + (size_t)s * n);
+      const float4 v = *reinterpret_cast<const float4*>(src + (size_t)s * n + 4);
+      a.x += u.x; a.y += u.y; a.z += u.z; a.w += u.w;
+      b.x += v.x; b.y += v.y; b.z += v.z; b.w += v.w;
+    }
+    *reinterpret_cast<uint4*>((is_dv ? dv : dk) + e) =
+        make_uint4(pack_bf16x2(a.x, a.y), pack_bf16x2(a.z, a.w), pack_bf16x2(b.x, b.y), pack_bf16x2(b.z, b.w));
+  }
+}
+
 // ------------------------------------------------------------------------------------
 // Main kernel.
 // ------------------------------------------------------------------------------------
@@ -340,6 +370,49 @@ __device__ __forceinline__ void st_row_chunk_sw128(uint32_t box, int r, int ch, 
   st_shared_v4(box + static_cast<uint32_t>(r) * 128u + (static_cast<uint32_t>(ch ^ (r & 7)) << 4),
                pack_bf16x2(x[0], x[1]), pack_bf16x2(x[2], x[3]), pack_bf16x2(x[4], x[5]),
                pack_bf16x2(x[6], x[7]));
+}
+
+// What a CTA walks: key tile j of key head bh, against the query tiles i0 … i0 + n_i − 1 of each of
+// its query heads (b·h numbers from q0h on), n steps in all.
+struct BwdWalk {
+  int j, bh, i0, n;
+  int n_i, q0h;  // MOD (dense: n and bh)
+  int h0;        // the first query head's number within its sequence
+  int used;      // rows in use: those behind are padding
+  int part;      // which part of the key head's query heads
+};
+
+// pos, head: the CTA's place in the unit order.
+template <int D, bool CAUSAL, int MOD>
+__device__ __forceinline__ BwdWalk bwd_walk(const BwdParams& p, int pos, int head) {
+  constexpr int kBQ = BwdCfg<D, MOD>::kBQ, kPer = 128 / kBQ;  // query tiles in 128 rows
+  BwdWalk w;
+  w.j = pos;
+  w.bh = w.q0h = head;
+  w.i0 = CAUSAL ? (w.j * 128) / kBQ : 0;
+  w.n = w.n_i = p.n_qt - w.i0;
+  w.used = p.T_pad;
+  w.h0 = w.part = 0;
+  if constexpr (MOD != 0) {
+    const int heads = p.mod.group / p.mod.parts;
+    w.bh = head / p.mod.parts;
+    w.part = head - w.bh * p.mod.parts;
+    const int b = w.bh / p.mod.Hkv;
+    w.h0 = (w.bh - b * p.mod.Hkv) * p.mod.group + w.part * heads;
+    w.q0h = w.bh * p.mod.group + w.part * heads;
+    if (p.mod.units) {
+      const int4 rec = __ldg(p.mod.units + (size_t)b * p.n_kt + pos);
+      w.j = rec.x;
+      w.i0 = rec.y * kPer;
+      w.n_i = max(0, rec.z * kPer - w.i0);
+      w.used = rec.w;
+    } else if (p.mod.causal) {
+      w.i0 = pos * kPer;
+      w.n_i = p.n_qt - w.i0;
+    }
+    w.n = w.n_i * heads;
+  }
+  return w;
 }
 
 template <int D, bool CAUSAL, int MOD = 0>
@@ -361,12 +434,9 @@ __global__ void __launch_bounds__(BwdCfg<D, MOD>::kThreads, 1)
   const int grp = blockIdx.x / per_group;
   const int within = blockIdx.x - grp * per_group;
   const int gsize = min(p.head_group, p.BH - grp * p.head_group);
-  int j = within / gsize;
-  const int bh = grp * p.head_group + within % gsize;  // (MOD: the key head's index)
-  int i0 = CAUSAL ? (j * 128) / C::kBQ : 0;
-  int n = p.n_qt - i0;
-  // MOD: the walk is the query tiles i0 … i0 + n_i − 1 of each of the key head's query heads
-  int n_i = n, used = p.T_pad, hk0 = 0;
+  const int u_pos = within / gsize, u_head = grp * p.head_group + within % gsize;
+  // (MOD reads its walk from memory, after the wait for the kernel before)
+  const BwdWalk dense = bwd_walk<D, CAUSAL, 0>(p, u_pos, u_head);
 
   if (threadIdx.x == 0) {
     mbar_init(&bars->kv_full, 1);
@@ -403,22 +473,8 @@ __global__ void __launch_bounds__(BwdCfg<D, MOD>::kThreads, 1)
   // (No early trigger for the dQ conversion: letting it be scheduled during this grid's
   // last wave measured 5 % slower at d = 128.)
   pdl_wait();
-  if constexpr (MOD != 0) {
-    constexpr int kPer = 128 / C::kBQ;  // query tiles in 128 rows
-    const int b = bh / p.mod.Hkv;
-    hk0 = (bh - b * p.mod.Hkv) * p.mod.group;
-    if (p.mod.units) {
-      const int4 rec = __ldg(p.mod.units + (size_t)b * p.n_kt + j);
-      j = rec.x;
-      i0 = rec.y * kPer;
-      n_i = max(0, rec.z * kPer - i0);
-      used = rec.w;
-    } else if (p.mod.causal) {
-      i0 = j * kPer;
-      n_i = p.n_qt - i0;
-    }
-    n = n_i * p.mod.group;
-  }
+  const BwdWalk wk = MOD != 0 ? bwd_walk<D, CAUSAL, MOD>(p, u_pos, u_head) : dense;
+  const int j = wk.j, bh = wk.bh, i0 = wk.i0, n = wk.n;
   const uint32_t tmem = bars->tmem_base;
   const WaitCtl wc{&bars->abort, p.status, p.timeout_ns};
   const WaitCtl drain_wc = drain_ctl(p.timeout_ns);
@@ -477,8 +533,8 @@ __global__ void __launch_bounds__(BwdCfg<D, MOD>::kThreads, 1)
       int i = i0 + t, bq = bh;  // query tile and (b·h) of this step
       if constexpr (MOD != 0) {
         i = i0 + ti;
-        bq = bh * p.mod.group + hg;
-        if (++ti == n_i) {
+        bq = wk.q0h + hg;
+        if (++ti == wk.n_i) {
           ti = 0;
           ++hg;
         }
@@ -533,11 +589,11 @@ __global__ void __launch_bounds__(BwdCfg<D, MOD>::kThreads, 1)
       for (int x = max(first, 0) * 8 + lane; x < rows * 8; x += 32) st_shared_v4(box + x * 16, 0u, 0u, 0u, 0u);
     };
     if constexpr (MOD != 0) {
-      if (ok && used < j * 128 + 128) {
+      if (ok && wk.used < j * 128 + 128) {
 #pragma unroll
         for (int b = 0; b < D / 64; ++b) {
-          zero_rows(k_s + b * C::kBox, used - j * 128, 128);
-          zero_rows(v_s + b * C::kBox, used - j * 128, 128);
+          zero_rows(k_s + b * C::kBox, wk.used - j * 128, 128);
+          zero_rows(v_s + b * C::kBox, wk.used - j * 128, 128);
         }
         fence_proxy_async_smem();
         __syncwarp();
@@ -550,12 +606,12 @@ __global__ void __launch_bounds__(BwdCfg<D, MOD>::kThreads, 1)
       FA_TRACE(1, t);
       if constexpr (MOD != 0) {
         const int i = i0 + ti;
-        if (++ti == n_i) ti = 0;
-        if (used < (i + 1) * C::kBQ) {
+        if (++ti == wk.n_i) ti = 0;
+        if (wk.used < (i + 1) * C::kBQ) {
 #pragma unroll
           for (int b = 0; b < D / 64; ++b) {
-            zero_rows(q_s(st) + b * C::kQBox, used - i * C::kBQ, C::kBQ);
-            zero_rows(do_s(st) + b * C::kQBox, used - i * C::kBQ, C::kBQ);
+            zero_rows(q_s(st) + b * C::kQBox, wk.used - i * C::kBQ, C::kBQ);
+            zero_rows(do_s(st) + b * C::kQBox, wk.used - i * C::kBQ, C::kBQ);
           }
           fence_proxy_async_smem();
           __syncwarp();
@@ -687,8 +743,8 @@ __global__ void __launch_bounds__(BwdCfg<D, MOD>::kThreads, 1)
       int it = i0 + t, bq = bh;
       if constexpr (MOD != 0) {
         it = i0 + ti;
-        bq = bh * p.mod.group + hg;
-        if (++ti == n_i) {
+        bq = wk.q0h + hg;
+        if (++ti == wk.n_i) {
           ti = 0;
           ++hg;
         }
@@ -739,8 +795,8 @@ __global__ void __launch_bounds__(BwdCfg<D, MOD>::kThreads, 1)
       for (; t < n; ++t) {
         int it = i0 + t, bq = bh;
         if constexpr (MOD != 0) {
-          it = i0 + t % n_i;
-          bq = bh * p.mod.group + t / n_i;
+          it = i0 + t % wk.n_i;
+          bq = wk.q0h + t / wk.n_i;
         }
         for (int c4 = 0; c4 < 16; ++c4) {
           float* dst = p.dq_acc + ((D == 64) ? dq_acc_offset(bq, it, p.n_qt, c4, r, D)
@@ -768,7 +824,7 @@ __global__ void __launch_bounds__(BwdCfg<D, MOD>::kThreads, 1)
     for (int t = 0, st = 0, ph = 0; t < n && ok; ++t) {
       const int i = MOD != 0 ? i0 + ti : i0 + t;
       if constexpr ((MOD & kModBias) != 0) {
-        if (ti == 0) nslope = __ldg(p.mod.slopes + hk0 + hg) * -1.4426950408889634f;
+        if (ti == 0) nslope = __ldg(p.mod.slopes + wk.h0 + hg) * -1.4426950408889634f;
       }
       const float* vec = reinterpret_cast<const float*>(sm + C::kVec + st * C::kVecBytes);
       if (!(ok = mbar_wait_warp_inl(&bars->q_full[st], ph, wc))) break;
@@ -851,7 +907,7 @@ __global__ void __launch_bounds__(BwdCfg<D, MOD>::kThreads, 1)
             }
           }
         }
-        if (++ti == n_i) {
+        if (++ti == wk.n_i) {
           ti = 0;
           ++hg;
         }
@@ -969,6 +1025,16 @@ __global__ void __launch_bounds__(BwdCfg<D, MOD>::kThreads, 1)
           if (MOD != 0 && n == 0) {  // a key tile that no query sees
 #pragma unroll
             for (int e = 0; e < 8; ++e) y[e] = 0.f;
+          }
+          if constexpr (MOD != 0) {
+            if (p.mod.parts > 1) {
+              const size_t rows = (size_t)(p.BH / p.mod.parts) * p.T;
+              float* out = p.mod.part_out +
+                           (((is_dv ? p.mod.parts : 0) + wk.part) * rows + (size_t)bh * p.T + key) * D + h * 32 + c;
+              reinterpret_cast<float4*>(out)[0] = make_float4(y[0], y[1], y[2], y[3]);
+              reinterpret_cast<float4*>(out)[1] = make_float4(y[4], y[5], y[6], y[7]);
+              continue;
+            }
           }
           uint4 v;
           v.x = pack_bf16x2(y[0], y[1]);

@@ -76,7 +76,7 @@ struct BwdLaunch {
 // Enqueues the three backward kernels (prep, main, dQ conversion) on a.stream.
 cudaError_t launch_bwd_d64(const BwdLaunch& a, bool causal);
 cudaError_t launch_bwd_d128(const BwdLaunch& a, bool causal);
-// The same with modified scores; a.p.BH counts key heads, q_heads = B·H.
+// The same with modified scores; a.p.BH counts key heads' parts, q_heads = B·H.
 cudaError_t launch_bwd_mod_d64(const BwdLaunch& a, int mod, int q_heads);
 cudaError_t launch_bwd_mod_d128(const BwdLaunch& a, int mod, int q_heads);
 

@@ -54,16 +54,48 @@ struct VisibleParams {
 };
 
 constexpr int kVisThreads = 1024;
+constexpr int kVisTiles = 1024;
+
+// The document starts and the paddings among 32 rows from i0 on, as bits (rows past `end`: 0).
+// Eight loads stand together, so a group costs four round trips.
+__device__ __forceinline__ void doc_bits(const int* ids, int i0, int end, uint32_t* starts, uint32_t* pads) {
+  uint32_t st = 0u, pad = 0u;
+  if (!ids) {
+    *starts = i0 == 0 && end > 0 ? 1u : 0u;
+    *pads = 0u;
+    return;
+  }
+  int prev = i0 > 0 && i0 < end ? ids[i0 - 1] : 0;
+#pragma unroll 1
+  for (int o = 0; o < 32 && i0 + o < end; o += 8) {
+    int id[8];
+#pragma unroll
+    for (int e = 0; e < 8; ++e) id[e] = ids[min(i0 + o + e, end - 1)];
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      const int i = i0 + o + e;
+      if (i < end) {
+        if (i == 0 || id[e] != prev) st |= 1u << (o + e);
+        if (id[e] < 0) pad |= 1u << (o + e);
+      }
+      prev = id[e];
+    }
+  }
+  *starts = st;
+  *pads = pad;
+}
 
 // One block a sequence. A document is a maximal run of equal ids, so a row's document starts at
 // the last change of id at or before it and ends at the next one after it: a running maximum and
-// a running minimum, each thread taking one stretch of rows and the block joining the stretches.
-// Then a warp a tile: its rows' extremes, the query tiles that see it, and its place among the
-// tiles by the number it has to walk (a count of the tiles before it: n_t² comparisons, which at
-// 16384 tokens are 4 a lane and tile).
+// a running minimum, each thread taking one stretch of rows (as bits, 32 rows at a time) and the
+// block joining the stretches. Then a warp a tile: its rows' extremes, the query tiles that see
+// it, and its place among the tiles by the number it has to walk (a count of the tiles before it:
+// n_t² comparisons, which at 16384 tokens are 4 a lane and tile). Latency is all it costs; the
+// tiles' extremes are kept in shared memory up to kVisTiles of them.
 __global__ void __launch_bounds__(kVisThreads) fa_visible_kernel(const VisibleParams p) {
   __shared__ int s_last[kVisThreads / 32], s_first[kVisThreads / 32];
   __shared__ int s_used;
+  __shared__ int2 s_span[kVisTiles], s_seen[kVisTiles];
   pdl_wait();
   pdl_launch_dependents();
   const int b = blockIdx.x, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -72,16 +104,19 @@ __global__ void __launch_bounds__(kVisThreads) fa_visible_kernel(const VisiblePa
   const long long T_pad = static_cast<long long>(n_t) * 128;
   const int* ids = p.ids ? p.ids + static_cast<size_t>(b) * T : nullptr;
   int2* rows = p.rows + static_cast<size_t>(b) * T_pad;
+  int2* span = n_t <= kVisTiles ? s_span : p.span + static_cast<size_t>(b) * n_t;
+  int2* seen = n_t <= kVisTiles ? s_seen : p.seen + static_cast<size_t>(b) * n_t;
   if (tid == 0) s_used = 0;
   const long long seg = (T_pad + kVisThreads - 1) / kVisThreads;
   const int a0 = static_cast<int>(min(static_cast<long long>(T), tid * seg));
   const int a1 = static_cast<int>(min(static_cast<long long>(T), (tid + 1) * seg));
+  uint32_t starts = 0u, pads = 0u;
   int last = -1, first = T;  // this stretch's last and first document starts
-  for (int i = a0; i < a1; ++i) {
-    const bool st = i == 0 || (ids && ids[i] != ids[i - 1]);
-    if (st) {
-      last = i;
-      if (first == T) first = i;
+  for (int g0 = a0; g0 < a1; g0 += 32) {
+    doc_bits(ids, g0, a1, &starts, &pads);
+    if (starts) {
+      last = g0 + 31 - __clz(starts);
+      if (first == T) first = g0 + __ffs(starts) - 1;
     }
   }
   // inclusive scans over the block's stretches: maximum from the left, minimum from the right
@@ -95,36 +130,61 @@ __global__ void __launch_bounds__(kVisThreads) fa_visible_kernel(const VisiblePa
   if (lane == 31) s_last[warp] = mx;
   if (lane == 0) s_first[warp] = mn;
   __syncthreads();
-  int before = __shfl_up_sync(0xffffffffu, mx, 1), after = __shfl_down_sync(0xffffffffu, mn, 1);
-  if (lane == 0) before = -1;
-  if (lane == 31) after = T;
-  for (int w = 0; w < warp; ++w) before = max(before, s_last[w]);
-  for (int w = warp + 1; w < kWarps; ++w) after = min(after, s_first[w]);
-  int cur = max(before, 0);
-  for (int i = a0; i < a1; ++i) {
-    if (ids && i > 0 && ids[i] != ids[i - 1]) cur = i;
-    rows[i].x = cur;
+  int cur = __shfl_up_sync(0xffffffffu, mx, 1), end = __shfl_down_sync(0xffffffffu, mn, 1);
+  if (lane == 0) cur = -1;
+  if (lane == 31) end = T;
+  {
+    // the warps before and after, a lane each
+    const int l = lane < warp ? s_last[lane] : -1, f = lane > warp ? s_first[lane] : T;
+    cur = max(max(cur, __reduce_max_sync(0xffffffffu, l)), 0);
+    end = min(end, __reduce_min_sync(0xffffffffu, f));
   }
-  int end = after, used = 0;
-  for (int i = a1 - 1; i >= a0; --i) {
-    const int lo = rows[i].x;
-    int2 r = make_int2(lo, end);
-    if (ids && ids[i] < 0) {
-      r = make_int2(0, 0);
-    } else {
-      if (p.causal) {
-        const int pre = p.prefix ? max(0, p.prefix[p.prefix_per_token ? static_cast<size_t>(b) * T + i
-                                                                      : static_cast<size_t>(b)])
-                                 : 0;
-        r.y = max(i + 1, pre > end - lo ? end : lo + pre);
+  const bool one = a1 - a0 <= 32;  // the stretch's bits are still in registers
+  if (!one) {  // the rows' starts, front to back, for the pass below
+    int c = cur;
+    for (int g0 = a0; g0 < a1; g0 += 32) {
+      doc_bits(ids, g0, a1, &starts, &pads);
+      for (int o = 0; o < min(32, a1 - g0); ++o) {
+        if ((starts >> o) & 1u) c = g0 + o;
+        rows[g0 + o].x = c;
       }
-      used = max(used, i + 1);
     }
-    rows[i] = r;
-    if (lo == i) end = i;
+  }
+  int used = 0;
+  const int* pre_at = nullptr;
+  int pre_all = 0;
+  if (p.prefix && p.causal) {
+    if (p.prefix_per_token) pre_at = p.prefix + static_cast<size_t>(b) * T;
+    else pre_all = max(0, p.prefix[b]);
+  }
+  for (int g0 = a0 + max(0, (a1 - a0 - 1)) / 32 * 32; g0 >= a0 && a1 > a0; g0 -= 32) {
+    if (!one) doc_bits(ids, g0, a1, &starts, &pads);
+    for (int o = min(32, a1 - g0) - 1; o >= 0; --o) {
+      const int i = g0 + o;
+      int lo;
+      if (one) {
+        const uint32_t at = starts & ((2u << o) - 1u);
+        lo = at ? g0 + 31 - __clz(at) : cur;
+      } else {
+        lo = rows[i].x;
+      }
+      int2 r = make_int2(lo, end);
+      if ((pads >> o) & 1u) {
+        r = make_int2(0, 0);
+      } else {
+        if (p.causal) {
+          const int pre = pre_at ? max(0, pre_at[i]) : pre_all;
+          r.y = max(i + 1, pre > end - lo ? end : lo + pre);
+        }
+        used = max(used, i + 1);
+      }
+      rows[i] = r;
+      if (lo == i) end = i;
+    }
   }
   for (long long i = T + tid; i < T_pad; i += kVisThreads) rows[i] = make_int2(0, 0);
-  atomicMax(&s_used, used);
+  used = __reduce_max_sync(0xffffffffu, used);
+  if (lane == 0) atomicMax(&s_used, used);
   __syncthreads();
   const size_t t0 = static_cast<size_t>(b) * n_t;
   for (int t = warp; t < n_t; t += kWarps) {
@@ -147,7 +207,7 @@ __global__ void __launch_bounds__(kVisThreads) fa_visible_kernel(const VisiblePa
     hi_max = __reduce_max_sync(0xffffffffu, hi_max);
     if (lane == 0) {
       p.whole[t0 + t] = make_int2(lo_max, hi_min);
-      p.span[t0 + t] = hi_max > lo_min ? make_int2(lo_min, hi_max) : make_int2(0, 0);
+      span[t] = hi_max > lo_min ? make_int2(lo_min, hi_max) : make_int2(0, 0);
     }
   }
   __syncthreads();
@@ -157,7 +217,7 @@ __global__ void __launch_bounds__(kVisThreads) fa_visible_kernel(const VisiblePa
     int f = n_t, l = 0;
     const int k0 = t * 128;
     for (int q = lane; q < n_t; q += 32) {
-      const int2 s = p.span[t0 + q];
+      const int2 s = span[q];
       if (s.y > k0 && s.x < k0 + 128) {
         f = min(f, q);
         l = max(l, q + 1);
@@ -165,15 +225,15 @@ __global__ void __launch_bounds__(kVisThreads) fa_visible_kernel(const VisiblePa
     }
     f = __reduce_min_sync(0xffffffffu, f);
     l = __reduce_max_sync(0xffffffffu, l);
-    if (lane == 0) p.seen[t0 + t] = l > f ? make_int2(f, l) : make_int2(0, 0);
+    if (lane == 0) seen[t] = l > f ? make_int2(f, l) : make_int2(0, 0);
   }
   __syncthreads();
   for (int t = warp; t < n_t; t += kWarps) {
-    const int2 s = p.span[t0 + t], k = p.seen[t0 + t];
+    const int2 s = span[t], k = seen[t];
     const int kb = s.x >> 7, ke = (s.y + 127) >> 7;
     int rf = 0, rb = 0;
     for (int q = lane; q < n_t; q += 32) {
-      const int2 os = p.span[t0 + q], ok = p.seen[t0 + q];
+      const int2 os = span[q], ok = seen[q];
       const int on = ((os.y + 127) >> 7) - (os.x >> 7), on2 = ok.y - ok.x;
       rf += on > ke - kb || (on == ke - kb && q < t);
       rb += on2 > k.y - k.x || (on2 == k.y - k.x && q < t);
@@ -198,6 +258,21 @@ bool mod_sizes(int B, int H, int Hkv, int T, int d) {
   return BH <= INT32_MAX && n_t * 128 <= INT32_MAX && BH * n_t <= INT32_MAX &&
          static_cast<long long>(T) * d * 2 < (1LL << 40) && BH * T * d < (1LL << 61);
 }
+
+// Parts that a key head's query heads are cut into in the backward (a divisor of them): the fewest
+// that give at least kMinCtas CTAs, four for each of a GB300's SMs, so that their unequal walks can
+// be shared out (H16 Hkv4 T8192 d128, five documents: SIDE_E µs with the 256 CTAs of whole groups,
+// SIDE_F in SIDE_G parts). Independent of the device, so that a workspace fits wherever it is made.
+int bwd_parts(int B, int H, int Hkv, int T) {
+  constexpr long long kMinCtas = 456;
+  const int group = H / Hkv;
+  const long long ctas = static_cast<long long>(B) * Hkv * ((static_cast<long long>(T) + 127) / 128);
+  int parts = 1;
+  while (parts < group && (group % parts != 0 || ctas * parts < kMinCtas)) ++parts;
+  return parts;
+}
+
+constexpr long long kFewCtas = 1100;
 
 bool any_misaligned(std::initializer_list<const void*> ps) {
   for (const void* x : ps)
@@ -322,6 +397,14 @@ int fa_fwd_mod(const void* q, const void* k, const void* v, void* o, float* lse,
   return e == cudaSuccess ? FA_OK : FA_ERR_LAUNCH;
 }
 
+size_t fa_bwd_mod_workspace_size(int B, int H, int Hkv, int T, int d) {
+  if (!mod_sizes(B, H, Hkv, T, d)) return 0;
+  const size_t base = fa_bwd_workspace_size(B, H, T, d);  // a multiple of 256
+  const int parts = bwd_parts(B, H, Hkv, T);
+  if (base == 0 || parts == 1) return base;
+  return base + static_cast<size_t>(2) * parts * B * Hkv * T * d * 4;
+}
+
 int fa_bwd_mod(const void* q, const void* k, const void* v, const void* o, const void* dout,
                const float* lse, void* dq, void* dk, void* dv, void* workspace, size_t workspace_bytes,
                const void* visible, int causal, float softcap, const float* slopes, int B, int H,
@@ -332,7 +415,7 @@ int fa_bwd_mod(const void* q, const void* k, const void* v, const void* o, const
   fa::CapFactors cap;
   if (!mod_sizes(B, H, Hkv, T, d) || !scale_ok(scale) || !cap_factors(scale, softcap, &cap))
     return FA_ERR_INVALID_ARG;
-  const size_t need = fa_bwd_workspace_size(B, H, T, d);
+  const size_t need = fa_bwd_mod_workspace_size(B, H, Hkv, T, d);
   if (need == 0 || workspace_bytes < need) return FA_ERR_INVALID_ARG;
   if (any_misaligned({q, k, v, o, dout, lse, dq, dk, dv}) || (reinterpret_cast<uintptr_t>(workspace) & 255u) ||
       (reinterpret_cast<uintptr_t>(visible) & 255u) || (reinterpret_cast<uintptr_t>(slopes) & 3u))
@@ -375,13 +458,18 @@ int fa_bwd_mod(const void* q, const void* k, const void* v, const void* o, const
   a.p.status = status;
   a.p.T = T;
   a.p.T_pad = T_pad;
-  a.p.BH = BHkv;
+  const int parts = bwd_parts(B, H, Hkv, T);
+  a.p.BH = BHkv * parts;
   a.p.n_qt = T_pad / bq;
   a.p.n_kt = n_t;
-  // Key heads per group: their query heads' Q and dO (bf16) plus the fp32 dQ accumulator, about
-  // 64 MB (half the L2).
-  const long long per_head = 8LL * T_pad * d * (H / Hkv);
-  a.p.head_group = static_cast<int>(std::max<long long>(1, std::min<long long>(BHkv, (64LL << 20) / per_head)));
+  // Heads whose units go out together, the longest walks first: with few CTAs all of them, since
+  // a long walk that starts late is the call's tail (H16 Hkv4 T8192 d128, five documents: SIDE_H ->
+  // SIDE_I µs); otherwise as many as keep their Q and dO (bf16) and dQ accumulator (fp32) in half
+  // the L2, 64 MB.
+  const long long per_head = 8LL * T_pad * d * (H / Hkv / parts);
+  const long long in_l2 = std::max<long long>(1, (64LL << 20) / per_head);
+  const bool few = static_cast<long long>(n_t) * a.p.BH <= kFewCtas;
+  a.p.head_group = static_cast<int>(std::min<long long>(a.p.BH, few ? a.p.BH : in_l2));
   a.p.scale = scale;
   a.p.scale_log2 = static_cast<float>(static_cast<double>(scale) * kLog2e);
   a.p.timeout_ns = timeout_ns ? timeout_ns : 2000000000ull;
@@ -395,13 +483,15 @@ int fa_bwd_mod(const void* q, const void* k, const void* v, const void* o, const
   a.p.mod.slopes = slopes;
   a.p.mod.Hkv = Hkv;
   a.p.mod.group = H / Hkv;
+  a.p.mod.parts = parts;
+  a.p.mod.part_out = reinterpret_cast<float*>(ws + fa_bwd_workspace_size(B, H, T, d));
   a.p.mod.cap = cap;
   a.p.mod.causal = causal != 0;
   a.o = static_cast<const __nv_bfloat16*>(o);
   a.dout = static_cast<const __nv_bfloat16*>(dout);
   a.lse = lse;
   a.dq = static_cast<__nv_bfloat16*>(dq);
-  a.grid_main = static_cast<unsigned>(static_cast<long long>(n_t) * BHkv);
+  a.grid_main = static_cast<unsigned>(static_cast<long long>(n_t) * a.p.BH);
   a.grid_prep = static_cast<unsigned>(sms) * 8u;
   a.grid_dq = static_cast<unsigned>(sms) * 8u;
   a.stream = static_cast<cudaStream_t>(stream);

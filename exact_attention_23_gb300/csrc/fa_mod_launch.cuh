@@ -18,7 +18,7 @@ cudaError_t launch_fwd_mod(const FwdLaunch& a) {
   return launch_pdl(fn, a.grid, Cfg1<D>::kThreads, smem, a.stream, a.tm_q, a.tm_k, a.tm_v, a.tm_o, a.p);
 }
 
-// a.p.BH counts key heads; q_heads = B·H.
+// a.p.BH counts key heads' parts; q_heads = B·H.
 template <int D, int MOD>
 cudaError_t launch_bwd_mod(const BwdLaunch& a, int q_heads) {
   using C = BwdCfg<D, MOD>;
@@ -32,6 +32,12 @@ cudaError_t launch_bwd_mod(const BwdLaunch& a, int q_heads) {
   e = launch_pdl(fn, a.grid_main, C::kThreads, C::kSmemBytes, a.stream, a.tm_q, a.tm_k, a.tm_v, a.tm_do,
                  a.p);
   if (e != cudaSuccess) return e;
+  if (a.p.mod.parts > 1) {
+    const size_t elems = static_cast<size_t>(a.p.BH / a.p.mod.parts) * a.p.T * D;
+    const float* part_out = a.p.mod.part_out;
+    e = launch_pdl(fa_bwd_sum_kernel, a.grid_dq, 256, 0, a.stream, part_out, a.p.dk, a.p.dv, elems, a.p.mod.parts);
+    if (e != cudaSuccess) return e;
+  }
   return launch_pdl(fa_bwd_dq_kernel<D>, a.grid_dq, 256, 0, a.stream, a.p.dq_acc, a.dq, a.p.T, a.p.n_qt,
                     q_heads, a.p.scale);
 }

@@ -11,12 +11,13 @@ import math
 
 import torch
 
-from . import _check, bwd_workspace
+from . import _check
 from ._binding import (
     FA_ERR_INVALID_ARG,
     FA_OK,
     FAError,
     fa_bwd_mod,
+    fa_bwd_mod_workspace_size,
     fa_fwd_mod,
     fa_fwd_tree,
     fa_fwd_tree_workspace_size,
@@ -202,12 +203,20 @@ def fwd_mod(q, k, v, visible=None, causal: bool | None = None, softcap: float = 
     return out, lse
 
 
+def bwd_mod_workspace(B: int, H: int, Hkv: int, T: int, d: int, device=None):
+    """A uint8 CUDA tensor large enough to serve as ``bwd_mod``'s workspace."""
+    n = fa_bwd_mod_workspace_size(B, H, Hkv, T, d)
+    if n == 0:
+        raise FAError(FA_ERR_INVALID_ARG, "fa_bwd_mod_workspace_size")
+    return torch.empty(n, dtype=_U8, device="cuda" if device is None else device)
+
+
 def bwd_mod(q, k, v, o, lse, do, visible=None, causal: bool | None = None, softcap: float = 0.0,
             slopes=None, scale: float | None = None, dq=None, dk=None, dv=None, workspace=None,
             status=None, timeout_ns: int = 0):
     """Gradients of ``fwd_mod`` through fa_bwd_mod: (dq [B, H, T, d], dk, dv [B, Hkv, T, d]), from
     its outputs ``o`` and ``lse`` and the gradient ``do`` of o; the other arguments as there.
-    ``workspace`` (see ``bwd_workspace``, with the query heads H) may be passed to reuse it."""
+    ``workspace`` (see ``bwd_mod_workspace``) may be passed to reuse it."""
     B, H, T, d, Hkv, causal = _check_mod(q, k, v, visible, causal, slopes)
     device = q.device
     _check_like(o, q, "o")
@@ -228,7 +237,7 @@ def bwd_mod(q, k, v, o, lse, do, visible=None, causal: bool | None = None, softc
     else:
         _check_like(dv, v, "dv")
     if workspace is None:
-        workspace = bwd_workspace(B, H, T, d, device=device)
+        workspace = bwd_mod_workspace(B, H, Hkv, T, d, device=device)
     else:
         _check_workspace(workspace, device)
     _check_status(status, device)

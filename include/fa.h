@@ -352,10 +352,11 @@ int fa_fwd_mod(const void* q, const void* k, const void* v, void* o, float* lse,
  * with P = exp(z − LSE) and dS = P ∘ (dO Vᵀ − D) ∘ (1 − tanh²), D = rowsum(dO ∘ O),
  *   dQ = scale · dS K,   dK = scale · dSᵀ Q,   dV = Pᵀ dO,
  * dK and dV summed over the query heads that share a key head. visible, causal, softcap, slopes
- * and scale are those of the forward. workspace: fa_bwd_workspace_size(B, H, T, d) bytes,
- * 256-byte aligned, as for fa_bwd. dQ is summed with atomic adds in an unspecified order (equal
+ * and scale are those of the forward. workspace: fa_bwd_mod_workspace_size(...) bytes (0:
+ * unsupported sizes), 256-byte aligned, otherwise as for fa_bwd. dQ is summed with atomic adds in an unspecified order (equal
  * within fp32 rounding from call to call, as fa_bwd's); dK and dV are the same bits every time.
  */
+size_t fa_bwd_mod_workspace_size(int B, int H, int Hkv, int T, int d);
 int fa_bwd_mod(const void* q, const void* k, const void* v, const void* o, const void* dout,
                const float* lse, void* dq, void* dk, void* dv, void* workspace, size_t workspace_bytes,
                const void* visible, int causal, float softcap, const float* slopes, int B, int H,

@@ -26,7 +26,7 @@ def _bwd(q=A, k=A + SZ, v=A + 2 * SZ, o=A + 3 * SZ, do=A + 4 * SZ, lse=A + 5 * S
          dk=A + 7 * SZ, dv=A + 8 * SZ, ws=A + 9 * SZ, ws_bytes=None, vis=None, causal=1, cap=0.0,
          slopes=None, B=2, H=4, Hkv=2, T=200, d=64, scale=0.125):
     if ws_bytes is None:
-        ws_bytes = fa.fa_bwd_workspace_size(B, H, T, d) or 1 << 20
+        ws_bytes = fa.fa_bwd_mod_workspace_size(B, H, Hkv, T, d) or 1 << 20
     return fa.fa_bwd_mod(q, k, v, o, do, lse, dq, dk, dv, ws, ws_bytes, vis, causal, cap, slopes, B,
                          H, Hkv, T, d, scale, None, 0, None)
 
@@ -77,6 +77,16 @@ def test_valid_calls_without_device_report_unsupported():
     assert _fwd(cap=30.0, slopes=A + 20 * SZ) == fa.FA_ERR_UNSUPPORTED_DEVICE
     assert _bwd(cap=30.0, vis=A + 21 * SZ) == fa.FA_ERR_UNSUPPORTED_DEVICE
     assert fa.fa_visible(None, None, 0, 1, A, 1 << 20, 1, 100, None) == fa.FA_ERR_UNSUPPORTED_DEVICE
+
+
+def test_bwd_workspace():
+    """The backward's own, and, where a key head's query heads are cut into parts, their sums."""
+    assert fa.fa_bwd_mod_workspace_size(4, 12, 12, 2048, 64) == fa.fa_bwd_workspace_size(4, 12, 2048, 64)
+    assert fa.fa_bwd_mod_workspace_size(1, 12, 12, 128, 64) == fa.fa_bwd_workspace_size(1, 12, 128, 64)
+    assert fa.fa_bwd_mod_workspace_size(1, 12, 4, 128, 128) == \
+        fa.fa_bwd_workspace_size(1, 12, 128, 128) + 2 * 3 * 4 * 128 * 128 * 4
+    for bad in ((0, 4, 2, 128, 64), (1, 4, 3, 128, 64), (1, 4, 2, 0, 64), (1, 4, 2, 128, 80)):
+        assert fa.fa_bwd_mod_workspace_size(*bad) == 0
 
 
 def test_wrappers_reject_cpu_tensors():
@@ -195,6 +205,38 @@ def test_parity_with_visible(B, H, Hkv, T, d, causal, cap, bias, lengths, pad, p
     seen = fa.visible(B, T, causal=causal, doc_ids=ids.cuda(),
                       prefix_len=None if pre is None else pre.cuda())
     ref.check(_run(q, k, v, do, seen, softcap=cap, slopes=sl), r, ALL)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("T,lengths,pad,causal,prefix", [
+    (1, (1,), 0, True, None), (31, (4, 9), 3, True, "b"), (1000, (128, 77), 0, False, None),
+    (33000, (1000, 1, 2048), 129, True, "t"), (70001, (50000, 333), 7, True, "b"),
+    (200000, (100, 60000, 17), 5000, True, None),
+])
+def test_visible_rows(T, lengths, pad, causal, prefix):
+    """Every row's interval, at lengths where a thread holds one row to several hundred."""
+    B = 2
+    ids = _ids(B, T, lengths, pad)
+    first = torch.cat((torch.ones(B, 1, dtype=torch.bool), ids[:, 1:] != ids[:, :-1]), 1)
+    at = torch.arange(T).expand(B, T)
+    lo = torch.where(first, at, torch.zeros_like(at)).cummax(1).values
+    nxt = torch.where(first, at, torch.full_like(at, T))
+    end = torch.cat((nxt[:, 1:], torch.full((B, 1), T)), 1).flip(1).cummin(1).values.flip(1)
+    pre = None
+    if prefix == "b":
+        pre = torch.tensor([5, 40000][:B], dtype=torch.int32)
+    elif prefix == "t":
+        pre = ((ids + 2) * 23 - 40).to(torch.int32)
+    hi = end
+    if causal:
+        n = torch.zeros_like(at) if pre is None else (pre.long()[:, None] if pre.dim() == 1 else pre.long())
+        hi = torch.maximum(at + 1, torch.minimum(end, lo + n.clamp(min=0)))
+    want = torch.stack((lo, hi), -1) * (ids >= 0)[..., None]
+    seen = fa.visible(B, T, causal=causal, doc_ids=ids.cuda(),
+                      prefix_len=None if pre is None else pre.cuda())
+    T_pad = -(-T // 128) * 128
+    rows = seen.buffer[:B * T_pad * 8].view(torch.int32).view(B, T_pad, 2).cpu().long()
+    assert torch.equal(rows[:, :T], want) and not rows[:, T:].any()
 
 
 @pytest.mark.gpu
