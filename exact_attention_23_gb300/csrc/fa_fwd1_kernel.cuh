@@ -61,11 +61,16 @@
 
 namespace fa {
 
-template <int D>
+// REF (kModRef, the softmax against a fixed reference): the parts of a row need no accumulators
+// of their own, so the row's keys can be split over more warps, which hide one another's latency,
+// at either head dim.
+constexpr int kRefParts = 2;
+template <int D, bool REF = false>
 struct Cfg1 {
   static_assert(D == 64 || D == 128, "head dim");
-  // Softmax halves: two O accumulators fit tensor memory at D = 64 only.
-  static constexpr int kHalves = (D == 64) ? 2 : 1;
+  // Softmax halves (parts): two O accumulators fit tensor memory at D = 64 only.
+  static constexpr int kHalves = REF ? kRefParts : (D == 64) ? 2 : 1;
+  static constexpr int kAcc = REF ? 1 : kHalves;         // O accumulators
   static constexpr int kCols = kBlockN / kHalves;        // keys per softmax warp and step
   static constexpr int kSoftWarps = 4 * kHalves;
   static constexpr int kWarpS = kSoftWarps;              // S issuer, TMEM owner
@@ -93,11 +98,12 @@ struct Cfg1 {
   static constexpr int kBarOff = kXchOff + 2 * kHalves * kBlockM * 8;
   static constexpr int kSmemBytes = kBarOff + 512 + 1024;  // barriers + 1 KB alignment slack
   static __host__ __device__ constexpr uint32_t col_s(int b) { return b ? 128u : 0u; }
-  static __host__ __device__ constexpr uint32_t col_o(int h) { return 256u + h * D; }
+  static __host__ __device__ constexpr uint32_t col_o(int h) { return 256u + (REF ? 0 : h * D); }
   static __host__ __device__ constexpr uint32_t col_p(int b) {
-    return 256u + kHalves * D + (b ? 64u : 0u);
+    return 256u + kAcc * D + (b ? 64u : 0u);
   }
-  static_assert(256 + kHalves * D + 128 <= 512, "tensor memory columns");
+  static_assert(256 + kAcc * D + 128 <= 512, "tensor memory columns");
+  static_assert(kSmemBytes <= 232448, "shared memory");
 };
 
 struct Bars1 {
@@ -175,11 +181,11 @@ __device__ __forceinline__ Unit unit1_of(const FwdParams& p, int L, const Segmen
 
 // MOD (bits kMod…): modified scores; always with GEN (rows may see no key) and CAUSAL false.
 template <int D, bool CAUSAL, bool GEN = false, int MOD = 0>
-__global__ void __launch_bounds__(Cfg1<D>::kThreads, 1)
+__global__ void __launch_bounds__(Cfg1<D, (MOD & kModRef) != 0>::kThreads, 1)
     fa_fwd1_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
                    const __grid_constant__ CUtensorMap tm_v, const __grid_constant__ CUtensorMap tm_o,
                    const FwdParams p) {
-  using C = Cfg1<D>;
+  using C = Cfg1<D, (MOD & kModRef) != 0>;
   constexpr bool kTree = (MOD & kModTree) != 0;
   constexpr bool kRef = (MOD & kModRef) != 0;  // the softmax is taken against 0
   constexpr bool kXform = (MOD & (kModCap | kModBias)) != 0;  // scores are modified before the softmax
@@ -212,8 +218,8 @@ __global__ void __launch_bounds__(Cfg1<D>::kThreads, 1)
     mbar_init(&bars->mma_done, 2);
 #pragma unroll
     for (int q = 0; q < 4; ++q) {
-      mbar_init(&bars->xch[q][0], 2);
-      mbar_init(&bars->xch[q][1], 2);
+      mbar_init(&bars->xch[q][0], C::kHalves > 2 ? C::kHalves : 2);
+      mbar_init(&bars->xch[q][1], C::kHalves > 2 ? C::kHalves : 2);
     }
     bars->abort = 0u;
     fence_mbar_init();
@@ -403,7 +409,7 @@ __global__ void __launch_bounds__(Cfg1<D>::kThreads, 1)
               for (int kk = 0; kk < C::kCols / 16; ++kk)
                 mma_ts(tmem + C::col_o(h), tmem + C::col_p(b) + h * (C::kCols / 2) + kk * 8,
                        sdesc_sw128(va + (h * (C::kCols / 16) + kk) * 2048, C::kSubBytes, 1024),
-                       idesc, (j > 0 || kk > 0) ? 1u : 0u);
+                       idesc, (j > 0 || kk > 0 || (kRef && h > 0)) ? 1u : 0u);
             mma_commit(&bars->pv_done[b]);
             mma_commit(&bars->kv_empty[st]);  // V(j) is free once this product is done
           }
@@ -489,7 +495,64 @@ __global__ void __launch_bounds__(Cfg1<D>::kThreads, 1)
     // merges them with the weights 2^(m_h − m) / l and writes them straight to memory.
     // Returns false when the meeting gave up (the rows are then written as failed).
     auto epilogue = [&](const RowOut& w, float l, float m) -> bool {
-      if constexpr (H == 2) {
+      if constexpr (kRef) {
+        // The parts of a row share O and the reference: they post their sums, meet, and each
+        // writes its columns.
+        const int par = ne & 1;
+        float* xs = reinterpret_cast<float*>(smem + C::kXchOff) + (par * H) * kBlockM;
+        xs[half * kBlockM + row] = l;
+        __threadfence_block();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&bars->xch[quad][par]);
+        const bool met = mbar_wait_warp(&bars->xch[quad][par], (ne >> 1) & 1, wc);
+        ++ne;
+        if (!met) {
+          tc_fence_before_sync();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&bars->o_free);
+          fail_rows(w);
+          return false;
+        }
+        float L = 0.0f;
+#pragma unroll
+        for (int h = 0; h < H; ++h) L += xs[h * kBlockM + row];
+        const float inv_l = !(L > 0.0f) ? 0.0f : 1.0f / L;
+        uint32_t o[kOutCols];
+        static_assert(kOutCols == 16 || kOutCols % 32 == 0, "output columns");
+        if constexpr (kOutCols == 16) {
+          tmem_ld16(t_o + c_out, o);
+          tmem_ld_wait();
+          reg_fence16(o);
+        } else {
+#pragma unroll
+          for (int c0 = 0; c0 < kOutCols; c0 += 32) tmem_ld32(t_o + c_out + c0, o + c0);
+          tmem_ld_wait();
+#pragma unroll
+          for (int c0 = 0; c0 < kOutCols; c0 += 32) reg_fence32(o + c0);
+        }
+        tc_fence_before_sync();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&bars->o_free);
+        if (w.in_range) {
+          if (w.partial) {
+            float4* prow = reinterpret_cast<float4*>(p.o_part + w.part_idx * D + c_out);
+#pragma unroll
+            for (int t = 0; t < kOutCols / 4; ++t)
+              prow[t] = make_float4(u2f(o[4 * t]) * inv_l, u2f(o[4 * t + 1]) * inv_l,
+                                    u2f(o[4 * t + 2]) * inv_l, u2f(o[4 * t + 3]) * inv_l);
+          } else {
+            uint4* orow = reinterpret_cast<uint4*>(p.o + w.row_idx * D + c_out);
+#pragma unroll
+            for (int t = 0; t < kOutCols / 8; ++t)
+              orow[t] = make_uint4(pack_bf16x2(u2f(o[8 * t]) * inv_l, u2f(o[8 * t + 1]) * inv_l),
+                                   pack_bf16x2(u2f(o[8 * t + 2]) * inv_l, u2f(o[8 * t + 3]) * inv_l),
+                                   pack_bf16x2(u2f(o[8 * t + 4]) * inv_l, u2f(o[8 * t + 5]) * inv_l),
+                                   pack_bf16x2(u2f(o[8 * t + 6]) * inv_l, u2f(o[8 * t + 7]) * inv_l));
+          }
+        }
+        write_lse(w, !(L > 0.0f) ? -INFINITY : log2f(L) * 0.69314718055994530942f);
+        return true;
+      } else if constexpr (H == 2) {
         const int par = ne & 1;
         float2* xs = reinterpret_cast<float2*>(smem + C::kXchOff) + (par * H) * kBlockM;
         xs[half * kBlockM + row] = make_float2(m, l);
@@ -910,8 +973,12 @@ __global__ void __launch_bounds__(Cfg1<D>::kThreads, 1)
         }
         FA1_TRACE(44, j);
         const uint32_t t_p = tmem + lane_off + C::col_p(b) + half * (kC / 2);
+        if constexpr (kC == 32) {
+          tmem_st16(t_p, pk);
+        } else {
 #pragma unroll
-        for (int c0 = 0; c0 < kC / 2; c0 += 32) tmem_st32(t_p + c0, pk + c0);
+          for (int c0 = 0; c0 < kC / 2; c0 += 32) tmem_st32(t_p + c0, pk + c0);
+        }
         tmem_st_wait();
         tc_fence_before_sync();
         __syncwarp();

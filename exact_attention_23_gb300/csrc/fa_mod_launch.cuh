@@ -12,10 +12,11 @@ template <int D, int MOD>
 cudaError_t launch_fwd_mod(const FwdLaunch& a) {
   auto* fn = &fa_fwd1_kernel<D, false, true, MOD>;
   static std::atomic<uint64_t> done[kMaxDevices / 64 + 1];
-  const int smem = Cfg1<D>::kSmemBytes;
+  using C = Cfg1<D, (MOD & kModRef) != 0>;
+  const int smem = C::kSmemBytes;
   const cudaError_t e = smem_opt_in(fn, smem, done);
   if (e != cudaSuccess) return e;
-  return launch_pdl(fn, a.grid, Cfg1<D>::kThreads, smem, a.stream, a.tm_q, a.tm_k, a.tm_v, a.tm_o, a.p);
+  return launch_pdl(fn, a.grid, C::kThreads, smem, a.stream, a.tm_q, a.tm_k, a.tm_v, a.tm_o, a.p);
 }
 
 // a.p.BH counts key heads' parts; q_heads = B·H.
