@@ -366,12 +366,14 @@ def run(state):
         if c["docs"] or c["prefix"]:
             seen = fa.visible(c["B"], c["T"], causal=c["causal"], doc_ids=s.get("doc_ids"),
                               prefix_len=s.get("prefix_len"), device=s["q"].device)
+        rest = torch.empty_like(s["q"]) if c["kind"] == "train" else None
         o, lse = fa.fwd_mod(s["q"], s["k"], s["v"], visible=seen, causal=c["causal"],
-                            softcap=c["softcap"], slopes=s["slopes"])
+                            softcap=c["softcap"], slopes=s["slopes"], rest=rest)
         if c["kind"] == "fwd":
             return {"o": o, "lse": lse}
         dq, dk, dv = fa.bwd_mod(s["q"], s["k"], s["v"], o, lse, s["do"], visible=seen,
-                                causal=c["causal"], softcap=c["softcap"], slopes=s["slopes"])
+                                causal=c["causal"], softcap=c["softcap"], slopes=s["slopes"],
+                                rest=rest)
         return {"o": o, "lse": lse, "dq": dq, "dk": dk, "dv": dv}
     if c["kind"] == "rope":
         return {x: _rotate(s[x], s["positions"], s["inv_freq"], c["interleaved"], s["mscale"],
