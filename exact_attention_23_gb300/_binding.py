@@ -45,6 +45,8 @@ class FAError(RuntimeError):
 def lib() -> ctypes.CDLL:
     """Load libfa.so (once). Raises if it has not been built."""
     global _lib
+    if _lib is not None:
+        return _lib
     with _lock:
         if _lib is None:
             if not os.path.exists(LIB_PATH):
@@ -84,9 +86,9 @@ def lib() -> ctypes.CDLL:
             L.fa_visible.argtypes = [vp, vp, i, i, vp, sz, i, i, vp]
             L.fa_visible.restype = i
             ull, ll = ctypes.c_ulonglong, ctypes.c_longlong
-            L.fa_fwd_mod.argtypes = [vp] * 6 + [i, f, vp, i, i, i, i, i, f, vp, ull, vp]
+            L.fa_fwd_mod.argtypes = [vp] * 7 + [i, f, vp, i, i, i, i, i, f, vp, ull, vp]
             L.fa_fwd_mod.restype = i
-            L.fa_bwd_mod.argtypes = [vp] * 10 + [sz, vp, i, f, vp, i, i, i, i, i, f, vp, ull, vp]
+            L.fa_bwd_mod.argtypes = [vp] * 11 + [sz, vp, i, f, vp, i, i, i, i, i, f, vp, ull, vp]
             L.fa_bwd_mod.restype = i
             L.fa_bwd_mod_workspace_size.argtypes = [i] * 5
             L.fa_bwd_mod_workspace_size.restype = sz
@@ -190,15 +192,15 @@ def fa_visible(doc_ids, prefix_len, prefix_per_token, causal, visible, visible_b
                             int(visible_bytes), B, T, stream)
 
 
-def fa_fwd_mod(q, k, v, o, lse, visible, causal, softcap, slopes, B, H, Hkv, T, d, scale, status,
-               timeout_ns, stream) -> int:
-    return lib().fa_fwd_mod(q, k, v, o, lse, visible, int(bool(causal)), float(softcap), slopes, B,
+def fa_fwd_mod(q, k, v, o, lse, rest, visible, causal, softcap, slopes, B, H, Hkv, T, d, scale,
+               status, timeout_ns, stream) -> int:
+    return lib().fa_fwd_mod(q, k, v, o, lse, rest, visible, int(bool(causal)), float(softcap), slopes, B,
                             H, Hkv, T, d, float(scale), status, int(timeout_ns), stream)
 
 
-def fa_bwd_mod(q, k, v, o, dout, lse, dq, dk, dv, workspace, workspace_bytes, visible, causal,
+def fa_bwd_mod(q, k, v, o, dout, lse, rest, dq, dk, dv, workspace, workspace_bytes, visible, causal,
                softcap, slopes, B, H, Hkv, T, d, scale, status, timeout_ns, stream) -> int:
-    return lib().fa_bwd_mod(q, k, v, o, dout, lse, dq, dk, dv, workspace, int(workspace_bytes),
+    return lib().fa_bwd_mod(q, k, v, o, dout, lse, rest, dq, dk, dv, workspace, int(workspace_bytes),
                             visible, int(bool(causal)), float(softcap), slopes, B, H, Hkv, T, d,
                             float(scale), status, int(timeout_ns), stream)
 

@@ -22,7 +22,7 @@ static cudaError_t launch_bwd(const BwdLaunch& a) {
   // All three as programmatic dependents: each one's launch and set-up overlap the tail of
   // the kernel before it, and each waits for it (pdl_wait) before reading its results.
   cudaError_t e = launch_pdl(fa_bwd_prep_kernel<D>, a.grid_prep, 256, 0, a.stream, a.o, a.dout,
-                             a.lse, a.lse2, a.dvec, a.p.dq_acc, a.p.T, a.p.T_pad, a.p.BH);
+                             a.lse, a.lse2, a.dvec, a.p.dq_acc, a.p.T, a.p.T_pad, a.p.BH, nullptr);
   if (e != cudaSuccess) return e;
   e = launch_pdl(fn, a.grid_main, BwdCfg<D>::kThreads, smem, a.stream, a.tm_q, a.tm_k, a.tm_v, a.tm_do,
                  a.p);

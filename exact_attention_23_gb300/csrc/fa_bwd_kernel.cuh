@@ -216,7 +216,7 @@ __host__ __device__ __forceinline__ size_t dq_acc_offset_t(int bh, int i, int n_
 // D/8 consecutive lanes share a row, each reading 8 columns (16 bytes) of O and dO.
 // ------------------------------------------------------------------------------------
 // MOD: a row that saw no key (lse = −∞) gets −∞ and D = 0, so that its P and dS are 0 whatever
-// its o and dO hold.
+// its o and dO hold; D takes o and, where it is given, what o's rounding left out.
 template <int D, bool MOD = false>
 __global__ void __launch_bounds__(256) fa_bwd_prep_kernel(const __nv_bfloat16* __restrict__ o,
                                                           const __nv_bfloat16* __restrict__ dout,
@@ -224,7 +224,8 @@ __global__ void __launch_bounds__(256) fa_bwd_prep_kernel(const __nv_bfloat16* _
                                                           float* __restrict__ lse2,
                                                           float* __restrict__ dvec,
                                                           float* __restrict__ dq_acc, int T,
-                                                          int T_pad, int BH) {
+                                                          int T_pad, int BH,
+                                                          const __nv_bfloat16* __restrict__ rest = nullptr) {
   constexpr int L = D / 8;
   pdl_wait();  // launched as a programmatic dependent (o, dO and lse may come from the previous kernel)
   pdl_launch_dependents();
@@ -250,6 +251,17 @@ __global__ void __launch_bounds__(256) fa_bwd_prep_kernel(const __nv_bfloat16* _
         const float2 fb2 = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&bv[e]));
         acc = fmaf(fa2.x, fb2.x, acc);
         acc = fmaf(fa2.y, fb2.y, acc);
+      }
+      if (MOD && rest) {
+        const uint4 r = *reinterpret_cast<const uint4*>(rest + off);
+        const uint32_t rv[4] = {r.x, r.y, r.z, r.w};
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const float2 fr2 = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&rv[e]));
+          const float2 fb2 = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&bv[e]));
+          acc = fmaf(fr2.x, fb2.x, acc);
+          acc = fmaf(fr2.y, fb2.y, acc);
+        }
       }
     }
 #pragma unroll

@@ -188,6 +188,8 @@ __global__ void __launch_bounds__(Cfg1<D, (MOD & kModRef) != 0>::kThreads, 1)
   using C = Cfg1<D, (MOD & kModRef) != 0>;
   constexpr bool kTree = (MOD & kModTree) != 0;
   constexpr bool kRef = (MOD & kModRef) != 0;  // the softmax is taken against 0
+  constexpr bool kRefRest = (MOD & kModRest) != 0;        // … with o's rest
+  constexpr bool kRest = MOD != 0 && !kTree && (!kRef || kRefRest);  // o's rest may be asked for
   constexpr bool kXform = (MOD & (kModCap | kModBias)) != 0;  // scores are modified before the softmax
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
@@ -455,6 +457,16 @@ __global__ void __launch_bounds__(Cfg1<D, (MOD & kModRef) != 0>::kThreads, 1)
                         static_cast<size_t>(q_row),
                     r0, bh, q_row < p.T, GEN && p.n_splits > 1};
     };
+    // The part of 8 values of a row that their rounding to bf16 (hi) leaves out, as bf16.
+    auto rest_of = [&](const float* x, const uint4& hi) {
+      const uint32_t u[4] = {hi.x, hi.y, hi.z, hi.w};
+      uint32_t lo[4];
+#pragma unroll
+      for (int e = 0; e < 4; ++e)
+        lo[e] = pack_bf16x2(x[2 * e] - __uint_as_float(u[e] << 16),
+                            x[2 * e + 1] - __uint_as_float(u[e] & 0xFFFF0000u));
+      return make_uint4(lo[0], lo[1], lo[2], lo[3]);
+    };
     constexpr int kOutCols = D / H;           // output columns this warp writes
     const int c_out = half * kOutCols;
     auto write_lse = [&](const RowOut& w, float v) {
@@ -475,6 +487,13 @@ __global__ void __launch_bounds__(Cfg1<D, (MOD & kModRef) != 0>::kThreads, 1)
         const uint32_t b2 = pack_bf16x2(u2f(bits), u2f(bits));
 #pragma unroll
         for (int t = 0; t < kOutCols / 8; ++t) orow[t] = make_uint4(b2, b2, b2, b2);
+        if constexpr (kRest) {
+          if (p.mod.rest) {
+            uint4* rrow = reinterpret_cast<uint4*>(p.mod.rest + w.row_idx * D + c_out);
+#pragma unroll
+            for (int t = 0; t < kOutCols / 8; ++t) rrow[t] = make_uint4(b2, b2, b2, b2);
+          }
+        }
       }
     };
     auto fail_rows = [&](const RowOut& w) {
@@ -499,8 +518,9 @@ __global__ void __launch_bounds__(Cfg1<D, (MOD & kModRef) != 0>::kThreads, 1)
         // The parts of a row share O and the reference: they post their sums, meet, and each
         // writes its columns.
         const int par = ne & 1;
-        float* xs = reinterpret_cast<float*>(smem + C::kXchOff) + (par * H) * kBlockM;
-        xs[half * kBlockM + row] = l;
+        // (m: the sum of the rounded weights, kRefRest)
+        float2* xs = reinterpret_cast<float2*>(smem + C::kXchOff) + (par * H) * kBlockM;
+        xs[half * kBlockM + row] = make_float2(l, m);
         __threadfence_block();
         __syncwarp();
         if (lane == 0) mbar_arrive(&bars->xch[quad][par]);
@@ -513,10 +533,14 @@ __global__ void __launch_bounds__(Cfg1<D, (MOD & kModRef) != 0>::kThreads, 1)
           fail_rows(w);
           return false;
         }
-        float L = 0.0f;
+        float L = 0.0f, LR = 0.0f;
 #pragma unroll
-        for (int h = 0; h < H; ++h) L += xs[h * kBlockM + row];
-        const float inv_l = !(L > 0.0f) ? 0.0f : 1.0f / L;
+        for (int h = 0; h < H; ++h) {
+          const float2 x = xs[h * kBlockM + row];
+          L += x.x;
+          LR += x.y;
+        }
+        const float inv_l = !(L > 0.0f) ? 0.0f : 1.0f / (kRefRest ? LR : L);
         uint32_t o[kOutCols];
         static_assert(kOutCols == 16 || kOutCols % 32 == 0, "output columns");
         if constexpr (kOutCols == 16) {
@@ -543,11 +567,19 @@ __global__ void __launch_bounds__(Cfg1<D, (MOD & kModRef) != 0>::kThreads, 1)
           } else {
             uint4* orow = reinterpret_cast<uint4*>(p.o + w.row_idx * D + c_out);
 #pragma unroll
-            for (int t = 0; t < kOutCols / 8; ++t)
-              orow[t] = make_uint4(pack_bf16x2(u2f(o[8 * t]) * inv_l, u2f(o[8 * t + 1]) * inv_l),
-                                   pack_bf16x2(u2f(o[8 * t + 2]) * inv_l, u2f(o[8 * t + 3]) * inv_l),
-                                   pack_bf16x2(u2f(o[8 * t + 4]) * inv_l, u2f(o[8 * t + 5]) * inv_l),
-                                   pack_bf16x2(u2f(o[8 * t + 6]) * inv_l, u2f(o[8 * t + 7]) * inv_l));
+            for (int t = 0; t < kOutCols / 8; ++t) {
+              const uint4 hi = make_uint4(pack_bf16x2(u2f(o[8 * t]) * inv_l, u2f(o[8 * t + 1]) * inv_l),
+                                          pack_bf16x2(u2f(o[8 * t + 2]) * inv_l, u2f(o[8 * t + 3]) * inv_l),
+                                          pack_bf16x2(u2f(o[8 * t + 4]) * inv_l, u2f(o[8 * t + 5]) * inv_l),
+                                          pack_bf16x2(u2f(o[8 * t + 6]) * inv_l, u2f(o[8 * t + 7]) * inv_l));
+              orow[t] = hi;
+              if constexpr (kRefRest) {
+                float x[8];
+#pragma unroll
+                for (int e = 0; e < 8; ++e) x[e] = u2f(o[8 * t + e]) * inv_l;
+                *reinterpret_cast<uint4*>(p.mod.rest + w.row_idx * D + c_out + 8 * t) = rest_of(x, hi);
+              }
+            }
           }
         }
         write_lse(w, !(L > 0.0f) ? -INFINITY : log2f(L) * 0.69314718055994530942f);
@@ -607,6 +639,15 @@ __global__ void __launch_bounds__(Cfg1<D, (MOD & kModRef) != 0>::kThreads, 1)
                                      fmaf(u2f(o0[x + 1]), w0, u2f(o1[x + 1]) * w1));
               }
               orow[t] = make_uint4(pk4[0], pk4[1], pk4[2], pk4[3]);
+              if constexpr (kRest) {
+                if (p.mod.rest) {
+                  float x8[8];
+#pragma unroll
+                  for (int e = 0; e < 8; ++e) x8[e] = fmaf(u2f(o0[8 * t + e]), w0, u2f(o1[8 * t + e]) * w1);
+                  *reinterpret_cast<uint4*>(p.mod.rest + w.row_idx * D + c_out + 8 * t) =
+                      rest_of(x8, make_uint4(pk4[0], pk4[1], pk4[2], pk4[3]));
+                }
+              }
             }
           }
         }
@@ -641,6 +682,30 @@ __global__ void __launch_bounds__(Cfg1<D, (MOD & kModRef) != 0>::kThreads, 1)
           }
           if (lane == 0) bulk_wait_group_read0();  // the slice's previous store has read it
           __syncwarp();
+          if constexpr (kRest) {
+            // The rest goes through the same slice first, and out of it in whole rows of 128 bytes.
+            if (p.mod.rest) {
+#pragma unroll
+              for (int ch = 0; ch < 8; ++ch) {
+                float x[8];
+#pragma unroll
+                for (int e = 0; e < 8; ++e) x[e] = u2f(o[8 * ch + e]) * inv_l;
+                const uint4 lo = rest_of(x, make_uint4(pack_bf16x2(x[0], x[1]), pack_bf16x2(x[2], x[3]),
+                                                       pack_bf16x2(x[4], x[5]), pack_bf16x2(x[6], x[7])));
+                st_shared_v4(ob + ((ch ^ (lane & 7)) << 4), lo.x, lo.y, lo.z, lo.w);
+              }
+              __syncwarp();
+              __nv_bfloat16* dst = p.mod.rest + (static_cast<size_t>(w.bh) * p.T + w.r0) * D + hb * 64;
+#pragma unroll
+              for (int it = 0; it < 8; ++it) {
+                const int r = it * 4 + (lane >> 3), ch = lane & 7;
+                if (w.r0 + r < p.T)
+                  *reinterpret_cast<uint4*>(dst + static_cast<size_t>(r) * D + ch * 8) =
+                      *reinterpret_cast<const uint4*>(slice + r * 128 + ((ch ^ (r & 7)) << 4));
+              }
+              __syncwarp();
+            }
+          }
 #pragma unroll
           for (int ch = 0; ch < 8; ++ch)
             st_shared_v4(ob + ((ch ^ (lane & 7)) << 4),
@@ -746,7 +811,7 @@ __global__ void __launch_bounds__(Cfg1<D, (MOD & kModRef) != 0>::kThreads, 1)
       }
       // reference max (base-2 scaled units) shared by O_h and l
       float m_ref = kRef ? 0.0f : -INFINITY;
-      float l = 0.0f;
+      float l = 0.0f, lr = 0.0f;  // lr (kRefRest): the sum of the rounded weights
       // the tile's K tiles (GEN: its walk, the next position fetched a step ahead)
       Walk w{nullptr, 0};
       int nx = 0;
@@ -927,7 +992,7 @@ __global__ void __launch_bounds__(Cfg1<D, (MOD & kModRef) != 0>::kThreads, 1)
         const uint64_t c2 = f2_pack(c, c);
         const float m_use = ((GEN || H == 2) && m_ref == -INFINITY) ? 0.0f : m_ref;
         const uint64_t nm2 = f2_pack(-m_use, -m_use);
-        uint64_t acc0 = f2_pack(0.f, 0.f), acc1 = acc0;
+        uint64_t acc0 = f2_pack(0.f, 0.f), acc1 = acc0, acc_r = acc0;
         uint32_t pk[kC / 2];
         auto exponentials = [&]<bool FUSED>() {
 #pragma unroll
@@ -944,6 +1009,8 @@ __global__ void __launch_bounds__(Cfg1<D, (MOD & kModRef) != 0>::kThreads, 1)
             if (t & 1) acc1 = f2_add(acc1, f2_pack(p0, p1));
             else acc0 = f2_add(acc0, f2_pack(p0, p1));
             pk[t] = pack_bf16x2(p0, p1);
+            if constexpr (kRefRest)
+              acc_r = f2_add(acc_r, f2_pack(u2f(pk[t] << 16), u2f(pk[t] & 0xFFFF0000u)));
           }
         };
         if (kRef && fused) exponentials.template operator()<kRef>();
@@ -989,6 +1056,10 @@ __global__ void __launch_bounds__(Cfg1<D, (MOD & kModRef) != 0>::kThreads, 1)
           f2_unpack(acc0, a0, a1);
           f2_unpack(acc1, b0, b1);
           l += (a0 + b0) + (a1 + b1);
+          if constexpr (kRefRest) {
+            f2_unpack(acc_r, a0, a1);
+            lr += a0 + a1;
+          }
         }
         // (j = 0) The previous unit's last P·V, step g − 1, is the one before this step's:
         // read its O out (releasing O to this unit's first P·V) and write it.
@@ -1014,7 +1085,7 @@ __global__ void __launch_bounds__(Cfg1<D, (MOD & kModRef) != 0>::kThreads, 1)
         fail_rows(cur);
         continue;
       }
-      *prec = make_float4(l, m_ref, __int_as_float(cur.r0), __int_as_float(kTree ? (u.split < 0 ? u.bh : -1 - u.split)
+      *prec = make_float4(l, kRefRest ? lr : m_ref, __int_as_float(cur.r0), __int_as_float(kTree ? (u.split < 0 ? u.bh : -1 - u.split)
                                                                                     : cur.bh + p.BH * u.split));
       pend = true;
     }

@@ -131,6 +131,7 @@ struct ModParams {
   const int2* rows;     // [B][T_pad] visible key interval [lo, hi) of each query row, or null
   const int4* units;    // [B][n_t] (query tile, first K tile, past the last, keys in use)
   const float* slopes;  // [H] distance-bias slopes (BIAS)
+  __nv_bfloat16* rest;  // [BH][T][D] what o's rounding leaves out, or null (not TREE)
   int T_pad;            // ceil(T/128) · 128
   int H;                // query heads
   FastDiv div_h;        // bh / H = batch

@@ -65,6 +65,7 @@ struct BwdLaunch {
   BwdParams p;
   const __nv_bfloat16* o;
   const __nv_bfloat16* dout;
+  const __nv_bfloat16* rest;  // modified scores: what o's rounding left out, or null
   const float* lse;
   float* lse2;
   float* dvec;

@@ -36,6 +36,7 @@ constexpr int kModOn = 1;    // modified scores with row intervals
 constexpr int kModCap = 2;   // tanh cap
 constexpr int kModBias = 4;  // distance bias
 constexpr int kModRef = 16;  // with a cap alone, small enough: the softmax's reference is 0 (below)
+constexpr int kModRest = 32; // kModRef with the output's rest: weights that sum to 1 as rounded
 constexpr int kModTree = 8;  // new tokens against a cache (fa_tree_walk.cuh)
 
 // The cap. With u = z / cap = in · s (s the raw score), the capped score in base 2 is
@@ -52,9 +53,13 @@ constexpr int kModTree = 8;  // new tokens against a cache (fa_tree_walk.cuh)
 // Capped scores are bounded, so a cap of up to 60 needs no running maximum (kModRef): 2^x for
 // |x| ≤ kCapRef is at most 2⁸⁸ and at least 2⁻⁸⁸, and neither sums of 2²⁰ such terms times bf16
 // values of ordinary size nor their inverses leave fp32's range; bf16 has the same exponents, so P
-// keeps its precision. The softmax is then taken against 0: no maximum, no rescaling, and no
+// keeps its relative precision. The softmax is then taken against 0: no maximum, no rescaling, and no
 // dependency between the capping of a step's last score and the exponential of its first, so
 // that FMA and MUFU work overlap (B1 H12 T16384 d64 causal: SIDE_C -> SIDE_D µs).
+// One thing is lost: against a row's maximum the weight of a key that outweighs the others is 1,
+// unrounded; against 0 it is rounded like any other. Where the output's rest is asked for
+// (kModRest), O is therefore divided by the sum of the rounded weights, not of the exact ones that
+// the LSE takes: then an outweighing key's share is 1 again.
 constexpr float kCapRef = 88.0f;
 constexpr float kCapBend = 0.8f;
 constexpr double kCapPoly[5] = {0.9999989943572278, -0.3332537198003981, 0.1323056561802812,

@@ -326,14 +326,14 @@ int fa_visible(const int* doc_ids, const int* prefix_len, int prefix_per_token, 
   return e == cudaSuccess ? FA_OK : FA_ERR_LAUNCH;
 }
 
-int fa_fwd_mod(const void* q, const void* k, const void* v, void* o, float* lse, const void* visible,
-               int causal, float softcap, const float* slopes, int B, int H, int Hkv, int T, int d,
+int fa_fwd_mod(const void* q, const void* k, const void* v, void* o, float* lse, void* rest,
+               const void* visible, int causal, float softcap, const float* slopes, int B, int H, int Hkv, int T, int d,
                float scale, int* status, unsigned long long timeout_ns, void* stream) {
   if (!q || !k || !v || !o || !lse) return FA_ERR_INVALID_ARG;
   fa::CapFactors cap;
   if (!mod_sizes(B, H, Hkv, T, d) || !scale_ok(scale) || !cap_factors(scale, softcap, &cap))
     return FA_ERR_INVALID_ARG;
-  if (any_misaligned({q, k, v, o, lse}) || (reinterpret_cast<uintptr_t>(visible) & 255u) ||
+  if (any_misaligned({q, k, v, o, lse, rest}) || (reinterpret_cast<uintptr_t>(visible) & 255u) ||
       (reinterpret_cast<uintptr_t>(slopes) & 3u))
     return FA_ERR_MISALIGNED;
   const int BH = B * H;
@@ -342,9 +342,11 @@ int fa_fwd_mod(const void* q, const void* k, const void* v, void* o, float* lse,
   const void* ins[5] = {q, k, v, visible, slopes};
   const size_t in_bytes[5] = {qb, kb, kb, fa_visible_size(B, T), static_cast<size_t>(H) * 4};
   for (int i = 0; i < 5; ++i)
-    if (ins[i] && (overlaps(o, qb, ins[i], in_bytes[i]) || overlaps(lse, lb, ins[i], in_bytes[i])))
+    if (ins[i] && (overlaps(o, qb, ins[i], in_bytes[i]) || overlaps(lse, lb, ins[i], in_bytes[i]) ||
+                   (rest && overlaps(rest, qb, ins[i], in_bytes[i]))))
       return FA_ERR_INVALID_ARG;
-  if (overlaps(o, qb, lse, lb)) return FA_ERR_INVALID_ARG;
+  if (overlaps(o, qb, lse, lb) || (rest && (overlaps(rest, qb, o, qb) || overlaps(rest, qb, lse, lb))))
+    return FA_ERR_INVALID_ARG;
   int dev = -1, sms = 0;
   const int st = check_device(&dev, &sms);
   if (st != FA_OK) return st;
@@ -367,7 +369,7 @@ int fa_fwd_mod(const void* q, const void* k, const void* v, void* o, float* lse,
   a.p.tiles_per_cta = 1;
   a.p.div_bh = fa::FastDiv::make(static_cast<uint32_t>(BH));
   a.p.div_splits = fa::FastDiv::make(1u);
-  const int mod = fwd_mod_bits(softcap, slopes);
+  const int mod = fwd_mod_bits(softcap, slopes, rest);
   // Unmodified scores take their maximum before the factor, as the dense kernels; others the
   // plain factor.
   a.p.scale_log2 = mod == fa::kModOn ? exponent_factor(static_cast<double>(scale) * kLog2e, &a.p.s_negate)
@@ -385,6 +387,7 @@ int fa_fwd_mod(const void* q, const void* k, const void* v, void* o, float* lse,
     a.p.mod.units = reinterpret_cast<const int4*>(base + l.fwd);
   }
   a.p.mod.slopes = slopes;
+  a.p.mod.rest = static_cast<__nv_bfloat16*>(rest);
   a.p.mod.T_pad = n_t * 128;
   a.p.mod.H = H;
   a.p.mod.div_h = fa::FastDiv::make(static_cast<uint32_t>(H));
@@ -406,8 +409,8 @@ size_t fa_bwd_mod_workspace_size(int B, int H, int Hkv, int T, int d) {
 }
 
 int fa_bwd_mod(const void* q, const void* k, const void* v, const void* o, const void* dout,
-               const float* lse, void* dq, void* dk, void* dv, void* workspace, size_t workspace_bytes,
-               const void* visible, int causal, float softcap, const float* slopes, int B, int H,
+               const float* lse, const void* rest, void* dq, void* dk, void* dv, void* workspace,
+               size_t workspace_bytes, const void* visible, int causal, float softcap, const float* slopes, int B, int H,
                int Hkv, int T, int d, float scale, int* status, unsigned long long timeout_ns,
                void* stream) {
   if (!q || !k || !v || !o || !dout || !lse || !dq || !dk || !dv || !workspace)
@@ -417,18 +420,18 @@ int fa_bwd_mod(const void* q, const void* k, const void* v, const void* o, const
     return FA_ERR_INVALID_ARG;
   const size_t need = fa_bwd_mod_workspace_size(B, H, Hkv, T, d);
   if (need == 0 || workspace_bytes < need) return FA_ERR_INVALID_ARG;
-  if (any_misaligned({q, k, v, o, dout, lse, dq, dk, dv}) || (reinterpret_cast<uintptr_t>(workspace) & 255u) ||
+  if (any_misaligned({q, k, v, o, dout, lse, rest, dq, dk, dv}) || (reinterpret_cast<uintptr_t>(workspace) & 255u) ||
       (reinterpret_cast<uintptr_t>(visible) & 255u) || (reinterpret_cast<uintptr_t>(slopes) & 3u))
     return FA_ERR_MISALIGNED;
   const int BH = B * H, BHkv = B * Hkv;
   const size_t qb = static_cast<size_t>(BH) * T * d * 2, kb = static_cast<size_t>(BHkv) * T * d * 2;
-  const void* ins[8] = {q, k, v, o, dout, lse, visible, slopes};
-  const size_t in_bytes[8] = {qb, kb, kb, qb, qb, static_cast<size_t>(BH) * T * 4, fa_visible_size(B, T),
-                              static_cast<size_t>(H) * 4};
+  const void* ins[9] = {q, k, v, o, dout, lse, visible, slopes, rest};
+  const size_t in_bytes[9] = {qb, kb, kb, qb, qb, static_cast<size_t>(BH) * T * 4, fa_visible_size(B, T),
+                              static_cast<size_t>(H) * 4, qb};
   const void* outs[4] = {dq, dk, dv, workspace};
   const size_t out_bytes[4] = {qb, kb, kb, need};
   for (int x = 0; x < 4; ++x) {
-    for (int y = 0; y < 8; ++y)
+    for (int y = 0; y < 9; ++y)
       if (ins[y] && overlaps(outs[x], out_bytes[x], ins[y], in_bytes[y])) return FA_ERR_INVALID_ARG;
     for (int y = x + 1; y < 4; ++y)
       if (overlaps(outs[x], out_bytes[x], outs[y], out_bytes[y])) return FA_ERR_INVALID_ARG;
@@ -489,6 +492,7 @@ int fa_bwd_mod(const void* q, const void* k, const void* v, const void* o, const
   a.p.mod.causal = causal != 0;
   a.o = static_cast<const __nv_bfloat16*>(o);
   a.dout = static_cast<const __nv_bfloat16*>(dout);
+  a.rest = static_cast<const __nv_bfloat16*>(rest);
   a.lse = lse;
   a.dq = static_cast<__nv_bfloat16*>(dq);
   a.grid_main = static_cast<unsigned>(static_cast<long long>(n_t) * a.p.BH);

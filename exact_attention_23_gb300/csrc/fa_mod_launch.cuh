@@ -28,7 +28,7 @@ cudaError_t launch_bwd_mod(const BwdLaunch& a, int q_heads) {
   cudaError_t e = smem_opt_in(fn, C::kSmemBytes, done);
   if (e != cudaSuccess) return e;
   e = launch_pdl(fa_bwd_prep_kernel<D, true>, a.grid_prep, 256, 0, a.stream, a.o, a.dout, a.lse, a.lse2,
-                 a.dvec, a.p.dq_acc, a.p.T, a.p.T_pad, q_heads);
+                 a.dvec, a.p.dq_acc, a.p.T, a.p.T_pad, q_heads, a.rest);
   if (e != cudaSuccess) return e;
   e = launch_pdl(fn, a.grid_main, C::kThreads, C::kSmemBytes, a.stream, a.tm_q, a.tm_k, a.tm_v, a.tm_do,
                  a.p);

@@ -175,14 +175,16 @@ def _check_mod(q, k, v, seen, causal, slopes):
 
 
 def fwd_mod(q, k, v, visible=None, causal: bool | None = None, softcap: float = 0.0, slopes=None,
-            scale: float | None = None, out=None, lse=None, status=None, timeout_ns: int = 0):
+            scale: float | None = None, out=None, lse=None, rest=None, status=None,
+            timeout_ns: int = 0):
     """Attention with modified scores through fa_fwd_mod: z = scale·q·k, capped to
     softcap·tanh(z / softcap) when ``softcap`` > 0, lowered by slopes[h]·|i − j| when ``slopes``
     (float32 [H]) is given; softmax over the visible keys.
 
     q is [B, H, T, d], k and v [B, Hkv, T, d] with Hkv a divisor of H. ``visible`` (from
     ``visible()``) says who sees whom; without it ``causal`` does (None: causal). Returns
-    (o, lse); a row that sees no key has o = 0 and lse = −inf.
+    (o, lse); a row that sees no key has o = 0 and lse = −inf. ``rest``, a tensor like q, is
+    written with what o's rounding to bf16 leaves out, for ``bwd_mod``.
     """
     B, H, T, d, Hkv, causal = _check_mod(q, k, v, visible, causal, slopes)
     device = q.device
@@ -196,9 +198,11 @@ def fwd_mod(q, k, v, visible=None, causal: bool | None = None, softcap: float = 
         lse = torch.empty((B, H, T), dtype=_FP32, device=device)
     else:
         _check_fp32(lse, (B, H, T), device, "lse")
+    if rest is not None:
+        _check_like(rest, q, "rest")
     _check_status(status, device)
     _call(device, "fa_fwd_mod", fa_fwd_mod, q.data_ptr(), k.data_ptr(), v.data_ptr(),
-          out.data_ptr(), lse.data_ptr(), None if visible is None else visible.buffer.data_ptr(),
+          out.data_ptr(), lse.data_ptr(), _ptr(rest), None if visible is None else visible.buffer.data_ptr(),
           causal, softcap, _ptr(slopes), B, H, Hkv, T, d, scale, _ptr(status), timeout_ns)
     return out, lse
 
@@ -212,10 +216,12 @@ def bwd_mod_workspace(B: int, H: int, Hkv: int, T: int, d: int, device=None):
 
 
 def bwd_mod(q, k, v, o, lse, do, visible=None, causal: bool | None = None, softcap: float = 0.0,
-            slopes=None, scale: float | None = None, dq=None, dk=None, dv=None, workspace=None,
-            status=None, timeout_ns: int = 0):
+            slopes=None, scale: float | None = None, rest=None, dq=None, dk=None, dv=None,
+            workspace=None, status=None, timeout_ns: int = 0):
     """Gradients of ``fwd_mod`` through fa_bwd_mod: (dq [B, H, T, d], dk, dv [B, Hkv, T, d]), from
-    its outputs ``o`` and ``lse`` and the gradient ``do`` of o; the other arguments as there.
+    its outputs ``o`` and ``lse`` and the gradient ``do`` of o; the other arguments as there. With
+    the ``rest`` that the forward wrote, dq and dk do not suffer from o's rounding (it shows where
+    one key takes most of a row's weight).
     ``workspace`` (see ``bwd_mod_workspace``) may be passed to reuse it."""
     B, H, T, d, Hkv, causal = _check_mod(q, k, v, visible, causal, slopes)
     device = q.device
@@ -240,9 +246,11 @@ def bwd_mod(q, k, v, o, lse, do, visible=None, causal: bool | None = None, softc
         workspace = bwd_mod_workspace(B, H, Hkv, T, d, device=device)
     else:
         _check_workspace(workspace, device)
+    if rest is not None:
+        _check_like(rest, q, "rest")
     _check_status(status, device)
     _call(device, "fa_bwd_mod", fa_bwd_mod, q.data_ptr(), k.data_ptr(), v.data_ptr(),
-          o.data_ptr(), do.data_ptr(), lse.data_ptr(), dq.data_ptr(), dk.data_ptr(),
+          o.data_ptr(), do.data_ptr(), lse.data_ptr(), _ptr(rest), dq.data_ptr(), dk.data_ptr(),
           dv.data_ptr(), workspace.data_ptr(), workspace.numel() * workspace.element_size(),
           None if visible is None else visible.buffer.data_ptr(), causal, softcap, _ptr(slopes),
           B, H, Hkv, T, d, scale, _ptr(status), timeout_ns)

@@ -16,18 +16,18 @@ BAD, MIS = fa.FA_ERR_INVALID_ARG, fa.FA_ERR_MISALIGNED
 
 # ------------------------------------------------------------------------- refusals (CPU)
 
-def _fwd(q=A, k=A + SZ, v=A + 2 * SZ, o=A + 3 * SZ, lse=A + 4 * SZ, vis=None, causal=1, cap=0.0,
+def _fwd(q=A, k=A + SZ, v=A + 2 * SZ, o=A + 3 * SZ, lse=A + 4 * SZ, rest=None, vis=None, causal=1, cap=0.0,
          slopes=None, B=2, H=4, Hkv=2, T=200, d=64, scale=0.125):
-    return fa.fa_fwd_mod(q, k, v, o, lse, vis, causal, cap, slopes, B, H, Hkv, T, d, scale, None, 0,
+    return fa.fa_fwd_mod(q, k, v, o, lse, rest, vis, causal, cap, slopes, B, H, Hkv, T, d, scale, None, 0,
                          None)
 
 
-def _bwd(q=A, k=A + SZ, v=A + 2 * SZ, o=A + 3 * SZ, do=A + 4 * SZ, lse=A + 5 * SZ, dq=A + 6 * SZ,
+def _bwd(q=A, k=A + SZ, v=A + 2 * SZ, o=A + 3 * SZ, do=A + 4 * SZ, lse=A + 5 * SZ, rest=None, dq=A + 6 * SZ,
          dk=A + 7 * SZ, dv=A + 8 * SZ, ws=A + 9 * SZ, ws_bytes=None, vis=None, causal=1, cap=0.0,
          slopes=None, B=2, H=4, Hkv=2, T=200, d=64, scale=0.125):
     if ws_bytes is None:
         ws_bytes = fa.fa_bwd_mod_workspace_size(B, H, Hkv, T, d) or 1 << 20
-    return fa.fa_bwd_mod(q, k, v, o, do, lse, dq, dk, dv, ws, ws_bytes, vis, causal, cap, slopes, B,
+    return fa.fa_bwd_mod(q, k, v, o, do, lse, rest, dq, dk, dv, ws, ws_bytes, vis, causal, cap, slopes, B,
                          H, Hkv, T, d, scale, None, 0, None)
 
 
@@ -45,6 +45,7 @@ COMMON = [
     (dict(o=0), BAD), (dict(o=A), BAD), (dict(o=A + SZ), BAD), (dict(lse=A + 3 * SZ), BAD),
     (dict(vis=A + 3 * SZ), BAD),       # o would overwrite the visibility
     (dict(slopes=A + 4 * SZ), BAD),    # lse would overwrite the slopes
+    (dict(rest=A + 3 * SZ), BAD), (dict(rest=A), BAD), (dict(rest=A + 20 * SZ + 8), MIS),
 ])
 def test_fwd_mod_refusals(kw, want):
     assert _fwd(**kw) == want
@@ -54,6 +55,7 @@ def test_fwd_mod_refusals(kw, want):
     (dict(do=0), BAD), (dict(dk=0), BAD), (dict(ws=0), BAD), (dict(ws_bytes=4096), BAD),
     (dict(dq=A), BAD), (dict(dk=A + 8 * SZ), BAD), (dict(ws=A + 5 * SZ), BAD),
     (dict(ws=A + 9 * SZ + 16), MIS), (dict(dv=A + 8 * SZ + 8), MIS), (dict(vis=A + 7 * SZ), BAD),
+    (dict(rest=A + 6 * SZ), BAD), (dict(rest=A + 20 * SZ + 4), MIS),
 ])
 def test_bwd_mod_refusals(kw, want):
     assert _bwd(**kw) == want
@@ -137,8 +139,9 @@ def _run(q, k, v, do, seen=None, **kw):
     t = [x.cuda() for x in (q, k, v, do)]
     sl = kw.pop("slopes", None)
     sl = None if sl is None else sl.cuda()
-    o, lse = fa.fwd_mod(*t[:3], visible=seen, slopes=sl, **kw)
-    dq, dk, dv = fa.bwd_mod(*t[:3], o, lse, t[3], visible=seen, slopes=sl, **kw)
+    rest = torch.full_like(t[0], math.nan) if kw.pop("with_rest", True) else None
+    o, lse = fa.fwd_mod(*t[:3], visible=seen, slopes=sl, rest=rest, **kw)
+    dq, dk, dv = fa.bwd_mod(*t[:3], o, lse, t[3], visible=seen, slopes=sl, rest=rest, **kw)
     torch.cuda.synchronize()
     return {"o": o, "lse": lse, "dq": dq, "dk": dk, "dv": dv}
 
@@ -271,6 +274,30 @@ def test_padding_may_hold_anything(d, cap):
     for n in ("o", "dq", "dk", "dv"):
         assert not dirty[n][:, :, T - pad:].any(), n
     assert torch.isneginf(dirty["lse"][:, :, T - pad:]).all()
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("d,cap", [(64, 0.0), (64, 30.0), (128, 0.0), (128, 30.0), (128, 80.0)])
+def test_rest_of_the_output(d, cap):
+    """o + rest is the output to the precision of its products (P in bf16), not of its own rounding,
+    and the gradients of peaked rows gain by it. In the norm, a rounding to bf16 is off by 2⁻⁸/√3 of
+    what it rounds at most: dQ is rounded twice (dS and itself), so within √2·2⁻⁸/√3 = 3.2e-3, and
+    the rounded P's share of D may add a quarter."""
+    B, H, Hkv, T = 2, 4, 2, 300
+    q, k, v, do = _tensors(B, H, Hkv, T, d, 31, 4.0)
+    ids = _ids(B, T, (100, 31), 20)
+    seen = fa.visible(B, T, doc_ids=ids.cuda())
+    r = ref.attention(q, k, v, ref.visible_mask(B, T, True, ids), d ** -0.5, cap, None, do)
+    rest = torch.full_like(q, math.nan).cuda()
+    o, lse = fa.fwd_mod(q.cuda(), k.cuda(), v.cuda(), visible=seen, softcap=cap, rest=rest)
+    assert torch.isfinite(rest).all() and not rest[:, :, T - 20:].any()
+    off = lambda x, y: float((x.double().cpu() - y).norm() / y.norm())
+    both = o.double() + rest.double()
+    assert off(both, r["o"]) <= 2.0 ** -8 / 3 ** 0.5 and off(both, r["o"]) < 0.7 * off(o, r["o"])
+    with_it, without = (_run(q, k, v, do, seen, softcap=cap, with_rest=x) for x in (True, False))
+    for n in ("dq", "dk"):
+        assert off(with_it[n], r[n]) <= 4e-3 and off(with_it[n], r[n]) < off(without[n], r[n]), n
+    ref.check(without, r, ALL)
 
 
 @pytest.mark.gpu
