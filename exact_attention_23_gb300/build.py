@@ -24,7 +24,8 @@ SOURCES = ["fa_api.cu", "fa_fwd1.cu", "fa_fwd1_gen.cu", "fa_fwd_pair.cu", "fa_fw
            "fa_fwd_gen_d128.cu", "fa_fwd_ext_api.cu", "fa_decode.cu", "fa_bwd_d64.cu", "fa_bwd_d128.cu",
            "fa_bwd_api.cu",
            "fa_noalloc.cu", "fa_hostio.cu", "fa_mod_fwd_d64.cu", "fa_mod_fwd_d128.cu",
-           "fa_mod_bwd_d64.cu", "fa_mod_bwd_d128.cu", "fa_mod_api.cu", "fa_rope.cu", "fa_tree.cu",
+           "fa_mod_bwd_d64.cu", "fa_mod_bwd_d128.cu", "fa_mod_pairs_d64.cu", "fa_mod_pairs_d128.cu",
+           "fa_mod_api.cu", "fa_rope.cu", "fa_tree.cu",
            "fa_tree_wide_d64.cu", "fa_tree_wide_d128.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ["-O3", "-lineinfo", "-std=c++20", "-Xcompiler", "-fPIC", "-Xptxas", "-v",

@@ -130,6 +130,8 @@ static_assert(sizeof(Bars) <= 512, "barrier block");
 struct ModParams {
   const int2* rows;     // [B][T_pad] visible key interval [lo, hi) of each query row, or null
   const int4* units;    // [B][n_t] (query tile, first K tile, past the last, keys in use)
+  const int4* pairs;    // [B][ceil(n_t/2)][2] (first query tile, keys in use, its first K tile, past
+                        //   its last), (the second tile's first and past its last, 0, 0)
   const float* slopes;  // [H] distance-bias slopes (BIAS)
   __nv_bfloat16* rest;  // [BH][T][D] what o's rounding leaves out, or null (not TREE)
   int T_pad;            // ceil(T/128) · 128
@@ -187,6 +189,7 @@ __device__ __forceinline__ float u2f(uint32_t u) { return __uint_as_float(u); }
 struct Unit {
   int bh, qt0, nkv[2], n_steps;
   int kb, ke;     // K-tile range [kb, ke) (dense: [0, n_steps))
+  int lo[2];      // MOD: tile i's K tiles are [lo[i], last[i])
   int last[2];    // last K tile visible to tile i (GEN, causal)
   int split, mh;  // key-range index; block-mask head
 };
@@ -224,8 +227,43 @@ __device__ __forceinline__ int walk_next(const Walk& w, int kt) {
   return kNoTile;
 }
 
-template <bool CAUSAL, bool GEN>
+// MOD (modified scores): both tiles' K tiles are contiguous ranges, from the visibility's records
+// (pairs with the longest walks first) or the causal or full ranges (the last pair first); the
+// unit walks their union.
+__device__ __forceinline__ Unit pair_unit_of(const FwdParams& p, int L) {
+  Unit u;
+  const int pos = static_cast<int>(p.div_bh.div(static_cast<uint32_t>(L)));
+  u.bh = L - pos * p.BH;
+  u.split = 0;
+  if (p.mod.pairs) {
+    const int b = static_cast<int>(p.mod.div_h.div(static_cast<uint32_t>(u.bh)));
+    const int4* r = p.mod.pairs + (static_cast<size_t>(b) * p.n_units + pos) * 2;
+    const int4 r0 = __ldg(r), r1 = __ldg(r + 1);
+    u.qt0 = r0.x;
+    u.mh = r0.y;
+    u.lo[0] = r0.z;
+    u.last[0] = r0.w;
+    u.lo[1] = r1.x;
+    u.last[1] = r1.y;
+  } else {
+    u.qt0 = (p.n_units - 1 - pos) * 2;
+    u.mh = p.n_kv * kBlockN;  // (rows past Tk are loaded as zeros)
+    u.lo[0] = u.lo[1] = 0;
+    u.last[0] = p.mod.causal ? u.qt0 + 1 : p.n_kv;
+    u.last[1] = u.qt0 + 1 >= p.n_qt ? 0 : (p.mod.causal ? u.qt0 + 2 : p.n_kv);
+  }
+  u.nkv[0] = max(0, u.last[0] - u.lo[0]);
+  u.nkv[1] = max(0, u.last[1] - u.lo[1]);
+  u.kb = min(u.nkv[0] > 0 ? u.lo[0] : 0x7fffffff, u.nkv[1] > 0 ? u.lo[1] : 0x7fffffff);
+  u.ke = max(u.nkv[0] > 0 ? u.last[0] : 0, u.nkv[1] > 0 ? u.last[1] : 0);
+  u.n_steps = max(0, u.ke - u.kb);
+  if (u.n_steps == 0) u.kb = 0;
+  return u;
+}
+
+template <bool CAUSAL, bool GEN, int MOD = 0>
 __device__ __forceinline__ Unit unit_of(const FwdParams& p, int L) {
+  if constexpr (MOD != 0) return pair_unit_of(p, L);
   Unit u;
   if constexpr (GEN) {
     // bh fastest, then key range, then query unit, the last query unit first (under the
@@ -283,7 +321,7 @@ __device__ __forceinline__ Unit unit_of(const FwdParams& p, int L) {
 // issuers). Step j is K tile kt, the smaller of the two tiles' next K tiles, and tile i takes
 // part when act[i]. (Dense units need none of this: step j is K tile j, and tile i is active
 // while j < nkv[i].)
-template <bool CAUSAL, bool GEN>
+template <bool CAUSAL, bool GEN, int MOD = 0>
 struct UnitSteps {
   Walk w[2];
   int nx[2];
@@ -291,7 +329,7 @@ struct UnitSteps {
   bool act[2];
   __device__ __forceinline__ void begin(const FwdParams& p, const Unit& u) {
     kt = -1;
-    if constexpr (GEN) {
+    if constexpr (GEN && MOD == 0) {
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
         w[i] = walk_of<CAUSAL>(p, u, i);
@@ -300,7 +338,11 @@ struct UnitSteps {
     }
   }
   __device__ __forceinline__ void next(const Unit& u, int j) {
-    if constexpr (GEN) {
+    if constexpr (MOD != 0) {
+      kt = u.kb + j;
+      act[0] = kt >= u.lo[0] && kt < u.last[0];
+      act[1] = kt >= u.lo[1] && kt < u.last[1];
+    } else if constexpr (GEN) {
       kt = min(nx[0], nx[1]);
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
@@ -317,12 +359,17 @@ struct UnitSteps {
 
 // QK8: Q and K arrive as e4m3 codes (their per-tensor scales folded into scale_log2) and
 // S = Q·Kᵀ runs as a kind::f8f6f4 product; V, P and O are as in the bf16 path.
-template <int D, bool CAUSAL, bool GEN = false, bool QK8 = false>
+// MOD (with GEN, CAUSAL false): documents and prefixes as row intervals (kModOn), or with a cap
+// against the fixed reference (kModRef, and kModRest).
+template <int D, bool CAUSAL, bool GEN = false, bool QK8 = false, int MOD = 0>
 __global__ void __launch_bounds__(kThreads, 1)
     fa_fwd_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
                   const __grid_constant__ CUtensorMap tm_v, const __grid_constant__ CUtensorMap tm_o,
                   const FwdParams p) {
   using C = Cfg<D, QK8>;
+  constexpr bool kRef = (MOD & kModRef) != 0;             // the softmax is taken against 0
+  constexpr bool kRefRest = (MOD & kModRest) != 0;        // … with o's rest
+  constexpr bool kRest = MOD != 0 && (!kRef || kRefRest);  // o's rest may be asked for
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
   Bars* bars = reinterpret_cast<Bars*>(smem + C::kBarOff);
@@ -401,7 +448,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     for (int r = 0; ok && r * grid < p.total_units; ++r) {
       const int L = unit_index(r, cta, grid);
       if (L >= p.total_units) continue;
-      const Unit u = unit_of<CAUSAL, GEN>(p, L);
+      const Unit u = unit_of<CAUSAL, GEN, MOD>(p, L);
       const int qb = qn % C::kQBufs;
       if (qn >= C::kQBufs &&
           !wait_w(&bars->q_empty[qb], ((qn / C::kQBufs) - 1) & 1, wc)) { ok = false; break; }
@@ -417,8 +464,10 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       __syncwarp();
       ++qn;
-      UnitSteps<CAUSAL, GEN> us;
+      UnitSteps<CAUSAL, GEN, MOD> us;
       if constexpr (GEN) us.begin(p, u);
+      int kvh = u.bh;  // the key head this query head reads
+      if constexpr (MOD != 0) kvh = static_cast<int>(p.mod.div_g.div(static_cast<uint32_t>(u.bh)));
       int kt = u.kb - 1;
       for (int j = 0; j < u.n_steps; ++j, ++g) {
         if constexpr (GEN) {
@@ -436,12 +485,12 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
           for (int s = 0; s < C::kQKSub; ++s)
             tma_load_3d_hint(smem + C::kKOff + st * C::kQKTileBytes + s * C::kQKSubBytes, &tm_k,
-                             &bars->k_full[st], s * 64, kt * kBlockN, u.bh, keep);
+                             &bars->k_full[st], s * 64, kt * kBlockN, kvh, keep);
           mbar_arrive_expect_tx(&bars->v_full[st], C::kTileBytes);
 #pragma unroll
           for (int s = 0; s < C::kSub; ++s)
             tma_load_3d_hint(smem + C::kVOff + st * C::kTileBytes + s * C::kSubBytes, &tm_v,
-                             &bars->v_full[st], s * 64, kt * kBlockN, u.bh, keep);
+                             &bars->v_full[st], s * 64, kt * kBlockN, kvh, keep);
         }
         __syncwarp();
       }
@@ -504,10 +553,10 @@ __global__ void __launch_bounds__(kThreads, 1)
       for (int r = 0; ok && r * grid < p.total_units; ++r) {
         const int L = unit_index(r, cta, grid);
         if (L >= p.total_units) continue;
-        const Unit u = unit_of<CAUSAL, GEN>(p, L);
+        const Unit u = unit_of<CAUSAL, GEN, MOD>(p, L);
         const int qb = qn % C::kQBufs;
         if (!wait_w(&bars->q_full[qb], (qn / C::kQBufs) & 1, wc)) { ok = false; break; }
-        UnitSteps<CAUSAL, GEN> us;
+        UnitSteps<CAUSAL, GEN, MOD> us;
         if constexpr (GEN) us.begin(p, u);
         for (int j = 0; j < u.n_steps; ++j, ++g) {
           if constexpr (GEN) us.next(u, j);
@@ -565,14 +614,27 @@ __global__ void __launch_bounds__(kThreads, 1)
       for (int r = 0; ok && r * grid < p.total_units; ++r) {
         const int L = unit_index(r, cta, grid);
         if (L >= p.total_units) continue;
-        const Unit u = unit_of<CAUSAL, GEN>(p, L);
-        UnitSteps<CAUSAL, GEN> us;
+        const Unit u = unit_of<CAUSAL, GEN, MOD>(p, L);
+        UnitSteps<CAUSAL, GEN, MOD> us;
         if constexpr (GEN) us.begin(p, u);
         int jt[2] = {0, 0};   // steps of this unit in which tile i was active
         for (int j = 0; j < u.n_steps; ++j, ++g) {
           if constexpr (GEN) us.next(u, j);
           const int st = g % C::kStages;
           if (!wait_w(&bars->v_full[st], (g / C::kStages) & 1, wc)) { ok = false; break; }
+          if constexpr (MOD != 0) {
+            // Keys behind the last one that some query of the sequence sees may hold anything
+            // (padding): their P is 0, and 0 · NaN must not reach O.
+            const int used = u.mh - us.kt * kBlockN;
+            if (used < kBlockN) {
+              for (int x = max(used, 0) * 8 + lane; x < kBlockN * 8; x += 32)
+#pragma unroll
+                for (int s = 0; s < C::kSub; ++s)
+                  st_shared_v4(v_base + st * C::kTileBytes + s * C::kSubBytes + x * 16, 0u, 0u, 0u, 0u);
+              fence_proxy_async_smem();
+              __syncwarp();
+            }
+          }
 #pragma unroll
           for (int i = 0; i < 2; ++i) {
             if (GEN ? !us.act[i] : j >= u.nkv[i]) continue;
@@ -662,7 +724,42 @@ __global__ void __launch_bounds__(kThreads, 1)
         const uint32_t b2 = pack_bf16x2(u2f(bits), u2f(bits));
 #pragma unroll
         for (int t = 0; t < D / 8; ++t) orow[t] = make_uint4(b2, b2, b2, b2);
+        if constexpr (kRest) {
+          if (p.mod.rest) {
+            uint4* rrow = reinterpret_cast<uint4*>(p.mod.rest + w.row_idx * D);
+#pragma unroll
+            for (int t = 0; t < D / 8; ++t) rrow[t] = make_uint4(b2, b2, b2, b2);
+          }
+        }
       }
+    };
+    // What the rounding to bf16 leaves out of n / 8 chunks of 8 values of this thread's row, x times
+    // mul, into the warp's staging slice at chunk ch0 on; flush_rest then writes the slice's rows, 64
+    // columns from c0, whole rows at a time (the slice's next use may follow at once).
+    auto stage_rest = [&](uint32_t ob, int ch0, const uint32_t* x, int n, float mul) {
+#pragma unroll
+      for (int t = 0; t < n / 8; ++t) {
+        uint32_t lo[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const float a = u2f(x[8 * t + 2 * e]) * mul, b = u2f(x[8 * t + 2 * e + 1]) * mul;
+          const uint32_t hi = pack_bf16x2(a, b);
+          lo[e] = pack_bf16x2(a - __uint_as_float(hi << 16), b - __uint_as_float(hi & 0xFFFF0000u));
+        }
+        st_shared_v4(ob + (((ch0 + t) ^ (lane & 7)) << 4), lo[0], lo[1], lo[2], lo[3]);
+      }
+    };
+    auto flush_rest = [&](const RowOut& w, const uint8_t* slice, int c0) {
+      __syncwarp();
+      __nv_bfloat16* dst = p.mod.rest + (static_cast<size_t>(w.bh) * p.T + w.r0) * D + c0;
+#pragma unroll
+      for (int it = 0; it < 8; ++it) {
+        const int r = it * 4 + (lane >> 3), ch = lane & 7;
+        if (w.r0 + r < p.T)
+          *reinterpret_cast<uint4*>(dst + static_cast<size_t>(r) * D + ch * 8) =
+              *reinterpret_cast<const uint4*>(slice + r * 128 + ((ch ^ (r & 7)) << 4));
+      }
+      __syncwarp();
     };
     auto fail_rows = [&](const RowOut& w) {
       write_const_row(w, 0x7FC00000u);
@@ -677,13 +774,20 @@ __global__ void __launch_bounds__(kThreads, 1)
     // map's 128-byte swizzle; conflict-free), and its lane 0 stores them as one 64 × 32
     // box; rows past the sequence are not written. The warp's previous store from the
     // slice (one unit back) must have read it out first.
+    // (kRef: the reference is 0, and m carries the sum of the rounded weights)
     auto store_o = [&](const RowOut& w, const uint32_t* o, float l, float m) {
-      const float inv_l = inv_of(l);
+      const float inv_l = inv_of(kRefRest ? m : l);
       if (D == 64 && !w.partial) {
         uint8_t* slice = smem + C::kOOff + (wg * 4 + quad) * 4096;
         const uint32_t ob = smem_u32(slice) + lane * 128;
         if (lane == 0) bulk_wait_group_read0();
         __syncwarp();
+        if constexpr (kRest && D == 64) {
+          if (p.mod.rest) {
+            stage_rest(ob, 0, o, 64, inv_l);
+            flush_rest(w, slice, 0);
+          }
+        }
 #pragma unroll
         for (int ch = 0; ch < D / 8; ++ch)
           st_shared_v4(ob + ((ch ^ (lane & 7)) << 4),
@@ -701,7 +805,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
         for (int c0 = 0; c0 < D; c0 += 32) write_row(w, o + c0, c0, inv_l);
       }
-      write_lse(w, lse_of(l, m));
+      write_lse(w, lse_of(l, kRef ? 0.0f : m));
     };
     // Reads O_i (after its last P·V) into registers and releases it to the next unit's
     // first P·V.
@@ -766,7 +870,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     for (int r = 0; r * grid < p.total_units; ++r) {
       const int L = unit_index(r, cta, grid);
       if (L >= p.total_units) continue;
-      const Unit u = unit_of<CAUSAL, GEN>(p, L);
+      const Unit u = unit_of<CAUSAL, GEN, MOD>(p, L);
       // (ternaries, not u.nkv[wg]: a runtime index would move the unit to local memory)
       const int n = wg ? u.nkv[1] : u.nkv[0];
       const int qt = u.qt0 + wg;
@@ -791,18 +895,31 @@ __global__ void __launch_bounds__(kThreads, 1)
         continue;
       }
 
-      float m_ref = -INFINITY;  // reference max (base-2 scaled units) shared by O and l
-      float l = 0.0f;
+      // reference max (base-2 scaled units) shared by O and l
+      float m_ref = kRef ? 0.0f : -INFINITY;
+      float l = 0.0f, lr = 0.0f;  // lr (kRefRest): the sum of the rounded weights
+      int vlo = 0, vhi = 0;  // MOD: this row's visible keys [lo, hi)
+      if constexpr (MOD != 0) {
+        const int b = static_cast<int>(p.mod.div_h.div(static_cast<uint32_t>(u.bh)));
+        if (p.mod.rows) {
+          const int2 r = __ldg(p.mod.rows + static_cast<size_t>(b) * p.mod.T_pad + q_row);
+          vlo = r.x;
+          vhi = r.y;
+        } else {
+          vhi = p.mod.causal ? min(q_row + 1, p.Tk) : p.Tk;
+        }
+      }
       // this tile's K tiles (GEN: its walk, the next position fetched a step ahead)
       Walk w{nullptr, 0};
       int nx = 0;
-      if constexpr (GEN) {
+      if constexpr (GEN && MOD == 0) {
         w = walk_of<CAUSAL>(p, u, wg);
         nx = walk_next(w, u.kb - 1);
       }
       int kt = u.kb - 1;  // (dense: u.kb = 0, step j is K tile j)
+      if constexpr (MOD != 0) kt = (wg ? u.lo[1] : u.lo[0]) - 1;
       for (int j = 0; j < n; ++j, ++gs) {
-        if constexpr (GEN) {
+        if constexpr (GEN && MOD == 0) {
           kt = nx;
           nx = walk_next(w, kt);
         } else {
@@ -815,7 +932,11 @@ __global__ void __launch_bounds__(kThreads, 1)
         // Keys past the end of the sequence, and (causal) keys after this query.
         int lim;
         bool masked;
-        if constexpr (GEN) {
+        const int vl = vlo - k0;  // (MOD: keys before it are masked too)
+        if constexpr (MOD != 0) {
+          lim = vhi - k0;
+          masked = __any_sync(0xffffffffu, lim < kBlockN || vl > 0);
+        } else if constexpr (GEN) {
           lim = (CAUSAL ? min(q_row + 1 + p.kv_off, p.Tk) : p.Tk) - k0;
           masked = lim < kBlockN;
         } else {
@@ -823,6 +944,78 @@ __global__ void __launch_bounds__(kThreads, 1)
           masked = (CAUSAL && kt == qt) || (k0 + kBlockN > p.T);
         }
 
+        uint64_t acc0, acc1;  // the row sum's pairs
+        if constexpr (kRef) {
+          acc0 = acc1 = f2_pack(0.f, 0.f);
+          // Capped scores against the fixed reference: no maximum, so the step goes through 32
+          // columns at a time, the next columns loading while these are exponentiated.
+          uint64_t acc_r = acc0;
+          constexpr int kPk = kBlockN / 2 / C::kPParts;  // bf16 pairs per part
+          constexpr int kChunks = kPk / 16;              // of 32 columns per part
+          uint32_t s[2][32];
+          tmem_ld32(t_s, s[0]);
+#pragma unroll
+          for (int h = 0; h < C::kPParts; ++h) {
+            uint32_t pk[kPk];
+#pragma unroll
+            for (int cc = 0; cc < kChunks; ++cc) {
+              const int ch = h * kChunks + cc;
+              uint32_t* x = s[ch & 1];
+              tmem_ld_wait();
+              reg_fence32(x);
+              if (ch + 1 < kBlockN / 32) {
+                tmem_ld32(t_s + (ch + 1) * 32, s[(ch + 1) & 1]);
+              } else if constexpr (C::kSepP) {
+                // S_i is in registers: the tensor core may overwrite it with the next S_i.
+                tc_fence_before_sync();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&bars->s_free[wg]);
+              }
+              auto exponentials = [&]<bool FAR, bool MASK>() {
+#pragma unroll
+                for (int t = 0; t < 16; ++t) {
+                  float x0, x1;
+                  f2_unpack(cap2<FAR>(f2_pack(u2f(x[2 * t]), u2f(x[2 * t + 1])), p.mod.cap), x0, x1);
+                  float p0 = ex2_approx(x0), p1 = ex2_approx(x1);
+                  if constexpr (MASK) {
+                    const int t0 = ch * 32 + 2 * t;
+                    if (t0 >= lim || t0 < vl) p0 = 0.0f;
+                    if (t0 + 1 >= lim || t0 + 1 < vl) p1 = 0.0f;
+                  }
+                  if (t & 1) acc1 = f2_add(acc1, f2_pack(p0, p1));
+                  else acc0 = f2_add(acc0, f2_pack(p0, p1));
+                  const uint32_t pw = pack_bf16x2(p0, p1);
+                  pk[cc * 16 + t] = pw;
+                  if constexpr (kRefRest) acc_r = f2_add(acc_r, f2_pack(u2f(pw << 16), u2f(pw & 0xFFFF0000u)));
+                }
+              };
+              if (cap_far<32>(x, p.mod.cap.limit)) exponentials.template operator()<true, true>();
+              else if (masked) exponentials.template operator()<false, true>();
+              else exponentials.template operator()<false, false>();
+            }
+            if constexpr (C::kSepP) {
+              if (gs > 0) {
+                if (!wait_w(h == C::kPParts - 1 ? &bars->pv_done[wg] : &bars->pv_part[wg][h], (gs - 1) & 1, wc)) {
+                  ok = false;
+                  break;
+                }
+                tc_fence_after_sync();
+              }
+            }
+#pragma unroll
+            for (int c0 = 0; c0 < kPk; c0 += 32) tmem_st32(t_p + h * kPk + c0, pk + c0);
+            tmem_st_wait();
+            tc_fence_before_sync();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&bars->p_full[wg][h]);
+          }
+          if (!ok) break;
+          if constexpr (kRefRest) {
+            float a0, a1;
+            f2_unpack(acc_r, a0, a1);
+            lr += a0 + a1;
+          }
+        } else {
         // S into registers. D = 64: all four 32-column loads in flight before one wait (one
         // TMEM round trip). D = 128: in two halves, the second loading while the first is
         // masked and maxed (measured faster there).
@@ -848,7 +1041,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (masked) {
 #pragma unroll
             for (int t = 0; t < kBlockN; ++t)
-              if (t >= lim) s[t] = __float_as_uint(-INFINITY);
+              if (t >= lim || (MOD != 0 && t < vl)) s[t] = __float_as_uint(-INFINITY);
           }
 #pragma unroll
           for (int a = 0; a < 8; ++a) mx[a] = fmaxf(u2f(s[2 * a]), u2f(s[2 * a + 1]));
@@ -867,7 +1060,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (masked) {
 #pragma unroll
             for (int t = 0; t < 64; ++t)
-              if (t >= lim) s[t] = __float_as_uint(-INFINITY);
+              if (t >= lim || (MOD != 0 && t < vl)) s[t] = __float_as_uint(-INFINITY);
           }
 #pragma unroll
           for (int a = 0; a < 8; ++a) mx[a] = fmaxf(u2f(s[2 * a]), u2f(s[2 * a + 1]));
@@ -882,7 +1075,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (masked) {
 #pragma unroll
             for (int t = 64; t < kBlockN; ++t)
-              if (t >= lim) s[t] = __float_as_uint(-INFINITY);
+              if (t >= lim || (MOD != 0 && t < vl)) s[t] = __float_as_uint(-INFINITY);
           }
 #pragma unroll
           for (int t = 64; t < kBlockN; t += 16)
@@ -913,7 +1106,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         // (general form: a row with no visible key so far keeps m_ref = −∞; its p are 0)
         const float m_use = (GEN && m_ref == -INFINITY) ? 0.0f : m_ref;
         const uint64_t nm2 = f2_pack(-m_use, -m_use);
-        uint64_t acc0 = f2_pack(0.f, 0.f), acc1 = acc0;
+        acc0 = f2_pack(0.f, 0.f);
+        acc1 = acc0;
         constexpr int kPk = kBlockN / 2 / C::kPParts;  // bf16 pairs per part
 #pragma unroll
         for (int h = 0; h < C::kPParts; ++h) {
@@ -972,6 +1166,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (lane == 0) mbar_arrive(&bars->p_full[wg][h]);
         }
         if (!ok) break;
+        }
         {
           float a0, a1, b0, b1;
           f2_unpack(acc0, a0, a1);
@@ -989,7 +1184,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         continue;
       }
       if (defer) {
-        park(cur, l, m_ref);
+        park(cur, l, kRefRest ? lr : m_ref);
         continue;
       }
 
@@ -999,7 +1194,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       FA_TRACE(24 + wg, 0);
       if (good) {
         tc_fence_after_sync();
-        const float inv_l = inv_of(l);
+        const float inv_l = inv_of(kRefRest ? lr : l);
         if (!cur.partial) {
           // 64 columns per round through the warp's staging slice, 32 at a time from TMEM.
           uint8_t* slice = smem + C::kOOff + (wg * 4 + quad) * 4096;
@@ -1008,6 +1203,19 @@ __global__ void __launch_bounds__(kThreads, 1)
           for (int hb = 0; hb < D / 64; ++hb) {
             if (lane == 0) bulk_wait_group_read0();  // the slice's previous store read it
             __syncwarp();
+            if constexpr (kRest) {
+              if (p.mod.rest) {
+#pragma unroll
+                for (int half = 0; half < 2; ++half) {
+                  uint32_t o[32];
+                  tmem_ld32(t_o + hb * 64 + half * 32, o);
+                  tmem_ld_wait();
+                  reg_fence32(o);
+                  stage_rest(ob, half * 4, o, 32, inv_l);
+                }
+                flush_rest(cur, slice, hb * 64);
+              }
+            }
 #pragma unroll
             for (int half = 0; half < 2; ++half) {
               uint32_t o[32];
@@ -1051,7 +1259,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           __syncwarp();
           if (lane == 0) mbar_arrive(&bars->o_free[wg]);
         }
-        write_lse(cur, lse_of(l, m_ref));
+        write_lse(cur, lse_of(l, m_ref));  // (kRef: m_ref is 0)
         FA_TRACE(26 + wg, 0);
       } else {
         ok = false;

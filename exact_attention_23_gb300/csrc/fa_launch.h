@@ -56,6 +56,10 @@ cudaError_t launch_decode_multi(const DecodeParams& p, int d, unsigned combine_g
 // Modified scores (fa_mod.cuh) on the one-tile kernel, mod the kMod… bits.
 cudaError_t launch_fwd_mod_d64(const FwdLaunch& a, int mod);
 cudaError_t launch_fwd_mod_d128(const FwdLaunch& a, int mod);
+// On the pair kernel, two query tiles a unit (a.p.tiles_per_cta = 2): kModOn, or with
+// kModRef.
+cudaError_t launch_fwd_mod_pairs_d64(const FwdLaunch& a, int mod);
+cudaError_t launch_fwd_mod_pairs_d128(const FwdLaunch& a, int mod);
 // New tokens against a cache on the same kernel (a.p.T the rows a key head, a.grid the stretches).
 cudaError_t launch_fwd_tree_d64(const FwdLaunch& a, int mod);
 cudaError_t launch_fwd_tree_d128(const FwdLaunch& a, int mod);

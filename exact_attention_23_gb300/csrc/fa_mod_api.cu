@@ -21,13 +21,16 @@ namespace fa {
 //   rows   int2 [B][T_pad]  visible keys [lo, hi) of each query row ((0, 0): none; padding too)
 //   fwd    int4 [B][n_t]    query tiles, most K tiles first: (tile, first K tile, past the last,
 //                           rows in use: one past the last row that sees or is seen)
+//   pairs  int4 [B][n_p][2] pairs of neighbouring query tiles, n_p = ceil(n_t / 2), the longest walk
+//                           first: (first tile, rows in use, its first K tile, past its last), (the
+//                           second tile's first K tile and past its last, 0, 0)
 //   bwd    int4 [B][n_t]    key tiles, most query tiles first: (tile, first query tile, past the
 //                           last, rows in use)
 //   whole  int2 [B][n_t]    (largest lo, smallest hi) over a tile's rows
 //   span   int2 [B][n_t]    (smallest lo, largest hi) over the rows that see a key
 //   seen   int2 [B][n_t]    (first, past the last) query tile that sees a key tile
 struct VisibleLayout {
-  size_t rows, fwd, bwd, whole, span, seen, bytes;
+  size_t rows, fwd, pairs, bwd, whole, span, seen, bytes;
 };
 
 static VisibleLayout visible_layout(int B, int T) {
@@ -36,7 +39,8 @@ static VisibleLayout visible_layout(int B, int T) {
   VisibleLayout l;
   l.rows = 0;
   l.fwd = up(b * n_t * 128 * 8);
-  l.bwd = l.fwd + up(b * n_t * 16);
+  l.pairs = l.fwd + up(b * n_t * 16);
+  l.bwd = l.pairs + up(b * ((n_t + 1) / 2) * 32);
   l.whole = l.bwd + up(b * n_t * 16);
   l.span = l.whole + up(b * n_t * 8);
   l.seen = l.span + up(b * n_t * 8);
@@ -49,7 +53,7 @@ struct VisibleParams {
   const int* prefix;  // [B] or [B][T] or null
   int prefix_per_token, causal, T, n_t;
   int2* rows;
-  int4 *fwd, *bwd;
+  int4 *fwd, *pairs, *bwd;
   int2 *whole, *span, *seen;
 };
 
@@ -245,6 +249,32 @@ __global__ void __launch_bounds__(kVisThreads) fa_visible_kernel(const VisiblePa
       p.bwd[t0 + rb] = make_int4(t, k.x, k.y, used);
     }
   }
+  // Pairs of query tiles, by the length of their union's walk.
+  const int n_p = (n_t + 1) / 2;
+  auto walk = [&](int t) {  // first K tile and past the last; (0, 0): none
+    const int2 s = t < n_t ? span[t] : make_int2(0, 0);
+    return make_int2(s.x >> 7, (s.y + 127) >> 7);
+  };
+  auto steps = [&](int2 a, int2 c) {
+    if (a.y <= a.x) return c.y - c.x;
+    if (c.y <= c.x) return a.y - a.x;
+    return max(a.y, c.y) - min(a.x, c.x);
+  };
+  for (int t = warp; t < n_p; t += kWarps) {
+    const int2 a = walk(2 * t), c = walk(2 * t + 1);
+    const int n = steps(a, c);
+    int r = 0;
+    for (int q = lane; q < n_p; q += 32) {
+      const int m = steps(walk(2 * q), walk(2 * q + 1));
+      r += m > n || (m == n && q < t);
+    }
+    r = __reduce_add_sync(0xffffffffu, r);
+    if (lane == 0) {
+      int4* out = p.pairs + (static_cast<size_t>(b) * n_p + r) * 2;
+      out[0] = make_int4(2 * t, used, a.x, a.y);
+      out[1] = make_int4(c.x, c.y, 0, 0);
+    }
+  }
 }
 
 }  // namespace fa
@@ -260,9 +290,10 @@ bool mod_sizes(int B, int H, int Hkv, int T, int d) {
 }
 
 // Parts that a key head's query heads are cut into in the backward (a divisor of them): the fewest
-// that give at least kMinCtas CTAs, four for each of a GB300's SMs, so that their unequal walks can
-// be shared out (H16 Hkv4 T8192 d128, five documents: SIDE_E µs with the 256 CTAs of whole groups,
-// SIDE_F in SIDE_G parts). Independent of the device, so that a workspace fits wherever it is made.
+// that give at least kMinCtas CTAs, three for each of a GB300's SMs, so that their unequal walks can
+// be shared out (H16 Hkv4 T8192 d128 capped, five documents: 609 µs with the 256 CTAs of whole
+// groups, 436 in two parts, 459 in four; B2 H16 Hkv4 T4096 causal, whose walks are even: 641, 620 and
+// 640). Independent of the device, so that a workspace fits wherever it is made.
 int bwd_parts(int B, int H, int Hkv, int T) {
   constexpr long long kMinCtas = 456;
   const int group = H / Hkv;
@@ -317,6 +348,7 @@ int fa_visible(const int* doc_ids, const int* prefix_len, int prefix_per_token, 
   p.n_t = static_cast<int>((static_cast<long long>(T) + 127) / 128);
   p.rows = reinterpret_cast<int2*>(base + l.rows);
   p.fwd = reinterpret_cast<int4*>(base + l.fwd);
+  p.pairs = reinterpret_cast<int4*>(base + l.pairs);
   p.bwd = reinterpret_cast<int4*>(base + l.bwd);
   p.whole = reinterpret_cast<int2*>(base + l.whole);
   p.span = reinterpret_cast<int2*>(base + l.span);
@@ -363,13 +395,21 @@ int fa_fwd_mod(const void* q, const void* k, const void* v, void* o, float* lse,
   a.p.status = status;
   a.p.T = T;
   a.p.BH = BH;
-  a.p.n_units = n_t;
-  a.p.total_units = n_t * BH;
+  const int mod = fwd_mod_bits(softcap, slopes, rest);
+  // Two query tiles a CTA, as in the dense forward, where every SM gets enough such units: causal,
+  // d64, B4 H12 T4096 152 -> 148 µs and, capped, 200 -> 178, B1 H12 T16384 551 -> 498 and 732 -> 599;
+  // d128, B2 H16 T4096 (3.4 units an SM) 157 -> 147 and 177 -> 157. With documents, whose walks are
+  // uneven and shorter, 3.4 units are too few (H16 T8192 d128, five documents, capped: 115 -> 120).
+  // Not with a bias (d64 T4096 204 -> 223) or a cap above 60, whose in-place scores do not fit its
+  // registers.
+  const bool pairs = static_cast<long long>((n_t + 1) / 2) * BH >= (visible ? 4LL : 3LL) * sms &&
+                     (mod == fa::kModOn || (mod & fa::kModRef));
+  a.p.n_units = pairs ? (n_t + 1) / 2 : n_t;
+  a.p.total_units = a.p.n_units * BH;
   a.p.n_kv = n_t;
-  a.p.tiles_per_cta = 1;
+  a.p.tiles_per_cta = pairs ? 2 : 1;
   a.p.div_bh = fa::FastDiv::make(static_cast<uint32_t>(BH));
   a.p.div_splits = fa::FastDiv::make(1u);
-  const int mod = fwd_mod_bits(softcap, slopes, rest);
   // Unmodified scores take their maximum before the factor, as the dense kernels; others the
   // plain factor.
   a.p.scale_log2 = mod == fa::kModOn ? exponent_factor(static_cast<double>(scale) * kLog2e, &a.p.s_negate)
@@ -385,6 +425,7 @@ int fa_fwd_mod(const void* q, const void* k, const void* v, void* o, float* lse,
     const uint8_t* base = static_cast<const uint8_t*>(visible);
     a.p.mod.rows = reinterpret_cast<const int2*>(base + l.rows);
     a.p.mod.units = reinterpret_cast<const int4*>(base + l.fwd);
+    a.p.mod.pairs = reinterpret_cast<const int4*>(base + l.pairs);
   }
   a.p.mod.slopes = slopes;
   a.p.mod.rest = static_cast<__nv_bfloat16*>(rest);
@@ -396,7 +437,8 @@ int fa_fwd_mod(const void* q, const void* k, const void* v, void* o, float* lse,
   a.p.mod.causal = causal != 0;
   a.grid = static_cast<unsigned>(std::min(a.p.total_units, sms));
   a.stream = static_cast<cudaStream_t>(stream);
-  const cudaError_t e = (d == 64) ? fa::launch_fwd_mod_d64(a, mod) : fa::launch_fwd_mod_d128(a, mod);
+  const cudaError_t e = pairs ? (d == 64 ? fa::launch_fwd_mod_pairs_d64(a, mod) : fa::launch_fwd_mod_pairs_d128(a, mod))
+                              : (d == 64 ? fa::launch_fwd_mod_d64(a, mod) : fa::launch_fwd_mod_d128(a, mod));
   return e == cudaSuccess ? FA_OK : FA_ERR_LAUNCH;
 }
 
@@ -466,8 +508,8 @@ int fa_bwd_mod(const void* q, const void* k, const void* v, const void* o, const
   a.p.n_qt = T_pad / bq;
   a.p.n_kt = n_t;
   // Heads whose units go out together, the longest walks first: with few CTAs all of them, since
-  // a long walk that starts late is the call's tail (H16 Hkv4 T8192 d128, five documents: SIDE_H ->
-  // SIDE_I µs); otherwise as many as keep their Q and dO (bf16) and dQ accumulator (fp32) in half
+  // a long walk that starts late is the call's tail (H16 Hkv4 T8192 d128 capped, five
+  // documents: 520 -> 436 µs); otherwise as many as keep their Q and dO (bf16) and dQ accumulator (fp32) in half
   // the L2, 64 MB.
   const long long per_head = 8LL * T_pad * d * (H / Hkv / parts);
   const long long in_l2 = std::max<long long>(1, (64LL << 20) / per_head);

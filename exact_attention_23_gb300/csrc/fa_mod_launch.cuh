@@ -19,6 +19,17 @@ cudaError_t launch_fwd_mod(const FwdLaunch& a) {
   return launch_pdl(fn, a.grid, C::kThreads, smem, a.stream, a.tm_q, a.tm_k, a.tm_v, a.tm_o, a.p);
 }
 
+// The same on the pair kernel (two query tiles a CTA; a.p.tiles_per_cta = 2).
+template <int D, int MOD>
+cudaError_t launch_fwd_mod_pairs(const FwdLaunch& a) {
+  auto* fn = &fa_fwd_kernel<D, false, true, false, MOD>;
+  static std::atomic<uint64_t> done[kMaxDevices / 64 + 1];
+  const int smem = Cfg<D>::kSmemBytes;
+  const cudaError_t e = smem_opt_in(fn, smem, done);
+  if (e != cudaSuccess) return e;
+  return launch_pdl(fn, a.grid, kThreads, smem, a.stream, a.tm_q, a.tm_k, a.tm_v, a.tm_o, a.p);
+}
+
 // a.p.BH counts key heads' parts; q_heads = B·H.
 template <int D, int MOD>
 cudaError_t launch_bwd_mod(const BwdLaunch& a, int q_heads) {
