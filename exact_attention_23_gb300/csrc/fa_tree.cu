@@ -65,8 +65,16 @@ int block_rows_log2(int R) { return R <= 16 ? 4 : R <= 32 ? 5 : 7; }
 // Chunks a stretch has at least.
 constexpr int kMinPer = 2, kMinPerWide = 1;
 
+// A cache of at most this many chunks goes without stretches where its entries fit the GPU at once,
+// a CTA each: no workspace, no second kernel and launch (2 µs of the host's, 3 to 6 of the GPU's).
+// A chunk of 64 keys takes such a CTA 0.5 µs at d = 64 and 0.85 at d = 128, one of 128 keys in the wide
+// kernel 1.1: B8 H12, one token, 1000 ragged keys, d64, 11.4 µs against 12.1 (B1: 11.4 against 8.0,
+// which the host's share makes up); B8 H16 Hkv4, 64 tokens, 1300 keys 14.4 against 20.9.
+int solo_chunks(bool wide_rows, int d) { return wide_rows ? 12 : d == 64 ? 18 : 10; }
+
 struct TreeSizes {
   int R, rows_log2, row_blocks, chunk_log2, min_per;
+  bool solo;
   long long entries, grid, slots;
   size_t lse_off, bytes;
 };
@@ -88,6 +96,14 @@ bool tree_sizes(int B, int H, int Hkv, int Tq, int Tmax, int d, int sms, TreeSiz
   const long long most = (z->entries * chunks + z->min_per - 1) / z->min_per;
   const long long fit = static_cast<long long>(sms) *
                         (wide(z->R) ? 1 : d == 64 ? TreeCfg<64>::kCtasPerSm : TreeCfg<128>::kCtasPerSm);
+  z->solo = chunks <= solo_chunks(wide(z->R), d) && z->entries <= fit;
+  if (z->solo) {
+    z->grid = z->entries;
+    z->slots = 0;
+    z->lse_off = 0;
+    z->bytes = 1;  // none needed
+    return true;
+  }
   z->grid = std::max<long long>(1, std::min(fit, most));
   z->slots = z->grid + z->entries;
   auto up = [](size_t x) { return (x + 255u) / 256u * 256u; };
@@ -115,7 +131,7 @@ int fa_fwd_tree(const void* q, const void* k_cache, const void* v_cache, void* o
                 int depths_per_batch, float softcap, const float* slopes, int B, int H, int Hkv, int Tq,
                 int Tmax, int d, float scale, void* workspace, size_t workspace_bytes, int* status,
                 unsigned long long timeout_ns, void* stream) {
-  if (!q || !k_cache || !v_cache || !o || !lse || !ctx_len || !workspace) return FA_ERR_INVALID_ARG;
+  if (!q || !k_cache || !v_cache || !o || !lse || !ctx_len) return FA_ERR_INVALID_ARG;
   fa::TreeSizes z;
   fa::CapFactors cap;
   if (!fa::tree_sizes(B, H, Hkv, Tq, Tmax, d, 1, &z) || !scale_ok(scale) || !cap_factors(scale, softcap, &cap))
@@ -132,15 +148,16 @@ int fa_fwd_tree(const void* q, const void* k_cache, const void* v_cache, void* o
   const size_t db = static_cast<size_t>(depths_per_batch ? B : 1) * Tq * 4;
   const int dst = check_device(&dev, &sms);
   if (dst == FA_OK && !fa::tree_sizes(B, H, Hkv, Tq, Tmax, d, sms, &z)) return FA_ERR_INVALID_ARG;
-  if (workspace_bytes < z.bytes) return FA_ERR_INVALID_ARG;
+  if (!z.solo && (!workspace || workspace_bytes < z.bytes)) return FA_ERR_INVALID_ARG;
   const void* ins[7] = {q, k_cache, v_cache, ctx_len, tree, depths, slopes};
   const size_t in_bytes[7] = {qb, cb, cb, static_cast<size_t>(B) * 4, tb, db, static_cast<size_t>(H) * 4};
   const void* outs[3] = {o, lse, workspace};
   const size_t out_bytes[3] = {qb, lb, z.bytes};
-  for (int x = 0; x < 3; ++x) {
+  const int n_outs = z.solo ? 2 : 3;
+  for (int x = 0; x < n_outs; ++x) {
     for (int y = 0; y < 7; ++y)
       if (ins[y] && overlaps(outs[x], out_bytes[x], ins[y], in_bytes[y])) return FA_ERR_INVALID_ARG;
-    for (int y = x + 1; y < 3; ++y)
+    for (int y = x + 1; y < n_outs; ++y)
       if (overlaps(outs[x], out_bytes[x], outs[y], out_bytes[y])) return FA_ERR_INVALID_ARG;
   }
   if (dst != FA_OK) return dst;
@@ -152,12 +169,14 @@ int fa_fwd_tree(const void* q, const void* k_cache, const void* v_cache, void* o
   a.p.q = static_cast<const __nv_bfloat16*>(q);
   a.p.o = static_cast<__nv_bfloat16*>(o);
   a.p.lse = lse;
-  a.p.o_part = reinterpret_cast<float*>(ws);
-  a.p.lse_part = reinterpret_cast<float*>(ws + z.lse_off);
+  if (!z.solo) {
+    a.p.o_part = reinterpret_cast<float*>(ws);
+    a.p.lse_part = reinterpret_cast<float*>(ws + z.lse_off);
+  }
   a.p.slopes = slopes;
   a.p.status = status;
   a.p.timeout_ns = timeout_ns ? timeout_ns : 2000000000ull;
-  a.p.list = fa::TreeList{ctx_len, B, Hkv, Tq, Tmax, z.row_blocks, z.min_per, z.chunk_log2};
+  a.p.list = fa::TreeList{ctx_len, B, Hkv, Tq, Tmax, z.row_blocks, z.min_per, z.chunk_log2, z.solo ? 1 : 0};
   a.p.mask = fa::TreeMask{tree, depths, fa::FastDiv::make(static_cast<uint32_t>(Tq)), tree_per_batch != 0,
                           depths_per_batch != 0};
   a.p.cap = cap;
@@ -210,6 +229,7 @@ int fa_fwd_tree(const void* q, const void* k_cache, const void* v_cache, void* o
     e = (d == 64) ? fa::launch_tree_rows<64>(a, 1 << z.rows_log2, mod) : fa::launch_tree_rows<128>(a, 1 << z.rows_log2, mod);
   }
   if (e != cudaSuccess) return FA_ERR_LAUNCH;
+  if (z.solo) return FA_OK;
   const long long rows = static_cast<long long>(BHkv) * z.R;
   const unsigned cg = static_cast<unsigned>(std::min<long long>((rows + 7) / 8, static_cast<long long>(sms) * 8));
   auto* combine = d == 64 ? &fa::fa_tree_combine_kernel<64> : &fa::fa_tree_combine_kernel<128>;

@@ -8,7 +8,7 @@
 // numbered in a row, and CTA c takes the c-th of equal stretches, whatever the lengths are (they
 // live on the device). A stretch crosses sequences in segments; a sequence that lies in several
 // stretches leaves one partial (normalised fp32 rows and LSE) per stretch for
-// fa_tree_combine_kernel. Stretch c's segment of list entry e has slot c + e: from one segment to
+// fa_tree_combine_kernel. (Caches short enough for one CTA an entry go without: solo.) Stretch c's segment of list entry e has slot c + e: from one segment to
 // the next c or e grows, so slots never meet.
 #pragma once
 
@@ -23,6 +23,7 @@ struct TreeList {
   int row_blocks;      // row blocks a key head
   int min_per;         // chunks a stretch has at least
   int chunk_log2;      // keys a chunk: 1 << chunk_log2
+  int solo;            // CTA c takes entry c whole: no partials, no second kernel
 };
 
 struct TreeMask {
@@ -98,6 +99,15 @@ struct TreeSegments {
   int b, hk, rb, entry, c0, c1;  // sequence, key head, row block, list entry, chunks [c0, c1)
   bool whole;                    // it covers its entry
   __device__ __forceinline__ void begin(const TreeList& p) {
+    if (p.solo) {
+      const int entries = p.Hkv * p.row_blocks;
+      at.b = static_cast<int>(blockIdx.x) / entries;
+      at.entry0 = at.b * entries;
+      at.chunks = tree_chunks(p, at.b);
+      pos = 0;
+      end = 1;
+      return;
+    }
     const int total = tree_locate(p, -1, &at);
     const int per = tree_per(p, total, gridDim.x);
     // (a list shorter than grid · min_per leaves later CTAs nothing)
@@ -107,6 +117,17 @@ struct TreeSegments {
   }
   __device__ __forceinline__ bool next(const TreeList& p) {
     if (pos >= end) return false;
+    if (p.solo) {  // (a sequence without keys has an empty segment, whose rows it writes)
+      pos = 1;
+      b = at.b;
+      entry = static_cast<int>(blockIdx.x);
+      hk = (entry - at.entry0) / p.row_blocks;
+      rb = entry - at.entry0 - hk * p.row_blocks;
+      c0 = 0;
+      c1 = at.chunks;
+      whole = true;
+      return true;
+    }
     const int entries = p.Hkv * p.row_blocks;
     int y = pos - at.start;
     while (y >= at.chunks * entries) {  // the next sequence with chunks

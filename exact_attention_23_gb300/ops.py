@@ -264,6 +264,10 @@ def fwd_tree_workspace(B: int, H: int, Hkv: int, Tq: int, Tmax: int, d: int, dev
     device = torch.device("cuda" if device is None else device)
     if device.index is None:
         device = torch.device("cuda", torch.cuda.current_device())
+    return torch.empty(_tree_bytes(B, H, Hkv, Tq, Tmax, d, device), dtype=_U8, device=device)
+
+
+def _tree_bytes(B, H, Hkv, Tq, Tmax, d, device):
     if device.index == torch.cuda.current_device():
         n = fa_fwd_tree_workspace_size(B, H, Hkv, Tq, Tmax, d)
     else:
@@ -271,7 +275,7 @@ def fwd_tree_workspace(B: int, H: int, Hkv: int, Tq: int, Tmax: int, d: int, dev
             n = fa_fwd_tree_workspace_size(B, H, Hkv, Tq, Tmax, d)
     if n == 0:
         raise FAError(FA_ERR_INVALID_ARG, "fa_fwd_tree_workspace_size")
-    return torch.empty(n, dtype=_U8, device=device)
+    return n
 
 
 def fwd_tree(q, k_cache, v_cache, ctx_len, tree=None, depths=None, softcap: float = 0.0,
@@ -318,16 +322,18 @@ def fwd_tree(q, k_cache, v_cache, ctx_len, tree=None, depths=None, softcap: floa
     else:
         _check_fp32(lse, (B, H, Tq), device, "lse")
     if workspace is None:
-        workspace = fwd_tree_workspace(B, H, Hkv, Tq, Tmax, d, device=device)
+        need = _tree_bytes(B, H, Hkv, Tq, Tmax, d, device)
+        if need > 1:
+            workspace = torch.empty(need, dtype=_U8, device=device)
     else:
         _check_workspace(workspace, device)
+        need = workspace.numel() * workspace.element_size()
     _check_status(status, device)
     _call(device, "fa_fwd_tree", fa_fwd_tree, q.data_ptr(), k_cache.data_ptr(),
           v_cache.data_ptr(), out.data_ptr(), lse.data_ptr(), ctx_len.data_ptr(), _ptr(tree),
           tree is not None and tree.dim() == 3, _ptr(depths),
           depths is not None and depths.dim() == 2, softcap, _ptr(slopes), B, H, Hkv, Tq, Tmax, d,
-          scale, workspace.data_ptr(), workspace.numel() * workspace.element_size(),
-          _ptr(status), timeout_ns)
+          scale, _ptr(workspace), need, _ptr(status), timeout_ns)
     return out, lse
 
 

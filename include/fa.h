@@ -433,9 +433,9 @@ int fa_rope_append(const void* q, long long q_sb, long long q_sh, long long q_st
  *             (tree[t][s] = s ≤ t)
  *   depths  : optional DEVICE int32 [Tq], or [B][Tq] with depths_per_batch; NULL: 0, 1, 2, …;
  *             used by the bias only
- *   workspace : DEVICE memory of fa_fwd_tree_workspace_size(...) bytes (for the current device; 0:
- *             unsupported sizes, or no usable device), 256-byte aligned, contents immaterial. Not
- *             shared with a call that may run at the same time.
+ *   workspace : DEVICE memory of fa_fwd_tree_workspace_size(...) bytes (for the current device; 1:
+ *             none is needed, NULL will do; 0: unsupported sizes, or no usable device), 256-byte
+ *             aligned, contents immaterial. Not shared with a call that may run at the same time.
  *
  * Cache rows behind a sequence's last new token may hold anything, NaN included.
  */

@@ -14,7 +14,7 @@ BAD, MIS = fa.FA_ERR_INVALID_ARG, fa.FA_ERR_MISALIGNED
 
 
 def _call(q=A, k=A + SZ, v=A + 2 * SZ, o=A + 3 * SZ, lse=A + 4 * SZ, ctx=A + 5 * SZ, tree=None,
-          depths=None, cap=0.0, slopes=None, B=2, H=4, Hkv=2, Tq=8, Tmax=100, d=64, scale=0.125,
+          depths=None, cap=0.0, slopes=None, B=2, H=4, Hkv=2, Tq=8, Tmax=5000, d=64, scale=0.125,
           ws=A + 6 * SZ, ws_bytes=1 << 30):
     return fa.fa_fwd_tree(q, k, v, o, lse, ctx, tree, 1, depths, 1, cap, slopes, B, H, Hkv, Tq, Tmax,
                           d, scale, ws, ws_bytes, None, 0, None)
@@ -38,6 +38,7 @@ def test_refusals(kw, want):
 @pytest.mark.skipif(torch.cuda.is_available(), reason="only meaningful without a CUDA device")
 def test_without_device():
     assert _call(tree=A + 7 * SZ + 1, cap=30.0) == fa.FA_ERR_UNSUPPORTED_DEVICE  # (bytes: any address)
+    assert _call(B=1, H=2, Hkv=1, Tmax=100, ws=None, ws_bytes=0) == fa.FA_ERR_UNSUPPORTED_DEVICE  # a short cache needs none
     assert fa.fa_fwd_tree_workspace_size(2, 4, 2, 8, 100, 64) == 0
     with pytest.raises(ValueError):
         x = torch.zeros(1, 1, 8, 64, dtype=torch.bfloat16)
@@ -104,7 +105,9 @@ def _check(ctx, H, Hkv, n, Tmax, d, tree=False, cap=0.0, bias=False, seed=0):
     ref.check({"o": o, "lse": lse}, r, ("o", "lse"))
 
 
+# room: longer caches have their work shared out in stretches, shorter ones a CTA an entry
 @pytest.mark.gpu
+@pytest.mark.parametrize("room", [0, 3300])
 @pytest.mark.parametrize("ctx,H,Hkv,n,Tmax,d,tree,cap,bias", [
     ([0], 1, 1, 1, 1, 64, False, 0.0, False),                    # one row in all
     ([5], 2, 2, 1, 6, 128, False, 0.0, False),
@@ -120,8 +123,8 @@ def _check(ctx, H, Hkv, n, Tmax, d, tree=False, cap=0.0, bias=False, seed=0):
     ([30, 2], 8, 1, 64, 100, 128, True, 20.0, False),            # 512 rows; one runs over the end
     ([100, 95, 120], 2, 1, 4, 100, 64, False, 0.0, False),       # full caches, drafts outside
 ])
-def test_parity(ctx, H, Hkv, n, Tmax, d, tree, cap, bias):
-    _check(ctx, H, Hkv, n, Tmax, d, tree, cap, bias)
+def test_parity(ctx, H, Hkv, n, Tmax, d, tree, cap, bias, room):
+    _check(ctx, H, Hkv, n, Tmax + room, d, tree, cap, bias)
 
 
 @pytest.mark.gpu
@@ -132,10 +135,11 @@ def test_parity_split_over_every_cta(d):
 
 
 @pytest.mark.gpu
-def test_many_sequences():
+@pytest.mark.parametrize("Tmax", [210, 2500])
+def test_many_sequences(Tmax):
     """More sequences than a warp has lanes, most of them short."""
     ctx = [(37 * b) % 200 - 1 for b in range(75)]
-    _check(ctx, 2, 1, 2, 210, 64, False, 0.0, False, seed=4)
+    _check(ctx, 2, 1, 2, Tmax, 64, False, 0.0, False, seed=4)
 
 
 @pytest.mark.gpu
@@ -258,5 +262,8 @@ def test_wrapper_refusals_on_device():
                  lambda: fa.fwd_tree(q[:, :3].contiguous(), k, v, ctx)):
         with pytest.raises(ValueError):
             call()
+    q, k, v = (x.cuda() for x in _data(2, 4, 2, 3, 5000, 64, 1))
     with pytest.raises(fa.FAError):
         fa.fwd_tree(q, k, v, ctx, workspace=torch.empty(256, dtype=torch.uint8, device="cuda"))
+    assert fa.fa_fwd_tree_workspace_size(2, 4, 2, 3, 20, 64) == 1
+    assert fa.fa_fwd_tree_workspace_size(2, 4, 2, 3, 5000, 64) > 1
