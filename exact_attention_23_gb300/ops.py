@@ -16,34 +16,35 @@ from ._binding import (
     FA_ERR_INVALID_ARG,
     FA_OK,
     FAError,
-    fa_bwd_mod,
     fa_bwd_mod_workspace_size,
-    fa_fwd_mod,
-    fa_fwd_tree,
     fa_fwd_tree_workspace_size,
-    fa_rope,
-    fa_rope_append,
-    fa_visible,
     fa_visible_size,
+    lib,
 )
 
 _BF16, _FP32, _INT32, _U8 = torch.bfloat16, torch.float32, torch.int32, torch.uint8
-# A device's current stream as an address (torch.cuda.current_stream makes a Stream object first,
-# 2 µs of a short call).
-_raw_stream = torch._C._cuda_getCurrentRawStream if hasattr(torch._C, "_cuda_getCurrentRawStream") \
-    else lambda index: torch.cuda.current_stream(index).cuda_stream
+# A device's current stream as an address, and the current device (torch.cuda.current_stream makes
+# a Stream object first, 2 µs of a short call).
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) \
+    or (lambda index: torch.cuda.current_stream(index).cuda_stream)
+_current_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
+_functions: dict = {}
 
 
-def _call(device, what, fn, *args):
-    """fn(*args, stream) with ``device`` current and its current stream; raises on a status."""
+def _call(device, name, *args):
+    """libfa.so's function ``name`` on args and ``device``'s current stream, with the device current;
+    raises on a status. (Truth values go as they are: its argument types take them for ints.)"""
+    fn = _functions.get(name)
+    if fn is None:
+        fn = _functions[name] = getattr(lib(), name)
     index = device.index
-    if index == torch.cuda.current_device():
+    if index == _current_device():
         rc = fn(*args, _raw_stream(index))
     else:
         with torch.cuda.device(index):
             rc = fn(*args, _raw_stream(index))
     if rc != FA_OK:
-        raise FAError(rc, what)
+        raise FAError(rc, name)
 
 
 def _ptr(t):
@@ -71,11 +72,12 @@ def _check_like(t, ref, name):
 
 
 def _check_int32(t, shapes, device, name):
-    if not isinstance(t, torch.Tensor) or t.dtype is not _INT32 or not t.is_contiguous() \
-            or not t.is_cuda or t.shape not in shapes:
+    if not isinstance(t, torch.Tensor) or t.dtype is not _INT32 or t.shape not in shapes \
+            or not t.is_contiguous() or not t.is_cuda:
         raise ValueError(f"{name} must be a contiguous CUDA int32 tensor of shape "
                          + " or ".join(str(list(s)) for s in shapes))
-    _same_device(t, device, name)
+    if t.device != device:
+        _same_device(t, device, name)
 
 
 def _check_fp32(t, shape, device, name):
@@ -141,7 +143,7 @@ def visible(B: int, T: int, causal: bool = True, doc_ids=None, prefix_len=None, 
     elif not isinstance(buffer, torch.Tensor) or buffer.dtype is not _U8 or not buffer.is_contiguous():
         raise ValueError("buffer must be a contiguous uint8 CUDA tensor")
     _same_device(buffer, device, "buffer")
-    _call(device, "fa_visible", fa_visible, _ptr(doc_ids), _ptr(prefix_len),
+    _call(device, "fa_visible", _ptr(doc_ids), _ptr(prefix_len),
           prefix_len is not None and prefix_len.dim() == 2, causal, buffer.data_ptr(),
           buffer.numel(), B, T)
     return Visible(buffer, B, T, bool(causal))
@@ -201,7 +203,7 @@ def fwd_mod(q, k, v, visible=None, causal: bool | None = None, softcap: float = 
     if rest is not None:
         _check_like(rest, q, "rest")
     _check_status(status, device)
-    _call(device, "fa_fwd_mod", fa_fwd_mod, q.data_ptr(), k.data_ptr(), v.data_ptr(),
+    _call(device, "fa_fwd_mod", q.data_ptr(), k.data_ptr(), v.data_ptr(),
           out.data_ptr(), lse.data_ptr(), _ptr(rest), None if visible is None else visible.buffer.data_ptr(),
           causal, softcap, _ptr(slopes), B, H, Hkv, T, d, scale, _ptr(status), timeout_ns)
     return out, lse
@@ -249,7 +251,7 @@ def bwd_mod(q, k, v, o, lse, do, visible=None, causal: bool | None = None, softc
     if rest is not None:
         _check_like(rest, q, "rest")
     _check_status(status, device)
-    _call(device, "fa_bwd_mod", fa_bwd_mod, q.data_ptr(), k.data_ptr(), v.data_ptr(),
+    _call(device, "fa_bwd_mod", q.data_ptr(), k.data_ptr(), v.data_ptr(),
           o.data_ptr(), do.data_ptr(), lse.data_ptr(), _ptr(rest), dq.data_ptr(), dk.data_ptr(),
           dv.data_ptr(), workspace.data_ptr(), workspace.numel() * workspace.element_size(),
           None if visible is None else visible.buffer.data_ptr(), causal, softcap, _ptr(slopes),
@@ -329,7 +331,7 @@ def fwd_tree(q, k_cache, v_cache, ctx_len, tree=None, depths=None, softcap: floa
         _check_workspace(workspace, device)
         need = workspace.numel() * workspace.element_size()
     _check_status(status, device)
-    _call(device, "fa_fwd_tree", fa_fwd_tree, q.data_ptr(), k_cache.data_ptr(),
+    _call(device, "fa_fwd_tree", q.data_ptr(), k_cache.data_ptr(),
           v_cache.data_ptr(), out.data_ptr(), lse.data_ptr(), ctx_len.data_ptr(), _ptr(tree),
           tree is not None and tree.dim() == 3, _ptr(depths),
           depths is not None and depths.dim() == 2, softcap, _ptr(slopes), B, H, Hkv, Tq, Tmax, d,
@@ -369,20 +371,21 @@ def rope_inv_freq(rot_dim: int, base: float = 10000.0, scaling: str | None = Non
 def _check_rows(t, name, shape, device):
     """A bf16 CUDA tensor of ``shape`` [B, n, T, d] and any strides that 16-byte vectors can read;
     its (batch, head, token) strides, 0 for a dimension of one."""
-    if not isinstance(t, torch.Tensor):
-        raise TypeError(f"{name} must be a torch.Tensor")
-    if not t.is_cuda or t.dtype is not _BF16 or t.dim() != 4:
-        raise ValueError(f"{name} must be a CUDA bfloat16 tensor of four dimensions")
-    if t.shape != shape:
-        raise ValueError(f"{name} must have shape {list(shape)}")
-    _same_device(t, device, name)
+    if not (type(t) is torch.Tensor and t.dtype is _BF16 and t.shape == shape
+            and t.device == device and t.is_cuda):
+        if not isinstance(t, torch.Tensor):
+            raise TypeError(f"{name} must be a torch.Tensor")
+        if not t.is_cuda or t.dtype is not _BF16 or t.dim() != 4:
+            raise ValueError(f"{name} must be a CUDA bfloat16 tensor of four dimensions")
+        if t.shape != shape:
+            raise ValueError(f"{name} must have shape {list(shape)}")
+        _same_device(t, device, name)
     sb, sh, st, sd = t.stride()
-    B, n, T, d = shape
-    if B == 1:
+    if shape[0] == 1:
         sb = 0
-    if n == 1:
+    if shape[1] == 1:
         sh = 0
-    if T == 1:
+    if shape[2] == 1:
         st = 0
     if sd != 1 or (sb | sh | st) & 7:
         raise ValueError(f"{name} must have a contiguous last dimension and other strides that "
@@ -438,7 +441,7 @@ def rope(q, k, inv_freq, positions=None, interleaved: bool = False, inverse: boo
         out_q = torch.empty(shape, dtype=_BF16, device=device)
     else:
         _check_like(out_q, q, "out_q")
-    _call(device, "fa_rope", fa_rope, q.data_ptr(), qs, out_q.data_ptr(), _ptr(k), ks,
+    _call(device, "fa_rope", q.data_ptr(), *qs, out_q.data_ptr(), _ptr(k), *ks,
           _ptr(out_k), _ptr(positions), per_batch, inv_freq.data_ptr(), rot, interleaved, inverse,
           mscale, B, H, Hkv, T, d)
     return out_q, out_k
@@ -472,8 +475,8 @@ def rope_append(q, k, v, k_cache, v_cache, ctx_len, inv_freq, positions=None,
         out = torch.empty(shape, dtype=_BF16, device=device)
     else:
         _check_like(out, q, "out")
-    _call(device, "fa_rope_append", fa_rope_append, q.data_ptr(), qs, out.data_ptr(),
-          k.data_ptr(), ks, v.data_ptr(), vs, k_cache.data_ptr(), v_cache.data_ptr(),
+    _call(device, "fa_rope_append", q.data_ptr(), *qs, out.data_ptr(),
+          k.data_ptr(), *ks, v.data_ptr(), *vs, k_cache.data_ptr(), v_cache.data_ptr(),
           ctx_len.data_ptr(), _ptr(positions), per_batch, inv_freq.data_ptr(), rot, interleaved,
           mscale, B, H, Hkv, Tq, Tmax, d)
     return out
