@@ -354,6 +354,42 @@ def test_captured_and_replayed():
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("d,rot,interleaved,cap", [(64, 64, False, 30.0), (128, 64, True, 0.0)])
+def test_training_step(d, rot, interleaved, cap):
+    """A layer's attention as it is trained: queries and keys of the packed projection turned, packed
+    documents, forward, backward, and the gradients turned back onto the projection's."""
+    B, H, Hkv, T = 2, 6, 2, 250
+    g = torch.Generator().manual_seed(17)
+    x = torch.randn(B, T, H + 2 * Hkv, d, generator=g).to(torch.bfloat16).cuda()
+    q, k, v = (x[:, :, s].transpose(1, 2) for s in (slice(0, H), slice(H, H + Hkv), slice(H + Hkv, None)))
+    do = torch.randn(B, H, T, d, generator=g).to(torch.bfloat16).cuda()
+    ids = _ids(B, T, (90, 41), 12)
+    f = fa.rope_inv_freq(rot, scaling="linear", factor=2.0)
+    sl = _slopes(H).cuda()
+    seen = fa.visible(B, T, doc_ids=ids.cuda())
+    q, k = fa.rope(q, k, f, interleaved=interleaved)
+    v = v.contiguous()
+    rest = torch.empty_like(q)
+    o, lse = fa.fwd_mod(q, k, v, visible=seen, softcap=cap, slopes=sl, rest=rest)
+    dq, dk, dv = fa.bwd_mod(q, k, v, o, lse, do, visible=seen, softcap=cap, slopes=sl, rest=rest)
+    gq, gk = fa.rope(dq, dk, f, interleaved=interleaved, inverse=True)
+    torch.cuda.synchronize()
+    r = ref.attention(q.cpu(), k.cpu(), v.cpu(), ref.visible_mask(B, T, True, ids), d ** -0.5, cap,
+                      sl.cpu(), do.cpu())
+    ref.check({"o": o, "lse": lse, "dq": dq, "dk": dk, "dv": dv}, r, ALL)
+    # turned back: the reference's gradients times e^(−i·angle), their bounds added over a pair
+    angle = torch.arange(T).double()[:, None] * f.cpu()
+    at = (slice(0, rot, 2), slice(1, rot, 2)) if interleaved else (slice(0, rot // 2), slice(rot // 2, rot))
+    for got, n in ((gq, "dq"), (gk, "dk")):
+        want, tol = r[n].clone(), r[n + "_tol"].clone()
+        z = torch.complex(r[n][..., at[0]], r[n][..., at[1]]) * torch.polar(torch.ones_like(angle), -angle)
+        pair = r[n + "_tol"][..., at[0]] + r[n + "_tol"][..., at[1]]
+        for s, y in zip(at, (z.real, z.imag)):
+            want[..., s], tol[..., s] = y, pair + ref.U * (y.abs() + pair) + 1e-6
+        ref.check({n: got}, {n: want, n + "_tol": tol}, (n,), "turned back")
+
+
+@pytest.mark.gpu
 def test_wrapper_refusals_on_device():
     q, k, v, do = (x.cuda() for x in _tensors(1, 4, 2, 40, 64, 8))
     seen = fa.visible(1, 40, causal=False)
