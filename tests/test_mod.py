@@ -211,6 +211,39 @@ def test_parity_with_visible(B, H, Hkv, T, d, causal, cap, bias, lengths, pad, p
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("T,d,causal,cap,lengths,pad,prefix,with_rest", [
+    (300, 64, True, 0.0, None, 0, None, True),
+    (290, 128, False, 0.0, None, 0, None, False),
+    (257, 64, True, 20.0, None, 0, None, False),               # far and near scores
+    (300, 128, True, 20.0, None, 0, None, True),
+    (300, 64, True, 50.0, (100, 1, 47), 30, "b", True),
+    (384, 128, True, 50.0, (300, 9), 140, None, False),        # a pair whose second tile sees nothing
+    (300, 64, False, 0.0, (129, 3), 17, None, True),
+    (280, 128, True, 0.0, (30, 128, 60), 0, "t", False),
+])
+def test_parity_with_many_heads(T, d, causal, cap, lengths, pad, prefix, with_rest):
+    """320 heads: two query tiles a CTA (documents, prefixes, caps of up to 60)."""
+    B, H, Hkv = 4, 80, 10
+    q, k, v, do = _tensors(B, H, Hkv, T, d, 19 * T + d, 4.0 if cap else 1.0)
+    ids = None if lengths is None else _ids(B, T, lengths, pad)
+    pre = None
+    if prefix == "b":
+        pre = torch.tensor([60 * b + 7 for b in range(B)], dtype=torch.int32)
+    elif prefix == "t":
+        pre = ((ids + 2) * 23 - 40).to(torch.int32)
+    ok = ref.visible_mask(B, T, causal, ids, pre)
+    r = ref.attention(q, k, v, ok, d ** -0.5, cap, None, do)
+    seen = None
+    if ids is not None:
+        seen = fa.visible(B, T, causal=causal, doc_ids=ids.cuda(),
+                          prefix_len=None if pre is None else pre.cuda())
+        if pad:                                                # padding may hold anything
+            for x, bad in ((q, math.nan), (k, math.inf), (v, math.nan), (do, math.nan)):
+                x[:, :, T - pad:] = bad
+    ref.check(_run(q, k, v, do, seen, softcap=cap, causal=causal, with_rest=with_rest), r, ALL)
+
+
+@pytest.mark.gpu
 @pytest.mark.parametrize("T,lengths,pad,causal,prefix", [
     (1, (1,), 0, True, None), (31, (4, 9), 3, True, "b"), (1000, (128, 77), 0, False, None),
     (33000, (1000, 1, 2048), 129, True, "t"), (70001, (50000, 333), 7, True, "b"),
