@@ -456,7 +456,8 @@ __global__ void __launch_bounds__(256) fa_tree_combine_kernel(const TreeParams p
   const int lane = threadIdx.x & 31;
   const int entries = p.list.Hkv * p.list.row_blocks;
   const long long rows = static_cast<long long>(p.list.B) * p.list.Hkv * p.R;
-  const int total = tree_locate(p.list, -1, nullptr);
+  int scan_n, scan_incl;
+  const int total = tree_total(p.list, &scan_n, &scan_incl);
   const int per = tree_per(p.list, total, stretches);
   for (long long row = static_cast<long long>(blockIdx.x) * 8 + (threadIdx.x >> 5); row < rows;
        row += static_cast<long long>(gridDim.x) * 8) {

@@ -45,13 +45,6 @@ __device__ __forceinline__ int tree_keys(const TreeList& p, int ctx) {
   return static_cast<int>(min(static_cast<long long>(ctx) + p.Tq, static_cast<long long>(p.Tmax)));
 }
 
-// Where a position of the list of all chunks lies.
-struct TreePlace {
-  int b, chunks;     // sequence, its chunks
-  int entry0;        // list entry of the sequence's first (key head, row block)
-  int start;         // position of its first chunk
-};
-
 __device__ __forceinline__ int tree_chunks(const TreeList& p, int b) {
   const int ctx = p.ctx_len[b];
   if (ctx < 0) return 0;
@@ -59,29 +52,26 @@ __device__ __forceinline__ int tree_chunks(const TreeList& p, int b) {
   return static_cast<int>((min(keys, static_cast<long long>(p.Tmax)) + (1 << p.chunk_log2) - 1) >> p.chunk_log2);
 }
 
-// The list's length, and (x ≥ 0) the sequence that position x lies in; whole warp. (Positions fit
-// an int: the host refuses longer lists.)
-__device__ __forceinline__ int tree_locate(const TreeList& p, int x, TreePlace* at) {
+// Of the 32 sequences from b0: this lane's chunks (of one list entry), and the positions up to and
+// with this lane's sequence; whole warp. (Positions fit an int: the host refuses longer lists.)
+__device__ __forceinline__ void tree_scan(const TreeList& p, int b0, int* chunks, int* incl) {
   const int lane = threadIdx.x & 31;
-  const int entries = p.Hkv * p.row_blocks;
+  *chunks = b0 + lane < p.B ? tree_chunks(p, b0 + lane) : 0;
+  int x = *chunks * p.Hkv * p.row_blocks;
+#pragma unroll
+  for (int off = 1; off < 32; off <<= 1) {
+    const int y = __shfl_up_sync(0xffffffffu, x, off);
+    if (lane >= off) x += y;
+  }
+  *incl = x;
+}
+
+// The list's length; the scan of its last 32 sequences stays in chunks and incl. Whole warp.
+__device__ __forceinline__ int tree_total(const TreeList& p, int* chunks, int* incl) {
   int run = 0;
   for (int b0 = 0; b0 < p.B; b0 += 32) {
-    const int n = b0 + lane < p.B ? tree_chunks(p, b0 + lane) : 0;
-    int incl = n * entries;
-#pragma unroll
-    for (int off = 1; off < 32; off <<= 1) {
-      const int y = __shfl_up_sync(0xffffffffu, incl, off);
-      if (lane >= off) incl += y;
-    }
-    const int total = __shfl_sync(0xffffffffu, incl, 31);
-    if (x >= run && x < run + total) {
-      const int w = __ffs(__ballot_sync(0xffffffffu, run + incl > x)) - 1;
-      at->b = b0 + w;
-      at->chunks = __shfl_sync(0xffffffffu, n, w);
-      at->start = run + __shfl_sync(0xffffffffu, incl, w) - at->chunks * entries;
-      at->entry0 = at->b * entries;
-    }
-    run += total;
+    tree_scan(p, b0, chunks, incl);
+    run += __shfl_sync(0xffffffffu, *incl, 31);
   }
   return run;
 }
@@ -93,7 +83,11 @@ __device__ __forceinline__ int tree_per(const TreeList& p, int total, int stretc
 
 // A stretch's segments in order.
 struct TreeSegments {
-  TreePlace at;
+  struct {
+    int b, chunks;               // sequence, its chunks
+    int entry0;                  // list entry of the sequence's first (key head, row block)
+    int start;                   // position of its first chunk
+  } at;
   int pos, end;                  // next position, past the stretch's last
   // the current segment
   int b, hk, rb, entry, c0, c1;  // sequence, key head, row block, list entry, chunks [c0, c1)
@@ -108,12 +102,28 @@ struct TreeSegments {
       end = 1;
       return;
     }
-    const int total = tree_locate(p, -1, &at);
+    int n, incl;
+    const int total = tree_total(p, &n, &incl);
     const int per = tree_per(p, total, gridDim.x);
     // (a list shorter than grid · min_per leaves later CTAs nothing)
     pos = static_cast<int>(min(static_cast<long long>(per) * blockIdx.x, static_cast<long long>(total)));
     end = min(total - pos, per) + pos;
-    if (pos < end) tree_locate(p, pos, &at);
+    if (pos >= end) return;
+    // The sequence that pos lies in: up to 32 sequences from the scan at hand (a second one, with
+    // its loads, cost every CTA 1 µs before its first key), else block by block.
+    int run = 0, b0 = 0;
+    if (p.B > 32)
+      for (;; b0 += 32) {
+        tree_scan(p, b0, &n, &incl);
+        const int sum = __shfl_sync(0xffffffffu, incl, 31);
+        if (pos < run + sum) break;
+        run += sum;
+      }
+    const int w = __ffs(__ballot_sync(0xffffffffu, run + incl > pos)) - 1;
+    at.b = b0 + w;
+    at.chunks = __shfl_sync(0xffffffffu, n, w);
+    at.entry0 = at.b * p.Hkv * p.row_blocks;
+    at.start = run + __shfl_sync(0xffffffffu, incl, w) - at.chunks * p.Hkv * p.row_blocks;
   }
   __device__ __forceinline__ bool next(const TreeList& p) {
     if (pos >= end) return false;
