@@ -861,10 +861,11 @@ __global__ void __launch_bounds__(Cfg1<D, (MOD & kModRef) != 0>::kThreads, 1)
         bool fused = false;  // kRef: a step without masks or far scores
         if constexpr (MOD != 0) {
           // Capped or biased scores to base-2 exponents in place (fa_mod.cuh); the bias is linear
-          // in the key where every key of the step lies at or before the warp's first row. (A far
-          // step, rare, takes the general bias.)
-          const bool left = kTree ? k0 + kC - 1 <= ctx : k0 + kC - 1 <= qt * kBlockM + quad * 32;
+          // in the key where every key of the step lies at or before the warp's first row (TREE: at or
+          // before this row's position, which depths may put anywhere). (A far step, rare, takes
+          // the general bias.)
           const float dist0 = kTree ? q_at - static_cast<float>(k0) : static_cast<float>(q_row - k0);
+          const bool left = kTree ? dist0 >= static_cast<float>(kC - 1) : k0 + kC - 1 <= qt * kBlockM + quad * 32;
           const float base = nslope * dist0;
           auto to_exponents = [&]<bool FAR, bool LEFT>() {
 #pragma unroll

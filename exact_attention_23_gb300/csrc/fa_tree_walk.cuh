@@ -110,15 +110,16 @@ struct TreeSegments {
     end = min(total - pos, per) + pos;
     if (pos >= end) return;
     // The sequence that pos lies in: up to 32 sequences from the scan at hand (a second one, with
-    // its loads, cost every CTA 1 µs before its first key), else block by block.
+    // its loads, cost every CTA 0.4 µs before its first key), else block by block.
     int run = 0, b0 = 0;
-    if (p.B > 32)
-      for (;; b0 += 32) {
+    if (p.B > 32) {
+      for (; b0 < p.B; b0 += 32) {
         tree_scan(p, b0, &n, &incl);
         const int sum = __shfl_sync(0xffffffffu, incl, 31);
         if (pos < run + sum) break;
         run += sum;
       }
+    }
     const int w = __ffs(__ballot_sync(0xffffffffu, run + incl > pos)) - 1;
     at.b = b0 + w;
     at.chunks = __shfl_sync(0xffffffffu, n, w);

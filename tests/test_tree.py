@@ -143,6 +143,37 @@ def test_many_sequences(Tmax):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("B", [3, 40])
+@pytest.mark.parametrize("n,Tmax", [(1, 90), (1, 4000), (20, 90), (20, 4000)])
+def test_nothing_active(B, n, Tmax):
+    q, k, v = (x.cuda() for x in _data(B, 4, 2, n, Tmax, 64, 6))
+    o, lse = fa.fwd_tree(q, k.fill_(math.nan), v.fill_(math.nan),
+                         torch.full((B,), -1, dtype=torch.int32, device="cuda"))
+    torch.cuda.synchronize()
+    assert not o.any() and torch.isneginf(lse).all()
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("H", [2, 16])
+@pytest.mark.parametrize("cap", [0.0, 20.0])
+def test_depths_anywhere(H, cap):
+    """Depths that put a new token in front of context keys: the bias is by distance on both sides."""
+    n, ctx, Tmax, d = 5, 300, 310, 64
+    q, k, v = _data(1, H, 1, n, Tmax, d, 14, 2.0)
+    dep = torch.tensor([-290, -140, 0, -1, 400], dtype=torch.int32)
+    tree = torch.eye(n, dtype=torch.uint8)
+    sl = torch.tensor([2.0 ** (-8.0 * (h + 1) / H) for h in range(H)])
+    qa = ctx + dep[None]
+    ka = torch.arange(Tmax)[None].clone()
+    ka[0, ctx:ctx + n] = qa[0]
+    r = ref.attention(q, k, v, _seen([ctx], n, Tmax, tree[None]), d ** -0.5, cap, sl, query_at=qa, key_at=ka)
+    o, lse = fa.fwd_tree(q.cuda(), k.cuda(), v.cuda(), torch.tensor([ctx], dtype=torch.int32).cuda(),
+                         tree=tree.cuda(), depths=dep.cuda(), softcap=cap, slopes=sl.cuda())
+    torch.cuda.synchronize()
+    ref.check({"o": o, "lse": lse}, r, ("o", "lse"))
+
+
+@pytest.mark.gpu
 def test_rows_of_the_tree_that_see_nothing_new():
     """A tree row of zeros sees the context alone, and without a context nothing."""
     q, k, v = _data(2, 2, 2, 4, 40, 64, 9)
