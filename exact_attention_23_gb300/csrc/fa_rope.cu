@@ -104,10 +104,10 @@ __global__ void __launch_bounds__(kRopeThreads, kRopeBlocks) fa_rope_kernel(cons
   }
   float cs[8], sn[8];
   if (turn && live && h0 < p.H + p.Hkv) {
-    const int pos = p.positions ? p.positions[p.pos_per_batch ? row : t] : ctx + t;
+    const long long pos = p.positions ? p.positions[p.pos_per_batch ? row : t] : static_cast<long long>(ctx) + t;
 #pragma unroll
     for (int e = 0; e < 8; ++e) {
-      const unsigned long long a = turns[u * 8 + e] * static_cast<unsigned long long>(static_cast<long long>(pos));
+      const unsigned long long a = turns[u * 8 + e] * static_cast<unsigned long long>(pos);
       const float x = static_cast<float>(static_cast<int>(a >> 32)) * 1.4629180792671596e-9f;  // 2π·2⁻³²
       cs[e] = __cosf(x) * p.mscale;
       sn[e] = __sinf(x) * (p.mscale * p.sign);
@@ -209,6 +209,15 @@ int rope_launch(RopeParams& p, bool append, int interleaved, int d, void* stream
              ? FA_OK : FA_ERR_LAUNCH;
 }
 
+// Whether an output lies over one of the small inputs.
+bool over_tables(const void* out, size_t bytes, const int* positions, int per_batch, const double* inv_freq,
+                 int rot_dim, const int* ctx_len, int B, int T) {
+  const size_t pb = static_cast<size_t>(per_batch ? B : 1) * T * 4;
+  return (positions && overlaps(out, bytes, positions, pb)) ||
+         overlaps(out, bytes, inv_freq, static_cast<size_t>(rot_dim) * 4) ||
+         (ctx_len && overlaps(out, bytes, ctx_len, static_cast<size_t>(B) * 4));
+}
+
 bool sizes_ok(int B, int H, int Hkv, int T, int d, int rot_dim, float mscale) {
   if (B <= 0 || H <= 0 || Hkv < 0 || T <= 0 || (d != 64 && d != 128)) return false;
   if (rot_dim <= 0 || rot_dim > d || (rot_dim & 15)) return false;
@@ -251,6 +260,9 @@ int fa_rope(const void* q, long long q_sb, long long q_sh, long long q_st, void*
   if (k && ((!k_in_place && overlaps(k_out, ko, k, ks)) || overlaps(q_out, qo, k, ks) ||
             overlaps(k_out, ko, q, qs) || overlaps(q_out, qo, k_out, ko)))
     return FA_ERR_INVALID_ARG;
+  if (over_tables(q_out, qo, positions, positions_per_batch, inv_freq, rot_dim, nullptr, B, T) ||
+      (k && over_tables(k_out, ko, positions, positions_per_batch, inv_freq, rot_dim, nullptr, B, T)))
+    return FA_ERR_INVALID_ARG;
   p.q_out = static_cast<__nv_bfloat16*>(q_out);
   p.k_out = static_cast<__nv_bfloat16*>(k_out);
   p.positions = positions;
@@ -292,6 +304,8 @@ int fa_rope_append(const void* q, long long q_sb, long long q_sh, long long q_st
   const void* ins[3] = {q, k, v};
   const size_t in_bytes[3] = {qs, ks, vs};
   for (int a = 0; a < 3; ++a) {
+    if (over_tables(outs[a], out_bytes[a], positions, positions_per_batch, inv_freq, rot_dim, ctx_len, B, Tq))
+      return FA_ERR_INVALID_ARG;
     for (int b = 0; b < 3; ++b)
       if (!(a == 0 && b == 0 && q_in_place) && overlaps(outs[a], out_bytes[a], ins[b], in_bytes[b]))
         return FA_ERR_INVALID_ARG;

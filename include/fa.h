@@ -336,7 +336,9 @@ int fa_visible(const int* doc_ids, const int* prefix_len, int prefix_per_token, 
  *
  *   visible : a buffer filled by fa_visible for this B and T, or NULL: then `causal` alone says
  *             who sees whom (with a buffer, `causal` is not looked at)
- *   softcap : finite, ≥ 0
+ *   softcap : finite, ≥ 0, and not below |scale| / 30000. A cap of at most 60 without slopes takes
+ *             the softmax without a running maximum: whatever the scores are, values v of
+ *             magnitudes from 2⁻³⁰ to 2²⁰ keep their precision (2⁻⁶⁰ to 2⁶⁰ with a cap of 30)
  *   slopes  : optional DEVICE float [H], finite; no gradient is taken of them
  *   rest    : optional bf16 [B, H, T, d], written with what o's rounding to bf16 leaves out (o + rest
  *             is the output to 16 bits), for fa_bwd_mod
@@ -381,6 +383,7 @@ int fa_bwd_mod(const void* q, const void* k, const void* v, const void* o, const
  *               whoever makes it); the angle keeps 2⁻⁶⁴ of a turn at every int32 position
  *   rot_dim   : a multiple of 16, 16 … d
  *   positions : DEVICE int32 [T], or [B][T] with positions_per_batch, or NULL (see each call)
+ *   (none of these may lie in an output)
  *   sources   : bf16, any strides (*_sb, *_sh, *_st elements a batch, head, token; ≥ 0 and
  *               multiples of 8; the d dimensions contiguous), so that a packed projection
  *               [B, T, heads, d] is read in place

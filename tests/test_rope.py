@@ -54,6 +54,14 @@ def test_rope_append_refusals(kw, want):
     assert _append(**kw) == want
 
 
+@pytest.mark.parametrize("call,kw", [
+    (_rope, dict(pos=A + SZ)), (_rope, dict(pos=A + 3 * SZ + 256, per=1)), (_rope, dict(f=A + 3 * SZ)),
+    (_append, dict(pos=A + SZ)), (_append, dict(f=A + 4 * SZ)), (_append, dict(ctx=A + 5 * SZ)),
+])
+def test_outputs_over_the_small_inputs_are_refused(call, kw):
+    assert call(**kw) == BAD
+
+
 @pytest.mark.skipif(torch.cuda.is_available(), reason="only meaningful without a CUDA device")
 def test_valid_calls_without_device_report_unsupported():
     assert _rope() == fa.FA_ERR_UNSUPPORTED_DEVICE
