@@ -518,7 +518,7 @@ __global__ void __launch_bounds__(Cfg1<D, (MOD & kModRef) != 0>::kThreads, 1)
         // The parts of a row share O and the reference: they post their sums, meet, and each
         // writes its columns.
         const int par = ne & 1;
-        // (m: the sum of the rounded weights, kRefRest)
+        // (m: the largest weight, kRefRest)
         float2* xs = reinterpret_cast<float2*>(smem + C::kXchOff) + (par * H) * kBlockM;
         xs[half * kBlockM + row] = make_float2(l, m);
         __threadfence_block();
@@ -533,14 +533,14 @@ __global__ void __launch_bounds__(Cfg1<D, (MOD & kModRef) != 0>::kThreads, 1)
           fail_rows(w);
           return false;
         }
-        float L = 0.0f, LR = 0.0f;
+        float L = 0.0f, top = 0.0f;
 #pragma unroll
         for (int h = 0; h < H; ++h) {
           const float2 x = xs[h * kBlockM + row];
           L += x.x;
-          LR += x.y;
+          if constexpr (kRefRest) top = fmaxf(top, x.y);
         }
-        const float inv_l = !(L > 0.0f) ? 0.0f : 1.0f / (kRefRest ? LR : L);
+        const float inv_l = !(L > 0.0f) ? 0.0f : 1.0f / (kRefRest ? top_rounded(L, top) : L);
         uint32_t o[kOutCols];
         static_assert(kOutCols == 16 || kOutCols % 32 == 0, "output columns");
         if constexpr (kOutCols == 16) {
@@ -811,7 +811,7 @@ __global__ void __launch_bounds__(Cfg1<D, (MOD & kModRef) != 0>::kThreads, 1)
       }
       // reference max (base-2 scaled units) shared by O_h and l
       float m_ref = kRef ? 0.0f : -INFINITY;
-      float l = 0.0f, lr = 0.0f;  // lr (kRefRest): the sum of the rounded weights
+      float l = 0.0f, top0 = 0.0f, top1 = 0.0f;  // (kRefRest: the largest weight of either parity)
       // the tile's K tiles (GEN: its walk, the next position fetched a step ahead)
       Walk w{nullptr, 0};
       int nx = 0;
@@ -993,7 +993,7 @@ __global__ void __launch_bounds__(Cfg1<D, (MOD & kModRef) != 0>::kThreads, 1)
         const uint64_t c2 = f2_pack(c, c);
         const float m_use = ((GEN || H == 2) && m_ref == -INFINITY) ? 0.0f : m_ref;
         const uint64_t nm2 = f2_pack(-m_use, -m_use);
-        uint64_t acc0 = f2_pack(0.f, 0.f), acc1 = acc0, acc_r = acc0;
+        uint64_t acc0 = f2_pack(0.f, 0.f), acc1 = acc0;
         uint32_t pk[kC / 2];
         auto exponentials = [&]<bool FUSED>() {
 #pragma unroll
@@ -1009,9 +1009,11 @@ __global__ void __launch_bounds__(Cfg1<D, (MOD & kModRef) != 0>::kThreads, 1)
             const float p1 = ex2_approx(x1);
             if (t & 1) acc1 = f2_add(acc1, f2_pack(p0, p1));
             else acc0 = f2_add(acc0, f2_pack(p0, p1));
+            if constexpr (kRefRest) {
+              if (t & 1) top1 = fmax3(top1, p0, p1);
+              else top0 = fmax3(top0, p0, p1);
+            }
             pk[t] = pack_bf16x2(p0, p1);
-            if constexpr (kRefRest)
-              acc_r = f2_add(acc_r, f2_pack(u2f(pk[t] << 16), u2f(pk[t] & 0xFFFF0000u)));
           }
         };
         if (kRef && fused) exponentials.template operator()<kRef>();
@@ -1057,10 +1059,6 @@ __global__ void __launch_bounds__(Cfg1<D, (MOD & kModRef) != 0>::kThreads, 1)
           f2_unpack(acc0, a0, a1);
           f2_unpack(acc1, b0, b1);
           l += (a0 + b0) + (a1 + b1);
-          if constexpr (kRefRest) {
-            f2_unpack(acc_r, a0, a1);
-            lr += a0 + a1;
-          }
         }
         // (j = 0) The previous unit's last P·V, step g − 1, is the one before this step's:
         // read its O out (releasing O to this unit's first P·V) and write it.
@@ -1086,7 +1084,7 @@ __global__ void __launch_bounds__(Cfg1<D, (MOD & kModRef) != 0>::kThreads, 1)
         fail_rows(cur);
         continue;
       }
-      *prec = make_float4(l, kRefRest ? lr : m_ref, __int_as_float(cur.r0), __int_as_float(kTree ? (u.split < 0 ? u.bh : -1 - u.split)
+      *prec = make_float4(l, kRefRest ? fmaxf(top0, top1) : m_ref, __int_as_float(cur.r0), __int_as_float(kTree ? (u.split < 0 ? u.bh : -1 - u.split)
                                                                                     : cur.bh + p.BH * u.split));
       pend = true;
     }

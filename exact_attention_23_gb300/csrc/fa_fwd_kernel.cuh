@@ -368,8 +368,9 @@ __global__ void __launch_bounds__(kThreads, 1)
                   const FwdParams p) {
   using C = Cfg<D, QK8>;
   constexpr bool kRef = (MOD & kModRef) != 0;             // the softmax is taken against 0
-  constexpr bool kRefRest = (MOD & kModRest) != 0;        // … with o's rest
-  constexpr bool kRest = MOD != 0 && (!kRef || kRefRest);  // o's rest may be asked for
+  constexpr bool kRest = (MOD & kModRest) != 0;           // o's rest is asked for
+  constexpr bool kRefRest = kRef && kRest;
+  constexpr bool kParts = GEN && MOD == 0;                // several key ranges are possible
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
   Bars* bars = reinterpret_cast<Bars*>(smem + C::kBarOff);
@@ -625,9 +626,8 @@ __global__ void __launch_bounds__(kThreads, 1)
           if constexpr (MOD != 0) {
             // Keys behind the last one that some query of the sequence sees may hold anything
             // (padding): their P is 0, and 0 · NaN must not reach O.
-            const int used = u.mh - us.kt * kBlockN;
-            if (used < kBlockN) {
-              for (int x = max(used, 0) * 8 + lane; x < kBlockN * 8; x += 32)
+            if (us.kt == u.mh / kBlockN) {
+              for (int x = u.mh % kBlockN * 8 + lane; x < kBlockN * 8; x += 32)
 #pragma unroll
                 for (int s = 0; s < C::kSub; ++s)
                   st_shared_v4(v_base + st * C::kTileBytes + s * C::kSubBytes + x * 16, 0u, 0u, 0u, 0u);
@@ -725,18 +725,16 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
         for (int t = 0; t < D / 8; ++t) orow[t] = make_uint4(b2, b2, b2, b2);
         if constexpr (kRest) {
-          if (p.mod.rest) {
-            uint4* rrow = reinterpret_cast<uint4*>(p.mod.rest + w.row_idx * D);
+          uint4* rrow = reinterpret_cast<uint4*>(p.mod.rest + w.row_idx * D);
 #pragma unroll
-            for (int t = 0; t < D / 8; ++t) rrow[t] = make_uint4(b2, b2, b2, b2);
-          }
+          for (int t = 0; t < D / 8; ++t) rrow[t] = make_uint4(b2, b2, b2, b2);
         }
       }
     };
-    // What the rounding to bf16 leaves out of n / 8 chunks of 8 values of this thread's row, x times
-    // mul, into the warp's staging slice at chunk ch0 on; flush_rest then writes the slice's rows, 64
-    // columns from c0, whole rows at a time (the slice's next use may follow at once).
-    auto stage_rest = [&](uint32_t ob, int ch0, const uint32_t* x, int n, float mul) {
+    // What the rounding to bf16 leaves out of n values x·mul of this thread's row, from column c0.
+    auto write_rest = [&](const RowOut& w, const uint32_t* x, int n, int c0, float mul) {
+      if (!w.in_range) return;
+      uint4* rrow = reinterpret_cast<uint4*>(p.mod.rest + w.row_idx * D + c0);
 #pragma unroll
       for (int t = 0; t < n / 8; ++t) {
         uint32_t lo[4];
@@ -746,20 +744,8 @@ __global__ void __launch_bounds__(kThreads, 1)
           const uint32_t hi = pack_bf16x2(a, b);
           lo[e] = pack_bf16x2(a - __uint_as_float(hi << 16), b - __uint_as_float(hi & 0xFFFF0000u));
         }
-        st_shared_v4(ob + (((ch0 + t) ^ (lane & 7)) << 4), lo[0], lo[1], lo[2], lo[3]);
+        rrow[t] = make_uint4(lo[0], lo[1], lo[2], lo[3]);
       }
-    };
-    auto flush_rest = [&](const RowOut& w, const uint8_t* slice, int c0) {
-      __syncwarp();
-      __nv_bfloat16* dst = p.mod.rest + (static_cast<size_t>(w.bh) * p.T + w.r0) * D + c0;
-#pragma unroll
-      for (int it = 0; it < 8; ++it) {
-        const int r = it * 4 + (lane >> 3), ch = lane & 7;
-        if (w.r0 + r < p.T)
-          *reinterpret_cast<uint4*>(dst + static_cast<size_t>(r) * D + ch * 8) =
-              *reinterpret_cast<const uint4*>(slice + r * 128 + ((ch ^ (r & 7)) << 4));
-      }
-      __syncwarp();
     };
     auto fail_rows = [&](const RowOut& w) {
       write_const_row(w, 0x7FC00000u);
@@ -774,20 +760,15 @@ __global__ void __launch_bounds__(kThreads, 1)
     // map's 128-byte swizzle; conflict-free), and its lane 0 stores them as one 64 × 32
     // box; rows past the sequence are not written. The warp's previous store from the
     // slice (one unit back) must have read it out first.
-    // (kRef: the reference is 0, and m carries the sum of the rounded weights)
+    // (kRef: the reference is 0, and m carries the largest weight)
     auto store_o = [&](const RowOut& w, const uint32_t* o, float l, float m) {
-      const float inv_l = inv_of(kRefRest ? m : l);
+      const float inv_l = inv_of(kRefRest ? top_rounded(l, m) : l);
       if (D == 64 && !w.partial) {
         uint8_t* slice = smem + C::kOOff + (wg * 4 + quad) * 4096;
         const uint32_t ob = smem_u32(slice) + lane * 128;
         if (lane == 0) bulk_wait_group_read0();
         __syncwarp();
-        if constexpr (kRest && D == 64) {
-          if (p.mod.rest) {
-            stage_rest(ob, 0, o, 64, inv_l);
-            flush_rest(w, slice, 0);
-          }
-        }
+        if constexpr (kRest && D == 64) write_rest(w, o, 64, 0, inv_l);
 #pragma unroll
         for (int ch = 0; ch < D / 8; ++ch)
           st_shared_v4(ob + ((ch ^ (lane & 7)) << 4),
@@ -828,7 +809,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     // The pending unit's l, m and output position wait in shared memory (this thread's
     // 16-byte record), not in registers the step loop needs. The fp32 partial rows of the
     // general form keep the immediate epilogue.
-    const bool defer = C::kDefer && !(GEN && p.n_splits > 1);
+    const bool defer = C::kDefer && !(kParts && p.n_splits > 1);
     bool pend = false;
     float4* const prec = reinterpret_cast<float4*>(smem + C::kPendOff) + wg * kBlockM + row;
     auto park = [&](const RowOut& w, float l, float m) {
@@ -881,7 +862,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                            static_cast<size_t>(q_row),
                        (static_cast<size_t>(u.split) * p.BH + u.bh) * static_cast<size_t>(p.T) +
                            q_row,
-                       qt * kBlockM + quad * 32, u.bh, q_row < p.T, GEN && p.n_splits > 1};
+                       qt * kBlockM + quad * 32, u.bh, q_row < p.T, kParts && p.n_splits > 1};
       if (!ok) {
         // A wait gave up earlier: mark every row this warpgroup owns as failed.
         if (pend) fail_pending();
@@ -897,7 +878,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 
       // reference max (base-2 scaled units) shared by O and l
       float m_ref = kRef ? 0.0f : -INFINITY;
-      float l = 0.0f, lr = 0.0f;  // lr (kRefRest): the sum of the rounded weights
+      float l = 0.0f, top0 = 0.0f, top1 = 0.0f;  // (kRefRest: the largest weight of either parity)
       int vlo = 0, vhi = 0;  // MOD: this row's visible keys [lo, hi)
       if constexpr (MOD != 0) {
         const int b = static_cast<int>(p.mod.div_h.div(static_cast<uint32_t>(u.bh)));
@@ -949,7 +930,6 @@ __global__ void __launch_bounds__(kThreads, 1)
           acc0 = acc1 = f2_pack(0.f, 0.f);
           // Capped scores against the fixed reference: no maximum, so the step goes through 32
           // columns at a time, the next columns loading while these are exponentiated.
-          uint64_t acc_r = acc0;
           constexpr int kPk = kBlockN / 2 / C::kPParts;  // bf16 pairs per part
           constexpr int kChunks = kPk / 16;              // of 32 columns per part
           uint32_t s[2][32];
@@ -984,9 +964,11 @@ __global__ void __launch_bounds__(kThreads, 1)
                   }
                   if (t & 1) acc1 = f2_add(acc1, f2_pack(p0, p1));
                   else acc0 = f2_add(acc0, f2_pack(p0, p1));
-                  const uint32_t pw = pack_bf16x2(p0, p1);
-                  pk[cc * 16 + t] = pw;
-                  if constexpr (kRefRest) acc_r = f2_add(acc_r, f2_pack(u2f(pw << 16), u2f(pw & 0xFFFF0000u)));
+                  if constexpr (kRefRest) {
+                    if (t & 1) top1 = fmax3(top1, p0, p1);
+                    else top0 = fmax3(top0, p0, p1);
+                  }
+                  pk[cc * 16 + t] = pack_bf16x2(p0, p1);
                 }
               };
               if (cap_far<32>(x, p.mod.cap.limit)) exponentials.template operator()<true, true>();
@@ -1010,11 +992,6 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (lane == 0) mbar_arrive(&bars->p_full[wg][h]);
           }
           if (!ok) break;
-          if constexpr (kRefRest) {
-            float a0, a1;
-            f2_unpack(acc_r, a0, a1);
-            lr += a0 + a1;
-          }
         } else {
         // S into registers. D = 64: all four 32-column loads in flight before one wait (one
         // TMEM round trip). D = 128: in two halves, the second loading while the first is
@@ -1184,7 +1161,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         continue;
       }
       if (defer) {
-        park(cur, l, kRefRest ? lr : m_ref);
+        park(cur, l, kRefRest ? fmaxf(top0, top1) : m_ref);
         continue;
       }
 
@@ -1194,7 +1171,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       FA_TRACE(24 + wg, 0);
       if (good) {
         tc_fence_after_sync();
-        const float inv_l = inv_of(kRefRest ? lr : l);
+        const float inv_l = inv_of(kRefRest ? top_rounded(l, fmaxf(top0, top1)) : l);
         if (!cur.partial) {
           // 64 columns per round through the warp's staging slice, 32 at a time from TMEM.
           uint8_t* slice = smem + C::kOOff + (wg * 4 + quad) * 4096;
@@ -1203,25 +1180,13 @@ __global__ void __launch_bounds__(kThreads, 1)
           for (int hb = 0; hb < D / 64; ++hb) {
             if (lane == 0) bulk_wait_group_read0();  // the slice's previous store read it
             __syncwarp();
-            if constexpr (kRest) {
-              if (p.mod.rest) {
-#pragma unroll
-                for (int half = 0; half < 2; ++half) {
-                  uint32_t o[32];
-                  tmem_ld32(t_o + hb * 64 + half * 32, o);
-                  tmem_ld_wait();
-                  reg_fence32(o);
-                  stage_rest(ob, half * 4, o, 32, inv_l);
-                }
-                flush_rest(cur, slice, hb * 64);
-              }
-            }
 #pragma unroll
             for (int half = 0; half < 2; ++half) {
               uint32_t o[32];
               tmem_ld32(t_o + hb * 64 + half * 32, o);
               tmem_ld_wait();
               reg_fence32(o);
+              if constexpr (kRest) write_rest(cur, o, 32, hb * 64 + half * 32, inv_l);
 #pragma unroll
               for (int t = 0; t < 4; ++t) {
                 const int ch = half * 4 + t;

@@ -59,8 +59,10 @@ constexpr int kModTree = 8;  // new tokens against a cache (fa_tree_walk.cuh)
 // on the two-tile kernel).
 // One thing is lost: against a row's maximum the weight of a key that outweighs the others is 1,
 // unrounded; against 0 it is rounded like any other. Where the output's rest is asked for
-// (kModRest), O is therefore divided by the sum of the rounded weights, not of the exact ones that
-// the LSE takes: then an outweighing key's share is 1 again.
+// (kModRest), O is therefore divided by the weights' sum with the largest one taken as rounded
+// (top_rounded), not by the sum that the LSE takes: then an outweighing key's share is 1 again.
+// (A maximum of three a pair, which the ALU takes beside the FMA's work. A second sum, over all the
+// rounded weights, is no more exact where it matters and cost a third of the kernel's time.)
 constexpr float kCapRef = 88.0f;
 constexpr float kCapBend = 0.8f;
 constexpr double kCapPoly[5] = {0.9999989943572278, -0.3332537198003981, 0.1323056561802812,
@@ -73,6 +75,11 @@ struct CapFactors {
   float bend;      // −1 / out²: 1 − tanh² = 1 + bend · (capped score)²
   float limit;     // raw scores up to this are |u| ≤ kCapBend
 };
+
+// The sum l of a row's weights with its largest one, w, rounded to bf16.
+__device__ __forceinline__ float top_rounded(float l, float w) {
+  return l + (__uint_as_float(pack_bf16x2(w, w) & 0xFFFF0000u) - w);
+}
 
 __device__ __forceinline__ uint64_t f2_splat(float x) { return f2_pack(x, x); }
 

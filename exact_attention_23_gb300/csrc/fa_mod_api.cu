@@ -396,14 +396,22 @@ int fa_fwd_mod(const void* q, const void* k, const void* v, void* o, float* lse,
   a.p.T = T;
   a.p.BH = BH;
   const int mod = fwd_mod_bits(softcap, slopes, rest);
-  // Two query tiles a CTA, as in the dense forward, where every SM gets enough such units: causal,
-  // d64, B4 H12 T4096 152 -> 148 µs and, capped, 200 -> 178, B1 H12 T16384 551 -> 498 and 732 -> 599;
-  // d128, B2 H16 T4096 (3.4 units an SM) 157 -> 147 and 177 -> 157. With documents, whose walks are
-  // uneven and shorter, 3.4 units are too few (H16 T8192 d128, five documents, capped: 115 -> 120).
+  // Two query tiles a CTA, as in the dense forward, where every SM gets enough such units (halves
+  // of units for each SM; one tile -> two tiles in µs):
+  //   plain scores 3, from causal d64 B4 H12 T1024 (1.3 units an SM) 19.3 -> 17.4, T2048 47 -> 45, d128
+  //     H16 T4096 (1.7) 79 -> 61; 1.3 units of long walks, d64 H12 T4096, 45.6 -> 47.0. With a
+  //     visibility at d = 64 5: its walks may be uneven (2.5 units, T2048: prefixes 49 -> 46, three
+  //     documents 39 -> 43; T8192 156 -> 130 and 101 -> 96), d128 as without (T2048, 1.7 units: 51 -> 42
+  //     and 39 -> 36).
+  //   capped 6 at d = 64 (H12 T4096 2.5 units 104.7 -> 104.9, T8192 192 -> 180, T16384 732 -> 610) and 3 at
+  //     d = 128 (H16 T4096 1.7 units 92 -> 80); with a visibility 8 (H16 T8192 d128, 3.4 units:
+  //     prefixes 339 -> 296, but eight documents 95 -> 105).
   // Not with a bias (d64 T4096 204 -> 223) or a cap above 60, whose in-place scores do not fit its
   // registers.
-  const bool pairs = static_cast<long long>((n_t + 1) / 2) * BH >= (visible ? 4LL : 3LL) * sms &&
-                     (mod == fa::kModOn || (mod & fa::kModRef));
+  const bool plain = (mod & ~fa::kModRest) == fa::kModOn;
+  const int halves = plain ? (visible && d == 64 ? 5 : 3) : visible ? 8 : d == 64 ? 6 : 3;
+  const bool pairs = static_cast<long long>((n_t + 1) / 2) * BH * 2 >= static_cast<long long>(halves) * sms &&
+                     (plain || (mod & fa::kModRef));
   a.p.n_units = pairs ? (n_t + 1) / 2 : n_t;
   a.p.total_units = a.p.n_units * BH;
   a.p.n_kv = n_t;
@@ -412,7 +420,7 @@ int fa_fwd_mod(const void* q, const void* k, const void* v, void* o, float* lse,
   a.p.div_splits = fa::FastDiv::make(1u);
   // Unmodified scores take their maximum before the factor, as the dense kernels; others the
   // plain factor.
-  a.p.scale_log2 = mod == fa::kModOn ? exponent_factor(static_cast<double>(scale) * kLog2e, &a.p.s_negate)
+  a.p.scale_log2 = plain ? exponent_factor(static_cast<double>(scale) * kLog2e, &a.p.s_negate)
                                      : static_cast<float>(static_cast<double>(scale) * kLog2e);
   a.p.timeout_ns = timeout_ns ? timeout_ns : 2000000000ull;
   a.p.Tk = T;

@@ -6,7 +6,8 @@ namespace fa {
 
 cudaError_t launch_fwd_mod_d128(const FwdLaunch& a, int mod) {
   switch (mod) {
-    case kModOn: return launch_fwd_mod<128, kModOn>(a);
+    case kModOn:
+    case kModOn | kModRest: return launch_fwd_mod<128, kModOn>(a);
     case kModOn | kModCap: return launch_fwd_mod<128, kModOn | kModCap>(a);
     case kModOn | kModCap | kModRef: return launch_fwd_mod<128, kModOn | kModCap | kModRef>(a);
     case kModOn | kModCap | kModRef | kModRest:

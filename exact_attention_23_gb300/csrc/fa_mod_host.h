@@ -54,6 +54,7 @@ inline int mod_bits(float softcap, const float* slopes) {
 // The forward's: a small enough cap alone takes the softmax against 0.
 inline int fwd_mod_bits(float softcap, const float* slopes, const void* rest) {
   const int mod = mod_bits(softcap, slopes);
+  if (mod == fa::kModOn) return mod | (rest ? fa::kModRest : 0);
   if (mod != (fa::kModOn | fa::kModCap) || softcap * kLog2e > fa::kCapRef) return mod;
   return mod | fa::kModRef | (rest ? fa::kModRest : 0);
 }
