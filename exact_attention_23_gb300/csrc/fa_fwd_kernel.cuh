@@ -933,7 +933,8 @@ __global__ void __launch_bounds__(kThreads, 1)
           constexpr int kPk = kBlockN / 2 / C::kPParts;  // bf16 pairs per part
           constexpr int kChunks = kPk / 16;              // of 32 columns per part
           uint32_t s[2][32];
-          tmem_ld32(t_s, s[0]);
+          float top_s[2];  // the columns' largest |S|
+          tmem_ld32_max<true>(t_s, s[0], &top_s[0]);
 #pragma unroll
           for (int h = 0; h < C::kPParts; ++h) {
             uint32_t pk[kPk];
@@ -943,8 +944,10 @@ __global__ void __launch_bounds__(kThreads, 1)
               uint32_t* x = s[ch & 1];
               tmem_ld_wait();
               reg_fence32(x);
+              asm volatile("" : "+f"(top_s[ch & 1]));  // (as reg_fence32)
+              const bool far = __any_sync(0xffffffffu, top_s[ch & 1] > p.mod.cap.limit);
               if (ch + 1 < kBlockN / 32) {
-                tmem_ld32(t_s + (ch + 1) * 32, s[(ch + 1) & 1]);
+                tmem_ld32_max<true>(t_s + (ch + 1) * 32, s[(ch + 1) & 1], &top_s[(ch + 1) & 1]);
               } else if constexpr (C::kSepP) {
                 // S_i is in registers: the tensor core may overwrite it with the next S_i.
                 tc_fence_before_sync();
@@ -971,7 +974,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                   pk[cc * 16 + t] = pack_bf16x2(p0, p1);
                 }
               };
-              if (cap_far<32>(x, p.mod.cap.limit)) exponentials.template operator()<true, true>();
+              if (far) exponentials.template operator()<true, true>();
               else if (masked) exponentials.template operator()<false, true>();
               else exponentials.template operator()<false, false>();
             }
