@@ -1001,7 +1001,38 @@ __global__ void __launch_bounds__(kThreads, 1)
         // masked and maxed (measured faster there).
         uint32_t s[kBlockN];
         float mx[8];
-        if constexpr (D == 64) {
+        if constexpr (MOD != 0) {
+          // The loads find the maximum; only a step with masked keys looks for it again.
+          float top_s[4];
+#pragma unroll
+          for (int i = 0; i < 4; ++i) tmem_ld32_max<false>(t_s + 32 * i, s + 32 * i, &top_s[i]);
+          tmem_ld_wait();
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            reg_fence32(s + 32 * i);
+            asm volatile("" : "+f"(top_s[i]));
+          }
+          if constexpr (C::kSepP) {
+            // S_i is in registers: the tensor core may overwrite it with the next S_i.
+            tc_fence_before_sync();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&bars->s_free[wg]);
+          }
+          if (masked) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              top_s[i] = -INFINITY;
+#pragma unroll
+              for (int t = 32 * i; t < 32 * i + 32; t += 2) {
+                if (t >= lim || t < vl) s[t] = __float_as_uint(-INFINITY);
+                if (t + 1 >= lim || t + 1 < vl) s[t + 1] = __float_as_uint(-INFINITY);
+                top_s[i] = fmax3(top_s[i], u2f(s[t]), u2f(s[t + 1]));
+              }
+            }
+          }
+#pragma unroll
+          for (int a = 0; a < 8; ++a) mx[a] = top_s[a & 3];
+        } else if constexpr (D == 64) {
           tmem_ld32(t_s + 0, s);
           tmem_ld32(t_s + 32, s + 32);
           tmem_ld32(t_s + 64, s + 64);
@@ -1021,7 +1052,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (masked) {
 #pragma unroll
             for (int t = 0; t < kBlockN; ++t)
-              if (t >= lim || (MOD != 0 && t < vl)) s[t] = __float_as_uint(-INFINITY);
+              if (t >= lim) s[t] = __float_as_uint(-INFINITY);
           }
 #pragma unroll
           for (int a = 0; a < 8; ++a) mx[a] = fmaxf(u2f(s[2 * a]), u2f(s[2 * a + 1]));
@@ -1040,7 +1071,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (masked) {
 #pragma unroll
             for (int t = 0; t < 64; ++t)
-              if (t >= lim || (MOD != 0 && t < vl)) s[t] = __float_as_uint(-INFINITY);
+              if (t >= lim) s[t] = __float_as_uint(-INFINITY);
           }
 #pragma unroll
           for (int a = 0; a < 8; ++a) mx[a] = fmaxf(u2f(s[2 * a]), u2f(s[2 * a + 1]));
@@ -1055,7 +1086,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (masked) {
 #pragma unroll
             for (int t = 64; t < kBlockN; ++t)
-              if (t >= lim || (MOD != 0 && t < vl)) s[t] = __float_as_uint(-INFINITY);
+              if (t >= lim) s[t] = __float_as_uint(-INFINITY);
           }
 #pragma unroll
           for (int t = 64; t < kBlockN; t += 16)
