@@ -848,11 +848,25 @@ __global__ void __launch_bounds__(Cfg1<D, (MOD & kModRef) != 0>::kThreads, 1)
         }
         uint32_t s[kC];
         const uint32_t t_s = tmem + lane_off + C::col_s(b) + half * kC;
+        // MOD: the loads find the largest score (plain), or magnitude (CAP).
+        constexpr bool kCap = (MOD & kModCap) != 0, kPlain = MOD != 0 && !kXform;
+        float top_s[kC / 32];
 #pragma unroll
-        for (int c0 = 0; c0 < kC; c0 += 32) tmem_ld32(t_s + c0, s + c0);
+        for (int c0 = 0; c0 < kC; c0 += 32) {
+          if constexpr (kCap || kPlain) tmem_ld32_max<kCap>(t_s + c0, s + c0, &top_s[c0 / 32]);
+          else tmem_ld32(t_s + c0, s + c0);
+        }
         tmem_ld_wait();
 #pragma unroll
-        for (int c0 = 0; c0 < kC; c0 += 32) reg_fence32(s + c0);
+        for (int c0 = 0; c0 < kC; c0 += 32) {
+          reg_fence32(s + c0);
+          if constexpr (kCap || kPlain) asm volatile("" : "+f"(top_s[c0 / 32]));
+        }
+        float s_max = -INFINITY;
+        if constexpr (kCap || kPlain) {
+#pragma unroll
+          for (int i = 0; i < kC / 32; ++i) s_max = fmaxf(s_max, top_s[i]);
+        }
         // S(g) is in registers: the tensor core may compute S(g + 2) into this region.
         tc_fence_before_sync();
         __syncwarp();
@@ -889,7 +903,7 @@ __global__ void __launch_bounds__(Cfg1<D, (MOD & kModRef) != 0>::kThreads, 1)
           };
           if constexpr (kXform) {
             bool far = false;
-            if constexpr ((MOD & kModCap) != 0) far = cap_far<kC>(s, p.mod.cap.limit);
+            if constexpr (kCap) far = __any_sync(0xffffffffu, s_max > p.mod.cap.limit);
             if constexpr (kRef) fused = !far && !__any_sync(0xffffffffu, masked);
             if (kRef && fused) {
               // capped where they are exponentiated, below
@@ -963,16 +977,17 @@ __global__ void __launch_bounds__(Cfg1<D, (MOD & kModRef) != 0>::kThreads, 1)
         float alpha = 1.0f;
         bool any_rescale = false;
         if constexpr (!kRef) {
-        float mx[8];
+        if (!kPlain || masked) {
+          float mx[8];
 #pragma unroll
-        for (int a = 0; a < 8; ++a) mx[a] = fmaxf(u2f(s[2 * a]), u2f(s[2 * a + 1]));
+          for (int a = 0; a < 8; ++a) mx[a] = fmaxf(u2f(s[2 * a]), u2f(s[2 * a + 1]));
 #pragma unroll
-        for (int t = 16; t < kC; t += 16)
+          for (int t = 16; t < kC; t += 16)
 #pragma unroll
-          for (int a = 0; a < 8; ++a) mx[a] = fmax3(mx[a], u2f(s[t + 2 * a]), u2f(s[t + 2 * a + 1]));
-        const float m_tile =
-            fmax3(fmax3(mx[0], mx[1], mx[2]), fmax3(mx[3], mx[4], mx[5]), fmaxf(mx[6], mx[7])) *
-            (kXform ? 1.0f : c);  // (capped or biased: already base-2 exponents)
+            for (int a = 0; a < 8; ++a) mx[a] = fmax3(mx[a], u2f(s[t + 2 * a]), u2f(s[t + 2 * a + 1]));
+          s_max = fmax3(fmax3(mx[0], mx[1], mx[2]), fmax3(mx[3], mx[4], mx[5]), fmaxf(mx[6], mx[7]));
+        }
+        const float m_tile = s_max * (kXform ? 1.0f : c);  // (capped or biased: already base-2 exponents)
 
         bool rescale = false;
         if (j == 0) {
