@@ -183,6 +183,19 @@ constexpr uint32_t kBwdFlagStarveQ = 1u;  // FA_FLAG_TEST_STARVE_Q
 // d = 128 (dQᵀ: thread = head dim c of a 64-query tile): [bh][tile][c/32][16][32 dims][4 rows],
 //   so the 32 dims of one drain warp and 16 consecutive query rows are 2 KB in one piece;
 //   dq_acc_offset_t(bh, i, n_qt, g, c) is head dim c of query rows 4·g .. 4·g+3.
+// tmem_load_cols (below), and the largest magnitude among the N (16 or 32) columns.
+template <int N>
+__device__ __forceinline__ float tmem_load_cols_absmax(uint32_t taddr, uint32_t* r) {
+  static_assert(N == 16 || N == 32, "one load");
+  float m;
+  if constexpr (N == 16) tmem_ld16_absmax(taddr, r, &m);
+  else tmem_ld32_max<true>(taddr, r, &m);
+  tmem_ld_wait();
+  if constexpr (N == 16) reg_fence16(r);
+  else reg_fence32(r);
+  asm volatile("" : "+f"(m));
+  return m;
+}
 // N consecutive TMEM columns (N = 16 or a multiple of 32) of the warp's 32 lanes into r,
 // with one wait for all of them.
 template <int N>
@@ -847,7 +860,9 @@ __global__ void __launch_bounds__(BwdCfg<D, MOD>::kThreads, 1)
       FA_TRACE(10, t);
       tc_fence_after_sync();
       uint32_t s[NC];
-      tmem_load_cols<NC>(tmem + lane_off + C::kColS + g * NC, s);
+      float top_s = 0.f;  // (CAP: the largest |S|)
+      if constexpr ((MOD & kModCap) != 0) top_s = tmem_load_cols_absmax<NC>(tmem + lane_off + C::kColS + g * NC, s);
+      else tmem_load_cols<NC>(tmem + lane_off + C::kColS + g * NC, s);
       tc_fence_before_sync();
       __syncwarp();
       if (lane == 0) mbar_arrive(&bars->s_free);
@@ -896,10 +911,20 @@ __global__ void __launch_bounds__(BwdCfg<D, MOD>::kThreads, 1)
           }
         };
         bool far = false;
-        if constexpr ((MOD & kModCap) != 0) far = cap_far<NC>(s, p.mod.cap.limit);
+        if constexpr ((MOD & kModCap) != 0) far = __any_sync(0xffffffffu, top_s > p.mod.cap.limit);
         if (far) probabilities.template operator()<true, false>();
         else if ((MOD & kModBias) != 0 && !left) probabilities.template operator()<false, false>();
         else probabilities.template operator()<false, true>();
+        // A crossed tile, too, has warps whose 32 keys every one of their queries sees (the causal
+        // diagonal: 6 of 16).
+        if (part) {
+          if (p.mod.rows) {
+            const int2 v = iv[lane & (NC - 1)];
+            part = __reduce_max_sync(0xffffffffu, v.x) > key - lane || __reduce_min_sync(0xffffffffu, v.y) <= key - lane + 31;
+          } else {
+            part = !left;
+          }
+        }
         if (part) {  // masked pairs to zero, whatever their exponentials were
 #pragma unroll
           for (int c = 0; c < NC; c += 2) {

@@ -83,17 +83,7 @@ __device__ __forceinline__ float top_rounded(float l, float w) {
 
 __device__ __forceinline__ uint64_t f2_splat(float x) { return f2_pack(x, x); }
 
-// Whether any of a warp's n raw scores lies beyond the polynomial's range (warp-uniform).
-template <int N>
-__device__ __forceinline__ bool cap_far(const uint32_t* s, float limit) {
-  float m = 0.0f;
-#pragma unroll
-  for (int t = 0; t < N; t += 2)
-    m = fmax3(m, fabsf(__uint_as_float(s[t])), fabsf(__uint_as_float(s[t + 1])));
-  return __any_sync(0xffffffffu, m > limit);
-}
-
-// A pair of raw scores to capped ones in base 2; `far` as cap_far.
+// A pair of raw scores to capped ones in base 2; FAR: some score of the warp is beyond the polynomial.
 __device__ __forceinline__ float cap_exp(float s, const CapFactors& k) {
   const float y = s * k.in_exp;
   float r;

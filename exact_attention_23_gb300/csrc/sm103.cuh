@@ -448,7 +448,18 @@ __device__ __forceinline__ void tmem_ld32(uint32_t taddr, uint32_t* r) {
       : "r"(taddr));
 }
 
-// The same, and the largest of the 32 values as fp32 (ABS: of their magnitudes; NaN passed over),
+// 16 columns, and the largest magnitude among them as fp32 (NaN passed over), found by the load.
+__device__ __forceinline__ void tmem_ld16_absmax(uint32_t taddr, uint32_t* r, float* m) {
+  asm volatile(
+      "tcgen05.ld.red.sync.aligned.32x32b.x16.max.abs.f32 "
+      "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, %16, [%17];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
+        "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]),
+        "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=f"(*m)
+      : "r"(taddr));
+}
+
+// 32 columns, and the largest of the 32 values as fp32 (ABS: of their magnitudes; NaN passed over),
 // found by the load itself.
 template <bool ABS>
 __device__ __forceinline__ void tmem_ld32_max(uint32_t taddr, uint32_t* r, float* m) {
