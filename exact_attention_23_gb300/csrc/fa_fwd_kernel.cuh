@@ -929,70 +929,92 @@ __global__ void __launch_bounds__(kThreads, 1)
         if constexpr (kRef) {
           acc0 = acc1 = f2_pack(0.f, 0.f);
           // Capped scores against the fixed reference: no maximum, so the step goes through 32
-          // columns at a time, the next columns loading while these are exponentiated.
-          constexpr int kPk = kBlockN / 2 / C::kPParts;  // bf16 pairs per part
-          constexpr int kChunks = kPk / 16;              // of 32 columns per part
+          // columns at a time, the next columns loading while these are exponentiated. The loads
+          // find the columns' largest |S|, which says whether the polynomial holds for them.
+          // A pair of keys' weights, packed (t: the pair's place among columns from which lim_c
+          // and vl_c count):
+          auto weights = [&]<bool FAR, bool MASK>(int t, uint32_t s0, uint32_t s1, int lim_c, int vl_c) {
+            float x0, x1;
+            f2_unpack(cap2<FAR>(f2_pack(u2f(s0), u2f(s1)), p.mod.cap), x0, x1);
+            float p0 = ex2_approx(x0), p1 = ex2_approx(x1);
+            if constexpr (MASK) {
+              if (2 * t >= lim_c || 2 * t < vl_c) p0 = 0.0f;
+              if (2 * t + 1 >= lim_c || 2 * t + 1 < vl_c) p1 = 0.0f;
+            }
+            if (t & 1) acc1 = f2_add(acc1, f2_pack(p0, p1));
+            else acc0 = f2_add(acc0, f2_pack(p0, p1));
+            if constexpr (kRefRest) {
+              if (t & 1) top1 = fmax3(top1, p0, p1);
+              else top0 = fmax3(top0, p0, p1);
+            }
+            return pack_bf16x2(p0, p1);
+          };
           uint32_t s[2][32];
-          float top_s[2];  // the columns' largest |S|
+          float top_s[2];
           tmem_ld32_max<true>(t_s, s[0], &top_s[0]);
+          // Two halves of the columns, kSpread: unrolled; otherwise one piece of code, and the rare
+          // far columns a loop over a copy in local memory, since a spread step that takes the
+          // other form now and then waits for instructions. (d128, B2 H16 T4096 causal: 141 µs
+          // spread, 136 not, and where 8 % of the 32s are far 288, 181; with o's rest 161, 153. d64,
+          // B1 H12 T16384: 532, 604; far ones 1600, 825; with o's rest 645 either way, T4096 B4 200, 184.)
+          constexpr bool kSpread = C::kSepP && !kRefRest && (MOD & kModTight) == 0;
+#pragma unroll (kSpread ? 2 : 1)
+          for (int h = 0; h < 2; ++h) {
+            uint32_t pk[32];
 #pragma unroll
-          for (int h = 0; h < C::kPParts; ++h) {
-            uint32_t pk[kPk];
-#pragma unroll
-            for (int cc = 0; cc < kChunks; ++cc) {
-              const int ch = h * kChunks + cc;
-              uint32_t* x = s[ch & 1];
+            for (int cc = 0; cc < 2; ++cc) {
+              uint32_t* x = s[cc];
               tmem_ld_wait();
               reg_fence32(x);
-              asm volatile("" : "+f"(top_s[ch & 1]));  // (as reg_fence32)
-              const bool far = __any_sync(0xffffffffu, top_s[ch & 1] > p.mod.cap.limit);
-              if (ch + 1 < kBlockN / 32) {
-                tmem_ld32_max<true>(t_s + (ch + 1) * 32, s[(ch + 1) & 1], &top_s[(ch + 1) & 1]);
+              asm volatile("" : "+f"(top_s[cc]));
+              const bool far = __any_sync(0xffffffffu, top_s[cc] > p.mod.cap.limit);
+              if (cc == 0 || h == 0) {
+                tmem_ld32_max<true>(t_s + (2 * h + cc + 1) * 32, s[1 - cc], &top_s[1 - cc]);
               } else if constexpr (C::kSepP) {
-                // S_i is in registers: the tensor core may overwrite it with the next S_i.
                 tc_fence_before_sync();
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&bars->s_free[wg]);
               }
-              auto exponentials = [&]<bool FAR, bool MASK>() {
+              const int lim_c = lim - (2 * h + cc) * 32, vl_c = vl - (2 * h + cc) * 32;
+              if (far && kSpread) {
 #pragma unroll
-                for (int t = 0; t < 16; ++t) {
-                  float x0, x1;
-                  f2_unpack(cap2<FAR>(f2_pack(u2f(x[2 * t]), u2f(x[2 * t + 1])), p.mod.cap), x0, x1);
-                  float p0 = ex2_approx(x0), p1 = ex2_approx(x1);
-                  if constexpr (MASK) {
-                    const int t0 = ch * 32 + 2 * t;
-                    if (t0 >= lim || t0 < vl) p0 = 0.0f;
-                    if (t0 + 1 >= lim || t0 + 1 < vl) p1 = 0.0f;
-                  }
-                  if (t & 1) acc1 = f2_add(acc1, f2_pack(p0, p1));
-                  else acc0 = f2_add(acc0, f2_pack(p0, p1));
-                  if constexpr (kRefRest) {
-                    if (t & 1) top1 = fmax3(top1, p0, p1);
-                    else top0 = fmax3(top0, p0, p1);
-                  }
-                  pk[cc * 16 + t] = pack_bf16x2(p0, p1);
+                for (int t = 0; t < 16; ++t)
+                  pk[cc * 16 + t] = weights.template operator()<true, true>(t, x[2 * t], x[2 * t + 1], lim_c, vl_c);
+              } else if (far) {
+                uint32_t copy[32];
+#pragma unroll
+                for (int t = 0; t < 32; ++t) copy[t] = x[t];
+#pragma unroll 1
+                for (int t0 = 0; t0 < 16; t0 += 4) {
+#pragma unroll
+                  for (int t = t0; t < t0 + 4; ++t)
+                    copy[t] = weights.template operator()<true, true>(t, copy[2 * t], copy[2 * t + 1], lim_c, vl_c);
                 }
-              };
-              if (far) exponentials.template operator()<true, true>();
-              else if (masked) exponentials.template operator()<false, true>();
-              else exponentials.template operator()<false, false>();
+#pragma unroll
+                for (int t = 0; t < 16; ++t) pk[cc * 16 + t] = copy[t];
+              } else if (masked) {
+#pragma unroll
+                for (int t = 0; t < 16; ++t)
+                  pk[cc * 16 + t] = weights.template operator()<false, true>(t, x[2 * t], x[2 * t + 1], lim_c, vl_c);
+              } else {
+#pragma unroll
+                for (int t = 0; t < 16; ++t)
+                  pk[cc * 16 + t] = weights.template operator()<false, false>(t, x[2 * t], x[2 * t + 1], 0, 0);
+              }
             }
             if constexpr (C::kSepP) {
-              if (gs > 0) {
-                if (!wait_w(h == C::kPParts - 1 ? &bars->pv_done[wg] : &bars->pv_part[wg][h], (gs - 1) & 1, wc)) {
-                  ok = false;
-                  break;
-                }
+              if (h == 0 && gs > 0) {
+                if (!wait_w(&bars->pv_done[wg], (gs - 1) & 1, wc)) { ok = false; break; }
                 tc_fence_after_sync();
               }
             }
-#pragma unroll
-            for (int c0 = 0; c0 < kPk; c0 += 32) tmem_st32(t_p + h * kPk + c0, pk + c0);
+            tmem_st32(t_p + h * 32, pk);
             tmem_st_wait();
-            tc_fence_before_sync();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&bars->p_full[wg][h]);
+            if (C::kPParts == 2 || h == 1) {
+              tc_fence_before_sync();
+              __syncwarp();
+              if (lane == 0) mbar_arrive(&bars->p_full[wg][C::kPParts == 2 ? h : 0]);
+            }
           }
           if (!ok) break;
         } else {

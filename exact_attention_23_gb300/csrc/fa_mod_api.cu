@@ -445,7 +445,10 @@ int fa_fwd_mod(const void* q, const void* k, const void* v, void* o, float* lse,
   a.p.mod.causal = causal != 0;
   a.grid = static_cast<unsigned>(std::min(a.p.total_units, sms));
   a.stream = static_cast<cudaStream_t>(stream);
-  const cudaError_t e = pairs ? (d == 64 ? fa::launch_fwd_mod_pairs_d64(a, mod) : fa::launch_fwd_mod_pairs_d128(a, mod))
+  // A small cap is one that scores are meant to reach (scale·q·k of unit rows has deviation 1): the
+  // step that stands far columns better (fa_fwd_kernel.cuh).
+  const int tight = d == 64 && mod == (fa::kModOn | fa::kModCap | fa::kModRef) && softcap < 25.0f ? fa::kModTight : 0;
+  const cudaError_t e = pairs ? (d == 64 ? fa::launch_fwd_mod_pairs_d64(a, mod | tight) : fa::launch_fwd_mod_pairs_d128(a, mod))
                               : (d == 64 ? fa::launch_fwd_mod_d64(a, mod) : fa::launch_fwd_mod_d128(a, mod));
   return e == cudaSuccess ? FA_OK : FA_ERR_LAUNCH;
 }
