@@ -768,7 +768,29 @@ __global__ void __launch_bounds__(kThreads, 1)
         const uint32_t ob = smem_u32(slice) + lane * 128;
         if (lane == 0) bulk_wait_group_read0();
         __syncwarp();
-        if constexpr (kRest && D == 64) write_rest(w, o, 64, 0, inv_l);
+        if constexpr (kRest && D == 64) {
+          // o's rest, through the same slice, whole rows at a time (straight from the registers,
+          // 16 bytes a row and store: B4 H12 T4096 132.8 µs against 129.3)
+#pragma unroll
+          for (int t = 0; t < 8; ++t) {
+            uint32_t lo[4];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              const float a = u2f(o[8 * t + 2 * e]) * inv_l, b = u2f(o[8 * t + 2 * e + 1]) * inv_l;
+              const uint32_t hi = pack_bf16x2(a, b);
+              lo[e] = pack_bf16x2(a - __uint_as_float(hi << 16), b - __uint_as_float(hi & 0xFFFF0000u));
+            }
+            st_shared_v4(ob + ((t ^ (lane & 7)) << 4), lo[0], lo[1], lo[2], lo[3]);
+          }
+          __syncwarp();
+          uint4* dst = reinterpret_cast<uint4*>(p.mod.rest + (static_cast<size_t>(w.bh) * p.T + w.r0) * D) + lane;
+#pragma unroll
+          for (int it = 0; it < 8; ++it) {
+            const int r = it * 4 + (lane >> 3);
+            if (w.r0 + r < p.T) dst[it * 32] = *reinterpret_cast<const uint4*>(slice + r * 128 + (((lane & 7) ^ (r & 7)) << 4));
+          }
+          __syncwarp();
+        }
 #pragma unroll
         for (int ch = 0; ch < D / 8; ++ch)
           st_shared_v4(ob + ((ch ^ (lane & 7)) << 4),

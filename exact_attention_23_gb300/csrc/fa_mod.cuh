@@ -37,7 +37,7 @@ constexpr int kModCap = 2;   // tanh cap
 constexpr int kModBias = 4;  // distance bias
 constexpr int kModRef = 16;  // with a cap alone, small enough: the softmax's reference is 0 (below)
 constexpr int kModRest = 32; // kModRef with the output's rest: weights that sum to 1 as rounded
-constexpr int kModTight = 64; // kModRef on two tiles, d = 64, without rest: scores often near the cap
+constexpr int kModTight = 64; // kModRef on two tiles, d = 64, without rest: masked or far steps are common
 constexpr int kModTree = 8;  // new tokens against a cache (fa_tree_walk.cuh)
 
 // The cap. With u = z / cap = in · s (s the raw score), the capped score in base 2 is

@@ -396,20 +396,18 @@ int fa_fwd_mod(const void* q, const void* k, const void* v, void* o, float* lse,
   a.p.T = T;
   a.p.BH = BH;
   const int mod = fwd_mod_bits(softcap, slopes, rest);
-  // Two query tiles a CTA, as in the dense forward, where every SM gets enough such units (halves
-  // of units for each SM; one tile -> two tiles in µs):
-  //   plain scores 3, from causal d64 B4 H12 T1024 (1.3 units an SM) 19.3 -> 17.4, T2048 47 -> 45, d128
-  //     H16 T4096 (1.7) 79 -> 61; 1.3 units of long walks, d64 H12 T4096, 45.6 -> 47.0. With a
-  //     visibility at d = 64 5: its walks may be uneven (2.5 units, T2048: prefixes 49 -> 46, three
-  //     documents 39 -> 43; T8192 156 -> 130 and 101 -> 96), d128 as without (T2048, 1.7 units: 51 -> 42
-  //     and 39 -> 36).
-  //   capped 6 at d = 64 (H12 T4096 2.5 units 104.7 -> 104.9, T8192 192 -> 180, T16384 732 -> 610) and 3 at
-  //     d = 128 (H16 T4096 1.7 units 92 -> 80); with a visibility 8 (H16 T8192 d128, 3.4 units:
-  //     prefixes 339 -> 296, but eight documents 95 -> 105).
-  // Not with a bias (d64 T4096 204 -> 223) or a cap above 60, whose in-place scores do not fit its
-  // registers.
+  // Two query tiles a CTA, as in the dense forward, where every SM gets 1.5 such units (one tile ->
+  // two tiles in µs; d64 H12, d128 H16 Hkv4):
+  //   plain, causal: d64 B3 T2048 (1.9 units an SM) 35 -> 31, d128 B1 T4096 (1.7) 79 -> 57; 1.3 units
+  //     of long walks, d64 B1 T4096, 42.0 -> 44.2
+  //   capped: d64 B3 T2048 46 -> 44, with eight documents and o's rest 34 -> 31, B1 T4096 (1.3) 60 -> 66;
+  //     d128 B1 T4096 91 -> 76, eight documents 41 -> 36; T8192 (3.4) with o's rest 343 -> 286, 112 -> 93
+  // or, plain with a visibility at d = 64, whose walks may be short, 2.5 of them: B4 T2048 (2.5)
+  // prefixes 49 -> 43 but eight documents 33 -> 36, B1 T8192 135 -> 123 and 53.5 -> 54.5.
+  // Not with a bias (d64 T4096 204 -> 204, d128 T8192 328 -> 448) or a cap above 60, whose in-place
+  // scores do not fit its registers.
   const bool plain = (mod & ~fa::kModRest) == fa::kModOn;
-  const int halves = plain ? (visible && d == 64 ? 5 : 3) : visible ? 8 : d == 64 ? 6 : 3;
+  const int halves = plain && visible && d == 64 ? 5 : 3;
   const bool pairs = static_cast<long long>((n_t + 1) / 2) * BH * 2 >= static_cast<long long>(halves) * sms &&
                      (plain || (mod & fa::kModRef));
   a.p.n_units = pairs ? (n_t + 1) / 2 : n_t;
@@ -445,9 +443,11 @@ int fa_fwd_mod(const void* q, const void* k, const void* v, void* o, float* lse,
   a.p.mod.causal = causal != 0;
   a.grid = static_cast<unsigned>(std::min(a.p.total_units, sms));
   a.stream = static_cast<cudaStream_t>(stream);
-  // A small cap is one that scores are meant to reach (scale·q·k of unit rows has deviation 1): the
-  // step that stands far columns better (fa_fwd_kernel.cuh).
-  const int tight = d == 64 && mod == (fa::kModOn | fa::kModCap | fa::kModRef) && softcap < 25.0f ? fa::kModTight : 0;
+  // Steps of the other forms, far or masked, are common where the cap is small (the scores of unit
+  // normal rows have deviation 1) or walks are short: the step that stands them better
+  // (fa_fwd_kernel.cuh; B4 H12 T2048, eight documents, cap 30: 48 -> 43 µs).
+  const int tight = d == 64 && mod == (fa::kModOn | fa::kModCap | fa::kModRef) && (visible || softcap < 25.0f)
+                        ? fa::kModTight : 0;
   const cudaError_t e = pairs ? (d == 64 ? fa::launch_fwd_mod_pairs_d64(a, mod | tight) : fa::launch_fwd_mod_pairs_d128(a, mod))
                               : (d == 64 ? fa::launch_fwd_mod_d64(a, mod) : fa::launch_fwd_mod_d128(a, mod));
   return e == cudaSuccess ? FA_OK : FA_ERR_LAUNCH;
