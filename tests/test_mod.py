@@ -244,6 +244,18 @@ def test_parity_with_many_heads(T, d, causal, cap, lengths, pad, prefix, with_re
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("cap,std,with_rest", [(30.0, 9.0, False), (30.0, 9.0, True), (8.0, 3.0, False),
+                                               (60.0, 40.0, True)])
+def test_parity_with_many_heads_and_far_scores(d, cap, std, with_rest):
+    """Scores on both sides of the polynomial's range, in the forms of the two-tile kernel."""
+    B, H, Hkv, T = 4, 80, 80, 260
+    q, k, v, do = _tensors(B, H, Hkv, T, d, 23 * d + int(cap), std)
+    r = ref.attention(q, k, v, ref.visible_mask(B, T, True), d ** -0.5, cap, None, do)
+    ref.check(_run(q, k, v, do, None, softcap=cap, with_rest=with_rest), r, ALL)
+
+
+@pytest.mark.gpu
 @pytest.mark.parametrize("T,lengths,pad,causal,prefix", [
     (1, (1,), 0, True, None), (31, (4, 9), 3, True, "b"), (1000, (128, 77), 0, False, None),
     (33000, (1000, 1, 2048), 129, True, "t"), (70001, (50000, 333), 7, True, "b"),
