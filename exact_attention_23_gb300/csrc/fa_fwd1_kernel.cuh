@@ -764,6 +764,9 @@ __global__ void __launch_bounds__(Cfg1<D, (MOD & kModRef) != 0>::kThreads, 1)
       if (!kTree && L >= p.total_units) continue;
       if (kTree && !sg.next(p.mod.list)) break;
       const Unit u = unit1_of<CAUSAL, GEN, MOD>(p, L, sg);
+      if constexpr (kTree) {
+        if (threadIdx.x == 0) sg.note_parts(p.mod.list);
+      }
       const int n = u.nkv[0];
       const int qt = u.qt0;
       const int q_row = qt * kBlockM + row;

@@ -76,7 +76,7 @@ struct TreeSizes {
   int R, rows_log2, row_blocks, chunk_log2, min_per;
   bool solo;
   long long entries, grid, slots;
-  size_t lse_off, bytes;
+  size_t lse_off, parts_off, bytes;
 };
 
 bool tree_sizes(int B, int H, int Hkv, int Tq, int Tmax, int d, int sms, TreeSizes* z) {
@@ -93,6 +93,7 @@ bool tree_sizes(int B, int H, int Hkv, int Tq, int Tmax, int d, int sms, TreeSiz
   if (z->entries > (1 << 28) || BHkv * R > (1LL << 40) || BHkv > (1LL << 60) / d / Tmax) return false;
   const long long chunks = (static_cast<long long>(Tmax) + (1 << z->chunk_log2) - 1) >> z->chunk_log2;
   if (z->entries * chunks > INT32_MAX - 128) return false;  // (the kernels number them with an int)
+  if (z->entries << (z->rows_log2 - 3) > INT32_MAX) return false;
   const long long most = (z->entries * chunks + z->min_per - 1) / z->min_per;
   const long long fit = static_cast<long long>(sms) *
                         (wide(z->R) ? 1 : d == 64 ? TreeCfg<64>::kCtasPerSm : TreeCfg<128>::kCtasPerSm);
@@ -100,7 +101,7 @@ bool tree_sizes(int B, int H, int Hkv, int Tq, int Tmax, int d, int sms, TreeSiz
   if (z->solo) {
     z->grid = z->entries;
     z->slots = 0;
-    z->lse_off = 0;
+    z->lse_off = z->parts_off = 0;
     z->bytes = 1;  // none needed
     return true;
   }
@@ -108,7 +109,8 @@ bool tree_sizes(int B, int H, int Hkv, int Tq, int Tmax, int d, int sms, TreeSiz
   z->slots = z->grid + z->entries;
   auto up = [](size_t x) { return (x + 255u) / 256u * 256u; };
   z->lse_off = up((static_cast<size_t>(z->slots) << z->rows_log2) * d * 4);
-  z->bytes = z->lse_off + up((static_cast<size_t>(z->slots) << z->rows_log2) * 4);
+  z->parts_off = z->lse_off + up((static_cast<size_t>(z->slots) << z->rows_log2) * 4);
+  z->bytes = z->parts_off + up(static_cast<size_t>(z->entries) * 8);
   return true;
 }
 
@@ -176,7 +178,8 @@ int fa_fwd_tree(const void* q, const void* k_cache, const void* v_cache, void* o
   a.p.slopes = slopes;
   a.p.status = status;
   a.p.timeout_ns = timeout_ns ? timeout_ns : 2000000000ull;
-  a.p.list = fa::TreeList{ctx_len, B, Hkv, Tq, Tmax, z.row_blocks, z.min_per, z.chunk_log2, z.solo ? 1 : 0};
+  a.p.list = fa::TreeList{ctx_len, B, Hkv, Tq, Tmax, z.row_blocks, z.min_per, z.chunk_log2, z.solo ? 1 : 0,
+                          z.solo ? nullptr : reinterpret_cast<int2*>(ws + z.parts_off)};
   a.p.mask = fa::TreeMask{tree, depths, fa::FastDiv::make(static_cast<uint32_t>(Tq)), tree_per_batch != 0,
                           depths_per_batch != 0};
   a.p.cap = cap;
@@ -230,10 +233,11 @@ int fa_fwd_tree(const void* q, const void* k_cache, const void* v_cache, void* o
   }
   if (e != cudaSuccess) return FA_ERR_LAUNCH;
   if (z.solo) return FA_OK;
-  const long long rows = static_cast<long long>(BHkv) * z.R;
-  const unsigned cg = static_cast<unsigned>(std::min<long long>((rows + 7) / 8, static_cast<long long>(sms) * 8));
+  const long long groups = z.entries << (z.rows_log2 - 3);  // of eight rows
+  const unsigned cg = static_cast<unsigned>(std::min<long long>(groups, static_cast<long long>(sms) * 8));
   auto* combine = d == 64 ? &fa::fa_tree_combine_kernel<64> : &fa::fa_tree_combine_kernel<128>;
-  e = fa::launch_pdl(combine, cg, 256, 0, a.stream, a.p, z.rows_log2, static_cast<int>(a.grid));
+  e = fa::launch_pdl(combine, cg, 256, 0, a.stream, a.p, z.rows_log2, static_cast<int>(a.grid),
+                     static_cast<unsigned>(groups));
   return e == cudaSuccess ? FA_OK : FA_ERR_LAUNCH;
 }
 

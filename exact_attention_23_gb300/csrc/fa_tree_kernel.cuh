@@ -153,6 +153,7 @@ __global__ void __launch_bounds__(kTreeBlock, TreeCfg<D>::kCtasPerSm)
   bool ok = true;
   while (sg.next(p.list)) {
     const int bh = sg.b * p.list.Hkv + sg.hk;
+    if (threadIdx.x == 0) sg.note_parts(p.list);
     const int ctx = p.list.ctx_len[sg.b], Tq = p.list.Tq;
     const int keys = tree_keys(p.list, ctx);
     const int r0 = sg.rb * kRows + rg * 16 + qr;    // this thread's rows: r0 and r0 + 8
@@ -445,42 +446,38 @@ __global__ void __launch_bounds__(kTreeBlock, TreeCfg<D>::kCtasPerSm)
 }
 
 // Joins the partials of the rows whose keys lie in several stretches (of `stretches`, the grid of
-// the kernel before), and writes the rows of sequences without keys. A warp a row: its lanes read
-// the partials' LSEs side by side, and kFlight partial rows are loaded before the first is used.
+// the kernel before), and writes the rows of sequences without keys. A warp a row, a block eight rows
+// of one list entry: its lanes read the partials' LSEs side by side, and kFlight partial rows are
+// loaded before the first is used.
 template <int D>
-__global__ void __launch_bounds__(256) fa_tree_combine_kernel(const TreeParams p, int rows_log2, int stretches) {
+__global__ void __launch_bounds__(256, D == 64 ? 6 : 3)
+    fa_tree_combine_kernel(const TreeParams p, int rows_log2, int stretches, unsigned groups) {
   constexpr int kV = D / 32;  // columns a lane
   constexpr int kFlight = 8;
   pdl_wait();
   pdl_launch_dependents();
   const int lane = threadIdx.x & 31;
-  const int entries = p.list.Hkv * p.list.row_blocks;
-  const long long rows = static_cast<long long>(p.list.B) * p.list.Hkv * p.R;
-  int scan_n, scan_incl;
-  const int total = tree_total(p.list, &scan_n, &scan_incl);
-  const int per = tree_per(p.list, total, stretches);
-  for (long long row = static_cast<long long>(blockIdx.x) * 8 + (threadIdx.x >> 5); row < rows;
-       row += static_cast<long long>(gridDim.x) * 8) {
-    const int bh = static_cast<int>(row / p.R);
-    const int r = static_cast<int>(row - static_cast<long long>(bh) * p.R);
-    const int b = bh / p.list.Hkv, hk = bh - b * p.list.Hkv, rb = r >> rows_log2;
-    const int chunks = tree_chunks(p.list, b);
+  const unsigned entries = static_cast<unsigned>(p.list.Hkv) * p.list.row_blocks;  // a sequence's
+  for (unsigned x0 = blockIdx.x; x0 < groups; x0 += gridDim.x) {
+    const unsigned entry = x0 >> (rows_log2 - 3);
+    const int b = static_cast<int>(entry / entries);
+    const unsigned rem = entry - b * entries, hk = rem / static_cast<unsigned>(p.list.row_blocks);
+    const int in_block = static_cast<int>((x0 << 3) & ((1u << rows_log2) - 1u)) + (threadIdx.x >> 5);
+    const int r = (static_cast<int>(rem - hk * p.list.row_blocks) << rows_log2) + in_block;
+    if (r >= p.R) continue;
+    const long long row = (static_cast<long long>(b) * p.list.Hkv + hk) * p.R + r;
+    const int ctx = p.list.ctx_len[b];
+    const int2 parts = p.list.parts[entry];
     __nv_bfloat16* dst = p.o + row * D + lane * kV;
-    if (chunks == 0) {
+    if (ctx < 0) {  // (no keys)
 #pragma unroll
       for (int x = 0; x < kV; x += 2) *reinterpret_cast<uint32_t*>(dst + x) = 0u;
       if (lane == 0) p.lse[row] = -INFINITY;
       continue;
     }
-    int before = 0;  // chunks of the sequences in front
-    for (int x = lane; x < b; x += 32) before += tree_chunks(p.list, x);
-    before = __reduce_add_sync(0xffffffffu, before);
-    const int e = hk * p.list.row_blocks + rb;
-    const int s = before * entries + e * chunks;
-    const int c0 = s / per, n = (s + chunks - 1) / per - c0 + 1;
-    if (n == 1) continue;
-    const size_t first = ((static_cast<size_t>(c0) + static_cast<size_t>(b) * entries + e) << rows_log2) +
-                         (r - (rb << rows_log2));
+    const int n = parts.y;
+    if (n <= 1 || parts.x < 0 || n > stretches - parts.x) continue;  // (one part: written already)
+    const size_t first = ((static_cast<size_t>(parts.x) + entry) << rows_log2) + in_block;
     float M = -INFINITY, L = 0.f, acc[kV];
 #pragma unroll
     for (int x = 0; x < kV; ++x) acc[x] = 0.f;

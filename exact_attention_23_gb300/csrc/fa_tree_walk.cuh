@@ -24,6 +24,7 @@ struct TreeList {
   int min_per;         // chunks a stretch has at least
   int chunk_log2;      // keys a chunk: 1 << chunk_log2
   int solo;            // CTA c takes entry c whole: no partials, no second kernel
+  int2* parts;         // [entries] the first stretch that an entry lies in, and their number
 };
 
 struct TreeMask {
@@ -76,11 +77,6 @@ __device__ __forceinline__ int tree_total(const TreeList& p, int* chunks, int* i
   return run;
 }
 
-// Chunks of a stretch, of `stretches` over a list of `total`.
-__device__ __forceinline__ int tree_per(const TreeList& p, int total, int stretches) {
-  return max((total + stretches - 1) / stretches, p.min_per);
-}
-
 // A stretch's segments in order.
 struct TreeSegments {
   struct {
@@ -89,6 +85,7 @@ struct TreeSegments {
     int start;                   // position of its first chunk
   } at;
   int pos, end;                  // next position, past the stretch's last
+  int per;                       // chunks a stretch
   // the current segment
   int b, hk, rb, entry, c0, c1;  // sequence, key head, row block, list entry, chunks [c0, c1)
   bool whole;                    // it covers its entry
@@ -104,7 +101,7 @@ struct TreeSegments {
     }
     int n, incl;
     const int total = tree_total(p, &n, &incl);
-    const int per = tree_per(p, total, gridDim.x);
+    per = max(static_cast<int>((total + gridDim.x - 1u) / gridDim.x), p.min_per);
     // (a list shorter than grid · min_per leaves later CTAs nothing)
     pos = static_cast<int>(min(static_cast<long long>(per) * blockIdx.x, static_cast<long long>(total)));
     end = min(total - pos, per) + pos;
@@ -158,6 +155,14 @@ struct TreeSegments {
     whole = c0 == 0 && c1 == at.chunks;
     pos += c1 - c0;
     return true;
+  }
+  // For fa_tree_combine_kernel: the CTA with an entry's first chunk says where its partials lie.
+  // (One thread, in every segment. The combine finding this by itself, from all the lengths, took
+  // it three more trips to memory and two divisions a row.)
+  __device__ __forceinline__ void note_parts(const TreeList& p) const {
+    if (p.solo || c0 != 0) return;
+    const int c = static_cast<int>(blockIdx.x);
+    p.parts[entry] = make_int2(c, whole ? 1 : (pos - c1 + at.chunks - 1) / per - c + 1);
   }
 };
 
