@@ -926,13 +926,40 @@ __global__ void __launch_bounds__(Cfg1<D, (MOD & kModRef) != 0>::kThreads, 1)
                 if (p.mod.mask.depths) depths = p.mod.mask.depths_of(u.last[0], Tq);
               }
               uint32_t bits[kC / 32];
+              // Rows of whole 16-byte pieces: the step's flags in one trip to memory, as words of
+              // 32 tokens, which are then shifted to where the step's keys begin (64 tokens, B8 H16
+              // Hkv4 ctx4000 d64: 28.7 µs with eight bytes a trip, as other rows take them, 27.5).
+              // Not for 128 columns a warp (d128): the code, twice as long and run once a segment,
+              // takes as long to fetch (64 tokens 41.8 -> 41.0, 16 tokens ctx16384 37.6 -> 39.1).
+              const bool pieces = kC == 64 && flags && ((reinterpret_cast<uintptr_t>(p.mod.mask.tree) | static_cast<unsigned>(Tq)) & 15u) == 0u;
+              uint32_t tw[kC / 32 + 1];
+              if (pieces) {
+                uint4 f[kC / 16 + 2];
+#pragma unroll
+                for (int i = 0; i < kC / 16 + 2; ++i) {
+                  const int t16 = (d0 >> 5) * 32 + i * 16;
+                  f[i] = t16 >= 0 && t16 < Tq ? __ldg(reinterpret_cast<const uint4*>(flags + t16)) : make_uint4(0u, 0u, 0u, 0u);
+                }
+#pragma unroll
+                for (int i = 0; i < kC / 32 + 1; ++i) {
+                  const uint32_t v[8] = {f[2 * i].x, f[2 * i].y, f[2 * i].z, f[2 * i].w,
+                                         f[2 * i + 1].x, f[2 * i + 1].y, f[2 * i + 1].z, f[2 * i + 1].w};
+                  tw[i] = 0u;
+#pragma unroll
+                  for (int e = 0; e < 8; ++e)  // four flags to four bits: byte k's bit to bit 24 + k
+                    tw[i] |= ((__vsetne4(v[e], 0u) * 0x01020408u) >> 24 & 15u) << (4 * e);
+                }
+              }
 #pragma unroll
               for (int w = 0; w < kC / 32; ++w) {
                 const int dw = d0 + w * 32;
                 // context keys, chain keys and rows of the cache: ranges
                 const int n_see = min(max(min(ctx, u.mh) - (k0 + w * 32), 0), 32);
                 uint32_t word = n_see >= 32 ? 0xFFFFFFFFu : (1u << n_see) - 1u;
-                if (flags) {
+                if (pieces) {
+                  const int n_keys = min(max(u.mh - (k0 + w * 32), 0), 32);
+                  word |= __funnelshift_r(tw[w], tw[w + 1], d0 & 31) & (n_keys >= 32 ? 0xFFFFFFFFu : (1u << n_keys) - 1u);
+                } else if (flags) {
 #pragma unroll 1
                   for (int t0 = max(0, -dw) & ~7; t0 < min(32, Tq - dw); t0 += 8) {
                     uint32_t f[8];

@@ -450,7 +450,7 @@ __global__ void __launch_bounds__(kTreeBlock, TreeCfg<D>::kCtasPerSm)
 // of one list entry: its lanes read the partials' LSEs side by side, and kFlight partial rows are
 // loaded before the first is used.
 template <int D>
-__global__ void __launch_bounds__(256, D == 64 ? 6 : 3)
+__global__ void __launch_bounds__(256, D == 64 ? 5 : 3)
     fa_tree_combine_kernel(const TreeParams p, int rows_log2, int stretches, unsigned groups) {
   constexpr int kV = D / 32;  // columns a lane
   constexpr int kFlight = 8;
