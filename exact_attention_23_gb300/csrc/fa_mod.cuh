@@ -56,7 +56,7 @@ constexpr int kModTree = 8;  // new tokens against a cache (fa_tree_walk.cuh)
 // values of ordinary size nor their inverses leave fp32's range; bf16 has the same exponents, so P
 // keeps its relative precision. The softmax is then taken against 0: no maximum, no rescaling, and no
 // dependency between the capping of a step's last score and the exponential of its first, so
-// that FMA and MUFU work overlap (B1 H12 T16384 d64 causal: 885 -> 712 µs, and 599
+// that FMA and MUFU work overlap (B1 H12 T16384 d64 causal: 885 -> 712 µs, and 532
 // on the two-tile kernel).
 // One thing is lost: against a row's maximum the weight of a key that outweighs the others is 1,
 // unrounded; against 0 it is rounded like any other. Where the output's rest is asked for

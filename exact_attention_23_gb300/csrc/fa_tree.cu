@@ -57,7 +57,7 @@ cudaError_t launch_tree_rows(const TreeLaunch& a, int rows, int mod) {
 
 // Up to 32 rows of a key head: the streaming kernel, in one block of 16 or 32 rows, so that the
 // keys are read once. More: blocks of 128 rows on the one-tile tensor-core kernel (B4 H16 Hkv4,
-// 16 tokens, 64 rows, up to 16384 keys, d = 128: 38 µs against 57 with 64 rows on mma.sync,
+// 16 tokens, 64 rows, up to 16384 keys, d = 128: 35 µs against 57 with 64 rows on mma.sync,
 // whose products then take longer than the keys' bytes).
 bool wide(int R) { return R > 32; }
 int block_rows_log2(int R) { return R <= 16 ? 4 : R <= 32 ? 5 : 7; }
@@ -66,11 +66,12 @@ int block_rows_log2(int R) { return R <= 16 ? 4 : R <= 32 ? 5 : 7; }
 constexpr int kMinPer = 2, kMinPerWide = 1;
 
 // A cache of at most this many chunks goes without stretches where its entries fit the GPU at once,
-// a CTA each: no workspace, no second kernel and launch (2 µs of the host's, 3 to 6 of the GPU's).
-// A chunk of 64 keys takes such a CTA 0.5 µs at d = 64 and 0.85 at d = 128, one of 128 keys in the wide
-// kernel 1.1: B8 H12, one token, 1000 ragged keys, d64, 11.4 µs against 12.1 (B1: 11.4 against 8.0,
-// which the host's share makes up); B8 H16 Hkv4, 64 tokens, 1300 keys 14.4 against 20.9.
-int solo_chunks(bool wide_rows, int d) { return wide_rows ? 12 : d == 64 ? 18 : 10; }
+// a CTA each: no workspace, no second kernel and launch, which are 3 µs of the host's in every call and
+// most of a short one's time. On the GPU, µs in stretches -> whole: one token, B8 H12 d64, 300 keys 9.5
+// -> 5.6, 600 10.9 -> 8.2, 1000 9.9 -> 11.4; B8 H16 Hkv4 d128, 300 keys 11.0 -> 8.4, 600 9.9 -> 12.2; the
+// wide kernel, d64, B8 64 tokens, 1300 keys 19.3 -> 14.1, d128, B4 16 tokens, 700 keys 13.0 -> 12.1, 1400
+// 14.9 -> 19.2.
+int solo_chunks(bool wide_rows, int d) { return wide_rows ? (d == 64 ? 12 : 8) : d == 64 ? 18 : 10; }
 
 struct TreeSizes {
   int R, rows_log2, row_blocks, chunk_log2, min_per;
