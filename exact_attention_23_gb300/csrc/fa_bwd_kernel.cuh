@@ -916,8 +916,10 @@ __global__ void __launch_bounds__(BwdCfg<D, MOD>::kThreads, 1)
         else if ((MOD & kModBias) != 0 && !left) probabilities.template operator()<false, false>();
         else probabilities.template operator()<false, true>();
         // A crossed tile, too, has warps whose 32 keys every one of their queries sees (the causal
-        // diagonal: 6 of 16).
-        if (part) {
+        // diagonal: 6 of 16; d128, B2 H16 T4096, plain 465 -> 454 µs, biased 496 -> 478, but capped and
+        // biased 560 -> 580).
+        constexpr bool kAsk = D == 64 || (MOD & (kModCap | kModBias)) != (kModCap | kModBias);
+        if (kAsk && part) {
           if (p.mod.rows) {
             const int2 v = iv[lane & (NC - 1)];
             part = __reduce_max_sync(0xffffffffu, v.x) > key - lane || __reduce_min_sync(0xffffffffu, v.y) <= key - lane + 31;
@@ -926,10 +928,34 @@ __global__ void __launch_bounds__(BwdCfg<D, MOD>::kThreads, 1)
           }
         }
         if (part) {  // masked pairs to zero, whatever their exponentials were
+          // Which queries see this thread's key, as bits (kBits; c: query q0 + c), or asked of each
+          // query: bits, B2 H12 T4096 d64 196 -> 193 µs, capped 239 -> 229; but d128, B2 H16 T4096,
+          // 455 -> 481, where only capped scores with documents gain (H16 Hkv4 T8192: 360 -> 352).
+          constexpr bool kBits = D == 64 || (MOD & kModCap) != 0;
+          uint32_t seen = 0u;
+          if (kBits && p.mod.rows) {
+            const int2 v = iv[lane & (NC - 1)];
+            const int lo = min(max(v.x - (key - lane), 0), 32), hi = min(max(v.y - (key - lane), 0), 32);
+            const uint32_t below = hi >= 32 ? 0xFFFFFFFFu : (1u << hi) - 1u;
+            seen = lo >= 32 ? 0u : (below >> lo) << lo;
+            // bits of keys, a lane a query -> bits of queries, a lane a key: 32 x 32 bits transposed
+#pragma unroll
+            for (int x = 16; x > 0; x >>= 1) {
+              const uint32_t m = x == 16 ? 0x0000FFFFu : x == 8 ? 0x00FF00FFu : x == 4 ? 0x0F0F0F0Fu : x == 2 ? 0x33333333u : 0x55555555u;
+              const uint32_t y = __shfl_xor_sync(0xffffffffu, seen, x);
+              seen = (lane & x) ? ((seen & ~m) | ((y >> x) & m)) : ((seen & m) | ((y << x) & ~m));
+            }
+          } else if (kBits) {
+            const int rel = key - q0;
+            seen = rel <= 0 ? 0xFFFFFFFFu : rel >= 32 ? 0u : 0xFFFFFFFFu << rel;
+          }
 #pragma unroll
           for (int c = 0; c < NC; c += 2) {
             bool out0, out1;
-            if (p.mod.rows) {
+            if (kBits) {
+              out0 = !((seen >> c) & 1u);
+              out1 = !((seen >> (c + 1)) & 1u);
+            } else if (p.mod.rows) {
               const int2 v0 = iv[c], v1 = iv[c + 1];
               out0 = key < v0.x || key >= v0.y;
               out1 = key < v1.x || key >= v1.y;
@@ -996,8 +1022,8 @@ __global__ void __launch_bounds__(BwdCfg<D, MOD>::kThreads, 1)
       FA_TRACE(15, t);
       tc_fence_after_sync();
       // dPᵀ for this warpgroup's columns (were a warpgroup to own NC = 64 columns: in two
-      // halves, to stay within the register budget)
-      constexpr int kDPB = (NC > 32) ? 32 : NC;  // columns per dPᵀ block
+      // halves, to stay within the register budget; capped at d = 64, B2 H12 T8192: 832 -> 800 µs)
+      constexpr int kDPB = (NC > 32) ? 32 : (D == 64 && (MOD & kModCap) != 0) ? 16 : NC;  // columns per dPᵀ block
 #pragma unroll
       for (int h = 0; h < NC / kDPB; ++h) {
         uint32_t dp[kDPB];
