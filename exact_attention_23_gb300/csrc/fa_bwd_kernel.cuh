@@ -630,8 +630,6 @@ __global__ void __launch_bounds__(BwdCfg<D, MOD>::kThreads, 1)
     int ti = 0;  // MOD: the step's query tile within the walk
     for (int t = 0, st = 0, ph = 0; t < n && ok; ++t) {
       if (!(ok = mbar_wait_warp_inl(&bars->q_full[st], ph, wc))) break;
-      if (t > 0 && !(ok = mbar_wait_warp_inl(&bars->s_free, (t - 1) & 1, wc))) break;
-      FA_TRACE(1, t);
       if constexpr (MOD != 0) {
         const int i = i0 + ti;
         if (++ti == wk.n_i) ti = 0;
@@ -645,6 +643,8 @@ __global__ void __launch_bounds__(BwdCfg<D, MOD>::kThreads, 1)
           __syncwarp();
         }
       }
+      if (t > 0 && !(ok = mbar_wait_warp_inl(&bars->s_free, (t - 1) & 1, wc))) break;
+      FA_TRACE(1, t);
       tc_fence_after_sync();
       if (lane == 0) {
 #pragma unroll
@@ -869,7 +869,10 @@ __global__ void __launch_bounds__(BwdCfg<D, MOD>::kThreads, 1)
       // Pᵀ = exp2(S·scale·log2e − log2e·LSE_q), zero where the key comes after the query
       // (the argument on fp32 pairs; the workspace holds −log2e·LSE)
       float pr[NC];
-      uint32_t pkm[MOD != 0 ? NC / 2 : 1];  // MOD: Pᵀ's pairs, packed as they are made
+      // MOD: Pᵀ's pairs, packed as they are made (CAP needs both, P and what dS multiplies; plain d64
+      // is faster without, B2 H12 T8192 672 -> 645 µs, but biased 700 -> 731 and d128 455 -> 479)
+      constexpr bool kTwo = MOD != 0 && !(D == 64 && MOD == kModOn);
+      uint32_t pkm[kTwo ? NC / 2 : 1];
       const float4* l4 = reinterpret_cast<const float4*>(vec + g * NC);
       const uint64_t c2 = f2_pack(p.scale_log2, p.scale_log2);
       if constexpr (MOD != 0) {
@@ -905,7 +908,7 @@ __global__ void __launch_bounds__(BwdCfg<D, MOD>::kThreads, 1)
             f2_unpack(x2, x[0], x[1]);
             pr[c] = ex2_approx(x[0]);
             pr[c + 1] = ex2_approx(x[1]);
-            pkm[c / 2] = pack_bf16x2(pr[c], pr[c + 1]);
+            if constexpr (kTwo) pkm[c / 2] = pack_bf16x2(pr[c], pr[c + 1]);
             if constexpr ((MOD & kModCap) != 0)
               f2_unpack(f2_mul(f2_pack(pr[c], pr[c + 1]), bend), pr[c], pr[c + 1]);
           }
@@ -965,11 +968,11 @@ __global__ void __launch_bounds__(BwdCfg<D, MOD>::kThreads, 1)
             }
             if (out0) {
               pr[c] = 0.f;
-              pkm[c / 2] &= 0xFFFF0000u;
+              if constexpr (kTwo) pkm[c / 2] &= 0xFFFF0000u;
             }
             if (out1) {
               pr[c + 1] = 0.f;
-              pkm[c / 2] &= 0x0000FFFFu;
+              if constexpr (kTwo) pkm[c / 2] &= 0x0000FFFFu;
             }
           }
         }
@@ -1003,7 +1006,7 @@ __global__ void __launch_bounds__(BwdCfg<D, MOD>::kThreads, 1)
       FA_TRACE(12, t);
       uint32_t pk[NC / 2];
 #pragma unroll
-      for (int c = 0; c < NC / 2; ++c) pk[c] = MOD != 0 ? pkm[c % (MOD != 0 ? NC / 2 : 1)] : pack_bf16x2(pr[2 * c], pr[2 * c + 1]);
+      for (int c = 0; c < NC / 2; ++c) pk[c] = kTwo ? pkm[c % (kTwo ? NC / 2 : 1)] : pack_bf16x2(pr[2 * c], pr[2 * c + 1]);
       tc_fence_after_sync();
       if constexpr (NC == 64) tmem_st32(tmem + lane_off + C::kColP + g * 32, pk);
       else if constexpr (NC == 32) tmem_st16(tmem + lane_off + C::kColP + g * 16, pk);
