@@ -69,10 +69,10 @@ struct BwdCfg {
   static_assert(D == 64 || D == 128, "head dim");
   static constexpr int kBQ = (D == 64) ? 128 : 64;    // query rows per tile
   // Compute warpgroups, each owning kNC query columns of a tile (32 at either head dim).
-  // (4 at d = 128, 16 columns each: 3 % slower; but where scores are capped or biased, whose
-  // arithmetic two warpgroups cannot hide, 8 to 17 % faster: B2 H16 T4096 d128 causal, cap 30,
-  // 601 -> 500 µs, with a distance bias 541 -> 499)
-  static constexpr int kCWG = (D == 64 || (MOD & (kModCap | kModBias)) != 0) ? 4 : 2;
+  // (4 at d = 128, 16 columns each: 3 to 5 % slower; but where scores are capped, whose
+  // arithmetic two warpgroups cannot hide, faster: B2 H16 T4096 d128 causal, cap 30, 430 -> 410 µs,
+  // with a distance bias too 495 -> 440; the bias alone 392 -> 395)
+  static constexpr int kCWG = (D == 64 || (MOD & kModCap) != 0) ? 4 : 2;
   static constexpr int kNC = kBQ / kCWG;
   static constexpr int kComputeWarps = 4 * kCWG;
   // Warp roles after the compute warps: 4 dQ drain warps, score issuer, gradient issuer,
@@ -443,6 +443,15 @@ __device__ __forceinline__ BwdWalk bwd_walk(const BwdParams& p, int pos, int hea
   return w;
 }
 
+// The roles' waits. MOD calls the slow path instead of having it at every wait: the steps are longer
+// there, and the instructions of all roles together no longer fit where they are fetched from without
+// a pause (B2 H16 T4096 d128: plain 452 -> 377 µs, capped 506 -> 424; d64 H12 capped 228 -> 202).
+template <int MOD>
+__device__ __forceinline__ bool bwd_wait(uint64_t* bar, uint32_t parity, const WaitCtl& w) {
+  if constexpr (MOD != 0) return mbar_wait_warp(bar, parity, w);
+  else return mbar_wait_warp_inl(bar, parity, w);
+}
+
 template <int D, bool CAUSAL, int MOD = 0>
 __global__ void __launch_bounds__(BwdCfg<D, MOD>::kThreads, 1)
     fa_bwd_main_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
@@ -523,8 +532,8 @@ __global__ void __launch_bounds__(BwdCfg<D, MOD>::kThreads, 1)
   // core when TMEM is released.
   auto teardown = [&]() {
     if (warp == C::kScoreWarp) {
-      mbar_wait_warp_inl(&bars->score_done, 0, drain_wc);
-      mbar_wait_warp_inl(&bars->grad_done, 0, drain_wc);
+      bwd_wait<MOD>(&bars->score_done, 0, drain_wc);
+      bwd_wait<MOD>(&bars->grad_done, 0, drain_wc);
     }
     tc_fence_before_sync();
     __syncthreads();
@@ -556,7 +565,7 @@ __global__ void __launch_bounds__(BwdCfg<D, MOD>::kThreads, 1)
     const bool starve = (p.flags & kBwdFlagStarveQ) != 0u;
     int ti = 0, hg = 0;  // MOD: the step's query tile within the walk, its head within the group
     for (int t = 0, st = 0, ph = 0; t < n && !starve; ++t) {
-      if (t >= NS && !mbar_wait_warp_inl(&bars->q_empty[st], ph ^ 1, wc)) break;
+      if (t >= NS && !bwd_wait<MOD>(&bars->q_empty[st], ph ^ 1, wc)) break;
       FA_TRACE(30, t);
       int i = i0 + t, bq = bh;  // query tile and (b·h) of this step
       if constexpr (MOD != 0) {
@@ -601,15 +610,15 @@ __global__ void __launch_bounds__(BwdCfg<D, MOD>::kThreads, 1)
       if (++st == NS) { st = 0; ph ^= 1; }
     }
     // No copy may still be in flight when the CTA exits.
-    mbar_wait_warp_inl(&bars->kv_full, 0, drain_wc);
+    bwd_wait<MOD>(&bars->kv_full, 0, drain_wc);
 #pragma unroll
     for (int s = 0; s < NS; ++s)
-      if (last_t[s] >= 0) mbar_wait_warp_inl(&bars->q_full[s], (last_t[s] / NS) & 1, drain_wc);
+      if (last_t[s] >= 0) bwd_wait<MOD>(&bars->q_full[s], (last_t[s] / NS) & 1, drain_wc);
   } else if (warp == C::kScoreWarp) {
     // ---------------------------------------------------------------- score issuer
     constexpr uint32_t kIdS = idesc_bf16(128, C::kBQ, false);  // Sᵀ = K·Qᵀ, dPᵀ = V·dOᵀ
     const uint32_t k_s = sbase + C::kK, v_s = sbase + C::kV;
-    bool ok = mbar_wait_warp_inl(&bars->kv_full, 0, wc);
+    bool ok = bwd_wait<MOD>(&bars->kv_full, 0, wc);
     // MOD: rows behind the last one in use (padding) may hold anything. Their P and dS are 0,
     // but 0 · NaN must not reach a product: their K, V, Q and dO rows are zeroed here, before the
     // first product that reads them (every other reader comes after it).
@@ -629,7 +638,7 @@ __global__ void __launch_bounds__(BwdCfg<D, MOD>::kThreads, 1)
     }
     int ti = 0;  // MOD: the step's query tile within the walk
     for (int t = 0, st = 0, ph = 0; t < n && ok; ++t) {
-      if (!(ok = mbar_wait_warp_inl(&bars->q_full[st], ph, wc))) break;
+      if (!(ok = bwd_wait<MOD>(&bars->q_full[st], ph, wc))) break;
       if constexpr (MOD != 0) {
         const int i = i0 + ti;
         if (++ti == wk.n_i) ti = 0;
@@ -643,7 +652,7 @@ __global__ void __launch_bounds__(BwdCfg<D, MOD>::kThreads, 1)
           __syncwarp();
         }
       }
-      if (t > 0 && !(ok = mbar_wait_warp_inl(&bars->s_free, (t - 1) & 1, wc))) break;
+      if (t > 0 && !(ok = bwd_wait<MOD>(&bars->s_free, (t - 1) & 1, wc))) break;
       FA_TRACE(1, t);
       tc_fence_after_sync();
       if (lane == 0) {
@@ -654,7 +663,7 @@ __global__ void __launch_bounds__(BwdCfg<D, MOD>::kThreads, 1)
         mma_commit(&bars->s_full);
       }
       __syncwarp();
-      if (t > 0 && !(ok = mbar_wait_warp_inl(&bars->dp_free, (t - 1) & 1, wc))) break;
+      if (t > 0 && !(ok = bwd_wait<MOD>(&bars->dp_free, (t - 1) & 1, wc))) break;
       FA_TRACE(2, t);
       tc_fence_after_sync();
       if (lane == 0) {
@@ -681,7 +690,7 @@ __global__ void __launch_bounds__(BwdCfg<D, MOD>::kThreads, 1)
     bool ok = true;
     for (int t = 0, st = 0; t < n && ok; ++t) {
       // dV += Pᵀ·dO_i (Pᵀ from TMEM)
-      if (!(ok = mbar_wait_warp_inl(&bars->p_full, t & 1, wc))) break;
+      if (!(ok = bwd_wait<MOD>(&bars->p_full, t & 1, wc))) break;
       FA_TRACE(3, t);
       tc_fence_after_sync();
       if (lane == 0) {
@@ -695,8 +704,8 @@ __global__ void __launch_bounds__(BwdCfg<D, MOD>::kThreads, 1)
       // dK += dSᵀ·Q_i, then dQ_i = dS·K_j (d = 64) or dQ_iᵀ = K_jᵀ·dSᵀ (d = 128)
       const int b = t & 1;
       const uint32_t ds_s = sbase + C::kDS + b * C::kDSBytes;
-      if (!(ok = mbar_wait_warp_inl(&bars->ds_full[b], (t >> 1) & 1, wc))) break;
-      if (!C::kSplitQ && t > 0 && !(ok = mbar_wait_warp_inl(&bars->dq_free, (t - 1) & 1, wc))) break;
+      if (!(ok = bwd_wait<MOD>(&bars->ds_full[b], (t >> 1) & 1, wc))) break;
+      if (!C::kSplitQ && t > 0 && !(ok = bwd_wait<MOD>(&bars->dq_free, (t - 1) & 1, wc))) break;
       FA_TRACE(4, t);
       tc_fence_after_sync();
       if (lane == 0) {
@@ -729,8 +738,8 @@ __global__ void __launch_bounds__(BwdCfg<D, MOD>::kThreads, 1)
     for (int t = 0; t < n && ok; ++t) {
       const int b = t & 1;
       const uint32_t ds_s = sbase + C::kDS + b * C::kDSBytes;
-      if (!(ok = mbar_wait_warp_inl(&bars->ds_full[b], (t >> 1) & 1, wc))) break;
-      if (t > 0 && !(ok = mbar_wait_warp_inl(&bars->dq_free, (t - 1) & 1, wc))) break;
+      if (!(ok = bwd_wait<MOD>(&bars->ds_full[b], (t >> 1) & 1, wc))) break;
+      if (t > 0 && !(ok = bwd_wait<MOD>(&bars->dq_free, (t - 1) & 1, wc))) break;
       tc_fence_after_sync();
       if (lane == 0) {
 #pragma unroll
@@ -766,7 +775,7 @@ __global__ void __launch_bounds__(BwdCfg<D, MOD>::kThreads, 1)
     int nchunk = 0;
     int ti = 0, hg = 0;  // MOD: as in the producer
     for (; t < n; ++t) {
-      if (!(ok = mbar_wait_warp_inl(&bars->dq_full, t & 1, wc))) break;
+      if (!(ok = bwd_wait<MOD>(&bars->dq_full, t & 1, wc))) break;
       FA_TRACE(20, t);
       int it = i0 + t, bq = bh;
       if constexpr (MOD != 0) {
@@ -855,8 +864,8 @@ __global__ void __launch_bounds__(BwdCfg<D, MOD>::kThreads, 1)
         if (ti == 0) nslope = __ldg(p.mod.slopes + wk.h0 + hg) * -1.4426950408889634f;
       }
       const float* vec = reinterpret_cast<const float*>(sm + C::kVec + st * C::kVecBytes);
-      if (!(ok = mbar_wait_warp_inl(&bars->q_full[st], ph, wc))) break;
-      if (!(ok = mbar_wait_warp_inl(&bars->s_full, t & 1, wc))) break;
+      if (!(ok = bwd_wait<MOD>(&bars->q_full[st], ph, wc))) break;
+      if (!(ok = bwd_wait<MOD>(&bars->s_full, t & 1, wc))) break;
       FA_TRACE(10, t);
       tc_fence_after_sync();
       uint32_t s[NC];
@@ -870,7 +879,7 @@ __global__ void __launch_bounds__(BwdCfg<D, MOD>::kThreads, 1)
       // (the argument on fp32 pairs; the workspace holds −log2e·LSE)
       float pr[NC];
       // MOD: Pᵀ's pairs, packed as they are made (CAP needs both, P and what dS multiplies; plain d64
-      // is faster without, B2 H12 T8192 672 -> 645 µs, but biased 700 -> 731 and d128 455 -> 479)
+      // is faster without, B2 H12 T4096 182 -> 178 µs, but d128, B2 H16 T4096, 377 -> 387)
       constexpr bool kTwo = MOD != 0 && !(D == 64 && MOD == kModOn);
       uint32_t pkm[kTwo ? NC / 2 : 1];
       const float4* l4 = reinterpret_cast<const float4*>(vec + g * NC);
@@ -919,10 +928,8 @@ __global__ void __launch_bounds__(BwdCfg<D, MOD>::kThreads, 1)
         else if ((MOD & kModBias) != 0 && !left) probabilities.template operator()<false, false>();
         else probabilities.template operator()<false, true>();
         // A crossed tile, too, has warps whose 32 keys every one of their queries sees (the causal
-        // diagonal: 6 of 16; d128, B2 H16 T4096, plain 465 -> 454 µs, biased 496 -> 478, but capped and
-        // biased 560 -> 580).
-        constexpr bool kAsk = D == 64 || (MOD & (kModCap | kModBias)) != (kModCap | kModBias);
-        if (kAsk && part) {
+        // diagonal: 6 of 16).
+        if (part) {
           if (p.mod.rows) {
             const int2 v = iv[lane & (NC - 1)];
             part = __reduce_max_sync(0xffffffffu, v.x) > key - lane || __reduce_min_sync(0xffffffffu, v.y) <= key - lane + 31;
@@ -932,9 +939,9 @@ __global__ void __launch_bounds__(BwdCfg<D, MOD>::kThreads, 1)
         }
         if (part) {  // masked pairs to zero, whatever their exponentials were
           // Which queries see this thread's key, as bits (kBits; c: query q0 + c), or asked of each
-          // query: bits, B2 H12 T4096 d64 196 -> 193 µs, capped 239 -> 229; but d128, B2 H16 T4096,
-          // 455 -> 481, where only capped scores with documents gain (H16 Hkv4 T8192: 360 -> 352).
-          constexpr bool kBits = D == 64 || (MOD & kModCap) != 0;
+          // query: bits, B2 H12 T4096 d64 182 -> 178 µs, capped 216 -> 202; but d128, B2 H16 T4096 capped,
+          // 412 -> 423.
+          constexpr bool kBits = D == 64;
           uint32_t seen = 0u;
           if (kBits && p.mod.rows) {
             const int2 v = iv[lane & (NC - 1)];
@@ -1002,7 +1009,7 @@ __global__ void __launch_bounds__(BwdCfg<D, MOD>::kThreads, 1)
       }
       }
       FA_TRACE(11, t);
-      if (t >= 1 && !(ok = mbar_wait_warp_inl(&bars->p_free, (t - 1) & 1, wc))) break;
+      if (t >= 1 && !(ok = bwd_wait<MOD>(&bars->p_free, (t - 1) & 1, wc))) break;
       FA_TRACE(12, t);
       uint32_t pk[NC / 2];
 #pragma unroll
@@ -1019,13 +1026,13 @@ __global__ void __launch_bounds__(BwdCfg<D, MOD>::kThreads, 1)
       // dSᵀ = Pᵀ ∘ (dPᵀ − D_q), into shared-memory buffer t mod 2
       const int b = t & 1;
       const uint32_t ds_box = sbase + C::kDS + b * C::kDSBytes + ds_box_idx * C::kBox;
-      if (!(ok = mbar_wait_warp_inl(&bars->dp_full, t & 1, wc))) break;
+      if (!(ok = bwd_wait<MOD>(&bars->dp_full, t & 1, wc))) break;
       FA_TRACE(14, t);
-      if (t >= 2 && !(ok = mbar_wait_warp_inl(&bars->ds_free[b], ((t >> 1) - 1) & 1, wc))) break;
+      if (t >= 2 && !(ok = bwd_wait<MOD>(&bars->ds_free[b], ((t >> 1) - 1) & 1, wc))) break;
       FA_TRACE(15, t);
       tc_fence_after_sync();
       // dPᵀ for this warpgroup's columns (were a warpgroup to own NC = 64 columns: in two
-      // halves, to stay within the register budget; capped at d = 64, B2 H12 T8192: 832 -> 800 µs)
+      // halves, to stay within the register budget; capped at d = 64, B2 H12 T4096: 208 -> 202 µs)
       constexpr int kDPB = (NC > 32) ? 32 : (D == 64 && (MOD & kModCap) != 0) ? 16 : NC;  // columns per dPᵀ block
 #pragma unroll
       for (int h = 0; h < NC / kDPB; ++h) {
@@ -1062,7 +1069,7 @@ __global__ void __launch_bounds__(BwdCfg<D, MOD>::kThreads, 1)
     }
     // ---- epilogue: warpgroup 0 writes dV_j, warpgroup 1 writes scale·dK_j (32 columns at
     // a time)
-    bool done = ok && mbar_wait_warp_inl(&bars->grad_done, 0, wc) && !bars->abort;
+    bool done = ok && bwd_wait<MOD>(&bars->grad_done, 0, wc) && !bars->abort;
     done = __shfl_sync(0xffffffffu, done ? 1u : 0u, 0) != 0u;  // warp-uniform (TMEM loads)
     const int key = j * 128 + r;
     tc_fence_after_sync();

@@ -291,9 +291,9 @@ bool mod_sizes(int B, int H, int Hkv, int T, int d) {
 
 // Parts that a key head's query heads are cut into in the backward (a divisor of them): the fewest
 // that give at least kMinCtas CTAs, three for each of a GB300's SMs, so that their unequal walks can
-// be shared out (H16 Hkv4 T8192 d128 capped, five documents: 609 µs with the 256 CTAs of whole
-// groups, 436 in two parts, 459 in four; B2 H16 Hkv4 T4096 causal, whose walks are even: 641, 620 and
-// 640). Independent of the device, so that a workspace fits wherever it is made.
+// be shared out (H16 Hkv4 T8192 d128 capped, five documents: 559 µs with the 256 CTAs of whole
+// groups, 475 in two parts, 519 in four; B2 T4096 causal, whose walks are even: 403, 411 and
+// 455). Independent of the device, so that a workspace fits wherever it is made.
 int bwd_parts(int B, int H, int Hkv, int T) {
   constexpr long long kMinCtas = 456;
   const int group = H / Hkv;
@@ -520,7 +520,7 @@ int fa_bwd_mod(const void* q, const void* k, const void* v, const void* o, const
   a.p.n_kt = n_t;
   // Heads whose units go out together, the longest walks first: with few CTAs all of them, since
   // a long walk that starts late is the call's tail (H16 Hkv4 T8192 d128 capped, five
-  // documents: 520 -> 436 µs); otherwise as many as keep their Q and dO (bf16) and dQ accumulator (fp32) in half
+  // documents: 496 -> 476 µs); otherwise as many as keep their Q and dO (bf16) and dQ accumulator (fp32) in half
   // the L2, 64 MB.
   const long long per_head = 8LL * T_pad * d * (H / Hkv / parts);
   const long long in_l2 = std::max<long long>(1, (64LL << 20) / per_head);
