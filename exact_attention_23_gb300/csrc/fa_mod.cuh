@@ -36,7 +36,7 @@ constexpr int kModOn = 1;    // modified scores with row intervals
 constexpr int kModCap = 2;   // tanh cap
 constexpr int kModBias = 4;  // distance bias
 constexpr int kModRef = 16;  // with a cap alone, small enough: the softmax's reference is 0 (below)
-constexpr int kModRest = 32; // kModRef with the output's rest: weights that sum to 1 as rounded
+constexpr int kModRest = 32; // o's rest is written (two tiles; one tile: kModRef only, others look at the pointer)
 constexpr int kModTight = 64; // kModRef on two tiles, d = 64, without rest: masked or far steps are common
 constexpr int kModTree = 8;  // new tokens against a cache (fa_tree_walk.cuh)
 
