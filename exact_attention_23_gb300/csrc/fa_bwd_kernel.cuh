@@ -889,7 +889,7 @@ __global__ void __launch_bounds__(BwdCfg<D, MOD>::kThreads, 1)
         const int q0 = i * C::kBQ + g * NC, key = j * 128 + r;
         bool part;  // some row of the stage does not see every key of the tile
         if (p.mod.rows) part = bars->whole[st] == 0u;
-        else part = p.mod.causal && j * 128 + 127 > i * C::kBQ;
+        else part = j * 128 + 127 >= (p.mod.causal ? min(i * C::kBQ + 1, p.T) : p.T);
         const bool left = j * 128 + qd * 32 + 31 <= q0;
         const float dist0 = static_cast<float>(q0 - key);
         const float base = nslope * dist0;
@@ -934,7 +934,7 @@ __global__ void __launch_bounds__(BwdCfg<D, MOD>::kThreads, 1)
             const int2 v = iv[lane & (NC - 1)];
             part = __reduce_max_sync(0xffffffffu, v.x) > key - lane || __reduce_min_sync(0xffffffffu, v.y) <= key - lane + 31;
           } else {
-            part = !left;
+            part = (p.mod.causal && !left) || key - lane + 31 >= p.T;
           }
         }
         if (part) {  // masked pairs to zero, whatever their exponentials were
@@ -943,6 +943,9 @@ __global__ void __launch_bounds__(BwdCfg<D, MOD>::kThreads, 1)
           // 412 -> 423.
           constexpr bool kBits = D == 64;
           uint32_t seen = 0u;
+          // without rows: queries from q0 + rel on see the key; none sees one behind the end, whose
+          // score of 0 (its row is loaded as zeros) may be far above every other of a query
+          const int rel = key >= p.T ? NC : p.mod.causal ? key - q0 : 0;
           if (kBits && p.mod.rows) {
             const int2 v = iv[lane & (NC - 1)];
             const int lo = min(max(v.x - (key - lane), 0), 32), hi = min(max(v.y - (key - lane), 0), 32);
@@ -956,7 +959,6 @@ __global__ void __launch_bounds__(BwdCfg<D, MOD>::kThreads, 1)
               seen = (lane & x) ? ((seen & ~m) | ((y >> x) & m)) : ((seen & m) | ((y << x) & ~m));
             }
           } else if (kBits) {
-            const int rel = key - q0;
             seen = rel <= 0 ? 0xFFFFFFFFu : rel >= 32 ? 0u : 0xFFFFFFFFu << rel;
           }
 #pragma unroll
@@ -970,8 +972,8 @@ __global__ void __launch_bounds__(BwdCfg<D, MOD>::kThreads, 1)
               out0 = key < v0.x || key >= v0.y;
               out1 = key < v1.x || key >= v1.y;
             } else {
-              out0 = key > q0 + c;
-              out1 = key > q0 + c + 1;
+              out0 = rel > c;
+              out1 = rel > c + 1;
             }
             if (out0) {
               pr[c] = 0.f;
