@@ -5,9 +5,9 @@
 
 namespace fa {
 
-template <int D, bool CAUSAL>
+template <int D, bool CAUSAL, bool RAGGED = false>
 static cudaError_t launch_bwd(const BwdLaunch& a) {
-  auto* fn = &fa_bwd_main_kernel<D, CAUSAL>;
+  auto* fn = &fa_bwd_main_kernel<D, CAUSAL, 0, RAGGED>;
   const int smem = BwdCfg<D>::kSmemBytes;
   // The shared-memory opt-in is a per-device attribute: set it once per device.
   static std::atomic<uint64_t> done[kMaxDevices / 64 + 1];
@@ -32,7 +32,8 @@ static cudaError_t launch_bwd(const BwdLaunch& a) {
 }
 
 cudaError_t launch_bwd_d64(const BwdLaunch& a, bool causal) {
-  return causal ? launch_bwd<64, true>(a) : launch_bwd<64, false>(a);
+  if (causal) return launch_bwd<64, true>(a);
+  return a.p.T % 128 != 0 ? launch_bwd<64, false, true>(a) : launch_bwd<64, false>(a);
 }
 
 }  // namespace fa

@@ -452,7 +452,11 @@ __device__ __forceinline__ bool bwd_wait(uint64_t* bar, uint32_t parity, const W
   else return mbar_wait_warp_inl(bar, parity, w);
 }
 
-template <int D, bool CAUSAL, int MOD = 0>
+// RAGGED (dense, not causal): T is no multiple of 128, and the last key tile's keys behind the end are
+// masked: their rows are loaded as zeros, and a score of 0 may be so far above every other of a query
+// that its P is infinite. (Causal masks them with the diagonal, MOD with the intervals' ends. A kernel
+// of its own, since the branch costs the step 3 %, B2 H16 T4000 d128 641 -> 664 µs; B2 H12 d64 346 -> 349.)
+template <int D, bool CAUSAL, int MOD = 0, bool RAGGED = false>
 __global__ void __launch_bounds__(BwdCfg<D, MOD>::kThreads, 1)
     fa_bwd_main_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
                        const __grid_constant__ CUtensorMap tm_v, const __grid_constant__ CUtensorMap tm_do,
@@ -1008,6 +1012,10 @@ __global__ void __launch_bounds__(BwdCfg<D, MOD>::kThreads, 1)
 #pragma unroll
         for (int c = 0; c < NC; ++c)
           if (rel > c) pr[c] = 0.f;
+      }
+      if (RAGGED && j * 128 + r >= p.T) {
+#pragma unroll
+        for (int c = 0; c < NC; ++c) pr[c] = 0.f;
       }
       }
       FA_TRACE(11, t);

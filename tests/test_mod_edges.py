@@ -37,6 +37,17 @@ def test_far_below_zero_without_visible(T, d, cap, slope):
 
 
 @pytest.mark.parametrize("d", [64, 128])
+def test_far_below_zero_in_the_dense_backward(d):
+    for T in (1, 129, 300):
+        q, k, v, do = _opposed(1, 2, 2, T, d, 5 * T + d)
+        r = ref.attention(q, k, v, ref.visible_mask(1, T, False), d ** -0.5, do=do)
+        t = [x.cuda() for x in (q, k, v, do)]
+        o, lse = fa.fwd(*t[:3], causal=False)
+        got = dict(zip(("dq", "dk", "dv"), fa.bwd(*t[:3], o, lse, t[3], causal=False)))
+        ref.check(got, r, ("dq", "dk", "dv"), f"T {T}")
+
+
+@pytest.mark.parametrize("d", [64, 128])
 def test_distances_that_raise_scores(d):
     """A negative slope: keys behind the end would be the farthest and outweigh all others."""
     B, H, Hkv, T = 1, 2, 1, 130
