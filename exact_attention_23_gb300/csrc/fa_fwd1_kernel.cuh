@@ -518,7 +518,7 @@ __global__ void __launch_bounds__(Cfg1<D, (MOD & kModRef) != 0>::kThreads, 1)
         // The parts of a row share O and the reference: they post their sums, meet, and each
         // writes its columns.
         const int par = ne & 1;
-        // (m: the largest weight, kRefRest)
+        // (m: the largest weight)
         float2* xs = reinterpret_cast<float2*>(smem + C::kXchOff) + (par * H) * kBlockM;
         xs[half * kBlockM + row] = make_float2(l, m);
         __threadfence_block();
@@ -538,9 +538,9 @@ __global__ void __launch_bounds__(Cfg1<D, (MOD & kModRef) != 0>::kThreads, 1)
         for (int h = 0; h < H; ++h) {
           const float2 x = xs[h * kBlockM + row];
           L += x.x;
-          if constexpr (kRefRest) top = fmaxf(top, x.y);
+          top = fmaxf(top, x.y);
         }
-        const float inv_l = !(L > 0.0f) ? 0.0f : 1.0f / (kRefRest ? top_rounded(L, top) : L);
+        const float inv_l = !(L > 0.0f) ? 0.0f : 1.0f / top_rounded(L, top);
         uint32_t o[kOutCols];
         static_assert(kOutCols == 16 || kOutCols % 32 == 0, "output columns");
         if constexpr (kOutCols == 16) {
@@ -814,7 +814,7 @@ __global__ void __launch_bounds__(Cfg1<D, (MOD & kModRef) != 0>::kThreads, 1)
       }
       // reference max (base-2 scaled units) shared by O_h and l
       float m_ref = kRef ? 0.0f : -INFINITY;
-      float l = 0.0f, top0 = 0.0f, top1 = 0.0f;  // (kRefRest: the largest weight of either parity)
+      float l = 0.0f, top = 0.0f, raw_top = -INFINITY;  // (kRef: for the largest weight)
       // the tile's K tiles (GEN: its walk, the next position fetched a step ahead)
       Walk w{nullptr, 0};
       int nx = 0;
@@ -853,10 +853,11 @@ __global__ void __launch_bounds__(Cfg1<D, (MOD & kModRef) != 0>::kThreads, 1)
         const uint32_t t_s = tmem + lane_off + C::col_s(b) + half * kC;
         // MOD: the loads find the largest score (plain), or magnitude (CAP).
         constexpr bool kCap = (MOD & kModCap) != 0, kPlain = MOD != 0 && !kXform;
-        float top_s[kC / 32];
+        float top_s[kC / 32], max_s[kC / 32];
 #pragma unroll
         for (int c0 = 0; c0 < kC; c0 += 32) {
-          if constexpr (kCap || kPlain) tmem_ld32_max<kCap>(t_s + c0, s + c0, &top_s[c0 / 32]);
+          if constexpr (kRef) tmem_ld32_absmax_max(t_s + c0, s + c0, &top_s[c0 / 32], &max_s[c0 / 32]);
+          else if constexpr (kCap || kPlain) tmem_ld32_max<kCap>(t_s + c0, s + c0, &top_s[c0 / 32]);
           else tmem_ld32(t_s + c0, s + c0);
         }
         tmem_ld_wait();
@@ -864,6 +865,7 @@ __global__ void __launch_bounds__(Cfg1<D, (MOD & kModRef) != 0>::kThreads, 1)
         for (int c0 = 0; c0 < kC; c0 += 32) {
           reg_fence32(s + c0);
           if constexpr (kCap || kPlain) asm volatile("" : "+f"(top_s[c0 / 32]));
+          if constexpr (kRef) asm volatile("" : "+f"(max_s[c0 / 32]));
         }
         float s_max = -INFINITY;
         if constexpr (kCap || kPlain) {
@@ -1054,15 +1056,19 @@ __global__ void __launch_bounds__(Cfg1<D, (MOD & kModRef) != 0>::kThreads, 1)
             const float p1 = ex2_approx(x1);
             if (t & 1) acc1 = f2_add(acc1, f2_pack(p0, p1));
             else acc0 = f2_add(acc0, f2_pack(p0, p1));
-            if constexpr (kRefRest) {
-              if (t & 1) top1 = fmax3(top1, p0, p1);
-              else top0 = fmax3(top0, p0, p1);
-            }
+            if constexpr (kRef && !FUSED) top = fmax3(top, p0, p1);
             pk[t] = pack_bf16x2(p0, p1);
           }
         };
-        if (kRef && fused) exponentials.template operator()<kRef>();
-        else exponentials.template operator()<false>();
+        if (kRef && fused) {
+          if constexpr (kRef) {
+#pragma unroll
+            for (int i = 0; i < kC / 32; ++i) raw_top = fmaxf(raw_top, max_s[i]);
+          }
+          exponentials.template operator()<kRef>();
+        } else {
+          exponentials.template operator()<false>();
+        }
         FA1_TRACE(42, j);
         if (any_rescale) {
           // Rows whose max jumped bring their O_h to the new reference before this step's
@@ -1129,7 +1135,7 @@ __global__ void __launch_bounds__(Cfg1<D, (MOD & kModRef) != 0>::kThreads, 1)
         fail_rows(cur);
         continue;
       }
-      *prec = make_float4(l, kRefRest ? fmaxf(top0, top1) : m_ref, __int_as_float(cur.r0), __int_as_float(kTree ? (u.split < 0 ? u.bh : -1 - u.split)
+      *prec = make_float4(l, kRef ? top_weight(top, raw_top, p.mod.cap) : m_ref, __int_as_float(cur.r0), __int_as_float(kTree ? (u.split < 0 ? u.bh : -1 - u.split)
                                                                                     : cur.bh + p.BH * u.split));
       pend = true;
     }

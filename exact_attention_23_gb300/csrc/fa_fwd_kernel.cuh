@@ -762,7 +762,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     // slice (one unit back) must have read it out first.
     // (kRef: the reference is 0, and m carries the largest weight)
     auto store_o = [&](const RowOut& w, const uint32_t* o, float l, float m) {
-      const float inv_l = inv_of(kRefRest ? top_rounded(l, m) : l);
+      const float inv_l = inv_of(kRef ? top_rounded(l, m) : l);
       if (D == 64 && !w.partial) {
         uint8_t* slice = smem + C::kOOff + (wg * 4 + quad) * 4096;
         const uint32_t ob = smem_u32(slice) + lane * 128;
@@ -900,7 +900,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 
       // reference max (base-2 scaled units) shared by O and l
       float m_ref = kRef ? 0.0f : -INFINITY;
-      float l = 0.0f, top0 = 0.0f, top1 = 0.0f;  // (kRefRest: the largest weight of either parity)
+      float l = 0.0f, top = 0.0f, raw_top = -INFINITY;
       int vlo = 0, vhi = 0;  // MOD: this row's visible keys [lo, hi)
       if constexpr (MOD != 0) {
         const int b = static_cast<int>(p.mod.div_h.div(static_cast<uint32_t>(u.bh)));
@@ -953,6 +953,10 @@ __global__ void __launch_bounds__(kThreads, 1)
           // Capped scores against the fixed reference: no maximum, so the step goes through 32
           // columns at a time, the next columns loading while these are exponentiated. The loads
           // find the columns' largest |S|, which says whether the polynomial holds for them.
+          // The row's largest score, for its largest weight: found by a second load at d = 64 (B1 H12
+          // T16384: 532 µs without it, 575 so, 597 by the ALU), by the ALU at d = 128 (B2 H16 T4096:
+          // 136, 146, 137).
+          constexpr bool kMaxLoad = D == 64;
           // A pair of keys' weights, packed (t: the pair's place among columns from which lim_c
           // and vl_c count):
           auto weights = [&]<bool FAR, bool MASK>(int t, uint32_t s0, uint32_t s1, int lim_c, int vl_c) {
@@ -965,20 +969,26 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             if (t & 1) acc1 = f2_add(acc1, f2_pack(p0, p1));
             else acc0 = f2_add(acc0, f2_pack(p0, p1));
-            if constexpr (kRefRest) {
-              if (t & 1) top1 = fmax3(top1, p0, p1);
-              else top0 = fmax3(top0, p0, p1);
+            if constexpr (FAR || MASK) {
+              top = fmax3(top, p0, p1);
+            } else if constexpr (!kMaxLoad) {
+              raw_top = fmax3(raw_top, u2f(s0), u2f(s1));
             }
             return pack_bf16x2(p0, p1);
           };
           uint32_t s[2][32];
-          float top_s[2];
-          tmem_ld32_max<true>(t_s, s[0], &top_s[0]);
+          float top_s[2], max_s[2] = {-INFINITY, -INFINITY};
+          auto load = [&](int c, int i) {
+            if constexpr (kMaxLoad) tmem_ld32_absmax_max(t_s + c * 32, s[i], &top_s[i], &max_s[i]);
+            else tmem_ld32_max<true>(t_s + c * 32, s[i], &top_s[i]);
+          };
+          load(0, 0);
           // Two halves of the columns, kSpread: unrolled; otherwise one piece of code, and the rare
           // far columns a loop over a copy in local memory, since a spread step that takes the
-          // other form now and then waits for instructions. (d128, B2 H16 T4096 causal: 141 µs
-          // spread, 136 not, and where 8 % of the 32s are far 288, 181; with o's rest 161, 153. d64,
-          // B1 H12 T16384: 532, 604; far ones 1600, 825; with o's rest 645 either way, T4096 B4 200, 184.)
+          // other form now and then waits for instructions. (Before o was divided with the rounded
+          // largest weight: d128, B2 H16 T4096 causal, 141 µs spread, 136 not, and where 8 % of the 32s
+          // are far 288, 181; d64, B1 H12 T16384, far ones 1600, 825. Now: d64, that size, 575 spread,
+          // 614 not; with o's rest 618.)
           constexpr bool kSpread = C::kSepP && !kRefRest && (MOD & kModTight) == 0;
 #pragma unroll (kSpread ? 2 : 1)
           for (int h = 0; h < 2; ++h) {
@@ -989,9 +999,10 @@ __global__ void __launch_bounds__(kThreads, 1)
               tmem_ld_wait();
               reg_fence32(x);
               asm volatile("" : "+f"(top_s[cc]));
+              if constexpr (kMaxLoad) asm volatile("" : "+f"(max_s[cc]));
               const bool far = __any_sync(0xffffffffu, top_s[cc] > p.mod.cap.limit);
               if (cc == 0 || h == 0) {
-                tmem_ld32_max<true>(t_s + (2 * h + cc + 1) * 32, s[1 - cc], &top_s[1 - cc]);
+                load(2 * h + cc + 1, 1 - cc);
               } else if constexpr (C::kSepP) {
                 tc_fence_before_sync();
                 __syncwarp();
@@ -1019,6 +1030,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 for (int t = 0; t < 16; ++t)
                   pk[cc * 16 + t] = weights.template operator()<false, true>(t, x[2 * t], x[2 * t + 1], lim_c, vl_c);
               } else {
+                if constexpr (kMaxLoad) raw_top = fmaxf(raw_top, max_s[cc]);
 #pragma unroll
                 for (int t = 0; t < 16; ++t)
                   pk[cc * 16 + t] = weights.template operator()<false, false>(t, x[2 * t], x[2 * t + 1], 0, 0);
@@ -1239,7 +1251,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         continue;
       }
       if (defer) {
-        park(cur, l, kRefRest ? fmaxf(top0, top1) : m_ref);
+        park(cur, l, kRef ? top_weight(top, raw_top, p.mod.cap) : m_ref);
         continue;
       }
 
@@ -1249,7 +1261,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       FA_TRACE(24 + wg, 0);
       if (good) {
         tc_fence_after_sync();
-        const float inv_l = inv_of(kRefRest ? top_rounded(l, fmaxf(top0, top1)) : l);
+        const float inv_l = inv_of(kRef ? top_rounded(l, top_weight(top, raw_top, p.mod.cap)) : l);
         if (!cur.partial) {
           // 64 columns per round through the warp's staging slice, 32 at a time from TMEM.
           uint8_t* slice = smem + C::kOOff + (wg * 4 + quad) * 4096;

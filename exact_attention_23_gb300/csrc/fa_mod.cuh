@@ -56,14 +56,17 @@ constexpr int kModTree = 8;  // new tokens against a cache (fa_tree_walk.cuh)
 // values of ordinary size nor their inverses leave fp32's range; bf16 has the same exponents, so P
 // keeps its relative precision. The softmax is then taken against 0: no maximum, no rescaling, and no
 // dependency between the capping of a step's last score and the exponential of its first, so
-// that FMA and MUFU work overlap (B1 H12 T16384 d64 causal: 885 -> 712 µs, and 532
+// that FMA and MUFU work overlap (B1 H12 T16384 d64 causal: 885 -> 712 µs, and 575
 // on the two-tile kernel).
-// One thing is lost: against a row's maximum the weight of a key that outweighs the others is 1,
-// unrounded; against 0 it is rounded like any other. Where the output's rest is asked for
-// (kModRest), O is therefore divided by the weights' sum with the largest one taken as rounded
-// (top_rounded), not by the sum that the LSE takes: then an outweighing key's share is 1 again.
-// (A maximum of three a pair, which the ALU takes beside the FMA's work. A second sum, over all the
-// rounded weights, is no more exact where it matters and cost a third of the kernel's time.)
+// Against a row's maximum the weight of a key that outweighs the others is 1, unrounded; against 0
+// it is rounded like any other, and a row of one key would not get that key's value. O is therefore
+// divided by the weights' sum with the largest one taken as rounded (top_rounded), not by the sum
+// that the LSE takes: then an outweighing key's share is 1 again (o's error with scores of deviation
+// 4, cap 30: 2.3e-3 -> 2.0e-3 of its norm, its own rounding being 1.66e-3). The largest weight is
+// that of the largest raw score, whose capped value is made again at the row's end, but for masked
+// and far columns, whose weights are looked at as they are made. (Looking at every weight: 609 µs for
+// the 575. A second sum, over all the rounded weights, is no more exact where it matters and cost a
+// third of the kernel's time.) A negative scale turns the products' sign on the tensor cores.
 constexpr float kCapRef = 88.0f;
 constexpr float kCapBend = 0.8f;
 constexpr double kCapPoly[5] = {0.9999989943572278, -0.3332537198003981, 0.1323056561802812,
@@ -105,6 +108,14 @@ __device__ __forceinline__ uint64_t cap2(uint64_t s, const CapFactors& k) {
     r = f2_fma(r, w, f2_splat(k.c[0]));
     return f2_mul(s, r);
   }
+}
+
+// A row's largest weight (kModRef): top, of those noted as weights, or that of the raw score `raw`,
+// the largest of the columns that the polynomial made (−∞: none).
+__device__ __forceinline__ float top_weight(float top, float raw, const CapFactors& k) {
+  float x, y;
+  f2_unpack(cap2<false>(f2_splat(raw), k), x, y);
+  return fmaxf(top, raw > -INFINITY ? ex2_approx(x) : 0.0f);
 }
 
 }  // namespace fa

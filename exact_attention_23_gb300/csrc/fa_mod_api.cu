@@ -396,6 +396,10 @@ int fa_fwd_mod(const void* q, const void* k, const void* v, void* o, float* lse,
   a.p.T = T;
   a.p.BH = BH;
   const int mod = fwd_mod_bits(softcap, slopes, rest);
+  if ((mod & fa::kModRef) && scale < 0.0f) {  // (the largest weight is that of the largest raw score)
+    a.p.s_negate = fa::kIdescNegateA;
+    cap_factors(-scale, softcap, &cap);
+  }
   // Two query tiles a CTA, as in the dense forward, where every SM gets 1.5 such units (one tile ->
   // two tiles in µs; d64 H12, d128 H16 Hkv4):
   //   plain, causal: d64 B3 T2048 (1.9 units an SM) 35 -> 31, d128 B1 T4096 (1.7) 79 -> 57; 1.3 units
@@ -445,8 +449,10 @@ int fa_fwd_mod(const void* q, const void* k, const void* v, void* o, float* lse,
   a.stream = static_cast<cudaStream_t>(stream);
   // Steps of the other forms, far or masked, are common where the cap is small (the scores of unit
   // normal rows have deviation 1) or walks are short: the step that stands them better
-  // (fa_fwd_kernel.cuh; B4 H12 T2048, eight documents, cap 30: 48 -> 43 µs).
-  const int tight = d == 64 && mod == (fa::kModOn | fa::kModCap | fa::kModRef) && (visible || softcap < 25.0f)
+  // (fa_fwd_kernel.cuh; H12 d64, µs: eight documents, cap 30, B4 T2048 48 -> 43; causal, B3 T2048 45 -> 40,
+  // B4 T4096 174 -> 170, B2 T6144 182 -> 182, T8192 165 -> 173; no mask, B3 T2048 58 -> 63).
+  const bool short_walks = visible || (causal && T <= 4096);
+  const int tight = d == 64 && mod == (fa::kModOn | fa::kModCap | fa::kModRef) && (short_walks || softcap < 25.0f)
                         ? fa::kModTight : 0;
   const cudaError_t e = pairs ? (d == 64 ? fa::launch_fwd_mod_pairs_d64(a, mod | tight) : fa::launch_fwd_mod_pairs_d128(a, mod))
                               : (d == 64 ? fa::launch_fwd_mod_d64(a, mod) : fa::launch_fwd_mod_d128(a, mod));

@@ -228,6 +228,10 @@ int fa_fwd_tree(const void* q, const void* k_cache, const void* v_cache, void* o
     f.grid = a.grid;
     f.stream = a.stream;
     const int fm = fwd_mod_bits(softcap, slopes, nullptr);
+    if ((fm & fa::kModRef) && scale < 0.0f) {  // (as in fa_fwd_mod)
+      f.p.s_negate = fa::kIdescNegateA;
+      cap_factors(-scale, softcap, &f.p.mod.cap);
+    }
     e = (d == 64) ? fa::launch_fwd_tree_d64(f, fm) : fa::launch_fwd_tree_d128(f, fm);
   } else {
     e = (d == 64) ? fa::launch_tree_rows<64>(a, 1 << z.rows_log2, mod) : fa::launch_tree_rows<128>(a, 1 << z.rows_log2, mod);

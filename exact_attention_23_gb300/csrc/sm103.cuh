@@ -489,6 +489,23 @@ __device__ __forceinline__ void tmem_ld32_max(uint32_t taddr, uint32_t* r, float
         : "r"(taddr));
 }
 
+// 32 columns, their largest magnitude and their largest value: two loads into the same registers.
+__device__ __forceinline__ void tmem_ld32_absmax_max(uint32_t taddr, uint32_t* r, float* a, float* m) {
+#define FA_REGS32 "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,%20,%21,%22," \
+                  "%23,%24,%25,%26,%27,%28,%29,%30,%31}"
+  asm volatile(
+      "tcgen05.ld.red.sync.aligned.32x32b.x32.max.abs.f32 " FA_REGS32 ", %32, [%34];\n\t"
+      "tcgen05.ld.red.sync.aligned.32x32b.x32.max.f32 " FA_REGS32 ", %33, [%34];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
+        "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]),
+        "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]), "=r"(r[17]), "=r"(r[18]),
+        "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]),
+        "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]),
+        "=r"(r[31]), "=f"(*a), "=f"(*m)
+      : "r"(taddr));
+#undef FA_REGS32
+}
+
 __device__ __forceinline__ void tmem_ld_wait() {
   asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
 }

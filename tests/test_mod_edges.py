@@ -1,5 +1,7 @@
 """Modified scores and cached contexts at their edges, on the GPU: keys behind a length that is no
-multiple of a tile. Bounds: those of mod_reference.py."""
+multiple of a tile, rows that see one key. Bounds: those of mod_reference.py."""
+
+import math
 
 import pytest
 import torch
@@ -7,6 +9,7 @@ import torch
 import exact_attention_23_gb300 as fa
 from tests import mod_reference as ref
 from tests.test_mod import ALL, _run, _tensors
+from tests.test_tree import _data as _tree_data
 
 pytestmark = pytest.mark.gpu
 
@@ -55,3 +58,59 @@ def test_distances_that_raise_scores(d):
     sl = torch.tensor([-1.5, -0.25])
     r = ref.attention(q, k, v, ref.visible_mask(B, T, False), d ** -0.5, 0.0, sl, do)
     ref.check(_run(q, k, v, do, causal=False, slopes=sl), r, ALL)
+
+
+# ------------------------------------------------------------------------ rows that see one key
+
+@pytest.mark.parametrize("with_rest", [False, True])
+@pytest.mark.parametrize("B,H,Hkv", [(1, 4, 2), (4, 80, 10)])      # one query tile a CTA, and two
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("cap", [0.0, 20.0, 50.0, 80.0])
+def test_a_row_of_one_key_is_its_value(B, H, Hkv, d, cap, with_rest):
+    """Documents of one token: the weight is 1, so o is v, to the last bit."""
+    T = 260
+    q, k, v, _ = _tensors(B, H, Hkv, T, d, 41, 4.0)
+    ids = torch.arange(T, dtype=torch.int32).repeat(B, 1)
+    seen = fa.visible(B, T, doc_ids=ids.cuda())
+    rest = torch.full_like(q, math.nan).cuda() if with_rest else None
+    o, _ = fa.fwd_mod(q.cuda(), k.cuda(), v.cuda(), visible=seen, softcap=cap, rest=rest)
+    assert torch.equal(o.cpu(), v.repeat_interleave(H // Hkv, 1))
+    # What is left of a value: the exponent is a score less its own rounding, 2⁻²⁴ of a score below
+    # 64 in base 2, so the weight and with it the sum are within 2⁻¹⁸ of 1.
+    assert rest is None or (rest.abs().float() <= 2.0 ** -18 * o.abs().float() + 1e-30).all()
+
+
+@pytest.mark.parametrize("with_rest", [False, True])
+@pytest.mark.parametrize("B,H", [(1, 4), (2, 160)])
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("cap,sign", [(0.0, 1.0), (50.0, 1.0), (50.0, -1.0), (20.0, 1.0), (80.0, -1.0)])
+def test_a_key_that_outweighs_all_others(B, H, d, cap, sign, with_rest):
+    """Queries that are their own key, no mask: half a bf16 step of o, of which the outweighing key's
+    rounding is no part; the others' rounding goes by their share (twice it, as in mod_reference.py),
+    and 2⁻¹⁸ is the fp32 arithmetic's."""
+    T = 256
+    q, _, v, _ = _tensors(B, H, H, T, d, 45, 2.0)
+    k = q if sign > 0 else -q
+    scale = sign * 8.0 / d                                         # own scores around 32
+    rest = torch.empty_like(q).cuda() if with_rest else None
+    o, _ = fa.fwd_mod(q.cuda(), k.cuda(), v.cuda(), causal=False, softcap=cap, scale=scale, rest=rest)
+    r = ref.attention(q, k, v, ref.visible_mask(B, T, False), scale, cap)
+    own = (q.double() * k.double()).sum(-1) * scale
+    own = cap * torch.tanh(own / cap) if cap else own
+    others = (1.0 - torch.exp(own - r["lse"]))[..., None] * v.double().abs().amax(2, keepdim=True)
+    assert float(others.max()) < 0.5
+    bound = (ref.U + 2.0 ** -18) * r["o"].abs() + 2 * ref.U * others
+    assert ((o.double().cpu() - r["o"]).abs() <= bound).all()
+
+
+@pytest.mark.parametrize("n", [9, 40])                             # streaming kernel, tensor cores
+@pytest.mark.parametrize("Tmax", [50, 3400])                       # a CTA an entry, and stretches
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("cap", [0.0, 20.0, 50.0, 80.0])
+def test_a_token_of_one_key_is_its_value(n, Tmax, d, cap):
+    """New tokens that see themselves alone."""
+    B, H = 2, 3
+    q, k, v = _tree_data(B, H, H, n, Tmax, d, 43, 4.0)
+    o, _ = fa.fwd_tree(q.cuda(), k.cuda(), v.cuda(), torch.zeros(B, dtype=torch.int32, device="cuda"),
+                       tree=torch.eye(n, dtype=torch.uint8).cuda(), softcap=cap)
+    assert torch.equal(o.cpu(), v[:, :, :n])
