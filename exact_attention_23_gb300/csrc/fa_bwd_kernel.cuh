@@ -131,7 +131,7 @@ struct BwdBars {
   uint64_t grad_done;   // every MMA of the gradient issuer done: dK, dV final
   uint32_t tmem_base;
   uint32_t abort;
-  uint32_t whole[3];    // MOD: the stage's rows all see every key of this CTA's tile
+  uint32_t whole[3];    // MOD: 1: the stage's rows all see every key of this CTA's tile; 2: some are padding
 };
 static_assert(sizeof(BwdBars) <= 256, "barrier block");
 
@@ -142,8 +142,9 @@ static_assert(sizeof(BwdBars) <= 256, "barrier block");
 // fa_bwd_sum_kernel adds the parts in order (no atomics: the same bits every time).
 struct BwdModParams {
   const int2* rows;     // [B][T_pad] visible key interval of each query row, or null
-  const int4* units;    // [B][n_kt] (key tile, first 128-row query tile, past the last, rows in use)
-  const int2* whole;    // [B][n_kt] (largest lo, smallest hi) over a 128-row query tile
+  const int4* units;    // [B][n_kt] (key tile, first 128-row query tile, past the last,
+                        //   2 · first tile with padding + whether the key tile has any)
+  const int2* whole;    // [B][n_kt] (largest lo, smallest hi) over a tile's 128 rows: hi is 0 with padding
   const float* slopes;  // [H]
   float* part_out;      // parts > 1: [2][parts][B·Hkv][T][D], dK (scaled) then dV
   int Hkv;              // key heads
@@ -406,8 +407,9 @@ struct BwdWalk {
   int j, bh, i0, n;
   int n_i, q0h;  // MOD (dense: n and bh)
   int h0;        // the first query head's number within its sequence
-  int used;      // rows in use: those behind are padding
   int part;      // which part of the key head's query heads
+  int pad0;      // the first query tile with padding
+  bool key_pad;  // the key tile has padding
 };
 
 // pos, head: the CTA's place in the unit order.
@@ -419,8 +421,9 @@ __device__ __forceinline__ BwdWalk bwd_walk(const BwdParams& p, int pos, int hea
   w.bh = w.q0h = head;
   w.i0 = CAUSAL ? (w.j * 128) / kBQ : 0;
   w.n = w.n_i = p.n_qt - w.i0;
-  w.used = p.T_pad;
   w.h0 = w.part = 0;
+  w.pad0 = p.n_qt;
+  w.key_pad = false;
   if constexpr (MOD != 0) {
     const int heads = p.mod.group / p.mod.parts;
     w.bh = head / p.mod.parts;
@@ -433,7 +436,8 @@ __device__ __forceinline__ BwdWalk bwd_walk(const BwdParams& p, int pos, int hea
       w.j = rec.x;
       w.i0 = rec.y * kPer;
       w.n_i = max(0, rec.z * kPer - w.i0);
-      w.used = rec.w;
+      w.pad0 = (rec.w >> 1) * kPer;
+      w.key_pad = (rec.w & 1) != 0;
     } else if (p.mod.causal) {
       w.i0 = pos * kPer;
       w.n_i = p.n_qt - w.i0;
@@ -588,7 +592,7 @@ __global__ void __launch_bounds__(BwdCfg<D, MOD>::kThreads, 1)
           if (p.mod.rows) {
             const int b = bh / p.mod.Hkv;
             const int2 w = __ldg(p.mod.whole + (size_t)b * p.n_kt + i * C::kBQ / 128);
-            bars->whole[st] = (w.x <= j * 128 && w.y >= j * 128 + 128) ? 1u : 0u;
+            bars->whole[st] = (w.x <= j * 128 && w.y >= j * 128 + 128) ? 1u : w.y == 0 ? 2u : 0u;
             vec_bytes = C::kVecBytes;
           }
           mbar_arrive_expect_tx(&bars->q_full[st], 2 * C::kQTile + vec_bytes);
@@ -622,22 +626,14 @@ __global__ void __launch_bounds__(BwdCfg<D, MOD>::kThreads, 1)
     // ---------------------------------------------------------------- score issuer
     constexpr uint32_t kIdS = idesc_bf16(128, C::kBQ, false);  // Sᵀ = K·Qᵀ, dPᵀ = V·dOᵀ
     const uint32_t k_s = sbase + C::kK, v_s = sbase + C::kV;
+    // MOD: rows of padding are zeroed in K, V, Q and dO here, before the first product that reads
+    // them (every other reader comes after it).
     bool ok = bwd_wait<MOD>(&bars->kv_full, 0, wc);
-    // MOD: rows behind the last one in use (padding) may hold anything. Their P and dS are 0,
-    // but 0 · NaN must not reach a product: their K, V, Q and dO rows are zeroed here, before the
-    // first product that reads them (every other reader comes after it).
-    auto zero_rows = [&](uint32_t box, int first, int rows) {
-      for (int x = max(first, 0) * 8 + lane; x < rows * 8; x += 32) st_shared_v4(box + x * 16, 0u, 0u, 0u, 0u);
-    };
     if constexpr (MOD != 0) {
-      if (ok && wk.used < j * 128 + 128) {
-#pragma unroll
-        for (int b = 0; b < D / 64; ++b) {
-          zero_rows(k_s + b * C::kBox, wk.used - j * 128, 128);
-          zero_rows(v_s + b * C::kBox, wk.used - j * 128, 128);
-        }
-        fence_proxy_async_smem();
-        __syncwarp();
+      if (ok && wk.key_pad) {
+        const int2* iv = p.mod.rows + (size_t)(bh / p.mod.Hkv) * p.T_pad + (size_t)j * 128;
+        zero_padding(k_s, D / 64, C::kBox, 128, iv);
+        zero_padding(v_s, D / 64, C::kBox, 128, iv);
       }
     }
     int ti = 0;  // MOD: the step's query tile within the walk
@@ -646,14 +642,10 @@ __global__ void __launch_bounds__(BwdCfg<D, MOD>::kThreads, 1)
       if constexpr (MOD != 0) {
         const int i = i0 + ti;
         if (++ti == wk.n_i) ti = 0;
-        if (wk.used < (i + 1) * C::kBQ) {
-#pragma unroll
-          for (int b = 0; b < D / 64; ++b) {
-            zero_rows(q_s(st) + b * C::kQBox, wk.used - i * C::kBQ, C::kBQ);
-            zero_rows(do_s(st) + b * C::kQBox, wk.used - i * C::kBQ, C::kBQ);
-          }
-          fence_proxy_async_smem();
-          __syncwarp();
+        if (i >= wk.pad0 && bars->whole[st] == 2u) {
+          const int2* iv = reinterpret_cast<const int2*>(sm + C::kVec + st * C::kVecBytes + 2 * C::kBQ * 4);
+          zero_padding(q_s(st), D / 64, C::kQBox, C::kBQ, iv);
+          zero_padding(do_s(st), D / 64, C::kQBox, C::kBQ, iv);
         }
       }
       if (t > 0 && !(ok = bwd_wait<MOD>(&bars->s_free, (t - 1) & 1, wc))) break;
@@ -892,7 +884,7 @@ __global__ void __launch_bounds__(BwdCfg<D, MOD>::kThreads, 1)
         // The modified scores' P, packed at once; pr keeps P · (1 − tanh²), what dS multiplies.
         const int q0 = i * C::kBQ + g * NC, key = j * 128 + r;
         bool part;  // some row of the stage does not see every key of the tile
-        if (p.mod.rows) part = bars->whole[st] == 0u;
+        if (p.mod.rows) part = bars->whole[st] != 1u;
         else part = j * 128 + 127 >= (p.mod.causal ? min(i * C::kBQ + 1, p.T) : p.T);
         const bool left = j * 128 + qd * 32 + 31 <= q0;
         const float dist0 = static_cast<float>(q0 - key);

@@ -167,7 +167,7 @@ __device__ __forceinline__ Unit unit1_of(const FwdParams& p, int L, const Segmen
       u.qt0 = p.n_qt - 1 - pos;
       u.kb = 0;
       u.ke = p.mod.causal ? u.qt0 + 1 : p.n_kv;
-      u.mh = p.n_kv * kBlockN;  // (rows past Tk are loaded as zeros)
+      u.mh = p.n_kv;
     }
     u.n_steps = max(0, u.ke - u.kb);
     u.nkv[0] = u.n_steps;
@@ -381,18 +381,15 @@ __global__ void __launch_bounds__(Cfg1<D, (MOD & kModRef) != 0>::kThreads, 1)
           const int st = g % C::kStages;
           const int b = g & 1;
           if (!mbar_wait_warp(&bars->v_full[st], (g / C::kStages) & 1, wc)) { ok = false; break; }
-          FA1_TRACE(8, j);
-          if (!mbar_wait_warp(&bars->p_full[b], (g >> 1) & 1, wc)) { ok = false; break; }
-          FA1_TRACE(11, j);
-          // A unit's first P·V overwrites O: the previous unit's O must have been read out.
-          if (j == 0 && nunits > 0 && !mbar_wait_warp(&bars->o_free, (nunits - 1) & 1, wc)) {
-            ok = false;
-            break;
+          if constexpr (MOD != 0 && !kTree) {
+            if (u.kb + j >= u.mh)
+              zero_padding(v_base + st * C::kTileBytes, C::kSub, C::kSubBytes, kBlockN,
+                           p.mod.rows + p.mod.div_h.div(static_cast<uint32_t>(u.bh)) * static_cast<size_t>(p.mod.T_pad) +
+                               (u.kb + j) * kBlockN);
           }
-          tc_fence_after_sync();
-          if constexpr (MOD != 0) {
-            // Keys that no query of the sequence sees and that lie behind all that some query
-            // does may hold anything (padding): their P is 0, and 0 · NaN must not reach O.
+          if constexpr (kTree) {
+            // Rows behind the sequence's keys may hold anything: their P is 0, and 0 · NaN must not
+            // reach O.
             const int used = u.mh - (u.kb + j) * kBlockN;
             if (used < kBlockN) {
               for (int x = used * 8 + lane; x < kBlockN * 8; x += 32)
@@ -403,6 +400,15 @@ __global__ void __launch_bounds__(Cfg1<D, (MOD & kModRef) != 0>::kThreads, 1)
               __syncwarp();
             }
           }
+          FA1_TRACE(8, j);
+          if (!mbar_wait_warp(&bars->p_full[b], (g >> 1) & 1, wc)) { ok = false; break; }
+          FA1_TRACE(11, j);
+          // A unit's first P·V overwrites O: the previous unit's O must have been read out.
+          if (j == 0 && nunits > 0 && !mbar_wait_warp(&bars->o_free, (nunits - 1) & 1, wc)) {
+            ok = false;
+            break;
+          }
+          tc_fence_after_sync();
           if (leader) {
             const uint32_t va = v_base + st * C::kTileBytes;
 #pragma unroll

@@ -129,9 +129,9 @@ static_assert(sizeof(Bars) <= 512, "barrier block");
 // Modified scores (the one-tile kernel's MOD instantiations; see fa_mod.cuh).
 struct ModParams {
   const int2* rows;     // [B][T_pad] visible key interval [lo, hi) of each query row, or null
-  const int4* units;    // [B][n_t] (query tile, first K tile, past the last, keys in use)
-  const int4* pairs;    // [B][ceil(n_t/2)][2] (first query tile, keys in use, its first K tile, past
-                        //   its last), (the second tile's first and past its last, 0, 0)
+  const int4* units;    // [B][n_t] (query tile, first K tile, past the last, first tile with padding)
+  const int4* pairs;    // [B][ceil(n_t/2)][2] (first query tile, first tile with padding, its first K
+                        //   tile, past its last), (the second tile's first and past its last, 0, 0)
   const float* slopes;  // [H] distance-bias slopes (BIAS)
   __nv_bfloat16* rest;  // [BH][T][D] what o's rounding leaves out, or null (not TREE)
   int T_pad;            // ceil(T/128) · 128
@@ -191,7 +191,7 @@ struct Unit {
   int kb, ke;     // K-tile range [kb, ke) (dense: [0, n_steps))
   int lo[2];      // MOD: tile i's K tiles are [lo[i], last[i])
   int last[2];    // last K tile visible to tile i (GEN, causal)
-  int split, mh;  // key-range index; block-mask head
+  int split, mh;  // key-range index; block-mask head (MOD: the first tile with padding)
 };
 
 __device__ __forceinline__ int unit_index(int round, int cta, int grid) {
@@ -247,7 +247,7 @@ __device__ __forceinline__ Unit pair_unit_of(const FwdParams& p, int L) {
     u.last[1] = r1.y;
   } else {
     u.qt0 = (p.n_units - 1 - pos) * 2;
-    u.mh = p.n_kv * kBlockN;  // (rows past Tk are loaded as zeros)
+    u.mh = p.n_kv;
     u.lo[0] = u.lo[1] = 0;
     u.last[0] = p.mod.causal ? u.qt0 + 1 : p.n_kv;
     u.last[1] = u.qt0 + 1 >= p.n_qt ? 0 : (p.mod.causal ? u.qt0 + 2 : p.n_kv);
@@ -624,16 +624,10 @@ __global__ void __launch_bounds__(kThreads, 1)
           const int st = g % C::kStages;
           if (!wait_w(&bars->v_full[st], (g / C::kStages) & 1, wc)) { ok = false; break; }
           if constexpr (MOD != 0) {
-            // Keys behind the last one that some query of the sequence sees may hold anything
-            // (padding): their P is 0, and 0 · NaN must not reach O.
-            if (us.kt == u.mh / kBlockN) {
-              for (int x = u.mh % kBlockN * 8 + lane; x < kBlockN * 8; x += 32)
-#pragma unroll
-                for (int s = 0; s < C::kSub; ++s)
-                  st_shared_v4(v_base + st * C::kTileBytes + s * C::kSubBytes + x * 16, 0u, 0u, 0u, 0u);
-              fence_proxy_async_smem();
-              __syncwarp();
-            }
+            if (us.kt >= u.mh)
+              zero_padding(v_base + st * C::kTileBytes, C::kSub, C::kSubBytes, kBlockN,
+                           p.mod.rows + p.mod.div_h.div(static_cast<uint32_t>(u.bh)) * static_cast<size_t>(p.mod.T_pad) +
+                               us.kt * kBlockN);
           }
 #pragma unroll
           for (int i = 0; i < 2; ++i) {

@@ -72,6 +72,29 @@ constexpr float kCapBend = 0.8f;
 constexpr double kCapPoly[5] = {0.9999989943572278, -0.3332537198003981, 0.1323056561802812,
                                 -0.04918014254491106, 0.012100138637293043};
 
+// Padding may hold anything. Its P (and dS) are 0, but 0 · NaN must not reach a product, so whoever
+// issues the first product of a tile zeroes its padded rows (those of an empty interval) in shared
+// memory: `boxes` boxes of [rows][64] bf16, box_bytes apart. Whole warp; rare, so called, not inlined.
+static __device__ __noinline__ void zero_padding(uint32_t tile, int boxes, int box_bytes, int rows,
+                                                 const int2* intervals) {
+  const uint32_t lane = threadIdx.x & 31;
+  uint32_t m = 0u;  // bit k: row 32·k + lane
+#pragma unroll 4
+  for (int k = 0; k < rows / 32; ++k) {
+    const int2 v = intervals[32 * k + lane];
+    if (v.y <= v.x) m |= 1u << k;
+  }
+  for (; m != 0u; m &= m - 1u) {
+    const uint32_t row = tile + (32 * (__ffs(m) - 1) + lane) * 128;
+    for (int x = 0; x < boxes; ++x)
+#pragma unroll
+      for (int c = 0; c < 8; ++c)  // (neighbouring rows at other pieces: no bank conflicts)
+        st_shared_v4(row + x * box_bytes + ((c + lane) & 7) * 16, 0u, 0u, 0u, 0u);
+  }
+  fence_proxy_async_smem();
+  __syncwarp();
+}
+
 struct CapFactors {
   float c[5];      // kCapPoly[k] · in^2k · scale · log2(e)
   float in_exp;    // 2·log2(e)·scale / cap

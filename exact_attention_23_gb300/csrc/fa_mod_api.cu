@@ -20,13 +20,13 @@ namespace fa {
 // What fa_visible writes (one buffer, sections on 256-byte boundaries):
 //   rows   int2 [B][T_pad]  visible keys [lo, hi) of each query row ((0, 0): none; padding too)
 //   fwd    int4 [B][n_t]    query tiles, most K tiles first: (tile, first K tile, past the last,
-//                           rows in use: one past the last row that sees or is seen)
+//                           first tile with padding or n_t)
 //   pairs  int4 [B][n_p][2] pairs of neighbouring query tiles, n_p = ceil(n_t / 2), the longest walk
-//                           first: (first tile, rows in use, its first K tile, past its last), (the
+//                           first: (first tile, first tile with padding, its first K tile, past its last), (the
 //                           second tile's first K tile and past its last, 0, 0)
 //   bwd    int4 [B][n_t]    key tiles, most query tiles first: (tile, first query tile, past the
-//                           last, rows in use)
-//   whole  int2 [B][n_t]    (largest lo, smallest hi) over a tile's rows
+//                           last, 2 · first tile with padding + whether this key tile has any)
+//   whole  int2 [B][n_t]    (largest lo, smallest hi) over a tile's rows: hi is 0 with padding, and only then
 //   span   int2 [B][n_t]    (smallest lo, largest hi) over the rows that see a key
 //   seen   int2 [B][n_t]    (first, past the last) query tile that sees a key tile
 struct VisibleLayout {
@@ -98,7 +98,7 @@ __device__ __forceinline__ void doc_bits(const int* ids, int i0, int end, uint32
 // tiles' extremes are kept in shared memory up to kVisTiles of them.
 __global__ void __launch_bounds__(kVisThreads) fa_visible_kernel(const VisibleParams p) {
   __shared__ int s_last[kVisThreads / 32], s_first[kVisThreads / 32];
-  __shared__ int s_used;
+  __shared__ int s_pad;
   __shared__ int2 s_span[kVisTiles], s_seen[kVisTiles];
   pdl_wait();
   pdl_launch_dependents();
@@ -110,7 +110,7 @@ __global__ void __launch_bounds__(kVisThreads) fa_visible_kernel(const VisiblePa
   int2* rows = p.rows + static_cast<size_t>(b) * T_pad;
   int2* span = n_t <= kVisTiles ? s_span : p.span + static_cast<size_t>(b) * n_t;
   int2* seen = n_t <= kVisTiles ? s_seen : p.seen + static_cast<size_t>(b) * n_t;
-  if (tid == 0) s_used = 0;
+  if (tid == 0) s_pad = n_t;
   const long long seg = (T_pad + kVisThreads - 1) / kVisThreads;
   const int a0 = static_cast<int>(min(static_cast<long long>(T), tid * seg));
   const int a1 = static_cast<int>(min(static_cast<long long>(T), (tid + 1) * seg));
@@ -154,7 +154,7 @@ __global__ void __launch_bounds__(kVisThreads) fa_visible_kernel(const VisiblePa
       }
     }
   }
-  int used = 0;
+  int padded = n_t;  // the first tile with padding
   const int* pre_at = nullptr;
   int pre_all = 0;
   if (p.prefix && p.causal) {
@@ -175,20 +175,20 @@ __global__ void __launch_bounds__(kVisThreads) fa_visible_kernel(const VisiblePa
       int2 r = make_int2(lo, end);
       if ((pads >> o) & 1u) {
         r = make_int2(0, 0);
+        padded = i >> 7;  // (from the back)
       } else {
         if (p.causal) {
           const int pre = pre_at ? max(0, pre_at[i]) : pre_all;
           r.y = max(i + 1, pre > end - lo ? end : lo + pre);
         }
-        used = max(used, i + 1);
       }
       rows[i] = r;
       if (lo == i) end = i;
     }
   }
   for (long long i = T + tid; i < T_pad; i += kVisThreads) rows[i] = make_int2(0, 0);
-  used = __reduce_max_sync(0xffffffffu, used);
-  if (lane == 0) atomicMax(&s_used, used);
+  padded = __reduce_min_sync(0xffffffffu, padded);
+  if (lane == 0) atomicMin(&s_pad, padded);
   __syncthreads();
   const size_t t0 = static_cast<size_t>(b) * n_t;
   for (int t = warp; t < n_t; t += kWarps) {
@@ -215,7 +215,7 @@ __global__ void __launch_bounds__(kVisThreads) fa_visible_kernel(const VisiblePa
     }
   }
   __syncthreads();
-  used = s_used;
+  padded = s_pad;
   for (int t = warp; t < n_t; t += kWarps) {
     // the query tiles whose rows see a key of this tile
     int f = n_t, l = 0;
@@ -245,8 +245,8 @@ __global__ void __launch_bounds__(kVisThreads) fa_visible_kernel(const VisiblePa
     rf = __reduce_add_sync(0xffffffffu, rf);
     rb = __reduce_add_sync(0xffffffffu, rb);
     if (lane == 0) {
-      p.fwd[t0 + rf] = make_int4(t, kb, ke, used);
-      p.bwd[t0 + rb] = make_int4(t, k.x, k.y, used);
+      p.fwd[t0 + rf] = make_int4(t, kb, ke, padded);
+      p.bwd[t0 + rb] = make_int4(t, k.x, k.y, 2 * padded + (p.whole[t0 + t].y == 0 ? 1 : 0));
     }
   }
   // Pairs of query tiles, by the length of their union's walk.
@@ -271,7 +271,7 @@ __global__ void __launch_bounds__(kVisThreads) fa_visible_kernel(const VisiblePa
     r = __reduce_add_sync(0xffffffffu, r);
     if (lane == 0) {
       int4* out = p.pairs + (static_cast<size_t>(b) * n_p + r) * 2;
-      out[0] = make_int4(2 * t, used, a.x, a.y);
+      out[0] = make_int4(2 * t, padded, a.x, a.y);
       out[1] = make_int4(c.x, c.y, 0, 0);
     }
   }

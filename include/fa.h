@@ -344,8 +344,8 @@ int fa_visible(const int* doc_ids, const int* prefix_len, int prefix_per_token, 
  *             is the output to 16 bits), for fa_bwd_mod
  *   status, timeout_ns : as for fa_fwd_ex
  *
- * Padding may hold anything: rows behind the last token that sees a key are never mixed into
- * others' results, NaN included. Padding in front of or between documents must be finite.
+ * Padding (a negative document id, in front of, between or behind the documents) may hold anything,
+ * NaN included: it is never mixed into other rows' results, here or in fa_bwd_mod.
  */
 int fa_fwd_mod(const void* q, const void* k, const void* v, void* o, float* lse, void* rest,
                const void* visible, int causal, float softcap, const float* slopes, int B, int H, int Hkv, int T, int d,

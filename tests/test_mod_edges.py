@@ -1,5 +1,6 @@
 """Modified scores and cached contexts at their edges, on the GPU: keys behind a length that is no
-multiple of a tile, rows that see one key. Bounds: those of mod_reference.py."""
+multiple of a tile, rows that see one key, padding of any value anywhere. Bounds: those of
+mod_reference.py."""
 
 import math
 
@@ -8,7 +9,7 @@ import torch
 
 import exact_attention_23_gb300 as fa
 from tests import mod_reference as ref
-from tests.test_mod import ALL, _run, _tensors
+from tests.test_mod import ALL, _run, _slopes, _tensors
 from tests.test_tree import _data as _tree_data
 
 pytestmark = pytest.mark.gpu
@@ -114,3 +115,38 @@ def test_a_token_of_one_key_is_its_value(n, Tmax, d, cap):
     o, _ = fa.fwd_tree(q.cuda(), k.cuda(), v.cuda(), torch.zeros(B, dtype=torch.int32, device="cuda"),
                        tree=torch.eye(n, dtype=torch.uint8).cuda(), softcap=cap)
     assert torch.equal(o.cpu(), v[:, :, :n])
+
+
+# ----------------------------------------------------------------- padding in front and between
+
+def _gaps(B, T):
+    """Padding in front of, between and behind ragged documents, other places in each sequence."""
+    rows = []
+    for b in range(B):
+        row, n = [-1] * (45 + 60 * b), b
+        while len(row) < T:
+            row += [n % 7] * (3, 90, 131, 40)[n % 4] + [-1] * (1, 17, 130)[n % 3]
+            n += 1
+        rows.append(row[:T - 20] + [-1] * 20)
+    return torch.tensor(rows, dtype=torch.int32)
+
+
+@pytest.mark.parametrize("with_rest", [False, True])
+@pytest.mark.parametrize("B,H,Hkv", [(2, 4, 2), (4, 80, 10)])
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("causal,cap,bias", [(True, 0.0, False), (False, 0.0, False), (True, 30.0, False),
+                                             (False, 80.0, False), (True, 0.0, True), (True, 30.0, True)])
+def test_padding_anywhere_may_hold_anything(B, H, Hkv, d, causal, cap, bias, with_rest):
+    T = 500
+    q, k, v, do = _tensors(B, H, Hkv, T, d, 51, 4.0 if cap else 1.0)
+    ids = _gaps(B, T)
+    seen = fa.visible(B, T, causal=causal, doc_ids=ids.cuda())
+    sl = _slopes(H) if bias else None
+    r = ref.attention(q, k, v, ref.visible_mask(B, T, causal, ids), d ** -0.5, cap, sl, do)
+    pad = (ids < 0)[:, None, :, None]
+    for x, bad in ((q, math.nan), (k, math.inf), (v, math.nan), (do, -math.inf)):
+        x.masked_fill_(pad, bad)
+    got = _run(q, k, v, do, seen, softcap=cap, slopes=sl, with_rest=with_rest)
+    ref.check(got, r, ALL)
+    for n in ("o", "dq", "dk", "dv"):
+        assert not got[n].masked_fill(~pad.cuda(), 0.0).any(), n
