@@ -463,6 +463,8 @@ __global__ void __launch_bounds__(Cfg1<D, (MOD & kModRef) != 0>::kThreads, 1)
                         static_cast<size_t>(q_row),
                     r0, bh, q_row < p.T, GEN && p.n_splits > 1};
     };
+    // A weight sum of a row that saw no key. (MOD: a score that is no number makes the row's o and LSE none.)
+    auto no_keys = [](float x) { return GEN && (MOD != 0 ? x == 0.0f : !(x > 0.0f)); };
     // The part of 8 values of a row that their rounding to bf16 (hi) leaves out, as bf16.
     auto rest_of = [&](const float* x, const uint4& hi) {
       const uint32_t u[4] = {hi.x, hi.y, hi.z, hi.w};
@@ -546,7 +548,7 @@ __global__ void __launch_bounds__(Cfg1<D, (MOD & kModRef) != 0>::kThreads, 1)
           L += x.x;
           top = fmaxf(top, x.y);
         }
-        const float inv_l = !(L > 0.0f) ? 0.0f : 1.0f / top_rounded(L, top);
+        const float inv_l = no_keys(L) ? 0.0f : 1.0f / top_rounded(L, top);
         uint32_t o[kOutCols];
         static_assert(kOutCols == 16 || kOutCols % 32 == 0, "output columns");
         if constexpr (kOutCols == 16) {
@@ -588,7 +590,7 @@ __global__ void __launch_bounds__(Cfg1<D, (MOD & kModRef) != 0>::kThreads, 1)
             }
           }
         }
-        write_lse(w, !(L > 0.0f) ? -INFINITY : log2f(L) * 0.69314718055994530942f);
+        write_lse(w, no_keys(L) ? -INFINITY : log2f(L) * 0.69314718055994530942f);
         return true;
       } else if constexpr (H == 2) {
         const int par = ne & 1;
@@ -613,7 +615,7 @@ __global__ void __launch_bounds__(Cfg1<D, (MOD & kModRef) != 0>::kThreads, 1)
         const float f0 = (m0 == -INFINITY) ? 0.0f : ex2_approx(m0 - M);
         const float f1 = (m1 == -INFINITY) ? 0.0f : ex2_approx(m1 - M);
         const float L = l0 * f0 + l1 * f1;
-        const float inv_l = (GEN && !(L > 0.0f)) ? 0.0f : 1.0f / L;
+        const float inv_l = no_keys(L) ? 0.0f : 1.0f / L;
         const float w0 = f0 * inv_l, w1 = f1 * inv_l;
         uint32_t o0[32], o1[32];
         tmem_ld32(tmem + lane_off + C::col_o(0) + c_out, o0);
@@ -657,10 +659,10 @@ __global__ void __launch_bounds__(Cfg1<D, (MOD & kModRef) != 0>::kThreads, 1)
             }
           }
         }
-        write_lse(w, (GEN && !(L > 0.0f)) ? -INFINITY : (M + log2f(L)) * 0.69314718055994530942f);
+        write_lse(w, no_keys(L) ? -INFINITY : (M + log2f(L)) * 0.69314718055994530942f);
         return true;
       } else {
-        const float inv_l = (GEN && !(l > 0.0f)) ? 0.0f : 1.0f / l;
+        const float inv_l = no_keys(l) ? 0.0f : 1.0f / l;
         uint8_t* slice = smem + C::kOOff + warp * 4096;
         const uint32_t ob = smem_u32(slice) + lane * 128;
 #pragma unroll 1
@@ -726,7 +728,7 @@ __global__ void __launch_bounds__(Cfg1<D, (MOD & kModRef) != 0>::kThreads, 1)
             bulk_commit_group();
           }
         }
-        write_lse(w, (GEN && !(l > 0.0f)) ? -INFINITY : (m + log2f(l)) * 0.69314718055994530942f);
+        write_lse(w, no_keys(l) ? -INFINITY : (m + log2f(l)) * 0.69314718055994530942f);
         return true;
       }
     };

@@ -745,10 +745,12 @@ __global__ void __launch_bounds__(kThreads, 1)
       write_const_row(w, 0x7FC00000u);
       write_lse(w, __uint_as_float(0x7FC00000u));
     };
+    // A weight sum of a row that saw no key. (MOD: a score that is no number makes the row's o and LSE none.)
+    auto no_keys = [](float x) { return GEN && (MOD != 0 ? x == 0.0f : !(x > 0.0f)); };
     auto lse_of = [&](float l, float m) {
-      return (GEN && !(l > 0.0f)) ? -INFINITY : (m + log2f(l)) * 0.69314718055994530942f;
+      return no_keys(l) ? -INFINITY : (m + log2f(l)) * 0.69314718055994530942f;
     };
-    auto inv_of = [&](float l) { return (GEN && !(l > 0.0f)) ? 0.0f : 1.0f / l; };
+    auto inv_of = [&](float l) { return no_keys(l) ? 0.0f : 1.0f / l; };
     // O_i, already read into registers (D = 64), to the output: each warp stages its 32
     // rows in its own 4 KB slice, 16-byte chunk c of row r at position c ^ (r mod 8) (the
     // map's 128-byte swizzle; conflict-free), and its lane 0 stores them as one 64 × 32

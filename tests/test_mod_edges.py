@@ -1,6 +1,6 @@
 """Modified scores and cached contexts at their edges, on the GPU: keys behind a length that is no
-multiple of a tile, rows that see one key, padding of any value anywhere. Bounds: those of
-mod_reference.py."""
+multiple of a tile, rows that see one key, padding of any value anywhere, values that are not
+numbers. Bounds: those of mod_reference.py."""
 
 import math
 
@@ -150,3 +150,38 @@ def test_padding_anywhere_may_hold_anything(B, H, Hkv, d, causal, cap, bias, wit
     ref.check(got, r, ALL)
     for n in ("o", "dq", "dk", "dv"):
         assert not got[n].masked_fill(~pad.cuda(), 0.0).any(), n
+
+
+# ----------------------------------------------------------------------- values that are no numbers
+
+@pytest.mark.parametrize("B,H,Hkv", [(1, 4, 2), (4, 80, 10)])
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("cap,bias", [(0.0, False), (30.0, False), (80.0, False), (0.0, True), (30.0, True)])
+def test_a_query_that_is_no_number(B, H, Hkv, d, cap, bias):
+    """Its row's o and LSE are none either, as in plain arithmetic; the other rows stay as they are."""
+    T = 260
+    q, k, v, _ = (x.cuda() for x in _tensors(B, H, Hkv, T, d, 61))
+    sl = _slopes(H).cuda() if bias else None
+    rows = torch.tensor([0, 77, 140, T - 1], device="cuda")
+    o, lse = fa.fwd_mod(q, k, v, softcap=cap, slopes=sl)
+    q[:, :, rows, 5] = math.nan
+    o2, lse2 = fa.fwd_mod(q, k, v, softcap=cap, slopes=sl)
+    hit = torch.zeros(T, dtype=torch.bool, device="cuda")
+    hit[rows] = True
+    assert torch.isnan(o2[:, :, hit].float()).all() and torch.isnan(lse2[:, :, hit]).all()
+    assert torch.equal(o2[:, :, ~hit], o[:, :, ~hit]) and torch.equal(lse2[:, :, ~hit], lse[:, :, ~hit])
+
+
+@pytest.mark.parametrize("n", [4, 40])
+@pytest.mark.parametrize("Tmax", [150, 3400])
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("cap", [0.0, 30.0, 80.0])
+def test_a_new_token_that_is_no_number(n, Tmax, d, cap):
+    q, k, v = (x.cuda() for x in _tree_data(2, 4, 4, n, Tmax, d, 63))
+    ctx = torch.tensor([100, Tmax - n], dtype=torch.int32, device="cuda")
+    o, lse = fa.fwd_tree(q, k, v, ctx, softcap=cap)
+    q[:, :, 2, 7] = math.nan
+    o2, lse2 = fa.fwd_tree(q, k, v, ctx, softcap=cap)
+    hit = torch.arange(n, device="cuda") == 2
+    assert torch.isnan(o2[:, :, hit].float()).all() and torch.isnan(lse2[:, :, hit]).all()
+    assert torch.equal(o2[:, :, ~hit], o[:, :, ~hit]) and torch.equal(lse2[:, :, ~hit], lse[:, :, ~hit])
