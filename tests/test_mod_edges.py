@@ -1,6 +1,7 @@
 """Modified scores and cached contexts at their edges, on the GPU: keys behind a length that is no
 multiple of a tile, rows that see one key, padding of any value anywhere, values that are not
-numbers. Bounds: those of mod_reference.py."""
+numbers, forms that the other files' sizes do not reach, records of long batches. Bounds: those of
+mod_reference.py."""
 
 import math
 
@@ -9,8 +10,8 @@ import torch
 
 import exact_attention_23_gb300 as fa
 from tests import mod_reference as ref
-from tests.test_mod import ALL, _run, _slopes, _tensors
-from tests.test_tree import _data as _tree_data
+from tests.test_mod import ALL, _ids, _run, _slopes, _tensors
+from tests.test_tree import _check as _check_tree, _data as _tree_data
 
 pytestmark = pytest.mark.gpu
 
@@ -185,3 +186,104 @@ def test_a_new_token_that_is_no_number(n, Tmax, d, cap):
     hit = torch.arange(n, device="cuda") == 2
     assert torch.isnan(o2[:, :, hit].float()).all() and torch.isnan(lse2[:, :, hit]).all()
     assert torch.equal(o2[:, :, ~hit], o[:, :, ~hit]) and torch.equal(lse2[:, :, ~hit], lse[:, :, ~hit])
+
+
+# ------------------------------------------------------------------ forms not reached elsewhere
+
+@pytest.mark.parametrize("T,lengths,pad,prefix,std", [
+    (300, (100, 1, 47), 30, "b", 9.0), (384, (300, 9), 140, None, 9.0), (290, (60, 200), 0, "t", 2.0),
+])
+@pytest.mark.parametrize("d", [64, 128])
+def test_capped_inference_on_documents(T, d, lengths, pad, prefix, std):
+    """Two query tiles a CTA, capped scores near and far, intervals with both ends, no rest."""
+    B, H, Hkv = 4, 80, 10
+    q, k, v, do = _tensors(B, H, Hkv, T, d, 29 * T + d, std)
+    ids = _ids(B, T, lengths, pad)
+    pre = None
+    if prefix == "b":
+        pre = torch.tensor([60 * b + 7 for b in range(B)], dtype=torch.int32)
+    elif prefix == "t":
+        pre = ((ids + 2) * 23 - 40).to(torch.int32)
+    r = ref.attention(q, k, v, ref.visible_mask(B, T, True, ids, pre), d ** -0.5, 30.0, None, do)
+    seen = fa.visible(B, T, doc_ids=ids.cuda(), prefix_len=None if pre is None else pre.cuda())
+    ref.check(_run(q, k, v, do, seen, softcap=30.0, with_rest=False), r, ALL)
+
+
+@pytest.mark.parametrize("room", [0, 3300])
+@pytest.mark.parametrize("ctx,H,Hkv,n,Tmax,tree,cap,bias", [
+    ([300, 77], 8, 2, 16, 320, True, 30.0, True),       # 64 rows
+    ([129, 0, -1], 12, 3, 33, 200, True, 80.0, True),   # 132 rows: two row blocks
+    ([500], 5, 5, 48, 560, True, 0.0, True),            # flags in whole 16-byte pieces
+    ([63], 5, 5, 50, 130, False, 30.0, True),
+    ([200, 31], 4, 1, 64, 270, True, 80.0, False),
+])
+def test_wide_rows_of_d128(ctx, H, Hkv, n, Tmax, tree, cap, bias, room):
+    _check_tree(ctx, H, Hkv, n, Tmax + room, 128, tree, cap, bias, seed=5)
+
+
+# ------------------------------------------------------------------------ the records of visible
+
+def _records(seen, B, T):
+    """(rows, fwd, pairs, bwd) of a Visible's buffer."""
+    up = lambda x: (x + 255) // 256 * 256
+    n_t = -(-T // 128)
+    at, out = 0, []
+    for count, width in ((B * n_t * 128, 2), (B * n_t, 4), (B * ((n_t + 1) // 2), 8), (B * n_t, 4)):
+        n = count * width * 4
+        out.append(seen.buffer[at:at + n].view(torch.int32).view(B, -1, width).cpu().long())
+        at += up(n)
+    return out
+
+
+@pytest.mark.parametrize("T,lengths,pad,causal,prefix", [
+    (1, (1,), 0, True, False), (129, (40, 50), 3, True, True), (1000, (128, 77), 300, False, False),
+    (33000, (1000, 1, 2048), 129, True, True), (200000, (100, 60000, 17), 5000, True, True),
+    (200000, (100, 60000, 17), 70000, False, False),
+])
+def test_walks_of_tiles(T, lengths, pad, causal, prefix):
+    """Each query tile's K tiles and each key tile's query tiles, once each, the longest first, made
+    from the rows' intervals (which test_mod.py checks); 1563 tiles a sequence at the longest."""
+    B = 2
+    ids = _ids(B, T, lengths, pad)
+    pre = torch.tensor([5, 40000], dtype=torch.int32) if prefix else None
+    seen = fa.visible(B, T, causal=causal, doc_ids=ids.cuda(), prefix_len=None if pre is None else pre.cuda())
+    rows, fwd, pairs, bwd = _records(seen, B, T)
+    n_t = -(-T // 128)
+    for b in range(B):
+        live = rows[b, :, 1] > rows[b, :, 0]
+        padded = torch.tensor([bool((ids[b, 128 * t:128 * (t + 1)] < 0).any()) for t in range(n_t)])
+        pad0 = int(padded.nonzero()[0]) if padded.any() else n_t      # the first tile with padding
+        lo = torch.where(live, rows[b, :, 0], torch.full_like(rows[b, :, 0], T)).view(n_t, 128).amin(1)
+        hi = torch.where(live, rows[b, :, 1], torch.zeros_like(rows[b, :, 1])).view(n_t, 128).amax(1)
+        some = hi > lo
+        zero = torch.zeros_like(lo)
+        k0, k1 = torch.where(some, lo // 128, zero), torch.where(some, (hi + 127) // 128, zero)
+        tile = torch.arange(n_t)
+        assert torch.equal(fwd[b, :, 0].sort().values, tile)
+        assert torch.equal(fwd[b, :, 1], k0[fwd[b, :, 0]]) and torch.equal(fwd[b, :, 2], k1[fwd[b, :, 0]])
+        assert (fwd[b, :, 3] == pad0).all()
+        n = fwd[b, :, 2] - fwd[b, :, 1]
+        assert (n[1:] <= n[:-1]).all()
+        # key tiles: the query tiles whose K tiles hold them
+        meets = some[None] & (lo[None] < 128 * (tile[:, None] + 1)) & (hi[None] > 128 * tile[:, None])
+        q0 = torch.where(meets, tile[None], torch.full_like(tile[None], n_t)).amin(1)
+        q1 = torch.where(meets, tile[None] + 1, torch.zeros_like(tile[None])).amax(1)
+        q0 = torch.where(q1 > 0, q0, zero)
+        assert torch.equal(bwd[b, :, 0].sort().values, tile)
+        assert torch.equal(bwd[b, :, 1], q0[bwd[b, :, 0]]) and torch.equal(bwd[b, :, 2], q1[bwd[b, :, 0]])
+        assert torch.equal(bwd[b, :, 3], 2 * pad0 + padded.long()[bwd[b, :, 0]])
+        n = bwd[b, :, 2] - bwd[b, :, 1]
+        assert (n[1:] <= n[:-1]).all()
+        # pairs
+        n_p = (n_t + 1) // 2
+        first = pairs[b, :, 0]
+        assert torch.equal(first.sort().values, 2 * torch.arange(n_p)) and (pairs[b, :, 1] == pad0).all()
+        k0, k1 = (torch.cat((x, torch.zeros(1, dtype=x.dtype))) for x in (k0, k1))
+        for i, (a, z) in enumerate(((2, 3), (4, 5))):
+            assert torch.equal(pairs[b, :, a], k0[first + i]) and torch.equal(pairs[b, :, z], k1[first + i])
+        empty = [k1[first + i] == k0[first + i] for i in (0, 1)]
+        big = torch.full_like(first, 1 << 30)
+        start = torch.minimum(*(torch.where(e, big, k0[first + i]) for i, e in enumerate(empty)))
+        stop = torch.maximum(*(torch.where(e, torch.zeros_like(big), k1[first + i]) for i, e in enumerate(empty)))
+        n = (stop - start).clamp(min=0)
+        assert (n[1:] <= n[:-1]).all()
