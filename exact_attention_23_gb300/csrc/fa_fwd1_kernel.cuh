@@ -793,7 +793,7 @@ __global__ void __launch_bounds__(Cfg1<D, (MOD & kModRef) != 0>::kThreads, 1)
       // MOD: this row's visible keys [lo, hi) and (BIAS) its head's slope in base 2, negated
       int vlo = 0, vhi = 0;
       float nslope = 0.0f;
-      // TREE: this row's token, its position, and its sequence's context
+      // TREE: this row's token, its position from the end of its sequence's context, and that context
       int tok = 0, ctx = 0;
       float q_at = 0.0f;
       if constexpr (kTree) {
@@ -805,7 +805,7 @@ __global__ void __launch_bounds__(Cfg1<D, (MOD & kModRef) != 0>::kThreads, 1)
         vhi = min(ctx, u.mh);
         if constexpr ((MOD & kModBias) != 0) {
           const int hk = u.bh - u.last[0] * p.mod.list.Hkv;
-          q_at = static_cast<float>(ctx + (p.mod.mask.depths ? p.mod.mask.depths_of(u.last[0], Tq)[tok] : tok));
+          q_at = static_cast<float>(p.mod.mask.depths ? p.mod.mask.depths_of(u.last[0], Tq)[tok] : tok);
           nslope = __ldg(p.mod.slopes + hk * (p.T / Tq) + hg) * -1.4426950408889634f;
         }
       } else if constexpr (MOD != 0) {
@@ -891,7 +891,8 @@ __global__ void __launch_bounds__(Cfg1<D, (MOD & kModRef) != 0>::kThreads, 1)
           // in the key where every key of the step lies at or before the warp's first row (TREE: at or
           // before this row's position, which depths may put anywhere). (A far step, rare, takes
           // the general bias.)
-          const float dist0 = kTree ? q_at - static_cast<float>(k0) : static_cast<float>(q_row - k0);
+          // (distances from differences of integers: positions past 2²⁴ are no fp32 numbers)
+          const float dist0 = kTree ? q_at + static_cast<float>(ctx - k0) : static_cast<float>(q_row - k0);
           const bool left = kTree ? dist0 >= static_cast<float>(kC - 1) : k0 + kC - 1 <= qt * kBlockM + quad * 32;
           const float base = nslope * dist0;
           auto to_exponents = [&]<bool FAR, bool LEFT>() {
@@ -989,7 +990,7 @@ __global__ void __launch_bounds__(Cfg1<D, (MOD & kModRef) != 0>::kThreads, 1)
                 if constexpr ((MOD & kModBias) != 0) {
                   if (depths) {  // from the keys' indices to their positions
                     const int dk = dw + lane;
-                    const float place = static_cast<float>(ctx + (dk < 0 ? dk : depths[min(dk, Tq - 1)]));
+                    const float place = static_cast<float>(dk < 0 ? dk : depths[min(dk, Tq - 1)]);
 #pragma unroll
                     for (int t = 0; t < 32; ++t) {
                       const float at = __shfl_sync(0xffffffffu, place, t);

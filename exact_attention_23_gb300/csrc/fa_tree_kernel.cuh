@@ -159,7 +159,7 @@ __global__ void __launch_bounds__(kTreeBlock, TreeCfg<D>::kCtasPerSm)
     const int r0 = sg.rb * kRows + rg * 16 + qr;    // this thread's rows: r0 and r0 + 8
     int tok[2];
     bool live[2];
-    float nsl[2] = {0.f, 0.f}, at[2] = {0.f, 0.f};
+    float nsl[2] = {0.f, 0.f}, at[2] = {0.f, 0.f};  // (at: positions from the end of the context)
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
       const int r = r0 + 8 * i;
@@ -167,8 +167,7 @@ __global__ void __launch_bounds__(kTreeBlock, TreeCfg<D>::kCtasPerSm)
       const int g = static_cast<int>(p.mask.div_tq.div(static_cast<uint32_t>(live[i] ? r : 0)));
       tok[i] = (live[i] ? r : 0) - g * Tq;
       if constexpr ((MOD & kModBias) != 0) {
-        const int depth = p.mask.depths ? p.mask.depths_of(sg.b, Tq)[tok[i]] : tok[i];
-        at[i] = static_cast<float>(ctx + depth);
+        at[i] = static_cast<float>(p.mask.depths ? p.mask.depths_of(sg.b, Tq)[tok[i]] : tok[i]);
         nsl[i] = p.slopes[sg.hk * (p.R / Tq) + g] * -1.4426950408889634f;
       }
     }
@@ -218,6 +217,8 @@ __global__ void __launch_bounds__(kTreeBlock, TreeCfg<D>::kCtasPerSm)
       __syncwarp();
       if (lane == 0) mbar_arrive(&empty[stk]);
       // ---- scores to base-2 exponents
+      // (BIAS: distances from the end of the context; positions past 2²⁴ are no fp32 numbers)
+      const float behind = static_cast<float>(ctx - key0);
       auto to_exponents = [&]<bool FAR>() {
 #pragma unroll
         for (int j = 0; j < NT; ++j)
@@ -228,7 +229,7 @@ __global__ void __launch_bounds__(kTreeBlock, TreeCfg<D>::kCtasPerSm)
             if constexpr ((MOD & kModCap) != 0) x2 = cap2<FAR>(s2, p.cap);
             else x2 = f2_mul(s2, f2_splat(p.scale_log2));
             if constexpr ((MOD & kModBias) != 0) {
-              const float d0 = at[i] - static_cast<float>(key0 + j * 8 + qc);
+              const float d0 = at[i] + (behind - static_cast<float>(j * 8 + qc));
               x2 = f2_add(x2, f2_pack(nsl[i] * fabsf(d0), nsl[i] * fabsf(d0 - 1.0f)));
             }
             f2_unpack(x2, s[j][2 * i], s[j][2 * i + 1]);
@@ -273,8 +274,7 @@ __global__ void __launch_bounds__(kTreeBlock, TreeCfg<D>::kCtasPerSm)
                 float& x = s[j0 + j][2 * i + e];
                 if constexpr ((MOD & kModBias) != 0) {  // from the key's index to its position
                   if (d >= 0)
-                    x += nsl[i] * (fabsf(at[i] - static_cast<float>(ctx + dep[j][e])) -
-                                   fabsf(at[i] - static_cast<float>(key)));
+                    x += nsl[i] * (fabsf(at[i] - static_cast<float>(dep[j][e])) - fabsf(at[i] - static_cast<float>(d)));
                 }
                 if (key >= keys || (d >= 0 && see[j][e][i] == 0)) x = -INFINITY;
               }

@@ -435,7 +435,7 @@ int fa_rope_append(const void* q, long long q_sb, long long q_sh, long long q_st
  *   tree    : optional DEVICE uint8 [Tq][Tq], or [B][Tq][Tq] with tree_per_batch; NULL: a chain
  *             (tree[t][s] = s ≤ t)
  *   depths  : optional DEVICE int32 [Tq], or [B][Tq] with depths_per_batch; NULL: 0, 1, 2, …;
- *             used by the bias only
+ *             used by the bias only (below 2²⁴ in magnitude; ctx_len has no such limit)
  *   workspace : DEVICE memory of fa_fwd_tree_workspace_size(...) bytes (for the current device; 1:
  *             none is needed, NULL will do; 0: unsupported sizes, or no usable device), 256-byte
  *             aligned, contents immaterial. Not shared with a call that may run at the same time.

@@ -1,7 +1,7 @@
 """Modified scores and cached contexts at their edges, on the GPU: keys behind a length that is no
 multiple of a tile, rows that see one key, padding of any value anywhere, values that are not
-numbers, forms that the other files' sizes do not reach, records of long batches. Bounds: those of
-mod_reference.py."""
+numbers, far positions, forms that the other files' sizes do not reach, records of long batches.
+Bounds: those of mod_reference.py."""
 
 import math
 
@@ -186,6 +186,33 @@ def test_a_new_token_that_is_no_number(n, Tmax, d, cap):
     hit = torch.arange(n, device="cuda") == 2
     assert torch.isnan(o2[:, :, hit].float()).all() and torch.isnan(lse2[:, :, hit]).all()
     assert torch.equal(o2[:, :, ~hit], o[:, :, ~hit]) and torch.equal(lse2[:, :, ~hit], lse[:, :, ~hit])
+
+
+# ------------------------------------------------------------------------------- far positions
+
+@pytest.mark.parametrize("H", [2, 16])                            # streaming kernel, tensor cores
+@pytest.mark.parametrize("d,ctx", [(64, (1 << 25) + 12345), (128, (1 << 24) + 77)])
+def test_bias_behind_16_million_keys(H, d, ctx):
+    """Positions past 2²⁴, which fp32 cannot tell apart: near keys keep their distances."""
+    n, near = 5, 512
+    Tmax = ctx + n + 3
+    q, k, v = _tree_data(1, H, 1, n, near, d, 71)                 # the last rows of the context and the new ones
+    kc, vc = (torch.zeros(1, 1, Tmax, d, dtype=torch.bfloat16, device="cuda") for _ in range(2))
+    first = ctx + n - near
+    kc[:, :, first:ctx + n], vc[:, :, first:ctx + n] = k.cuda(), v.cuda()
+    sl = torch.tensor([0.5 + 0.1 * h for h in range(H)])          # e^−0.5·507 of what lies before
+    dep = torch.tensor([0, 1, 1, 2, 3], dtype=torch.int32)
+    tree = torch.eye(n, dtype=torch.uint8)
+    tree[3, 0] = tree[4, 0] = tree[4, 3] = 1
+    at = ctx + dep.long()[None]
+    ka = torch.arange(first, first + near)[None].clone()
+    ka[0, near - n:] = at[0]
+    ok = torch.ones(1, n, near, dtype=torch.bool)
+    ok[0, :, near - n:] = tree.bool()
+    r = ref.attention(q, k, v, ok, d ** -0.5, 0.0, sl, query_at=at, key_at=ka)
+    o, lse = fa.fwd_tree(q.cuda(), kc, vc, torch.tensor([ctx], dtype=torch.int32, device="cuda"),
+                         tree=tree.cuda(), depths=dep.cuda(), slopes=sl.cuda())
+    ref.check({"o": o, "lse": lse}, r, ("o", "lse"))
 
 
 # ------------------------------------------------------------------ forms not reached elsewhere
