@@ -65,13 +65,19 @@ int block_rows_log2(int R) { return R <= 16 ? 4 : R <= 32 ? 5 : 7; }
 // Chunks a stretch has at least.
 constexpr int kMinPer = 2, kMinPerWide = 1;
 
-// A cache of at most this many chunks goes without stretches where its entries fit the GPU at once,
-// a CTA each: no workspace, no second kernel and launch, which are 3 µs of the host's in every call and
-// most of a short one's time. On the GPU, µs in stretches -> whole: one token, B8 H12 d64, 300 keys 9.5
-// -> 5.6, 600 10.9 -> 8.2, 1000 9.9 -> 11.4; B8 H16 Hkv4 d128, 300 keys 11.0 -> 8.4, 600 9.9 -> 12.2; the
-// wide kernel, d64, B8 64 tokens, 1300 keys 19.3 -> 14.1, d128, B4 16 tokens, 700 keys 13.0 -> 12.1, 1400
-// 14.9 -> 19.2.
-int solo_chunks(bool wide_rows, int d) { return wide_rows ? (d == 64 ? 12 : 8) : d == 64 ? 18 : 10; }
+// Entries that fit the GPU at once go without stretches, a CTA each, where a CTA then walks at most
+// join_chunks more chunks than its stretch would have: what the partials' way through memory and the
+// second kernel are worth. By GPU time, with every context full (µs in stretches / whole, at 64-key
+// chunks, wide 128; cap 30):
+//   one token, d64 (join 7)    8 entries, 6 chunks 6.7 / 6.1, 10 chunks 6.8 / 8.3;  96 entries, 10 chunks
+//                              10.7 / 8.6, 18 chunks 11.6 / 13.2;  456 entries, 24 chunks 35.4 / 30.6
+//   d128 (5)                   8, 4: 8.1 / 7.1, 8: 8.2 / 10.6;  96, 8: 13.8 / 10.9, 12: 11.6 / 14.4;
+//                              304, 24: 43.8 / 40.2
+//   wide, d64, 256 rows (5)    8, 4: 9.4 / 8.5, 8: 9.9 / 12.4;  32, 6: 13.7 / 10.9, 12: 14.6 / 16.9;  128, 12: 29.4 / 17.8
+//   d128, 64 rows (4)          4, 4: 9.9 / 9.8, 6: 9.9 / 12.2;  64, 8: 18.3 / 15.3, 16 entries, 8: 12.9 / 14.9
+// Not beyond the chunks measured: stretches share out unequal contexts, a CTA an entry does not.
+int join_chunks(bool wide_rows, int d) { return wide_rows ? (d == 64 ? 5 : 4) : d == 64 ? 7 : 5; }
+constexpr int kSoloChunks = 24, kSoloChunksWide = 12;
 
 struct TreeSizes {
   int R, rows_log2, row_blocks, chunk_log2, min_per;
@@ -98,7 +104,9 @@ bool tree_sizes(int B, int H, int Hkv, int Tq, int Tmax, int d, int sms, TreeSiz
   const long long most = (z->entries * chunks + z->min_per - 1) / z->min_per;
   const long long fit = static_cast<long long>(sms) *
                         (wide(z->R) ? 1 : d == 64 ? TreeCfg<64>::kCtasPerSm : TreeCfg<128>::kCtasPerSm);
-  z->solo = chunks <= solo_chunks(wide(z->R), d) && z->entries <= fit;
+  const long long per = std::max<long long>(z->min_per, (z->entries * chunks + fit - 1) / fit);  // a stretch's
+  z->solo = z->entries <= fit && chunks <= per + join_chunks(wide(z->R), d) &&
+            chunks <= (wide(z->R) ? kSoloChunksWide : kSoloChunks);
   if (z->solo) {
     z->grid = z->entries;
     z->slots = 0;

@@ -7,6 +7,7 @@ arguments, and looks for what is wrong only when it does not.
 
 from __future__ import annotations
 
+import functools
 import math
 
 import torch
@@ -266,15 +267,14 @@ def fwd_tree_workspace(B: int, H: int, Hkv: int, Tq: int, Tmax: int, d: int, dev
     device = torch.device("cuda" if device is None else device)
     if device.index is None:
         device = torch.device("cuda", torch.cuda.current_device())
-    return torch.empty(_tree_bytes(B, H, Hkv, Tq, Tmax, d, device), dtype=_U8, device=device)
+    return torch.empty(_tree_bytes(B, H, Hkv, Tq, Tmax, d, device.index), dtype=_U8, device=device)
 
 
-def _tree_bytes(B, H, Hkv, Tq, Tmax, d, device):
-    if device.index == torch.cuda.current_device():
+@functools.lru_cache(maxsize=256)
+def _tree_bytes(B, H, Hkv, Tq, Tmax, d, index):
+    """fa_fwd_tree_workspace_size on device ``index``, a function of its arguments alone."""
+    with torch.cuda.device(index):
         n = fa_fwd_tree_workspace_size(B, H, Hkv, Tq, Tmax, d)
-    else:
-        with torch.cuda.device(device):
-            n = fa_fwd_tree_workspace_size(B, H, Hkv, Tq, Tmax, d)
     if n == 0:
         raise FAError(FA_ERR_INVALID_ARG, "fa_fwd_tree_workspace_size")
     return n
@@ -324,7 +324,7 @@ def fwd_tree(q, k_cache, v_cache, ctx_len, tree=None, depths=None, softcap: floa
     else:
         _check_fp32(lse, (B, H, Tq), device, "lse")
     if workspace is None:
-        need = _tree_bytes(B, H, Hkv, Tq, Tmax, d, device)
+        need = _tree_bytes(B, H, Hkv, Tq, Tmax, d, device.index)
         if need > 1:
             workspace = torch.empty(need, dtype=_U8, device=device)
     else:
