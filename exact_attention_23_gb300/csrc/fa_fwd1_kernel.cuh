@@ -62,14 +62,13 @@
 namespace fa {
 
 // REF (kModRef, the softmax against a fixed reference): the parts of a row need no accumulators
-// of their own, so the row's keys can be split over more warps, which hide one another's latency,
-// at either head dim.
-constexpr int kRefParts = 2;
+// of their own, so the row's keys are split over two warps, which hide one another's latency, at
+// either head dim.
 template <int D, bool REF = false>
 struct Cfg1 {
   static_assert(D == 64 || D == 128, "head dim");
   // Softmax halves (parts): two O accumulators fit tensor memory at D = 64 only.
-  static constexpr int kHalves = REF ? kRefParts : (D == 64) ? 2 : 1;
+  static constexpr int kHalves = (REF || D == 64) ? 2 : 1;
   static constexpr int kAcc = REF ? 1 : kHalves;         // O accumulators
   static constexpr int kCols = kBlockN / kHalves;        // keys per softmax warp and step
   static constexpr int kSoftWarps = 4 * kHalves;
@@ -220,8 +219,8 @@ __global__ void __launch_bounds__(Cfg1<D, (MOD & kModRef) != 0>::kThreads, 1)
     mbar_init(&bars->mma_done, 2);
 #pragma unroll
     for (int q = 0; q < 4; ++q) {
-      mbar_init(&bars->xch[q][0], C::kHalves > 2 ? C::kHalves : 2);
-      mbar_init(&bars->xch[q][1], C::kHalves > 2 ? C::kHalves : 2);
+      mbar_init(&bars->xch[q][0], 2);
+      mbar_init(&bars->xch[q][1], 2);
     }
     bars->abort = 0u;
     fence_mbar_init();
@@ -550,18 +549,11 @@ __global__ void __launch_bounds__(Cfg1<D, (MOD & kModRef) != 0>::kThreads, 1)
         }
         const float inv_l = no_keys(L) ? 0.0f : 1.0f / top_rounded(L, top);
         uint32_t o[kOutCols];
-        static_assert(kOutCols == 16 || kOutCols % 32 == 0, "output columns");
-        if constexpr (kOutCols == 16) {
-          tmem_ld16(t_o + c_out, o);
-          tmem_ld_wait();
-          reg_fence16(o);
-        } else {
 #pragma unroll
-          for (int c0 = 0; c0 < kOutCols; c0 += 32) tmem_ld32(t_o + c_out + c0, o + c0);
-          tmem_ld_wait();
+        for (int c0 = 0; c0 < kOutCols; c0 += 32) tmem_ld32(t_o + c_out + c0, o + c0);
+        tmem_ld_wait();
 #pragma unroll
-          for (int c0 = 0; c0 < kOutCols; c0 += 32) reg_fence32(o + c0);
-        }
+        for (int c0 = 0; c0 < kOutCols; c0 += 32) reg_fence32(o + c0);
         tc_fence_before_sync();
         __syncwarp();
         if (lane == 0) mbar_arrive(&bars->o_free);
@@ -1103,12 +1095,8 @@ __global__ void __launch_bounds__(Cfg1<D, (MOD & kModRef) != 0>::kThreads, 1)
         }
         FA1_TRACE(44, j);
         const uint32_t t_p = tmem + lane_off + C::col_p(b) + half * (kC / 2);
-        if constexpr (kC == 32) {
-          tmem_st16(t_p, pk);
-        } else {
 #pragma unroll
-          for (int c0 = 0; c0 < kC / 2; c0 += 32) tmem_st32(t_p + c0, pk + c0);
-        }
+        for (int c0 = 0; c0 < kC / 2; c0 += 32) tmem_st32(t_p + c0, pk + c0);
         tmem_st_wait();
         tc_fence_before_sync();
         __syncwarp();
