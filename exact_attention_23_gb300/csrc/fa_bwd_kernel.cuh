@@ -364,14 +364,15 @@ __global__ void __launch_bounds__(256) fa_bwd_dq_kernel(const float* __restrict_
   }
 }
 
-// dK and dV = the sums of their parts' fp32 rows, as bf16: part_out is [2][parts][n], 8 values a
-// thread and step.
-static __global__ void __launch_bounds__(256) fa_bwd_sum_kernel(const float* __restrict__ part_out,
-                                                                __nv_bfloat16* __restrict__ dk,
-                                                                __nv_bfloat16* __restrict__ dv, size_t n,
-                                                                int parts) {
+// dK and dV = the sums of their parts' fp32 rows, as bf16: part_out is [2][parts][rows][D], 8 values
+// a thread and step. (A template, so that only the files that launch it hold it.)
+template <int D>
+__global__ void __launch_bounds__(256) fa_bwd_sum_kernel(const float* __restrict__ part_out,
+                                                         __nv_bfloat16* __restrict__ dk,
+                                                         __nv_bfloat16* __restrict__ dv, size_t rows, int parts) {
   pdl_wait();
   pdl_launch_dependents();
+  const size_t n = rows * D;
   const size_t stride = (size_t)gridDim.x * blockDim.x * 8;
   for (size_t x = ((size_t)blockIdx.x * blockDim.x + threadIdx.x) * 8; x < 2 * n; x += stride) {
     const bool is_dv = x >= n;

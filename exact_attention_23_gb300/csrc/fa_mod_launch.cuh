@@ -45,9 +45,9 @@ cudaError_t launch_bwd_mod(const BwdLaunch& a, int q_heads) {
                  a.p);
   if (e != cudaSuccess) return e;
   if (a.p.mod.parts > 1) {
-    const size_t elems = static_cast<size_t>(a.p.BH / a.p.mod.parts) * a.p.T * D;
+    const size_t rows = static_cast<size_t>(a.p.BH / a.p.mod.parts) * a.p.T;
     const float* part_out = a.p.mod.part_out;
-    e = launch_pdl(fa_bwd_sum_kernel, a.grid_dq, 256, 0, a.stream, part_out, a.p.dk, a.p.dv, elems, a.p.mod.parts);
+    e = launch_pdl(fa_bwd_sum_kernel<D>, a.grid_dq, 256, 0, a.stream, part_out, a.p.dk, a.p.dv, rows, a.p.mod.parts);
     if (e != cudaSuccess) return e;
   }
   return launch_pdl(fa_bwd_dq_kernel<D>, a.grid_dq, 256, 0, a.stream, a.p.dq_acc, a.dq, a.p.T, a.p.n_qt,
