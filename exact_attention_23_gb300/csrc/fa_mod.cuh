@@ -49,7 +49,10 @@ constexpr int kModTree = 8;  // new tokens against a cache (fa_tree_walk.cuh)
 // (tanh.approx.f32 has a relative error of 2⁻¹¹: 0.02 of a score at a cap of 50.) The polynomial
 // takes six packed operations a pair of scores and none of the MUFU's, which the softmax's own
 // exponentials fill (8 cycles a warp and score); the exponential form takes two MUFU operations a
-// score more. A warp takes it, for a whole step, only where one of its scores needs it.
+// score more. A warp takes it, for the columns that it decides for at once (32, or a step's), where
+// one of its scores needs it. How often goes by the scores and the cap: with scores of deviation 4
+// never at caps of 30 and 50, at 20 in 12 % of the 32s and 38 % of the 128s, at 10 always (forward,
+// B1 H12 T16384 d64, 575, 827 and 2187 µs; backward, B2 H16 T4096 d128, 422, 457 and 446).
 //
 // Capped scores are bounded, so a cap of up to 60 needs no running maximum (kModRef): 2^x for
 // |x| ≤ kCapRef is at most 2⁸⁸ and at least 2⁻⁸⁸, and neither sums of 2²⁰ such terms times bf16

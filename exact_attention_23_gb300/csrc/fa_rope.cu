@@ -9,8 +9,9 @@
 // position 10⁶ an fp32 step is 0.06 rad), so it is kept as a fixed-point fraction of a turn:
 // frequency / 2π in units of 2⁻⁶⁴ turns, multiplied by the integer position modulo 2⁶⁴, which
 // drops whole turns exactly. The top 32 bits are the angle within ±π, where __cosf and __sinf are
-// within 2⁻²¹ of the values: against the results' rounding to bf16, 2⁻⁹ of theirs, no choice of
-// the slower functions could show.
+// within 2⁻²¹. That is absolute: a result is within 2⁻²⁰·m·(|a| + |b|) before its rounding to bf16,
+// beside which the slower functions would show only where a·cos − b·sin cancels to less than
+// 2⁻¹¹·(|a| + |b|).
 // Each block makes the fixed-point frequencies once, in shared memory: five fp64 operations a
 // pair, of which an SM does two lanes a clock (every thread making its own took 13 of the 20 µs
 // of B4 H12+12 T1024 d64).

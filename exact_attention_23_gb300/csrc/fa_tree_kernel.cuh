@@ -8,19 +8,19 @@
 // head's work is R = (H / Hkv)·Tq query rows against its sequence: q, o and lse, [B, H, Tq, D] in
 // memory, are [B·Hkv, R, D] as they stand.
 //
-// Bound: the keys are read once for a row block of up to 64 rows, 4·R FLOP a byte: memory
-// bandwidth, as long as the products and the softmax of 64 rows keep up with it. So the kernel is
-// a streaming kernel: per CTA a TMA producer warp runs a ring of tiles, the K and then the V of
-// each chunk of 64 keys, completed on mbarriers, in front of four compute warps, and two or three
-// CTAs share an SM.
+// Here: key heads of up to 32 rows, in one row block of 16 or 32 (more go to the tensor-core kernel).
 //
-// Products on mma.sync m16n8k16: a row block has 16, 32 or 64 rows, and a tcgen05 product has at
-// least 64 rows on tensor memory lanes that only the same quarter of the warps can read, so at 16
-// rows its softmax would run on 16 lanes of one warp. Here a warp owns 16 rows and their state in
-// registers: RG = rows / 16 row groups times KG = 4 / RG key groups, a key group taking its
-// quarter (half, all) of each chunk with a running maximum, sum and O of its own, merged once per
-// segment through shared memory. K is read as B fragments by ldmatrix, V by ldmatrix.trans, both
-// conflict-free out of the 128-byte-swizzled boxes that TMA writes.
+// Bound: the keys are read once, 4·R FLOP a byte: memory bandwidth. So the kernel is a streaming
+// kernel: per CTA a TMA producer warp runs a ring of tiles, the K and then the V of each chunk of 64
+// keys, completed on mbarriers, in front of four compute warps, and two or three CTAs share an SM.
+//
+// Products on mma.sync m16n8k16: a tcgen05 product has at least 64 rows on tensor memory lanes that
+// only the same quarter of the warps can read, so at 16 rows its softmax would run on 16 lanes of
+// one warp. Here a warp owns 16 rows and their state in registers: RG = 1 or 2 row groups times
+// KG = 4 / RG key groups, a key group taking its quarter or half of each chunk with a running maximum,
+// sum and O of its own, merged once per segment through shared memory. K is read as B fragments by
+// ldmatrix, V by ldmatrix.trans, both conflict-free out of the 128-byte-swizzled boxes that TMA
+// writes.
 #pragma once
 
 #include "fa_fwd_kernel.cuh"

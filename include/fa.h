@@ -357,9 +357,9 @@ int fa_fwd_mod(const void* q, const void* k, const void* v, void* o, float* lse,
  *   dQ = scale · dS K,   dK = scale · dSᵀ Q,   dV = Pᵀ dO,
  * dK and dV summed over the query heads that share a key head. D is what a row's dP is measured
  * from, so where one key takes most of a row's weight, the rounding of o decides how exact dQ and
- * dK are: with the forward's rest (else NULL) D is taken from o + rest (83 tokens in three
- * documents, scores of standard deviation 4: dQ's error 2.5e-3 of its norm instead of 4.4e-3,
- * the rounding of dQ itself being 1.7e-3). visible, causal, softcap, slopes
+ * dK are: with the forward's rest (else NULL) D is taken from o + rest (the worst of 120 shapes with
+ * scores of standard deviation 4: dQ's error 2.8e-3 of its norm instead of 6.3e-3, the rounding of
+ * dQ itself being 1.7e-3). visible, causal, softcap, slopes
  * and scale are those of the forward. workspace: fa_bwd_mod_workspace_size(...) bytes (0:
  * unsupported sizes), 256-byte aligned, otherwise as for fa_bwd. dQ is summed with atomic adds in an unspecified order (equal
  * within fp32 rounding from call to call, as fa_bwd's); dK and dV are the same bits every time.
@@ -380,7 +380,10 @@ int fa_bwd_mod(const void* q, const void* k, const void* v, const void* o, const
  * n · inv_freq[i] and multiplied by mscale; the rest of the head is copied.
  *
  *   inv_freq  : DEVICE double [rot_dim/2], radians per position (scaled for long contexts by
- *               whoever makes it); the angle keeps 2⁻⁶⁴ of a turn at every int32 position
+ *               whoever makes it). Whole turns are dropped exactly at every int32 position: the
+ *               angle is off by the position times the frequency's rounding (2⁻⁵² of it, 2⁻⁶⁵ of
+ *               a turn) and by fp32's step, 2⁻²⁶ of a turn. Before their rounding to bf16 a
+ *               pair's results are within 2⁻²⁰ · mscale · (|a| + |b|)
  *   rot_dim   : a multiple of 16, 16 … d
  *   positions : DEVICE int32 [T], or [B][T] with positions_per_batch, or NULL (see each call)
  *   (none of these may lie in an output)
@@ -420,6 +423,9 @@ int fa_rope_append(const void* q, long long q_sb, long long q_sh, long long q_st
  * ---------------------------------------------------------------------------------------
  * fa_fwd_tree — new tokens against a cache: one decoded token a sequence, a chain of them (a
  * chunk of a prompt), or the nodes of a tree of drafted tokens, each of which sees its ancestors.
+ * (Every new token walks all keys of its sequence, later tokens' among them: a prompt of 2048 tokens
+ * into an empty cache takes 2.7 times fa_fwd_mod's time, H12 d64 45 µs and 16. One that has the
+ * cache to itself is better given to fa_fwd_mod.)
  *
  * Sequence b holds ctx_len[b] tokens in rows 0 … ctx_len[b] − 1 of the caches [B, Hkv, Tmax, d],
  * and its Tq new tokens' keys and values, already written (fa_rope_append), in the rows behind:
@@ -440,7 +446,8 @@ int fa_rope_append(const void* q, long long q_sb, long long q_sh, long long q_st
  *             none is needed, NULL will do; 0: unsupported sizes, or no usable device), 256-byte
  *             aligned, contents immaterial. Not shared with a call that may run at the same time.
  *
- * Cache rows behind a sequence's last new token may hold anything, NaN included.
+ * Cache rows behind a sequence's last new token may hold anything, NaN included; the new tokens'
+ * own rows must be finite, seen or not.
  */
 size_t fa_fwd_tree_workspace_size(int B, int H, int Hkv, int Tq, int Tmax, int d);
 int fa_fwd_tree(const void* q, const void* k_cache, const void* v_cache, void* o, float* lse,
