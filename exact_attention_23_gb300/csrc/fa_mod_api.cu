@@ -401,19 +401,17 @@ int fa_fwd_mod(const void* q, const void* k, const void* v, void* o, float* lse,
     cap_factors(-scale, softcap, &cap);
   }
   // Two query tiles a CTA, as in the dense forward, where every SM gets 1.5 such units (one tile ->
-  // two tiles in µs; d64 H12, d128 H16 Hkv4):
-  //   plain, causal: d64 B3 T2048 (1.9 units an SM) 35 -> 31, d128 B1 T4096 (1.7) 79 -> 57; 1.3 units
-  //     of long walks, d64 B1 T4096, 42.0 -> 44.2
-  //   capped: d64 B3 T2048 46 -> 44, with eight documents and o's rest 34 -> 31, B1 T4096 (1.3) 60 -> 66;
-  //     d128 B1 T4096 91 -> 76, eight documents 41 -> 36; T8192 (3.4) with o's rest 343 -> 286, 112 -> 93
-  // or, plain with a visibility at d = 64, whose walks may be short, 2.5 of them: B4 T2048 (2.5)
-  // prefixes 49 -> 43 but eight documents 33 -> 36, B1 T8192 135 -> 123 and 53.5 -> 54.5.
+  // two tiles in µs; d64 H12, d128 H16 Hkv4; causal, eight documents, a prefix of a third):
+  //   plain   d64 B3 T2048 (1.9 units an SM) 34 -> 30, 14.7 -> 12.9, 37 -> 34; d128 B1 T4096 (1.7) 76 -> 55,
+  //           22 -> 20, 89 -> 65; below, d64 B2 T2048 (1.3) 26 -> 25, 11.3 -> 12.8, 29 -> 25, B1 T4096 (1.3) 42
+  //           -> 44, 13.4 -> 12.8, 47 -> 44, d128 T2048 (0.8) 24 -> 31, 11.6 -> 10.0, 29 -> 30
+  //   capped  d64 B3 T2048 46 -> 40, 17.5 -> 15.4, 50 -> 47; d128 B1 T4096 86 -> 73, 25 -> 23, 100 -> 85, T8192
+  //           (3.4) with o's rest 328 -> 282, 78 -> 64, 367 -> 334; below, d64 B1 T4096 56 -> 61, 16.5 ->
+  //           15.3, 63 -> 62, d128 T2048 27 -> 40, 12.9 -> 11.3, 33 -> 40
   // Not with a bias (d64 T4096 204 -> 204, d128 T8192 328 -> 448) or a cap above 60, whose in-place
   // scores do not fit its registers.
   const bool plain = (mod & ~fa::kModRest) == fa::kModOn;
-  const int halves = plain && visible && d == 64 ? 5 : 3;
-  const bool pairs = static_cast<long long>((n_t + 1) / 2) * BH * 2 >= static_cast<long long>(halves) * sms &&
-                     (plain || (mod & fa::kModRef));
+  const bool pairs = static_cast<long long>((n_t + 1) / 2) * BH * 2 >= 3ll * sms && (plain || (mod & fa::kModRef));
   a.p.n_units = pairs ? (n_t + 1) / 2 : n_t;
   a.p.total_units = a.p.n_units * BH;
   a.p.n_kv = n_t;
