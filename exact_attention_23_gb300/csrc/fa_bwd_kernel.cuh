@@ -633,8 +633,7 @@ __global__ void __launch_bounds__(BwdCfg<D, MOD>::kThreads, 1)
     if constexpr (MOD != 0) {
       if (ok && wk.key_pad) {
         const int2* iv = p.mod.rows + (size_t)(bh / p.mod.Hkv) * p.T_pad + (size_t)j * 128;
-        zero_padding(k_s, D / 64, C::kBox, 128, iv);
-        zero_padding(v_s, D / 64, C::kBox, 128, iv);
+        zero_padding(k_s, 2 * (D / 64), C::kBox, 128, iv);  // (K, and V behind it)
       }
     }
     int ti = 0;  // MOD: the step's query tile within the walk
@@ -645,8 +644,7 @@ __global__ void __launch_bounds__(BwdCfg<D, MOD>::kThreads, 1)
         if (++ti == wk.n_i) ti = 0;
         if (i >= wk.pad0 && bars->whole[st] == 2u) {
           const int2* iv = reinterpret_cast<const int2*>(sm + C::kVec + st * C::kVecBytes + 2 * C::kBQ * 4);
-          zero_padding(q_s(st), D / 64, C::kQBox, C::kBQ, iv);
-          zero_padding(do_s(st), D / 64, C::kQBox, C::kBQ, iv);
+          zero_padding(q_s(st), 2 * (D / 64), C::kQBox, C::kBQ, iv);  // (Q, and dO behind it)
         }
       }
       if (t > 0 && !(ok = bwd_wait<MOD>(&bars->s_free, (t - 1) & 1, wc))) break;

@@ -382,9 +382,9 @@ __global__ void __launch_bounds__(Cfg1<D, (MOD & kModRef) != 0>::kThreads, 1)
           if (!mbar_wait_warp(&bars->v_full[st], (g / C::kStages) & 1, wc)) { ok = false; break; }
           if constexpr (MOD != 0 && !kTree) {
             if (u.kb + j >= u.mh)
-              zero_padding(v_base + st * C::kTileBytes, C::kSub, C::kSubBytes, kBlockN,
-                           p.mod.rows + p.mod.div_h.div(static_cast<uint32_t>(u.bh)) * static_cast<size_t>(p.mod.T_pad) +
-                               (u.kb + j) * kBlockN);
+              zero_padding_called(v_base + st * C::kTileBytes, C::kSub, C::kSubBytes, kBlockN,
+                                  p.mod.rows + p.mod.div_h.div(static_cast<uint32_t>(u.bh)) * static_cast<size_t>(p.mod.T_pad) +
+                                      (u.kb + j) * kBlockN);
           }
           if constexpr (kTree) {
             // Rows behind the sequence's keys may hold anything: their P is 0, and 0 · NaN must not

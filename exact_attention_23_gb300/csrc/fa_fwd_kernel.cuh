@@ -625,9 +625,9 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (!wait_w(&bars->v_full[st], (g / C::kStages) & 1, wc)) { ok = false; break; }
           if constexpr (MOD != 0) {
             if (us.kt >= u.mh)
-              zero_padding(v_base + st * C::kTileBytes, C::kSub, C::kSubBytes, kBlockN,
-                           p.mod.rows + p.mod.div_h.div(static_cast<uint32_t>(u.bh)) * static_cast<size_t>(p.mod.T_pad) +
-                               us.kt * kBlockN);
+              zero_padding_called(v_base + st * C::kTileBytes, C::kSub, C::kSubBytes, kBlockN,
+                                  p.mod.rows + p.mod.div_h.div(static_cast<uint32_t>(u.bh)) * static_cast<size_t>(p.mod.T_pad) +
+                                      us.kt * kBlockN);
           }
 #pragma unroll
           for (int i = 0; i < 2; ++i) {
