@@ -303,7 +303,12 @@ int bwd_parts(int B, int H, int Hkv, int T) {
   return parts;
 }
 
-constexpr long long kFewCtas = 1100;
+// CTAs of the backward up to which all heads' units go out together (fa_bwd_mod). In L2-sized groups ->
+// together, µs, five and two documents and causal: 512 CTAs (H16 Hkv4 T8192 d128) 361 -> 297, 608 -> 458, 651
+// -> 649; 1280 (H20 T8192 d128) 394 -> 363, 632 -> 548, 792 -> 786, (H10 T16384 d64, cap 30) 401 -> 369, 737
+// -> 665, 1077 -> 1064; 1408 (H22) 402 -> 406, 640 -> 606, 875 -> 864, (H11) 404 -> 405, 743 -> 731, 1188 -> 1167;
+// 1536 (B2 H12) 433 -> 448, 656 -> 659, 944 -> 940; 2048 (B2 H16) 569 -> 613, 866 -> 881, 1250 -> 1252.
+constexpr long long kFewCtas = 1400;
 
 bool any_misaligned(std::initializer_list<const void*> ps) {
   for (const void* x : ps)
@@ -523,9 +528,8 @@ int fa_bwd_mod(const void* q, const void* k, const void* v, const void* o, const
   a.p.n_qt = T_pad / bq;
   a.p.n_kt = n_t;
   // Heads whose units go out together, the longest walks first: with few CTAs all of them, since
-  // a long walk that starts late is the call's tail (H16 Hkv4 T8192 d128 capped, five
-  // documents: 496 -> 476 µs); otherwise as many as keep their Q and dO (bf16) and dQ accumulator (fp32) in half
-  // the L2, 64 MB.
+  // a long walk that starts late is the call's tail; otherwise as many as keep their Q and dO (bf16)
+  // and dQ accumulator (fp32) in half the L2, 64 MB.
   const long long per_head = 8LL * T_pad * d * (H / Hkv / parts);
   const long long in_l2 = std::max<long long>(1, (64LL << 20) / per_head);
   const bool few = static_cast<long long>(n_t) * a.p.BH <= kFewCtas;
