@@ -8,7 +8,8 @@ per-row natural-log logsumexp in fp32. ``fwd_kv`` attends Tq queries to Tk ≥ T
 ``bwd(q, k, v, o, lse, do, causal)`` returns the gradients (dq, dk, dv) (d = 64 or 128).
 ``fwd_mod`` and ``bwd_mod`` are attention with modified scores (a tanh cap, a bias by distance,
 documents and prefixes through ``visible``, key heads shared by query heads) and its gradients;
-``rope`` and ``rope_append`` turn queries and keys by their positions, and ``fwd_tree`` attends
+``rope`` and ``rope_append`` turn queries and keys by their positions (``norm_rope`` and
+``norm_rope_append`` after a norm of each head's row, ``norm_rope_bwd`` the way back), and ``fwd_tree`` attends
 new tokens (one, a chain, a tree of drafts) to a cache of ragged contexts.
 The work is done by the CUDA kernels of ``libfa.so`` through its C ABI (include/fa.h);
 this module only allocates outputs and workspace with PyTorch and passes pointers and the
@@ -47,6 +48,10 @@ from ._binding import (  # noqa: F401
     fa_fwd_mod,
     fa_fwd_tree,
     fa_fwd_tree_workspace_size,
+    fa_norm_rope,
+    fa_norm_rope_append,
+    fa_norm_rope_bwd,
+    fa_norm_rope_bwd_workspace_size,
     fa_rope,
     fa_rope_append,
     fa_visible,
@@ -316,6 +321,7 @@ def q_tiles(T: int, rows: int = 128) -> int:
 # The operators of ops.py, imported with torch on their first use.
 _OPS = ("Visible", "visible", "fwd_mod", "bwd_mod_workspace", "bwd_mod",
         "rope_inv_freq", "rope", "rope_append",
+        "norm_rope", "norm_rope_bwd_workspace", "norm_rope_bwd", "norm_rope_append",
         "fwd_tree_workspace", "fwd_tree")
 
 

@@ -30,7 +30,8 @@ EXPORTS = ("fa_fwd", "fa_fwd_ex", "fa_fwd_fp8", "fa_fwd_host_workspace_size", "f
            "fa_fwd_block_sparse", "fa_bwd_workspace_size", "fa_bwd", "fa_bwd_ex",
            "fa_bwd_noalloc", "fa_visible_size", "fa_visible", "fa_fwd_mod", "fa_bwd_mod",
            "fa_bwd_mod_workspace_size", "fa_rope",
-           "fa_rope_append", "fa_fwd_tree_workspace_size", "fa_fwd_tree", "fa_strerror", "fa_version")
+           "fa_rope_append", "fa_norm_rope", "fa_norm_rope_append", "fa_norm_rope_bwd_workspace_size",
+           "fa_norm_rope_bwd", "fa_fwd_tree_workspace_size", "fa_fwd_tree", "fa_strerror", "fa_version")
 
 _lock = threading.Lock()
 _lib = None
@@ -98,6 +99,16 @@ def lib() -> ctypes.CDLL:
             L.fa_rope_append.argtypes = (src + [vp] + src + src + [vp, vp, vp, vp, i, vp, i, i, f]
                                          + [i] * 6 + [vp])
             L.fa_rope_append.restype = i
+            L.fa_norm_rope.argtypes = (src + [vp] + src + [vp, vp, vp, f, vp, i, vp, i, i, f] + [i] * 5 + [vp])
+            L.fa_norm_rope.restype = i
+            L.fa_norm_rope_append.argtypes = (src + [vp] + src + src + [vp, vp, f, vp, vp, vp, vp, i, vp, i, i, f]
+                                              + [i] * 6 + [vp])
+            L.fa_norm_rope_append.restype = i
+            L.fa_norm_rope_bwd_workspace_size.argtypes = [i]
+            L.fa_norm_rope_bwd_workspace_size.restype = sz
+            L.fa_norm_rope_bwd.argtypes = (src + src + [vp] + src + src + [vp] + [vp] * 4
+                                           + [f, vp, i, vp, i, i, f] + [i] * 5 + [vp, sz, vp])
+            L.fa_norm_rope_bwd.restype = i
             L.fa_fwd_tree_workspace_size.argtypes = [i] * 6
             L.fa_fwd_tree_workspace_size.restype = sz
             L.fa_fwd_tree.argtypes = ([vp] * 7 + [i, vp, i, f, vp] + [i] * 6 + [f, vp, sz, vp, ull, vp])
@@ -224,6 +235,39 @@ def fa_rope_append(q, q_strides, q_out, k, k_strides, v, v_strides, k_cache, v_c
                                 v_cache, ctx_len, positions, int(positions_per_batch), inv_freq,
                                 rot_dim, int(interleaved), float(mscale), B, H, Hkv, Tq, Tmax, d,
                                 stream)
+
+
+def fa_norm_rope(q, q_strides, q_out, k, k_strides, k_out, q_weight, k_weight, eps, positions,
+                 positions_per_batch, inv_freq, rot_dim, interleaved, mscale, B, H, Hkv, T, d,
+                 stream) -> int:
+    """Strides as for fa_rope."""
+    return lib().fa_norm_rope(q, *q_strides, q_out, k, *k_strides, k_out, q_weight, k_weight,
+                              float(eps), positions, int(positions_per_batch), inv_freq, rot_dim,
+                              int(interleaved), float(mscale), B, H, Hkv, T, d, stream)
+
+
+def fa_norm_rope_append(q, q_strides, q_out, k, k_strides, v, v_strides, q_weight, k_weight, eps,
+                        k_cache, v_cache, ctx_len, positions, positions_per_batch, inv_freq, rot_dim,
+                        interleaved, mscale, B, H, Hkv, Tq, Tmax, d, stream) -> int:
+    return lib().fa_norm_rope_append(q, *q_strides, q_out, k, *k_strides, v, *v_strides, q_weight,
+                                     k_weight, float(eps), k_cache, v_cache, ctx_len, positions,
+                                     int(positions_per_batch), inv_freq, rot_dim, int(interleaved),
+                                     float(mscale), B, H, Hkv, Tq, Tmax, d, stream)
+
+
+def fa_norm_rope_bwd_workspace_size(d) -> int:
+    return int(lib().fa_norm_rope_bwd_workspace_size(d))
+
+
+def fa_norm_rope_bwd(gq, gq_strides, q, q_strides, dq, gk, gk_strides, k, k_strides, dk, q_weight,
+                     k_weight, dq_weight, dk_weight, eps, positions, positions_per_batch, inv_freq,
+                     rot_dim, interleaved, mscale, B, H, Hkv, T, d, workspace, workspace_bytes,
+                     stream) -> int:
+    return lib().fa_norm_rope_bwd(gq, *gq_strides, q, *q_strides, dq, gk, *gk_strides, k, *k_strides,
+                                  dk, q_weight, k_weight, dq_weight, dk_weight, float(eps), positions,
+                                  int(positions_per_batch), inv_freq, rot_dim, int(interleaved),
+                                  float(mscale), B, H, Hkv, T, d, workspace, int(workspace_bytes),
+                                  stream)
 
 
 def fa_fwd_tree_workspace_size(B, H, Hkv, Tq, Tmax, d) -> int:

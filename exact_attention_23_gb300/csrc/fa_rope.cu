@@ -26,20 +26,13 @@
 #include <cuda_runtime.h>
 #include <stdint.h>
 
-#include <algorithm>
-#include <cmath>
-
 #include "fa.h"
 #include "fa_host.h"
 #include "fa_pdl.h"
+#include "fa_rope.cuh"
 #include "sm103.cuh"
 
 namespace fa {
-
-struct RopeSrc {
-  const __nv_bfloat16* p;
-  long long sb, sh, st;  // strides in elements
-};
 
 struct RopeParams {
   RopeSrc q, k, v;
@@ -62,23 +55,13 @@ constexpr int kRopeThreads = 128;
 constexpr int kRopeBlocks = 8;
 constexpr int kRopeFlight = 4;  // heads whose loads a thread keeps in flight
 
-__device__ __forceinline__ void unpack8(const uint4& w, float* f) {
-  const uint32_t u[4] = {w.x, w.y, w.z, w.w};
-#pragma unroll
-  for (int e = 0; e < 4; ++e) {
-    f[2 * e] = __uint_as_float(u[e] << 16);
-    f[2 * e + 1] = __uint_as_float(u[e] & 0xFFFF0000u);
-  }
-}
-
 template <bool INTER, bool APPEND>
 __global__ void __launch_bounds__(kRopeThreads, kRopeBlocks) fa_rope_kernel(const RopeParams p) {
   __shared__ unsigned long long turns[64];  // turns a position, in 2⁻⁶⁴
   pdl_wait();
   pdl_launch_dependents();
   if (threadIdx.x < 8 * p.rot_units) {
-    const double f = p.inv_freq[threadIdx.x] * 0.15915494309189533577;  // 1 / 2π
-    turns[threadIdx.x] = __double2ull_rn((f - floor(f)) * 18446744073709551616.0);
+    turns[threadIdx.x] = turns_of(p.inv_freq[threadIdx.x]);
   }
   __syncthreads();
   const unsigned ch = blockIdx.x / p.n_blocks;
@@ -108,8 +91,7 @@ __global__ void __launch_bounds__(kRopeThreads, kRopeBlocks) fa_rope_kernel(cons
     const long long pos = p.positions ? p.positions[p.pos_per_batch ? row : t] : static_cast<long long>(ctx) + t;
 #pragma unroll
     for (int e = 0; e < 8; ++e) {
-      const unsigned long long a = turns[u * 8 + e] * static_cast<unsigned long long>(pos);
-      const float x = static_cast<float>(static_cast<int>(a >> 32)) * 1.4629180792671596e-9f;  // 2π·2⁻³²
+      const float x = angle_of(turns[u * 8 + e], pos);
       cs[e] = __cosf(x) * p.mscale;
       sn[e] = __sinf(x) * (p.mscale * p.sign);
     }
@@ -171,21 +153,6 @@ namespace {
 
 using namespace fa::host;
 
-// The bytes a strided [B, heads, T, d] source spans, or 0 when its strides are not usable
-// (negative, or rows that a 16-byte vector cannot read).
-size_t span_bytes(const RopeSrc& s, int B, int heads, int T, int d) {
-  if (s.sb < 0 || s.sh < 0 || s.st < 0 || (s.sb & 7) || (s.sh & 7) || (s.st & 7)) return 0;
-  constexpr long long kMax = 1LL << 60;
-  if ((B > 1 && s.sb > kMax / B) || (heads > 1 && s.sh > kMax / heads) || (T > 1 && s.st > kMax / T))
-    return 0;
-  return static_cast<size_t>((B - 1) * s.sb + (heads - 1) * s.sh + (T - 1) * s.st + d) * 2;
-}
-
-bool contiguous(const RopeSrc& s, int B, int heads, int T, int d) {
-  return (T == 1 || s.st == d) && (heads == 1 || s.sh == static_cast<long long>(T) * d) &&
-         (B == 1 || s.sb == static_cast<long long>(heads) * T * d);
-}
-
 int rope_launch(RopeParams& p, bool append, int interleaved, int d, void* stream) {
   int dev = -1, sms = 0;
   const int st = check_device(&dev, &sms);
@@ -208,23 +175,6 @@ int rope_launch(RopeParams& p, bool append, int interleaved, int d, void* stream
                     : (interleaved ? &fa_rope_kernel<true, false> : &fa_rope_kernel<false, false>);
   return launch_pdl(fn, static_cast<unsigned>(grid), kRopeThreads, 0, s, p) == cudaSuccess
              ? FA_OK : FA_ERR_LAUNCH;
-}
-
-// Whether an output lies over one of the small inputs.
-bool over_tables(const void* out, size_t bytes, const int* positions, int per_batch, const double* inv_freq,
-                 int rot_dim, const int* ctx_len, int B, int T) {
-  const size_t pb = static_cast<size_t>(per_batch ? B : 1) * T * 4;
-  return (positions && overlaps(out, bytes, positions, pb)) ||
-         overlaps(out, bytes, inv_freq, static_cast<size_t>(rot_dim) * 4) ||
-         (ctx_len && overlaps(out, bytes, ctx_len, static_cast<size_t>(B) * 4));
-}
-
-bool sizes_ok(int B, int H, int Hkv, int T, int d, int rot_dim, float mscale) {
-  if (B <= 0 || H <= 0 || Hkv < 0 || T <= 0 || (d != 64 && d != 128)) return false;
-  if (rot_dim <= 0 || rot_dim > d || (rot_dim & 15)) return false;
-  if (!std::isfinite(mscale)) return false;
-  const long long rows = static_cast<long long>(B) * T;
-  return rows < (1LL << 40) && H <= (1 << 20) && Hkv <= (1 << 20);
 }
 
 }  // namespace

@@ -19,6 +19,7 @@ from ._binding import (
     FAError,
     fa_bwd_mod_workspace_size,
     fa_fwd_tree_workspace_size,
+    fa_norm_rope_bwd_workspace_size,
     fa_visible_size,
     lib,
 )
@@ -479,4 +480,145 @@ def rope_append(q, k, v, k_cache, v_cache, ctx_len, inv_freq, positions=None,
           k.data_ptr(), *ks, v.data_ptr(), *vs, k_cache.data_ptr(), v_cache.data_ptr(),
           ctx_len.data_ptr(), _ptr(positions), per_batch, inv_freq.data_ptr(), rot, interleaved,
           mscale, B, H, Hkv, Tq, Tmax, d)
+    return out
+
+
+# -------------------------------------------------------- head norms with rotary positions
+
+def _check_weight(t, d, device, name):
+    if not (isinstance(t, torch.Tensor) and t.dtype is _FP32 and t.shape == (d,) and t.device == device
+            and t.is_contiguous()):
+        _check_fp32(t, (d,), device, name)
+
+
+def _check_four(t, name, heads):
+    if not isinstance(t, torch.Tensor) or t.dim() != 4:
+        raise ValueError(f"{name} must be a tensor of shape [B, {heads}, T, d]")
+
+
+def norm_rope(q, k, q_weight, k_weight, inv_freq, positions=None, interleaved: bool = False,
+              mscale: float = 1.0, eps: float = 1e-6, out_q=None, out_k=None):
+    """Queries [B, H, T, d] and keys [B, Hkv, T, d] (or None, with ``k_weight`` None) normed and turned
+    in one pass, through fa_norm_rope: each head's row is divided by √(mean of its squares + eps),
+    multiplied by its weight (float32 [d], one for queries and one for keys) and turned as ``rope``
+    does. Inputs may be views of a packed projection; ``out_q``/``out_k`` may be the (contiguous)
+    inputs themselves. Returns (q, k)."""
+    _check_four(q, "q", "H")
+    shape, device = q.shape, q.device
+    B, H, T, d = shape
+    qs = _check_rows(q, "q", shape, device)
+    _check_weight(q_weight, d, device, "q_weight")
+    if k is None:
+        Hkv, ks = 0, (0, 0, 0)
+        if out_k is not None or k_weight is not None:
+            raise ValueError("out_k or k_weight without k")
+    else:
+        _check_four(k, "k", "Hkv")
+        Hkv = k.shape[1]
+        ks = _check_rows(k, "k", (B, Hkv, T, d), device)
+        _check_weight(k_weight, d, device, "k_weight")
+        if out_k is None:
+            out_k = torch.empty((B, Hkv, T, d), dtype=_BF16, device=device)
+        else:
+            _check_like(out_k, k, "out_k")
+    rot, per_batch = _check_turn(inv_freq, positions, B, T, d, device)
+    if out_q is None:
+        out_q = torch.empty(shape, dtype=_BF16, device=device)
+    else:
+        _check_like(out_q, q, "out_q")
+    _call(device, "fa_norm_rope", q.data_ptr(), *qs, out_q.data_ptr(), _ptr(k), *ks, _ptr(out_k),
+          q_weight.data_ptr(), _ptr(k_weight), eps, _ptr(positions), per_batch, inv_freq.data_ptr(),
+          rot, interleaved, mscale, B, H, Hkv, T, d)
+    return out_q, out_k
+
+
+def norm_rope_bwd_workspace(d: int, device=None):
+    """A uint8 CUDA tensor that serves as ``norm_rope_bwd``'s workspace for head dim d, at any size."""
+    n = fa_norm_rope_bwd_workspace_size(d)
+    if n == 0:
+        raise FAError(FA_ERR_INVALID_ARG, "fa_norm_rope_bwd_workspace_size")
+    return torch.empty(n, dtype=_U8, device="cuda" if device is None else device)
+
+
+def norm_rope_bwd(gq, gk, q, k, q_weight, k_weight, inv_freq, positions=None, interleaved: bool = False,
+                  mscale: float = 1.0, eps: float = 1e-6, dq=None, dk=None, dq_weight=None,
+                  dk_weight=None, workspace=None):
+    """Gradients of ``norm_rope`` through fa_norm_rope_bwd, from those of its results, ``gq`` and
+    ``gk`` (as ``bwd_mod`` returns them; any strides), and its inputs; the other arguments as there.
+    Returns (dq, dk, dq_weight, dk_weight): contiguous rows in bf16 and float32 [d] sums over all rows
+    (added in a fixed order: the same bits every time). gk, k and k_weight may be None together.
+    ``dq``/``dk`` may be the (contiguous) ``gq``/``gk``; ``workspace``: see ``norm_rope_bwd_workspace``.
+    """
+    _check_four(q, "q", "H")
+    shape, device = q.shape, q.device
+    B, H, T, d = shape
+    qs = _check_rows(q, "q", shape, device)
+    gqs = _check_rows(gq, "gq", shape, device)
+    _check_weight(q_weight, d, device, "q_weight")
+    if k is None:
+        Hkv, ks, gks = 0, (0, 0, 0), (0, 0, 0)
+        if any(x is not None for x in (gk, k_weight, dk, dk_weight)):
+            raise ValueError("gk, k_weight, dk or dk_weight without k")
+    else:
+        _check_four(k, "k", "Hkv")
+        Hkv = k.shape[1]
+        kshape = (B, Hkv, T, d)
+        ks = _check_rows(k, "k", kshape, device)
+        gks = _check_rows(gk, "gk", kshape, device)
+        _check_weight(k_weight, d, device, "k_weight")
+        if dk is None:
+            dk = torch.empty(kshape, dtype=_BF16, device=device)
+        else:
+            _check_like(dk, k, "dk")
+        if dk_weight is None:
+            dk_weight = torch.empty(d, dtype=_FP32, device=device)
+        else:
+            _check_weight(dk_weight, d, device, "dk_weight")
+    rot, per_batch = _check_turn(inv_freq, positions, B, T, d, device)
+    if dq is None:
+        dq = torch.empty(shape, dtype=_BF16, device=device)
+    else:
+        _check_like(dq, q, "dq")
+    if dq_weight is None:
+        dq_weight = torch.empty(d, dtype=_FP32, device=device)
+    else:
+        _check_weight(dq_weight, d, device, "dq_weight")
+    if workspace is None:
+        workspace = norm_rope_bwd_workspace(d, device=device)
+    else:
+        _check_workspace(workspace, device)
+    _call(device, "fa_norm_rope_bwd", gq.data_ptr(), *gqs, q.data_ptr(), *qs, dq.data_ptr(), _ptr(gk),
+          *gks, _ptr(k), *ks, _ptr(dk), q_weight.data_ptr(), _ptr(k_weight), dq_weight.data_ptr(),
+          _ptr(dk_weight), eps, _ptr(positions), per_batch, inv_freq.data_ptr(), rot, interleaved,
+          mscale, B, H, Hkv, T, d, workspace.data_ptr(), workspace.numel() * workspace.element_size())
+    return dq, dk, dq_weight, dk_weight
+
+
+def norm_rope_append(q, k, v, q_weight, k_weight, k_cache, v_cache, ctx_len, inv_freq, positions=None,
+                     interleaved: bool = False, mscale: float = 1.0, eps: float = 1e-6, out=None):
+    """A serving step's new tokens through fa_norm_rope_append: ``rope_append`` with the norm of
+    ``norm_rope`` in front of the rotation (v goes into its cache as it is)."""
+    _check_four(q, "q", "H")
+    shape, device = q.shape, q.device
+    B, H, Tq, d = shape
+    _check_on(k_cache, device, "k_cache")
+    _check_on(v_cache, device, "v_cache")
+    Bk, Hkv, Tmax, dk = cache = k_cache.shape
+    if v_cache.shape != cache or Bk != B or dk != d:
+        raise ValueError("k_cache and v_cache must be [B, Hkv, Tmax, d]")
+    qs = _check_rows(q, "q", shape, device)
+    new = (B, Hkv, Tq, d)
+    ks, vs = _check_rows(k, "k", new, device), _check_rows(v, "v", new, device)
+    _check_weight(q_weight, d, device, "q_weight")
+    _check_weight(k_weight, d, device, "k_weight")
+    _check_int32(ctx_len, ((B,),), device, "ctx_len")
+    rot, per_batch = _check_turn(inv_freq, positions, B, Tq, d, device)
+    if out is None:
+        out = torch.empty(shape, dtype=_BF16, device=device)
+    else:
+        _check_like(out, q, "out")
+    _call(device, "fa_norm_rope_append", q.data_ptr(), *qs, out.data_ptr(), k.data_ptr(), *ks,
+          v.data_ptr(), *vs, q_weight.data_ptr(), k_weight.data_ptr(), eps, k_cache.data_ptr(),
+          v_cache.data_ptr(), ctx_len.data_ptr(), _ptr(positions), per_batch, inv_freq.data_ptr(), rot,
+          interleaved, mscale, B, H, Hkv, Tq, Tmax, d)
     return out

@@ -421,6 +421,52 @@ int fa_rope_append(const void* q, long long q_sb, long long q_sh, long long q_st
 
 /*
  * ---------------------------------------------------------------------------------------
+ * Norms of queries and keys for each head, with the rotation in the same pass.
+ *
+ *   n = x / √(mean(x²) + eps)   over the d dimensions of a head's row
+ *   y = n ∘ w, turned as by fa_rope
+ *
+ *   q_weight, k_weight : DEVICE float [d], one for all query heads and one for all key heads
+ *   eps                : finite and > 0
+ *   everything else as for fa_rope and fa_rope_append (Hkv 0: k, k_out and k_weight NULL)
+ *
+ * The sums are taken in fp32 and a result is rounded once.
+ * ---------------------------------------------------------------------------------------
+ */
+int fa_norm_rope(const void* q, long long q_sb, long long q_sh, long long q_st, void* q_out, const void* k,
+                 long long k_sb, long long k_sh, long long k_st, void* k_out, const float* q_weight,
+                 const float* k_weight, float eps, const int* positions, int positions_per_batch,
+                 const double* inv_freq, int rot_dim, int interleaved, float mscale, int B, int H, int Hkv,
+                 int T, int d, void* stream);
+int fa_norm_rope_append(const void* q, long long q_sb, long long q_sh, long long q_st, void* q_out,
+                        const void* k, long long k_sb, long long k_sh, long long k_st, const void* v,
+                        long long v_sb, long long v_sh, long long v_st, const float* q_weight,
+                        const float* k_weight, float eps, void* k_cache, void* v_cache, const int* ctx_len,
+                        const int* positions, int positions_per_batch, const double* inv_freq, int rot_dim,
+                        int interleaved, float mscale, int B, int H, int Hkv, int Tq, int Tmax, int d,
+                        void* stream);
+
+/*
+ * fa_norm_rope_bwd — the gradients of fa_norm_rope, from those of its results (gq, gk; strided as its
+ * inputs) and its inputs q, k: with h = g turned back,
+ *   dx = (h ∘ w − n · mean(h ∘ w ∘ n)) / √(mean(x²) + eps),   dw = Σ_rows h ∘ n
+ * dq, dk: contiguous bf16 (they may be the contiguous gq, gk); dq_weight, dk_weight: DEVICE float [d],
+ * written, summed in a fixed order. workspace: fa_norm_rope_bwd_workspace_size(d) bytes (0: unsupported
+ * d), 256-byte aligned, contents immaterial, not shared with a call that may run at the same time.
+ * Hkv 0: everything of the keys NULL.
+ */
+size_t fa_norm_rope_bwd_workspace_size(int d);
+int fa_norm_rope_bwd(const void* gq, long long gq_sb, long long gq_sh, long long gq_st, const void* q,
+                     long long q_sb, long long q_sh, long long q_st, void* dq, const void* gk,
+                     long long gk_sb, long long gk_sh, long long gk_st, const void* k, long long k_sb,
+                     long long k_sh, long long k_st, void* dk, const float* q_weight, const float* k_weight,
+                     float* dq_weight, float* dk_weight, float eps, const int* positions,
+                     int positions_per_batch, const double* inv_freq, int rot_dim, int interleaved,
+                     float mscale, int B, int H, int Hkv, int T, int d, void* workspace,
+                     size_t workspace_bytes, void* stream);
+
+/*
+ * ---------------------------------------------------------------------------------------
  * fa_fwd_tree — new tokens against a cache: one decoded token a sequence, a chain of them (a
  * chunk of a prompt), or the nodes of a tree of drafted tokens, each of which sees its ancestors.
  * (Every new token walks all keys of its sequence, later tokens' among them: a prompt of 2048 tokens
