@@ -7,7 +7,8 @@ per-row natural-log logsumexp in fp32. ``fwd_kv`` attends Tq queries to Tk ≥ T
 ``fwd_block_sparse`` skips 128×128 blocks switched off by a block mask.
 ``bwd(q, k, v, o, lse, do, causal)`` returns the gradients (dq, dk, dv) (d = 64 or 128).
 ``fwd_mod`` and ``bwd_mod`` are attention with modified scores (a tanh cap, a bias by distance,
-documents and prefixes through ``visible``, key heads shared by query heads) and its gradients;
+documents, prefixes, sliding windows and sinks through ``visible``, key heads shared by query heads)
+and its gradients;
 ``rope`` and ``rope_append`` turn queries and keys by their positions (``norm_rope`` and
 ``norm_rope_append`` after a norm of each head's row, ``norm_rope_bwd`` the way back), and ``fwd_tree`` attends
 new tokens (one, a chain, a tree of drafts) to a cache of ragged contexts.
@@ -36,6 +37,8 @@ from ._binding import (  # noqa: F401
     fa_bwd_ex,
     fa_bwd_mod,
     fa_bwd_mod_workspace_size,
+    fa_bwd_window,
+    fa_bwd_window_workspace_size,
     fa_bwd_workspace_size,
     fa_fwd,
     fa_fwd_block_sparse,
@@ -47,7 +50,10 @@ from ._binding import (  # noqa: F401
     fa_fwd_kv_workspace_size,
     fa_fwd_mod,
     fa_fwd_tree,
+    fa_fwd_tree_window,
+    fa_fwd_tree_window_workspace_size,
     fa_fwd_tree_workspace_size,
+    fa_fwd_window,
     fa_norm_rope,
     fa_norm_rope_append,
     fa_norm_rope_bwd,
@@ -56,6 +62,8 @@ from ._binding import (  # noqa: F401
     fa_rope_append,
     fa_visible,
     fa_visible_size,
+    fa_visible_window,
+    fa_visible_window_size,
     lib,
     strerror,
     version,

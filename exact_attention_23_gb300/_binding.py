@@ -31,7 +31,9 @@ EXPORTS = ("fa_fwd", "fa_fwd_ex", "fa_fwd_fp8", "fa_fwd_host_workspace_size", "f
            "fa_bwd_noalloc", "fa_visible_size", "fa_visible", "fa_fwd_mod", "fa_bwd_mod",
            "fa_bwd_mod_workspace_size", "fa_rope",
            "fa_rope_append", "fa_norm_rope", "fa_norm_rope_append", "fa_norm_rope_bwd_workspace_size",
-           "fa_norm_rope_bwd", "fa_fwd_tree_workspace_size", "fa_fwd_tree", "fa_strerror", "fa_version")
+           "fa_norm_rope_bwd", "fa_fwd_tree_workspace_size", "fa_fwd_tree", "fa_visible_window_size", "fa_visible_window",
+           "fa_fwd_window", "fa_bwd_window_workspace_size", "fa_bwd_window",
+           "fa_fwd_tree_window_workspace_size", "fa_fwd_tree_window", "fa_strerror", "fa_version")
 
 _lock = threading.Lock()
 _lib = None
@@ -113,6 +115,21 @@ def lib() -> ctypes.CDLL:
             L.fa_fwd_tree_workspace_size.restype = sz
             L.fa_fwd_tree.argtypes = ([vp] * 7 + [i, vp, i, f, vp] + [i] * 6 + [f, vp, sz, vp, ull, vp])
             L.fa_fwd_tree.restype = i
+            L.fa_visible_window_size.argtypes = [i] * 4
+            L.fa_visible_window_size.restype = sz
+            L.fa_visible_window.argtypes = [vp, i, i, vp, sz, i, i, vp]
+            L.fa_visible_window.restype = i
+            L.fa_fwd_window.argtypes = [vp] * 7 + [i, i, f, vp, i, i, i, i, i, f, vp, ull, vp]
+            L.fa_fwd_window.restype = i
+            L.fa_bwd_window_workspace_size.argtypes = [i] * 7
+            L.fa_bwd_window_workspace_size.restype = sz
+            L.fa_bwd_window.argtypes = [vp] * 11 + [sz, vp, i, i, f, vp, i, i, i, i, i, f, vp, ull, vp]
+            L.fa_bwd_window.restype = i
+            L.fa_fwd_tree_window_workspace_size.argtypes = [i] * 8
+            L.fa_fwd_tree_window_workspace_size.restype = sz
+            L.fa_fwd_tree_window.argtypes = ([vp] * 7 + [i, vp, i, i, i, f, vp] + [i] * 6
+                                             + [f, vp, sz, vp, ull, vp])
+            L.fa_fwd_tree_window.restype = i
             L.fa_strerror.argtypes = [i]
             L.fa_strerror.restype = ctypes.c_char_p
             L.fa_version.argtypes = []
@@ -281,3 +298,41 @@ def fa_fwd_tree(q, k_cache, v_cache, o, lse, ctx_len, tree, tree_per_batch, dept
                              int(depths_per_batch), float(softcap), slopes, B, H, Hkv, Tq, Tmax, d,
                              float(scale), workspace, int(workspace_bytes), status, int(timeout_ns),
                              stream)
+
+
+def fa_visible_window_size(B, T, window, sinks) -> int:
+    return int(lib().fa_visible_window_size(B, T, window, sinks))
+
+
+def fa_visible_window(doc_ids, window, sinks, visible, visible_bytes, B, T, stream) -> int:
+    return lib().fa_visible_window(doc_ids, window, sinks, visible, int(visible_bytes), B, T, stream)
+
+
+def fa_fwd_window(q, k, v, o, lse, rest, visible, window, sinks, softcap, slopes, B, H, Hkv, T, d,
+                  scale, status, timeout_ns, stream) -> int:
+    return lib().fa_fwd_window(q, k, v, o, lse, rest, visible, window, sinks, float(softcap), slopes, B,
+                               H, Hkv, T, d, float(scale), status, int(timeout_ns), stream)
+
+
+def fa_bwd_window_workspace_size(B, H, Hkv, T, d, window, sinks) -> int:
+    return int(lib().fa_bwd_window_workspace_size(B, H, Hkv, T, d, window, sinks))
+
+
+def fa_bwd_window(q, k, v, o, dout, lse, rest, dq, dk, dv, workspace, workspace_bytes, visible, window,
+                  sinks, softcap, slopes, B, H, Hkv, T, d, scale, status, timeout_ns, stream) -> int:
+    return lib().fa_bwd_window(q, k, v, o, dout, lse, rest, dq, dk, dv, workspace, int(workspace_bytes),
+                               visible, window, sinks, float(softcap), slopes, B, H, Hkv, T, d,
+                               float(scale), status, int(timeout_ns), stream)
+
+
+def fa_fwd_tree_window_workspace_size(B, H, Hkv, Tq, Tmax, d, window, sinks) -> int:
+    return int(lib().fa_fwd_tree_window_workspace_size(B, H, Hkv, Tq, Tmax, d, window, sinks))
+
+
+def fa_fwd_tree_window(q, k_cache, v_cache, o, lse, ctx_len, tree, tree_per_batch, depths,
+                       depths_per_batch, window, sinks, softcap, slopes, B, H, Hkv, Tq, Tmax, d, scale,
+                       workspace, workspace_bytes, status, timeout_ns, stream) -> int:
+    return lib().fa_fwd_tree_window(q, k_cache, v_cache, o, lse, ctx_len, tree, int(tree_per_batch),
+                                    depths, int(depths_per_batch), window, sinks, float(softcap), slopes,
+                                    B, H, Hkv, Tq, Tmax, d, float(scale), workspace, int(workspace_bytes),
+                                    status, int(timeout_ns), stream)

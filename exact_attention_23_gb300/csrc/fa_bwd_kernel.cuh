@@ -147,6 +147,13 @@ struct BwdModParams {
   const int2* whole;    // [B][n_kt] (largest lo, smallest hi) over a tile's 128 rows: hi is 0 with padding
   const float* slopes;  // [H]
   float* part_out;      // parts > 1: [2][parts][B·Hkv][T][D], dK (scaled) then dV
+  // SINK: `units` are [B][n_rec][2], the second (slot of a cut walk's piece or −1, whether the key tile has
+  // sinks beyond a window, 0, 0); the pieces' sums go to slots and fa_bwd_pieces_kernel adds them in order.
+  const int2* sink_rows;  // [B][T_pad] a row's visible sinks, an interval in front of its rows entry
+  const int4* cuts;     // [B][n_cut] the cut key tiles: (tile, first slot, slots, 0)
+  float* piece_out;     // [2][B·Hkv·parts][n_slots][128][D], dK (scaled) then dV
+  int n_rec;            // walks a key head's part (n_kt, or with pieces)
+  int n_cut, n_slots;
   int Hkv;              // key heads
   int group;            // query heads per key head
   int parts;            // parts of a group (BH then counts B·Hkv·parts)
@@ -391,6 +398,40 @@ __global__ void __launch_bounds__(256) fa_bwd_sum_kernel(const float* __restrict
   }
 }
 
+// dK and dV of the key tiles whose walks were cut: their pieces' fp32 rows, of every part in order, as
+// bf16. A block 32 rows of a cut tile of a key head (blockIdx.x = (key head · n_cut + cut) · 4 + quarter).
+template <int D>
+__global__ void __launch_bounds__(256) fa_bwd_pieces_kernel(const float* __restrict__ piece_out,
+                                                            const int4* __restrict__ cuts,
+                                                            __nv_bfloat16* __restrict__ dk,
+                                                            __nv_bfloat16* __restrict__ dv, int Hkv, int BHkv, int T,
+                                                            int n_cut, int n_slots, int parts) {
+  pdl_wait();
+  pdl_launch_dependents();
+  const int quarter = blockIdx.x & 3, x = static_cast<int>(blockIdx.x >> 2), bh = x / n_cut;
+  const int4 cut = cuts[(size_t)(bh / Hkv) * n_cut + (x - bh * n_cut)];
+  if (cut.z == 0) return;
+  for (int e = threadIdx.x; e < 2 * 32 * (D / 8); e += 256) {
+    const bool is_dv = e >= 32 * (D / 8);
+    const int r = quarter * 32 + (e / (D / 8)) % 32, c = e % (D / 8) * 8, key = cut.x * 128 + r;
+    if (key >= T) continue;
+    float4 a = make_float4(0.f, 0.f, 0.f, 0.f), b = a;
+    for (int s = 0; s < parts; ++s) {
+      const float* src = piece_out +
+          ((((is_dv ? (size_t)BHkv * parts : 0) + (size_t)bh * parts + s) * n_slots + cut.y) * 128 + r) * D + c;
+#pragma unroll 4
+      for (int i = 0; i < cut.z; ++i) {
+        const float4 u = *reinterpret_cast<const float4*>(src + (size_t)i * 128 * D);
+        const float4 v = *reinterpret_cast<const float4*>(src + (size_t)i * 128 * D + 4);
+        a.x += u.x; a.y += u.y; a.z += u.z; a.w += u.w;
+        b.x += v.x; b.y += v.y; b.z += v.z; b.w += v.w;
+      }
+    }
+    *reinterpret_cast<uint4*>((is_dv ? dv : dk) + ((size_t)bh * T + key) * D + c) =
+        make_uint4(pack_bf16x2(a.x, a.y), pack_bf16x2(a.z, a.w), pack_bf16x2(b.x, b.y), pack_bf16x2(b.z, b.w));
+  }
+}
+
 // ------------------------------------------------------------------------------------
 // Main kernel.
 // ------------------------------------------------------------------------------------
@@ -411,6 +452,8 @@ struct BwdWalk {
   int part;      // which part of the key head's query heads
   int pad0;      // the first query tile with padding
   bool key_pad;  // the key tile has padding
+  int slot;      // SINK: where a piece's sums go, or −1
+  bool sinks;    // SINK: the key tile has sinks that are seen from beyond a window
 };
 
 // pos, head: the CTA's place in the unit order.
@@ -425,6 +468,8 @@ __device__ __forceinline__ BwdWalk bwd_walk(const BwdParams& p, int pos, int hea
   w.h0 = w.part = 0;
   w.pad0 = p.n_qt;
   w.key_pad = false;
+  w.slot = -1;
+  w.sinks = false;
   if constexpr (MOD != 0) {
     const int heads = p.mod.group / p.mod.parts;
     w.bh = head / p.mod.parts;
@@ -433,7 +478,14 @@ __device__ __forceinline__ BwdWalk bwd_walk(const BwdParams& p, int pos, int hea
     w.h0 = (w.bh - b * p.mod.Hkv) * p.mod.group + w.part * heads;
     w.q0h = w.bh * p.mod.group + w.part * heads;
     if (p.mod.units) {
-      const int4 rec = __ldg(p.mod.units + (size_t)b * p.n_kt + pos);
+      constexpr bool kSink = (MOD & kModSink) != 0;
+      const int4* at = p.mod.units + (kSink ? ((size_t)b * p.mod.n_rec + pos) * 2 : (size_t)b * p.n_kt + pos);
+      const int4 rec = __ldg(at);
+      if constexpr (kSink) {
+        const int4 more = __ldg(at + 1);
+        w.slot = more.x;
+        w.sinks = more.y != 0;
+      }
       w.j = rec.x;
       w.i0 = rec.y * kPer;
       w.n_i = max(0, rec.z * kPer - w.i0);
@@ -476,7 +528,8 @@ __global__ void __launch_bounds__(BwdCfg<D, MOD>::kThreads, 1)
   // accumulator stay in L2 while its CTAs run; within a group, heaviest units first (under
   // the causal mask key tile j sees the query tiles from the one holding query 128·j on),
   // all heads at one j together.
-  const int per_group = p.head_group * p.n_kt;
+  constexpr bool kSink = (MOD & kModSink) != 0;
+  const int per_group = p.head_group * (kSink ? p.mod.n_rec : p.n_kt);
   const int grp = blockIdx.x / per_group;
   const int within = blockIdx.x - grp * per_group;
   const int gsize = min(p.head_group, p.BH - grp * p.head_group);
@@ -875,7 +928,7 @@ __global__ void __launch_bounds__(BwdCfg<D, MOD>::kThreads, 1)
       float pr[NC];
       // MOD: Pᵀ's pairs, packed as they are made (CAP needs both, P and what dS multiplies; plain d64
       // is faster without, B2 H12 T4096 182 -> 178 µs, but d128, B2 H16 T4096, 377 -> 387)
-      constexpr bool kTwo = MOD != 0 && !(D == 64 && MOD == kModOn);
+      constexpr bool kTwo = MOD != 0 && !(D == 64 && (MOD & ~kModSink) == kModOn);
       uint32_t pkm[kTwo ? NC / 2 : 1];
       const float4* l4 = reinterpret_cast<const float4*>(vec + g * NC);
       const uint64_t c2 = f2_pack(p.scale_log2, p.scale_log2);
@@ -936,7 +989,7 @@ __global__ void __launch_bounds__(BwdCfg<D, MOD>::kThreads, 1)
           // Which queries see this thread's key, as bits (kBits; c: query q0 + c), or asked of each
           // query: bits, B2 H12 T4096 d64 182 -> 178 µs, capped 216 -> 202; but d128, B2 H16 T4096 capped,
           // 412 -> 423.
-          constexpr bool kBits = D == 64;
+          constexpr bool kBits = D == 64 || kSink;
           uint32_t seen = 0u;
           // without rows: queries from q0 + rel on see the key; none sees one behind the end, whose
           // score of 0 (its row is loaded as zeros) may be far above every other of a query
@@ -946,6 +999,12 @@ __global__ void __launch_bounds__(BwdCfg<D, MOD>::kThreads, 1)
             const int lo = min(max(v.x - (key - lane), 0), 32), hi = min(max(v.y - (key - lane), 0), 32);
             const uint32_t below = hi >= 32 ? 0xFFFFFFFFu : (1u << hi) - 1u;
             seen = lo >= 32 ? 0u : (below >> lo) << lo;
+            if constexpr (kSink) {
+              if (wk.sinks) {  // (few walks have any)
+                const int2 k = __ldg(p.mod.sink_rows + (size_t)(bh / p.mod.Hkv) * p.T_pad + q0 + (lane & (NC - 1)));
+                seen |= bits_of(k.x - (key - lane), k.y - (key - lane));
+              }
+            }
             // bits of keys, a lane a query -> bits of queries, a lane a key: 32 x 32 bits transposed
 #pragma unroll
             for (int x = 16; x > 0; x >>= 1) {
@@ -1104,6 +1163,14 @@ __global__ void __launch_bounds__(BwdCfg<D, MOD>::kThreads, 1)
             for (int e = 0; e < 8; ++e) y[e] = 0.f;
           }
           if constexpr (MOD != 0) {
+            if (kSink && wk.slot >= 0) {
+              float* out = p.mod.piece_out +
+                           ((((is_dv ? (size_t)p.BH : 0) + (size_t)bh * p.mod.parts + wk.part) * p.mod.n_slots + wk.slot) * 128 + r) * D +
+                           h * 32 + c;
+              reinterpret_cast<float4*>(out)[0] = make_float4(y[0], y[1], y[2], y[3]);
+              reinterpret_cast<float4*>(out)[1] = make_float4(y[4], y[5], y[6], y[7]);
+              continue;
+            }
             if (p.mod.parts > 1) {
               const size_t rows = (size_t)(p.BH / p.mod.parts) * p.T;
               float* out = p.mod.part_out +

@@ -133,7 +133,7 @@ struct NoSegments {
   __device__ __forceinline__ bool next(const TreeList&) { return false; }
 };
 template <int MOD>
-using SegmentsOf = std::conditional_t<(MOD & kModTree) != 0, TreeSegments, NoSegments>;
+using SegmentsOf = std::conditional_t<(MOD & kModTree) != 0, TreeSegments<(MOD & kModSink) != 0>, NoSegments>;
 
 template <bool CAUSAL, bool GEN, int MOD, typename Segments>
 __device__ __forceinline__ Unit unit1_of(const FwdParams& p, int L, const Segments& sg) {
@@ -149,6 +149,7 @@ __device__ __forceinline__ Unit unit1_of(const FwdParams& p, int L, const Segmen
     u.last[0] = sg.b;
     u.last[1] = __ldg(p.mod.list.ctx_len + sg.b);
     u.mh = tree_keys(p.mod.list, u.last[1]);
+    if constexpr ((MOD & kModSink) != 0) tree_window(p.mod.list, u.last[1], &u.sb[0], &u.se[0]);
     return u;
   } else if constexpr (MOD != 0) {
     Unit u;
@@ -169,6 +170,13 @@ __device__ __forceinline__ Unit unit1_of(const FwdParams& p, int L, const Segmen
       u.mh = p.n_kv;
     }
     u.n_steps = max(0, u.ke - u.kb);
+    if constexpr ((MOD & kModSink) != 0) {
+      const int b = static_cast<int>(p.mod.div_h.div(static_cast<uint32_t>(u.bh)));
+      const int2 k = __ldg(p.mod.sink_units + static_cast<size_t>(b) * p.n_qt + pos);
+      u.sb[0] = k.x;
+      u.se[0] = k.y;
+      u.n_steps += k.y - k.x;
+    }
     u.nkv[0] = u.n_steps;
     u.nkv[1] = 0;
     u.last[0] = u.last[1] = 0;
@@ -189,6 +197,7 @@ __global__ void __launch_bounds__(Cfg1<D, (MOD & kModRef) != 0>::kThreads, 1)
   constexpr bool kRef = (MOD & kModRef) != 0;  // the softmax is taken against 0
   constexpr bool kRefRest = (MOD & kModRest) != 0;        // … with o's rest
   constexpr bool kRest = MOD != 0 && !kTree && (!kRef || kRefRest);  // o's rest may be asked for
+  constexpr bool kSink = (MOD & kModSink) != 0;  // a second interval a row (TREE: a window and sinks)
   constexpr bool kXform = (MOD & (kModCap | kModBias)) != 0;  // scores are modified before the softmax
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
@@ -280,7 +289,8 @@ __global__ void __launch_bounds__(Cfg1<D, (MOD & kModRef) != 0>::kThreads, 1)
       if constexpr (MOD != 0) kvh = static_cast<int>(p.mod.div_g.div(static_cast<uint32_t>(u.bh)));
       for (int j = 0; j < u.n_steps; ++j, ++g) {
         us.next(u, j);
-        const int kt = us.kt;
+        int kt = us.kt;
+        if constexpr (kSink) kt = sink_step_tile<MOD>(u, j);
         const int st = g % C::kStages;
         const int use = g / C::kStages;
         if (use > 0 && !mbar_wait_warp(&bars->kv_empty[st], (use - 1) & 1, wc)) { ok = false; break; }
@@ -380,23 +390,32 @@ __global__ void __launch_bounds__(Cfg1<D, (MOD & kModRef) != 0>::kThreads, 1)
           const int st = g % C::kStages;
           const int b = g & 1;
           if (!mbar_wait_warp(&bars->v_full[st], (g / C::kStages) & 1, wc)) { ok = false; break; }
+          int vt = u.kb + j;
+          if constexpr (kSink) vt = sink_step_tile<MOD>(u, j);
           if constexpr (MOD != 0 && !kTree) {
-            if (u.kb + j >= u.mh)
+            if (vt >= u.mh)
               zero_padding_called(v_base + st * C::kTileBytes, C::kSub, C::kSubBytes, kBlockN,
                                   p.mod.rows + p.mod.div_h.div(static_cast<uint32_t>(u.bh)) * static_cast<size_t>(p.mod.T_pad) +
-                                      (u.kb + j) * kBlockN);
+                                      vt * kBlockN);
           }
           if constexpr (kTree) {
             // Rows behind the sequence's keys may hold anything: their P is 0, and 0 · NaN must not
             // reach O.
-            const int used = u.mh - (u.kb + j) * kBlockN;
-            if (used < kBlockN) {
-              for (int x = used * 8 + lane; x < kBlockN * 8; x += 32)
+            const int used = u.mh - vt * kBlockN;
+            auto zero_rows = [&](int r0, int r1) {
+              for (int x = r0 * 8 + lane; x < r1 * 8; x += 32)
 #pragma unroll
                 for (int s = 0; s < C::kSub; ++s)
                   st_shared_v4(v_base + st * C::kTileBytes + s * C::kSubBytes + x * 16, 0u, 0u, 0u, 0u);
               fence_proxy_async_smem();
               __syncwarp();
+            };
+            if (used < kBlockN) zero_rows(used, kBlockN);
+            if constexpr (kSink) {
+              // … and so may those between the sinks and every token's window.
+              const int r0 = max(p.mod.list.sinks - vt * kBlockN, 0);
+              const int r1 = min(min(tree_window_start(p.mod.list, u.last[1]) - vt * kBlockN, used), kBlockN);
+              if (r0 < r1) zero_rows(r0, r1);
             }
           }
           FA1_TRACE(8, j);
@@ -784,9 +803,10 @@ __global__ void __launch_bounds__(Cfg1<D, (MOD & kModRef) != 0>::kThreads, 1)
       }
       // MOD: this row's visible keys [lo, hi) and (BIAS) its head's slope in base 2, negated
       int vlo = 0, vhi = 0;
+      int slo = 0, shi = 0;  // SINK: and its sinks
       float nslope = 0.0f;
       // TREE: this row's token, its position from the end of its sequence's context, and that context
-      int tok = 0, ctx = 0;
+      int tok = 0, ctx = 0, dep = 0;
       float q_at = 0.0f;
       if constexpr (kTree) {
         const int r = min(q_row, p.T - 1);
@@ -795,6 +815,10 @@ __global__ void __launch_bounds__(Cfg1<D, (MOD & kModRef) != 0>::kThreads, 1)
         tok = r - hg * Tq;
         ctx = u.last[1];
         vhi = min(ctx, u.mh);
+        if constexpr (kSink) {
+          dep = p.mod.mask.depths ? tree_depth(p.mod.mask.depths_of(u.last[0], Tq)[tok]) : tok;
+          vlo = tree_row_start(p.mod.list, ctx, dep);
+        }
         if constexpr ((MOD & kModBias) != 0) {
           const int hk = u.bh - u.last[0] * p.mod.list.Hkv;
           q_at = static_cast<float>(p.mod.mask.depths ? p.mod.mask.depths_of(u.last[0], Tq)[tok] : tok);
@@ -806,6 +830,11 @@ __global__ void __launch_bounds__(Cfg1<D, (MOD & kModRef) != 0>::kThreads, 1)
           const int2 r = __ldg(p.mod.rows + static_cast<size_t>(b) * p.mod.T_pad + q_row);
           vlo = r.x;
           vhi = r.y;
+          if constexpr (kSink) {
+            const int2 k = __ldg(p.mod.sink_rows + static_cast<size_t>(b) * p.mod.T_pad + q_row);
+            slo = k.x;
+            shi = k.y;
+          }
         } else {
           vhi = p.mod.causal ? min(q_row + 1, p.Tk) : p.Tk;
         }
@@ -824,7 +853,9 @@ __global__ void __launch_bounds__(Cfg1<D, (MOD & kModRef) != 0>::kThreads, 1)
       }
       int kt = u.kb - 1;  // (dense: u.kb = 0, step j is K tile j)
       for (int j = 0; j < n; ++j, ++g) {
-        if constexpr (GEN) {
+        if constexpr (kSink) {
+          kt = sink_step_tile<MOD>(u, j);
+        } else if constexpr (GEN) {
           kt = nx;
           nx = walk_next(w, kt);
         } else {
@@ -842,6 +873,7 @@ __global__ void __launch_bounds__(Cfg1<D, (MOD & kModRef) != 0>::kThreads, 1)
         if constexpr (MOD != 0) {
           lim = vhi - k0;
           masked = lim < kC || vlo > k0;
+          if constexpr (kSink) masked = __any_sync(0xffffffffu, masked);
         } else if constexpr (GEN) {
           lim = (CAUSAL ? min(q_row + 1 + p.kv_off, p.Tk) : p.Tk) - k0;
           masked = lim < kC;
@@ -959,6 +991,7 @@ __global__ void __launch_bounds__(Cfg1<D, (MOD & kModRef) != 0>::kThreads, 1)
                 // context keys, chain keys and rows of the cache: ranges
                 const int n_see = min(max(min(ctx, u.mh) - (k0 + w * 32), 0), 32);
                 uint32_t word = n_see >= 32 ? 0xFFFFFFFFu : (1u << n_see) - 1u;
+                if constexpr (kSink) word &= ~bits_below(vlo - k0 - w * 32) | bits_below(p.mod.list.sinks - k0 - w * 32);
                 if (pieces) {
                   const int n_keys = min(max(u.mh - (k0 + w * 32), 0), 32);
                   word |= __funnelshift_r(tw[w], tw[w + 1], d0 & 31) & (n_keys >= 32 ? 0xFFFFFFFFu : (1u << n_keys) - 1u);
@@ -976,7 +1009,21 @@ __global__ void __launch_bounds__(Cfg1<D, (MOD & kModRef) != 0>::kThreads, 1)
                   }
                 } else {
                   const int n_chain = min(max(min(tok + 1, u.mh - ctx) - dw, 0), 32);
-                  if (dw > -32) word |= n_chain >= 32 ? 0xFFFFFFFFu : (1u << n_chain) - 1u;
+                  if constexpr (kSink) word |= bits_of(-dw, n_chain);
+                  else if (dw > -32) word |= n_chain >= 32 ? 0xFFFFFFFFu : (1u << n_chain) - 1u;
+                }
+                if constexpr (kSink) {
+                  // Tokens as deep as the window is wide may have outrun others.
+                  if (dw > -32 && __any_sync(0xffffffffu, dep >= p.mod.list.window)) {
+                    const int* at = p.mod.mask.depths ? p.mod.mask.depths_of(u.last[0], Tq) : nullptr;
+                    const int dk = min(max(dw + lane, 0), Tq - 1), mine = at ? tree_depth(at[dk]) : dk;
+#pragma unroll 1
+                    for (int t = 0; t < 32; ++t) {
+                      const int there = __shfl_sync(0xffffffffu, mine, t);
+                      if (dw + t >= 0 && dep - there >= p.mod.list.window && there >= p.mod.list.sinks - ctx)
+                        word &= ~(1u << t);
+                    }
+                  }
                 }
                 bits[w] = word;
                 if constexpr ((MOD & kModBias) != 0) {
@@ -998,9 +1045,19 @@ __global__ void __launch_bounds__(Cfg1<D, (MOD & kModRef) != 0>::kThreads, 1)
             }
           } else if (masked) {
             const int vl = vlo - k0;
+            if constexpr (kSink) {
 #pragma unroll
-            for (int t = 0; t < kC; ++t)
-              if (t >= lim || t < vl) s[t] = __float_as_uint(-INFINITY);
+              for (int c0 = 0; c0 < kC; c0 += 32) {
+                const uint32_t seen = bits_of(vl - c0, lim - c0) | bits_of(slo - k0 - c0, shi - k0 - c0);
+#pragma unroll
+                for (int t = 0; t < 32; ++t)
+                  if (!((seen >> t) & 1u)) s[c0 + t] = __float_as_uint(-INFINITY);
+              }
+            } else {
+#pragma unroll
+              for (int t = 0; t < kC; ++t)
+                if (t >= lim || t < vl) s[t] = __float_as_uint(-INFINITY);
+            }
           }
         } else if (masked) {
 #pragma unroll

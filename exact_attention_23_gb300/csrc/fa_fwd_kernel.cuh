@@ -132,6 +132,9 @@ struct ModParams {
   const int4* units;    // [B][n_t] (query tile, first K tile, past the last, first tile with padding)
   const int4* pairs;    // [B][ceil(n_t/2)][2] (first query tile, first tile with padding, its first K
                         //   tile, past its last), (the second tile's first and past its last, 0, 0)
+  const int2* sink_rows;   // SINK: [B][T_pad] a row's visible sinks, an interval in front of its rows entry
+  const int2* sink_units;  // SINK: [B][n_t] the sinks' K tiles of each of `units`, all before its first
+  const int4* sink_pairs;  // SINK: [B][ceil(n_t/2)] the same of both tiles of each of `pairs`
   const float* slopes;  // [H] distance-bias slopes (BIAS)
   __nv_bfloat16* rest;  // [BH][T][D] what o's rounding leaves out, or null (not TREE)
   int T_pad;            // ceil(T/128) · 128
@@ -192,7 +195,21 @@ struct Unit {
   int lo[2];      // MOD: tile i's K tiles are [lo[i], last[i])
   int last[2];    // last K tile visible to tile i (GEN, causal)
   int split, mh;  // key-range index; block-mask head (MOD: the first tile with padding)
+  int sb[2], se[2];  // SINK: tile i's K tiles with sinks, [sb[i], se[i]), come before its others (TREE:
+                     //   list chunks from sb[0] on lie se[0] chunks further)
+  int ub, un;        // SINK, two tiles: the union's first of them, and how many lie before kb
 };
+
+// SINK, one tile: the K tile of step j.
+template <int MOD>
+__device__ __forceinline__ int sink_step_tile(const Unit& u, int j) {
+  if constexpr ((MOD & kModTree) != 0) {
+    const int c = u.kb + j;
+    return c < u.sb[0] ? c : c + u.se[0];
+  }
+  const int ns = u.se[0] - u.sb[0];
+  return j < ns ? u.sb[0] + j : u.kb + j - ns;
+}
 
 __device__ __forceinline__ int unit_index(int round, int cta, int grid) {
   return round * grid + ((round & 1) ? grid - 1 - cta : cta);
@@ -230,6 +247,7 @@ __device__ __forceinline__ int walk_next(const Walk& w, int kt) {
 // MOD (modified scores): both tiles' K tiles are contiguous ranges, from the visibility's records
 // (pairs with the longest walks first) or the causal or full ranges (the last pair first); the
 // unit walks their union.
+template <bool SINK>
 __device__ __forceinline__ Unit pair_unit_of(const FwdParams& p, int L) {
   Unit u;
   const int pos = static_cast<int>(p.div_bh.div(static_cast<uint32_t>(L)));
@@ -245,6 +263,13 @@ __device__ __forceinline__ Unit pair_unit_of(const FwdParams& p, int L) {
     u.last[0] = r0.w;
     u.lo[1] = r1.x;
     u.last[1] = r1.y;
+    if constexpr (SINK) {
+      const int4 k = __ldg(p.mod.sink_pairs + static_cast<size_t>(b) * p.n_units + pos);
+      u.sb[0] = k.x;
+      u.se[0] = k.y;
+      u.sb[1] = k.z;
+      u.se[1] = k.w;
+    }
   } else {
     u.qt0 = (p.n_units - 1 - pos) * 2;
     u.mh = p.n_kv;
@@ -258,12 +283,20 @@ __device__ __forceinline__ Unit pair_unit_of(const FwdParams& p, int L) {
   u.ke = max(u.nkv[0] > 0 ? u.last[0] : 0, u.nkv[1] > 0 ? u.last[1] : 0);
   u.n_steps = max(0, u.ke - u.kb);
   if (u.n_steps == 0) u.kb = 0;
+  if constexpr (SINK) {
+    const int n0 = u.se[0] - u.sb[0], n1 = u.se[1] - u.sb[1];
+    u.ub = min(n0 > 0 ? u.sb[0] : u.kb, n1 > 0 ? u.sb[1] : u.kb);
+    u.un = max(0, min(max(n0 > 0 ? u.se[0] : 0, n1 > 0 ? u.se[1] : 0), u.kb) - u.ub);
+    u.nkv[0] += n0;
+    u.nkv[1] += n1;
+    u.n_steps += u.un;
+  }
   return u;
 }
 
 template <bool CAUSAL, bool GEN, int MOD = 0>
 __device__ __forceinline__ Unit unit_of(const FwdParams& p, int L) {
-  if constexpr (MOD != 0) return pair_unit_of(p, L);
+  if constexpr (MOD != 0) return pair_unit_of<(MOD & kModSink) != 0>(p, L);
   Unit u;
   if constexpr (GEN) {
     // bh fastest, then key range, then query unit, the last query unit first (under the
@@ -340,8 +373,13 @@ struct UnitSteps {
   __device__ __forceinline__ void next(const Unit& u, int j) {
     if constexpr (MOD != 0) {
       kt = u.kb + j;
+      if constexpr ((MOD & kModSink) != 0) kt = j < u.un ? u.ub + j : kt - u.un;
       act[0] = kt >= u.lo[0] && kt < u.last[0];
       act[1] = kt >= u.lo[1] && kt < u.last[1];
+      if constexpr ((MOD & kModSink) != 0) {
+        act[0] = act[0] || (kt >= u.sb[0] && kt < u.se[0]);
+        act[1] = act[1] || (kt >= u.sb[1] && kt < u.se[1]);
+      }
     } else if constexpr (GEN) {
       kt = min(nx[0], nx[1]);
 #pragma unroll
@@ -371,6 +409,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   constexpr bool kRest = (MOD & kModRest) != 0;           // o's rest is asked for
   constexpr bool kRefRest = kRef && kRest;
   constexpr bool kParts = GEN && MOD == 0;                // several key ranges are possible
+  constexpr bool kSink = (MOD & kModSink) != 0;           // a second interval a row
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
   Bars* bars = reinterpret_cast<Bars*>(smem + C::kBarOff);
@@ -898,12 +937,18 @@ __global__ void __launch_bounds__(kThreads, 1)
       float m_ref = kRef ? 0.0f : -INFINITY;
       float l = 0.0f, top = 0.0f, raw_top = -INFINITY;
       int vlo = 0, vhi = 0;  // MOD: this row's visible keys [lo, hi)
+      int slo = 0, shi = 0;  // SINK: and its sinks
       if constexpr (MOD != 0) {
         const int b = static_cast<int>(p.mod.div_h.div(static_cast<uint32_t>(u.bh)));
         if (p.mod.rows) {
           const int2 r = __ldg(p.mod.rows + static_cast<size_t>(b) * p.mod.T_pad + q_row);
           vlo = r.x;
           vhi = r.y;
+          if constexpr (kSink) {
+            const int2 k = __ldg(p.mod.sink_rows + static_cast<size_t>(b) * p.mod.T_pad + q_row);
+            slo = k.x;
+            shi = k.y;
+          }
         } else {
           vhi = p.mod.causal ? min(q_row + 1, p.Tk) : p.Tk;
         }
@@ -917,10 +962,13 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       int kt = u.kb - 1;  // (dense: u.kb = 0, step j is K tile j)
       if constexpr (MOD != 0) kt = (wg ? u.lo[1] : u.lo[0]) - 1;
+      const int n_sink = kSink ? (wg ? u.se[1] - u.sb[1] : u.se[0] - u.sb[0]) : 0;
       for (int j = 0; j < n; ++j, ++gs) {
         if constexpr (GEN && MOD == 0) {
           kt = nx;
           nx = walk_next(w, kt);
+        } else if constexpr (kSink) {
+          kt = j < n_sink ? (wg ? u.sb[1] : u.sb[0]) + j : (wg ? u.lo[1] : u.lo[0]) + j - n_sink;
         } else {
           ++kt;
         }
@@ -959,7 +1007,10 @@ __global__ void __launch_bounds__(kThreads, 1)
             float x0, x1;
             f2_unpack(cap2<FAR>(f2_pack(u2f(s0), u2f(s1)), p.mod.cap), x0, x1);
             float p0 = ex2_approx(x0), p1 = ex2_approx(x1);
-            if constexpr (MASK) {
+            if constexpr (MASK && kSink) {  // (lim_c: the visible columns as bits)
+              if (!((static_cast<uint32_t>(lim_c) >> (2 * t)) & 1u)) p0 = 0.0f;
+              if (!((static_cast<uint32_t>(lim_c) >> (2 * t + 1)) & 1u)) p1 = 0.0f;
+            } else if constexpr (MASK) {
               if (2 * t >= lim_c || 2 * t < vl_c) p0 = 0.0f;
               if (2 * t + 1 >= lim_c || 2 * t + 1 < vl_c) p1 = 0.0f;
             }
@@ -985,7 +1036,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           // largest weight: d128, B2 H16 T4096 causal, 141 µs spread, 136 not, and where 8 % of the 32s
           // are far 288, 181; d64, B1 H12 T16384, far ones 1600, 825. Now: d64, that size, 575 spread,
           // 614 not; with o's rest 618.)
-          constexpr bool kSpread = C::kSepP && !kRefRest && (MOD & kModTight) == 0;
+          constexpr bool kSpread = C::kSepP && !kRefRest && (MOD & (kModTight | kModSink)) == 0;
 #pragma unroll (kSpread ? 2 : 1)
           for (int h = 0; h < 2; ++h) {
             uint32_t pk[32];
@@ -1004,7 +1055,10 @@ __global__ void __launch_bounds__(kThreads, 1)
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&bars->s_free[wg]);
               }
-              const int lim_c = lim - (2 * h + cc) * 32, vl_c = vl - (2 * h + cc) * 32;
+              int lim_c = lim - (2 * h + cc) * 32;
+              const int vl_c = vl - (2 * h + cc) * 32;
+              if constexpr (kSink)
+                lim_c = static_cast<int>(bits_of(vl_c, lim_c) | bits_of(slo - k0 - (2 * h + cc) * 32, shi - k0 - (2 * h + cc) * 32));
               if (far && kSpread) {
 #pragma unroll
                 for (int t = 0; t < 16; ++t)
@@ -1074,10 +1128,11 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
               top_s[i] = -INFINITY;
+              const uint32_t seen = kSink ? bits_of(vl - 32 * i, lim - 32 * i) | bits_of(slo - k0 - 32 * i, shi - k0 - 32 * i) : 0u;
 #pragma unroll
               for (int t = 32 * i; t < 32 * i + 32; t += 2) {
-                if (t >= lim || t < vl) s[t] = __float_as_uint(-INFINITY);
-                if (t + 1 >= lim || t + 1 < vl) s[t + 1] = __float_as_uint(-INFINITY);
+                if (kSink ? !((seen >> (t - 32 * i)) & 1u) : t >= lim || t < vl) s[t] = __float_as_uint(-INFINITY);
+                if (kSink ? !((seen >> (t + 1 - 32 * i)) & 1u) : t + 1 >= lim || t + 1 < vl) s[t + 1] = __float_as_uint(-INFINITY);
                 top_s[i] = fmax3(top_s[i], u2f(s[t]), u2f(s[t + 1]));
               }
             }

@@ -60,9 +60,16 @@ cudaError_t launch_fwd_mod_d128(const FwdLaunch& a, int mod);
 // kModRef.
 cudaError_t launch_fwd_mod_pairs_d64(const FwdLaunch& a, int mod);
 cudaError_t launch_fwd_mod_pairs_d128(const FwdLaunch& a, int mod);
+// The same with sinks in front of a sliding window.
+cudaError_t launch_fwd_sink_d64(const FwdLaunch& a, int mod);
+cudaError_t launch_fwd_sink_d128(const FwdLaunch& a, int mod);
+cudaError_t launch_fwd_sink_pairs_d64(const FwdLaunch& a, int mod);
+cudaError_t launch_fwd_sink_pairs_d128(const FwdLaunch& a, int mod);
 // New tokens against a cache on the same kernel (a.p.T the rows a key head, a.grid the stretches).
 cudaError_t launch_fwd_tree_d64(const FwdLaunch& a, int mod);
 cudaError_t launch_fwd_tree_d128(const FwdLaunch& a, int mod);
+cudaError_t launch_fwd_tree_window_d64(const FwdLaunch& a, int mod);  // with a window and sinks
+cudaError_t launch_fwd_tree_window_d128(const FwdLaunch& a, int mod);
 
 struct BwdLaunch {
   CUtensorMap tm_q, tm_k, tm_v, tm_do;
@@ -84,5 +91,8 @@ cudaError_t launch_bwd_d128(const BwdLaunch& a, bool causal);
 // The same with modified scores; a.p.BH counts key heads' parts, q_heads = B·H.
 cudaError_t launch_bwd_mod_d64(const BwdLaunch& a, int mod, int q_heads);
 cudaError_t launch_bwd_mod_d128(const BwdLaunch& a, int mod, int q_heads);
+// … and sinks in front of a sliding window (walks cut into pieces).
+cudaError_t launch_bwd_sink_d64(const BwdLaunch& a, int mod, int q_heads);
+cudaError_t launch_bwd_sink_d128(const BwdLaunch& a, int mod, int q_heads);
 
 }  // namespace fa

@@ -6,8 +6,9 @@
 //   key j is visible to query i iff lo_i ≤ j < hi_i
 //
 // Every mask here is one interval of keys per query row: causal [0, i + 1), a prompt that sees
-// itself [0, max(i + 1, prefix)), a packed document [start, ...) and their combinations. So a row
-// needs two integers, a tile of rows walks one contiguous range of K tiles, and only tiles that
+// itself [0, max(i + 1, prefix)), a packed document [start, ...), a sliding window [i + 1 − window, …)
+// and their combinations; sinks (kModSink), the first tokens of a document that stay visible behind
+// the window, are a second one in front of it. So a row needs two integers (or four), a tile of rows walks one contiguous range of K tiles, and only tiles that
 // an interval's end crosses compare element by element. fa_visible_kernel makes the intervals
 // and the walks once for a batch; every layer's forward and backward reads them.
 #pragma once
@@ -39,6 +40,7 @@ constexpr int kModRef = 16;  // with a cap alone, small enough: the softmax's re
 constexpr int kModRest = 32; // o's rest is written (two tiles; one tile: kModRef only, others look at the pointer)
 constexpr int kModTight = 64; // kModRef on two tiles, d = 64, without rest: masked or far steps are common
 constexpr int kModTree = 8;  // new tokens against a cache (fa_tree_walk.cuh)
+constexpr int kModSink = 128;  // a second interval of keys a row, in front of the first (TREE: a window and sinks)
 
 // The cap. With u = z / cap = in · s (s the raw score), the capped score in base 2 is
 //   |u| ≤ 0.8:  s · (c0 + c1·s² + … + c4·s⁸): tanh(u)/u ≈ P(u²), P of degree 4 fitted by
@@ -111,6 +113,10 @@ struct CapFactors {
   float bend;      // −1 / out²: 1 − tanh² = 1 + bend · (capped score)²
   float limit;     // raw scores up to this are |u| ≤ kCapBend
 };
+
+// The bits [lo, hi) of a word, as far as it has them.
+__device__ __forceinline__ uint32_t bits_below(int n) { return n >= 32 ? 0xFFFFFFFFu : n <= 0 ? 0u : (1u << n) - 1u; }
+__device__ __forceinline__ uint32_t bits_of(int lo, int hi) { return bits_below(hi) & ~bits_below(lo); }
 
 // The sum l of a row's weights with its largest one, w, rounded to bf16.
 __device__ __forceinline__ float top_rounded(float l, float w) {

@@ -48,6 +48,54 @@ static VisibleLayout visible_layout(int B, int T) {
   return l;
 }
 
+// What fa_visible_window adds behind it where there are sinks:
+//   sink_rows   int2 [B][T_pad]   the sinks that a row sees beside its window, an interval before lo
+//   sink_units  int2 [B][n_t]     their K tiles for each of fwd, all before its first
+//   sink_pairs  int4 [B][n_p]     the same for both tiles of each of pairs
+//   pieces      int4 [B][n_rec][2]  takes the place of bwd: a key tile with sinks is seen by query tiles up
+//                 to its document's end, and such a walk is cut into pieces of at most `piece` query
+//                 tiles, most first: (tile, first query tile, past the last, as in bwd), (the slot of a cut
+//                 tile's piece or −1, whether the tile has sinks beyond a window, 0, 0); tile n_t: no piece
+//   cuts        int4 [B][n_cut]   the cut key tiles: (tile, first slot, slots, 0); no slots: none
+//   far, near   per tile, where a sequence has more than kVisTiles
+struct WindowLayout {
+  VisibleLayout base;
+  size_t sink_rows, sink_units, sink_pairs, pieces, cuts, far, near, bytes;
+  int piece, n_rec, n_cut, n_slots;
+};
+
+constexpr int kMaxSinks = 1024;
+
+static WindowLayout window_layout(int B, int T, int window, int sinks) {
+  auto up = [](size_t x) { return (x + 255u) / 256u * 256u; };
+  WindowLayout l{};
+  l.base = visible_layout(B, T);
+  l.bytes = l.base.bytes;
+  const size_t b = static_cast<size_t>(B);
+  const long long n_t = (static_cast<long long>(T) + 127) / 128;
+  l.n_rec = static_cast<int>(n_t);
+  if (sinks == 0) return l;
+  // A key tile without sinks is seen by at most (window + 126) / 128 + 1 query tiles: it is never cut.
+  l.piece = static_cast<int>(std::max<long long>(8, std::min<long long>(window, T) / 128 + 2));
+  // Pieces beyond one a tile. A walk of n > piece ≥ 8 query tiles leaves at most (n − 1) / piece of them, and
+  // it is that of a document of 128·(n − 2) tokens and more, so n − 1 ≤ 8/7 of its length in tiles (n ≥ 9);
+  // at most (sinks + 126) / 128 + 1 tiles hold a document's sinks, and documents do not overlap.
+  const long long holds = (sinks + 126) / 128 + 1;
+  const long long extra = (n_t * holds * 8 + 7 * l.piece - 1) / (7 * l.piece);
+  l.n_rec = static_cast<int>(n_t + extra);
+  l.n_cut = static_cast<int>(std::min(extra, n_t));
+  l.n_slots = static_cast<int>(extra + l.n_cut);
+  l.sink_rows = l.bytes;
+  l.sink_units = l.sink_rows + up(b * n_t * 128 * 8);
+  l.sink_pairs = l.sink_units + up(b * n_t * 8);
+  l.pieces = l.sink_pairs + up(b * ((n_t + 1) / 2) * 16);
+  l.cuts = l.pieces + up(b * l.n_rec * 32);
+  l.far = l.cuts + up(b * l.n_cut * 16);
+  l.near = l.far + up(b * n_t * 4);
+  l.bytes = l.near + up(b * n_t * 8);
+  return l;
+}
+
 struct VisibleParams {
   const int* ids;     // [B][T] or null
   const int* prefix;  // [B] or [B][T] or null
@@ -55,6 +103,11 @@ struct VisibleParams {
   int2* rows;
   int4 *fwd, *pairs, *bwd;
   int2 *whole, *span, *seen;
+  // a sliding window and sinks
+  int window, sinks, piece, n_rec, n_cut;
+  int2 *sink_rows, *sink_units, *near;
+  int4 *sink_pairs, *pieces, *cuts;
+  int* far;
 };
 
 constexpr int kVisThreads = 1024;
@@ -95,11 +148,15 @@ __device__ __forceinline__ void doc_bits(const int* ids, int i0, int end, uint32
 // block joining the stretches. Then a warp a tile: its rows' extremes, the query tiles that see
 // it, and its place among the tiles by the number it has to walk (a count of the tiles before it:
 // n_t² comparisons, which at 16384 tokens are 4 a lane and tile). Latency is all it costs; the
-// tiles' extremes are kept in shared memory up to kVisTiles of them.
+// tiles' extremes are kept in shared memory up to kVisTiles of them. WINDOW: rows see the last
+// `window` keys at most; SINK: and the first `sinks` of their document (fa_visible_window).
+template <bool WINDOW, bool SINK>
 __global__ void __launch_bounds__(kVisThreads) fa_visible_kernel(const VisibleParams p) {
   __shared__ int s_last[kVisThreads / 32], s_first[kVisThreads / 32];
   __shared__ int s_pad;
   __shared__ int2 s_span[kVisTiles], s_seen[kVisTiles];
+  __shared__ int s_far[SINK ? kVisTiles : 1];   // past the last query tile that sees a key tile's sinks, 0: none beyond a window
+  __shared__ int2 s_near[SINK ? kVisTiles : 1]; // a query tile's K tiles with sinks, before its first
   pdl_wait();
   pdl_launch_dependents();
   const int b = blockIdx.x, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -110,6 +167,14 @@ __global__ void __launch_bounds__(kVisThreads) fa_visible_kernel(const VisiblePa
   int2* rows = p.rows + static_cast<size_t>(b) * T_pad;
   int2* span = n_t <= kVisTiles ? s_span : p.span + static_cast<size_t>(b) * n_t;
   int2* seen = n_t <= kVisTiles ? s_seen : p.seen + static_cast<size_t>(b) * n_t;
+  int* far = nullptr;
+  int2 *near = nullptr, *sink_rows = nullptr;
+  if constexpr (SINK) {
+    far = n_t <= kVisTiles ? s_far : p.far + static_cast<size_t>(b) * n_t;
+    near = n_t <= kVisTiles ? s_near : p.near + static_cast<size_t>(b) * n_t;
+    sink_rows = p.sink_rows + static_cast<size_t>(b) * T_pad;
+    for (int t = tid; t < n_t; t += kVisThreads) far[t] = 0;
+  }
   if (tid == 0) s_pad = n_t;
   const long long seg = (T_pad + kVisThreads - 1) / kVisThreads;
   const int a0 = static_cast<int>(min(static_cast<long long>(T), tid * seg));
@@ -161,6 +226,11 @@ __global__ void __launch_bounds__(kVisThreads) fa_visible_kernel(const VisiblePa
     if (p.prefix_per_token) pre_at = p.prefix + static_cast<size_t>(b) * T;
     else pre_all = max(0, p.prefix[b]);
   }
+  int far_tile = -1, far_end = 0;  // SINK: the key tile at hand, and its last document's end
+  auto flush_far = [&]() {
+    if (far_end > 0) atomicMax(far + far_tile, (far_end + 127) >> 7);
+    far_end = 0;
+  };
   for (int g0 = a0 + max(0, (a1 - a0 - 1)) / 32 * 32; g0 >= a0 && a1 > a0; g0 -= 32) {
     if (!one) doc_bits(ids, g0, a1, &starts, &pads);
     for (int o = min(32, a1 - g0) - 1; o >= 0; --o) {
@@ -173,20 +243,36 @@ __global__ void __launch_bounds__(kVisThreads) fa_visible_kernel(const VisiblePa
         lo = rows[i].x;
       }
       int2 r = make_int2(lo, end);
+      int2 sink = make_int2(0, 0);
       if ((pads >> o) & 1u) {
         r = make_int2(0, 0);
         padded = i >> 7;  // (from the back)
       } else {
-        if (p.causal) {
+        if constexpr (WINDOW) {
+          r = make_int2(max(lo, i + 1 - p.window), i + 1);
+          if constexpr (SINK) {
+            if (lo < r.x) sink = make_int2(lo, min(lo + p.sinks, r.x));
+            if (i - lo < p.sinks && end - i > p.window) {  // seen from beyond the window
+              if (far_tile != i >> 7) flush_far();
+              far_tile = i >> 7;
+              far_end = max(far_end, end);
+            }
+          }
+        } else if (p.causal) {
           const int pre = pre_at ? max(0, pre_at[i]) : pre_all;
           r.y = max(i + 1, pre > end - lo ? end : lo + pre);
         }
       }
       rows[i] = r;
+      if constexpr (SINK) sink_rows[i] = sink;
       if (lo == i) end = i;
     }
   }
-  for (long long i = T + tid; i < T_pad; i += kVisThreads) rows[i] = make_int2(0, 0);
+  if constexpr (SINK) flush_far();
+  for (long long i = T + tid; i < T_pad; i += kVisThreads) {
+    rows[i] = make_int2(0, 0);
+    if constexpr (SINK) sink_rows[i] = make_int2(0, 0);
+  }
   padded = __reduce_min_sync(0xffffffffu, padded);
   if (lane == 0) atomicMin(&s_pad, padded);
   __syncthreads();
@@ -213,6 +299,23 @@ __global__ void __launch_bounds__(kVisThreads) fa_visible_kernel(const VisiblePa
       p.whole[t0 + t] = make_int2(lo_max, hi_min);
       span[t] = hi_max > lo_min ? make_int2(lo_min, hi_max) : make_int2(0, 0);
     }
+    if constexpr (SINK) {
+      // The tiles with sinks before the walk's first. (Documents that start within it have theirs in the walk.)
+      const int kb = lo_min >> 7;
+      int first_sink = T, past = 0;
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        const int i = t * 128 + lane + 32 * k;
+        const int2 s = i < T ? sink_rows[i] : make_int2(0, 0);
+        if (s.y > s.x && s.x >> 7 < kb) {
+          first_sink = min(first_sink, s.x);
+          past = max(past, s.y);
+        }
+      }
+      first_sink = __reduce_min_sync(0xffffffffu, first_sink);
+      past = __reduce_max_sync(0xffffffffu, past);
+      if (lane == 0) near[t] = past > 0 ? make_int2(first_sink >> 7, min((past + 127) >> 7, kb)) : make_int2(0, 0);
+    }
   }
   __syncthreads();
   padded = s_pad;
@@ -229,24 +332,84 @@ __global__ void __launch_bounds__(kVisThreads) fa_visible_kernel(const VisiblePa
     }
     f = __reduce_min_sync(0xffffffffu, f);
     l = __reduce_max_sync(0xffffffffu, l);
+    if constexpr (SINK) {
+      if (far[t] > 0) {
+        f = min(f, t);
+        l = max(l, far[t]);
+      }
+    }
     if (lane == 0) seen[t] = l > f ? make_int2(f, l) : make_int2(0, 0);
   }
   __syncthreads();
+  // SINK: a key tile's pieces, and the length of the longest
+  auto pieces_of = [&](int t) {
+    const int n = seen[t].y - seen[t].x;
+    return far[t] > 0 && n > p.piece ? (n + p.piece - 1) / p.piece : 1;
+  };
+  int n_pieces = 0, n_cuts = 0;
   for (int t = warp; t < n_t; t += kWarps) {
     const int2 s = span[t], k = seen[t];
     const int kb = s.x >> 7, ke = (s.y + 127) >> 7;
-    int rf = 0, rb = 0;
-    for (int q = lane; q < n_t; q += 32) {
-      const int2 os = span[q], ok = seen[q];
-      const int on = ((os.y + 127) >> 7) - (os.x >> 7), on2 = ok.y - ok.x;
-      rf += on > ke - kb || (on == ke - kb && q < t);
-      rb += on2 > k.y - k.x || (on2 == k.y - k.x && q < t);
+    if constexpr (SINK) {
+      const int2 sk = near[t];
+      const int n = ke - kb + sk.y - sk.x, pc = pieces_of(t), m = k.y - k.x, len = (m + pc - 1) / pc;
+      int rf = 0, rb = 0, slot = 0, cut = 0, all = 0, cuts = 0;
+      for (int q = lane; q < n_t; q += 32) {
+        const int2 os = span[q], ok = seen[q], osk = near[q];
+        const int on = ((os.y + 127) >> 7) - (os.x >> 7) + osk.y - osk.x;
+        const int opc = pieces_of(q), olen = (ok.y - ok.x + opc - 1) / opc;
+        rf += on > n || (on == n && q < t);
+        if (olen > len || (olen == len && q < t)) rb += opc;
+        if (opc > 1 && q < t) {
+          slot += opc;
+          ++cut;
+        }
+        all += opc;
+        cuts += opc > 1;
+      }
+      rf = __reduce_add_sync(0xffffffffu, rf);
+      rb = __reduce_add_sync(0xffffffffu, rb);
+      slot = __reduce_add_sync(0xffffffffu, slot);
+      cut = __reduce_add_sync(0xffffffffu, cut);
+      n_pieces = __reduce_add_sync(0xffffffffu, all);
+      n_cuts = __reduce_add_sync(0xffffffffu, cuts);
+      if (lane == 0) {
+        p.fwd[t0 + rf] = make_int4(t, kb, ke, padded);
+        p.sink_units[t0 + rf] = sk;
+        if (pc > 1 && cut < p.n_cut) p.cuts[static_cast<size_t>(b) * p.n_cut + cut] = make_int4(t, slot, pc, 0);
+      }
+      // pieces of len or len − 1 query tiles
+      const int longer = m - (len - 1) * pc;
+      for (int i = lane; i < pc && rb + i < p.n_rec; i += 32) {
+        const int q0 = k.x + i * (len - 1) + min(i, longer);
+        int4* out = p.pieces + (static_cast<size_t>(b) * p.n_rec + rb + i) * 2;
+        out[0] = make_int4(t, q0, q0 + len - (i < longer ? 0 : 1), 2 * padded + (p.whole[t0 + t].y == 0 ? 1 : 0));
+        out[1] = make_int4(pc > 1 ? slot + i : -1, far[t] > 0, 0, 0);
+      }
+    } else {
+      int rf = 0, rb = 0;
+      for (int q = lane; q < n_t; q += 32) {
+        const int2 os = span[q], ok = seen[q];
+        const int on = ((os.y + 127) >> 7) - (os.x >> 7), on2 = ok.y - ok.x;
+        rf += on > ke - kb || (on == ke - kb && q < t);
+        rb += on2 > k.y - k.x || (on2 == k.y - k.x && q < t);
+      }
+      rf = __reduce_add_sync(0xffffffffu, rf);
+      rb = __reduce_add_sync(0xffffffffu, rb);
+      if (lane == 0) {
+        p.fwd[t0 + rf] = make_int4(t, kb, ke, padded);
+        p.bwd[t0 + rb] = make_int4(t, k.x, k.y, 2 * padded + (p.whole[t0 + t].y == 0 ? 1 : 0));
+      }
     }
-    rf = __reduce_add_sync(0xffffffffu, rf);
-    rb = __reduce_add_sync(0xffffffffu, rb);
-    if (lane == 0) {
-      p.fwd[t0 + rf] = make_int4(t, kb, ke, padded);
-      p.bwd[t0 + rb] = make_int4(t, k.x, k.y, 2 * padded + (p.whole[t0 + t].y == 0 ? 1 : 0));
+  }
+  if constexpr (SINK) {
+    if (warp == 0) {  // (it has had tile 0)
+      for (int i = n_pieces + lane; i < p.n_rec; i += 32) {
+        int4* out = p.pieces + (static_cast<size_t>(b) * p.n_rec + i) * 2;
+        out[0] = make_int4(n_t, 0, 0, 2 * n_t);
+        out[1] = make_int4(-1, 0, 0, 0);
+      }
+      for (int i = n_cuts + lane; i < p.n_cut; i += 32) p.cuts[static_cast<size_t>(b) * p.n_cut + i] = make_int4(0, 0, 0, 0);
     }
   }
   // Pairs of query tiles, by the length of their union's walk.
@@ -273,6 +436,10 @@ __global__ void __launch_bounds__(kVisThreads) fa_visible_kernel(const VisiblePa
       int4* out = p.pairs + (static_cast<size_t>(b) * n_p + r) * 2;
       out[0] = make_int4(2 * t, padded, a.x, a.y);
       out[1] = make_int4(c.x, c.y, 0, 0);
+      if constexpr (SINK) {
+        const int2 k0 = near[2 * t], k1 = 2 * t + 1 < n_t ? near[2 * t + 1] : make_int2(0, 0);
+        p.sink_pairs[static_cast<size_t>(b) * n_p + r] = make_int4(k0.x, k0.y, k1.x, k1.y);
+      }
     }
   }
 }
@@ -316,21 +483,14 @@ bool any_misaligned(std::initializer_list<const void*> ps) {
   return false;
 }
 
-}  // namespace
+bool window_ok(int window, int sinks) { return window >= 1 && sinks >= 0 && sinks <= fa::kMaxSinks; }
 
-extern "C" {
+size_t up256(size_t x) { return (x + 255u) / 256u * 256u; }
 
-size_t fa_visible_size(int B, int T) {
-  if (B <= 0 || T <= 0) return 0;
-  const long long n_t = (static_cast<long long>(T) + 127) / 128;
-  if (n_t * 128 > INT32_MAX || n_t * B > INT32_MAX) return 0;
-  return fa::visible_layout(B, T).bytes;
-}
-
-int fa_visible(const int* doc_ids, const int* prefix_len, int prefix_per_token, int causal,
-               void* visible, size_t visible_bytes, int B, int T, void* stream) {
+// fa_visible and fa_visible_window (window > 0), whose buffer has `need` bytes.
+int make_visible(const int* doc_ids, const int* prefix_len, int prefix_per_token, int causal, int window, int sinks,
+                 void* visible, size_t visible_bytes, size_t need, int B, int T, void* stream) {
   if (!visible) return FA_ERR_INVALID_ARG;
-  const size_t need = fa_visible_size(B, T);
   if (need == 0 || visible_bytes < need) return FA_ERR_INVALID_ARG;
   if ((reinterpret_cast<uintptr_t>(visible) & 255u) || (reinterpret_cast<uintptr_t>(doc_ids) & 3u) ||
       (reinterpret_cast<uintptr_t>(prefix_len) & 3u))
@@ -358,14 +518,35 @@ int fa_visible(const int* doc_ids, const int* prefix_len, int prefix_per_token, 
   p.whole = reinterpret_cast<int2*>(base + l.whole);
   p.span = reinterpret_cast<int2*>(base + l.span);
   p.seen = reinterpret_cast<int2*>(base + l.seen);
-  const cudaError_t e = fa::launch_pdl(fa::fa_visible_kernel, static_cast<unsigned>(B), fa::kVisThreads, 0,
+  auto* fn = &fa::fa_visible_kernel<false, false>;
+  if (window > 0) {
+    p.window = window;
+    p.sinks = sinks;
+    fn = &fa::fa_visible_kernel<true, false>;
+    if (sinks > 0) {
+      const fa::WindowLayout wl = fa::window_layout(B, T, window, sinks);
+      p.piece = wl.piece;
+      p.n_rec = wl.n_rec;
+      p.n_cut = wl.n_cut;
+      p.sink_rows = reinterpret_cast<int2*>(base + wl.sink_rows);
+      p.sink_units = reinterpret_cast<int2*>(base + wl.sink_units);
+      p.sink_pairs = reinterpret_cast<int4*>(base + wl.sink_pairs);
+      p.pieces = reinterpret_cast<int4*>(base + wl.pieces);
+      p.cuts = reinterpret_cast<int4*>(base + wl.cuts);
+      p.far = reinterpret_cast<int*>(base + wl.far);
+      p.near = reinterpret_cast<int2*>(base + wl.near);
+      fn = &fa::fa_visible_kernel<true, true>;
+    }
+  }
+  const cudaError_t e = fa::launch_pdl(fn, static_cast<unsigned>(B), fa::kVisThreads, 0,
                                        static_cast<cudaStream_t>(stream), p);
   return e == cudaSuccess ? FA_OK : FA_ERR_LAUNCH;
 }
 
-int fa_fwd_mod(const void* q, const void* k, const void* v, void* o, float* lse, void* rest,
-               const void* visible, int causal, float softcap, const float* slopes, int B, int H, int Hkv, int T, int d,
-               float scale, int* status, unsigned long long timeout_ns, void* stream) {
+// fa_fwd_mod and fa_fwd_window (window > 0), whose visibility has visible_bytes.
+int fwd_mod(const void* q, const void* k, const void* v, void* o, float* lse, void* rest, const void* visible,
+            size_t visible_bytes, int causal, int window, int sinks, float softcap, const float* slopes, int B, int H,
+            int Hkv, int T, int d, float scale, int* status, unsigned long long timeout_ns, void* stream) {
   if (!q || !k || !v || !o || !lse) return FA_ERR_INVALID_ARG;
   fa::CapFactors cap;
   if (!mod_sizes(B, H, Hkv, T, d) || !scale_ok(scale) || !cap_factors(scale, softcap, &cap))
@@ -377,7 +558,7 @@ int fa_fwd_mod(const void* q, const void* k, const void* v, void* o, float* lse,
   const size_t qb = static_cast<size_t>(BH) * T * d * 2, kb = static_cast<size_t>(B) * Hkv * T * d * 2;
   const size_t lb = static_cast<size_t>(BH) * T * 4;
   const void* ins[5] = {q, k, v, visible, slopes};
-  const size_t in_bytes[5] = {qb, kb, kb, fa_visible_size(B, T), static_cast<size_t>(H) * 4};
+  const size_t in_bytes[5] = {qb, kb, kb, visible_bytes, static_cast<size_t>(H) * 4};
   for (int i = 0; i < 5; ++i)
     if (ins[i] && (overlaps(o, qb, ins[i], in_bytes[i]) || overlaps(lse, lb, ins[i], in_bytes[i]) ||
                    (rest && overlaps(rest, qb, ins[i], in_bytes[i]))))
@@ -439,6 +620,12 @@ int fa_fwd_mod(const void* q, const void* k, const void* v, void* o, float* lse,
     a.p.mod.rows = reinterpret_cast<const int2*>(base + l.rows);
     a.p.mod.units = reinterpret_cast<const int4*>(base + l.fwd);
     a.p.mod.pairs = reinterpret_cast<const int4*>(base + l.pairs);
+    if (sinks > 0) {
+      const fa::WindowLayout wl = fa::window_layout(B, T, window, sinks);
+      a.p.mod.sink_rows = reinterpret_cast<const int2*>(base + wl.sink_rows);
+      a.p.mod.sink_units = reinterpret_cast<const int2*>(base + wl.sink_units);
+      a.p.mod.sink_pairs = reinterpret_cast<const int4*>(base + wl.sink_pairs);
+    }
   }
   a.p.mod.slopes = slopes;
   a.p.mod.rest = static_cast<__nv_bfloat16*>(rest);
@@ -457,30 +644,26 @@ int fa_fwd_mod(const void* q, const void* k, const void* v, void* o, float* lse,
   const bool short_walks = visible || (causal && T <= 4096);
   const int tight = d == 64 && mod == (fa::kModOn | fa::kModCap | fa::kModRef) && (short_walks || softcap < 25.0f)
                         ? fa::kModTight : 0;
+  if (sinks > 0) {
+    const cudaError_t e = pairs ? (d == 64 ? fa::launch_fwd_sink_pairs_d64(a, mod) : fa::launch_fwd_sink_pairs_d128(a, mod))
+                                : (d == 64 ? fa::launch_fwd_sink_d64(a, mod) : fa::launch_fwd_sink_d128(a, mod));
+    return e == cudaSuccess ? FA_OK : FA_ERR_LAUNCH;
+  }
   const cudaError_t e = pairs ? (d == 64 ? fa::launch_fwd_mod_pairs_d64(a, mod | tight) : fa::launch_fwd_mod_pairs_d128(a, mod))
                               : (d == 64 ? fa::launch_fwd_mod_d64(a, mod) : fa::launch_fwd_mod_d128(a, mod));
   return e == cudaSuccess ? FA_OK : FA_ERR_LAUNCH;
 }
 
-size_t fa_bwd_mod_workspace_size(int B, int H, int Hkv, int T, int d) {
-  if (!mod_sizes(B, H, Hkv, T, d)) return 0;
-  const size_t base = fa_bwd_workspace_size(B, H, T, d);  // a multiple of 256
-  const int parts = bwd_parts(B, H, Hkv, T);
-  if (base == 0 || parts == 1) return base;
-  return base + static_cast<size_t>(2) * parts * B * Hkv * T * d * 4;
-}
-
-int fa_bwd_mod(const void* q, const void* k, const void* v, const void* o, const void* dout,
-               const float* lse, const void* rest, void* dq, void* dk, void* dv, void* workspace,
-               size_t workspace_bytes, const void* visible, int causal, float softcap, const float* slopes, int B, int H,
-               int Hkv, int T, int d, float scale, int* status, unsigned long long timeout_ns,
-               void* stream) {
+// fa_bwd_mod and fa_bwd_window, with a workspace of `need` bytes.
+int bwd_mod(const void* q, const void* k, const void* v, const void* o, const void* dout, const float* lse,
+            const void* rest, void* dq, void* dk, void* dv, void* workspace, size_t workspace_bytes, size_t need,
+            const void* visible, size_t visible_bytes, int causal, int window, int sinks, float softcap, const float* slopes,
+            int B, int H, int Hkv, int T, int d, float scale, int* status, unsigned long long timeout_ns, void* stream) {
   if (!q || !k || !v || !o || !dout || !lse || !dq || !dk || !dv || !workspace)
     return FA_ERR_INVALID_ARG;
   fa::CapFactors cap;
   if (!mod_sizes(B, H, Hkv, T, d) || !scale_ok(scale) || !cap_factors(scale, softcap, &cap))
     return FA_ERR_INVALID_ARG;
-  const size_t need = fa_bwd_mod_workspace_size(B, H, Hkv, T, d);
   if (need == 0 || workspace_bytes < need) return FA_ERR_INVALID_ARG;
   if (any_misaligned({q, k, v, o, dout, lse, rest, dq, dk, dv}) || (reinterpret_cast<uintptr_t>(workspace) & 255u) ||
       (reinterpret_cast<uintptr_t>(visible) & 255u) || (reinterpret_cast<uintptr_t>(slopes) & 3u))
@@ -488,7 +671,7 @@ int fa_bwd_mod(const void* q, const void* k, const void* v, const void* o, const
   const int BH = B * H, BHkv = B * Hkv;
   const size_t qb = static_cast<size_t>(BH) * T * d * 2, kb = static_cast<size_t>(BHkv) * T * d * 2;
   const void* ins[9] = {q, k, v, o, dout, lse, visible, slopes, rest};
-  const size_t in_bytes[9] = {qb, kb, kb, qb, qb, static_cast<size_t>(BH) * T * 4, fa_visible_size(B, T),
+  const size_t in_bytes[9] = {qb, kb, kb, qb, qb, static_cast<size_t>(BH) * T * 4, visible_bytes,
                               static_cast<size_t>(H) * 4, qb};
   const void* outs[4] = {dq, dk, dv, workspace};
   const size_t out_bytes[4] = {qb, kb, kb, need};
@@ -509,6 +692,7 @@ int fa_bwd_mod(const void* q, const void* k, const void* v, const void* o, const
       !encode_map(enc, &a.tm_v, v, T, d, BHkv) || !encode_map(enc, &a.tm_do, dout, T, d, BH, bq))
     return FA_ERR_INVALID_ARG;
   const int n_t = (T + 127) / 128, T_pad = n_t * 128;
+  int n_rec = n_t;  // walks a key head's part
   auto up = [](size_t x) { return (x + 255u) / 256u * 256u; };
   const size_t rows = static_cast<size_t>(BH) * T_pad;
   uint8_t* ws = static_cast<uint8_t*>(workspace);
@@ -543,7 +727,18 @@ int fa_bwd_mod(const void* q, const void* k, const void* v, const void* o, const
     a.p.mod.rows = reinterpret_cast<const int2*>(base + l.rows);
     a.p.mod.units = reinterpret_cast<const int4*>(base + l.bwd);
     a.p.mod.whole = reinterpret_cast<const int2*>(base + l.whole);
+    if (sinks > 0) {
+      const fa::WindowLayout wl = fa::window_layout(B, T, window, sinks);
+      a.p.mod.units = reinterpret_cast<const int4*>(base + wl.pieces);
+      a.p.mod.sink_rows = reinterpret_cast<const int2*>(base + wl.sink_rows);
+      a.p.mod.cuts = reinterpret_cast<const int4*>(base + wl.cuts);
+      a.p.mod.piece_out = reinterpret_cast<float*>(ws + up256(fa_bwd_mod_workspace_size(B, H, Hkv, T, d)));
+      a.p.mod.n_cut = wl.n_cut;
+      a.p.mod.n_slots = wl.n_slots;
+      n_rec = wl.n_rec;
+    }
   }
+  a.p.mod.n_rec = n_rec;
   a.p.mod.slopes = slopes;
   a.p.mod.Hkv = Hkv;
   a.p.mod.group = H / Hkv;
@@ -556,13 +751,98 @@ int fa_bwd_mod(const void* q, const void* k, const void* v, const void* o, const
   a.rest = static_cast<const __nv_bfloat16*>(rest);
   a.lse = lse;
   a.dq = static_cast<__nv_bfloat16*>(dq);
-  a.grid_main = static_cast<unsigned>(static_cast<long long>(n_t) * a.p.BH);
+  a.grid_main = static_cast<unsigned>(static_cast<long long>(n_rec) * a.p.BH);
   a.grid_prep = static_cast<unsigned>(sms) * 8u;
   a.grid_dq = static_cast<unsigned>(sms) * 8u;
   a.stream = static_cast<cudaStream_t>(stream);
   const int mod = mod_bits(softcap, slopes);
-  const cudaError_t e = (d == 64) ? fa::launch_bwd_mod_d64(a, mod, BH) : fa::launch_bwd_mod_d128(a, mod, BH);
+  const cudaError_t e = sinks > 0 ? (d == 64 ? fa::launch_bwd_sink_d64(a, mod, BH) : fa::launch_bwd_sink_d128(a, mod, BH))
+                                  : (d == 64) ? fa::launch_bwd_mod_d64(a, mod, BH) : fa::launch_bwd_mod_d128(a, mod, BH);
   return e == cudaSuccess ? FA_OK : FA_ERR_LAUNCH;
+}
+
+}  // namespace
+
+extern "C" {
+
+size_t fa_visible_size(int B, int T) {
+  if (B <= 0 || T <= 0) return 0;
+  const long long n_t = (static_cast<long long>(T) + 127) / 128;
+  if (n_t * 128 > INT32_MAX || n_t * B > INT32_MAX) return 0;
+  return fa::visible_layout(B, T).bytes;
+}
+
+int fa_visible(const int* doc_ids, const int* prefix_len, int prefix_per_token, int causal,
+               void* visible, size_t visible_bytes, int B, int T, void* stream) {
+  return make_visible(doc_ids, prefix_len, prefix_per_token, causal, 0, 0, visible, visible_bytes,
+                      fa_visible_size(B, T), B, T, stream);
+}
+
+size_t fa_visible_window_size(int B, int T, int window, int sinks) {
+  if (fa_visible_size(B, T) == 0 || !window_ok(window, sinks)) return 0;
+  const fa::WindowLayout l = fa::window_layout(B, T, window, sinks);
+  return static_cast<long long>(l.n_rec) * B > INT32_MAX ? 0 : l.bytes;
+}
+
+int fa_visible_window(const int* doc_ids, int window, int sinks, void* visible, size_t visible_bytes, int B,
+                      int T, void* stream) {
+  return make_visible(doc_ids, nullptr, 0, 1, window, sinks, visible, visible_bytes,
+                      fa_visible_window_size(B, T, window, sinks), B, T, stream);
+}
+
+int fa_fwd_mod(const void* q, const void* k, const void* v, void* o, float* lse, void* rest,
+               const void* visible, int causal, float softcap, const float* slopes, int B, int H, int Hkv, int T, int d,
+               float scale, int* status, unsigned long long timeout_ns, void* stream) {
+  return fwd_mod(q, k, v, o, lse, rest, visible, fa_visible_size(B, T), causal, 0, 0, softcap, slopes, B, H, Hkv, T, d,
+                 scale, status, timeout_ns, stream);
+}
+
+int fa_fwd_window(const void* q, const void* k, const void* v, void* o, float* lse, void* rest,
+                  const void* visible, int window, int sinks, float softcap, const float* slopes, int B, int H, int Hkv,
+                  int T, int d, float scale, int* status, unsigned long long timeout_ns, void* stream) {
+  const size_t vb = fa_visible_window_size(B, T, window, sinks);
+  if (!visible || vb == 0) return FA_ERR_INVALID_ARG;
+  return fwd_mod(q, k, v, o, lse, rest, visible, vb, 1, window, sinks, softcap, slopes, B, H, Hkv, T, d, scale, status,
+                 timeout_ns, stream);
+}
+
+size_t fa_bwd_mod_workspace_size(int B, int H, int Hkv, int T, int d) {
+  if (!mod_sizes(B, H, Hkv, T, d)) return 0;
+  const size_t base = fa_bwd_workspace_size(B, H, T, d);  // a multiple of 256
+  const int parts = bwd_parts(B, H, Hkv, T);
+  if (base == 0 || parts == 1) return base;
+  return base + static_cast<size_t>(2) * parts * B * Hkv * T * d * 4;
+}
+
+int fa_bwd_mod(const void* q, const void* k, const void* v, const void* o, const void* dout,
+               const float* lse, const void* rest, void* dq, void* dk, void* dv, void* workspace,
+               size_t workspace_bytes, const void* visible, int causal, float softcap, const float* slopes, int B, int H,
+               int Hkv, int T, int d, float scale, int* status, unsigned long long timeout_ns,
+               void* stream) {
+  return bwd_mod(q, k, v, o, dout, lse, rest, dq, dk, dv, workspace, workspace_bytes,
+                 fa_bwd_mod_workspace_size(B, H, Hkv, T, d), visible, fa_visible_size(B, T), causal, 0, 0, softcap, slopes,
+                 B, H, Hkv, T, d, scale, status, timeout_ns, stream);
+}
+
+size_t fa_bwd_window_workspace_size(int B, int H, int Hkv, int T, int d, int window, int sinks) {
+  const size_t base = fa_bwd_mod_workspace_size(B, H, Hkv, T, d);
+  if (base == 0 || fa_visible_window_size(B, T, window, sinks) == 0) return 0;
+  if (sinks == 0) return base;
+  const fa::WindowLayout l = fa::window_layout(B, T, window, sinks);
+  if (static_cast<long long>(l.n_rec) * B * Hkv * bwd_parts(B, H, Hkv, T) > INT32_MAX) return 0;
+  return up256(base) + static_cast<size_t>(2) * bwd_parts(B, H, Hkv, T) * B * Hkv * l.n_slots * 128 * d * 4;
+}
+
+int fa_bwd_window(const void* q, const void* k, const void* v, const void* o, const void* dout,
+                  const float* lse, const void* rest, void* dq, void* dk, void* dv, void* workspace,
+                  size_t workspace_bytes, const void* visible, int window, int sinks, float softcap, const float* slopes,
+                  int B, int H, int Hkv, int T, int d, float scale, int* status, unsigned long long timeout_ns,
+                  void* stream) {
+  const size_t vb = fa_visible_window_size(B, T, window, sinks);
+  if (!visible || vb == 0) return FA_ERR_INVALID_ARG;
+  return bwd_mod(q, k, v, o, dout, lse, rest, dq, dk, dv, workspace, workspace_bytes,
+                 fa_bwd_window_workspace_size(B, H, Hkv, T, d, window, sinks), visible, vb, 1, window, sinks, softcap, slopes,
+                 B, H, Hkv, T, d, scale, status, timeout_ns, stream);
 }
 
 }  // extern "C"

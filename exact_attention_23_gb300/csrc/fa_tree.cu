@@ -14,46 +14,13 @@
 #include "fa_launch.h"
 #include "fa_mod_host.h"
 #include "fa_pdl.h"
-#include "fa_tree_kernel.cuh"
+#include "fa_tree_launch.cuh"
 
 using namespace fa::host;
 
 namespace fa {
 
 namespace {
-
-struct TreeLaunch {
-  CUtensorMap tm_k, tm_v;
-  TreeParams p;
-  unsigned grid;
-  cudaStream_t stream;
-};
-
-template <int D, int RG, int MOD>
-cudaError_t launch_tree(const TreeLaunch& a) {
-  auto* fn = &fa_tree_kernel<D, RG, MOD>;
-  const int smem = TreeCfg<D>::kSmemBytes;
-  static std::atomic<uint64_t> done[kMaxDevices / 64 + 1];
-  cudaError_t e = smem_opt_in(fn, smem, done);
-  if (e != cudaSuccess) return e;
-  return launch_pdl(fn, a.grid, kTreeBlock, smem, a.stream, a.tm_k, a.tm_v, a.p);
-}
-
-template <int D, int RG>
-cudaError_t launch_tree_mod(const TreeLaunch& a, int mod) {
-  switch (mod) {
-    case kModOn: return launch_tree<D, RG, kModOn>(a);
-    case kModOn | kModCap: return launch_tree<D, RG, kModOn | kModCap>(a);
-    case kModOn | kModBias: return launch_tree<D, RG, kModOn | kModBias>(a);
-    default: return launch_tree<D, RG, kModOn | kModCap | kModBias>(a);
-  }
-}
-
-template <int D>
-cudaError_t launch_tree_rows(const TreeLaunch& a, int rows, int mod) {
-  return rows == 16 ? launch_tree_mod<D, 1>(a, mod)
-                    : launch_tree_mod<D, 2>(a, mod);
-}
 
 // Up to 32 rows of a key head: the streaming kernel, in one block of 16 or 32 rows, so that the
 // keys are read once. More: blocks of 128 rows on the one-tile tensor-core kernel (B4 H16 Hkv4,
@@ -86,7 +53,8 @@ struct TreeSizes {
   size_t lse_off, parts_off, bytes;
 };
 
-bool tree_sizes(int B, int H, int Hkv, int Tq, int Tmax, int d, int sms, TreeSizes* z) {
+// (window 0: none)
+bool tree_sizes(int B, int H, int Hkv, int Tq, int Tmax, int d, int window, int sinks, int sms, TreeSizes* z) {
   if (B <= 0 || H <= 0 || Hkv <= 0 || Tq <= 0 || Tmax <= 0 || H % Hkv != 0 || (d != 64 && d != 128))
     return false;
   const long long R = static_cast<long long>(H / Hkv) * Tq, BHkv = static_cast<long long>(B) * Hkv;
@@ -98,7 +66,10 @@ bool tree_sizes(int B, int H, int Hkv, int Tq, int Tmax, int d, int sms, TreeSiz
   z->min_per = wide(z->R) ? kMinPerWide : kMinPer;
   z->entries = BHkv * z->row_blocks;
   if (z->entries > (1 << 28) || BHkv * R > (1LL << 40) || BHkv > (1LL << 60) / d / Tmax) return false;
-  const long long chunks = (static_cast<long long>(Tmax) + (1 << z->chunk_log2) - 1) >> z->chunk_log2;
+  auto chunks_of = [&](long long keys) { return (keys + (1 << z->chunk_log2) - 1) >> z->chunk_log2; };
+  long long chunks = chunks_of(Tmax);
+  if (window > 0)  // those with sinks, and those that a window and the new tokens can reach into
+    chunks = std::min(chunks, chunks_of(std::min(sinks, Tmax)) + chunks_of(static_cast<long long>(window) - 1 + Tq) + 1);
   if (z->entries * chunks > INT32_MAX - 128) return false;  // (the kernels number them with an int)
   if (z->entries << (z->rows_log2 - 3) > INT32_MAX) return false;
   const long long most = (z->entries * chunks + z->min_per - 1) / z->min_per;
@@ -127,25 +98,28 @@ bool tree_sizes(int B, int H, int Hkv, int Tq, int Tmax, int d, int sms, TreeSiz
 
 }  // namespace fa
 
-extern "C" {
+namespace {
 
-size_t fa_fwd_tree_workspace_size(int B, int H, int Hkv, int Tq, int Tmax, int d) {
+size_t tree_workspace(int B, int H, int Hkv, int Tq, int Tmax, int d, int window, int sinks) {
   fa::TreeSizes z;
-  if (!fa::tree_sizes(B, H, Hkv, Tq, Tmax, d, 1, &z)) return 0;
+  if (!fa::tree_sizes(B, H, Hkv, Tq, Tmax, d, window, sinks, 1, &z)) return 0;
   int dev = -1, sms = 0;
   if (check_device(&dev, &sms) != FA_OK) return 0;
-  return fa::tree_sizes(B, H, Hkv, Tq, Tmax, d, sms, &z) ? z.bytes : 0;
+  return fa::tree_sizes(B, H, Hkv, Tq, Tmax, d, window, sinks, sms, &z) ? z.bytes : 0;
 }
 
-int fa_fwd_tree(const void* q, const void* k_cache, const void* v_cache, void* o, float* lse,
-                const int* ctx_len, const unsigned char* tree, int tree_per_batch, const int* depths,
-                int depths_per_batch, float softcap, const float* slopes, int B, int H, int Hkv, int Tq,
-                int Tmax, int d, float scale, void* workspace, size_t workspace_bytes, int* status,
-                unsigned long long timeout_ns, void* stream) {
+bool tree_window_ok(int window, int sinks) { return window >= 1 && sinks >= 0; }
+
+// fa_fwd_tree, and fa_fwd_tree_window (window > 0).
+int fwd_tree(const void* q, const void* k_cache, const void* v_cache, void* o, float* lse, const int* ctx_len,
+             const unsigned char* tree, int tree_per_batch, const int* depths, int depths_per_batch, int window,
+             int sinks, float softcap, const float* slopes, int B, int H, int Hkv, int Tq, int Tmax, int d,
+             float scale, void* workspace, size_t workspace_bytes, int* status, unsigned long long timeout_ns,
+             void* stream) {
   if (!q || !k_cache || !v_cache || !o || !lse || !ctx_len) return FA_ERR_INVALID_ARG;
   fa::TreeSizes z;
   fa::CapFactors cap;
-  if (!fa::tree_sizes(B, H, Hkv, Tq, Tmax, d, 1, &z) || !scale_ok(scale) || !cap_factors(scale, softcap, &cap))
+  if (!fa::tree_sizes(B, H, Hkv, Tq, Tmax, d, window, sinks, 1, &z) || !scale_ok(scale) || !cap_factors(scale, softcap, &cap))
     return FA_ERR_INVALID_ARG;
   const uintptr_t words = reinterpret_cast<uintptr_t>(ctx_len) | reinterpret_cast<uintptr_t>(depths) |
                           reinterpret_cast<uintptr_t>(slopes);
@@ -158,7 +132,7 @@ int fa_fwd_tree(const void* q, const void* k_cache, const void* v_cache, void* o
   const size_t tb = static_cast<size_t>(tree_per_batch ? B : 1) * Tq * Tq;
   const size_t db = static_cast<size_t>(depths_per_batch ? B : 1) * Tq * 4;
   const int dst = check_device(&dev, &sms);
-  if (dst == FA_OK && !fa::tree_sizes(B, H, Hkv, Tq, Tmax, d, sms, &z)) return FA_ERR_INVALID_ARG;
+  if (dst == FA_OK && !fa::tree_sizes(B, H, Hkv, Tq, Tmax, d, window, sinks, sms, &z)) return FA_ERR_INVALID_ARG;
   if (!z.solo && (!workspace || workspace_bytes < z.bytes)) return FA_ERR_INVALID_ARG;
   const void* ins[7] = {q, k_cache, v_cache, ctx_len, tree, depths, slopes};
   const size_t in_bytes[7] = {qb, cb, cb, static_cast<size_t>(B) * 4, tb, db, static_cast<size_t>(H) * 4};
@@ -188,7 +162,7 @@ int fa_fwd_tree(const void* q, const void* k_cache, const void* v_cache, void* o
   a.p.status = status;
   a.p.timeout_ns = timeout_ns ? timeout_ns : 2000000000ull;
   a.p.list = fa::TreeList{ctx_len, B, Hkv, Tq, Tmax, z.row_blocks, z.min_per, z.chunk_log2, z.solo ? 1 : 0,
-                          z.solo ? nullptr : reinterpret_cast<int2*>(ws + z.parts_off)};
+                          z.solo ? nullptr : reinterpret_cast<int2*>(ws + z.parts_off), window, sinks};
   a.p.mask = fa::TreeMask{tree, depths, fa::FastDiv::make(static_cast<uint32_t>(Tq)), tree_per_batch != 0,
                           depths_per_batch != 0};
   a.p.cap = cap;
@@ -240,9 +214,12 @@ int fa_fwd_tree(const void* q, const void* k_cache, const void* v_cache, void* o
       f.p.s_negate = fa::kIdescNegateA;
       cap_factors(-scale, softcap, &f.p.mod.cap);
     }
-    e = (d == 64) ? fa::launch_fwd_tree_d64(f, fm) : fa::launch_fwd_tree_d128(f, fm);
+    if (window > 0) e = (d == 64) ? fa::launch_fwd_tree_window_d64(f, fm) : fa::launch_fwd_tree_window_d128(f, fm);
+    else e = (d == 64) ? fa::launch_fwd_tree_d64(f, fm) : fa::launch_fwd_tree_d128(f, fm);
+  } else if (window > 0) {
+    e = (d == 64) ? fa::launch_tree_window_d64(a, 1 << z.rows_log2, mod) : fa::launch_tree_window_d128(a, 1 << z.rows_log2, mod);
   } else {
-    e = (d == 64) ? fa::launch_tree_rows<64>(a, 1 << z.rows_log2, mod) : fa::launch_tree_rows<128>(a, 1 << z.rows_log2, mod);
+    e = (d == 64) ? fa::launch_tree_rows<64, 0>(a, 1 << z.rows_log2, mod) : fa::launch_tree_rows<128, 0>(a, 1 << z.rows_log2, mod);
   }
   if (e != cudaSuccess) return FA_ERR_LAUNCH;
   if (z.solo) return FA_OK;
@@ -252,6 +229,37 @@ int fa_fwd_tree(const void* q, const void* k_cache, const void* v_cache, void* o
   e = fa::launch_pdl(combine, cg, 256, 0, a.stream, a.p, z.rows_log2, static_cast<int>(a.grid),
                      static_cast<unsigned>(groups));
   return e == cudaSuccess ? FA_OK : FA_ERR_LAUNCH;
+}
+
+}  // namespace
+
+extern "C" {
+
+size_t fa_fwd_tree_workspace_size(int B, int H, int Hkv, int Tq, int Tmax, int d) {
+  return tree_workspace(B, H, Hkv, Tq, Tmax, d, 0, 0);
+}
+
+int fa_fwd_tree(const void* q, const void* k_cache, const void* v_cache, void* o, float* lse,
+                const int* ctx_len, const unsigned char* tree, int tree_per_batch, const int* depths,
+                int depths_per_batch, float softcap, const float* slopes, int B, int H, int Hkv, int Tq,
+                int Tmax, int d, float scale, void* workspace, size_t workspace_bytes, int* status,
+                unsigned long long timeout_ns, void* stream) {
+  return fwd_tree(q, k_cache, v_cache, o, lse, ctx_len, tree, tree_per_batch, depths, depths_per_batch, 0, 0, softcap,
+                  slopes, B, H, Hkv, Tq, Tmax, d, scale, workspace, workspace_bytes, status, timeout_ns, stream);
+}
+
+size_t fa_fwd_tree_window_workspace_size(int B, int H, int Hkv, int Tq, int Tmax, int d, int window, int sinks) {
+  return tree_window_ok(window, sinks) ? tree_workspace(B, H, Hkv, Tq, Tmax, d, window, sinks) : 0;
+}
+
+int fa_fwd_tree_window(const void* q, const void* k_cache, const void* v_cache, void* o, float* lse,
+                       const int* ctx_len, const unsigned char* tree, int tree_per_batch, const int* depths,
+                       int depths_per_batch, int window, int sinks, float softcap, const float* slopes, int B, int H,
+                       int Hkv, int Tq, int Tmax, int d, float scale, void* workspace, size_t workspace_bytes,
+                       int* status, unsigned long long timeout_ns, void* stream) {
+  if (!tree_window_ok(window, sinks)) return FA_ERR_INVALID_ARG;
+  return fwd_tree(q, k_cache, v_cache, o, lse, ctx_len, tree, tree_per_batch, depths, depths_per_batch, window, sinks,
+                  softcap, slopes, B, H, Hkv, Tq, Tmax, d, scale, workspace, workspace_bytes, status, timeout_ns, stream);
 }
 
 }  // extern "C"

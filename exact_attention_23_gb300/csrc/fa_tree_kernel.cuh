@@ -87,6 +87,7 @@ __global__ void __launch_bounds__(kTreeBlock, TreeCfg<D>::kCtasPerSm)
   constexpr int NT = NK / 8;               // score tiles of 16 rows × 8 keys
   constexpr int kRows = RG * 16;
   constexpr int kDT = D / 8;               // output tiles of 16 rows × 8 columns
+  constexpr bool kWin = (MOD & kModSink) != 0;  // a window and sinks
   extern __shared__ uint8_t smem_raw[];
   uint8_t* sm = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
   __shared__ uint64_t full[C::kStages], empty[C::kStages];
@@ -106,7 +107,7 @@ __global__ void __launch_bounds__(kTreeBlock, TreeCfg<D>::kCtasPerSm)
   pdl_wait();
   pdl_launch_dependents();
   const WaitCtl wc{&abort_flag, p.status, p.timeout_ns};
-  TreeSegments sg;
+  TreeSegments<kWin> sg;
   sg.begin(p.list);
 
   if (warp == 4) {
@@ -119,6 +120,8 @@ __global__ void __launch_bounds__(kTreeBlock, TreeCfg<D>::kCtasPerSm)
     bool ok = true;
     while (ok && sg.next(p.list)) {
       const int bh = sg.b * p.list.Hkv + sg.hk;
+      int sc = 0, gap = 0;
+      if constexpr (kWin) tree_window(p.list, p.list.ctx_len[sg.b], &sc, &gap);
       for (int u = 2 * sg.c0; ok && u < 2 * sg.c1; ++u, ++n) {  // K and V tiles in turn
         const int st = n % C::kStages;
         if (n >= C::kStages && !mbar_wait_warp(&empty[st], ((n / C::kStages) - 1) & 1, wc)) {
@@ -131,7 +134,7 @@ __global__ void __launch_bounds__(kTreeBlock, TreeCfg<D>::kCtasPerSm)
 #pragma unroll
           for (int x = 0; x < D / 64; ++x)
             tma_load_3d(dst + x * C::kBoxBytes, (u & 1) ? &tm_v : &tm_k, &full[st], x * 64,
-                        (u >> 1) * kTreeKeys, bh);
+                        ((u >> 1) + ((u >> 1) < sc ? 0 : gap)) * kTreeKeys, bh);
         }
         __syncwarp();
       }
@@ -158,6 +161,12 @@ __global__ void __launch_bounds__(kTreeBlock, TreeCfg<D>::kCtasPerSm)
     const int keys = tree_keys(p.list, ctx);
     const int r0 = sg.rb * kRows + rg * 16 + qr;    // this thread's rows: r0 and r0 + 8
     int tok[2];
+    int dep[2] = {0, 0}, lo[2] = {0, 0};  // WINDOW: the rows' depths, and their first context keys
+    int sc = 0, gap = 0, lo_all = 0;
+    if constexpr (kWin) {
+      tree_window(p.list, ctx, &sc, &gap);
+      lo_all = tree_window_start(p.list, ctx);
+    }
     bool live[2];
     float nsl[2] = {0.f, 0.f}, at[2] = {0.f, 0.f};  // (at: positions from the end of the context)
 #pragma unroll
@@ -166,6 +175,10 @@ __global__ void __launch_bounds__(kTreeBlock, TreeCfg<D>::kCtasPerSm)
       live[i] = r < p.R;
       const int g = static_cast<int>(p.mask.div_tq.div(static_cast<uint32_t>(live[i] ? r : 0)));
       tok[i] = (live[i] ? r : 0) - g * Tq;
+      if constexpr (kWin) {
+        dep[i] = p.mask.depths ? tree_depth(p.mask.depths_of(sg.b, Tq)[tok[i]]) : tok[i];
+        lo[i] = tree_row_start(p.list, ctx, dep[i]);
+      }
       if constexpr ((MOD & kModBias) != 0) {
         at[i] = static_cast<float>(p.mask.depths ? p.mask.depths_of(sg.b, Tq)[tok[i]] : tok[i]);
         nsl[i] = p.slopes[sg.hk * (p.R / Tq) + g] * -1.4426950408889634f;
@@ -193,7 +206,7 @@ __global__ void __launch_bounds__(kTreeBlock, TreeCfg<D>::kCtasPerSm)
       if (ok && !mbar_wait_warp(&full[stk], (n / C::kStages) & 1, wc)) ok = false;
       if (!ok) continue;  // (walk on: the merges below are joined by every warp)
       const uint32_t kt = ring + stk * C::kTile, vt = ring + stv * C::kTile;
-      const int key0 = c * kTreeKeys + kg * NK;    // this warp's first key
+      const int key0 = (c + (!kWin || c < sc ? 0 : gap)) * kTreeKeys + kg * NK;  // this warp's first key
       // ---- S = Q·Kᵀ
       // (32 dimensions of every key at a time: the fragments' loads stand together in front of
       // products that do not wait for one another)
@@ -245,14 +258,27 @@ __global__ void __launch_bounds__(kTreeBlock, TreeCfg<D>::kCtasPerSm)
       }
       if (far) to_exponents.template operator()<true>();
       else to_exponents.template operator()<false>();
-      // ---- the new tokens' keys: the tree, and their depths in the bias
+      if constexpr (kWin) {
+        if (__any_sync(0xffffffffu, key0 < max(lo[0], lo[1]))) {
+#pragma unroll
+          for (int j = 0; j < NT; ++j)
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+              const int key = key0 + j * 8 + qc + e;
+#pragma unroll
+              for (int i = 0; i < 2; ++i)
+                if (key >= p.list.sinks && key < min(lo[i], ctx)) s[j][2 * i + e] = -INFINITY;
+            }
+        }
+      }
+      // ---- the new tokens' keys: the tree, and their depths in the bias and the window
       const bool tail = key0 + NK > min(ctx, keys);  // (a context may fill the cache)
       if (tail) {
         // Flags and depths are loaded for a pair of tiles at once, from clamped places, so that no
         // load waits for another.
 #pragma unroll
         for (int j0 = 0; j0 < NT; j0 += 2) {
-          int see[2][2][2], dep[2][2];
+          int see[2][2][2], place[2][2];
 #pragma unroll
           for (int j = 0; j < 2; ++j)
 #pragma unroll
@@ -261,8 +287,8 @@ __global__ void __launch_bounds__(kTreeBlock, TreeCfg<D>::kCtasPerSm)
 #pragma unroll
               for (int i = 0; i < 2; ++i)
                 see[j][e][i] = p.mask.tree ? p.mask.row(sg.b, tok[i], Tq)[dc] : (d <= tok[i] ? 1 : 0);
-              if constexpr ((MOD & kModBias) != 0)
-                dep[j][e] = p.mask.depths ? p.mask.depths_of(sg.b, Tq)[dc] : dc;
+              if constexpr ((MOD & (kModBias | kModSink)) != 0)
+                place[j][e] = p.mask.depths ? p.mask.depths_of(sg.b, Tq)[dc] : dc;
             }
 #pragma unroll
           for (int j = 0; j < 2; ++j)
@@ -274,7 +300,11 @@ __global__ void __launch_bounds__(kTreeBlock, TreeCfg<D>::kCtasPerSm)
                 float& x = s[j0 + j][2 * i + e];
                 if constexpr ((MOD & kModBias) != 0) {  // from the key's index to its position
                   if (d >= 0)
-                    x += nsl[i] * (fabsf(at[i] - static_cast<float>(dep[j][e])) - fabsf(at[i] - static_cast<float>(d)));
+                    x += nsl[i] * (fabsf(at[i] - static_cast<float>(place[j][e])) - fabsf(at[i] - static_cast<float>(d)));
+                }
+                if constexpr (kWin) {
+                  const int there = tree_depth(place[j][e]);
+                  if (d >= 0 && dep[i] - there >= p.list.window && there >= p.list.sinks - ctx) x = -INFINITY;
                 }
                 if (key >= keys || (d >= 0 && see[j][e][i] == 0)) x = -INFINITY;
               }
@@ -322,7 +352,8 @@ __global__ void __launch_bounds__(kTreeBlock, TreeCfg<D>::kCtasPerSm)
         ok = false;
         continue;
       }
-      const bool cut = key0 + NK > keys;  // rows behind the last key may hold anything: taken as 0
+      // rows behind the last key may hold anything: taken as 0 (WINDOW: and those before every token's)
+      const bool cut = key0 + NK > keys || (kWin && key0 < lo_all && key0 + NK > p.list.sinks);
 #pragma unroll
       for (int k = 0; k < NT / 2; ++k) {
         const int row = kg * NK + k * 16 + (lane & 7) + ((lane >> 3) & 1) * 8;
@@ -331,7 +362,8 @@ __global__ void __launch_bounds__(kTreeBlock, TreeCfg<D>::kCtasPerSm)
 #pragma unroll
           for (int h = 0; h < 2; ++h) {
             const int key = key0 + k * 16 + h * 8 + qc;
-            keep[h] = (key < keys ? 0x0000FFFFu : 0u) | (key + 1 < keys ? 0xFFFF0000u : 0u);
+            auto used = [&](int k) { return k < keys && !(kWin && k >= p.list.sinks && k < lo_all); };
+            keep[h] = (used(key) ? 0x0000FFFFu : 0u) | (used(key + 1) ? 0xFFFF0000u : 0u);
           }
         }
 #pragma unroll

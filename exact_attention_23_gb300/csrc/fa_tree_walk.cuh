@@ -25,6 +25,7 @@ struct TreeList {
   int chunk_log2;      // keys a chunk: 1 << chunk_log2
   int solo;            // CTA c takes entry c whole: no partials, no second kernel
   int2* parts;         // [entries] the first stretch that an entry lies in, and their number
+  int window, sinks;   // WINDOW: see tree_window
 };
 
 struct TreeMask {
@@ -46,18 +47,45 @@ __device__ __forceinline__ int tree_keys(const TreeList& p, int ctx) {
   return static_cast<int>(min(static_cast<long long>(ctx) + p.Tq, static_cast<long long>(p.Tmax)));
 }
 
+// WINDOW. A token at position ctx + depth (depths below 0 count as 0) sees the context's keys behind
+// position ctx + depth − window and those before `sinks`, and of the new tokens that it sees otherwise
+// those whose positions are such. So a sequence's list holds the chunks with sinks and those from the
+// first window's start on: list chunk c is chunk c of the cache up to sc and chunk c + gap from there.
+__device__ __forceinline__ int tree_depth(int depth) { return max(depth, 0); }
+// The first row of the context in a token's window, and in any token's.
+__device__ __forceinline__ int tree_row_start(const TreeList& p, int ctx, int depth) {
+  const long long lo = static_cast<long long>(ctx) + depth - p.window + 1;
+  return static_cast<int>(min(max(lo, 0ll), static_cast<long long>(p.Tmax)));
+}
+__device__ __forceinline__ int tree_window_start(const TreeList& p, int ctx) { return tree_row_start(p, ctx, 0); }
+// (One chunk stays, whatever is left of the window, so that a sequence with a context has an entry.)
+__device__ __forceinline__ int tree_window(const TreeList& p, int ctx, int* sc, int* gap) {
+  const int size = 1 << p.chunk_log2, keys = tree_keys(p, ctx);
+  const int total = (keys + size - 1) >> p.chunk_log2;
+  const int first = min(tree_window_start(p, ctx) >> p.chunk_log2, total - 1);
+  *sc = (min(p.sinks, keys) + size - 1) >> p.chunk_log2;
+  *gap = max(0, first - *sc);
+  return total - *gap;
+}
+
+template <bool WINDOW>
 __device__ __forceinline__ int tree_chunks(const TreeList& p, int b) {
   const int ctx = p.ctx_len[b];
   if (ctx < 0) return 0;
+  if constexpr (WINDOW) {
+    int sc, gap;
+    return tree_window(p, ctx, &sc, &gap);
+  }
   const long long keys = static_cast<long long>(ctx) + p.Tq;
   return static_cast<int>((min(keys, static_cast<long long>(p.Tmax)) + (1 << p.chunk_log2) - 1) >> p.chunk_log2);
 }
 
 // Of the 32 sequences from b0: this lane's chunks (of one list entry), and the positions up to and
 // with this lane's sequence; whole warp. (Positions fit an int: the host refuses longer lists.)
+template <bool WINDOW>
 __device__ __forceinline__ void tree_scan(const TreeList& p, int b0, int* chunks, int* incl) {
   const int lane = threadIdx.x & 31;
-  *chunks = b0 + lane < p.B ? tree_chunks(p, b0 + lane) : 0;
+  *chunks = b0 + lane < p.B ? tree_chunks<WINDOW>(p, b0 + lane) : 0;
   int x = *chunks * p.Hkv * p.row_blocks;
 #pragma unroll
   for (int off = 1; off < 32; off <<= 1) {
@@ -68,16 +96,18 @@ __device__ __forceinline__ void tree_scan(const TreeList& p, int b0, int* chunks
 }
 
 // The list's length; the scan of its last 32 sequences stays in chunks and incl. Whole warp.
+template <bool WINDOW>
 __device__ __forceinline__ int tree_total(const TreeList& p, int* chunks, int* incl) {
   int run = 0;
   for (int b0 = 0; b0 < p.B; b0 += 32) {
-    tree_scan(p, b0, chunks, incl);
+    tree_scan<WINDOW>(p, b0, chunks, incl);
     run += __shfl_sync(0xffffffffu, *incl, 31);
   }
   return run;
 }
 
 // A stretch's segments in order.
+template <bool WINDOW>
 struct TreeSegments {
   struct {
     int b, chunks;               // sequence, its chunks
@@ -94,13 +124,13 @@ struct TreeSegments {
       const int entries = p.Hkv * p.row_blocks;
       at.b = static_cast<int>(blockIdx.x) / entries;
       at.entry0 = at.b * entries;
-      at.chunks = tree_chunks(p, at.b);
+      at.chunks = tree_chunks<WINDOW>(p, at.b);
       pos = 0;
       end = 1;
       return;
     }
     int n, incl;
-    const int total = tree_total(p, &n, &incl);
+    const int total = tree_total<WINDOW>(p, &n, &incl);
     per = max(static_cast<int>((total + gridDim.x - 1u) / gridDim.x), p.min_per);
     // (a list shorter than grid · min_per leaves later CTAs nothing)
     pos = static_cast<int>(min(static_cast<long long>(per) * blockIdx.x, static_cast<long long>(total)));
@@ -111,7 +141,7 @@ struct TreeSegments {
     int run = 0, b0 = 0;
     if (p.B > 32) {
       for (; b0 < p.B; b0 += 32) {
-        tree_scan(p, b0, &n, &incl);
+        tree_scan<WINDOW>(p, b0, &n, &incl);
         const int sum = __shfl_sync(0xffffffffu, incl, 31);
         if (pos < run + sum) break;
         run += sum;
@@ -143,7 +173,7 @@ struct TreeSegments {
       at.entry0 += entries;
       y = pos - at.start;
       ++at.b;
-      at.chunks = tree_chunks(p, at.b);
+      at.chunks = tree_chunks<WINDOW>(p, at.b);
     }
     const int e = y / at.chunks;
     b = at.b;

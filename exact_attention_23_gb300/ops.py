@@ -18,9 +18,12 @@ from ._binding import (
     FA_OK,
     FAError,
     fa_bwd_mod_workspace_size,
+    fa_bwd_window_workspace_size,
+    fa_fwd_tree_window_workspace_size,
     fa_fwd_tree_workspace_size,
     fa_norm_rope_bwd_workspace_size,
     fa_visible_size,
+    fa_visible_window_size,
     lib,
 )
 
@@ -109,23 +112,39 @@ class Visible:
     """Who sees whom in a batch, made by ``visible``: an opaque device buffer that ``fwd_mod`` and
     ``bwd_mod`` calls of the same B and T read."""
 
-    __slots__ = ("buffer", "B", "T", "causal")
+    __slots__ = ("buffer", "B", "T", "causal", "window", "sinks")
 
-    def __init__(self, buffer, B: int, T: int, causal: bool):
+    def __init__(self, buffer, B: int, T: int, causal: bool, window: int = 0, sinks: int = 0):
         self.buffer, self.B, self.T, self.causal = buffer, B, T, causal
+        self.window, self.sinks = window, sinks
+
+
+def _check_window(window, sinks, most):
+    """A sliding window (0: none) and its sinks."""
+    if type(window) is not int or type(sinks) is not int or window < 0 or sinks < 0:
+        raise ValueError("window and sinks must be whole numbers of at least 0")
+    if sinks and not window:
+        raise ValueError("sinks without a window: without one every token stays visible")
+    if window > 0x7FFFFFFF or sinks > most:
+        raise ValueError(f"window must be below 2**31, sinks at most {most}")
 
 
 def visible(B: int, T: int, causal: bool = True, doc_ids=None, prefix_len=None, device=None,
-            buffer=None) -> Visible:
+            buffer=None, window: int = 0, sinks: int = 0) -> Visible:
     """The visibility of a batch of B sequences of T tokens, for every layer's ``fwd_mod`` and
     ``bwd_mod``.
 
     ``doc_ids`` (int32 [B, T]): a document is a maximal run of equal ids and sees itself only; a
     negative id is padding, which sees nothing and is seen by nothing. ``causal``: key j is
     visible to query i when j ≤ i or j is one of the first ``prefix_len`` tokens of their document
-    (int32 [B], or [B, T] with each token holding its document's). ``buffer``, a uint8 CUDA tensor
-    of fa_visible_size(B, T) bytes, may be given to reuse it.
+    (int32 [B], or [B, T] with each token holding its document's). ``window`` > 0 (causal, no
+    prefixes): a token sees the last ``window`` tokens of its document, itself among them, and the
+    document's first ``sinks`` (at most 1024). ``buffer``, a uint8 CUDA tensor of fa_visible_size(B, T)
+    bytes (with a window fa_visible_window_size(B, T, window, sinks)), may be given to reuse it.
     """
+    _check_window(window, sinks, 1024)
+    if window and (not causal or prefix_len is not None):
+        raise ValueError("a window is causal and takes no prefixes")
     if device is None:
         device = next((t.device for t in (doc_ids, prefix_len, buffer) if t is not None), "cuda")
     device = torch.device(device)
@@ -137,7 +156,7 @@ def visible(B: int, T: int, causal: bool = True, doc_ids=None, prefix_len=None, 
         _check_int32(doc_ids, ((B, T),), device, "doc_ids")
     if prefix_len is not None:
         _check_int32(prefix_len, ((B,), (B, T)), device, "prefix_len")
-    need = fa_visible_size(B, T)
+    need = fa_visible_window_size(B, T, window, sinks) if window else fa_visible_size(B, T)
     if need == 0:
         raise FAError(FA_ERR_INVALID_ARG, "fa_visible_size")
     if buffer is None:
@@ -145,6 +164,10 @@ def visible(B: int, T: int, causal: bool = True, doc_ids=None, prefix_len=None, 
     elif not isinstance(buffer, torch.Tensor) or buffer.dtype is not _U8 or not buffer.is_contiguous():
         raise ValueError("buffer must be a contiguous uint8 CUDA tensor")
     _same_device(buffer, device, "buffer")
+    if window:
+        _call(device, "fa_visible_window", _ptr(doc_ids), window, sinks, buffer.data_ptr(),
+              buffer.numel(), B, T)
+        return Visible(buffer, B, T, True, window, sinks)
     _call(device, "fa_visible", _ptr(doc_ids), _ptr(prefix_len),
           prefix_len is not None and prefix_len.dim() == 2, causal, buffer.data_ptr(),
           buffer.numel(), B, T)
@@ -205,15 +228,23 @@ def fwd_mod(q, k, v, visible=None, causal: bool | None = None, softcap: float = 
     if rest is not None:
         _check_like(rest, q, "rest")
     _check_status(status, device)
+    if visible is not None and visible.window:
+        _call(device, "fa_fwd_window", q.data_ptr(), k.data_ptr(), v.data_ptr(), out.data_ptr(),
+              lse.data_ptr(), _ptr(rest), visible.buffer.data_ptr(), visible.window, visible.sinks,
+              softcap, _ptr(slopes), B, H, Hkv, T, d, scale, _ptr(status), timeout_ns)
+        return out, lse
     _call(device, "fa_fwd_mod", q.data_ptr(), k.data_ptr(), v.data_ptr(),
           out.data_ptr(), lse.data_ptr(), _ptr(rest), None if visible is None else visible.buffer.data_ptr(),
           causal, softcap, _ptr(slopes), B, H, Hkv, T, d, scale, _ptr(status), timeout_ns)
     return out, lse
 
 
-def bwd_mod_workspace(B: int, H: int, Hkv: int, T: int, d: int, device=None):
-    """A uint8 CUDA tensor large enough to serve as ``bwd_mod``'s workspace."""
-    n = fa_bwd_mod_workspace_size(B, H, Hkv, T, d)
+def bwd_mod_workspace(B: int, H: int, Hkv: int, T: int, d: int, device=None, window: int = 0,
+                      sinks: int = 0):
+    """A uint8 CUDA tensor large enough to serve as ``bwd_mod``'s workspace (with a visibility that has
+    this window and these sinks)."""
+    n = (fa_bwd_window_workspace_size(B, H, Hkv, T, d, window, sinks) if window
+         else fa_bwd_mod_workspace_size(B, H, Hkv, T, d))
     if n == 0:
         raise FAError(FA_ERR_INVALID_ARG, "fa_bwd_mod_workspace_size")
     return torch.empty(n, dtype=_U8, device="cuda" if device is None else device)
@@ -247,12 +278,20 @@ def bwd_mod(q, k, v, o, lse, do, visible=None, causal: bool | None = None, softc
     else:
         _check_like(dv, v, "dv")
     if workspace is None:
-        workspace = bwd_mod_workspace(B, H, Hkv, T, d, device=device)
+        workspace = bwd_mod_workspace(B, H, Hkv, T, d, device, *(() if visible is None else
+                                                                 (visible.window, visible.sinks)))
     else:
         _check_workspace(workspace, device)
     if rest is not None:
         _check_like(rest, q, "rest")
     _check_status(status, device)
+    if visible is not None and visible.window:
+        _call(device, "fa_bwd_window", q.data_ptr(), k.data_ptr(), v.data_ptr(), o.data_ptr(),
+              do.data_ptr(), lse.data_ptr(), _ptr(rest), dq.data_ptr(), dk.data_ptr(), dv.data_ptr(),
+              workspace.data_ptr(), workspace.numel() * workspace.element_size(),
+              visible.buffer.data_ptr(), visible.window, visible.sinks, softcap, _ptr(slopes),
+              B, H, Hkv, T, d, scale, _ptr(status), timeout_ns)
+        return dq, dk, dv
     _call(device, "fa_bwd_mod", q.data_ptr(), k.data_ptr(), v.data_ptr(),
           o.data_ptr(), do.data_ptr(), lse.data_ptr(), _ptr(rest), dq.data_ptr(), dk.data_ptr(),
           dv.data_ptr(), workspace.data_ptr(), workspace.numel() * workspace.element_size(),
@@ -263,19 +302,23 @@ def bwd_mod(q, k, v, o, lse, do, visible=None, causal: bool | None = None, softc
 
 # -------------------------------------------------------------- new tokens against a cache
 
-def fwd_tree_workspace(B: int, H: int, Hkv: int, Tq: int, Tmax: int, d: int, device=None):
+def fwd_tree_workspace(B: int, H: int, Hkv: int, Tq: int, Tmax: int, d: int, device=None,
+                       window: int = 0, sinks: int = 0):
     """A uint8 CUDA tensor large enough to serve as ``fwd_tree``'s workspace."""
+    _check_window(window, sinks, 0x7FFFFFFF)
     device = torch.device("cuda" if device is None else device)
     if device.index is None:
         device = torch.device("cuda", torch.cuda.current_device())
-    return torch.empty(_tree_bytes(B, H, Hkv, Tq, Tmax, d, device.index), dtype=_U8, device=device)
+    return torch.empty(_tree_bytes(B, H, Hkv, Tq, Tmax, d, window, sinks, device.index), dtype=_U8,
+                       device=device)
 
 
 @functools.lru_cache(maxsize=256)
-def _tree_bytes(B, H, Hkv, Tq, Tmax, d, index):
+def _tree_bytes(B, H, Hkv, Tq, Tmax, d, window, sinks, index):
     """fa_fwd_tree_workspace_size on device ``index``, a function of its arguments alone."""
     with torch.cuda.device(index):
-        n = fa_fwd_tree_workspace_size(B, H, Hkv, Tq, Tmax, d)
+        n = (fa_fwd_tree_window_workspace_size(B, H, Hkv, Tq, Tmax, d, window, sinks) if window
+             else fa_fwd_tree_workspace_size(B, H, Hkv, Tq, Tmax, d))
     if n == 0:
         raise FAError(FA_ERR_INVALID_ARG, "fa_fwd_tree_workspace_size")
     return n
@@ -283,7 +326,7 @@ def _tree_bytes(B, H, Hkv, Tq, Tmax, d, index):
 
 def fwd_tree(q, k_cache, v_cache, ctx_len, tree=None, depths=None, softcap: float = 0.0,
              slopes=None, scale: float | None = None, out=None, lse=None, workspace=None,
-             status=None, timeout_ns: int = 0):
+             status=None, timeout_ns: int = 0, window: int = 0, sinks: int = 0):
     """New tokens q [B, H, Tq, d] against caches [B, Hkv, Tmax, d] through fa_fwd_tree: sequence b
     holds ``ctx_len[b]`` tokens (int32 [B]; negative: inactive) and behind them, already written
     (``rope_append``), its Tq new ones.
@@ -291,9 +334,13 @@ def fwd_tree(q, k_cache, v_cache, ctx_len, tree=None, depths=None, softcap: floa
     A new token sees the whole context and, of the new tokens, those where ``tree`` (uint8 or bool
     [Tq, Tq] or [B, Tq, Tq], nonzero = row t sees token s) says so; without it a chain: itself and
     the ones before. ``softcap`` and ``slopes`` as for ``fwd_mod``, the bias measured between
-    positions ctx_len[b] + ``depths`` (int32 [Tq] or [B, Tq]; None: 0, 1, …). Returns (o, lse); a
-    token that sees nothing has o = 0 and lse = −inf. ``workspace``: see ``fwd_tree_workspace``.
+    positions ctx_len[b] + ``depths`` (int32 [Tq] or [B, Tq]; None: 0, 1, …). With ``window`` > 0 a
+    token sees, of these, the rows less than ``window`` positions behind its own and those at positions
+    below ``sinks``; the other rows of the cache are not read. Returns (o, lse); a token that sees
+    nothing has o = 0 and lse = −inf. ``workspace``: see ``fwd_tree_workspace``.
     """
+    if window or sinks:
+        _check_window(window, sinks, 0x7FFFFFFF)
     _check(q, "q")
     device = q.device
     _check_on(k_cache, device, "k_cache")
@@ -325,13 +372,20 @@ def fwd_tree(q, k_cache, v_cache, ctx_len, tree=None, depths=None, softcap: floa
     else:
         _check_fp32(lse, (B, H, Tq), device, "lse")
     if workspace is None:
-        need = _tree_bytes(B, H, Hkv, Tq, Tmax, d, device.index)
+        need = _tree_bytes(B, H, Hkv, Tq, Tmax, d, window, sinks, device.index)
         if need > 1:
             workspace = torch.empty(need, dtype=_U8, device=device)
     else:
         _check_workspace(workspace, device)
         need = workspace.numel() * workspace.element_size()
     _check_status(status, device)
+    if window:
+        _call(device, "fa_fwd_tree_window", q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(),
+              out.data_ptr(), lse.data_ptr(), ctx_len.data_ptr(), _ptr(tree),
+              tree is not None and tree.dim() == 3, _ptr(depths),
+              depths is not None and depths.dim() == 2, window, sinks, softcap, _ptr(slopes), B, H, Hkv,
+              Tq, Tmax, d, scale, _ptr(workspace), need, _ptr(status), timeout_ns)
+        return out, lse
     _call(device, "fa_fwd_tree", q.data_ptr(), k_cache.data_ptr(),
           v_cache.data_ptr(), out.data_ptr(), lse.data_ptr(), ctx_len.data_ptr(), _ptr(tree),
           tree is not None and tree.dim() == 3, _ptr(depths),

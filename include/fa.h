@@ -373,6 +373,38 @@ int fa_bwd_mod(const void* q, const void* k, const void* v, const void* o, const
 
 /*
  * ---------------------------------------------------------------------------------------
+ * A sliding window and sinks. Causal attention in which a token sees, of its document, the last
+ * `window` tokens (itself among them) and the first `sinks`:
+ *
+ *   key j is visible to query i  iff  same document, j ≤ i, and (i − j < window or j < start + sinks)
+ *
+ * start being the document's first token. Everything else (caps, biases, shared key heads, documents,
+ * padding, rows, outputs) is as for fa_visible, fa_fwd_mod and fa_bwd_mod. Work grows with T·window:
+ * only the K tiles with visible keys are walked, and gradients of the sinks, which every later token of
+ * the document sees, are summed in pieces (in a fixed order: dK and dV are the same bits every time).
+ *
+ *   window : ≥ 1 (more than T: no limit)
+ *   sinks  : 0 … 1024
+ *   visible : DEVICE buffer of fa_visible_window_size(B, T, window, sinks) bytes (0: unsupported sizes),
+ *             256-byte aligned, filled by fa_visible_window for the same B, T, window and sinks
+ *   workspace : fa_bwd_window_workspace_size(...) bytes (0: unsupported sizes), as for fa_bwd_mod
+ * ---------------------------------------------------------------------------------------
+ */
+size_t fa_visible_window_size(int B, int T, int window, int sinks);
+int fa_visible_window(const int* doc_ids, int window, int sinks, void* visible, size_t visible_bytes, int B,
+                      int T, void* stream);
+int fa_fwd_window(const void* q, const void* k, const void* v, void* o, float* lse, void* rest,
+                  const void* visible, int window, int sinks, float softcap, const float* slopes, int B, int H,
+                  int Hkv, int T, int d, float scale, int* status, unsigned long long timeout_ns, void* stream);
+size_t fa_bwd_window_workspace_size(int B, int H, int Hkv, int T, int d, int window, int sinks);
+int fa_bwd_window(const void* q, const void* k, const void* v, const void* o, const void* dout,
+                  const float* lse, const void* rest, void* dq, void* dk, void* dv, void* workspace,
+                  size_t workspace_bytes, const void* visible, int window, int sinks, float softcap,
+                  const float* slopes, int B, int H, int Hkv, int T, int d, float scale, int* status,
+                  unsigned long long timeout_ns, void* stream);
+
+/*
+ * ---------------------------------------------------------------------------------------
  * Rotary positions.
  *
  * The first rot_dim dimensions of a head are pairs, dimensions (i, i + rot_dim/2), or (2i,
@@ -501,6 +533,21 @@ int fa_fwd_tree(const void* q, const void* k_cache, const void* v_cache, void* o
                 int depths_per_batch, float softcap, const float* slopes, int B, int H, int Hkv, int Tq,
                 int Tmax, int d, float scale, void* workspace, size_t workspace_bytes, int* status,
                 unsigned long long timeout_ns, void* stream);
+
+/*
+ * fa_fwd_tree_window — fa_fwd_tree with a sliding window and sinks (window ≥ 1, sinks ≥ 0). Token t, at
+ * position ctx_len[b] + depths[t] (depths below 0 count as 0 here), sees of what it sees otherwise the
+ * rows whose position is less than `window` behind its own, and those whose position is below `sinks`;
+ * a context row's position is its index. Only the rows that some token may see are read: rows between
+ * the sinks and the first token's window may hold anything, NaN included, as those behind the last new
+ * token. workspace: fa_fwd_tree_window_workspace_size(...) bytes, as for fa_fwd_tree.
+ */
+size_t fa_fwd_tree_window_workspace_size(int B, int H, int Hkv, int Tq, int Tmax, int d, int window, int sinks);
+int fa_fwd_tree_window(const void* q, const void* k_cache, const void* v_cache, void* o, float* lse,
+                       const int* ctx_len, const unsigned char* tree, int tree_per_batch, const int* depths,
+                       int depths_per_batch, int window, int sinks, float softcap, const float* slopes, int B,
+                       int H, int Hkv, int Tq, int Tmax, int d, float scale, void* workspace,
+                       size_t workspace_bytes, int* status, unsigned long long timeout_ns, void* stream);
 
 /* Static text for a status code (never NULL). */
 const char* fa_strerror(int status);
