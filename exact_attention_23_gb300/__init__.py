@@ -11,7 +11,8 @@ documents, prefixes, sliding windows and sinks through ``visible``, key heads sh
 and its gradients;
 ``rope`` and ``rope_append`` turn queries and keys by their positions (``norm_rope`` and
 ``norm_rope_append`` after a norm of each head's row, ``norm_rope_bwd`` the way back), and ``fwd_tree`` attends
-new tokens (one, a chain, a tree of drafts) to a cache of ragged contexts.
+new tokens (one, a chain, a tree of drafts) to a cache of ragged contexts, ``fwd_tree4`` to one that
+is held in 4 bits (``cache4``, ``append4``, ``read4``).
 The work is done by the CUDA kernels of ``libfa.so`` through its C ABI (include/fa.h);
 this module only allocates outputs and workspace with PyTorch and passes pointers and the
 current stream.
@@ -33,6 +34,7 @@ from ._binding import (  # noqa: F401
     FA_FLAG_CTA_PAIR,
     FA_OK,
     FAError,
+    fa_append4,
     fa_bwd,
     fa_bwd_ex,
     fa_bwd_mod,
@@ -50,6 +52,8 @@ from ._binding import (  # noqa: F401
     fa_fwd_kv_workspace_size,
     fa_fwd_mod,
     fa_fwd_tree,
+    fa_fwd_tree4,
+    fa_fwd_tree4_workspace_size,
     fa_fwd_tree_window,
     fa_fwd_tree_window_workspace_size,
     fa_fwd_tree_workspace_size,
@@ -58,6 +62,7 @@ from ._binding import (  # noqa: F401
     fa_norm_rope_append,
     fa_norm_rope_bwd,
     fa_norm_rope_bwd_workspace_size,
+    fa_read4,
     fa_rope,
     fa_rope_append,
     fa_visible,
@@ -330,7 +335,8 @@ def q_tiles(T: int, rows: int = 128) -> int:
 _OPS = ("Visible", "visible", "fwd_mod", "bwd_mod_workspace", "bwd_mod",
         "rope_inv_freq", "rope", "rope_append",
         "norm_rope", "norm_rope_bwd_workspace", "norm_rope_bwd", "norm_rope_append",
-        "fwd_tree_workspace", "fwd_tree")
+        "fwd_tree_workspace", "fwd_tree",
+        "Cache4", "cache4", "append4", "read4", "fwd_tree4_workspace", "fwd_tree4")
 
 
 def __getattr__(name):

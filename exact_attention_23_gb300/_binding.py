@@ -33,7 +33,8 @@ EXPORTS = ("fa_fwd", "fa_fwd_ex", "fa_fwd_fp8", "fa_fwd_host_workspace_size", "f
            "fa_rope_append", "fa_norm_rope", "fa_norm_rope_append", "fa_norm_rope_bwd_workspace_size",
            "fa_norm_rope_bwd", "fa_fwd_tree_workspace_size", "fa_fwd_tree", "fa_visible_window_size", "fa_visible_window",
            "fa_fwd_window", "fa_bwd_window_workspace_size", "fa_bwd_window",
-           "fa_fwd_tree_window_workspace_size", "fa_fwd_tree_window", "fa_strerror", "fa_version")
+           "fa_fwd_tree_window_workspace_size", "fa_fwd_tree_window", "fa_append4", "fa_read4",
+           "fa_fwd_tree4_workspace_size", "fa_fwd_tree4", "fa_strerror", "fa_version")
 
 _lock = threading.Lock()
 _lib = None
@@ -130,6 +131,14 @@ def lib() -> ctypes.CDLL:
             L.fa_fwd_tree_window.argtypes = ([vp] * 7 + [i, vp, i, i, i, f, vp] + [i] * 6
                                              + [f, vp, sz, vp, ull, vp])
             L.fa_fwd_tree_window.restype = i
+            L.fa_append4.argtypes = src + src + [vp] * 5 + [i] * 5 + [vp]
+            L.fa_append4.restype = i
+            L.fa_read4.argtypes = [vp] * 7 + [i] * 5 + [vp]
+            L.fa_read4.restype = i
+            L.fa_fwd_tree4_workspace_size.argtypes = [i] * 8
+            L.fa_fwd_tree4_workspace_size.restype = sz
+            L.fa_fwd_tree4.argtypes = [vp] * 9 + [i, vp, i, i, i, f, vp] + [i] * 6 + [f, vp, sz, vp, ull, vp]
+            L.fa_fwd_tree4.restype = i
             L.fa_strerror.argtypes = [i]
             L.fa_strerror.restype = ctypes.c_char_p
             L.fa_version.argtypes = []
@@ -336,3 +345,29 @@ def fa_fwd_tree_window(q, k_cache, v_cache, o, lse, ctx_len, tree, tree_per_batc
                                     depths, int(depths_per_batch), window, sinks, float(softcap), slopes,
                                     B, H, Hkv, Tq, Tmax, d, float(scale), workspace, int(workspace_bytes),
                                     status, int(timeout_ns), stream)
+
+
+def fa_append4(k, k_strides, v, v_strides, k_codes, k_scales, v_codes, v_scales, ctx_len, B, Hkv, Tq,
+               Tmax, d, stream) -> int:
+    """Strides as for fa_rope."""
+    return lib().fa_append4(k, *k_strides, v, *v_strides, k_codes, k_scales, v_codes, v_scales, ctx_len,
+                            B, Hkv, Tq, Tmax, d, stream)
+
+
+def fa_read4(k_codes, k_scales, v_codes, v_scales, start, k_out, v_out, B, Hkv, n, Tmax, d,
+             stream) -> int:
+    return lib().fa_read4(k_codes, k_scales, v_codes, v_scales, start, k_out, v_out, B, Hkv, n, Tmax, d,
+                          stream)
+
+
+def fa_fwd_tree4_workspace_size(B, H, Hkv, Tq, Tmax, d, window, sinks) -> int:
+    return int(lib().fa_fwd_tree4_workspace_size(B, H, Hkv, Tq, Tmax, d, window, sinks))
+
+
+def fa_fwd_tree4(q, k_codes, k_scales, v_codes, v_scales, o, lse, ctx_len, tree, tree_per_batch, depths,
+                 depths_per_batch, window, sinks, softcap, slopes, B, H, Hkv, Tq, Tmax, d, scale,
+                 workspace, workspace_bytes, status, timeout_ns, stream) -> int:
+    return lib().fa_fwd_tree4(q, k_codes, k_scales, v_codes, v_scales, o, lse, ctx_len, tree,
+                              int(tree_per_batch), depths, int(depths_per_batch), window, sinks,
+                              float(softcap), slopes, B, H, Hkv, Tq, Tmax, d, float(scale), workspace,
+                              int(workspace_bytes), status, int(timeout_ns), stream)

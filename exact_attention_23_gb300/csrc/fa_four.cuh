@@ -1,0 +1,90 @@
+// Rows held in 4 bits (include/fa.h: fa_append4). A row's d values are groups of 32; a group is a scale s
+// (its largest magnitude over 7, rounded up to five significant bits, as bf16) times whole numbers −7 … 7,
+// kept plus 8 in four bits. Seven times a five-bit number has eight bits: every value is a bf16 number,
+// so codes become tensor-core operands without a rounding.
+//
+// The order of a row's codes makes a thread's operand fragments out of whole words, eight codes each:
+//   keys    word c·(d/32) + w: dimensions 32w + 4c + (0, 2, 16, 18, 1, 3, 17, 19). Thread c of a quad reads
+//           its d/32 words in one piece; bits 4i and 16 + 4i of a word are the pairs of the B fragments
+//           of two products of 16 dimensions, whose order within the 16 is (4c, 4c + 1 | 4c + 2, 4c + 3)
+//           for the thread: any order does, as long as Q's fragments have the same.
+//   values  word 8h + n: dimensions 64h + n + 8·(0 … 7): column n of eight 16 × 8 products.
+#pragma once
+
+#include <cuda_bf16.h>
+#include <stdint.h>
+
+#include "sm103.cuh"
+
+namespace fa {
+
+// From codes to values: with a code in bits 3 … 6 of a half word, under the exponent of 16, the half is the bf16
+// number 16 + code; (16 + code)·s − 24·s = (code − 8)·s in one fused operation, exact since 24·s has
+// seven bits. (Not under the exponent of 128, where no shift would be needed: 136·s has ten.)
+struct FourScale {
+  __nv_bfloat162 s, off;
+};
+__device__ __forceinline__ __nv_bfloat162 as_bf162(uint32_t x) { return *reinterpret_cast<__nv_bfloat162*>(&x); }
+__device__ __forceinline__ FourScale four_scale(uint32_t pair) {
+  FourScale f;
+  f.s = as_bf162(pair);
+  f.off = __hmul2(f.s, as_bf162(0xC1C0C1C0u));  // −24
+  return f;
+}
+// The pair of codes at bits 4i and 16 + 4i of a word, as bf16 values.
+template <int I>
+__device__ __forceinline__ uint32_t four_pair(uint32_t word, const FourScale& f) {
+  const uint32_t at = I == 0 ? word << 3 : word >> (I == 0 ? 0 : 4 * I - 3);
+  const __nv_bfloat162 x = __hfma2(as_bf162((at & 0x00780078u) | 0x41804180u), f.s, f.off);
+  return *reinterpret_cast<const uint32_t*>(&x);
+}
+
+// A group's scale from the bits of its largest magnitude. Below 2⁻¹⁰⁰: zeros. From 2¹²⁵ on (infinities and NaN
+// among them): a NaN, which the whole group then stands for.
+__device__ __forceinline__ float four_scale_of(uint32_t top_bits) {
+  if (top_bits >= 0x7E000000u) return __uint_as_float(0x7FC00000u);
+  if (top_bits < 0x0D800000u) return 0.f;
+  const uint32_t q = __float_as_uint(__fdiv_rn(__uint_as_float(top_bits), 7.0f));
+  return __uint_as_float((q + 0x7FFFFu) & ~0x7FFFFu);
+}
+// The nearest whole number to x / s, ties to even, plus 8. x·(1/s) can be off by its roundings where x / s lies half-way
+// between two numbers, and nowhere else (an eight-bit over a five-bit number comes no nearer to
+// one than 2⁻¹¹); there the remainder x − n·s, which is exact, is half of s.
+__device__ __forceinline__ uint32_t four_code(float x, float s, float inv) {
+  float n = rintf(x * inv);
+  const float rem = fmaf(-n, s, x);
+  const int k = static_cast<int>(n);
+  if (fabsf(rem) * 2.0f == s && (k & 1)) return static_cast<uint32_t>(k + (rem > 0.f ? 9 : 7));
+  return static_cast<uint32_t>(k + 8);
+}
+
+// Eight lanes' words as an 8 × 8 matrix of codes (lane x, nibble n), transposed.
+__device__ __forceinline__ uint32_t four_transpose(uint32_t w, int x) {
+  uint32_t y = __shfl_xor_sync(0xffffffffu, w, 4);
+  w = (x & 4) ? (w & 0xFFFF0000u) | (y >> 16) : (w & 0x0000FFFFu) | (y << 16);
+  y = __shfl_xor_sync(0xffffffffu, w, 2);
+  w = (x & 2) ? (w & 0xFF00FF00u) | ((y >> 8) & 0x00FF00FFu) : (w & 0x00FF00FFu) | ((y << 8) & 0xFF00FF00u);
+  y = __shfl_xor_sync(0xffffffffu, w, 1);
+  return (x & 1) ? (w & 0xF0F0F0F0u) | ((y >> 4) & 0x0F0F0F0Fu) : (w & 0x0F0F0F0Fu) | ((y << 4) & 0xF0F0F0F0u);
+}
+
+// Between eight dimensions in a row (lane x of eight holds 8x … 8x + 7) and the keys' words: lanes x and x ^ 2
+// exchange halves, so that lane x holds, of its group of 32, dimensions 4c + (0 … 3) and 16 + 4c +
+// (0 … 3), c = four_key_word(x); then nibbles a0 a1 a2 a3 b0 b1 b2 b3 become a0 a2 b0 b2 a1 a3 b1 b3.
+__device__ __forceinline__ int four_key_word(int x) { return 2 * (x & 1) + ((x >> 1) & 1); }
+__device__ __forceinline__ uint32_t four_halves(uint32_t w, int x) {
+  const uint32_t y = __shfl_xor_sync(0xffffffffu, w, 2);
+  return (x & 2) ? (w & 0xFFFF0000u) | (y >> 16) : (w & 0x0000FFFFu) | (y << 16);
+}
+__device__ __forceinline__ uint32_t four_to_key(uint32_t w, int x) {
+  w = four_halves(w, x);
+  return (w & 0x0000000Fu) | ((w >> 4) & 0x000000F0u) | ((w >> 8) & 0x00000F00u) | ((w >> 12) & 0x0000F000u) |
+         ((w << 12) & 0x000F0000u) | ((w << 8) & 0x00F00000u) | ((w << 4) & 0x0F000000u) | (w & 0xF0000000u);
+}
+__device__ __forceinline__ uint32_t four_from_key(uint32_t w, int x) {
+  w = (w & 0x0000000Fu) | ((w & 0x000000F0u) << 4) | ((w & 0x00000F00u) << 8) | ((w & 0x0000F000u) << 12) |
+      ((w & 0x000F0000u) >> 12) | ((w & 0x00F00000u) >> 8) | ((w & 0x0F000000u) >> 4) | (w & 0xF0000000u);
+  return four_halves(w, x);
+}
+
+}  // namespace fa

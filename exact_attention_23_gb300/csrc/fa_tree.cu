@@ -45,6 +45,7 @@ constexpr int kMinPer = 2, kMinPerWide = 1;
 // Not beyond the chunks measured: stretches share out unequal contexts, a CTA an entry does not.
 int join_chunks(bool wide_rows, int d) { return wide_rows ? (d == 64 ? 5 : 4) : d == 64 ? 7 : 5; }
 constexpr int kSoloChunks = 24, kSoloChunksWide = 12;
+constexpr int kJoinChunksFour = 4, kSoloChunksFour = 12;
 
 struct TreeSizes {
   int R, rows_log2, row_blocks, chunk_log2, min_per;
@@ -53,31 +54,43 @@ struct TreeSizes {
   size_t lse_off, parts_off, bytes;
 };
 
-// (window 0: none)
-bool tree_sizes(int B, int H, int Hkv, int Tq, int Tmax, int d, int window, int sinks, int sms, TreeSizes* z) {
+// What the new tokens go against: a window (0: none) with sinks, a cache in 4 bits.
+struct TreeForm {
+  int window, sinks;
+  bool four;
+};
+
+// CTAs of the streaming kernel an SM holds.
+int tree_ctas(int d, bool four) {
+  return d == 64 ? (four ? TreeCfg<64, true>::kCtasPerSm : TreeCfg<64>::kCtasPerSm)
+                 : (four ? TreeCfg<128, true>::kCtasPerSm : TreeCfg<128>::kCtasPerSm);
+}
+
+bool tree_sizes(int B, int H, int Hkv, int Tq, int Tmax, int d, const TreeForm& form, int sms, TreeSizes* z) {
   if (B <= 0 || H <= 0 || Hkv <= 0 || Tq <= 0 || Tmax <= 0 || H % Hkv != 0 || (d != 64 && d != 128))
     return false;
   const long long R = static_cast<long long>(H / Hkv) * Tq, BHkv = static_cast<long long>(B) * Hkv;
   if (static_cast<long long>(B) * H > INT32_MAX || R > (1 << 24) || Tmax > (1 << 30)) return false;
   z->R = static_cast<int>(R);
-  z->rows_log2 = block_rows_log2(z->R);
+  // (4 bits: blocks of at most 32 rows, the tensor-core kernel's operands being bf16 in shared memory)
+  const bool is_wide = wide(z->R) && !form.four;
+  z->rows_log2 = form.four ? std::min(block_rows_log2(z->R), 5) : block_rows_log2(z->R);
   z->row_blocks = (z->R + (1 << z->rows_log2) - 1) >> z->rows_log2;
-  z->chunk_log2 = wide(z->R) ? 7 : 6;
-  z->min_per = wide(z->R) ? kMinPerWide : kMinPer;
+  z->chunk_log2 = is_wide || form.four ? 7 : 6;
+  z->min_per = is_wide || form.four ? kMinPerWide : kMinPer;
   z->entries = BHkv * z->row_blocks;
   if (z->entries > (1 << 28) || BHkv * R > (1LL << 40) || BHkv > (1LL << 60) / d / Tmax) return false;
   auto chunks_of = [&](long long keys) { return (keys + (1 << z->chunk_log2) - 1) >> z->chunk_log2; };
   long long chunks = chunks_of(Tmax);
-  if (window > 0)  // those with sinks, and those that a window and the new tokens can reach into
-    chunks = std::min(chunks, chunks_of(std::min(sinks, Tmax)) + chunks_of(static_cast<long long>(window) - 1 + Tq) + 1);
+  if (form.window > 0)  // those with sinks, and those that a window and the new tokens can reach into
+    chunks = std::min(chunks, chunks_of(std::min(form.sinks, Tmax)) + chunks_of(static_cast<long long>(form.window) - 1 + Tq) + 1);
   if (z->entries * chunks > INT32_MAX - 128) return false;  // (the kernels number them with an int)
   if (z->entries << (z->rows_log2 - 3) > INT32_MAX) return false;
   const long long most = (z->entries * chunks + z->min_per - 1) / z->min_per;
-  const long long fit = static_cast<long long>(sms) *
-                        (wide(z->R) ? 1 : d == 64 ? TreeCfg<64>::kCtasPerSm : TreeCfg<128>::kCtasPerSm);
+  const long long fit = static_cast<long long>(sms) * (is_wide ? 1 : tree_ctas(d, form.four));
   const long long per = std::max<long long>(z->min_per, (z->entries * chunks + fit - 1) / fit);  // a stretch's
-  z->solo = z->entries <= fit && chunks <= per + join_chunks(wide(z->R), d) &&
-            chunks <= (wide(z->R) ? kSoloChunksWide : kSoloChunks);
+  z->solo = z->entries <= fit && chunks <= per + (form.four ? kJoinChunksFour : join_chunks(is_wide, d)) &&
+            chunks <= (form.four ? kSoloChunksFour : is_wide ? kSoloChunksWide : kSoloChunks);
   if (z->solo) {
     z->grid = z->entries;
     z->slots = 0;
@@ -100,56 +113,63 @@ bool tree_sizes(int B, int H, int Hkv, int Tq, int Tmax, int d, int window, int 
 
 namespace {
 
-size_t tree_workspace(int B, int H, int Hkv, int Tq, int Tmax, int d, int window, int sinks) {
+size_t tree_workspace(int B, int H, int Hkv, int Tq, int Tmax, int d, const fa::TreeForm& form) {
   fa::TreeSizes z;
-  if (!fa::tree_sizes(B, H, Hkv, Tq, Tmax, d, window, sinks, 1, &z)) return 0;
+  if (!fa::tree_sizes(B, H, Hkv, Tq, Tmax, d, form, 1, &z)) return 0;
   int dev = -1, sms = 0;
   if (check_device(&dev, &sms) != FA_OK) return 0;
-  return fa::tree_sizes(B, H, Hkv, Tq, Tmax, d, window, sinks, sms, &z) ? z.bytes : 0;
+  return fa::tree_sizes(B, H, Hkv, Tq, Tmax, d, form, sms, &z) ? z.bytes : 0;
 }
 
 bool tree_window_ok(int window, int sinks) { return window >= 1 && sinks >= 0; }
+// (a cache in 4 bits may go without a window)
+bool four_ok(int Tmax, int window, int sinks) {
+  return Tmax % 8 == 0 && (tree_window_ok(window, sinks) || (window == 0 && sinks == 0));
+}
 
-// fa_fwd_tree, and fa_fwd_tree_window (window > 0).
-int fwd_tree(const void* q, const void* k_cache, const void* v_cache, void* o, float* lse, const int* ctx_len,
-             const unsigned char* tree, int tree_per_batch, const int* depths, int depths_per_batch, int window,
-             int sinks, float softcap, const float* slopes, int B, int H, int Hkv, int Tq, int Tmax, int d,
-             float scale, void* workspace, size_t workspace_bytes, int* status, unsigned long long timeout_ns,
-             void* stream) {
+// fa_fwd_tree, fa_fwd_tree_window and fa_fwd_tree4 (whose caches are codes, with scales).
+int fwd_tree(const void* q, const void* k_cache, const void* v_cache, const void* k_scales, const void* v_scales,
+             void* o, float* lse, const int* ctx_len, const unsigned char* tree, int tree_per_batch,
+             const int* depths, int depths_per_batch, const fa::TreeForm& form, float softcap, const float* slopes,
+             int B, int H, int Hkv, int Tq, int Tmax, int d, float scale, void* workspace, size_t workspace_bytes,
+             int* status, unsigned long long timeout_ns, void* stream) {
   if (!q || !k_cache || !v_cache || !o || !lse || !ctx_len) return FA_ERR_INVALID_ARG;
+  if (form.four && (!k_scales || !v_scales)) return FA_ERR_INVALID_ARG;
   fa::TreeSizes z;
   fa::CapFactors cap;
-  if (!fa::tree_sizes(B, H, Hkv, Tq, Tmax, d, window, sinks, 1, &z) || !scale_ok(scale) || !cap_factors(scale, softcap, &cap))
+  if (!fa::tree_sizes(B, H, Hkv, Tq, Tmax, d, form, 1, &z) || !scale_ok(scale) || !cap_factors(scale, softcap, &cap))
     return FA_ERR_INVALID_ARG;
   const uintptr_t words = reinterpret_cast<uintptr_t>(ctx_len) | reinterpret_cast<uintptr_t>(depths) |
                           reinterpret_cast<uintptr_t>(slopes);
-  if (!aligned16(q) || !aligned16(k_cache) || !aligned16(v_cache) || !aligned16(o) || !aligned16(lse) ||
+  if (!aligned16(q) || !aligned16(k_cache) || !aligned16(v_cache) || !aligned16(k_scales) || !aligned16(v_scales) ||
+      !aligned16(o) || !aligned16(lse) ||
       (reinterpret_cast<uintptr_t>(workspace) & 255u) || (words & 3u))
     return FA_ERR_MISALIGNED;
   int dev = -1, sms = 0;
-  const size_t qb = static_cast<size_t>(B) * H * Tq * d * 2, cb = static_cast<size_t>(B) * Hkv * Tmax * d * 2;
+  const size_t qb = static_cast<size_t>(B) * H * Tq * d * 2, cb = static_cast<size_t>(B) * Hkv * Tmax * (form.four ? d / 2 : d * 2);
+  const size_t sb = static_cast<size_t>(B) * Hkv * Tmax * (d / 16);
   const size_t lb = static_cast<size_t>(B) * H * Tq * 4;
   const size_t tb = static_cast<size_t>(tree_per_batch ? B : 1) * Tq * Tq;
   const size_t db = static_cast<size_t>(depths_per_batch ? B : 1) * Tq * 4;
   const int dst = check_device(&dev, &sms);
-  if (dst == FA_OK && !fa::tree_sizes(B, H, Hkv, Tq, Tmax, d, window, sinks, sms, &z)) return FA_ERR_INVALID_ARG;
+  if (dst == FA_OK && !fa::tree_sizes(B, H, Hkv, Tq, Tmax, d, form, sms, &z)) return FA_ERR_INVALID_ARG;
   if (!z.solo && (!workspace || workspace_bytes < z.bytes)) return FA_ERR_INVALID_ARG;
-  const void* ins[7] = {q, k_cache, v_cache, ctx_len, tree, depths, slopes};
-  const size_t in_bytes[7] = {qb, cb, cb, static_cast<size_t>(B) * 4, tb, db, static_cast<size_t>(H) * 4};
+  const void* ins[9] = {q, k_cache, v_cache, ctx_len, tree, depths, slopes, k_scales, v_scales};
+  const size_t in_bytes[9] = {qb, cb, cb, static_cast<size_t>(B) * 4, tb, db, static_cast<size_t>(H) * 4, sb, sb};
   const void* outs[3] = {o, lse, workspace};
   const size_t out_bytes[3] = {qb, lb, z.bytes};
   const int n_outs = z.solo ? 2 : 3;
   for (int x = 0; x < n_outs; ++x) {
-    for (int y = 0; y < 7; ++y)
+    for (int y = 0; y < 9; ++y)
       if (ins[y] && overlaps(outs[x], out_bytes[x], ins[y], in_bytes[y])) return FA_ERR_INVALID_ARG;
     for (int y = x + 1; y < n_outs; ++y)
       if (overlaps(outs[x], out_bytes[x], outs[y], out_bytes[y])) return FA_ERR_INVALID_ARG;
   }
   if (dst != FA_OK) return dst;
-  EncodeTiledFn enc = encode_fn();
-  if (!enc) return FA_ERR_LAUNCH;
+  EncodeTiledFn enc = form.four ? nullptr : encode_fn();
+  if (!enc && !form.four) return FA_ERR_LAUNCH;
   uint8_t* ws = static_cast<uint8_t*>(workspace);
-  fa::TreeLaunch a;
+  fa::TreeLaunch a{};
   a.p = fa::TreeParams{};
   a.p.q = static_cast<const __nv_bfloat16*>(q);
   a.p.o = static_cast<__nv_bfloat16*>(o);
@@ -162,7 +182,8 @@ int fwd_tree(const void* q, const void* k_cache, const void* v_cache, void* o, f
   a.p.status = status;
   a.p.timeout_ns = timeout_ns ? timeout_ns : 2000000000ull;
   a.p.list = fa::TreeList{ctx_len, B, Hkv, Tq, Tmax, z.row_blocks, z.min_per, z.chunk_log2, z.solo ? 1 : 0,
-                          z.solo ? nullptr : reinterpret_cast<int2*>(ws + z.parts_off), window, sinks};
+                          z.solo ? nullptr : reinterpret_cast<int2*>(ws + z.parts_off),
+                          form.four && form.window == 0 ? INT32_MAX : form.window, form.sinks};
   a.p.mask = fa::TreeMask{tree, depths, fa::FastDiv::make(static_cast<uint32_t>(Tq)), tree_per_batch != 0,
                           depths_per_batch != 0};
   a.p.cap = cap;
@@ -172,10 +193,18 @@ int fwd_tree(const void* q, const void* k_cache, const void* v_cache, void* o, f
   a.stream = static_cast<cudaStream_t>(stream);
   const int mod = mod_bits(softcap, slopes), BHkv = B * Hkv;
   const int box = 1 << z.chunk_log2;
-  if (!encode_map(enc, &a.tm_k, k_cache, Tmax, d, BHkv, box) || !encode_map(enc, &a.tm_v, v_cache, Tmax, d, BHkv, box))
+  if (form.four) {
+    a.p.k4 = static_cast<const uint8_t*>(k_cache);
+    a.p.v4 = static_cast<const uint8_t*>(v_cache);
+    a.p.ks = static_cast<const __nv_bfloat16*>(k_scales);
+    a.p.vs = static_cast<const __nv_bfloat16*>(v_scales);
+  } else if (!encode_map(enc, &a.tm_k, k_cache, Tmax, d, BHkv, box) || !encode_map(enc, &a.tm_v, v_cache, Tmax, d, BHkv, box)) {
     return FA_ERR_INVALID_ARG;
+  }
   cudaError_t e;
-  if (fa::wide(z.R)) {
+  if (form.four) {
+    e = (d == 64) ? fa::launch_tree_four_d64(a, 1 << z.rows_log2, mod) : fa::launch_tree_four_d128(a, 1 << z.rows_log2, mod);
+  } else if (fa::wide(z.R)) {
     fa::FwdLaunch f;
     f.p = fa::FwdParams{};
     f.tm_k = a.tm_k;
@@ -214,9 +243,9 @@ int fwd_tree(const void* q, const void* k_cache, const void* v_cache, void* o, f
       f.p.s_negate = fa::kIdescNegateA;
       cap_factors(-scale, softcap, &f.p.mod.cap);
     }
-    if (window > 0) e = (d == 64) ? fa::launch_fwd_tree_window_d64(f, fm) : fa::launch_fwd_tree_window_d128(f, fm);
+    if (form.window > 0) e = (d == 64) ? fa::launch_fwd_tree_window_d64(f, fm) : fa::launch_fwd_tree_window_d128(f, fm);
     else e = (d == 64) ? fa::launch_fwd_tree_d64(f, fm) : fa::launch_fwd_tree_d128(f, fm);
-  } else if (window > 0) {
+  } else if (form.window > 0) {
     e = (d == 64) ? fa::launch_tree_window_d64(a, 1 << z.rows_log2, mod) : fa::launch_tree_window_d128(a, 1 << z.rows_log2, mod);
   } else {
     e = (d == 64) ? fa::launch_tree_rows<64, 0>(a, 1 << z.rows_log2, mod) : fa::launch_tree_rows<128, 0>(a, 1 << z.rows_log2, mod);
@@ -236,7 +265,7 @@ int fwd_tree(const void* q, const void* k_cache, const void* v_cache, void* o, f
 extern "C" {
 
 size_t fa_fwd_tree_workspace_size(int B, int H, int Hkv, int Tq, int Tmax, int d) {
-  return tree_workspace(B, H, Hkv, Tq, Tmax, d, 0, 0);
+  return tree_workspace(B, H, Hkv, Tq, Tmax, d, {0, 0, false});
 }
 
 int fa_fwd_tree(const void* q, const void* k_cache, const void* v_cache, void* o, float* lse,
@@ -244,12 +273,12 @@ int fa_fwd_tree(const void* q, const void* k_cache, const void* v_cache, void* o
                 int depths_per_batch, float softcap, const float* slopes, int B, int H, int Hkv, int Tq,
                 int Tmax, int d, float scale, void* workspace, size_t workspace_bytes, int* status,
                 unsigned long long timeout_ns, void* stream) {
-  return fwd_tree(q, k_cache, v_cache, o, lse, ctx_len, tree, tree_per_batch, depths, depths_per_batch, 0, 0, softcap,
-                  slopes, B, H, Hkv, Tq, Tmax, d, scale, workspace, workspace_bytes, status, timeout_ns, stream);
+  return fwd_tree(q, k_cache, v_cache, nullptr, nullptr, o, lse, ctx_len, tree, tree_per_batch, depths, depths_per_batch,
+                  {0, 0, false}, softcap, slopes, B, H, Hkv, Tq, Tmax, d, scale, workspace, workspace_bytes, status, timeout_ns, stream);
 }
 
 size_t fa_fwd_tree_window_workspace_size(int B, int H, int Hkv, int Tq, int Tmax, int d, int window, int sinks) {
-  return tree_window_ok(window, sinks) ? tree_workspace(B, H, Hkv, Tq, Tmax, d, window, sinks) : 0;
+  return tree_window_ok(window, sinks) ? tree_workspace(B, H, Hkv, Tq, Tmax, d, {window, sinks, false}) : 0;
 }
 
 int fa_fwd_tree_window(const void* q, const void* k_cache, const void* v_cache, void* o, float* lse,
@@ -258,8 +287,23 @@ int fa_fwd_tree_window(const void* q, const void* k_cache, const void* v_cache, 
                        int Hkv, int Tq, int Tmax, int d, float scale, void* workspace, size_t workspace_bytes,
                        int* status, unsigned long long timeout_ns, void* stream) {
   if (!tree_window_ok(window, sinks)) return FA_ERR_INVALID_ARG;
-  return fwd_tree(q, k_cache, v_cache, o, lse, ctx_len, tree, tree_per_batch, depths, depths_per_batch, window, sinks,
-                  softcap, slopes, B, H, Hkv, Tq, Tmax, d, scale, workspace, workspace_bytes, status, timeout_ns, stream);
+  return fwd_tree(q, k_cache, v_cache, nullptr, nullptr, o, lse, ctx_len, tree, tree_per_batch, depths, depths_per_batch,
+                  {window, sinks, false}, softcap, slopes, B, H, Hkv, Tq, Tmax, d, scale, workspace, workspace_bytes, status, timeout_ns, stream);
+}
+
+size_t fa_fwd_tree4_workspace_size(int B, int H, int Hkv, int Tq, int Tmax, int d, int window, int sinks) {
+  return four_ok(Tmax, window, sinks) ? tree_workspace(B, H, Hkv, Tq, Tmax, d, {window, sinks, true}) : 0;
+}
+
+int fa_fwd_tree4(const void* q, const void* k_codes, const void* k_scales, const void* v_codes, const void* v_scales,
+                 void* o, float* lse, const int* ctx_len, const unsigned char* tree, int tree_per_batch,
+                 const int* depths, int depths_per_batch, int window, int sinks, float softcap, const float* slopes,
+                 int B, int H, int Hkv, int Tq, int Tmax, int d, float scale, void* workspace, size_t workspace_bytes,
+                 int* status, unsigned long long timeout_ns, void* stream) {
+  if (!four_ok(Tmax, window, sinks)) return FA_ERR_INVALID_ARG;
+  return fwd_tree(q, k_codes, v_codes, k_scales, v_scales, o, lse, ctx_len, tree, tree_per_batch, depths, depths_per_batch,
+                  {window, sinks, true}, softcap, slopes, B, H, Hkv, Tq, Tmax, d, scale, workspace, workspace_bytes, status,
+                  timeout_ns, stream);
 }
 
 }  // extern "C"

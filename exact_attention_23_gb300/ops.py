@@ -19,6 +19,7 @@ from ._binding import (
     FAError,
     fa_bwd_mod_workspace_size,
     fa_bwd_window_workspace_size,
+    fa_fwd_tree4_workspace_size,
     fa_fwd_tree_window_workspace_size,
     fa_fwd_tree_workspace_size,
     fa_norm_rope_bwd_workspace_size,
@@ -324,6 +325,21 @@ def _tree_bytes(B, H, Hkv, Tq, Tmax, d, window, sinks, index):
     return n
 
 
+def _check_tree(ctx_len, tree, depths, slopes, B, H, Tq, device):
+    """The context lengths of a batch, and what its new tokens see of one another."""
+    _check_int32(ctx_len, ((B,),), device, "ctx_len")
+    if tree is not None:
+        if not isinstance(tree, torch.Tensor) or tree.dtype not in (_U8, torch.bool) \
+                or not tree.is_contiguous() or tree.shape not in ((Tq, Tq), (B, Tq, Tq)):
+            raise ValueError(f"tree must be a contiguous uint8 or bool tensor of shape "
+                             f"[{Tq}, {Tq}] or [{B}, {Tq}, {Tq}]")
+        _same_device(tree, device, "tree")
+    if depths is not None:
+        _check_int32(depths, ((Tq,), (B, Tq)), device, "depths")
+    if slopes is not None:
+        _check_fp32(slopes, (H,), device, "slopes")
+
+
 def fwd_tree(q, k_cache, v_cache, ctx_len, tree=None, depths=None, softcap: float = 0.0,
              slopes=None, scale: float | None = None, out=None, lse=None, workspace=None,
              status=None, timeout_ns: int = 0, window: int = 0, sinks: int = 0):
@@ -350,17 +366,7 @@ def fwd_tree(q, k_cache, v_cache, ctx_len, tree=None, depths=None, softcap: floa
     if v_cache.shape != shape or Bk != B or dk != d or Hkv == 0 or H % Hkv:
         raise ValueError("q must be [B, H, Tq, d] and the caches [B, Hkv, Tmax, d] with Hkv a "
                          "divisor of H")
-    _check_int32(ctx_len, ((B,),), device, "ctx_len")
-    if tree is not None:
-        if not isinstance(tree, torch.Tensor) or tree.dtype not in (_U8, torch.bool) \
-                or not tree.is_contiguous() or tree.shape not in ((Tq, Tq), (B, Tq, Tq)):
-            raise ValueError(f"tree must be a contiguous uint8 or bool tensor of shape "
-                             f"[{Tq}, {Tq}] or [{B}, {Tq}, {Tq}]")
-        _same_device(tree, device, "tree")
-    if depths is not None:
-        _check_int32(depths, ((Tq,), (B, Tq)), device, "depths")
-    if slopes is not None:
-        _check_fp32(slopes, (H,), device, "slopes")
+    _check_tree(ctx_len, tree, depths, slopes, B, H, Tq, device)
     if scale is None:
         scale = 1.0 / math.sqrt(d)
     if out is None:
@@ -676,3 +682,148 @@ def norm_rope_append(q, k, v, q_weight, k_weight, k_cache, v_cache, ctx_len, inv
           v_cache.data_ptr(), ctx_len.data_ptr(), _ptr(positions), per_batch, inv_freq.data_ptr(), rot,
           interleaved, mscale, B, H, Hkv, Tq, Tmax, d)
     return out
+
+
+# ------------------------------------------------------------------- a cache held in 4 bits
+
+class Cache4:
+    """Keys and values of B sequences in 4 bits: codes, uint8 [B, Hkv, Tmax, d/2], and scales, bfloat16
+    [B, Hkv, Tmax, d/32], of each (the format: include/fa.h). ``cache4`` makes an empty one."""
+
+    __slots__ = ("k_codes", "k_scales", "v_codes", "v_scales", "shape", "device")
+
+    def __init__(self, k_codes, k_scales, v_codes, v_scales):
+        if not isinstance(k_codes, torch.Tensor) or k_codes.dim() != 4 or not k_codes.is_cuda:
+            raise ValueError("k_codes must be a CUDA tensor of shape [B, Hkv, Tmax, d/2]")
+        B, Hkv, Tmax, half = codes = k_codes.shape
+        if half not in (32, 64) or Tmax % 8:
+            raise ValueError("d must be 64 or 128 and Tmax a multiple of 8")
+        scales, device = (B, Hkv, Tmax, half // 16), k_codes.device
+        for t, shape, dtype, name in ((k_codes, codes, _U8, "k_codes"), (k_scales, scales, _BF16, "k_scales"),
+                                      (v_codes, codes, _U8, "v_codes"), (v_scales, scales, _BF16, "v_scales")):
+            if not isinstance(t, torch.Tensor) or t.dtype is not dtype or t.shape != shape \
+                    or not t.is_contiguous():
+                raise ValueError(f"{name} must be a contiguous {dtype} tensor of shape {list(shape)}")
+            if t.device != device:
+                _same_device(t, device, name)
+        self.k_codes, self.k_scales, self.v_codes, self.v_scales = k_codes, k_scales, v_codes, v_scales
+        self.shape, self.device = (B, Hkv, Tmax, 2 * half), device
+
+    def _ptrs(self):
+        return (self.k_codes.data_ptr(), self.k_scales.data_ptr(), self.v_codes.data_ptr(),
+                self.v_scales.data_ptr())
+
+
+def cache4(B: int, Hkv: int, Tmax: int, d: int, device=None) -> Cache4:
+    """An empty 4-bit cache for B sequences of up to Tmax tokens (a multiple of 8): every row zeros."""
+    device = torch.device("cuda" if device is None else device)
+    if d not in (64, 128) or Tmax % 8:
+        raise ValueError("d must be 64 or 128 and Tmax a multiple of 8")
+    codes = [torch.full((B, Hkv, Tmax, d // 2), 0x88, dtype=_U8, device=device) for _ in range(2)]
+    scales = [torch.zeros((B, Hkv, Tmax, d // 32), dtype=_BF16, device=device) for _ in range(2)]
+    return Cache4(codes[0], scales[0], codes[1], scales[1])
+
+
+def _check_cache4(cache):
+    if not isinstance(cache, Cache4):
+        raise TypeError("cache must be a Cache4")
+    return cache.shape
+
+
+def append4(k, v, cache, ctx_len):
+    """A serving step's new keys (turned already) and values [B, Hkv, Tq, d] (any strides) into rows
+    ctx_len[b] … of a 4-bit cache, through fa_append4. ``ctx_len``: int32 [B]; negative: an inactive
+    sequence, whose rows stay. Rows past Tmax are not written."""
+    B, Hkv, Tmax, d = _check_cache4(cache)
+    _check_four(k, "k", "Hkv")
+    device, Tq = cache.device, k.shape[2]
+    new = (B, Hkv, Tq, d)
+    ks, vs = _check_rows(k, "k", new, device), _check_rows(v, "v", new, device)
+    _check_int32(ctx_len, ((B,),), device, "ctx_len")
+    _call(device, "fa_append4", k.data_ptr(), *ks, v.data_ptr(), *vs, *cache._ptrs(),
+          ctx_len.data_ptr(), B, Hkv, Tq, Tmax, d)
+
+
+def read4(cache, start, n: int, out_k=None, out_v=None):
+    """Rows start[b] … start[b] + n − 1 (int32 [B]) of a 4-bit cache as the bf16 values they stand for,
+    through fa_read4: (k, v), [B, Hkv, n, d]. Rows past Tmax, and all of a negative start, are zeros."""
+    B, Hkv, Tmax, d = _check_cache4(cache)
+    device, shape = cache.device, (B, Hkv, n, d)
+    _check_int32(start, ((B,),), device, "start")
+    outs = []
+    for t, name in ((out_k, "out_k"), (out_v, "out_v")):
+        if t is None:
+            t = torch.empty(shape, dtype=_BF16, device=device)
+        else:
+            _check_on(t, device, name)
+            if t.shape != shape:
+                raise ValueError(f"{name} must have shape {list(shape)}")
+        outs.append(t)
+    _call(device, "fa_read4", *cache._ptrs(), start.data_ptr(), outs[0].data_ptr(), outs[1].data_ptr(),
+          B, Hkv, n, Tmax, d)
+    return outs[0], outs[1]
+
+
+@functools.lru_cache(maxsize=256)
+def _tree4_bytes(B, H, Hkv, Tq, Tmax, d, window, sinks, index):
+    """fa_fwd_tree4_workspace_size on device ``index``, a function of its arguments alone."""
+    with torch.cuda.device(index):
+        n = fa_fwd_tree4_workspace_size(B, H, Hkv, Tq, Tmax, d, window, sinks)
+    if n == 0:
+        raise FAError(FA_ERR_INVALID_ARG, "fa_fwd_tree4_workspace_size")
+    return n
+
+
+def fwd_tree4_workspace(B: int, H: int, Hkv: int, Tq: int, Tmax: int, d: int, device=None,
+                        window: int = 0, sinks: int = 0):
+    """A uint8 CUDA tensor large enough to serve as ``fwd_tree4``'s workspace."""
+    _check_window(window, sinks, 0x7FFFFFFF)
+    device = torch.device("cuda" if device is None else device)
+    if device.index is None:
+        device = torch.device("cuda", torch.cuda.current_device())
+    return torch.empty(_tree4_bytes(B, H, Hkv, Tq, Tmax, d, window, sinks, device.index), dtype=_U8,
+                       device=device)
+
+
+def fwd_tree4(q, cache, ctx_len, tree=None, depths=None, softcap: float = 0.0, slopes=None,
+              scale: float | None = None, out=None, lse=None, workspace=None, status=None,
+              timeout_ns: int = 0, window: int = 0, sinks: int = 0):
+    """``fwd_tree`` over a 4-bit cache, through fa_fwd_tree4: new tokens q [B, H, Tq, d] against the
+    ctx_len[b] tokens of their sequence and one another, whose keys and values ``append4`` has written
+    behind them. Every other argument, the window included, and the results as there; keys and values are
+    what the codes stand for (``read4``), exactly."""
+    _check(q, "q")
+    device = q.device
+    Bk, Hkv, Tmax, dk = _check_cache4(cache)
+    if window or sinks:
+        _check_window(window, sinks, 0x7FFFFFFF)
+    B, H, Tq, d = q.shape
+    if Bk != B or dk != d or Hkv == 0 or H % Hkv:
+        raise ValueError("q must be [B, H, Tq, d] and the cache for [B, Hkv, Tmax, d] with Hkv a divisor "
+                         "of H")
+    if cache.device != device:
+        raise ValueError(f"cache must be on {device}, as the other tensors")
+    _check_tree(ctx_len, tree, depths, slopes, B, H, Tq, device)
+    if scale is None:
+        scale = 1.0 / math.sqrt(d)
+    if out is None:
+        out = torch.empty_like(q)
+    else:
+        _check_like(out, q, "out")
+    if lse is None:
+        lse = torch.empty((B, H, Tq), dtype=_FP32, device=device)
+    else:
+        _check_fp32(lse, (B, H, Tq), device, "lse")
+    if workspace is None:
+        need = _tree4_bytes(B, H, Hkv, Tq, Tmax, d, window, sinks, device.index)
+        if need > 1:
+            workspace = torch.empty(need, dtype=_U8, device=device)
+    else:
+        _check_workspace(workspace, device)
+        need = workspace.numel() * workspace.element_size()
+    _check_status(status, device)
+    _call(device, "fa_fwd_tree4", q.data_ptr(), *cache._ptrs(), out.data_ptr(), lse.data_ptr(),
+          ctx_len.data_ptr(), _ptr(tree), tree is not None and tree.dim() == 3, _ptr(depths),
+          depths is not None and depths.dim() == 2, window, sinks, softcap, _ptr(slopes), B, H, Hkv, Tq,
+          Tmax, d, scale, _ptr(workspace), need, _ptr(status), timeout_ns)
+    return out, lse

@@ -549,6 +549,47 @@ int fa_fwd_tree_window(const void* q, const void* k_cache, const void* v_cache, 
                        int H, int Hkv, int Tq, int Tmax, int d, float scale, void* workspace,
                        size_t workspace_bytes, int* status, unsigned long long timeout_ns, void* stream);
 
+/*
+ * ---------------------------------------------------------------------------------------
+ * A cache held in 4 bits. A row of d values is d/32 groups; a group is a scale (bf16: its largest
+ * magnitude over 7, rounded up to five significant bits) times whole numbers −7 … 7, each the nearest
+ * (ties to even) to the value over the scale, kept plus 8 in four bits. Every such value is a bf16
+ * number. A group whose largest magnitude is below 2⁻¹⁰⁰ is zeros; one with a magnitude of 2¹²⁵ or more,
+ * an infinity or a NaN is NaN throughout.
+ *
+ *   k_codes, v_codes   : DEVICE uint8 [B][Hkv][Tmax][d/2], Tmax a multiple of 8. In a row, as 32-bit
+ *                        words of eight codes (code 0 in the lowest bits): keys, word c·(d/32) + w holds
+ *                        dimensions 32w + 4c + (0, 2, 16, 18, 1, 3, 17, 19); values, word 8h + n holds
+ *                        dimensions 64h + n + 8·(0 … 7)
+ *   k_scales, v_scales : DEVICE bf16 [B][Hkv][Tmax][d/32]
+ *   (all four 16-byte aligned, overlapping nothing)
+ *
+ * fa_append4 — a serving step's new keys and values [B, Hkv, Tq, d] (bf16, strided as fa_rope's sources;
+ * keys turned already) into rows ctx_len[b] … of the caches. ctx_len: DEVICE int32 [B]; negative: an
+ * inactive sequence, whose rows stay. Rows past Tmax are not written, nothing else is touched.
+ *
+ * fa_read4 — rows start[b] … start[b] + n − 1 as the bf16 values they stand for, k_out and v_out
+ * [B, Hkv, n, d]. Rows past Tmax, and all of a negative start, are zeros.
+ *
+ * fa_fwd_tree4 — fa_fwd_tree (window 0) or fa_fwd_tree_window over such a cache: q, o and lse and every
+ * other argument as there, the keys and values being what the codes stand for, exactly. (More than 32
+ * query rows a key head are taken in blocks of 32, each of which reads the cache.)
+ * workspace: fa_fwd_tree4_workspace_size(...) bytes, as for fa_fwd_tree.
+ * ---------------------------------------------------------------------------------------
+ */
+int fa_append4(const void* k, long long k_sb, long long k_sh, long long k_st, const void* v, long long v_sb,
+               long long v_sh, long long v_st, void* k_codes, void* k_scales, void* v_codes, void* v_scales,
+               const int* ctx_len, int B, int Hkv, int Tq, int Tmax, int d, void* stream);
+int fa_read4(const void* k_codes, const void* k_scales, const void* v_codes, const void* v_scales,
+             const int* start, void* k_out, void* v_out, int B, int Hkv, int n, int Tmax, int d, void* stream);
+size_t fa_fwd_tree4_workspace_size(int B, int H, int Hkv, int Tq, int Tmax, int d, int window, int sinks);
+int fa_fwd_tree4(const void* q, const void* k_codes, const void* k_scales, const void* v_codes,
+                 const void* v_scales, void* o, float* lse, const int* ctx_len, const unsigned char* tree,
+                 int tree_per_batch, const int* depths, int depths_per_batch, int window, int sinks,
+                 float softcap, const float* slopes, int B, int H, int Hkv, int Tq, int Tmax, int d, float scale,
+                 void* workspace, size_t workspace_bytes, int* status, unsigned long long timeout_ns,
+                 void* stream);
+
 /* Static text for a status code (never NULL). */
 const char* fa_strerror(int status);
 
