@@ -29,7 +29,7 @@ SOURCES = ["fa_api.cu", "fa_fwd1.cu", "fa_fwd1_gen.cu", "fa_fwd_pair.cu", "fa_fw
            "fa_tree_wide_d64.cu", "fa_tree_wide_d128.cu", "fa_sink_fwd_d64.cu", "fa_sink_fwd_d128.cu",
            "fa_sink_pairs_d64.cu", "fa_sink_pairs_d128.cu", "fa_sink_bwd_d64.cu", "fa_sink_bwd_d128.cu",
            "fa_tree_window_d64.cu", "fa_tree_window_d128.cu", "fa_tree_window_wide_d64.cu",
-           "fa_tree_window_wide_d128.cu", "fa_four.cu", "fa_tree_four_d64.cu", "fa_tree_four_d128.cu"]
+           "fa_tree_window_wide_d128.cu", "fa_four.cu", "fa_tree4_d64.cu", "fa_tree4_d128.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ["-O3", "-lineinfo", "-std=c++20", "-Xcompiler", "-fPIC", "-Xptxas", "-v",
          "-I", INCLUDE, "-I", CSRC]

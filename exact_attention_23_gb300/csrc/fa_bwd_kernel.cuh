@@ -399,37 +399,40 @@ __global__ void __launch_bounds__(256) fa_bwd_sum_kernel(const float* __restrict
 }
 
 // dK and dV of the key tiles whose walks were cut: their pieces' fp32 rows, of every part in order, as
-// bf16. A block 32 rows of a cut tile of a key head (blockIdx.x = (key head · n_cut + cut) · 4 + quarter).
+// bf16. A block takes kPieceRows rows of a cut tile of a key head, a thread 8 values of one of its rows
+// (blockIdx.x = (key head · n_cut + cut) · 128 / kPieceRows + which rows): the pieces are read one
+// behind the other, so what counts is that no thread has more than one such chain.
+template <int D>
+constexpr int kPieceRows = 2048 / D / 2;  // (dK and dV, 256 threads of 8 values)
 template <int D>
 __global__ void __launch_bounds__(256) fa_bwd_pieces_kernel(const float* __restrict__ piece_out,
                                                             const int4* __restrict__ cuts,
                                                             __nv_bfloat16* __restrict__ dk,
                                                             __nv_bfloat16* __restrict__ dv, int Hkv, int BHkv, int T,
                                                             int n_cut, int n_slots, int parts) {
+  constexpr int kBlocks = 128 / kPieceRows<D>;
   pdl_wait();
   pdl_launch_dependents();
-  const int quarter = blockIdx.x & 3, x = static_cast<int>(blockIdx.x >> 2), bh = x / n_cut;
+  const int x = static_cast<int>(blockIdx.x / kBlocks), bh = x / n_cut;
   const int4 cut = cuts[(size_t)(bh / Hkv) * n_cut + (x - bh * n_cut)];
-  if (cut.z == 0) return;
-  for (int e = threadIdx.x; e < 2 * 32 * (D / 8); e += 256) {
-    const bool is_dv = e >= 32 * (D / 8);
-    const int r = quarter * 32 + (e / (D / 8)) % 32, c = e % (D / 8) * 8, key = cut.x * 128 + r;
-    if (key >= T) continue;
-    float4 a = make_float4(0.f, 0.f, 0.f, 0.f), b = a;
-    for (int s = 0; s < parts; ++s) {
-      const float* src = piece_out +
-          ((((is_dv ? (size_t)BHkv * parts : 0) + (size_t)bh * parts + s) * n_slots + cut.y) * 128 + r) * D + c;
-#pragma unroll 4
-      for (int i = 0; i < cut.z; ++i) {
-        const float4 u = *reinterpret_cast<const float4*>(src + (size_t)i * 128 * D);
-        const float4 v = *reinterpret_cast<const float4*>(src + (size_t)i * 128 * D + 4);
-        a.x += u.x; a.y += u.y; a.z += u.z; a.w += u.w;
-        b.x += v.x; b.y += v.y; b.z += v.z; b.w += v.w;
-      }
+  const bool is_dv = threadIdx.x >= 128;
+  const int e = threadIdx.x & 127, c = e % (D / 8) * 8;
+  const int r = static_cast<int>(blockIdx.x % kBlocks) * kPieceRows<D> + e / (D / 8), key = cut.x * 128 + r;
+  if (cut.z == 0 || key >= T) return;
+  float4 a = make_float4(0.f, 0.f, 0.f, 0.f), b = a;
+  for (int s = 0; s < parts; ++s) {
+    const float* src = piece_out +
+        ((((is_dv ? (size_t)BHkv * parts : 0) + (size_t)bh * parts + s) * n_slots + cut.y) * 128 + r) * D + c;
+#pragma unroll 8
+    for (int i = 0; i < cut.z; ++i) {
+      const float4 u = *reinterpret_cast<const float4*>(src + (size_t)i * 128 * D);
+      const float4 v = *reinterpret_cast<const float4*>(src + (size_t)i * 128 * D + 4);
+      a.x += u.x; a.y += u.y; a.z += u.z; a.w += u.w;
+      b.x += v.x; b.y += v.y; b.z += v.z; b.w += v.w;
     }
-    *reinterpret_cast<uint4*>((is_dv ? dv : dk) + ((size_t)bh * T + key) * D + c) =
-        make_uint4(pack_bf16x2(a.x, a.y), pack_bf16x2(a.z, a.w), pack_bf16x2(b.x, b.y), pack_bf16x2(b.z, b.w));
   }
+  *reinterpret_cast<uint4*>((is_dv ? dv : dk) + ((size_t)bh * T + key) * D + c) =
+      make_uint4(pack_bf16x2(a.x, a.y), pack_bf16x2(a.z, a.w), pack_bf16x2(b.x, b.y), pack_bf16x2(b.z, b.w));
 }
 
 // ------------------------------------------------------------------------------------

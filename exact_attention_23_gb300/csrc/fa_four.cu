@@ -26,34 +26,28 @@ struct FourParams {
   uint8_t* codes[2];             // keys', values': [B][Hkv][Tmax][d/2]
   __nv_bfloat16* scales[2];      // [B][Hkv][Tmax][d/32]
   const int* start;              // [B]: the first of the n rows; < 0: none
-  long long rows;                // 2 · B · Hkv · n
+  unsigned blocks;               // blocks a head
   int B, Hkv, n, Tmax;
 };
 
 constexpr int kFourThreads = 256;
 constexpr int kFourFlight = 4;
 
-// The row that a number stands for.
-struct FourRow {
-  int kv, b, h, t;
-  size_t at;      // row of the cache
-  bool in, held;  // the number is one; the cache has the row
+// The rows of a block, all of one head: kFourFlight times the rows its threads take at once.
+struct FourBlock {
+  int kv, b, h, t0;
+  size_t head;  // b·Hkv + h
 };
-__device__ __forceinline__ FourRow four_row(const FourParams& p, long long r) {
-  FourRow x;
-  x.in = r < p.rows;
-  const long long y = x.in ? r / p.n : 0;
-  x.t = static_cast<int>((x.in ? r : 0) - y * p.n);
-  const int heads = p.B * p.Hkv, z = static_cast<int>(y);
-  x.kv = z >= heads;
-  const int bh = z - x.kv * heads;
-  x.b = bh / p.Hkv;
-  x.h = bh - x.b * p.Hkv;
-  const int start = p.start[x.b];
-  const long long row = static_cast<long long>(start) + x.t;
-  x.held = x.in && start >= 0 && row < p.Tmax;
-  x.at = static_cast<size_t>(bh) * p.Tmax + static_cast<size_t>(x.held ? row : 0);
-  return x;
+__device__ __forceinline__ FourBlock four_block(const FourParams& p, int rows) {
+  const unsigned x = blockIdx.x / p.blocks, heads = static_cast<unsigned>(p.B) * p.Hkv;
+  FourBlock f;
+  f.t0 = static_cast<int>(blockIdx.x - x * p.blocks) * rows;
+  f.kv = x >= heads;
+  const unsigned bh = x - (f.kv ? heads : 0u);
+  f.head = bh;
+  f.b = static_cast<int>(bh / static_cast<unsigned>(p.Hkv));
+  f.h = static_cast<int>(bh - static_cast<unsigned>(f.b) * p.Hkv);
+  return f;
 }
 
 // Which word of a row lane x (of d/8) holds, in the keys' or the values' order.
@@ -67,17 +61,16 @@ __global__ void __launch_bounds__(kFourThreads) fa_append4_kernel(const FourPara
   pdl_wait();
   pdl_launch_dependents();
   constexpr int kLanes = D / 8, kRows = kFourThreads / kLanes;  // rows a block takes at once
-  const int x = threadIdx.x % kLanes;
-  const long long r0 = static_cast<long long>(blockIdx.x) * (kRows * kFourFlight) + threadIdx.x / kLanes;
-  FourRow row[kFourFlight];
-  uint4 in[kFourFlight];
+  const FourBlock f = four_block(p, kRows * kFourFlight);
+  const int x = threadIdx.x % kLanes, t0 = f.t0 + threadIdx.x / kLanes;
+  const int start = p.start[f.b];
+  const RopeSrc s = f.kv ? p.v : p.k;
+  const __nv_bfloat16* src = s.p + f.b * s.sb + f.h * s.sh + x * 8;
+  uint4 in[kFourFlight];  // (read whether or not the cache has the row: no load waits for the length)
 #pragma unroll
   for (int i = 0; i < kFourFlight; ++i) {
-    row[i] = four_row(p, r0 + i * kRows);
-    const RopeSrc s = row[i].kv ? p.v : p.k;
-    in[i] = make_uint4(0u, 0u, 0u, 0u);
-    if (row[i].held)
-      in[i] = *reinterpret_cast<const uint4*>(s.p + row[i].b * s.sb + row[i].h * s.sh + row[i].t * s.st + x * 8);
+    const int t = t0 + i * kRows;
+    in[i] = t < p.n ? *reinterpret_cast<const uint4*>(src + t * s.st) : make_uint4(0u, 0u, 0u, 0u);
   }
 #pragma unroll
   for (int i = 0; i < kFourFlight; ++i) {
@@ -88,20 +81,16 @@ __global__ void __launch_bounds__(kFourThreads) fa_append4_kernel(const FourPara
     for (int e = 0; e < 8; ++e) top = max(top, __float_as_uint(v[e]) & 0x7FFFFFFFu);
     top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
     top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
-    const float s = four_scale_of(top);
+    const float sc = four_scale_of(top);
     uint32_t w = 0x88888888u;  // (zeros, and groups that are no numbers)
-    if (s > 0.f) {
-      const float inv = __frcp_rn(s);
-      w = 0u;
-#pragma unroll
-      for (int e = 0; e < 8; ++e) w |= four_code(v[e], s, inv) << (4 * e);
-    }
-    // (the lanes of a warp hold rows of both kinds where the keys end)
-    const uint32_t wk = four_to_key(w, x), wv = four_transpose(w, x & 7);
-    if (!row[i].held) continue;
-    const int kv = row[i].kv;
-    *reinterpret_cast<uint32_t*>(p.codes[kv] + row[i].at * (D / 2) + four_word<D>(kv, x) * 4) = kv ? wv : wk;
-    if ((x & 3) == 0) p.scales[kv][row[i].at * (D / 32) + (x >> 2)] = __float2bfloat16_rn(s);
+    if (sc > 0.f) w = four_codes(v, sc);
+    w = f.kv ? four_transpose(w, x & 7) : four_to_key(w, x);
+    const int t = t0 + i * kRows;
+    const long long row = static_cast<long long>(start) + t;
+    if (start < 0 || t >= p.n || row >= p.Tmax) continue;
+    const size_t at = f.head * p.Tmax + static_cast<size_t>(row);
+    *reinterpret_cast<uint32_t*>(p.codes[f.kv] + at * (D / 2) + four_word<D>(f.kv, x) * 4) = w;
+    if ((x & 3) == 0) p.scales[f.kv][at * (D / 32) + (x >> 2)] = __float2bfloat16_rn(sc);
   }
 }
 
@@ -110,33 +99,33 @@ __global__ void __launch_bounds__(kFourThreads) fa_read4_kernel(const FourParams
   pdl_wait();
   pdl_launch_dependents();
   constexpr int kLanes = D / 8, kRows = kFourThreads / kLanes;
-  const int x = threadIdx.x % kLanes;
-  const long long r0 = static_cast<long long>(blockIdx.x) * (kRows * kFourFlight) + threadIdx.x / kLanes;
-  FourRow row[kFourFlight];
-  uint32_t w[kFourFlight];
-  float s[kFourFlight];
+  const FourBlock f = four_block(p, kRows * kFourFlight);
+  const int x = threadIdx.x % kLanes, t0 = f.t0 + threadIdx.x / kLanes;
+  const int start = p.start[f.b];
+  uint32_t w[kFourFlight], s[kFourFlight];  // (a scale twice in a word)
 #pragma unroll
   for (int i = 0; i < kFourFlight; ++i) {
-    row[i] = four_row(p, r0 + i * kRows);
-    const int kv = row[i].kv;
+    const int t = t0 + i * kRows;
+    const long long row = static_cast<long long>(start) + t;
     w[i] = 0u;
-    s[i] = 0.f;
-    if (row[i].held) {
-      w[i] = *reinterpret_cast<const uint32_t*>(p.codes[kv] + row[i].at * (D / 2) + four_word<D>(kv, x) * 4);
-      s[i] = __bfloat162float(p.scales[kv][row[i].at * (D / 32) + (x >> 2)]);
-    }
+    s[i] = 0u;
+    if (start < 0 || t >= p.n || row >= p.Tmax) continue;
+    const size_t at = f.head * p.Tmax + static_cast<size_t>(row);
+    w[i] = *reinterpret_cast<const uint32_t*>(p.codes[f.kv] + at * (D / 2) + four_word<D>(f.kv, x) * 4);
+    s[i] = reinterpret_cast<const unsigned short*>(p.scales[f.kv])[at * (D / 32) + (x >> 2)] * 0x10001u;
   }
+  __nv_bfloat16* out = (f.kv ? p.v_out : p.k_out) + f.head * p.n * D + x * 8;
 #pragma unroll
   for (int i = 0; i < kFourFlight; ++i) {
-    const uint32_t a = four_from_key(w[i], x), b = four_transpose(w[i], x & 7);
-    const uint32_t c = row[i].kv ? b : a;
-    if (!row[i].in) continue;
-    float v[8];
-#pragma unroll
-    for (int e = 0; e < 8; ++e) v[e] = row[i].held ? static_cast<float>(static_cast<int>((c >> (4 * e)) & 15u) - 8) * s[i] : 0.f;
-    __nv_bfloat16* out = row[i].kv ? p.v_out : p.k_out;
-    *reinterpret_cast<uint4*>(out + ((static_cast<size_t>(row[i].b) * p.Hkv + row[i].h) * p.n + row[i].t) * D + x * 8) =
-        make_uint4(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]), pack_bf16x2(v[4], v[5]), pack_bf16x2(v[6], v[7]));
+    const int t = t0 + i * kRows;
+    const uint32_t c = f.kv ? four_transpose(w[i], x & 7) : four_from_key(w[i], x);
+    if (t >= p.n) continue;
+    // (with a scale of 0 where no row was read: zeros, of either sign as they come)
+    const FourScale g = four_scale(s[i]);
+    const uint32_t x0 = four_pair<0>(c, g), x1 = four_pair<1>(c, g), x2 = four_pair<2>(c, g), x3 = four_pair<3>(c, g);
+    *reinterpret_cast<uint4*>(out + static_cast<size_t>(t) * D) =
+        make_uint4(__byte_perm(x0, x1, 0x5410), __byte_perm(x2, x3, 0x5410), __byte_perm(x0, x1, 0x7632),
+                   __byte_perm(x2, x3, 0x7632));
   }
 }
 
@@ -148,8 +137,8 @@ bool four_sizes(int B, int Hkv, int n, int Tmax, int d) {
   if (B <= 0 || Hkv <= 0 || n <= 0 || Tmax <= 0 || Tmax % 8 != 0 || (d != 64 && d != 128)) return false;
   const long long heads = static_cast<long long>(B) * Hkv;
   if (heads > (1 << 30) || heads > (1LL << 60) / d / Tmax || heads > (1LL << 38) / n) return false;
-  // (blocks of at least 64 rows)
-  return 2 * heads * n / 64 < INT32_MAX;
+  // (a block takes at least 64 rows of a head)
+  return 2 * heads * ((static_cast<long long>(n) + 63) / 64) < INT32_MAX;
 }
 
 // Sizes, pointers and overlaps of both calls: `rows` are the bf16 rows of keys and values.
@@ -177,9 +166,10 @@ int four_check(const FourParams& p, int d, const void* const rows[2], const size
 }
 
 template <typename Fn>
-int four_launch(Fn* fn, const FourParams& p, int d, void* stream) {
-  const long long per = static_cast<long long>(kFourThreads) / (d / 8) * kFourFlight;
-  const unsigned grid = static_cast<unsigned>((p.rows + per - 1) / per);
+int four_launch(Fn* fn, FourParams& p, int d, void* stream) {
+  const unsigned per = kFourThreads / (static_cast<unsigned>(d) / 8) * kFourFlight;
+  p.blocks = (static_cast<unsigned>(p.n) + per - 1) / per;
+  const unsigned grid = 2u * static_cast<unsigned>(p.B) * p.Hkv * p.blocks;
   return launch_pdl(fn, grid, kFourThreads, 0, static_cast<cudaStream_t>(stream), p) == cudaSuccess ? FA_OK : FA_ERR_LAUNCH;
 }
 
@@ -210,7 +200,6 @@ int fa_append4(const void* k, long long k_sb, long long k_sh, long long k_st, co
   p.scales[0] = static_cast<__nv_bfloat16*>(k_scales);
   p.scales[1] = static_cast<__nv_bfloat16*>(v_scales);
   p.start = ctx_len;
-  p.rows = 2LL * B * Hkv * Tq;
   p.B = B; p.Hkv = Hkv; p.n = Tq; p.Tmax = Tmax;
   if (!aligned16(k) || !aligned16(v) || four_misaligned(p)) return FA_ERR_MISALIGNED;
   const void* rows[2] = {k, v};
@@ -233,7 +222,6 @@ int fa_read4(const void* k_codes, const void* k_scales, const void* v_codes, con
   p.scales[0] = static_cast<__nv_bfloat16*>(const_cast<void*>(k_scales));
   p.scales[1] = static_cast<__nv_bfloat16*>(const_cast<void*>(v_scales));
   p.start = start;
-  p.rows = 2LL * B * Hkv * n;
   p.B = B; p.Hkv = Hkv; p.n = n; p.Tmax = Tmax;
   if (!aligned16(k_out) || !aligned16(v_out) || four_misaligned(p)) return FA_ERR_MISALIGNED;
   const void* rows[2] = {k_out, v_out};

@@ -44,18 +44,28 @@ __device__ __forceinline__ uint32_t four_pair(uint32_t word, const FourScale& f)
 __device__ __forceinline__ float four_scale_of(uint32_t top_bits) {
   if (top_bits >= 0x7E000000u) return __uint_as_float(0x7FC00000u);
   if (top_bits < 0x0D800000u) return 0.f;
-  const uint32_t q = __float_as_uint(__fdiv_rn(__uint_as_float(top_bits), 7.0f));
+  // (times a little less than 1/7: a quotient that has five bits stays below itself and is rounded up to it,
+  // and an eight-bit number over 7 comes no nearer to any other than 2⁻⁹ of it)
+  const uint32_t q = __float_as_uint(__uint_as_float(top_bits) * 0.14285701f);
   return __uint_as_float((q + 0x7FFFFu) & ~0x7FFFFu);
 }
-// The nearest whole number to x / s, ties to even, plus 8. x·(1/s) can be off by its roundings where x / s lies half-way
-// between two numbers, and nowhere else (an eight-bit over a five-bit number comes no nearer to
-// one than 2⁻¹¹); there the remainder x − n·s, which is exact, is half of s.
-__device__ __forceinline__ uint32_t four_code(float x, float s, float inv) {
-  float n = rintf(x * inv);
-  const float rem = fmaf(-n, s, x);
-  const int k = static_cast<int>(n);
-  if (fabsf(rem) * 2.0f == s && (k & 1)) return static_cast<uint32_t>(k + (rem > 0.f ? 9 : 7));
-  return static_cast<uint32_t>(k + 8);
+
+// Eight values over a scale s, each the nearest whole number, ties to even, plus 8, as a word (number e at bits
+// 4e). x·i + 1.5·2²³ rounds x·i to a whole number in the sum's lowest bits; i a little below 1/s and a
+// little above it give the same one except where x / s lies half-way between two (an eight-bit over a five-bit
+// number comes no nearer to half-way than 2⁻¹¹): then they give both, and the even one is taken.
+__device__ __forceinline__ uint32_t four_codes(const float* v, float s) {
+  float inv;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(inv) : "f"(s));  // within 2⁻²³
+  const float lo = inv * (1.0f - 0x1p-21f), hi = inv * (1.0f + 0x1p-21f);
+  constexpr float kRound = 12582912.0f + 8.0f;  // bits 0x4B400008
+  uint32_t w = 0u;
+#pragma unroll
+  for (int e = 7; e >= 0; --e) {
+    const uint32_t a = __float_as_uint(fmaf(v[e], lo, kRound)), b = __float_as_uint(fmaf(v[e], hi, kRound));
+    w = w * 16u + ((a & 1u) ? b : a);
+  }
+  return w - 0x4B400000u * 0x11111111u;  // (0x4B400000 in every place)
 }
 
 // Eight lanes' words as an 8 × 8 matrix of codes (lane x, nibble n), transposed.

@@ -40,7 +40,6 @@ constexpr int kModRef = 16;  // with a cap alone, small enough: the softmax's re
 constexpr int kModRest = 32; // o's rest is written (two tiles; one tile: kModRef only, others look at the pointer)
 constexpr int kModTight = 64; // kModRef on two tiles, d = 64, without rest: masked or far steps are common
 constexpr int kModTree = 8;  // new tokens against a cache (fa_tree_walk.cuh)
-constexpr int kModFour = 256;  // a cache held in 4 bits (fa_four.cuh; always with kModSink)
 constexpr int kModSink = 128;  // a second interval of keys a row, in front of the first (TREE: a window and sinks)
 
 // The cap. With u = z / cap = in · s (s the raw score), the capped score in base 2 is

@@ -100,6 +100,7 @@ struct VisibleParams {
   const int* ids;     // [B][T] or null
   const int* prefix;  // [B] or [B][T] or null
   int prefix_per_token, causal, T, n_t;
+  uint32_t by_seg;    // ⌈2³² / seg⌉, seg the rows a thread's stretch has: ⌊i / seg⌋ is the upper half of its product with i < 2¹⁵, seg > 1
   int2* rows;
   int4 *fwd, *pairs, *bwd;
   int2 *whole, *span, *seen;
@@ -145,9 +146,10 @@ __device__ __forceinline__ void doc_bits(const int* ids, int i0, int end, uint32
 // One block a sequence. A document is a maximal run of equal ids, so a row's document starts at
 // the last change of id at or before it and ends at the next one after it: a running maximum and
 // a running minimum, each thread taking one stretch of rows (as bits, 32 rows at a time) and the
-// block joining the stretches. Then a warp a tile: its rows' extremes, the query tiles that see
-// it, and its place among the tiles by the number it has to walk (a count of the tiles before it:
-// n_t² comparisons, which at 16384 tokens are 4 a lane and tile). Latency is all it costs; the
+// block joining the stretches. Then a warp a tile: its rows (from their stretch's bits, where a stretch
+// has at most 32, so that rows are written side by side: T 16384 VIS) and their extremes, the query tiles
+// that see it, and its place among the tiles by the number it has to walk (a count of the tiles before
+// it: n_t² comparisons, which at 16384 tokens are 4 a lane and tile). Latency is all it costs; the
 // tiles' extremes are kept in shared memory up to kVisTiles of them. WINDOW: rows see the last
 // `window` keys at most; SINK: and the first `sinks` of their document (fa_visible_window).
 template <bool WINDOW, bool SINK>
@@ -157,6 +159,10 @@ __global__ void __launch_bounds__(kVisThreads) fa_visible_kernel(const VisiblePa
   __shared__ int2 s_span[kVisTiles], s_seen[kVisTiles];
   __shared__ int s_far[SINK ? kVisTiles : 1];   // past the last query tile that sees a key tile's sinks, 0: none beyond a window
   __shared__ int2 s_near[SINK ? kVisTiles : 1]; // a query tile's K tiles with sinks, before its first
+  // A stretch's document starts and paddings as bits, the document it starts in and the next one's start; then
+  // a tile's steps in the forward, those of a piece of its walk in the backward and the pieces, and a pair's steps.
+  static_assert(kVisThreads == kVisTiles, "one array for both");
+  __shared__ int4 s_four[kVisThreads];
   pdl_wait();
   pdl_launch_dependents();
   const int b = blockIdx.x, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -208,8 +214,34 @@ __global__ void __launch_bounds__(kVisThreads) fa_visible_kernel(const VisiblePa
     cur = max(max(cur, __reduce_max_sync(0xffffffffu, l)), 0);
     end = min(end, __reduce_min_sync(0xffffffffu, f));
   }
-  const bool one = a1 - a0 <= 32;  // the stretch's bits are still in registers
-  if (!one) {  // the rows' starts, front to back, for the pass below
+  const int* pre_at = nullptr;
+  int pre_all = 0;
+  if (p.prefix && p.causal) {
+    if (p.prefix_per_token) pre_at = p.prefix + static_cast<size_t>(b) * T;
+    else pre_all = max(0, p.prefix[b]);
+  }
+  // Row i's keys, its document being [lo, end); SINK: and its sinks, and who sees it as one.
+  auto row_of = [&](int i, int lo, int end, bool pad, int2* sink) {
+    *sink = make_int2(0, 0);
+    if (pad) return make_int2(0, 0);
+    int2 r = make_int2(lo, end);
+    if constexpr (WINDOW) {
+      r = make_int2(max(lo, i + 1 - p.window), i + 1);
+      if constexpr (SINK) {
+        if (lo < r.x) *sink = make_int2(lo, min(lo + p.sinks, r.x));
+        if (i - lo < p.sinks && end - i > p.window) atomicMax(far + (i >> 7), (end + 127) >> 7);  // seen from beyond the window
+      }
+    } else if (p.causal) {
+      const int pre = pre_at ? max(0, pre_at[i]) : pre_all;
+      r.y = max(i + 1, pre > end - lo ? end : lo + pre);
+    }
+    return r;
+  };
+  const bool one = seg <= 32;  // a stretch is one group of bits
+  if (one) {
+    s_four[tid] = make_int4(static_cast<int>(starts), static_cast<int>(pads), cur, end);
+  } else {
+    // The rows' document starts, front to back, then the rows from the back.
     int c = cur;
     for (int g0 = a0; g0 < a1; g0 += 32) {
       doc_bits(ids, g0, a1, &starts, &pads);
@@ -218,72 +250,52 @@ __global__ void __launch_bounds__(kVisThreads) fa_visible_kernel(const VisiblePa
         rows[g0 + o].x = c;
       }
     }
-  }
-  int padded = n_t;  // the first tile with padding
-  const int* pre_at = nullptr;
-  int pre_all = 0;
-  if (p.prefix && p.causal) {
-    if (p.prefix_per_token) pre_at = p.prefix + static_cast<size_t>(b) * T;
-    else pre_all = max(0, p.prefix[b]);
-  }
-  int far_tile = -1, far_end = 0;  // SINK: the key tile at hand, and its last document's end
-  auto flush_far = [&]() {
-    if (far_end > 0) atomicMax(far + far_tile, (far_end + 127) >> 7);
-    far_end = 0;
-  };
-  for (int g0 = a0 + max(0, (a1 - a0 - 1)) / 32 * 32; g0 >= a0 && a1 > a0; g0 -= 32) {
-    if (!one) doc_bits(ids, g0, a1, &starts, &pads);
-    for (int o = min(32, a1 - g0) - 1; o >= 0; --o) {
-      const int i = g0 + o;
-      int lo;
-      if (one) {
-        const uint32_t at = starts & ((2u << o) - 1u);
-        lo = at ? g0 + 31 - __clz(at) : cur;
-      } else {
-        lo = rows[i].x;
+    int padded = n_t;
+    for (int g0 = a0 + max(0, (a1 - a0 - 1)) / 32 * 32; g0 >= a0 && a1 > a0; g0 -= 32) {
+      doc_bits(ids, g0, a1, &starts, &pads);
+      for (int o = min(32, a1 - g0) - 1; o >= 0; --o) {
+        const int i = g0 + o, lo = rows[i].x;
+        const bool pad = (pads >> o) & 1u;
+        if (pad) padded = i >> 7;  // (from the back)
+        int2 sink;
+        rows[i] = row_of(i, lo, end, pad, &sink);
+        if constexpr (SINK) sink_rows[i] = sink;
+        if (lo == i) end = i;
       }
-      int2 r = make_int2(lo, end);
-      int2 sink = make_int2(0, 0);
-      if ((pads >> o) & 1u) {
-        r = make_int2(0, 0);
-        padded = i >> 7;  // (from the back)
-      } else {
-        if constexpr (WINDOW) {
-          r = make_int2(max(lo, i + 1 - p.window), i + 1);
-          if constexpr (SINK) {
-            if (lo < r.x) sink = make_int2(lo, min(lo + p.sinks, r.x));
-            if (i - lo < p.sinks && end - i > p.window) {  // seen from beyond the window
-              if (far_tile != i >> 7) flush_far();
-              far_tile = i >> 7;
-              far_end = max(far_end, end);
-            }
-          }
-        } else if (p.causal) {
-          const int pre = pre_at ? max(0, pre_at[i]) : pre_all;
-          r.y = max(i + 1, pre > end - lo ? end : lo + pre);
-        }
-      }
-      rows[i] = r;
-      if constexpr (SINK) sink_rows[i] = sink;
-      if (lo == i) end = i;
     }
+    padded = __reduce_min_sync(0xffffffffu, padded);
+    if (lane == 0) atomicMin(&s_pad, padded);
   }
-  if constexpr (SINK) flush_far();
   for (long long i = T + tid; i < T_pad; i += kVisThreads) {
     rows[i] = make_int2(0, 0);
     if constexpr (SINK) sink_rows[i] = make_int2(0, 0);
   }
-  padded = __reduce_min_sync(0xffffffffu, padded);
-  if (lane == 0) atomicMin(&s_pad, padded);
   __syncthreads();
   const size_t t0 = static_cast<size_t>(b) * n_t;
   for (int t = warp; t < n_t; t += kWarps) {
     int lo_min = T, hi_max = 0, lo_max = 0, hi_min = T;
+    int2 sinks[4];
+    bool pads_here = false;
 #pragma unroll
     for (int k = 0; k < 4; ++k) {
       const int i = t * 128 + lane + 32 * k;
+      sinks[k] = make_int2(0, 0);
       if (i >= T) continue;
-      const int2 r = rows[i];
+      int2 r;
+      if (one) {
+        const int s = seg == 1 ? i : static_cast<int>(__umulhi(p.by_seg, static_cast<uint32_t>(i)));
+        const int4 f = s_four[s];
+        const int o = i - s * static_cast<int>(seg);
+        const uint32_t st = static_cast<uint32_t>(f.x), at = st & ((2u << o) - 1u), after = st & ~((2u << o) - 1u);
+        const bool pad = (static_cast<uint32_t>(f.y) >> o) & 1u;
+        pads_here |= pad;
+        r = row_of(i, at ? i - o + 31 - __clz(at) : f.z, after ? i - o + __ffs(after) - 1 : f.w, pad, &sinks[k]);
+        rows[i] = r;
+        if constexpr (SINK) sink_rows[i] = sinks[k];
+      } else {
+        r = rows[i];
+        if constexpr (SINK) sinks[k] = sink_rows[i];
+      }
       lo_max = max(lo_max, r.x);
       hi_min = min(hi_min, r.y);
       if (r.y > r.x) {
@@ -295,6 +307,7 @@ __global__ void __launch_bounds__(kVisThreads) fa_visible_kernel(const VisiblePa
     hi_min = __reduce_min_sync(0xffffffffu, hi_min);
     lo_max = __reduce_max_sync(0xffffffffu, lo_max);
     hi_max = __reduce_max_sync(0xffffffffu, hi_max);
+    if (__any_sync(0xffffffffu, pads_here) && lane == 0) atomicMin(&s_pad, t);
     if (lane == 0) {
       p.whole[t0 + t] = make_int2(lo_max, hi_min);
       span[t] = hi_max > lo_min ? make_int2(lo_min, hi_max) : make_int2(0, 0);
@@ -305,8 +318,7 @@ __global__ void __launch_bounds__(kVisThreads) fa_visible_kernel(const VisiblePa
       int first_sink = T, past = 0;
 #pragma unroll
       for (int k = 0; k < 4; ++k) {
-        const int i = t * 128 + lane + 32 * k;
-        const int2 s = i < T ? sink_rows[i] : make_int2(0, 0);
+        const int2 s = sinks[k];
         if (s.y > s.x && s.x >> 7 < kb) {
           first_sink = min(first_sink, s.x);
           past = max(past, s.y);
@@ -318,7 +330,7 @@ __global__ void __launch_bounds__(kVisThreads) fa_visible_kernel(const VisiblePa
     }
   }
   __syncthreads();
-  padded = s_pad;
+  const int padded = s_pad;
   for (int t = warp; t < n_t; t += kWarps) {
     // the query tiles whose rows see a key of this tile
     int f = n_t, l = 0;
@@ -341,31 +353,54 @@ __global__ void __launch_bounds__(kVisThreads) fa_visible_kernel(const VisiblePa
     if (lane == 0) seen[t] = l > f ? make_int2(f, l) : make_int2(0, 0);
   }
   __syncthreads();
-  // SINK: a key tile's pieces, and the length of the longest
-  auto pieces_of = [&](int t) {
-    const int n = seen[t].y - seen[t].x;
-    return far[t] > 0 && n > p.piece ? (n + p.piece - 1) / p.piece : 1;
+  // What tiles are sorted by: a query tile's steps, a key tile's (SINK: its pieces, and the length of the
+  // longest), and a pair's, the length of its union's walk.
+  const int n_p = (n_t + 1) / 2;
+  auto walk = [&](int t) {  // first K tile and past the last; (0, 0): none
+    const int2 s = t < n_t ? span[t] : make_int2(0, 0);
+    return make_int2(s.x >> 7, (s.y + 127) >> 7);
   };
+  auto lengths_of = [&](int t) {
+    const int2 s = walk(t);
+    int4 x = make_int4(s.y - s.x, seen[t].y - seen[t].x, 1, 0);
+    if constexpr (SINK) {
+      x.x += near[t].y - near[t].x;
+      if (far[t] > 0 && x.y > p.piece) {
+        x.z = (x.y + p.piece - 1) / p.piece;
+        x.y = (x.y + x.z - 1) / x.z;
+      }
+    }
+    if (t < n_p) {
+      const int2 a = walk(2 * t), c = walk(2 * t + 1);
+      x.w = a.y <= a.x ? c.y - c.x : c.y <= c.x ? a.y - a.x : max(a.y, c.y) - min(a.x, c.x);
+    }
+    return x;
+  };
+  const bool kept = n_t > 32 && n_t <= kVisTiles;  // (few: made where they are looked at, one a lane)
+  if (kept) {
+    if (tid < n_t) s_four[tid] = lengths_of(tid);
+    __syncthreads();
+  }
+  auto lengths = [&](int t) { return kept ? s_four[t] : lengths_of(t); };
   int n_pieces = 0, n_cuts = 0;
   for (int t = warp; t < n_t; t += kWarps) {
     const int2 s = span[t], k = seen[t];
     const int kb = s.x >> 7, ke = (s.y + 127) >> 7;
+    const int4 me = lengths(t);
     if constexpr (SINK) {
       const int2 sk = near[t];
-      const int n = ke - kb + sk.y - sk.x, pc = pieces_of(t), m = k.y - k.x, len = (m + pc - 1) / pc;
+      const int pc = me.z, m = k.y - k.x, len = me.y;
       int rf = 0, rb = 0, slot = 0, cut = 0, all = 0, cuts = 0;
       for (int q = lane; q < n_t; q += 32) {
-        const int2 os = span[q], ok = seen[q], osk = near[q];
-        const int on = ((os.y + 127) >> 7) - (os.x >> 7) + osk.y - osk.x;
-        const int opc = pieces_of(q), olen = (ok.y - ok.x + opc - 1) / opc;
-        rf += on > n || (on == n && q < t);
-        if (olen > len || (olen == len && q < t)) rb += opc;
-        if (opc > 1 && q < t) {
-          slot += opc;
+        const int4 o = lengths(q);
+        rf += o.x > me.x || (o.x == me.x && q < t);
+        if (o.y > len || (o.y == len && q < t)) rb += o.z;
+        if (o.z > 1 && q < t) {
+          slot += o.z;
           ++cut;
         }
-        all += opc;
-        cuts += opc > 1;
+        all += o.z;
+        cuts += o.z > 1;
       }
       rf = __reduce_add_sync(0xffffffffu, rf);
       rb = __reduce_add_sync(0xffffffffu, rb);
@@ -389,10 +424,9 @@ __global__ void __launch_bounds__(kVisThreads) fa_visible_kernel(const VisiblePa
     } else {
       int rf = 0, rb = 0;
       for (int q = lane; q < n_t; q += 32) {
-        const int2 os = span[q], ok = seen[q];
-        const int on = ((os.y + 127) >> 7) - (os.x >> 7), on2 = ok.y - ok.x;
-        rf += on > ke - kb || (on == ke - kb && q < t);
-        rb += on2 > k.y - k.x || (on2 == k.y - k.x && q < t);
+        const int4 o = lengths(q);
+        rf += o.x > me.x || (o.x == me.x && q < t);
+        rb += o.y > me.y || (o.y == me.y && q < t);
       }
       rf = __reduce_add_sync(0xffffffffu, rf);
       rb = __reduce_add_sync(0xffffffffu, rb);
@@ -412,23 +446,12 @@ __global__ void __launch_bounds__(kVisThreads) fa_visible_kernel(const VisiblePa
       for (int i = n_cuts + lane; i < p.n_cut; i += 32) p.cuts[static_cast<size_t>(b) * p.n_cut + i] = make_int4(0, 0, 0, 0);
     }
   }
-  // Pairs of query tiles, by the length of their union's walk.
-  const int n_p = (n_t + 1) / 2;
-  auto walk = [&](int t) {  // first K tile and past the last; (0, 0): none
-    const int2 s = t < n_t ? span[t] : make_int2(0, 0);
-    return make_int2(s.x >> 7, (s.y + 127) >> 7);
-  };
-  auto steps = [&](int2 a, int2 c) {
-    if (a.y <= a.x) return c.y - c.x;
-    if (c.y <= c.x) return a.y - a.x;
-    return max(a.y, c.y) - min(a.x, c.x);
-  };
   for (int t = warp; t < n_p; t += kWarps) {
     const int2 a = walk(2 * t), c = walk(2 * t + 1);
-    const int n = steps(a, c);
+    const int n = lengths(t).w;
     int r = 0;
     for (int q = lane; q < n_p; q += 32) {
-      const int m = steps(walk(2 * q), walk(2 * q + 1));
+      const int m = lengths(q).w;
       r += m > n || (m == n && q < t);
     }
     r = __reduce_add_sync(0xffffffffu, r);
@@ -511,6 +534,8 @@ int make_visible(const int* doc_ids, const int* prefix_len, int prefix_per_token
   p.causal = causal != 0;
   p.T = T;
   p.n_t = static_cast<int>((static_cast<long long>(T) + 127) / 128);
+  const uint64_t seg = (static_cast<uint64_t>(p.n_t) * 128 + fa::kVisThreads - 1) / fa::kVisThreads;
+  p.by_seg = static_cast<uint32_t>((0xFFFFFFFFull + seg) / seg);
   p.rows = reinterpret_cast<int2*>(base + l.rows);
   p.fwd = reinterpret_cast<int4*>(base + l.fwd);
   p.pairs = reinterpret_cast<int4*>(base + l.pairs);

@@ -54,7 +54,7 @@ cudaError_t launch_bwd_mod(const BwdLaunch& a, int q_heads) {
     const BwdModParams& m = a.p.mod;
     const int key_heads = a.p.BH / m.parts;
     const float* piece_out = m.piece_out;
-    e = launch_pdl(fa_bwd_pieces_kernel<D>, static_cast<unsigned>(key_heads) * m.n_cut * 4u, 256, 0, a.stream, piece_out,
+    e = launch_pdl(fa_bwd_pieces_kernel<D>, static_cast<unsigned>(key_heads) * m.n_cut * (128 / kPieceRows<D>), 256, 0, a.stream, piece_out,
                    m.cuts, a.p.dk, a.p.dv, m.Hkv, key_heads, a.p.T, m.n_cut, m.n_slots, m.parts);
     if (e != cudaSuccess) return e;
   }

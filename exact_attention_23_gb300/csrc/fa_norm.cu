@@ -26,6 +26,7 @@
 
 #include "fa.h"
 #include "fa_host.h"
+#include "fa_mod.cuh"
 #include "fa_pdl.h"
 #include "fa_rope.cuh"
 #include "sm103.cuh"
@@ -47,6 +48,7 @@ struct NormParams {
   int pos_per_batch;
   int B, H, Hkv, T, Tmax, rot_units;
   int heads, chunk;                      // q + k (+ v) heads; heads a thread walks
+  FastDiv div_t, div_q, div_k;           // by T; backward: by the queries' and the keys' head chunks
   float mscale, eps;
 };
 
@@ -54,7 +56,6 @@ constexpr int kNormThreads = 128;
 constexpr int kNormPerSm = 5;
 constexpr int kNormFlight = 2;   // heads whose loads a thread keeps in flight
 constexpr int kNormBackPerSm = 4;
-constexpr int kNormBackFlight = 2;
 constexpr int kNormBlocks = 608;  // of the backward, at most (the workspace's rows)
 
 // The sum over the lanes of a row.
@@ -123,9 +124,9 @@ __global__ void __launch_bounds__(kNormThreads, kNormPerSm) fa_norm_kernel(const
   const long long item = static_cast<long long>(blockIdx.x - ch * p.n_blocks) * kNormThreads + threadIdx.x;
   const bool in = item < p.n_items;  // (whole rows: the lanes of a row stay together)
   const int u = static_cast<int>(item % kUnits);
-  const long long row = in ? item / kUnits : 0;
-  const int b = static_cast<int>(row / p.T);
-  const int t = static_cast<int>(row - static_cast<long long>(b) * p.T);
+  const uint32_t row = in ? static_cast<uint32_t>(item / kUnits) : 0u;
+  const int b = static_cast<int>(p.div_t.div(row));
+  const int t = static_cast<int>(row) - b * p.T;
   const Unit16 at = Unit16::of<INTER>(u, p.rot_units);
   const int h0 = static_cast<int>(ch) * p.chunk, h1 = min(p.heads, h0 + p.chunk);
   int ctx = 0;
@@ -228,89 +229,128 @@ __global__ void __launch_bounds__(kNormThreads, kNormBackPerSm) fa_norm_bwd_kern
   __nv_bfloat16* const out = is_q ? p.q_out : p.k_out;
   const int u = static_cast<int>(threadIdx.x % kUnits);
   const Unit16 at = Unit16::of<INTER>(u, p.rot_units);
-  float acc[16];
+  const FastDiv div = is_q ? p.div_q : p.div_k;
+  const uint32_t n_tasks = div.d * p.n_blocks, step = is_q ? p.q_blocks : gridDim.x - p.q_blocks;
+  // A row of a task: (position, head), where its vectors lie, and its position's number.
+  struct Row {
+    const __nv_bfloat16 *x, *g;
+    __nv_bfloat16* dst;
+    int left;       // heads of the task behind it
+    bool in;        // (whole rows: the lanes of a row stay together)
+    int pos;
+  };
+  auto open = [&](uint32_t task) {
+    Row r;
+    const uint32_t block = div.div(task);  // (a position's chunks go out together)
+    const int h0 = static_cast<int>(task - block * div.d) * p.chunk;
+    r.left = min(heads, h0 + p.chunk) - h0 - 1;
+    const long long item = static_cast<long long>(block) * kNormThreads + threadIdx.x;
+    r.in = item < p.n_items;
+    const uint32_t row = r.in ? static_cast<uint32_t>(item / kUnits) : 0u;
+    const int b = static_cast<int>(p.div_t.div(row));
+    const int t = static_cast<int>(row) - b * p.T;
+    r.x = xs.p + b * xs.sb + t * xs.st + h0 * xs.sh;
+    r.g = gs.p + b * gs.sb + t * gs.st + h0 * gs.sh;
+    r.dst = out + ((static_cast<size_t>(b) * heads + h0) * p.T + t) * D;
+    r.pos = p.positions ? p.positions[p.pos_per_batch ? row : t] : t;
+    return r;
+  };
+  auto load = [&](const Row& r, uint4 (&v)[4]) {
+    v[0] = v[1] = v[2] = v[3] = make_uint4(0u, 0u, 0u, 0u);
+    if (!r.in) return;
+    v[0] = *reinterpret_cast<const uint4*>(r.x + at.c0);
+    v[1] = *reinterpret_cast<const uint4*>(r.x + at.c1);
+    v[2] = *reinterpret_cast<const uint4*>(r.g + at.c0);
+    v[3] = *reinterpret_cast<const uint4*>(r.g + at.c1);
+  };
+  uint64_t acc[8];  // pairs of neighbouring dimensions
 #pragma unroll
-  for (int e = 0; e < 16; ++e) acc[e] = 0.f;
-  const long long chunks = (heads + p.chunk - 1) / p.chunk;
-  const long long n_tasks = chunks * p.n_blocks;
-  const long long step = is_q ? p.q_blocks : gridDim.x - p.q_blocks;
-  for (long long task = is_q ? blockIdx.x : blockIdx.x - p.q_blocks; task < n_tasks; task += step) {
-    const long long block = task / chunks;  // (a position's chunks go out together)
-    const int h0 = static_cast<int>(task - block * chunks) * p.chunk, h1 = min(heads, h0 + p.chunk);
-    const long long item = block * kNormThreads + threadIdx.x;
-    const bool in = item < p.n_items;  // (whole rows)
-    const long long row = in ? item / kUnits : 0;
-    const int b = static_cast<int>(row / p.T);
-    const int t = static_cast<int>(row - static_cast<long long>(b) * p.T);
+  for (int e = 0; e < 8; ++e) acc[e] = f2_pack(0.f, 0.f);
+  uint32_t task = is_q ? blockIdx.x : blockIdx.x - p.q_blocks;
+  if (task < n_tasks) {
     float cs[8], sn[8];
-    if (at.turn) {
-      const long long pos = p.positions ? p.positions[p.pos_per_batch ? row : t] : t;
+    Row cur = open(task);
+    uint4 v[4];
+    load(cur, v);
+    bool fresh = true;  // the row is its task's first
+    while (true) {
+      // The next row's vectors are on their way while this one's are worked on.
+      Row next = cur;
+      const bool same = cur.left > 0;
+      bool more = true;
+      if (same) {
+        --next.left;
+        next.x += xs.sh;
+        next.g += gs.sh;
+        next.dst += static_cast<size_t>(p.T) * D;
+      } else {
+        task += step;
+        more = task < n_tasks;
+        if (more) next = open(task);
+      }
+      uint4 nv[4];
+      if (more) load(next, nv);
+      if (fresh && at.turn) {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          const float x = angle_of(turns[u * 8 + e], cur.pos);
+          cs[e] = __cosf(x) * p.mscale;
+          sn[e] = __sinf(x) * -p.mscale;
+        }
+      }
+      float y[16];
+      unpack8(v[2], y);
+      unpack8(v[3], y + 8);
+      if (at.turn) turn16<INTER>(y, cs, sn);
+      uint64_t x2[8], y2[8], yw[8], ss = f2_pack(0.f, 0.f), sd = ss;
 #pragma unroll
       for (int e = 0; e < 8; ++e) {
-        const float x = angle_of(turns[u * 8 + e], pos);
-        cs[e] = __cosf(x) * p.mscale;
-        sn[e] = __sinf(x) * -p.mscale;
+        const uint4& xv = v[e / 4];
+        const uint32_t x = e % 4 == 0 ? xv.x : e % 4 == 1 ? xv.y : e % 4 == 2 ? xv.z : xv.w;
+        x2[e] = f2_pack(__uint_as_float(x << 16), __uint_as_float(x & 0xFFFF0000u));
+        y2[e] = f2_pack(y[2 * e], y[2 * e + 1]);
+        const float2 w = *reinterpret_cast<const float2*>(weight + (e < 4 ? at.c0 + 2 * e : at.c1 + 2 * e - 8));
+        yw[e] = f2_mul(y2[e], f2_pack(w.x, w.y));
+        ss = f2_fma(x2[e], x2[e], ss);
+        sd = f2_fma(yw[e], x2[e], sd);
       }
-    }
-    const __nv_bfloat16* const x_at = xs.p + b * xs.sb + t * xs.st;
-    const __nv_bfloat16* const g_at = gs.p + b * gs.sb + t * gs.st;
-    for (int hb = h0; hb < h1; hb += kNormBackFlight) {
-      uint4 xv[kNormBackFlight][2], gv[kNormBackFlight][2];
+      float s0, s1, d0, d1;
+      f2_unpack(ss, s0, s1);
+      f2_unpack(sd, d0, d1);
+      const float sum_x = row_sum<D>(s0 + s1), sum_d = row_sum<D>(d0 + d1);
+      const float r = rsqrtf(fmaf(sum_x, 1.0f / D, p.eps));
+      const uint64_t r2 = f2_pack(r, r), back = f2_pack(-r * r * sum_d * (1.0f / D), -r * r * sum_d * (1.0f / D));
 #pragma unroll
-      for (int i = 0; i < kNormBackFlight; ++i) {
-        const int h = hb + i;
-        xv[i][0] = xv[i][1] = gv[i][0] = gv[i][1] = make_uint4(0u, 0u, 0u, 0u);
-        if (h >= h1 || !in) continue;
-        const __nv_bfloat16 *xp = x_at + h * xs.sh, *gp = g_at + h * gs.sh;
-        xv[i][0] = *reinterpret_cast<const uint4*>(xp + at.c0);
-        xv[i][1] = *reinterpret_cast<const uint4*>(xp + at.c1);
-        gv[i][0] = *reinterpret_cast<const uint4*>(gp + at.c0);
-        gv[i][1] = *reinterpret_cast<const uint4*>(gp + at.c1);
+      for (int e = 0; e < 8; ++e) {
+        acc[e] = f2_fma(y2[e], f2_mul(x2[e], r2), acc[e]);
+        const uint64_t z = f2_mul(f2_fma(x2[e], back, yw[e]), r2);
+        f2_unpack(z, y[2 * e], y[2 * e + 1]);
       }
-#pragma unroll
-      for (int i = 0; i < kNormBackFlight; ++i) {
-        const int h = hb + i;
-        if (h >= h1) continue;  // (block-uniform)
-        float x[16], y[16], w[16];
-        unpack8(xv[i][0], x);
-        unpack8(xv[i][1], x + 8);
-        unpack8(gv[i][0], y);
-        unpack8(gv[i][1], y + 8);
-        if (at.turn) turn16<INTER>(y, cs, sn);
-        weights16(weight, at, w);
-        float ss = 0.f, sd = 0.f;
-#pragma unroll
-        for (int e = 0; e < 16; ++e) {
-          ss = fmaf(x[e], x[e], ss);
-          sd = fmaf(y[e] * w[e], x[e], sd);
-        }
-        ss = row_sum<D>(ss);
-        sd = row_sum<D>(sd);
-        const float r = rsqrtf(fmaf(ss, 1.0f / D, p.eps));
-        const float back = r * r * sd * (1.0f / D);
-#pragma unroll
-        for (int e = 0; e < 16; ++e) {
-          acc[e] = fmaf(y[e], x[e] * r, acc[e]);
-          y[e] = r * fmaf(y[e], w[e], -x[e] * back);
-        }
-        if (!in) continue;
-        __nv_bfloat16* dst = out + ((static_cast<size_t>(b) * heads + h) * p.T + t) * D;
-        *reinterpret_cast<uint4*>(dst + at.c0) = pack8(y);
-        *reinterpret_cast<uint4*>(dst + at.c1) = pack8(y + 8);
+      if (cur.in) {
+        *reinterpret_cast<uint4*>(cur.dst + at.c0) = pack8(y);
+        *reinterpret_cast<uint4*>(cur.dst + at.c1) = pack8(y + 8);
       }
+      if (!more) break;
+      cur = next;
+      fresh = !same;
+#pragma unroll
+      for (int e = 0; e < 4; ++e) v[e] = nv[e];
     }
   }
   // The block's sums: lanes with the same dimensions, then the warps.
+  float a[16];
+#pragma unroll
+  for (int e = 0; e < 8; ++e) f2_unpack(acc[e], a[2 * e], a[2 * e + 1]);
 #pragma unroll
   for (int e = 0; e < 16; ++e)
 #pragma unroll
-    for (int off = kUnits; off < 32; off <<= 1) acc[e] += __shfl_xor_sync(0xffffffffu, acc[e], off);
+    for (int off = kUnits; off < 32; off <<= 1) a[e] += __shfl_xor_sync(0xffffffffu, a[e], off);
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   if (lane < kUnits) {
 #pragma unroll
     for (int e = 0; e < 8; ++e) {
-      sums[warp][at.c0 + e] = acc[e];
-      sums[warp][at.c1 + e] = acc[e + 8];
+      sums[warp][at.c0 + e] = a[e];
+      sums[warp][at.c1 + e] = a[e + 8];
     }
   }
   __syncthreads();
@@ -352,6 +392,8 @@ namespace {
 using namespace fa::host;
 
 bool norm_eps_ok(float eps) { return std::isfinite(eps) && eps > 0.0f; }
+// (the kernels number rows with 32 bits; more than 2³¹ do not fit a GPU's memory)
+bool norm_rows_ok(int B, int T) { return static_cast<long long>(B) * T <= INT32_MAX; }
 
 int norm_launch(NormParams& p, bool append, int interleaved, int d, void* stream) {
   int dev = -1, sms = 0;
@@ -367,6 +409,7 @@ int norm_launch(NormParams& p, bool append, int interleaved, int d, void* stream
   const long long grid = blocks * ((p.heads + chunk - 1) / chunk);
   if (grid > INT32_MAX) return FA_ERR_INVALID_ARG;
   p.n_blocks = static_cast<unsigned>(blocks);
+  p.div_t = FastDiv::make(static_cast<uint32_t>(p.T));
   using Fn = void (*)(const NormParams);
   static constexpr Fn fns[2][2][2] = {
       {{&fa_norm_kernel<64, false, false>, &fa_norm_kernel<64, false, true>},
@@ -404,7 +447,7 @@ int fa_norm_rope(const void* q, long long q_sb, long long q_sh, long long q_st, 
                  const float* k_weight, float eps, const int* positions, int positions_per_batch,
                  const double* inv_freq, int rot_dim, int interleaved, float mscale, int B, int H, int Hkv,
                  int T, int d, void* stream) {
-  if (!q || !q_out || !inv_freq || !q_weight || !sizes_ok(B, H, Hkv, T, d, rot_dim, mscale) || !norm_eps_ok(eps))
+  if (!q || !q_out || !inv_freq || !q_weight || !sizes_ok(B, H, Hkv, T, d, rot_dim, mscale) || !norm_eps_ok(eps) || !norm_rows_ok(B, T))
     return FA_ERR_INVALID_ARG;
   if ((Hkv > 0) != (k != nullptr) || (Hkv > 0) != (k_out != nullptr) || (Hkv > 0) != (k_weight != nullptr))
     return FA_ERR_INVALID_ARG;
@@ -453,7 +496,8 @@ int fa_norm_rope_append(const void* q, long long q_sb, long long q_sh, long long
                         int interleaved, float mscale, int B, int H, int Hkv, int Tq, int Tmax, int d,
                         void* stream) {
   if (!q || !q_out || !k || !v || !k_cache || !v_cache || !ctx_len || !inv_freq || !q_weight || !k_weight ||
-      !sizes_ok(B, H, Hkv, Tq, d, rot_dim, mscale) || !norm_eps_ok(eps) || Hkv <= 0 || Tmax <= 0)
+      !sizes_ok(B, H, Hkv, Tq, d, rot_dim, mscale) || !norm_eps_ok(eps) || !norm_rows_ok(B, Tq) ||
+      Hkv <= 0 || Tmax <= 0)
     return FA_ERR_INVALID_ARG;
   NormParams p{};
   p.q = {static_cast<const __nv_bfloat16*>(q), q_sb, q_sh, q_st};
@@ -513,7 +557,7 @@ int fa_norm_rope_bwd(const void* gq, long long gq_sb, long long gq_sh, long long
                      float mscale, int B, int H, int Hkv, int T, int d, void* workspace,
                      size_t workspace_bytes, void* stream) {
   if (!gq || !q || !dq || !inv_freq || !q_weight || !dq_weight || !workspace ||
-      !sizes_ok(B, H, Hkv, T, d, rot_dim, mscale) || !norm_eps_ok(eps))
+      !sizes_ok(B, H, Hkv, T, d, rot_dim, mscale) || !norm_eps_ok(eps) || !norm_rows_ok(B, T))
     return FA_ERR_INVALID_ARG;
   const bool keys = Hkv > 0;
   for (const void* x : {gk, k, static_cast<const void*>(dk), static_cast<const void*>(k_weight),
@@ -573,12 +617,17 @@ int fa_norm_rope_bwd(const void* gq, long long gq_sb, long long gq_sh, long long
   if (blocks > INT32_MAX) return FA_ERR_INVALID_ARG;
   p.n_blocks = static_cast<unsigned>(blocks);
   const long long most = std::min<long long>(kNormBlocks, static_cast<long long>(kNormBackPerSm) * sms);
-  // Heads a thread walks: as many as give every block of the grid a task.
+  // Heads a thread walks: as many as leave every block of the grid eight tasks, of which the last may be
+  // one too many (B1 H16+4 T16384 d128, 2.1 tasks of 16 heads a block: 58 µs; 8.4 of 4: KK).
   auto tasks = [&](int heads, long long chunk) { return (heads + chunk - 1) / chunk * blocks; };
   long long chunk = std::max(H, Hkv);
-  while (chunk > 1 && tasks(H, chunk) + (keys ? tasks(Hkv, chunk) : 0) < most) chunk = (chunk + 1) / 2;
+  while (chunk > 1 && tasks(H, chunk) + (keys ? tasks(Hkv, chunk) : 0) < 8 * most) chunk = (chunk + 1) / 2;
   p.chunk = static_cast<int>(chunk);
   const long long nq = tasks(H, chunk), nk = keys ? tasks(Hkv, chunk) : 0;
+  if (nq > INT32_MAX || nk > INT32_MAX) return FA_ERR_INVALID_ARG;
+  p.div_t = FastDiv::make(static_cast<uint32_t>(T));
+  p.div_q = FastDiv::make(static_cast<uint32_t>((H + chunk - 1) / chunk));
+  p.div_k = FastDiv::make(static_cast<uint32_t>(std::max<long long>(1, (Hkv + chunk - 1) / chunk)));
   const long long grid = std::max<long long>(keys ? 2 : 1, std::min(most, nq + nk));
   // Blocks shared out as the rows are.
   const long long qb = keys ? std::min(std::max<long long>(1, grid * H / (H + Hkv)), grid - 1) : grid;

@@ -60,10 +60,11 @@ struct TreeForm {
   bool four;
 };
 
-// CTAs of the streaming kernel an SM holds.
-int tree_ctas(int d, bool four) {
-  return d == 64 ? (four ? TreeCfg<64, true>::kCtasPerSm : TreeCfg<64>::kCtasPerSm)
-                 : (four ? TreeCfg<128, true>::kCtasPerSm : TreeCfg<128>::kCtasPerSm);
+// CTAs of the streaming kernels an SM holds.
+int tree_ctas(int d) { return d == 64 ? TreeCfg<64>::kCtasPerSm : TreeCfg<128>::kCtasPerSm; }
+int tree4_ctas(int d, int rows) {
+  return rows == 8 ? (d == 64 ? Tree4Cfg<64, 1>::kCtasPerSm : Tree4Cfg<128, 1>::kCtasPerSm)
+                   : (d == 64 ? Tree4Cfg<64, 2>::kCtasPerSm : Tree4Cfg<128, 2>::kCtasPerSm);
 }
 
 bool tree_sizes(int B, int H, int Hkv, int Tq, int Tmax, int d, const TreeForm& form, int sms, TreeSizes* z) {
@@ -72,9 +73,9 @@ bool tree_sizes(int B, int H, int Hkv, int Tq, int Tmax, int d, const TreeForm& 
   const long long R = static_cast<long long>(H / Hkv) * Tq, BHkv = static_cast<long long>(B) * Hkv;
   if (static_cast<long long>(B) * H > INT32_MAX || R > (1 << 24) || Tmax > (1 << 30)) return false;
   z->R = static_cast<int>(R);
-  // (4 bits: blocks of at most 32 rows, the tensor-core kernel's operands being bf16 in shared memory)
+  // (4 bits: blocks of 8 or 16 rows, the tensor-core kernel's operands being bf16 in shared memory)
   const bool is_wide = wide(z->R) && !form.four;
-  z->rows_log2 = form.four ? std::min(block_rows_log2(z->R), 5) : block_rows_log2(z->R);
+  z->rows_log2 = form.four ? (z->R <= 8 ? 3 : 4) : block_rows_log2(z->R);
   z->row_blocks = (z->R + (1 << z->rows_log2) - 1) >> z->rows_log2;
   z->chunk_log2 = is_wide || form.four ? 7 : 6;
   z->min_per = is_wide || form.four ? kMinPerWide : kMinPer;
@@ -87,7 +88,7 @@ bool tree_sizes(int B, int H, int Hkv, int Tq, int Tmax, int d, const TreeForm& 
   if (z->entries * chunks > INT32_MAX - 128) return false;  // (the kernels number them with an int)
   if (z->entries << (z->rows_log2 - 3) > INT32_MAX) return false;
   const long long most = (z->entries * chunks + z->min_per - 1) / z->min_per;
-  const long long fit = static_cast<long long>(sms) * (is_wide ? 1 : tree_ctas(d, form.four));
+  const long long fit = static_cast<long long>(sms) * (is_wide ? 1 : form.four ? tree4_ctas(d, 1 << z->rows_log2) : tree_ctas(d));
   const long long per = std::max<long long>(z->min_per, (z->entries * chunks + fit - 1) / fit);  // a stretch's
   z->solo = z->entries <= fit && chunks <= per + (form.four ? kJoinChunksFour : join_chunks(is_wide, d)) &&
             chunks <= (form.four ? kSoloChunksFour : is_wide ? kSoloChunksWide : kSoloChunks);
@@ -193,17 +194,14 @@ int fwd_tree(const void* q, const void* k_cache, const void* v_cache, const void
   a.stream = static_cast<cudaStream_t>(stream);
   const int mod = mod_bits(softcap, slopes), BHkv = B * Hkv;
   const int box = 1 << z.chunk_log2;
-  if (form.four) {
-    a.p.k4 = static_cast<const uint8_t*>(k_cache);
-    a.p.v4 = static_cast<const uint8_t*>(v_cache);
-    a.p.ks = static_cast<const __nv_bfloat16*>(k_scales);
-    a.p.vs = static_cast<const __nv_bfloat16*>(v_scales);
-  } else if (!encode_map(enc, &a.tm_k, k_cache, Tmax, d, BHkv, box) || !encode_map(enc, &a.tm_v, v_cache, Tmax, d, BHkv, box)) {
+  if (!form.four && (!encode_map(enc, &a.tm_k, k_cache, Tmax, d, BHkv, box) || !encode_map(enc, &a.tm_v, v_cache, Tmax, d, BHkv, box)))
     return FA_ERR_INVALID_ARG;
-  }
   cudaError_t e;
   if (form.four) {
-    e = (d == 64) ? fa::launch_tree_four_d64(a, 1 << z.rows_log2, mod) : fa::launch_tree_four_d128(a, 1 << z.rows_log2, mod);
+    const fa::Tree4Launch f{{a.p, static_cast<const uint8_t*>(k_cache), static_cast<const uint8_t*>(v_cache),
+                             static_cast<const __nv_bfloat16*>(k_scales), static_cast<const __nv_bfloat16*>(v_scales)},
+                            a.grid, a.stream};
+    e = (d == 64) ? fa::launch_tree4_d64(f, 1 << z.rows_log2, mod) : fa::launch_tree4_d128(f, 1 << z.rows_log2, mod);
   } else if (fa::wide(z.R)) {
     fa::FwdLaunch f;
     f.p = fa::FwdParams{};

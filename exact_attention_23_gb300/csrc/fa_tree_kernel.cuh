@@ -21,13 +21,8 @@
 // sum and O of its own, merged once per segment through shared memory. K is read as B fragments by
 // ldmatrix, V by ldmatrix.trans, both conflict-free out of the 128-byte-swizzled boxes that TMA
 // writes.
-//
-// FOUR: the cache is held in 4 bits (fa_four.cuh). Chunks are 128 keys, whose codes and scales are two
-// contiguous pieces each of K and V; a thread reads the words that hold its fragments and makes the bf16
-// operands of the same products from them, a shift, a mask and a fused multiply-add a pair of values.
 #pragma once
 
-#include "fa_four.cuh"
 #include "fa_fwd_kernel.cuh"
 #include "fa_mod.cuh"
 #include "fa_tree_walk.cuh"
@@ -49,22 +44,18 @@ struct TreeParams {
   CapFactors cap;
   float scale_log2;
   int R;                   // query rows a key head: (H / Hkv) · Tq
-  const uint8_t *k4, *v4;  // FOUR: [BHkv][Tmax][D/2] codes
-  const __nv_bfloat16 *ks, *vs;  // [BHkv][Tmax][D/32] scales
 };
 
+constexpr int kTreeKeys = 64;        // keys per chunk
 constexpr int kTreeThreads = 128;    // compute threads
 constexpr int kTreeBlock = kTreeThreads + 32;
 constexpr float kTreeTau = 8.0f;     // lazy rescale, as the other forward kernels
 
-template <int D, bool FOUR = false>
+template <int D>
 struct TreeCfg {
-  static constexpr int kChunkLog2 = FOUR ? 7 : 6;
-  static constexpr int kKeys = 1 << kChunkLog2;            // keys per chunk
-  static constexpr int kBoxBytes = kKeys * 128;            // 64 keys × 64 columns
-  static constexpr int kCodes = kKeys * D / 2;             // FOUR: a tile's codes, in front of its scales
-  static constexpr int kTile = FOUR ? kCodes + kKeys * D / 16 : kBoxBytes * (D / 64);  // K or V of a chunk
-  static constexpr int kStages = FOUR ? (D == 64 ? 10 : 8) : (D == 64) ? 7 : 5;        // K or V tiles in flight
+  static constexpr int kBoxBytes = kTreeKeys * 128;        // 64 keys × 64 columns
+  static constexpr int kTile = kBoxBytes * (D / 64);       // K or V of a chunk
+  static constexpr int kStages = (D == 64) ? 7 : 5;        // K or V tiles in flight
   static constexpr int kCtasPerSm = (D == 64) ? 3 : 2;
   // the key groups' merge: three 16-row fp32 O blocks at most
   static constexpr int kMergeOff = kStages * kTile;
@@ -79,16 +70,6 @@ __device__ __forceinline__ void ldsm4_t(uint32_t addr, uint32_t (&r)[4]) {
   asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
                : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(addr) : "memory");
 }
-// N = 1, 2 or 4 words of shared memory.
-template <int N>
-__device__ __forceinline__ void lds_words(uint32_t addr, uint32_t (&r)[N]) {
-  if constexpr (N == 1) asm volatile("ld.shared.b32 %0, [%1];" : "=r"(r[0]) : "r"(addr) : "memory");
-  else if constexpr (N == 2)
-    asm volatile("ld.shared.v2.b32 {%0,%1}, [%2];" : "=r"(r[0]), "=r"(r[1]) : "r"(addr) : "memory");
-  else
-    asm volatile("ld.shared.v4.b32 {%0,%1,%2,%3}, [%4];" : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
-                 : "r"(addr) : "memory");
-}
 __device__ __forceinline__ void mma16816(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
   asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
       "{%0,%1,%2,%3};"
@@ -97,13 +78,12 @@ __device__ __forceinline__ void mma16816(float (&c)[4], const uint32_t (&a)[4], 
 }
 
 template <int D, int RG, int MOD>
-__global__ void __launch_bounds__(kTreeBlock, TreeCfg<D, (MOD & kModFour) != 0>::kCtasPerSm)
+__global__ void __launch_bounds__(kTreeBlock, TreeCfg<D>::kCtasPerSm)
     fa_tree_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
                    const TreeParams p) {
-  constexpr bool kFour = (MOD & kModFour) != 0;
-  using C = TreeCfg<D, kFour>;
+  using C = TreeCfg<D>;
   constexpr int KG = 4 / RG;               // key groups
-  constexpr int NK = C::kKeys / KG;       // keys of a chunk a warp takes
+  constexpr int NK = kTreeKeys / KG;       // keys of a chunk a warp takes
   constexpr int NT = NK / 8;               // score tiles of 16 rows × 8 keys
   constexpr int kRows = RG * 16;
   constexpr int kDT = D / 8;               // output tiles of 16 rows × 8 columns
@@ -132,7 +112,7 @@ __global__ void __launch_bounds__(kTreeBlock, TreeCfg<D, (MOD & kModFour) != 0>:
 
   if (warp == 4) {
     // ---------------------------------------------------------------- producer
-    if (!kFour && lane == 0) {
+    if (lane == 0) {
       tma_prefetch_desc(&tm_k);
       tma_prefetch_desc(&tm_v);
     }
@@ -150,20 +130,11 @@ __global__ void __launch_bounds__(kTreeBlock, TreeCfg<D, (MOD & kModFour) != 0>:
         }
         if (lane == 0) {
           uint8_t* dst = sm + st * C::kTile;
-          const int key0 = ((u >> 1) + ((u >> 1) < sc ? 0 : gap)) * C::kKeys;
-          if constexpr (kFour) {
-            // (Tmax is a multiple of 8: sizes and addresses are multiples of 16 bytes)
-            const int rows = min(C::kKeys, p.list.Tmax - key0);
-            const size_t at = static_cast<size_t>(bh) * p.list.Tmax + key0;
-            mbar_arrive_expect_tx(&full[st], rows * (D / 2 + D / 16));
-            bulk_load(dst, ((u & 1) ? p.v4 : p.k4) + at * (D / 2), rows * (D / 2), &full[st]);
-            bulk_load(dst + C::kCodes, ((u & 1) ? p.vs : p.ks) + at * (D / 32), rows * (D / 16), &full[st]);
-          } else {
-            mbar_arrive_expect_tx(&full[st], C::kTile);
+          mbar_arrive_expect_tx(&full[st], C::kTile);
 #pragma unroll
-            for (int x = 0; x < D / 64; ++x)
-              tma_load_3d(dst + x * C::kBoxBytes, (u & 1) ? &tm_v : &tm_k, &full[st], x * 64, key0, bh);
-          }
+          for (int x = 0; x < D / 64; ++x)
+            tma_load_3d(dst + x * C::kBoxBytes, (u & 1) ? &tm_v : &tm_k, &full[st], x * 64,
+                        ((u >> 1) + ((u >> 1) < sc ? 0 : gap)) * kTreeKeys, bh);
         }
         __syncwarp();
       }
@@ -215,16 +186,14 @@ __global__ void __launch_bounds__(kTreeBlock, TreeCfg<D, (MOD & kModFour) != 0>:
     }
     uint32_t qf[D / 16][4];
     {
-      // (FOUR: 16 dimensions in the order that the keys' words have them in)
-      constexpr int kNext = kFour ? 2 : 8;
-      const __nv_bfloat16* q0 = p.q + (static_cast<size_t>(bh) * p.R + r0) * D + (kFour ? 2 : 1) * qc;
+      const __nv_bfloat16* q0 = p.q + (static_cast<size_t>(bh) * p.R + r0) * D + qc;
       const __nv_bfloat16* q1 = q0 + 8 * D;
 #pragma unroll
       for (int k = 0; k < D / 16; ++k) {
         qf[k][0] = live[0] ? *reinterpret_cast<const uint32_t*>(q0 + k * 16) : 0u;
         qf[k][1] = live[1] ? *reinterpret_cast<const uint32_t*>(q1 + k * 16) : 0u;
-        qf[k][2] = live[0] ? *reinterpret_cast<const uint32_t*>(q0 + k * 16 + kNext) : 0u;
-        qf[k][3] = live[1] ? *reinterpret_cast<const uint32_t*>(q1 + k * 16 + kNext) : 0u;
+        qf[k][2] = live[0] ? *reinterpret_cast<const uint32_t*>(q0 + k * 16 + 8) : 0u;
+        qf[k][3] = live[1] ? *reinterpret_cast<const uint32_t*>(q1 + k * 16 + 8) : 0u;
       }
     }
     float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
@@ -237,30 +206,15 @@ __global__ void __launch_bounds__(kTreeBlock, TreeCfg<D, (MOD & kModFour) != 0>:
       if (ok && !mbar_wait_warp(&full[stk], (n / C::kStages) & 1, wc)) ok = false;
       if (!ok) continue;  // (walk on: the merges below are joined by every warp)
       const uint32_t kt = ring + stk * C::kTile, vt = ring + stv * C::kTile;
-      const int key0 = (c + (!kWin || c < sc ? 0 : gap)) * C::kKeys + kg * NK;  // this warp's first key
+      const int key0 = (c + (!kWin || c < sc ? 0 : gap)) * kTreeKeys + kg * NK;  // this warp's first key
       // ---- S = Q·Kᵀ
       // (32 dimensions of every key at a time: the fragments' loads stand together in front of
       // products that do not wait for one another)
       float s[NT][4];
 #pragma unroll
       for (int j = 0; j < NT; ++j) s[j][0] = s[j][1] = s[j][2] = s[j][3] = 0.f;
-      if constexpr (kFour) {
 #pragma unroll
-        for (int j = 0; j < NT; ++j) {
-          const uint32_t row = kg * NK + j * 8 + qr;
-          uint32_t w[D / 32], sc2[D / 64];  // this thread's words of a key, and the key's scales
-          lds_words(kt + row * (D / 2) + (lane & 3) * (D / 8), w);
-          lds_words(kt + C::kCodes + row * (D / 16), sc2);
-#pragma unroll
-          for (int x = 0; x < D / 32; ++x) {
-            const FourScale f = four_scale(__byte_perm(sc2[x / 2], 0u, x & 1 ? 0x3232 : 0x1010));
-            mma16816(s[j], qf[2 * x], four_pair<0>(w[x], f), four_pair<1>(w[x], f));
-            mma16816(s[j], qf[2 * x + 1], four_pair<2>(w[x], f), four_pair<3>(w[x], f));
-          }
-        }
-      }
-#pragma unroll
-      for (int k = 0; k < (kFour ? 0 : D / 32); ++k) {
+      for (int k = 0; k < D / 32; ++k) {
         uint32_t b[NT][4];
         const int ch = (k & 1) * 4 + (lane >> 3);
 #pragma unroll
@@ -402,7 +356,7 @@ __global__ void __launch_bounds__(kTreeBlock, TreeCfg<D, (MOD & kModFour) != 0>:
       const bool cut = key0 + NK > keys || (kWin && key0 < lo_all && key0 + NK > p.list.sinks);
 #pragma unroll
       for (int k = 0; k < NT / 2; ++k) {
-        const int row = kg * NK + k * 16 + (kFour ? qc : (lane & 7) + ((lane >> 3) & 1) * 8);
+        const int row = kg * NK + k * 16 + (lane & 7) + ((lane >> 3) & 1) * 8;
         uint32_t keep[2] = {0xFFFFFFFFu, 0xFFFFFFFFu};
         if (cut) {
 #pragma unroll
@@ -412,34 +366,8 @@ __global__ void __launch_bounds__(kTreeBlock, TreeCfg<D, (MOD & kModFour) != 0>:
             keep[h] = (used(key) ? 0x0000FFFFu : 0u) | (used(key + 1) ? 0xFFFF0000u : 0u);
           }
         }
-        if constexpr (kFour) {
-          // keys row, row + 1 and row + 8, row + 9: column qr of every eighth dimension
-          uint32_t sc2[4][D / 64];
 #pragma unroll
-          for (int e = 0; e < 4; ++e)
-            lds_words(vt + C::kCodes + (row + (e & 1) + (e >> 1) * 8) * (D / 16), sc2[e]);
-#pragma unroll
-          for (int h = 0; h < D / 64; ++h) {
-            uint32_t w[4][1];
-#pragma unroll
-            for (int e = 0; e < 4; ++e)
-              lds_words(vt + (row + (e & 1) + (e >> 1) * 8) * (D / 2) + (8 * h + qr) * 4, w[e]);
-#pragma unroll
-            for (int g = 0; g < 2; ++g) {  // dimensions 64h + 32g …
-              const uint32_t half = g ? 0x7632 : 0x5410;
-              const uint32_t u0 = __byte_perm(w[0][0], w[1][0], half), u1 = __byte_perm(w[2][0], w[3][0], half);
-              const FourScale f0 = four_scale(__byte_perm(sc2[0][h], sc2[1][h], half) & keep[0]);
-              const FourScale f1 = four_scale(__byte_perm(sc2[2][h], sc2[3][h], half) & keep[1]);
-              float(*oo)[4] = o + 8 * h + 4 * g;
-              mma16816(oo[0], pf[k], four_pair<0>(u0, f0), four_pair<0>(u1, f1));
-              mma16816(oo[1], pf[k], four_pair<1>(u0, f0), four_pair<1>(u1, f1));
-              mma16816(oo[2], pf[k], four_pair<2>(u0, f0), four_pair<2>(u1, f1));
-              mma16816(oo[3], pf[k], four_pair<3>(u0, f0), four_pair<3>(u1, f1));
-            }
-          }
-        }
-#pragma unroll
-        for (int x0 = 0; x0 < (kFour ? 0 : D / 16); x0 += 4) {
+        for (int x0 = 0; x0 < D / 16; x0 += 4) {
           uint32_t b[4][4];
 #pragma unroll
           for (int x = 0; x < 4; ++x) {
