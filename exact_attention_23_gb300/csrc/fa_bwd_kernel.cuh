@@ -147,6 +147,11 @@ struct BwdModParams {
   const int2* whole;    // [B][n_kt] (largest lo, smallest hi) over a tile's 128 rows: hi is 0 with padding
   const float* slopes;  // [H]
   float* part_out;      // parts > 1: [2][parts][B·Hkv][T][D], dK (scaled) then dV
+  int Hkv;              // key heads
+  int group;            // query heads per key head
+  int parts;            // parts of a group (BH then counts B·Hkv·parts)
+  CapFactors cap;       // (CAP)
+  int causal;           // without rows
   // SINK: `units` are [B][n_rec][2], the second (slot of a cut walk's piece or −1, whether the key tile has
   // sinks beyond a window, 0, 0); the pieces' sums go to slots and fa_bwd_pieces_kernel adds them in order.
   const int2* sink_rows;  // [B][T_pad] a row's visible sinks, an interval in front of its rows entry
@@ -154,11 +159,6 @@ struct BwdModParams {
   float* piece_out;     // [2][B·Hkv·parts][n_slots][128][D], dK (scaled) then dV
   int n_rec;            // walks a key head's part (n_kt, or with pieces)
   int n_cut, n_slots;
-  int Hkv;              // key heads
-  int group;            // query heads per key head
-  int parts;            // parts of a group (BH then counts B·Hkv·parts)
-  CapFactors cap;       // (CAP)
-  int causal;           // without rows
 };
 
 struct BwdParams {

@@ -129,8 +129,8 @@ static_assert(sizeof(Bars1) <= 512, "barrier block");
 // TREE (with MOD): the CTA's stretch of all (sequence, key head, row block, key chunk) is walked
 // segment by segment instead of the list; a segment is a unit of 128 of a key head's R rows.
 struct NoSegments {
-  __device__ __forceinline__ void begin(const TreeList&) {}
-  __device__ __forceinline__ bool next(const TreeList&) { return false; }
+  __device__ __forceinline__ void begin(const TreeList&, const TreeReach&) {}
+  __device__ __forceinline__ bool next(const TreeList&, const TreeReach&) { return false; }
 };
 template <int MOD>
 using SegmentsOf = std::conditional_t<(MOD & kModTree) != 0, TreeSegments<(MOD & kModSink) != 0>, NoSegments>;
@@ -149,7 +149,7 @@ __device__ __forceinline__ Unit unit1_of(const FwdParams& p, int L, const Segmen
     u.last[0] = sg.b;
     u.last[1] = __ldg(p.mod.list.ctx_len + sg.b);
     u.mh = tree_keys(p.mod.list, u.last[1]);
-    if constexpr ((MOD & kModSink) != 0) tree_window(p.mod.list, u.last[1], &u.sb[0], &u.se[0]);
+    if constexpr ((MOD & kModSink) != 0) tree_window(p.mod.list, p.mod.reach, u.last[1], &u.sb[0], &u.se[0]);
     return u;
   } else if constexpr (MOD != 0) {
     Unit u;
@@ -172,7 +172,7 @@ __device__ __forceinline__ Unit unit1_of(const FwdParams& p, int L, const Segmen
     u.n_steps = max(0, u.ke - u.kb);
     if constexpr ((MOD & kModSink) != 0) {
       const int b = static_cast<int>(p.mod.div_h.div(static_cast<uint32_t>(u.bh)));
-      const int2 k = __ldg(p.mod.sink_units + static_cast<size_t>(b) * p.n_qt + pos);
+      const int2 k = p.mod.sink_units ? __ldg(p.mod.sink_units + static_cast<size_t>(b) * p.n_qt + pos) : make_int2(0, 0);
       u.sb[0] = k.x;
       u.se[0] = k.y;
       u.n_steps += k.y - k.x;
@@ -264,11 +264,11 @@ __global__ void __launch_bounds__(Cfg1<D, (MOD & kModRef) != 0>::kThreads, 1)
     int g = 0, qn = 0, ql = 0;
     bool ok = true;
     SegmentsOf<MOD> sg;
-    if constexpr (kTree) sg.begin(p.mod.list);
+    if constexpr (kTree) sg.begin(p.mod.list, p.mod.reach);
     for (int r = 0; ok && (kTree || r * grid < p.total_units); ++r) {
       const int L = unit_index(r, cta, grid);
       if (!kTree && L >= p.total_units) continue;
-      if (kTree && !sg.next(p.mod.list)) break;
+      if (kTree && !sg.next(p.mod.list, p.mod.reach)) break;
       const Unit u = unit1_of<CAUSAL, GEN, MOD>(p, L, sg);
       const int qb = qn & 1;
       if (qn >= 2 && !mbar_wait_warp(&bars->q_empty[qb], ((qn >> 1) - 1) & 1, wc)) { ok = false; break; }
@@ -335,11 +335,11 @@ __global__ void __launch_bounds__(Cfg1<D, (MOD & kModRef) != 0>::kThreads, 1)
       const uint32_t k_base = smem_u32(smem + C::kKOff);
       int g = 0, qn = 0;
       SegmentsOf<MOD> sg;
-      if constexpr (kTree) sg.begin(p.mod.list);
+      if constexpr (kTree) sg.begin(p.mod.list, p.mod.reach);
       for (int r = 0; ok && (kTree || r * grid < p.total_units); ++r) {
         const int L = unit_index(r, cta, grid);
         if (!kTree && L >= p.total_units) continue;
-        if (kTree && !sg.next(p.mod.list)) break;
+        if (kTree && !sg.next(p.mod.list, p.mod.reach)) break;
         const Unit u = unit1_of<CAUSAL, GEN, MOD>(p, L, sg);
         const int qb = qn & 1;
         if (!mbar_wait_warp(&bars->q_full[qb], (qn >> 1) & 1, wc)) { ok = false; break; }
@@ -380,11 +380,11 @@ __global__ void __launch_bounds__(Cfg1<D, (MOD & kModRef) != 0>::kThreads, 1)
       const uint32_t v_base = smem_u32(smem + C::kVOff);
       int g = 0, nunits = 0;
       SegmentsOf<MOD> sg;
-      if constexpr (kTree) sg.begin(p.mod.list);
+      if constexpr (kTree) sg.begin(p.mod.list, p.mod.reach);
       for (int r = 0; ok && (kTree || r * grid < p.total_units); ++r) {
         const int L = unit_index(r, cta, grid);
         if (!kTree && L >= p.total_units) continue;
-        if (kTree && !sg.next(p.mod.list)) break;
+        if (kTree && !sg.next(p.mod.list, p.mod.reach)) break;
         const Unit u = unit1_of<CAUSAL, GEN, MOD>(p, L, sg);
         for (int j = 0; j < u.n_steps; ++j, ++g) {
           const int st = g % C::kStages;
@@ -413,8 +413,8 @@ __global__ void __launch_bounds__(Cfg1<D, (MOD & kModRef) != 0>::kThreads, 1)
             if (used < kBlockN) zero_rows(used, kBlockN);
             if constexpr (kSink) {
               // … and so may those between the sinks and every token's window.
-              const int r0 = max(p.mod.list.sinks - vt * kBlockN, 0);
-              const int r1 = min(min(tree_window_start(p.mod.list, u.last[1]) - vt * kBlockN, used), kBlockN);
+              const int r0 = max(p.mod.reach.sinks - vt * kBlockN, 0);
+              const int r1 = min(min(tree_window_start(p.mod.list, p.mod.reach, u.last[1]) - vt * kBlockN, used), kBlockN);
               if (r0 < r1) zero_rows(r0, r1);
             }
           }
@@ -777,11 +777,11 @@ __global__ void __launch_bounds__(Cfg1<D, (MOD & kModRef) != 0>::kThreads, 1)
     };
 
     SegmentsOf<MOD> sg;
-    if constexpr (kTree) sg.begin(p.mod.list);
+    if constexpr (kTree) sg.begin(p.mod.list, p.mod.reach);
     for (int r = 0; kTree || r * grid < p.total_units; ++r) {
       const int L = unit_index(r, cta, grid);
       if (!kTree && L >= p.total_units) continue;
-      if (kTree && !sg.next(p.mod.list)) break;
+      if (kTree && !sg.next(p.mod.list, p.mod.reach)) break;
       const Unit u = unit1_of<CAUSAL, GEN, MOD>(p, L, sg);
       if constexpr (kTree) {
         if (threadIdx.x == 0) sg.note_parts(p.mod.list);
@@ -817,7 +817,7 @@ __global__ void __launch_bounds__(Cfg1<D, (MOD & kModRef) != 0>::kThreads, 1)
         vhi = min(ctx, u.mh);
         if constexpr (kSink) {
           dep = p.mod.mask.depths ? tree_depth(p.mod.mask.depths_of(u.last[0], Tq)[tok]) : tok;
-          vlo = tree_row_start(p.mod.list, ctx, dep);
+          vlo = tree_row_start(p.mod.list, p.mod.reach, ctx, dep);
         }
         if constexpr ((MOD & kModBias) != 0) {
           const int hk = u.bh - u.last[0] * p.mod.list.Hkv;
@@ -831,7 +831,7 @@ __global__ void __launch_bounds__(Cfg1<D, (MOD & kModRef) != 0>::kThreads, 1)
           vlo = r.x;
           vhi = r.y;
           if constexpr (kSink) {
-            const int2 k = __ldg(p.mod.sink_rows + static_cast<size_t>(b) * p.mod.T_pad + q_row);
+            const int2 k = p.mod.sink_rows ? __ldg(p.mod.sink_rows + static_cast<size_t>(b) * p.mod.T_pad + q_row) : make_int2(0, 0);
             slo = k.x;
             shi = k.y;
           }
@@ -910,6 +910,7 @@ __global__ void __launch_bounds__(Cfg1<D, (MOD & kModRef) != 0>::kThreads, 1)
         if (lane == 0) mbar_arrive(&bars->s_free[b]);
         FA1_TRACE(20, j);
         bool fused = false;  // kRef: a step without masks or far scores
+        uint32_t unseen = 0u;  // SINK, not TREE: the 32s of columns that no row of the warp sees, as bits
         if constexpr (MOD != 0) {
           // Capped or biased scores to base-2 exponents in place (fa_mod.cuh); the bias is linear
           // in the key where every key of the step lies at or before the warp's first row (TREE: at or
@@ -991,7 +992,7 @@ __global__ void __launch_bounds__(Cfg1<D, (MOD & kModRef) != 0>::kThreads, 1)
                 // context keys, chain keys and rows of the cache: ranges
                 const int n_see = min(max(min(ctx, u.mh) - (k0 + w * 32), 0), 32);
                 uint32_t word = n_see >= 32 ? 0xFFFFFFFFu : (1u << n_see) - 1u;
-                if constexpr (kSink) word &= ~bits_below(vlo - k0 - w * 32) | bits_below(p.mod.list.sinks - k0 - w * 32);
+                if constexpr (kSink) word &= ~bits_below(vlo - k0 - w * 32) | bits_below(p.mod.reach.sinks - k0 - w * 32);
                 if (pieces) {
                   const int n_keys = min(max(u.mh - (k0 + w * 32), 0), 32);
                   word |= __funnelshift_r(tw[w], tw[w + 1], d0 & 31) & (n_keys >= 32 ? 0xFFFFFFFFu : (1u << n_keys) - 1u);
@@ -1014,13 +1015,13 @@ __global__ void __launch_bounds__(Cfg1<D, (MOD & kModRef) != 0>::kThreads, 1)
                 }
                 if constexpr (kSink) {
                   // Tokens as deep as the window is wide may have outrun others.
-                  if (dw > -32 && __any_sync(0xffffffffu, dep >= p.mod.list.window)) {
+                  if (dw > -32 && __any_sync(0xffffffffu, dep >= p.mod.reach.window)) {
                     const int* at = p.mod.mask.depths ? p.mod.mask.depths_of(u.last[0], Tq) : nullptr;
                     const int dk = min(max(dw + lane, 0), Tq - 1), mine = at ? tree_depth(at[dk]) : dk;
 #pragma unroll 1
                     for (int t = 0; t < 32; ++t) {
                       const int there = __shfl_sync(0xffffffffu, mine, t);
-                      if (dw + t >= 0 && dep - there >= p.mod.list.window && there >= p.mod.list.sinks - ctx)
+                      if (dw + t >= 0 && dep - there >= p.mod.reach.window && there >= p.mod.reach.sinks - ctx)
                         word &= ~(1u << t);
                     }
                   }
@@ -1049,6 +1050,7 @@ __global__ void __launch_bounds__(Cfg1<D, (MOD & kModRef) != 0>::kThreads, 1)
 #pragma unroll
               for (int c0 = 0; c0 < kC; c0 += 32) {
                 const uint32_t seen = bits_of(vl - c0, lim - c0) | bits_of(slo - k0 - c0, shi - k0 - c0);
+                if (!__any_sync(0xffffffffu, seen != 0u)) unseen |= 1u << (c0 / 32);
 #pragma unroll
                 for (int t = 0; t < 32; ++t)
                   if (!((seen >> t) & 1u)) s[c0 + t] = __float_as_uint(-INFINITY);
@@ -1100,9 +1102,9 @@ __global__ void __launch_bounds__(Cfg1<D, (MOD & kModRef) != 0>::kThreads, 1)
         const uint64_t nm2 = f2_pack(-m_use, -m_use);
         uint64_t acc0 = f2_pack(0.f, 0.f), acc1 = acc0;
         uint32_t pk[kC / 2];
-        auto exponentials = [&]<bool FUSED>() {
+        auto exponentials = [&]<bool FUSED>(int t0, int n) {
 #pragma unroll
-          for (int t = 0; t < kC / 2; ++t) {
+          for (int t = t0; t < t0 + n; ++t) {
             const uint64_t s2 = f2_pack(u2f(s[2 * t]), u2f(s[2 * t + 1]));
             uint64_t x2;
             if constexpr (FUSED) x2 = cap2<false>(s2, p.mod.cap);
@@ -1123,9 +1125,19 @@ __global__ void __launch_bounds__(Cfg1<D, (MOD & kModRef) != 0>::kThreads, 1)
 #pragma unroll
             for (int i = 0; i < kC / 32; ++i) raw_top = fmaxf(raw_top, max_s[i]);
           }
-          exponentials.template operator()<kRef>();
+          exponentials.template operator()<kRef>(0, kC / 2);
+        } else if (kSink && !kTree && unseen != 0u) {  // (their weights are 0)
+#pragma unroll
+          for (int t = 0; t < kC / 2; t += 16) {
+            if ((unseen >> (t / 16)) & 1u) {
+#pragma unroll
+              for (int e = 0; e < 16; ++e) pk[t + e] = 0u;
+            } else {
+              exponentials.template operator()<false>(t, 16);
+            }
+          }
         } else {
-          exponentials.template operator()<false>();
+          exponentials.template operator()<false>(0, kC / 2);
         }
         FA1_TRACE(42, j);
         if (any_rescale) {

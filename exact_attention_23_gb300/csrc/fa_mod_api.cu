@@ -622,7 +622,11 @@ int fwd_mod(const void* q, const void* k, const void* v, void* o, float* lse, vo
   // Not with a bias (d64 T4096 204 -> 204, d128 T8192 328 -> 448) or a cap above 60, whose in-place
   // scores do not fit its registers.
   const bool plain = (mod & ~fa::kModRest) == fa::kModOn;
-  const bool pairs = static_cast<long long>((n_t + 1) / 2) * BH * 2 >= 3ll * sms && (plain || (mod & fa::kModRef));
+  // Nor at d = 64 with a short window, whose walks are mostly edges (B1 H12 T16384, one tile -> two: window 256
+  // 54.6 -> 59.1, with four sinks 70.3 -> 76.2; 512 66.7 -> 67.3, 82.7 -> 86.1; 1024 94.6 -> 90.4, 110 -> 111;
+  // 4096 with sinks 256 -> 242; d128 H16 Hkv4 T8192 with sinks 512 87.0 -> 80.5, 1024 111 -> 99).
+  const bool pairs = static_cast<long long>((n_t + 1) / 2) * BH * 2 >= 3ll * sms && (plain || (mod & fa::kModRef)) &&
+                     (window == 0 || d == 128 || window > 512);
   a.p.n_units = pairs ? (n_t + 1) / 2 : n_t;
   a.p.total_units = a.p.n_units * BH;
   a.p.n_kv = n_t;
@@ -669,7 +673,9 @@ int fwd_mod(const void* q, const void* k, const void* v, void* o, float* lse, vo
   const bool short_walks = visible || (causal && T <= 4096);
   const int tight = d == 64 && mod == (fa::kModOn | fa::kModCap | fa::kModRef) && (short_walks || softcap < 25.0f)
                         ? fa::kModTight : 0;
-  if (sinks > 0) {
+  // (a window without sinks: the two-tile kernel has its intervals; the one-tile kernel with sinks skips the
+  // columns that none of a warp's rows sees, T16384 H12 d64 window 256 58.0 -> 54.6 µs)
+  if (window > 0 && (sinks > 0 || !pairs)) {
     const cudaError_t e = pairs ? (d == 64 ? fa::launch_fwd_sink_pairs_d64(a, mod) : fa::launch_fwd_sink_pairs_d128(a, mod))
                                 : (d == 64 ? fa::launch_fwd_sink_d64(a, mod) : fa::launch_fwd_sink_d128(a, mod));
     return e == cudaSuccess ? FA_OK : FA_ERR_LAUNCH;

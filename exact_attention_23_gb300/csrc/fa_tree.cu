@@ -43,7 +43,13 @@ constexpr int kMinPer = 2, kMinPerWide = 1;
 //   wide, d64, 256 rows (5)    8, 4: 9.4 / 8.5, 8: 9.9 / 12.4;  32, 6: 13.7 / 10.9, 12: 14.6 / 16.9;  128, 12: 29.4 / 17.8
 //   d128, 64 rows (4)          4, 4: 9.9 / 9.8, 6: 9.9 / 12.2;  64, 8: 18.3 / 15.3, 16 entries, 8: 12.9 / 14.9
 // Not beyond the chunks measured: stretches share out unequal contexts, a CTA an entry does not.
-int join_chunks(bool wide_rows, int d) { return wide_rows ? (d == 64 ? 5 : 4) : d == 64 ? 7 : 5; }
+//   a window, d64 (10)         192, 18: 19.2 / 17.0, 10: 12.3 / 11.4;  48, 18: 9.4 / 14.1;  384, 18: 27.6 / 23.4
+//                              (its contexts are as unequal, but what is left of them is not)
+//   4 bits (4), 128-key chunks d64: 48, 4: 7.2 / 6.0, 8: 7.5 / 8.7, 12: 10.4 / 11.6;  192, 8: 13.1 / 9.9
+//                              d128: 32, 8: 7.8 / 11.0;  128, 6: 10.9 / 9.2
+int join_chunks(bool wide_rows, int d, bool window) {
+  return wide_rows ? (d == 64 ? 5 : 4) : d == 64 ? (window ? 10 : 7) : 5;
+}
 constexpr int kSoloChunks = 24, kSoloChunksWide = 12;
 constexpr int kJoinChunksFour = 4, kSoloChunksFour = 12;
 
@@ -90,7 +96,7 @@ bool tree_sizes(int B, int H, int Hkv, int Tq, int Tmax, int d, const TreeForm& 
   const long long most = (z->entries * chunks + z->min_per - 1) / z->min_per;
   const long long fit = static_cast<long long>(sms) * (is_wide ? 1 : form.four ? tree4_ctas(d, 1 << z->rows_log2) : tree_ctas(d));
   const long long per = std::max<long long>(z->min_per, (z->entries * chunks + fit - 1) / fit);  // a stretch's
-  z->solo = z->entries <= fit && chunks <= per + (form.four ? kJoinChunksFour : join_chunks(is_wide, d)) &&
+  z->solo = z->entries <= fit && chunks <= per + (form.four ? kJoinChunksFour : join_chunks(is_wide, d, form.window > 0)) &&
             chunks <= (form.four ? kSoloChunksFour : is_wide ? kSoloChunksWide : kSoloChunks);
   if (z->solo) {
     z->grid = z->entries;
@@ -183,8 +189,8 @@ int fwd_tree(const void* q, const void* k_cache, const void* v_cache, const void
   a.p.status = status;
   a.p.timeout_ns = timeout_ns ? timeout_ns : 2000000000ull;
   a.p.list = fa::TreeList{ctx_len, B, Hkv, Tq, Tmax, z.row_blocks, z.min_per, z.chunk_log2, z.solo ? 1 : 0,
-                          z.solo ? nullptr : reinterpret_cast<int2*>(ws + z.parts_off),
-                          form.four && form.window == 0 ? INT32_MAX : form.window, form.sinks};
+                          z.solo ? nullptr : reinterpret_cast<int2*>(ws + z.parts_off)};
+  a.p.reach = fa::TreeReach{form.four && form.window == 0 ? INT32_MAX : form.window, form.sinks};
   a.p.mask = fa::TreeMask{tree, depths, fa::FastDiv::make(static_cast<uint32_t>(Tq)), tree_per_batch != 0,
                           depths_per_batch != 0};
   a.p.cap = cap;
@@ -234,6 +240,7 @@ int fwd_tree(const void* q, const void* k_cache, const void* v_cache, const void
     f.p.mod.cap = cap;
     f.p.mod.list = a.p.list;
     f.p.mod.mask = a.p.mask;
+    f.p.mod.reach = a.p.reach;
     f.grid = a.grid;
     f.stream = a.stream;
     const int fm = fwd_mod_bits(softcap, slopes, nullptr);

@@ -82,16 +82,16 @@ __global__ void __launch_bounds__(kTreeBlock, Tree4Cfg<D, NB>::kCtasPerSm) fa_tr
   pdl_launch_dependents();
   const WaitCtl wc{&abort_flag, p.status, p.timeout_ns};
   TreeSegments<true> sg;
-  sg.begin(p.list);
+  sg.begin(p.list, p.reach);
 
   if (warp == 4) {
     // ---------------------------------------------------------------- producer
     int n = 0;
     bool ok = true;
-    while (ok && sg.next(p.list)) {
+    while (ok && sg.next(p.list, p.reach)) {
       const size_t head = static_cast<size_t>(sg.b) * p.list.Hkv + sg.hk;
       int sc, gap;
-      tree_window(p.list, p.list.ctx_len[sg.b], &sc, &gap);
+      tree_window(p.list, p.reach, p.list.ctx_len[sg.b], &sc, &gap);
       for (int u = 2 * sg.c0; ok && u < 2 * sg.c1; ++u, ++n) {  // K and V tiles in turn
         const int st = n % C::kStages;
         if (n >= C::kStages && !mbar_wait_warp(&empty[st], ((n / C::kStages) - 1) & 1, wc)) {
@@ -127,14 +127,14 @@ __global__ void __launch_bounds__(kTreeBlock, Tree4Cfg<D, NB>::kCtasPerSm) fa_tr
   const float nan = __uint_as_float(0x7FC00000u);
   int n = 0;
   bool ok = true;
-  while (sg.next(p.list)) {
+  while (sg.next(p.list, p.reach)) {
     const int bh = sg.b * p.list.Hkv + sg.hk;
     if (threadIdx.x == 0) sg.note_parts(p.list);
     const int ctx = p.list.ctx_len[sg.b], Tq = p.list.Tq;
     const int keys = tree_keys(p.list, ctx);
     int sc, gap;
-    tree_window(p.list, ctx, &sc, &gap);
-    const int lo_all = tree_window_start(p.list, ctx);
+    tree_window(p.list, p.reach, ctx, &sc, &gap);
+    const int lo_all = tree_window_start(p.list, p.reach, ctx);
     int tok[2 * NB], dep[2 * NB], lo[2 * NB];  // token, depth (as the window takes it), first context key
     float nsl[2 * NB], at[2 * NB];             // (at: positions from the end of the context)
     int lo_max = 0;
@@ -145,7 +145,7 @@ __global__ void __launch_bounds__(kTreeBlock, Tree4Cfg<D, NB>::kCtasPerSm) fa_tr
       tok[i] = r - g * Tq;
       const int d = p.mask.depths ? p.mask.depths_of(sg.b, Tq)[tok[i]] : tok[i];
       dep[i] = tree_depth(d);
-      lo[i] = tree_row_start(p.list, ctx, dep[i]);
+      lo[i] = tree_row_start(p.list, p.reach, ctx, dep[i]);
       lo_max = max(lo_max, lo[i]);
       if constexpr ((MOD & kModBias) != 0) {
         at[i] = static_cast<float>(d);
@@ -253,7 +253,7 @@ __global__ void __launch_bounds__(kTreeBlock, Tree4Cfg<D, NB>::kCtasPerSm) fa_tr
             const int key = key0 + mt * 16 + h * 8 + qr;
 #pragma unroll
             for (int i = 0; i < 2 * NB; ++i)
-              if (key >= p.list.sinks && key < min(lo[i], ctx)) s[mt][i >> 1][2 * h + (i & 1)] = -INFINITY;
+              if (key >= p.reach.sinks && key < min(lo[i], ctx)) s[mt][i >> 1][2 * h + (i & 1)] = -INFINITY;
           }
       }
       // ---- the new tokens' keys: the tree, and their depths in the bias and the window
@@ -280,7 +280,7 @@ __global__ void __launch_bounds__(kTreeBlock, Tree4Cfg<D, NB>::kCtasPerSm) fa_tr
                 if (d >= 0)
                   x += nsl[i] * (fabsf(at[i] - static_cast<float>(place[h])) - fabsf(at[i] - static_cast<float>(d)));
               }
-              if (d >= 0 && (see[h][i] == 0 || (dep[i] - there >= p.list.window && there >= p.list.sinks - ctx))) x = -INFINITY;
+              if (d >= 0 && (see[h][i] == 0 || (dep[i] - there >= p.reach.window && there >= p.reach.sinks - ctx))) x = -INFINITY;
               if (key >= keys) x = -INFINITY;
             }
           }
@@ -334,7 +334,7 @@ __global__ void __launch_bounds__(kTreeBlock, Tree4Cfg<D, NB>::kCtasPerSm) fa_tr
       }
       // Rows behind the last key, and those before every token's window, may hold anything: with a scale of 0
       // they are 0.
-      const bool cut = key0 + 32 > keys || (key0 < lo_all && key0 + 32 > p.list.sinks);
+      const bool cut = key0 + 32 > keys || (key0 < lo_all && key0 + 32 > p.reach.sinks);
 #pragma unroll
       for (int mt = 0; mt < 2; ++mt) {
         const int row = warp * 32 + mt * 16 + qc;  // this thread's keys: row, row + 1, row + 8, row + 9
@@ -346,7 +346,7 @@ __global__ void __launch_bounds__(kTreeBlock, Tree4Cfg<D, NB>::kCtasPerSm) fa_tr
 #pragma unroll
           for (int h = 0; h < 2; ++h) {
             const int key = key0 + mt * 16 + h * 8 + qc;
-            auto used = [&](int k) { return k < keys && !(k >= p.list.sinks && k < lo_all); };
+            auto used = [&](int k) { return k < keys && !(k >= p.reach.sinks && k < lo_all); };
             keep[h] = (used(key) ? 0x0000FFFFu : 0u) | (used(key + 1) ? 0xFFFF0000u : 0u);
           }
         }

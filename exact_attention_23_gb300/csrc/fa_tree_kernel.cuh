@@ -44,6 +44,7 @@ struct TreeParams {
   CapFactors cap;
   float scale_log2;
   int R;                   // query rows a key head: (H / Hkv) · Tq
+  TreeReach reach;         // WINDOW
 };
 
 constexpr int kTreeKeys = 64;        // keys per chunk
@@ -108,7 +109,7 @@ __global__ void __launch_bounds__(kTreeBlock, TreeCfg<D>::kCtasPerSm)
   pdl_launch_dependents();
   const WaitCtl wc{&abort_flag, p.status, p.timeout_ns};
   TreeSegments<kWin> sg;
-  sg.begin(p.list);
+  sg.begin(p.list, p.reach);
 
   if (warp == 4) {
     // ---------------------------------------------------------------- producer
@@ -118,10 +119,10 @@ __global__ void __launch_bounds__(kTreeBlock, TreeCfg<D>::kCtasPerSm)
     }
     int n = 0;
     bool ok = true;
-    while (ok && sg.next(p.list)) {
+    while (ok && sg.next(p.list, p.reach)) {
       const int bh = sg.b * p.list.Hkv + sg.hk;
       int sc = 0, gap = 0;
-      if constexpr (kWin) tree_window(p.list, p.list.ctx_len[sg.b], &sc, &gap);
+      if constexpr (kWin) tree_window(p.list, p.reach, p.list.ctx_len[sg.b], &sc, &gap);
       for (int u = 2 * sg.c0; ok && u < 2 * sg.c1; ++u, ++n) {  // K and V tiles in turn
         const int st = n % C::kStages;
         if (n >= C::kStages && !mbar_wait_warp(&empty[st], ((n / C::kStages) - 1) & 1, wc)) {
@@ -154,7 +155,7 @@ __global__ void __launch_bounds__(kTreeBlock, TreeCfg<D>::kCtasPerSm)
   const float nan = __uint_as_float(0x7FC00000u);
   int n = 0;
   bool ok = true;
-  while (sg.next(p.list)) {
+  while (sg.next(p.list, p.reach)) {
     const int bh = sg.b * p.list.Hkv + sg.hk;
     if (threadIdx.x == 0) sg.note_parts(p.list);
     const int ctx = p.list.ctx_len[sg.b], Tq = p.list.Tq;
@@ -164,8 +165,8 @@ __global__ void __launch_bounds__(kTreeBlock, TreeCfg<D>::kCtasPerSm)
     int dep[2] = {0, 0}, lo[2] = {0, 0};  // WINDOW: the rows' depths, and their first context keys
     int sc = 0, gap = 0, lo_all = 0;
     if constexpr (kWin) {
-      tree_window(p.list, ctx, &sc, &gap);
-      lo_all = tree_window_start(p.list, ctx);
+      tree_window(p.list, p.reach, ctx, &sc, &gap);
+      lo_all = tree_window_start(p.list, p.reach, ctx);
     }
     bool live[2];
     float nsl[2] = {0.f, 0.f}, at[2] = {0.f, 0.f};  // (at: positions from the end of the context)
@@ -177,7 +178,7 @@ __global__ void __launch_bounds__(kTreeBlock, TreeCfg<D>::kCtasPerSm)
       tok[i] = (live[i] ? r : 0) - g * Tq;
       if constexpr (kWin) {
         dep[i] = p.mask.depths ? tree_depth(p.mask.depths_of(sg.b, Tq)[tok[i]]) : tok[i];
-        lo[i] = tree_row_start(p.list, ctx, dep[i]);
+        lo[i] = tree_row_start(p.list, p.reach, ctx, dep[i]);
       }
       if constexpr ((MOD & kModBias) != 0) {
         at[i] = static_cast<float>(p.mask.depths ? p.mask.depths_of(sg.b, Tq)[tok[i]] : tok[i]);
@@ -267,7 +268,7 @@ __global__ void __launch_bounds__(kTreeBlock, TreeCfg<D>::kCtasPerSm)
               const int key = key0 + j * 8 + qc + e;
 #pragma unroll
               for (int i = 0; i < 2; ++i)
-                if (key >= p.list.sinks && key < min(lo[i], ctx)) s[j][2 * i + e] = -INFINITY;
+                if (key >= p.reach.sinks && key < min(lo[i], ctx)) s[j][2 * i + e] = -INFINITY;
             }
         }
       }
@@ -304,7 +305,7 @@ __global__ void __launch_bounds__(kTreeBlock, TreeCfg<D>::kCtasPerSm)
                 }
                 if constexpr (kWin) {
                   const int there = tree_depth(place[j][e]);
-                  if (d >= 0 && dep[i] - there >= p.list.window && there >= p.list.sinks - ctx) x = -INFINITY;
+                  if (d >= 0 && dep[i] - there >= p.reach.window && there >= p.reach.sinks - ctx) x = -INFINITY;
                 }
                 if (key >= keys || (d >= 0 && see[j][e][i] == 0)) x = -INFINITY;
               }
@@ -353,7 +354,7 @@ __global__ void __launch_bounds__(kTreeBlock, TreeCfg<D>::kCtasPerSm)
         continue;
       }
       // rows behind the last key may hold anything: taken as 0 (WINDOW: and those before every token's)
-      const bool cut = key0 + NK > keys || (kWin && key0 < lo_all && key0 + NK > p.list.sinks);
+      const bool cut = key0 + NK > keys || (kWin && key0 < lo_all && key0 + NK > p.reach.sinks);
 #pragma unroll
       for (int k = 0; k < NT / 2; ++k) {
         const int row = kg * NK + k * 16 + (lane & 7) + ((lane >> 3) & 1) * 8;
@@ -362,7 +363,7 @@ __global__ void __launch_bounds__(kTreeBlock, TreeCfg<D>::kCtasPerSm)
 #pragma unroll
           for (int h = 0; h < 2; ++h) {
             const int key = key0 + k * 16 + h * 8 + qc;
-            auto used = [&](int k) { return k < keys && !(kWin && k >= p.list.sinks && k < lo_all); };
+            auto used = [&](int k) { return k < keys && !(kWin && k >= p.reach.sinks && k < lo_all); };
             keep[h] = (used(key) ? 0x0000FFFFu : 0u) | (used(key + 1) ? 0xFFFF0000u : 0u);
           }
         }

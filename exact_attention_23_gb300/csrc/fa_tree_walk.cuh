@@ -25,6 +25,9 @@ struct TreeList {
   int chunk_log2;      // keys a chunk: 1 << chunk_log2
   int solo;            // CTA c takes entry c whole: no partials, no second kernel
   int2* parts;         // [entries] the first stretch that an entry lies in, and their number
+};
+
+struct TreeReach {
   int window, sinks;   // WINDOW: see tree_window
 };
 
@@ -53,28 +56,30 @@ __device__ __forceinline__ int tree_keys(const TreeList& p, int ctx) {
 // first window's start on: list chunk c is chunk c of the cache up to sc and chunk c + gap from there.
 __device__ __forceinline__ int tree_depth(int depth) { return max(depth, 0); }
 // The first row of the context in a token's window, and in any token's.
-__device__ __forceinline__ int tree_row_start(const TreeList& p, int ctx, int depth) {
-  const long long lo = static_cast<long long>(ctx) + depth - p.window + 1;
+__device__ __forceinline__ int tree_row_start(const TreeList& p, const TreeReach& w, int ctx, int depth) {
+  const long long lo = static_cast<long long>(ctx) + depth - w.window + 1;
   return static_cast<int>(min(max(lo, 0ll), static_cast<long long>(p.Tmax)));
 }
-__device__ __forceinline__ int tree_window_start(const TreeList& p, int ctx) { return tree_row_start(p, ctx, 0); }
+__device__ __forceinline__ int tree_window_start(const TreeList& p, const TreeReach& w, int ctx) {
+  return tree_row_start(p, w, ctx, 0);
+}
 // (One chunk stays, whatever is left of the window, so that a sequence with a context has an entry.)
-__device__ __forceinline__ int tree_window(const TreeList& p, int ctx, int* sc, int* gap) {
+__device__ __forceinline__ int tree_window(const TreeList& p, const TreeReach& w, int ctx, int* sc, int* gap) {
   const int size = 1 << p.chunk_log2, keys = tree_keys(p, ctx);
   const int total = (keys + size - 1) >> p.chunk_log2;
-  const int first = min(tree_window_start(p, ctx) >> p.chunk_log2, total - 1);
-  *sc = (min(p.sinks, keys) + size - 1) >> p.chunk_log2;
+  const int first = min(tree_window_start(p, w, ctx) >> p.chunk_log2, total - 1);
+  *sc = (min(w.sinks, keys) + size - 1) >> p.chunk_log2;
   *gap = max(0, first - *sc);
   return total - *gap;
 }
 
 template <bool WINDOW>
-__device__ __forceinline__ int tree_chunks(const TreeList& p, int b) {
+__device__ __forceinline__ int tree_chunks(const TreeList& p, const TreeReach& w, int b) {
   const int ctx = p.ctx_len[b];
   if (ctx < 0) return 0;
   if constexpr (WINDOW) {
     int sc, gap;
-    return tree_window(p, ctx, &sc, &gap);
+    return tree_window(p, w, ctx, &sc, &gap);
   }
   const long long keys = static_cast<long long>(ctx) + p.Tq;
   return static_cast<int>((min(keys, static_cast<long long>(p.Tmax)) + (1 << p.chunk_log2) - 1) >> p.chunk_log2);
@@ -83,9 +88,9 @@ __device__ __forceinline__ int tree_chunks(const TreeList& p, int b) {
 // Of the 32 sequences from b0: this lane's chunks (of one list entry), and the positions up to and
 // with this lane's sequence; whole warp. (Positions fit an int: the host refuses longer lists.)
 template <bool WINDOW>
-__device__ __forceinline__ void tree_scan(const TreeList& p, int b0, int* chunks, int* incl) {
+__device__ __forceinline__ void tree_scan(const TreeList& p, const TreeReach& w, int b0, int* chunks, int* incl) {
   const int lane = threadIdx.x & 31;
-  *chunks = b0 + lane < p.B ? tree_chunks<WINDOW>(p, b0 + lane) : 0;
+  *chunks = b0 + lane < p.B ? tree_chunks<WINDOW>(p, w, b0 + lane) : 0;
   int x = *chunks * p.Hkv * p.row_blocks;
 #pragma unroll
   for (int off = 1; off < 32; off <<= 1) {
@@ -97,10 +102,10 @@ __device__ __forceinline__ void tree_scan(const TreeList& p, int b0, int* chunks
 
 // The list's length; the scan of its last 32 sequences stays in chunks and incl. Whole warp.
 template <bool WINDOW>
-__device__ __forceinline__ int tree_total(const TreeList& p, int* chunks, int* incl) {
+__device__ __forceinline__ int tree_total(const TreeList& p, const TreeReach& w, int* chunks, int* incl) {
   int run = 0;
   for (int b0 = 0; b0 < p.B; b0 += 32) {
-    tree_scan<WINDOW>(p, b0, chunks, incl);
+    tree_scan<WINDOW>(p, w, b0, chunks, incl);
     run += __shfl_sync(0xffffffffu, *incl, 31);
   }
   return run;
@@ -119,18 +124,18 @@ struct TreeSegments {
   // the current segment
   int b, hk, rb, entry, c0, c1;  // sequence, key head, row block, list entry, chunks [c0, c1)
   bool whole;                    // it covers its entry
-  __device__ __forceinline__ void begin(const TreeList& p) {
+  __device__ __forceinline__ void begin(const TreeList& p, const TreeReach& reach) {
     if (p.solo) {
       const int entries = p.Hkv * p.row_blocks;
       at.b = static_cast<int>(blockIdx.x) / entries;
       at.entry0 = at.b * entries;
-      at.chunks = tree_chunks<WINDOW>(p, at.b);
+      at.chunks = tree_chunks<WINDOW>(p, reach, at.b);
       pos = 0;
       end = 1;
       return;
     }
     int n, incl;
-    const int total = tree_total<WINDOW>(p, &n, &incl);
+    const int total = tree_total<WINDOW>(p, reach, &n, &incl);
     per = max(static_cast<int>((total + gridDim.x - 1u) / gridDim.x), p.min_per);
     // (a list shorter than grid · min_per leaves later CTAs nothing)
     pos = static_cast<int>(min(static_cast<long long>(per) * blockIdx.x, static_cast<long long>(total)));
@@ -141,7 +146,7 @@ struct TreeSegments {
     int run = 0, b0 = 0;
     if (p.B > 32) {
       for (; b0 < p.B; b0 += 32) {
-        tree_scan<WINDOW>(p, b0, &n, &incl);
+        tree_scan<WINDOW>(p, reach, b0, &n, &incl);
         const int sum = __shfl_sync(0xffffffffu, incl, 31);
         if (pos < run + sum) break;
         run += sum;
@@ -153,7 +158,7 @@ struct TreeSegments {
     at.entry0 = at.b * p.Hkv * p.row_blocks;
     at.start = run + __shfl_sync(0xffffffffu, incl, w) - at.chunks * p.Hkv * p.row_blocks;
   }
-  __device__ __forceinline__ bool next(const TreeList& p) {
+  __device__ __forceinline__ bool next(const TreeList& p, const TreeReach& reach) {
     if (pos >= end) return false;
     if (p.solo) {  // (a sequence without keys has an empty segment, whose rows it writes)
       pos = 1;
@@ -173,7 +178,7 @@ struct TreeSegments {
       at.entry0 += entries;
       y = pos - at.start;
       ++at.b;
-      at.chunks = tree_chunks<WINDOW>(p, at.b);
+      at.chunks = tree_chunks<WINDOW>(p, reach, at.b);
     }
     const int e = y / at.chunks;
     b = at.b;
