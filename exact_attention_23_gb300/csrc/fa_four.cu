@@ -72,25 +72,23 @@ __global__ void __launch_bounds__(kFourThreads) fa_append4_kernel(const FourPara
     const int t = t0 + i * kRows;
     in[i] = t < p.n ? *reinterpret_cast<const uint4*>(src + t * s.st) : make_uint4(0u, 0u, 0u, 0u);
   }
+  // (rows behind `end` have no place in the cache, or are none)
+  const int end = start < 0 ? 0 : static_cast<int>(min(static_cast<long long>(p.n), static_cast<long long>(p.Tmax) - start));
+  const size_t at = f.head * p.Tmax + static_cast<size_t>(max(start, 0)) + t0;
+  uint8_t* codes = p.codes[f.kv] + at * (D / 2) + four_word<D>(f.kv, x) * 4;
+  __nv_bfloat16* scales = p.scales[f.kv] + at * (D / 32) + (x >> 2);
 #pragma unroll
   for (int i = 0; i < kFourFlight; ++i) {
     float v[8];
     unpack8(in[i], v);
-    uint32_t top = 0u;
-#pragma unroll
-    for (int e = 0; e < 8; ++e) top = max(top, __float_as_uint(v[e]) & 0x7FFFFFFFu);
-    top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
-    top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
-    const float sc = four_scale_of(top);
+    const float sc = four_scale_of(four_top(in[i]));
     uint32_t w = 0x88888888u;  // (zeros, and groups that are no numbers)
     if (sc > 0.f) w = four_codes(v, sc);
     w = f.kv ? four_transpose(w, x & 7) : four_to_key(w, x);
     const int t = t0 + i * kRows;
-    const long long row = static_cast<long long>(start) + t;
-    if (start < 0 || t >= p.n || row >= p.Tmax) continue;
-    const size_t at = f.head * p.Tmax + static_cast<size_t>(row);
-    *reinterpret_cast<uint32_t*>(p.codes[f.kv] + at * (D / 2) + four_word<D>(f.kv, x) * 4) = w;
-    if ((x & 3) == 0) p.scales[f.kv][at * (D / 32) + (x >> 2)] = __float2bfloat16_rn(sc);
+    if (t >= end) continue;
+    *reinterpret_cast<uint32_t*>(codes + i * kRows * (D / 2)) = w;
+    if ((x & 3) == 0) scales[i * kRows * (D / 32)] = __float2bfloat16_rn(sc);
   }
 }
 
@@ -102,17 +100,18 @@ __global__ void __launch_bounds__(kFourThreads) fa_read4_kernel(const FourParams
   const FourBlock f = four_block(p, kRows * kFourFlight);
   const int x = threadIdx.x % kLanes, t0 = f.t0 + threadIdx.x / kLanes;
   const int start = p.start[f.b];
+  const int end = start < 0 ? 0 : static_cast<int>(min(static_cast<long long>(p.n), static_cast<long long>(p.Tmax) - start));
+  const size_t at = f.head * p.Tmax + static_cast<size_t>(max(start, 0)) + t0;
+  const uint8_t* codes = p.codes[f.kv] + at * (D / 2) + four_word<D>(f.kv, x) * 4;
+  const unsigned short* scales = reinterpret_cast<const unsigned short*>(p.scales[f.kv]) + at * (D / 32) + (x >> 2);
   uint32_t w[kFourFlight], s[kFourFlight];  // (a scale twice in a word)
 #pragma unroll
   for (int i = 0; i < kFourFlight; ++i) {
-    const int t = t0 + i * kRows;
-    const long long row = static_cast<long long>(start) + t;
     w[i] = 0u;
     s[i] = 0u;
-    if (start < 0 || t >= p.n || row >= p.Tmax) continue;
-    const size_t at = f.head * p.Tmax + static_cast<size_t>(row);
-    w[i] = *reinterpret_cast<const uint32_t*>(p.codes[f.kv] + at * (D / 2) + four_word<D>(f.kv, x) * 4);
-    s[i] = reinterpret_cast<const unsigned short*>(p.scales[f.kv])[at * (D / 32) + (x >> 2)] * 0x10001u;
+    if (t0 + i * kRows >= end) continue;
+    w[i] = *reinterpret_cast<const uint32_t*>(codes + i * kRows * (D / 2));
+    s[i] = scales[i * kRows * (D / 32)] * 0x10001u;
   }
   __nv_bfloat16* out = (f.kv ? p.v_out : p.k_out) + f.head * p.n * D + x * 8;
 #pragma unroll

@@ -51,21 +51,29 @@ __device__ __forceinline__ float four_scale_of(uint32_t top_bits) {
 }
 
 // Eight values over a scale s, each the nearest whole number, ties to even, plus 8, as a word (number e at bits
-// 4e). x·i + 1.5·2²³ rounds x·i to a whole number in the sum's lowest bits; i a little below 1/s and a
-// little above it give the same one except where x / s lies half-way between two (an eight-bit over a five-bit
-// number comes no nearer to half-way than 2⁻¹¹): then they give both, and the even one is taken.
+// 4e). The quotient is x·(1/s) with 1/s in two parts, within 2⁻²⁴ of itself before the addition of
+// 1.5·2²³ + 8, in whose lowest bits it becomes a whole number: so a quotient half-way between two numbers,
+// which fp32 has, is found exactly (an eight-bit over a five-bit number comes no nearer to half-way than
+// 2⁻¹¹ otherwise). All on the multiply-add pipe; the bits are gathered there too.
 __device__ __forceinline__ uint32_t four_codes(const float* v, float s) {
   float inv;
-  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(inv) : "f"(s));  // within 2⁻²³
-  const float lo = inv * (1.0f - 0x1p-21f), hi = inv * (1.0f + 0x1p-21f);
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(inv) : "f"(s));
+  const float rest = fmaf(-s, inv, 1.0f) * inv;
   constexpr float kRound = 12582912.0f + 8.0f;  // bits 0x4B400008
   uint32_t w = 0u;
 #pragma unroll
-  for (int e = 7; e >= 0; --e) {
-    const uint32_t a = __float_as_uint(fmaf(v[e], lo, kRound)), b = __float_as_uint(fmaf(v[e], hi, kRound));
-    w = w * 16u + ((a & 1u) ? b : a);
-  }
+  for (int e = 7; e >= 0; --e) w = w * 16u + __float_as_uint(fmaf(v[e], inv, v[e] * rest) + kRound);
   return w - 0x4B400000u * 0x11111111u;  // (0x4B400000 in every place)
+}
+// The bits of the largest magnitude among eight bf16 values and those of the other three lanes of a group; a
+// NaN's where there is one.
+__device__ __forceinline__ uint32_t four_top(const uint4& x) {
+  auto top = [](__nv_bfloat162 a, __nv_bfloat162 b) { return __hmax2_nan(a, b); };
+  __nv_bfloat162 m = top(top(__habs2(as_bf162(x.x)), __habs2(as_bf162(x.y))), top(__habs2(as_bf162(x.z)), __habs2(as_bf162(x.w))));
+#pragma unroll
+  for (int off = 1; off <= 2; off <<= 1) m = top(m, as_bf162(__shfl_xor_sync(0xffffffffu, *reinterpret_cast<const uint32_t*>(&m), off)));
+  const uint32_t u = *reinterpret_cast<const uint32_t*>(&m);
+  return max(u << 16, u & 0xFFFF0000u);
 }
 
 // Eight lanes' words as an 8 × 8 matrix of codes (lane x, nibble n), transposed.

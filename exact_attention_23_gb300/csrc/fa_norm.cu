@@ -53,8 +53,8 @@ struct NormParams {
 };
 
 constexpr int kNormThreads = 128;
-constexpr int kNormPerSm = 5;
-constexpr int kNormFlight = 2;   // heads whose loads a thread keeps in flight
+constexpr int kNormPerSm = 8;
+constexpr int kNormFlight = 1;   // heads whose loads a thread keeps in flight
 constexpr int kNormBackPerSm = 4;
 constexpr int kNormBlocks = 608;  // of the backward, at most (the workspace's rows)
 
@@ -99,24 +99,37 @@ __device__ __forceinline__ uint4 pack8(const float* v) {
                     pack_bf16x2(v[6], v[7]));
 }
 
-__device__ __forceinline__ void weights16(const float* w, const Unit16& at, float* v) {
-#pragma unroll
-  for (int e = 0; e < 8; e += 4) {
-    *reinterpret_cast<float4*>(v + e) = *reinterpret_cast<const float4*>(w + at.c0 + e);
-    *reinterpret_cast<float4*>(v + 8 + e) = *reinterpret_cast<const float4*>(w + at.c1 + e);
+// Pair e of the sixteen bf16 values of two vectors, as fp32.
+__device__ __forceinline__ uint64_t pair_of(const uint4& a, const uint4& b, int e) {
+  const uint4& v = e < 4 ? a : b;
+  const uint32_t x = e % 4 == 0 ? v.x : e % 4 == 1 ? v.y : e % 4 == 2 ? v.z : v.w;
+  return f2_pack(__uint_as_float(x << 16), __uint_as_float(x & 0xFFFF0000u));
+}
+
+// Where dimension c of a weight lies in shared memory: each unit's 16 values are four vectors whose
+// neighbours are the next units', so that the lanes of a row read without bank conflicts.
+template <int D, bool INTER>
+__device__ __forceinline__ int weight_at(int c, int rot_units) {
+  int u = c / 16, e = c % 16;
+  if (!INTER && c < 16 * rot_units) {
+    const int half = c >= 8 * rot_units;
+    u = c / 8 - (half ? rot_units : 0);
+    e = c % 8 + 8 * half;
   }
+  return ((e / 4) * (D / 16) + u) * 4 + e % 4;
 }
 
 template <int D, bool INTER, bool APPEND>
 __global__ void __launch_bounds__(kNormThreads, kNormPerSm) fa_norm_kernel(const NormParams p) {
   __shared__ unsigned long long turns[64];
-  __shared__ float weight[2][D];
+  __shared__ __align__(16) float weight[2][D];
   pdl_wait();
   pdl_launch_dependents();
   if (threadIdx.x < 8 * p.rot_units) turns[threadIdx.x] = turns_of(p.inv_freq[threadIdx.x]);
   if (threadIdx.x < D) {
-    weight[0][threadIdx.x] = p.wq[threadIdx.x];
-    if (p.Hkv > 0) weight[1][threadIdx.x] = p.wk[threadIdx.x];
+    const int at = weight_at<D, INTER>(threadIdx.x, p.rot_units);
+    weight[0][at] = p.wq[threadIdx.x];
+    if (p.Hkv > 0) weight[1][at] = p.wk[threadIdx.x];
   }
   __syncthreads();
   constexpr int kUnits = D / 16;
@@ -161,17 +174,18 @@ __global__ void __launch_bounds__(kNormThreads, kNormPerSm) fa_norm_kernel(const
       x0[i] = *reinterpret_cast<const uint4*>(src + at.c0);
       x1[i] = *reinterpret_cast<const uint4*>(src + at.c1);
     }
+    // (on pairs of neighbouring dimensions)
     float r[kNormFlight];
 #pragma unroll
     for (int i = 0; i < kNormFlight; ++i) {
-      float v[16], s0 = 0.f, s1 = 0.f;
-      unpack8(x0[i], v);
-      unpack8(x1[i], v + 8);
+      uint64_t ss = f2_pack(0.f, 0.f);
 #pragma unroll
       for (int e = 0; e < 8; ++e) {
-        s0 = fmaf(v[e], v[e], s0);
-        s1 = fmaf(v[e + 8], v[e + 8], s1);
+        const uint64_t v = pair_of(x0[i], x1[i], e);
+        ss = f2_fma(v, v, ss);
       }
+      float s0, s1;
+      f2_unpack(ss, s0, s1);
       r[i] = s0 + s1;
     }
 #pragma unroll
@@ -184,12 +198,14 @@ __global__ void __launch_bounds__(kNormThreads, kNormPerSm) fa_norm_kernel(const
       const bool is_q = h < p.H, is_k = !is_q && h < p.H + p.Hkv;
       uint4 y0 = x0[i], y1 = x1[i];
       if (live && (is_q || is_k)) {
-        float v[16], w[16];
-        unpack8(x0[i], v);
-        unpack8(x1[i], v + 8);
-        weights16(weight[is_q ? 0 : 1], at, w);
+        float v[16];
+        const uint64_t r2 = f2_pack(r[i], r[i]);
 #pragma unroll
-        for (int e = 0; e < 16; ++e) v[e] = v[e] * r[i] * w[e];
+        for (int j = 0; j < 4; ++j) {
+          const float4 w = *reinterpret_cast<const float4*>(&weight[is_q ? 0 : 1][(j * kUnits + u) * 4]);
+          f2_unpack(f2_mul(f2_mul(pair_of(x0[i], x1[i], 2 * j), r2), f2_pack(w.x, w.y)), v[4 * j], v[4 * j + 1]);
+          f2_unpack(f2_mul(f2_mul(pair_of(x0[i], x1[i], 2 * j + 1), r2), f2_pack(w.z, w.w)), v[4 * j + 2], v[4 * j + 3]);
+        }
         if (at.turn) turn16<INTER>(v, cs, sn);
         y0 = pack8(v);
         y1 = pack8(v + 8);
@@ -215,13 +231,13 @@ __global__ void __launch_bounds__(kNormThreads, kNormPerSm) fa_norm_kernel(const
 template <int D, bool INTER>
 __global__ void __launch_bounds__(kNormThreads, kNormBackPerSm) fa_norm_bwd_kernel(const NormParams p) {
   __shared__ unsigned long long turns[64];
-  __shared__ float weight[D];
+  __shared__ __align__(16) float weight[D];
   __shared__ float sums[kNormThreads / 32][D];
   pdl_wait();
   pdl_launch_dependents();
   const bool is_q = blockIdx.x < p.q_blocks;
   if (threadIdx.x < 8 * p.rot_units) turns[threadIdx.x] = turns_of(p.inv_freq[threadIdx.x]);
-  if (threadIdx.x < D) weight[threadIdx.x] = (is_q ? p.wq : p.wk)[threadIdx.x];
+  if (threadIdx.x < D) weight[weight_at<D, INTER>(threadIdx.x, p.rot_units)] = (is_q ? p.wq : p.wk)[threadIdx.x];
   __syncthreads();
   constexpr int kUnits = D / 16;
   const int heads = is_q ? p.H : p.Hkv;
@@ -305,11 +321,9 @@ __global__ void __launch_bounds__(kNormThreads, kNormBackPerSm) fa_norm_bwd_kern
       uint64_t x2[8], y2[8], yw[8], ss = f2_pack(0.f, 0.f), sd = ss;
 #pragma unroll
       for (int e = 0; e < 8; ++e) {
-        const uint4& xv = v[e / 4];
-        const uint32_t x = e % 4 == 0 ? xv.x : e % 4 == 1 ? xv.y : e % 4 == 2 ? xv.z : xv.w;
-        x2[e] = f2_pack(__uint_as_float(x << 16), __uint_as_float(x & 0xFFFF0000u));
+        x2[e] = pair_of(v[0], v[1], e);
         y2[e] = f2_pack(y[2 * e], y[2 * e + 1]);
-        const float2 w = *reinterpret_cast<const float2*>(weight + (e < 4 ? at.c0 + 2 * e : at.c1 + 2 * e - 8));
+        const float2 w = *reinterpret_cast<const float2*>(weight + (e / 2 * kUnits + u) * 4 + e % 2 * 2);
         yw[e] = f2_mul(y2[e], f2_pack(w.x, w.y));
         ss = f2_fma(x2[e], x2[e], ss);
         sd = f2_fma(yw[e], x2[e], sd);

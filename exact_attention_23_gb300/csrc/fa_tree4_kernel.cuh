@@ -31,8 +31,8 @@ struct Tree4Cfg {
   static constexpr int kKeys = 128;                        // keys per chunk
   static constexpr int kCodes = kKeys * D / 2;             // a tile's codes, in front of its scales
   static constexpr int kTile = kCodes + kKeys * D / 16;    // K or V of a chunk
-  static constexpr int kStages = 6;                        // K or V tiles in flight
-  static constexpr int kCtasPerSm = D == 64 && NB == 1 ? 3 : 2;
+  static constexpr int kStages = 4;                        // K or V tiles in flight
+  static constexpr int kCtasPerSm = NB == 1 ? 3 : 2;
   static constexpr int kRows = NB * 8;
   static constexpr int kRowStride = D + 8;                 // (floats; rows of the merge without bank conflicts)
   static constexpr int kMergeOff = kStages * kTile;
@@ -41,13 +41,20 @@ struct Tree4Cfg {
 
 // N = 1, 2 or 4 words of shared memory.
 template <int N>
-__device__ __forceinline__ void lds_words(uint32_t addr, uint32_t (&r)[N]) {
-  if constexpr (N == 1) asm volatile("ld.shared.b32 %0, [%1];" : "=r"(r[0]) : "r"(addr) : "memory");
-  else if constexpr (N == 2)
-    asm volatile("ld.shared.v2.b32 {%0,%1}, [%2];" : "=r"(r[0]), "=r"(r[1]) : "r"(addr) : "memory");
-  else
-    asm volatile("ld.shared.v4.b32 {%0,%1,%2,%3}, [%4];" : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
-                 : "r"(addr) : "memory");
+__device__ __forceinline__ void lds_words(const uint8_t* at, uint32_t (&r)[N]) {
+  if constexpr (N == 1) {
+    r[0] = *reinterpret_cast<const uint32_t*>(at);
+  } else if constexpr (N == 2) {
+    const uint2 x = *reinterpret_cast<const uint2*>(at);
+    r[0] = x.x;
+    r[1] = x.y;
+  } else {
+    const uint4 x = *reinterpret_cast<const uint4*>(at);
+    r[0] = x.x;
+    r[1] = x.y;
+    r[2] = x.z;
+    r[3] = x.w;
+  }
 }
 // An 8 × 8 matrix of 16-bit numbers, a row a quad, transposed.
 __device__ __forceinline__ uint32_t movmatrix_t(uint32_t x) {
@@ -122,10 +129,14 @@ __global__ void __launch_bounds__(kTreeBlock, Tree4Cfg<D, NB>::kCtasPerSm) fa_tr
   // A result's element e of key tile mt and row block nb: key mt·16 + qr + 8·(e / 2) of the warp's 32, query
   // row nb·8 + qc + e % 2. O's: dimension 16·tile + qr + 8·(e / 2).
   const int qr = lane >> 2, qc = (lane & 3) * 2;
-  const uint32_t ring = smem_u32(sm);
+  // This thread's first words within a tile: of key qr of the warp's 32 (K), and of key qc (V)
+  const uint8_t* const k_words = sm + (warp * 32 + qr) * (D / 2) + qc * (D / 16);
+  const uint8_t* const k_scales = sm + C::kCodes + (warp * 32 + qr) * (D / 16);
+  const uint8_t* const v_words = sm + (warp * 32 + qc) * (D / 2) + qr * 4;
+  const uint8_t* const v_scales = sm + C::kCodes + (warp * 32 + qc) * (D / 16);
   float* const xo = reinterpret_cast<float*>(sm + C::kMergeOff);  // [4][rows][D + 8]
   const float nan = __uint_as_float(0x7FC00000u);
-  int n = 0;
+  int st = 0, ph = 0;  // the ring's next slot, and its phase
   bool ok = true;
   while (sg.next(p.list, p.reach)) {
     const int bh = sg.b * p.list.Hkv + sg.hk;
@@ -178,22 +189,23 @@ __global__ void __launch_bounds__(kTreeBlock, Tree4Cfg<D, NB>::kCtasPerSm) fa_tr
 #pragma unroll
       for (int nb = 0; nb < NB; ++nb) o[x][nb][0] = o[x][nb][1] = o[x][nb][2] = o[x][nb][3] = 0.f;
 
-    for (int c = sg.c0; c < sg.c1; ++c, n += 2) {
-      const int stk = n % C::kStages, stv = (n + 1) % C::kStages;
-      if (ok && !mbar_wait_warp(&full[stk], (n / C::kStages) & 1, wc)) ok = false;
-      if (!ok) continue;  // (walk on: the merges below are joined by every warp)
-      const uint32_t kt = ring + stk * C::kTile, vt = ring + stv * C::kTile;
+    static_assert(C::kStages % 2 == 0, "a chunk's K and V have neighbouring slots");
+    for (int c = sg.c0; c < sg.c1 && ok; ++c) {  // (a failed warp walks on: the merges below are joined by all)
+      if (!mbar_wait_warp(&full[st], ph, wc)) {
+        ok = false;
+        break;
+      }
+      const int kt = st * C::kTile, vt = kt + C::kTile;
       const int key0 = (c + (c < sc ? 0 : gap)) * C::kKeys + warp * 32;  // this warp's first key
       // ---- Sᵀ = K·Qᵀ
       float s[2][NB][4];
 #pragma unroll
       for (int mt = 0; mt < 2; ++mt) {
-        const uint32_t row = warp * 32 + mt * 16 + qr;
         uint32_t wa[kW], wb[kW], sa[kS], sb[kS];  // keys qr and qr + 8 of the tile
-        lds_words(kt + row * (D / 2) + qc * (D / 16), wa);
-        lds_words(kt + (row + 8) * (D / 2) + qc * (D / 16), wb);
-        lds_words(kt + C::kCodes + row * (D / 16), sa);
-        lds_words(kt + C::kCodes + (row + 8) * (D / 16), sb);
+        lds_words(k_words + kt + mt * 16 * (D / 2), wa);
+        lds_words(k_words + kt + (mt * 16 + 8) * (D / 2), wb);
+        lds_words(k_scales + kt + mt * 16 * (D / 16), sa);
+        lds_words(k_scales + kt + (mt * 16 + 8) * (D / 16), sb);
 #pragma unroll
         for (int nb = 0; nb < NB; ++nb) s[mt][nb][0] = s[mt][nb][1] = s[mt][nb][2] = s[mt][nb][3] = 0.f;
 #pragma unroll
@@ -210,7 +222,7 @@ __global__ void __launch_bounds__(kTreeBlock, Tree4Cfg<D, NB>::kCtasPerSm) fa_tr
         }
       }
       __syncwarp();
-      if (lane == 0) mbar_arrive(&empty[stk]);
+      if (lane == 0) mbar_arrive(&empty[st]);
       // ---- scores to base-2 exponents
       // (BIAS: distances from the end of the context; positions past 2²⁴ are no fp32 numbers)
       const float behind = static_cast<float>(ctx - key0 - qr);
@@ -328,39 +340,40 @@ __global__ void __launch_bounds__(kTreeBlock, Tree4Cfg<D, NB>::kCtasPerSm) fa_tr
           }
       }
       // ---- Oᵀ += Vᵀ·Pᵀ
-      if (!mbar_wait_warp(&full[stv], ((n + 1) / C::kStages) & 1, wc)) {
+      if (!mbar_wait_warp(&full[st + 1], ph, wc)) {
         ok = false;
-        continue;
+        break;
       }
       // Rows behind the last key, and those before every token's window, may hold anything: with a scale of 0
       // they are 0.
       const bool cut = key0 + 32 > keys || (key0 < lo_all && key0 + 32 > p.reach.sinks);
 #pragma unroll
       for (int mt = 0; mt < 2; ++mt) {
-        const int row = warp * 32 + mt * 16 + qc;  // this thread's keys: row, row + 1, row + 8, row + 9
+        // this thread's keys: qc, qc + 1, qc + 8, qc + 9 of the tile
         uint32_t sv[4][kS];
 #pragma unroll
-        for (int e = 0; e < 4; ++e) lds_words(vt + C::kCodes + (row + (e & 1) + (e >> 1) * 8) * (D / 16), sv[e]);
-        uint32_t keep[2] = {0xFFFFFFFFu, 0xFFFFFFFFu};
-        if (cut) {
+        for (int e = 0; e < 4; ++e) {
+          const int key = mt * 16 + (e & 1) + (e >> 1) * 8;
+          lds_words(v_scales + vt + key * (D / 16), sv[e]);
+          if (cut) {
+            const int k = key0 + key + qc;
+            if (k >= keys || (k >= p.reach.sinks && k < lo_all)) {
 #pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            const int key = key0 + mt * 16 + h * 8 + qc;
-            auto used = [&](int k) { return k < keys && !(k >= p.reach.sinks && k < lo_all); };
-            keep[h] = (used(key) ? 0x0000FFFFu : 0u) | (used(key + 1) ? 0xFFFF0000u : 0u);
+              for (int h = 0; h < kS; ++h) sv[e][h] = 0u;
+            }
           }
         }
 #pragma unroll
         for (int h = 0; h < D / 64; ++h) {
           uint32_t w[4][1];
 #pragma unroll
-          for (int e = 0; e < 4; ++e) lds_words(vt + (row + (e & 1) + (e >> 1) * 8) * (D / 2) + (8 * h + qr) * 4, w[e]);
+          for (int e = 0; e < 4; ++e) lds_words(v_words + vt + (mt * 16 + (e & 1) + (e >> 1) * 8) * (D / 2) + 32 * h, w[e]);
 #pragma unroll
           for (int g = 0; g < 2; ++g) {  // dimensions 64h + 32g …
             const uint32_t half = g ? 0x7632 : 0x5410;
             const uint32_t u0 = __byte_perm(w[0][0], w[1][0], half), u1 = __byte_perm(w[2][0], w[3][0], half);
-            const FourScale f0 = four_scale(__byte_perm(sv[0][h], sv[1][h], half) & keep[0]);
-            const FourScale f1 = four_scale(__byte_perm(sv[2][h], sv[3][h], half) & keep[1]);
+            const FourScale f0 = four_scale(__byte_perm(sv[0][h], sv[1][h], half));
+            const FourScale f1 = four_scale(__byte_perm(sv[2][h], sv[3][h], half));
             const uint32_t a0[4] = {four_pair<0>(u0, f0), four_pair<1>(u0, f0), four_pair<0>(u1, f1), four_pair<1>(u1, f1)};
             const uint32_t a1[4] = {four_pair<2>(u0, f0), four_pair<3>(u0, f0), four_pair<2>(u1, f1), four_pair<3>(u1, f1)};
 #pragma unroll
@@ -372,7 +385,12 @@ __global__ void __launch_bounds__(kTreeBlock, Tree4Cfg<D, NB>::kCtasPerSm) fa_tr
         }
       }
       __syncwarp();
-      if (lane == 0) mbar_arrive(&empty[stv]);
+      if (lane == 0) mbar_arrive(&empty[st + 1]);
+      st += 2;
+      if (st == C::kStages) {
+        st = 0;
+        ph ^= 1;
+      }
     }
 
     // ---- the segment's end: the warps' parts in shared memory, then rows over all threads
