@@ -134,6 +134,7 @@ using namespace fa::host;
 
 bool four_sizes(int B, int Hkv, int n, int Tmax, int d) {
   if (B <= 0 || Hkv <= 0 || n <= 0 || Tmax <= 0 || Tmax % 8 != 0 || (d != 64 && d != 128)) return false;
+  if (n > (1 << 30)) return false;  // (rows behind the last of a block fit an int)
   const long long heads = static_cast<long long>(B) * Hkv;
   if (heads > (1 << 30) || heads > (1LL << 60) / d / Tmax || heads > (1LL << 38) / n) return false;
   // (a block takes at least 64 rows of a head)

@@ -288,9 +288,13 @@ __global__ void __launch_bounds__(Cfg1<D, (MOD & kModRef) != 0>::kThreads, 1)
       int kvh = u.bh;  // the key head this query head reads
       if constexpr (MOD != 0) kvh = static_cast<int>(p.mod.div_g.div(static_cast<uint32_t>(u.bh)));
       for (int j = 0; j < u.n_steps; ++j, ++g) {
-        us.next(u, j);
-        int kt = us.kt;
-        if constexpr (kSink) kt = sink_step_tile<MOD>(u, j);
+        int kt;
+        if constexpr (kSink) {
+          kt = sink_step_tile<MOD>(u, j);
+        } else {
+          us.next(u, j);
+          kt = us.kt;
+        }
         const int st = g % C::kStages;
         const int use = g / C::kStages;
         if (use > 0 && !mbar_wait_warp(&bars->kv_empty[st], (use - 1) & 1, wc)) { ok = false; break; }

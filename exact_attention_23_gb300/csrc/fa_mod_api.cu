@@ -81,7 +81,7 @@ static WindowLayout window_layout(int B, int T, int window, int sinks) {
   // it is that of a document of 128·(n − 2) tokens and more, so n − 1 ≤ 8/7 of its length in tiles (n ≥ 9);
   // at most (sinks + 126) / 128 + 1 tiles hold a document's sinks, and documents do not overlap.
   const long long holds = (sinks + 126) / 128 + 1;
-  const long long extra = (n_t * holds * 8 + 7 * l.piece - 1) / (7 * l.piece);
+  const long long extra = n_t <= l.piece ? 0 : (n_t * holds * 8 + 7 * l.piece - 1) / (7 * l.piece);
   l.n_rec = static_cast<int>(n_t + extra);
   l.n_cut = static_cast<int>(std::min(extra, n_t));
   l.n_slots = static_cast<int>(extra + l.n_cut);

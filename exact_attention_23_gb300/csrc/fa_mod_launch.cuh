@@ -52,11 +52,13 @@ cudaError_t launch_bwd_mod(const BwdLaunch& a, int q_heads) {
   }
   if constexpr ((MOD & kModSink) != 0) {
     const BwdModParams& m = a.p.mod;
-    const int key_heads = a.p.BH / m.parts;
-    const float* piece_out = m.piece_out;
-    e = launch_pdl(fa_bwd_pieces_kernel<D>, static_cast<unsigned>(key_heads) * m.n_cut * (128 / kPieceRows<D>), 256, 0, a.stream, piece_out,
-                   m.cuts, a.p.dk, a.p.dv, m.Hkv, key_heads, a.p.T, m.n_cut, m.n_slots, m.parts);
-    if (e != cudaSuccess) return e;
+    if (m.n_cut > 0) {
+      const int key_heads = a.p.BH / m.parts;
+      const float* piece_out = m.piece_out;
+      e = launch_pdl(fa_bwd_pieces_kernel<D>, static_cast<unsigned>(key_heads) * m.n_cut * (128 / kPieceRows<D>), 256, 0,
+                     a.stream, piece_out, m.cuts, a.p.dk, a.p.dv, m.Hkv, key_heads, a.p.T, m.n_cut, m.n_slots, m.parts);
+      if (e != cudaSuccess) return e;
+    }
   }
   return launch_pdl(fa_bwd_dq_kernel<D>, a.grid_dq, 256, 0, a.stream, a.p.dq_acc, a.dq, a.p.T, a.p.n_qt,
                     q_heads, a.p.scale);

@@ -540,7 +540,7 @@ int fa_fwd_tree(const void* q, const void* k_cache, const void* v_cache, void* o
  * rows whose position is less than `window` behind its own, and those whose position is below `sinks`;
  * a context row's position is its index. Only the rows that some token may see are read: rows between
  * the sinks and the first token's window may hold anything, NaN included, as those behind the last new
- * token. workspace: fa_fwd_tree_window_workspace_size(...) bytes, as for fa_fwd_tree.
+ * token. depths are below 2²⁴ here too. workspace: fa_fwd_tree_window_workspace_size(...) bytes, as for fa_fwd_tree.
  */
 size_t fa_fwd_tree_window_workspace_size(int B, int H, int Hkv, int Tq, int Tmax, int d, int window, int sinks);
 int fa_fwd_tree_window(const void* q, const void* k_cache, const void* v_cache, void* o, float* lse,

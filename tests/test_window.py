@@ -189,6 +189,13 @@ def test_parity_with_many_heads(T, d, window, sinks, cap, lengths, pad, with_res
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("d,cap,lengths", [(64, 0.0, None), (64, 30.0, (900, 200)), (128, 0.0, (1000, 3))])
+def test_parity_of_wider_windows_with_many_heads(d, cap, lengths):
+    """Two query tiles a CTA at either head dim, whose sinks lie in tiles before both walks."""
+    _check(1, 80, 10, 1100, d, 600, 4, cap, False, lengths, 11 if lengths else 0)
+
+
+@pytest.mark.gpu
 def test_a_window_over_everything_is_causal_attention():
     q, k, v, do = _tensors(2, 4, 2, 500, 64, 8)
     wide = fa.visible(2, 500, window=500, sinks=4, device="cuda")
