@@ -35,7 +35,13 @@ __device__ __forceinline__ FourScale four_scale(uint32_t pair) {
 template <int I>
 __device__ __forceinline__ uint32_t four_pair(uint32_t word, const FourScale& f) {
   const uint32_t at = I == 0 ? word << 3 : word >> (I == 0 ? 0 : 4 * I - 3);
-  const __nv_bfloat162 x = __hfma2(as_bf162((at & 0x00780078u) | 0x41804180u), f.s, f.off);
+  // (mask and exponent in registers, so that both are one operation, which with two constants in its code
+  // they are not: B8 H16 Hkv4 ctx60000 d128 65.8 -> 56.3 µs)
+  uint32_t mask, exponent, y;
+  asm("mov.b32 %0, 0x00780078;" : "=r"(mask));
+  asm("mov.b32 %0, 0x41804180;" : "=r"(exponent));
+  asm("lop3.b32 %0, %1, %2, %3, 0xEA;" : "=r"(y) : "r"(at), "r"(mask), "r"(exponent));  // (at & mask) | exponent
+  const __nv_bfloat162 x = __hfma2(as_bf162(y), f.s, f.off);
   return *reinterpret_cast<const uint32_t*>(&x);
 }
 

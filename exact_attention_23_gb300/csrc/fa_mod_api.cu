@@ -147,7 +147,8 @@ __device__ __forceinline__ void doc_bits(const int* ids, int i0, int end, uint32
 // the last change of id at or before it and ends at the next one after it: a running maximum and
 // a running minimum, each thread taking one stretch of rows (as bits, 32 rows at a time) and the
 // block joining the stretches. Then a warp a tile: its rows (from their stretch's bits, where a stretch
-// has at most 32, so that rows are written side by side: T 16384 VIS) and their extremes, the query tiles
+// has at most 32, so that rows are written side by side: T 16384
+// 17.3 -> 12.0 µs, with sinks 42.6 -> 16.1, half of that the lengths below being made once) and their extremes, the query tiles
 // that see it, and its place among the tiles by the number it has to walk (a count of the tiles before
 // it: n_t² comparisons, which at 16384 tokens are 4 a lane and tile). Latency is all it costs; the
 // tiles' extremes are kept in shared memory up to kVisTiles of them. WINDOW: rows see the last

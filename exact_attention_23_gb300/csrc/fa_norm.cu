@@ -14,6 +14,12 @@
 // of a row exchange its sums in 2 or 3 shuffles, and nothing but the rows goes through memory: 4
 // bytes an element forward, 6 backward.
 //
+// What bounds them: on long batches the rows' way from memory, forward B4 H12+12 T16384 d64 (403 MB)
+// 81.8 µs, 4.9 TB/s, backward B1 H16+4 T16384 d128 (252 MB) 50.2 µs, 5.0 TB/s (copying: 6.8); on short ones the launch and one
+// wave's latency, B4 H12+12 T1024 d64 7.0 µs, one token 2.5. Arithmetic is on pairs of neighbouring
+// dimensions (fp32x2), weights lie in shared memory in the order that lanes read them in, and rows are
+// numbered with 32 bits, whose divisions are multiplications (backward 65 -> 51 µs).
+//
 // dw sums over all rows. A block of the backward takes queries or keys, never both, and keeps its 16
 // sums a thread in registers over all its rows (a persistent grid), so that a call leaves at most
 // kNormBlocks rows of partial sums; fa_norm_dw_kernel adds them in order: the same bits every time.
@@ -52,9 +58,13 @@ struct NormParams {
   float mscale, eps;
 };
 
+// Forward: one head's loads a thread in flight and eight blocks an SM (61 registers): B4 H12+12 T1024 d64 7.0 µs,
+// B1 H16+4 T16384 d128 35.7; two heads, five blocks 7.6 and 41.7; four heads, four blocks 7.7 and 37.4.
 constexpr int kNormThreads = 128;
 constexpr int kNormPerSm = 8;
 constexpr int kNormFlight = 1;   // heads whose loads a thread keeps in flight
+// Backward: one row at hand and the next on its way, 124 registers: four blocks an SM 51.4 µs, three 54.7. (Two heads
+// at once without the next: 57.7. A ring of four rows in shared memory by asynchronous copies: 69.)
 constexpr int kNormBackPerSm = 4;
 constexpr int kNormBlocks = 608;  // of the backward, at most (the workspace's rows)
 
@@ -632,7 +642,7 @@ int fa_norm_rope_bwd(const void* gq, long long gq_sb, long long gq_sh, long long
   p.n_blocks = static_cast<unsigned>(blocks);
   const long long most = std::min<long long>(kNormBlocks, static_cast<long long>(kNormBackPerSm) * sms);
   // Heads a thread walks: as many as leave every block of the grid eight tasks, of which the last may be
-  // one too many (B1 H16+4 T16384 d128, 2.1 tasks of 16 heads a block: 58 µs; 8.4 of 4: KK).
+  // one too many (B1 H16+4 T16384 d128, 2.1 tasks of 16 heads a block: 56.8 µs; 8.4 of 4: 51.4).
   auto tasks = [&](int heads, long long chunk) { return (heads + chunk - 1) / chunk * blocks; };
   long long chunk = std::max(H, Hkv);
   while (chunk > 1 && tasks(H, chunk) + (keys ? tasks(Hkv, chunk) : 0) < 8 * most) chunk = (chunk + 1) / 2;

@@ -9,6 +9,12 @@
 // pay for no row that is not there, as 16 rows would). P goes from the layout of a result to that of an
 // operand by movmatrix. More rows than 16 are further entries of the list.
 //
+// Measured: B8 H16 Hkv4, one token, contexts to 16384, d128 (59 MB) 24.0 µs, to 60000 (217 MB) 56.1, 3.9 TB/s (41 with
+// operands left unmade: shifts, masks and multiply-adds are what it spends on top of streaming); B4 12 heads,
+// 8 drafts, to 4000, d64 13.5. With the query rows on the 16 side and 16 of them always: 36.4 and 17.4.
+// Three CTAs an SM, four at d = 64, and four tiles a ring for 8 rows (16384 keys to 60000: three 24.0 and 56.1, two
+// 23.5 and 59.2); two CTAs for 16, whose registers spill otherwise.
+//
 // A CTA's four compute warps take 32 keys each of a chunk of 128, with a running maximum, sum and O of
 // their own, behind a producer warp that copies the chunk's codes and scales, two contiguous pieces each
 // of K and V, into a ring; the warps' parts meet in shared memory at a segment's end.
@@ -32,7 +38,7 @@ struct Tree4Cfg {
   static constexpr int kCodes = kKeys * D / 2;             // a tile's codes, in front of its scales
   static constexpr int kTile = kCodes + kKeys * D / 16;    // K or V of a chunk
   static constexpr int kStages = 4;                        // K or V tiles in flight
-  static constexpr int kCtasPerSm = NB == 1 ? 3 : 2;
+  static constexpr int kCtasPerSm = NB == 2 ? 2 : D == 64 ? 4 : 3;
   static constexpr int kRows = NB * 8;
   static constexpr int kRowStride = D + 8;                 // (floats; rows of the merge without bank conflicts)
   static constexpr int kMergeOff = kStages * kTile;
