@@ -343,7 +343,7 @@ __global__ void __launch_bounds__(kNormThreads, kNormBackPerSm) fa_norm_bwd_kern
       f2_unpack(sd, d0, d1);
       const float sum_x = row_sum<D>(s0 + s1), sum_d = row_sum<D>(d0 + d1);
       const float r = rsqrtf(fmaf(sum_x, 1.0f / D, p.eps));
-      const uint64_t r2 = f2_pack(r, r), back = f2_pack(-r * r * sum_d * (1.0f / D), -r * r * sum_d * (1.0f / D));
+      const uint64_t r2 = f2_pack(r, r), back = f2_splat(-r * (1.0f / D) * (r * sum_d));  // (r² may overflow)
 #pragma unroll
       for (int e = 0; e < 8; ++e) {
         acc[e] = f2_fma(y2[e], f2_mul(x2[e], r2), acc[e]);

@@ -462,7 +462,8 @@ int fa_rope_append(const void* q, long long q_sb, long long q_sh, long long q_st
  *   eps                : finite and > 0
  *   everything else as for fa_rope and fa_rope_append (Hkv 0: k, k_out and k_weight NULL)
  *
- * The sums are taken in fp32 and a result is rounded once.
+ * The sums are taken in fp32 (a row whose squares' mean passes its range, magnitudes of 2⁶¹ and more, is
+ * zeros) and a result is rounded once.
  * ---------------------------------------------------------------------------------------
  */
 int fa_norm_rope(const void* q, long long q_sb, long long q_sh, long long q_st, void* q_out, const void* k,

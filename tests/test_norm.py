@@ -308,6 +308,20 @@ def test_rows_of_zeros_and_extremes():
 
 
 @pytest.mark.gpu
+def test_eps_whose_square_root_inverse_squared_is_no_number():
+    # (1/√eps)² = 2^133 passes fp32's range, 1/√eps and the gradient do not
+    eps, f, w = 2.0 ** -133, fa.rope_inv_freq(64), torch.ones(64, device="cuda")
+    x = torch.zeros(1, 1, 3, 64, dtype=torch.bfloat16, device="cuda")
+    x[0, 0, 1], x[0, 0, 2] = 2.0 ** -64, 2.0 ** -62
+    pos, g = torch.arange(3).expand(1, 3), torch.ones_like(x)
+    _near(fa.norm_rope(x, None, w, None, f, eps=eps)[0], _forward(x, w, pos, f, False, 1.0, eps))
+    dx, _, dw, _ = fa.norm_rope_bwd(g, None, x, None, w, None, f, eps=eps)
+    rows, sums = _backward(g, x, w, pos, f, False, 1.0, eps)
+    _near(dx, rows)
+    _near(dw, sums)
+
+
+@pytest.mark.gpu
 @pytest.mark.parametrize("B,H,Hkv,n,Tmax,d,rot,interleaved", [
     (1, 4, 2, 1, 20, 64, 64, False), (4, 6, 2, 9, 64, 128, 64, True), (5, 3, 3, 33, 50, 64, 16, False),
 ])
