@@ -288,7 +288,8 @@ __device__ __forceinline__ Unit pair_unit_of(const FwdParams& p, int L) {
   if constexpr (SINK) {
     const int n0 = u.se[0] - u.sb[0], n1 = u.se[1] - u.sb[1];
     u.ub = min(n0 > 0 ? u.sb[0] : u.kb, n1 > 0 ? u.sb[1] : u.kb);
-    u.un = max(0, min(max(n0 > 0 ? u.se[0] : 0, n1 > 0 ? u.se[1] : 0), u.kb) - u.ub);
+    // (those of the second tile may lie within the walk, at the first tile's own keys, far behind the first's)
+    u.un = max(0, min(max(n0 > 0 ? u.se[0] : 0, n1 > 0 && u.sb[1] < u.kb ? u.se[1] : 0), u.kb) - u.ub);
     u.nkv[0] += n0;
     u.nkv[1] += n1;
     u.n_steps += u.un;

@@ -1,5 +1,5 @@
-// Host side of attention with modified scores (include/fa.h: fa_visible, fa_fwd_mod, fa_bwd_mod)
-// and the kernel that makes a batch's visibility.
+// Host side of attention with modified scores (include/fa.h: fa_visible, fa_fwd_mod, fa_bwd_mod, and
+// their forms with a window) and the kernel that makes a batch's visibility.
 #include <cuda.h>
 #include <cuda_runtime.h>
 #include <stddef.h>

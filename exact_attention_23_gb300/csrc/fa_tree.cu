@@ -1,5 +1,5 @@
-// Host side of attention of new tokens against a cache (include/fa.h: fa_fwd_tree) and the
-// instantiations of its kernels.
+// Host side of attention of new tokens against a cache (include/fa.h: fa_fwd_tree,
+// fa_fwd_tree_window, fa_fwd_tree4) and the instantiations of its kernels without a window.
 #include <cuda.h>
 #include <cuda_runtime.h>
 #include <stddef.h>

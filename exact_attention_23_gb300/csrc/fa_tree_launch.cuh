@@ -78,7 +78,7 @@ cudaError_t launch_tree4_mod(const Tree4Launch& a, int mod) {
 cudaError_t launch_tree4_d64(const Tree4Launch& a, int rows, int mod);
 cudaError_t launch_tree4_d128(const Tree4Launch& a, int rows, int mod);
 
-// With a sliding window and sinks (fa_tree_window.cu).
+// With a sliding window and sinks (fa_tree_window_d….cu).
 cudaError_t launch_tree_window_d64(const TreeLaunch& a, int rows, int mod);
 cudaError_t launch_tree_window_d128(const TreeLaunch& a, int rows, int mod);
 
