@@ -45,25 +45,49 @@ constexpr int kMinPer = 2, kMinPerWide = 1;
 // Not beyond the chunks measured: stretches share out unequal contexts, a CTA an entry does not.
 //   a window, d64 (10)         192, 18: 19.2 / 17.0, 10: 12.3 / 11.4;  48, 18: 9.4 / 14.1;  384, 18: 27.6 / 23.4
 //                              (its contexts are as unequal, but what is left of them is not)
-//   4 bits (4), 128-key chunks d64: 48, 4: 7.2 / 6.0, 8: 7.5 / 8.7, 12: 10.4 / 11.6;  192, 8: 13.1 / 9.9
-//                              d128: 32, 8: 7.8 / 11.0;  128, 6: 10.9 / 9.2
-int join_chunks(bool wide_rows, int d, bool window) {
-  return wide_rows ? (d == 64 ? 5 : 4) : d == 64 ? (window ? 10 : 7) : 5;
-}
-constexpr int kSoloChunks = 24, kSoloChunksWide = 12;
-constexpr int kJoinChunksFour = 4, kSoloChunksFour = 12;
-
-struct TreeSizes {
-  int R, rows_log2, row_blocks, chunk_log2, min_per;
-  bool solo;
-  long long entries, grid, slots;
-  size_t lse_off, parts_off, bytes;
-};
+//   4 bits, 128-key chunks     d64: 48, 4: 7.2 / 6.0, 8: 7.5 / 8.7;  192, 8: 13.1 / 9.9;  d128: 128, 6: 10.9 / 9.2
+// With a window or in 4 bits, such an entry is taken by a cluster of CTAs, which join their parts through shared memory:
+// as many as fit the GPU at once (2, 4 or 8. Clusters that do not all fit wait: of 456 places pairs find 456, fours
+// 440, sevens 413, eights 408; 64 entries in sevens 9.8 -> 13.1 µs, 152 in fours on 608 places 19.2 -> 23.9). µs in
+// stretches / in clusters, the chunks of a CTA in these in brackets, every context full:
+//   a window, d64              8, 18: 7.8 / 6.3 (3), 66: 10.3 / 9.3 (9);  40, 34: 12.1 / 9.4 (5);  96, 18: 12.9 / 9.7 (5);
+//                              200, 66: 48.4 / 39.0 (33)
+//   d128                       8, 18: 9.6 / 8.6 (3), 66: 12.5 / 13.8 (9);  24, 34: 14.7 / 11.8 (5);  104, 34: 29.1 / 25.6 (17)
+//   4 bits, full / contexts from none to full (there it is the longest that counts)
+//   d64, to 8 rows             24, 32: 9.3 / 7.8 (4), 8.8 / 7.3;  40, 64: 15.2 / 15.8 (8), 12.3 / 12.2;  104, 64: 24.6 / 24.1
+//                              (13), 17.8 / 19.3
+//   d64, 16 rows               64, 32: 17.1 / 13.4 (8), 18.5 / 12.5;  104, 64: 32.6 / 37.3 (32), 31.7 / 33.5
+//   d128, to 8 rows            40, 32: 13.3 / 11.6 (4), 11.3 / 10.5, 64: 19.6 / 19.4 (8), 13.8 / 16.2
+//   d128, 16 rows              24, 32: 17.4 / 14.0 (4), 16.6 / 13.2;  96, 64: 50.0 / 45.2 (22), 46.1 / 43.7
 
 // What the new tokens go against: a window (0: none) with sinks, a cache in 4 bits.
 struct TreeForm {
   int window, sinks;
   bool four;
+};
+
+int join_chunks(bool wide_rows, int d, const TreeForm& form) {
+  if (form.four) return d == 64 ? 3 : 2;
+  return wide_rows ? (d == 64 ? 5 : 4) : d == 64 ? (form.window > 0 ? 10 : 7) : 5;
+}
+int solo_chunks(bool wide_rows, int d, int rows_log2, const TreeForm& form) {
+  if (form.four) return rows_log2 > 3 ? 24 : d == 64 ? 8 : 6;
+  return wide_rows ? 12 : form.window > 0 ? 34 : 24;
+}
+// CTAs a cluster, where `fit` fit the GPU (two or three chunks are one CTA's: 128 entries of two in 4 bits 4.9 µs, by
+// twos 5.5; 8 of four 6.0, by fours 4.9).
+int cluster_ctas(long long entries, long long chunks, long long fit) {
+  if (chunks < 4) return 1;
+  int ctas = entries * 2 <= fit ? 2 : 1;
+  while (ctas > 1 && ctas < 8 && ctas * 2 <= chunks && entries * ctas * 2 <= fit - fit / (ctas == 2 ? 16 : 8)) ctas *= 2;
+  return ctas;
+}
+
+struct TreeSizes {
+  int R, rows_log2, row_blocks, chunk_log2, min_per;
+  int solo;  // CTAs an entry without stretches, 0: stretches
+  long long entries, grid, slots;
+  size_t lse_off, parts_off, bytes;
 };
 
 // CTAs of the streaming kernels an SM holds.
@@ -96,10 +120,14 @@ bool tree_sizes(int B, int H, int Hkv, int Tq, int Tmax, int d, const TreeForm& 
   const long long most = (z->entries * chunks + z->min_per - 1) / z->min_per;
   const long long fit = static_cast<long long>(sms) * (is_wide ? 1 : form.four ? tree4_ctas(d, 1 << z->rows_log2) : tree_ctas(d));
   const long long per = std::max<long long>(z->min_per, (z->entries * chunks + fit - 1) / fit);  // a stretch's
-  z->solo = z->entries <= fit && chunks <= per + (form.four ? kJoinChunksFour : join_chunks(is_wide, d, form.window > 0)) &&
-            chunks <= (form.four ? kSoloChunksFour : is_wide ? kSoloChunksWide : kSoloChunks);
+  const bool streams = !is_wide && (form.four || form.window > 0);
+  const int ctas = streams ? cluster_ctas(z->entries, chunks, fit) : 1;
+  const long long most_chunks = (chunks + ctas - 1) / ctas;  // a CTA's
+  const bool whole = z->entries <= fit && most_chunks <= per + join_chunks(is_wide, d, form) &&
+                     most_chunks <= solo_chunks(is_wide, d, z->rows_log2, form);
+  z->solo = whole ? ctas : 0;
   if (z->solo) {
-    z->grid = z->entries;
+    z->grid = z->entries * z->solo;
     z->slots = 0;
     z->lse_off = z->parts_off = 0;
     z->bytes = 1;  // none needed
@@ -188,7 +216,7 @@ int fwd_tree(const void* q, const void* k_cache, const void* v_cache, const void
   a.p.slopes = slopes;
   a.p.status = status;
   a.p.timeout_ns = timeout_ns ? timeout_ns : 2000000000ull;
-  a.p.list = fa::TreeList{ctx_len, B, Hkv, Tq, Tmax, z.row_blocks, z.min_per, z.chunk_log2, z.solo ? 1 : 0,
+  a.p.list = fa::TreeList{ctx_len, B, Hkv, Tq, Tmax, z.row_blocks, z.min_per, z.chunk_log2, z.solo,
                           z.solo ? nullptr : reinterpret_cast<int2*>(ws + z.parts_off)};
   a.p.reach = fa::TreeReach{form.four && form.window == 0 ? INT32_MAX : form.window, form.sinks};
   a.p.mask = fa::TreeMask{tree, depths, fa::FastDiv::make(static_cast<uint32_t>(Tq)), tree_per_batch != 0,

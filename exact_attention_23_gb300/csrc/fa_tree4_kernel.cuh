@@ -79,6 +79,7 @@ __global__ void __launch_bounds__(kTreeBlock, Tree4Cfg<D, NB>::kCtasPerSm) fa_tr
   __shared__ uint64_t full[C::kStages], empty[C::kStages];
   __shared__ uint32_t abort_flag;
   __shared__ float xm[4][C::kRows], xl[4][C::kRows];
+  __shared__ float2 ml[C::kRows];  // (solo in a cluster)
   const TreeParams& p = pp.t;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   if (threadIdx.x == 0) {
@@ -444,6 +445,13 @@ __global__ void __launch_bounds__(kTreeBlock, Tree4Cfg<D, NB>::kCtasPerSm) fa_tr
         acc[6] = fmaf(f, b.z, acc[6]);
         acc[7] = fmaf(f, b.w, acc[7]);
       }
+      if (p.list.solo > 1) {  // (into the places of the first part, which this thread has read)
+        float4* dst = reinterpret_cast<float4*>(xo + rr * C::kRowStride + col);
+        dst[0] = make_float4(acc[0], acc[1], acc[2], acc[3]);
+        dst[1] = make_float4(acc[4], acc[5], acc[6], acc[7]);
+        if (col == 0) ml[rr] = make_float2(M, failed ? nan : L);
+        continue;
+      }
       const bool none = L == 0.f;
       const float inv = failed ? nan : (none ? 0.f : 1.f / L);
       const float ls = failed ? nan : (none ? -INFINITY : (M + log2f(L)) * 0.69314718055994530942f);
@@ -462,6 +470,10 @@ __global__ void __launch_bounds__(kTreeBlock, Tree4Cfg<D, NB>::kCtasPerSm) fa_tr
         dst[1] = make_float4(acc[4], acc[5], acc[6], acc[7]);
         if (col == 0) p.lse_part[row] = ls;
       }
+    }
+    if (p.list.solo > 1) {
+      tree_cluster_join<D>(p, xo, C::kRowStride, ml, C::kRows, bh, sg.rb);
+      return;
     }
     // the merge area may be rewritten once every row has been read
     asm volatile("bar.sync 1, %0;" ::"n"(kTreeThreads) : "memory");

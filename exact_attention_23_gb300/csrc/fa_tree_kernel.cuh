@@ -78,6 +78,53 @@ __device__ __forceinline__ void mma16816(float (&c)[4], const uint32_t (&a)[4], 
       : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
 
+// An entry in a cluster of CTAs (solo > 1): each has left its keys' part of the rows in its shared memory, fp32
+// sums `part` [rows][stride] and `ml`, a row's reference and sum of weights (a NaN where the CTA failed), and
+// takes a share of rows × 4 columns to join over all.
+template <int D>
+__device__ __forceinline__ void tree_cluster_join(const TreeParams& p, const float* part, int stride, const float2* ml,
+                                                  int rows, int bh, int rb) {
+  constexpr int kMost = 8, kPer = D / 4;  // CTAs; threads a row
+  __syncwarp();
+  cluster_sync_all();
+  const uint32_t ctas = cluster_ctas();
+  for (uint32_t x = cluster_ctarank() * kTreeThreads + threadIdx.x; x < static_cast<uint32_t>(rows) * kPer; x += ctas * kTreeThreads) {
+    const int rr = static_cast<int>(x) / kPer, col = static_cast<int>(x) % kPer * 4, r = rb * rows + rr;
+    if (r >= p.R) break;
+    float2 w[kMost];
+    float4 y[kMost];
+    float M = -INFINITY, L = 0.f, acc[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+    for (int s = 0; s < kMost; ++s) {
+      w[s] = make_float2(-INFINITY, 0.f);
+      y[s] = make_float4(0.f, 0.f, 0.f, 0.f);
+      if (s < ctas) {
+        w[s] = ld_cluster2(mapa_shared(ml + rr, s));
+        y[s] = ld_cluster4(mapa_shared(part + rr * stride + col, s));
+      }
+    }
+#pragma unroll
+    for (int s = 0; s < kMost; ++s) M = fmaxf(M, w[s].x);
+#pragma unroll
+    for (int s = 0; s < kMost; ++s) {
+      const float f = w[s].x == -INFINITY ? 0.f : ex2_approx(w[s].x - M);
+      L = fmaf(f, w[s].y, L);
+      acc[0] = fmaf(f, y[s].x, acc[0]);
+      acc[1] = fmaf(f, y[s].y, acc[1]);
+      acc[2] = fmaf(f, y[s].z, acc[2]);
+      acc[3] = fmaf(f, y[s].w, acc[3]);
+    }
+    const bool none = L == 0.f;
+    const float inv = none ? 0.f : 1.f / L;
+    const size_t row = static_cast<size_t>(bh) * p.R + r;
+    *reinterpret_cast<uint2*>(p.o + row * D + col) =
+        make_uint2(pack_bf16x2(acc[0] * inv, acc[1] * inv), pack_bf16x2(acc[2] * inv, acc[3] * inv));
+    if (col == 0) p.lse[row] = none ? -INFINITY : (M + log2f(L)) * 0.69314718055994530942f;
+  }
+  __syncwarp();
+  cluster_sync_all();  // no CTA leaves before its part has been read
+}
+
 template <int D, int RG, int MOD>
 __global__ void __launch_bounds__(kTreeBlock, TreeCfg<D>::kCtasPerSm)
     fa_tree_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
@@ -94,6 +141,7 @@ __global__ void __launch_bounds__(kTreeBlock, TreeCfg<D>::kCtasPerSm)
   __shared__ uint64_t full[C::kStages], empty[C::kStages];
   __shared__ uint32_t abort_flag;
   __shared__ float xm[3][16], xl[3][16];
+  __shared__ float2 ml[kWin ? kRows : 1];  // (solo in a cluster)
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   if (threadIdx.x == 0) {
 #pragma unroll
@@ -448,6 +496,24 @@ __global__ void __launch_bounds__(kTreeBlock, TreeCfg<D>::kCtasPerSm)
       }
     }
     const bool failed = !ok || *static_cast<volatile uint32_t*>(&abort_flag) != 0u;
+    if constexpr (kWin) {
+      if (p.list.solo > 1) {
+        if (kg == 0) {  // (into the places of the first part, which this thread has read)
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
+            const int rr = rg * 16 + qr + 8 * i;
+            if ((lane & 3) == 0) ml[rr] = make_float2(m[i], failed ? nan : l[i]);
+#pragma unroll
+            for (int x = 0; x < kDT; ++x)
+              *reinterpret_cast<float2*>(xo + (rg * (KG - 1) * 16 + qr + 8 * i) * D + x * 8 + qc) =
+                  make_float2(o[x][2 * i], o[x][2 * i + 1]);
+          }
+        }
+        static_assert(RG == 1 || KG == 2, "row rr lies at rr · D");
+        tree_cluster_join<D>(p, xo, D, ml, kRows, bh, sg.rb);
+        return;
+      }
+    }
     if (kg == 0) {
       const size_t slot = static_cast<size_t>(blockIdx.x) + sg.entry;
 #pragma unroll

@@ -5,6 +5,7 @@
 #include <cuda.h>
 #include <cuda_runtime.h>
 
+#include <algorithm>
 #include <atomic>
 
 #include "fa_mod_host.h"
@@ -28,7 +29,8 @@ cudaError_t launch_tree(const TreeLaunch& a) {
   static std::atomic<uint64_t> done[kMaxDevices / 64 + 1];
   cudaError_t e = smem_opt_in(fn, smem, done);
   if (e != cudaSuccess) return e;
-  return launch_pdl(fn, a.grid, kTreeBlock, smem, a.stream, a.tm_k, a.tm_v, a.p);
+  const unsigned cluster = (MOD & kModSink) != 0 ? std::max(a.p.list.solo, 1) : 1;
+  return launch_pdl_clusters(fn, a.grid, cluster, kTreeBlock, smem, a.stream, a.tm_k, a.tm_v, a.p);
 }
 
 // EXTRA: kModSink or nothing.
@@ -62,7 +64,7 @@ cudaError_t launch_tree4(const Tree4Launch& a) {
   static std::atomic<uint64_t> done[kMaxDevices / 64 + 1];
   const cudaError_t e = smem_opt_in(fn, smem, done);
   if (e != cudaSuccess) return e;
-  return launch_pdl(fn, a.grid, kTreeBlock, smem, a.stream, a.p);
+  return launch_pdl_clusters(fn, a.grid, static_cast<unsigned>(std::max(a.p.t.list.solo, 1)), kTreeBlock, smem, a.stream, a.p);
 }
 
 template <int D, int NB>

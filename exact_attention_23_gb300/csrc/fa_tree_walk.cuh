@@ -23,7 +23,7 @@ struct TreeList {
   int row_blocks;      // row blocks a key head
   int min_per;         // chunks a stretch has at least
   int chunk_log2;      // keys a chunk: 1 << chunk_log2
-  int solo;            // CTA c takes entry c whole: no partials, no second kernel
+  int solo;            // CTA c takes entry c whole: no partials, no second kernel (WINDOW: cluster c, of `solo` CTAs)
   int2* parts;         // [entries] the first stretch that an entry lies in, and their number
 };
 
@@ -127,7 +127,7 @@ struct TreeSegments {
   __device__ __forceinline__ void begin(const TreeList& p, const TreeReach& reach) {
     if (p.solo) {
       const int entries = p.Hkv * p.row_blocks;
-      at.b = static_cast<int>(blockIdx.x) / entries;
+      at.b = static_cast<int>(WINDOW ? cluster_id() : blockIdx.x) / entries;
       at.entry0 = at.b * entries;
       at.chunks = tree_chunks<WINDOW>(p, reach, at.b);
       pos = 0;
@@ -163,12 +163,17 @@ struct TreeSegments {
     if (p.solo) {  // (a sequence without keys has an empty segment, whose rows it writes)
       pos = 1;
       b = at.b;
-      entry = static_cast<int>(blockIdx.x);
+      entry = static_cast<int>(WINDOW ? cluster_id() : blockIdx.x);
       hk = (entry - at.entry0) / p.row_blocks;
       rb = entry - at.entry0 - hk * p.row_blocks;
       c0 = 0;
       c1 = at.chunks;
       whole = true;
+      if constexpr (WINDOW) {  // (a list has fewer than 2²⁴ chunks an entry, a cluster at most 8 CTAs)
+        const int rank = static_cast<int>(cluster_ctarank()), ctas = static_cast<int>(cluster_ctas());
+        c0 = at.chunks * rank / ctas;
+        c1 = at.chunks * (rank + 1) / ctas;
+      }
       return true;
     }
     const int entries = p.Hkv * p.row_blocks;

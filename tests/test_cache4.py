@@ -278,6 +278,25 @@ def test_long_contexts_in_many_stretches(H, d):
     _check([40000, 123, 9000, 0, 21111], H, 1, 3, 40104, d, tree=True, seed=3)
 
 
+# Entries taken by clusters of 8, 4 and 2 CTAs, as in test_window.
+@pytest.mark.gpu
+@pytest.mark.parametrize("B,H,Hkv,n,Tmax,d,window,sinks,tree,cap,bias,whole", [
+    (4, 4, 4, 1, 2000, 64, 0, 0, False, 0.0, False, True),           # 16 entries
+    (4, 8, 4, 8, 2000, 64, 0, 0, True, 30.0, True, True),            # 16, of 16 rows
+    (3, 4, 1, 2, 3200, 128, 1900, 130, False, 0.0, True, True),
+    (6, 16, 2, 5, 1600, 128, 0, 0, True, 0.0, False, True),          # 40 rows: three blocks of 16
+    (20, 4, 4, 1, 1400, 64, 0, 0, False, 30.0, False, True),         # 80
+    (20, 4, 4, 1, 904, 128, 0, 0, False, 0.0, True, True),
+    (75, 2, 2, 1, 640, 128, 500, 4, False, 0.0, False, True),        # 150
+    (80, 2, 2, 1, 1040, 64, 0, 0, False, 0.0, False, True),
+    (3, 4, 4, 1, 20000, 128, 15000, 4, False, 0.0, False, False),
+])
+def test_clusters(B, H, Hkv, n, Tmax, d, window, sinks, tree, cap, bias, whole):
+    assert (fa.fa_fwd_tree4_workspace_size(B, H, Hkv, n, Tmax, d, window, sinks) == 1) == whole
+    ctx = [Tmax - n, -1, 0, 129, Tmax // 2, 250, Tmax, 1] * 10
+    _check(ctx[:B], H, Hkv, n, Tmax, d, window, sinks, tree, cap, bias, seed=B)
+
+
 @pytest.mark.gpu
 @pytest.mark.parametrize("Tmax", [208, 5000])
 def test_many_sequences(Tmax):

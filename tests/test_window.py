@@ -419,6 +419,26 @@ def test_long_contexts_in_many_stretches(H, d):
     _check_tree([40000, 123, 9000, 0, 21111], H, 1, 3, 40100, d, 6000, 300, True, seed=3)
 
 
+# Entries taken by clusters of 8, 4 and 2 CTAs, which need no workspace, with contexts that leave some of a
+# cluster without a chunk or all of it, and long windows that go in stretches.
+@pytest.mark.gpu
+@pytest.mark.parametrize("B,H,Hkv,n,Tmax,d,window,sinks,tree,cap,bias,whole", [
+    (4, 4, 4, 1, 1200, 64, 1100, 3, False, 0.0, False, True),        # 16 entries
+    (4, 16, 2, 4, 1200, 64, 700, 130, True, 0.0, True, True),        # 8, of 32 rows
+    (5, 8, 1, 4, 900, 128, 800, 0, True, 30.0, False, True),
+    (15, 4, 4, 1, 700, 64, 600, 4, False, 30.0, True, True),         # 60
+    (20, 6, 3, 3, 600, 128, 300, 4, True, 0.0, False, True),
+    (75, 2, 2, 1, 400, 64, 300, 1, False, 0.0, False, True),         # 150
+    (66, 8, 2, 1, 500, 128, 300, 4, False, 0.0, True, True),
+    (3, 4, 4, 1, 9000, 64, 8000, 4, False, 0.0, False, False),
+    (3, 4, 2, 8, 9000, 128, 7000, 4, True, 0.0, False, False),
+])
+def test_clusters(B, H, Hkv, n, Tmax, d, window, sinks, tree, cap, bias, whole):
+    assert (fa.fa_fwd_tree_window_workspace_size(B, H, Hkv, n, Tmax, d, window, sinks) == 1) == whole
+    ctx = [Tmax - n, -1, 0, 65, Tmax // 2, 130, Tmax, 1] * 10
+    _check_tree(ctx[:B], H, Hkv, n, Tmax, d, window, sinks, tree, cap, bias, seed=B)
+
+
 @pytest.mark.gpu
 @pytest.mark.parametrize("Tmax", [210, 5000])
 def test_many_sequences(Tmax):
