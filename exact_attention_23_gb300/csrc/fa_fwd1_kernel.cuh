@@ -135,6 +135,52 @@ struct NoSegments {
 template <int MOD>
 using SegmentsOf = std::conditional_t<(MOD & kModTree) != 0, TreeSegments<(MOD & kModSink) != 0>, NoSegments>;
 
+// TREE, an entry in a cluster of CTAs: the rows from the CTAs' partial ones (normalised, pieces swizzled) and their
+// LSE (`lse`, the first of four floats a row), each CTA a share of rows × 4 columns.
+template <int D>
+__device__ __forceinline__ void tree_cluster_rows(const FwdParams& p, const uint8_t* part, const uint8_t* lse, uint32_t threads) {
+  constexpr int kMost = 8, kPer = D / 4;  // CTAs; threads a row
+  __syncwarp();
+  cluster_sync_all();
+  const uint32_t ctas = cluster_ctas(), entry = cluster_id();
+  const uint32_t bh = entry / static_cast<uint32_t>(p.mod.list.row_blocks), rb = entry - bh * p.mod.list.row_blocks;
+  const uint32_t rows = min(static_cast<uint32_t>(kBlockM), p.T - rb * kBlockM);
+  for (uint32_t x = cluster_ctarank() * threads + threadIdx.x; x < rows * kPer; x += ctas * threads) {
+    const uint32_t rr = x / kPer, piece = x % kPer;
+    float w[kMost], M = -INFINITY, L = 0.f, acc[4] = {0.f, 0.f, 0.f, 0.f};
+    float4 y[kMost];
+#pragma unroll
+    for (int s = 0; s < kMost; ++s) {
+      w[s] = -INFINITY;
+      y[s] = make_float4(0.f, 0.f, 0.f, 0.f);
+      if (s < ctas) {
+        w[s] = ld_cluster1(mapa_shared(lse + rr * 16, s));
+        y[s] = ld_cluster4(mapa_shared(part + rr * (D * 4) + ((piece ^ (rr & 7)) << 4), s));
+      }
+    }
+#pragma unroll
+    for (int s = 0; s < kMost; ++s) M = fmaxf(M, w[s]);
+    const float mu = M == -INFINITY ? 0.f : M;
+#pragma unroll
+    for (int s = 0; s < kMost; ++s) {
+      const float f = ex2_approx((w[s] - mu) * 1.4426950408889634f);
+      L += f;
+      if (f == 0.f) continue;  // (a CTA without keys may hold anything)
+      acc[0] = fmaf(f, y[s].x, acc[0]);
+      acc[1] = fmaf(f, y[s].y, acc[1]);
+      acc[2] = fmaf(f, y[s].z, acc[2]);
+      acc[3] = fmaf(f, y[s].w, acc[3]);
+    }
+    const float inv = L == 0.f ? 0.f : 1.f / L;
+    const size_t row = static_cast<size_t>(bh) * p.T + rb * kBlockM + rr;
+    *reinterpret_cast<uint2*>(p.o + row * D + piece * 4) =
+        make_uint2(pack_bf16x2(acc[0] * inv, acc[1] * inv), pack_bf16x2(acc[2] * inv, acc[3] * inv));
+    if (piece == 0) p.lse[row] = L == 0.f ? -INFINITY : mu + log2f(L) * 0.69314718055994530942f;
+  }
+  __syncwarp();
+  cluster_sync_all();  // no CTA leaves before its part has been read
+}
+
 template <bool CAUSAL, bool GEN, int MOD, typename Segments>
 __device__ __forceinline__ Unit unit1_of(const FwdParams& p, int L, const Segments& sg) {
   if constexpr ((MOD & kModTree) != 0) {
@@ -198,6 +244,8 @@ __global__ void __launch_bounds__(Cfg1<D, (MOD & kModRef) != 0>::kThreads, 1)
   constexpr bool kRefRest = (MOD & kModRest) != 0;        // … with o's rest
   constexpr bool kRest = MOD != 0 && !kTree && (!kRef || kRefRest);  // o's rest may be asked for
   constexpr bool kSink = (MOD & kModSink) != 0;  // a second interval a row (TREE: a window and sinks)
+  constexpr bool kCluster = kTree && kSink;  // an entry may be a cluster's
+  static_assert(!kCluster || C::kQBufs * C::kTileBytes == kBlockM * D * 4, "partial rows in Q's place");
   constexpr bool kXform = (MOD & (kModCap | kModBias)) != 0;  // scores are modified before the softmax
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
@@ -474,12 +522,22 @@ __global__ void __launch_bounds__(Cfg1<D, (MOD & kModRef) != 0>::kThreads, 1)
       int r0, bh;
       bool in_range, partial;
     };
+    // (TREE: an entry in a cluster of CTAs leaves its partial rows in the place of Q, as fp32 with the 16-byte
+    // pieces of row r at piece ^ (r mod 8), and their LSE in that of the deferred records.)
+    const bool clustered = kCluster && p.mod.list.solo > 1;
+    const int swz = clustered ? row & 7 : 0;
+    auto part_row = [&](const RowOut& w) {
+      if constexpr (kCluster) {
+        if (clustered) return reinterpret_cast<float4*>(smem + C::kQOff + row * D * 4);
+      }
+      return reinterpret_cast<float4*>(p.o_part + w.part_idx * D);
+    };
     auto row_out = [&](int bh, int split, int r0) {
       const int q_row = r0 + lane;
       if constexpr (kTree)  // split: the partial's slot, or −1
         return RowOut{static_cast<size_t>(bh) * static_cast<size_t>(p.T) + static_cast<size_t>(q_row),
                       static_cast<size_t>(split) * kBlockM + static_cast<size_t>(row), r0, bh,
-                      q_row < p.T, split >= 0};
+                      q_row < p.T, split >= 0 || clustered};
       return RowOut{static_cast<size_t>(bh) * static_cast<size_t>(p.T) + static_cast<size_t>(q_row),
                     (static_cast<size_t>(split) * p.BH + bh) * static_cast<size_t>(p.T) +
                         static_cast<size_t>(q_row),
@@ -501,14 +559,15 @@ __global__ void __launch_bounds__(Cfg1<D, (MOD & kModRef) != 0>::kThreads, 1)
     const int c_out = half * kOutCols;
     auto write_lse = [&](const RowOut& w, float v) {
       if (!w.in_range || half != 0) return;
-      if (w.partial) p.lse_part[w.part_idx] = v;
+      if (kCluster && clustered) reinterpret_cast<float*>(smem + C::kPendOff)[4 * row] = v;
+      else if (w.partial) p.lse_part[w.part_idx] = v;
       else p.lse[w.row_idx] = v;
     };
     // A row that saw no key (general form: O = 0, LSE = −∞) or a failed unit (NaN).
     auto write_const_row = [&](const RowOut& w, uint32_t bits) {
       if (!w.in_range) return;
       if (w.partial) {
-        float4* prow = reinterpret_cast<float4*>(p.o_part + w.part_idx * D + c_out);
+        float4* prow = part_row(w) + c_out / 4;
         const float f = u2f(bits);
 #pragma unroll
         for (int t = 0; t < kOutCols / 4; ++t) prow[t] = make_float4(f, f, f, f);
@@ -582,10 +641,10 @@ __global__ void __launch_bounds__(Cfg1<D, (MOD & kModRef) != 0>::kThreads, 1)
         if (lane == 0) mbar_arrive(&bars->o_free);
         if (w.in_range) {
           if (w.partial) {
-            float4* prow = reinterpret_cast<float4*>(p.o_part + w.part_idx * D + c_out);
+            float4* prow = part_row(w) + c_out / 4;
 #pragma unroll
             for (int t = 0; t < kOutCols / 4; ++t)
-              prow[t] = make_float4(u2f(o[4 * t]) * inv_l, u2f(o[4 * t + 1]) * inv_l,
+              prow[t ^ swz] = make_float4(u2f(o[4 * t]) * inv_l, u2f(o[4 * t + 1]) * inv_l,
                                     u2f(o[4 * t + 2]) * inv_l, u2f(o[4 * t + 3]) * inv_l);
           } else {
             uint4* orow = reinterpret_cast<uint4*>(p.o + w.row_idx * D + c_out);
@@ -643,10 +702,10 @@ __global__ void __launch_bounds__(Cfg1<D, (MOD & kModRef) != 0>::kThreads, 1)
         if (lane == 0) mbar_arrive(&bars->o_free);
         if (w.in_range) {
           if (w.partial) {
-            float4* prow = reinterpret_cast<float4*>(p.o_part + w.part_idx * D + c_out);
+            float4* prow = part_row(w) + c_out / 4;
 #pragma unroll
             for (int t = 0; t < 8; ++t)
-              prow[t] = make_float4(fmaf(u2f(o0[4 * t]), w0, u2f(o1[4 * t]) * w1),
+              prow[t ^ swz] = make_float4(fmaf(u2f(o0[4 * t]), w0, u2f(o1[4 * t]) * w1),
                                     fmaf(u2f(o0[4 * t + 1]), w0, u2f(o1[4 * t + 1]) * w1),
                                     fmaf(u2f(o0[4 * t + 2]), w0, u2f(o1[4 * t + 2]) * w1),
                                     fmaf(u2f(o0[4 * t + 3]), w0, u2f(o1[4 * t + 3]) * w1));
@@ -695,10 +754,10 @@ __global__ void __launch_bounds__(Cfg1<D, (MOD & kModRef) != 0>::kThreads, 1)
           }
           if (GEN && w.partial) {
             if (w.in_range) {
-              float4* prow = reinterpret_cast<float4*>(p.o_part + w.part_idx * D + hb * 64);
+              float4* prow = part_row(w) + hb * 16;
 #pragma unroll
               for (int t = 0; t < 16; ++t)
-                prow[t] = make_float4(u2f(o[4 * t]) * inv_l, u2f(o[4 * t + 1]) * inv_l,
+                prow[t ^ swz] = make_float4(u2f(o[4 * t]) * inv_l, u2f(o[4 * t + 1]) * inv_l,
                                       u2f(o[4 * t + 2]) * inv_l, u2f(o[4 * t + 3]) * inv_l);
             }
             continue;
@@ -1221,6 +1280,9 @@ __global__ void __launch_bounds__(Cfg1<D, (MOD & kModRef) != 0>::kThreads, 1)
     __syncwarp();
     tc_fence_after_sync();
     tmem_dealloc(tmem, 512);
+  }
+  if constexpr (kCluster) {
+    if (p.mod.list.solo > 1) tree_cluster_rows<D>(p, smem + C::kQOff, smem + C::kPendOff, C::kThreads);
   }
 }
 

@@ -1,6 +1,7 @@
 // Launches of the MOD kernels (modified scores), shared by their instantiation files. Internal.
 #pragma once
 
+#include <algorithm>
 #include <atomic>
 
 #include "fa_launch.h"
@@ -16,7 +17,9 @@ cudaError_t launch_fwd_mod(const FwdLaunch& a) {
   const int smem = C::kSmemBytes;
   const cudaError_t e = smem_opt_in(fn, smem, done);
   if (e != cudaSuccess) return e;
-  return launch_pdl(fn, a.grid, C::kThreads, smem, a.stream, a.tm_q, a.tm_k, a.tm_v, a.tm_o, a.p);
+  constexpr bool kClusters = (MOD & kModTree) != 0 && (MOD & kModSink) != 0;
+  return launch_pdl_clusters(fn, a.grid, kClusters ? static_cast<unsigned>(std::max(a.p.mod.list.solo, 1)) : 1u, C::kThreads,
+                             smem, a.stream, a.tm_q, a.tm_k, a.tm_v, a.tm_o, a.p);
 }
 
 // The same on the pair kernel (two query tiles a CTA; a.p.tiles_per_cta = 2).

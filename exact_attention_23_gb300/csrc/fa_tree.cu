@@ -47,12 +47,15 @@ constexpr int kMinPer = 2, kMinPerWide = 1;
 //                              (its contexts are as unequal, but what is left of them is not)
 //   4 bits, 128-key chunks     d64: 48, 4: 7.2 / 6.0, 8: 7.5 / 8.7;  192, 8: 13.1 / 9.9;  d128: 128, 6: 10.9 / 9.2
 // With a window or in 4 bits, such an entry is taken by a cluster of CTAs, which join their parts through shared memory:
-// as many as fit the GPU at once (2, 4 or 8. Clusters that do not all fit wait: of 456 places pairs find 456, fours
-// 440, sevens 413, eights 408; 64 entries in sevens 9.8 -> 13.1 µs, 152 in fours on 608 places 19.2 -> 23.9). µs in
-// stretches / in clusters, the chunks of a CTA in these in brackets, every context full:
+// as many as fit the GPU at once. (Clusters that do not all fit wait: of 152 places, one an SM, pairs find 152, threes
+// 138, fours 144, sixes 138, eights 120, of 304 304, 291, 296, 276, 288; 152 entries in fours on 608 places 19.2 ->
+// 23.9 µs, 16 in eights on 152 21.6 -> 28.9.) µs in stretches / in clusters, the chunks of a CTA in these in brackets,
+// every context full:
 //   a window, d64              8, 18: 7.8 / 6.3 (3), 66: 10.3 / 9.3 (9);  40, 34: 12.1 / 9.4 (5);  96, 18: 12.9 / 9.7 (5);
 //                              200, 66: 48.4 / 39.0 (33)
 //   d128                       8, 18: 9.6 / 8.6 (3), 66: 12.5 / 13.8 (9);  24, 34: 14.7 / 11.8 (5);  104, 34: 29.1 / 25.6 (17)
+//   wide, d64, 128 rows        4, 34: 17.4 / 11.3 (5);  32, 16: 15.5 / 12.2 (4), 66: 28.6 / 23.3 (17);  64, 34: 30.6 / 23.7 (17)
+//   d128, 64 rows              4, 34: 18.4 / 13.9 (5), 66: 19.4 / 18.1 (9);  32, 34: 27.0 / 23.2 (9);  64, 66: 60.5 / 58.1 (33)
 //   4 bits, full / contexts from none to full (there it is the longest that counts)
 //   d64, to 8 rows             24, 32: 9.3 / 7.8 (4), 8.8 / 7.3;  40, 64: 15.2 / 15.8 (8), 12.3 / 12.2;  104, 64: 24.6 / 24.1
 //                              (13), 17.8 / 19.3
@@ -68,19 +71,23 @@ struct TreeForm {
 
 int join_chunks(bool wide_rows, int d, const TreeForm& form) {
   if (form.four) return d == 64 ? 3 : 2;
-  return wide_rows ? (d == 64 ? 5 : 4) : d == 64 ? (form.window > 0 ? 10 : 7) : 5;
+  if (form.window > 0) return wide_rows ? 7 : d == 64 ? 10 : 5;
+  return wide_rows ? (d == 64 ? 5 : 4) : d == 64 ? 7 : 5;
 }
 int solo_chunks(bool wide_rows, int d, int rows_log2, const TreeForm& form) {
   if (form.four) return rows_log2 > 3 ? 24 : d == 64 ? 8 : 6;
-  return wide_rows ? 12 : form.window > 0 ? 34 : 24;
+  return form.window > 0 ? 34 : wide_rows ? 12 : 24;
 }
-// CTAs a cluster, where `fit` fit the GPU (two or three chunks are one CTA's: 128 entries of two in 4 bits 4.9 µs, by
-// twos 5.5; 8 of four 6.0, by fours 4.9).
-int cluster_ctas(long long entries, long long chunks, long long fit) {
-  if (chunks < 4) return 1;
-  int ctas = entries * 2 <= fit ? 2 : 1;
-  while (ctas > 1 && ctas < 8 && ctas * 2 <= chunks && entries * ctas * 2 <= fit - fit / (ctas == 2 ? 16 : 8)) ctas *= 2;
-  return ctas;
+// CTAs a cluster, where `fit` fit the GPU: the most that leave every cluster a place at once. (Few chunks are one CTA's:
+// 128 entries of two in 4 bits 4.9 µs, by twos 5.5; 8 of four 6.0, by fours 4.9; wide, d128, 64 entries of four 11.2,
+// by twos 12.5; 4 of four 10.2, by fours 8.9.)
+int cluster_ctas(bool wide_rows, long long entries, long long chunks, long long fit) {
+  if (chunks < (wide_rows && entries > 16 ? 8 : 4)) return 1;
+  // (and the places that they find, in sixteenths)
+  const int most[5][2] = {{8, wide_rows ? 12 : 14}, {6, 14}, {4, 15}, {3, 14}, {2, 16}};
+  for (const auto& m : most)
+    if (m[0] <= chunks && entries * m[0] <= fit * m[1] / 16) return m[0];
+  return 1;
 }
 
 struct TreeSizes {
@@ -120,8 +127,7 @@ bool tree_sizes(int B, int H, int Hkv, int Tq, int Tmax, int d, const TreeForm& 
   const long long most = (z->entries * chunks + z->min_per - 1) / z->min_per;
   const long long fit = static_cast<long long>(sms) * (is_wide ? 1 : form.four ? tree4_ctas(d, 1 << z->rows_log2) : tree_ctas(d));
   const long long per = std::max<long long>(z->min_per, (z->entries * chunks + fit - 1) / fit);  // a stretch's
-  const bool streams = !is_wide && (form.four || form.window > 0);
-  const int ctas = streams ? cluster_ctas(z->entries, chunks, fit) : 1;
+  const int ctas = form.four || form.window > 0 ? cluster_ctas(is_wide, z->entries, chunks, fit) : 1;
   const long long most_chunks = (chunks + ctas - 1) / ctas;  // a CTA's
   const bool whole = z->entries <= fit && most_chunks <= per + join_chunks(is_wide, d, form) &&
                      most_chunks <= solo_chunks(is_wide, d, z->rows_log2, form);

@@ -11,7 +11,7 @@
 //
 // Measured: B8 H16 Hkv4, one token, contexts to 16384, d128 (59 MB) 24.0 µs, to 60000 (217 MB) 56.1, 3.9 TB/s (41 with
 // operands left unmade: shifts, masks and multiply-adds are what it spends on top of streaming); B4 12 heads,
-// 8 drafts, to 4000, d64 13.5. With the query rows on the 16 side and 16 of them always: 36.4 and 17.4.
+// 8 drafts, to 4000, d64 10.6 (in clusters of eight CTAs; 13.5 in stretches). With the query rows on the 16 side and 16 of them always: 36.4 and 17.4.
 // Three CTAs an SM, four at d = 64, and four tiles a ring for 8 rows (16384 keys to 60000: three 24.0 and 56.1, two
 // 23.5 and 59.2); two CTAs for 16, whose registers spill otherwise.
 //

@@ -8,7 +8,8 @@
 // numbered in a row, and CTA c takes the c-th of equal stretches, whatever the lengths are (they
 // live on the device). A stretch crosses sequences in segments; a sequence that lies in several
 // stretches leaves one partial (normalised fp32 rows and LSE) per stretch for
-// fa_tree_combine_kernel. (Caches short enough for one CTA an entry go without: solo.) Stretch c's segment of list entry e has slot c + e: from one segment to
+// fa_tree_combine_kernel. (Caches short enough for one CTA an entry, with a window
+// or in 4 bits a cluster of them, go without: solo.) Stretch c's segment of list entry e has slot c + e: from one segment to
 // the next c or e grows, so slots never meet.
 #pragma once
 

@@ -278,7 +278,7 @@ def test_long_contexts_in_many_stretches(H, d):
     _check([40000, 123, 9000, 0, 21111], H, 1, 3, 40104, d, tree=True, seed=3)
 
 
-# Entries taken by clusters of 8, 4 and 2 CTAs, as in test_window.
+# Entries taken by clusters of 8, 6, 4, 3 and 2 CTAs, as in test_window.
 @pytest.mark.gpu
 @pytest.mark.parametrize("B,H,Hkv,n,Tmax,d,window,sinks,tree,cap,bias,whole", [
     (4, 4, 4, 1, 2000, 64, 0, 0, False, 0.0, False, True),           # 16 entries
@@ -289,6 +289,9 @@ def test_long_contexts_in_many_stretches(H, d):
     (20, 4, 4, 1, 904, 128, 0, 0, False, 0.0, True, True),
     (75, 2, 2, 1, 640, 128, 500, 4, False, 0.0, False, True),        # 150
     (80, 2, 2, 1, 1040, 64, 0, 0, False, 0.0, False, True),
+    (15, 2, 2, 9, 800, 64, 0, 0, True, 0.0, False, True),            # 30, of 9 rows
+    (17, 4, 4, 1, 1400, 128, 0, 0, False, 30.0, False, True),        # 68, by fours
+    (33, 4, 4, 1, 1040, 64, 0, 0, False, 0.0, False, True),
     (3, 4, 4, 1, 20000, 128, 15000, 4, False, 0.0, False, False),
 ])
 def test_clusters(B, H, Hkv, n, Tmax, d, window, sinks, tree, cap, bias, whole):

@@ -419,7 +419,7 @@ def test_long_contexts_in_many_stretches(H, d):
     _check_tree([40000, 123, 9000, 0, 21111], H, 1, 3, 40100, d, 6000, 300, True, seed=3)
 
 
-# Entries taken by clusters of 8, 4 and 2 CTAs, which need no workspace, with contexts that leave some of a
+# Entries taken by clusters of 8, 6, 4, 3 and 2 CTAs, which need no workspace, with contexts that leave some of a
 # cluster without a chunk or all of it, and long windows that go in stretches.
 @pytest.mark.gpu
 @pytest.mark.parametrize("B,H,Hkv,n,Tmax,d,window,sinks,tree,cap,bias,whole", [
@@ -430,8 +430,17 @@ def test_long_contexts_in_many_stretches(H, d):
     (20, 6, 3, 3, 600, 128, 300, 4, True, 0.0, False, True),
     (75, 2, 2, 1, 400, 64, 300, 1, False, 0.0, False, True),         # 150
     (66, 8, 2, 1, 500, 128, 300, 4, False, 0.0, True, True),
+    (20, 4, 4, 1, 700, 64, 600, 4, False, 0.0, True, True),          # 80, by fours
+    (26, 6, 3, 3, 700, 128, 600, 4, True, 30.0, False, True),        # 78, by threes
+    (2, 16, 4, 16, 2600, 128, 2400, 4, True, 0.0, True, True),       # of 64 rows
+    (4, 16, 4, 13, 1600, 128, 1400, 200, False, 30.0, False, True),  # 16, by sixes
+    (10, 12, 4, 12, 1500, 64, 1300, 4, True, 80.0, False, True),     # 40, by threes
+    (16, 16, 4, 20, 1200, 64, 1100, 4, True, 30.0, False, True),     # 64, by twos
+    (1, 12, 1, 50, 2200, 64, 2000, 0, False, 30.0, True, True),      # 600 rows
+    (2, 9, 1, 16, 2200, 128, 2000, 1, False, 0.0, False, True),
     (3, 4, 4, 1, 9000, 64, 8000, 4, False, 0.0, False, False),
     (3, 4, 2, 8, 9000, 128, 7000, 4, True, 0.0, False, False),
+    (1, 8, 1, 16, 18000, 64, 16000, 4, False, 0.0, False, False),
 ])
 def test_clusters(B, H, Hkv, n, Tmax, d, window, sinks, tree, cap, bias, whole):
     assert (fa.fa_fwd_tree_window_workspace_size(B, H, Hkv, n, Tmax, d, window, sinks) == 1) == whole
