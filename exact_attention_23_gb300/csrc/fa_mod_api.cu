@@ -150,9 +150,11 @@ __device__ __forceinline__ void doc_bits(const int* ids, int i0, int end, uint32
 // has at most 32, so that rows are written side by side: T 16384
 // 17.3 -> 12.0 µs, with sinks 42.6 -> 16.1, half of that the lengths below being made once) and their extremes, the query tiles
 // that see it, and its place among the tiles by the number it has to walk (a count of the tiles before
-// it: n_t² comparisons, which at 16384 tokens are 4 a lane and tile). Latency is all it costs; the
+// it: n_t² comparisons, which at 16384 tokens are 4 a lane and tile). The
 // tiles' extremes are kept in shared memory up to kVisTiles of them. WINDOW: rows see the last
 // `window` keys at most; SINK: and the first `sinks` of their document (fa_visible_window).
+// Long sequences of a small batch go to a cluster of CTAs a sequence, each with every `ctas`-th tile: all find the
+// documents, and tell one another of their tiles through shared memory.
 template <bool WINDOW, bool SINK>
 __global__ void __launch_bounds__(kVisThreads) fa_visible_kernel(const VisibleParams p) {
   __shared__ int s_last[kVisThreads / 32], s_first[kVisThreads / 32];
@@ -166,8 +168,9 @@ __global__ void __launch_bounds__(kVisThreads) fa_visible_kernel(const VisiblePa
   __shared__ int4 s_four[kVisThreads];
   pdl_wait();
   pdl_launch_dependents();
-  const int b = blockIdx.x, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  constexpr int kWarps = kVisThreads / 32;
+  const int ctas = static_cast<int>(cluster_ctas()), rank = static_cast<int>(cluster_ctarank());
+  const int b = static_cast<int>(cluster_id()), tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int step = ctas * (kVisThreads / 32), tile0 = rank + ctas * warp;  // a warp's tiles
   const int T = p.T, n_t = p.n_t;
   const long long T_pad = static_cast<long long>(n_t) * 128;
   const int* ids = p.ids ? p.ids + static_cast<size_t>(b) * T : nullptr;
@@ -180,9 +183,21 @@ __global__ void __launch_bounds__(kVisThreads) fa_visible_kernel(const VisiblePa
     far = n_t <= kVisTiles ? s_far : p.far + static_cast<size_t>(b) * n_t;
     near = n_t <= kVisTiles ? s_near : p.near + static_cast<size_t>(b) * n_t;
     sink_rows = p.sink_rows + static_cast<size_t>(b) * T_pad;
-    for (int t = tid; t < n_t; t += kVisThreads) far[t] = 0;
+    for (int t = rank + ctas * tid; t < n_t; t += ctas * kVisThreads) far[t] = 0;
   }
   if (tid == 0) s_pad = n_t;
+  if (ctas > 1) {  // (no word from another CTA before its places are ready)
+    __syncwarp();
+    cluster_arrive_all();
+  }
+  auto sync_all = [&]() {
+    if (ctas > 1) {
+      __syncwarp();
+      cluster_sync_all();
+    } else {
+      __syncthreads();
+    }
+  };
   const long long seg = (T_pad + kVisThreads - 1) / kVisThreads;
   const int a0 = static_cast<int>(min(static_cast<long long>(T), tid * seg));
   const int a1 = static_cast<int>(min(static_cast<long long>(T), (tid + 1) * seg));
@@ -272,8 +287,9 @@ __global__ void __launch_bounds__(kVisThreads) fa_visible_kernel(const VisiblePa
     if constexpr (SINK) sink_rows[i] = make_int2(0, 0);
   }
   __syncthreads();
+  if (ctas > 1) cluster_wait_all();
   const size_t t0 = static_cast<size_t>(b) * n_t;
-  for (int t = warp; t < n_t; t += kWarps) {
+  for (int t = tile0; t < n_t; t += step) {
     int lo_min = T, hi_max = 0, lo_max = 0, hi_min = T;
     int2 sinks[4];
     bool pads_here = false;
@@ -308,11 +324,13 @@ __global__ void __launch_bounds__(kVisThreads) fa_visible_kernel(const VisiblePa
     hi_min = __reduce_min_sync(0xffffffffu, hi_min);
     lo_max = __reduce_max_sync(0xffffffffu, lo_max);
     hi_max = __reduce_max_sync(0xffffffffu, hi_max);
-    if (__any_sync(0xffffffffu, pads_here) && lane == 0) atomicMin(&s_pad, t);
+    if (__any_sync(0xffffffffu, pads_here) && lane < ctas) red_min_cluster(mapa_shared(&s_pad, lane), t);
+    const int2 sp = hi_max > lo_min ? make_int2(lo_min, hi_max) : make_int2(0, 0);
     if (lane == 0) {
       p.whole[t0 + t] = make_int2(lo_max, hi_min);
-      span[t] = hi_max > lo_min ? make_int2(lo_min, hi_max) : make_int2(0, 0);
+      span[t] = sp;
     }
+    if (lane < ctas && lane != rank) st_cluster2(mapa_shared(s_span + t, lane), sp);
     if constexpr (SINK) {
       // The tiles with sinks before the walk's first. (Documents that start within it have theirs in the walk.)
       const int kb = lo_min >> 7;
@@ -327,12 +345,18 @@ __global__ void __launch_bounds__(kVisThreads) fa_visible_kernel(const VisiblePa
       }
       first_sink = __reduce_min_sync(0xffffffffu, first_sink);
       past = __reduce_max_sync(0xffffffffu, past);
-      if (lane == 0) near[t] = past > 0 ? make_int2(first_sink >> 7, min((past + 127) >> 7, kb)) : make_int2(0, 0);
+      const int2 nr = past > 0 ? make_int2(first_sink >> 7, min((past + 127) >> 7, kb)) : make_int2(0, 0);
+      if (lane == 0) near[t] = nr;
+      __syncwarp();
+      if (lane < ctas && lane != rank) {
+        st_cluster2(mapa_shared(s_near + t, lane), nr);
+        st_cluster1(mapa_shared(s_far + t, lane), far[t]);
+      }
     }
   }
-  __syncthreads();
+  sync_all();
   const int padded = s_pad;
-  for (int t = warp; t < n_t; t += kWarps) {
+  for (int t = tile0; t < n_t; t += step) {
     // the query tiles whose rows see a key of this tile
     int f = n_t, l = 0;
     const int k0 = t * 128;
@@ -379,12 +403,18 @@ __global__ void __launch_bounds__(kVisThreads) fa_visible_kernel(const VisiblePa
   };
   const bool kept = n_t > 32 && n_t <= kVisTiles;  // (few: made where they are looked at, one a lane)
   if (kept) {
-    if (tid < n_t) s_four[tid] = lengths_of(tid);
-    __syncthreads();
+    const int t = rank + ctas * tid;
+    if (t < n_t) {
+      const int4 x = lengths_of(t);
+      s_four[t] = x;
+      for (int c = 0; c < ctas; ++c)
+        if (c != rank) st_cluster4(mapa_shared(s_four + t, c), x);
+    }
+    sync_all();
   }
   auto lengths = [&](int t) { return kept ? s_four[t] : lengths_of(t); };
   int n_pieces = 0, n_cuts = 0;
-  for (int t = warp; t < n_t; t += kWarps) {
+  for (int t = tile0; t < n_t; t += step) {
     const int2 s = span[t], k = seen[t];
     const int kb = s.x >> 7, ke = (s.y + 127) >> 7;
     const int4 me = lengths(t);
@@ -438,7 +468,7 @@ __global__ void __launch_bounds__(kVisThreads) fa_visible_kernel(const VisiblePa
     }
   }
   if constexpr (SINK) {
-    if (warp == 0) {  // (it has had tile 0)
+    if (tile0 == 0) {  // (it has had one)
       for (int i = n_pieces + lane; i < p.n_rec; i += 32) {
         int4* out = p.pieces + (static_cast<size_t>(b) * p.n_rec + i) * 2;
         out[0] = make_int4(n_t, 0, 0, 2 * n_t);
@@ -447,7 +477,7 @@ __global__ void __launch_bounds__(kVisThreads) fa_visible_kernel(const VisiblePa
       for (int i = n_cuts + lane; i < p.n_cut; i += 32) p.cuts[static_cast<size_t>(b) * p.n_cut + i] = make_int4(0, 0, 0, 0);
     }
   }
-  for (int t = warp; t < n_p; t += kWarps) {
+  for (int t = tile0; t < n_p; t += step) {
     const int2 a = walk(2 * t), c = walk(2 * t + 1);
     const int n = lengths(t).w;
     int r = 0;
@@ -564,8 +594,16 @@ int make_visible(const int* doc_ids, const int* prefix_len, int prefix_per_token
       fn = &fa::fa_visible_kernel<true, true>;
     }
   }
-  const cudaError_t e = fa::launch_pdl(fn, static_cast<unsigned>(B), fa::kVisThreads, 0,
-                                       static_cast<cudaStream_t>(stream), p);
+  // A cluster a sequence from 4097 to 32768 tokens, of as many CTAs as leave every cluster a place (sms SMs: pairs
+  // find them all, fours 144 of 152, eights 120; 16 eights 6.8 -> 13 µs). One CTA -> eight, µs: causal T8192 7.6 ->
+  // 5.3, T16384 12.5 -> 5.6, T32768 24.7 -> 7.0; a window and sinks 10.0 -> 6.3, 17.1 -> 6.8, 34.9 -> 8.8; documents of
+  // 700 9.2 -> 6.9, 17.3 -> 10.3, 41.6 -> 24.1 (which all CTAs look for).
+  unsigned ctas = 1;
+  if (seg <= 32 && p.n_t > 32)
+    for (const unsigned c : {2u, 4u, 8u})
+      if (B <= sms * (c == 2 ? 16 : c == 4 ? 15 : 12) / 16 / static_cast<int>(c)) ctas = c;
+  const cudaError_t e = fa::launch_pdl_clusters(fn, static_cast<unsigned>(B) * ctas, ctas, fa::kVisThreads, 0,
+                                                static_cast<cudaStream_t>(stream), p);
   return e == cudaSuccess ? FA_OK : FA_ERR_LAUNCH;
 }
 

@@ -605,7 +605,9 @@ __device__ __forceinline__ uint32_t cluster_id() {
   asm volatile("mov.u32 %0, %%clusterid.x;" : "=r"(r));
   return r;
 }
-// Every thread of every CTA of the cluster (release / acquire ordering).
+// Every thread of every CTA of the cluster (release / acquire ordering), in two halves or at once.
+__device__ __forceinline__ void cluster_arrive_all() { asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory"); }
+__device__ __forceinline__ void cluster_wait_all() { asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory"); }
 __device__ __forceinline__ void cluster_sync_all() {
   asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
@@ -631,6 +633,20 @@ __device__ __forceinline__ float4 ld_cluster4(uint32_t at) {
   asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
                : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "r"(at) : "memory");
   return v;
+}
+// Stores to it, and the smaller of it and v.
+__device__ __forceinline__ void st_cluster1(uint32_t at, int v) {
+  asm volatile("st.shared::cluster.s32 [%0], %1;" :: "r"(at), "r"(v) : "memory");
+}
+__device__ __forceinline__ void st_cluster2(uint32_t at, int2 v) {
+  asm volatile("st.shared::cluster.v2.s32 [%0], {%1, %2};" :: "r"(at), "r"(v.x), "r"(v.y) : "memory");
+}
+__device__ __forceinline__ void st_cluster4(uint32_t at, int4 v) {
+  asm volatile("st.shared::cluster.v4.s32 [%0], {%1, %2, %3, %4};" :: "r"(at), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w)
+               : "memory");
+}
+__device__ __forceinline__ void red_min_cluster(uint32_t at, int v) {
+  asm volatile("red.relaxed.cluster.shared::cluster.min.s32 [%0], %1;" :: "r"(at), "r"(v) : "memory");
 }
 // One arrival on an mbarrier of another CTA of the cluster (its shared::cluster address),
 // with relaxed ordering: it publishes no memory writes, only that this thread's tensor-memory

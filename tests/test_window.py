@@ -206,6 +206,7 @@ def test_a_window_over_everything_is_causal_attention():
 
 @pytest.mark.gpu
 @pytest.mark.parametrize("T,lengths,window,sinks", [
+    (4097, (700, 1, 2048), 300, 4), (16384, (128,), 64, 1), (32768, (30000, 5), 1024, 130),  # in clusters
     (33000, (1000, 1, 2048), 300, 4), (150001, (100000, 333), 2000, 9), (140000, (139000,), 64, 1)])
 def test_visible_rows(T, lengths, window, sinks):
     """Every row's two intervals, every walk's records: each visible pair lies in a tile of its query
