@@ -148,7 +148,7 @@ __device__ __forceinline__ void doc_bits(const int* ids, int i0, int end, uint32
 // a running minimum, each thread taking one stretch of rows (as bits, 32 rows at a time) and the
 // block joining the stretches. Then a warp a tile: its rows (from their stretch's bits, where a stretch
 // has at most 32, so that rows are written side by side: T 16384
-// 17.3 -> 12.0 µs, with sinks 42.6 -> 16.1, half of that the lengths below being made once) and their extremes, the query tiles
+// 17.3 -> 12.0 µs on one CTA, with sinks 42.6 -> 16.1, half of that the lengths below being made once) and their extremes, the query tiles
 // that see it, and its place among the tiles by the number it has to walk (a count of the tiles before
 // it: n_t² comparisons, which at 16384 tokens are 4 a lane and tile). The
 // tiles' extremes are kept in shared memory up to kVisTiles of them. WINDOW: rows see the last
@@ -661,9 +661,9 @@ int fwd_mod(const void* q, const void* k, const void* v, void* o, float* lse, vo
   // Not with a bias (d64 T4096 204 -> 204, d128 T8192 328 -> 448) or a cap above 60, whose in-place
   // scores do not fit its registers.
   const bool plain = (mod & ~fa::kModRest) == fa::kModOn;
-  // Nor at d = 64 with a short window, whose walks are mostly edges (B1 H12 T16384, one tile -> two: window 256
-  // 54.6 -> 59.1, with four sinks 70.3 -> 76.2; 512 66.7 -> 67.3, 82.7 -> 86.1; 1024 94.6 -> 90.4, 110 -> 111;
-  // 4096 with sinks 256 -> 242; d128 H16 Hkv4 T8192 with sinks 512 87.0 -> 80.5, 1024 111 -> 99).
+  // Nor at d = 64 with a short window, whose walks are mostly edges (B1 H12 T16384, visibility and forward, one tile ->
+  // two: window 256 49.5 -> 51.7, with four sinks 61.5 -> 65.3; 512 61.5 -> 61.5, 74.1 -> 77.8; 1024 89.8 -> 84.7, 102
+  // -> 102; 4096 237 -> 211, 247 -> 233; d128 H16 Hkv4 T8192 with sinks 512 81.4 -> 76.9, 1024 105 -> 95.7).
   const bool pairs = static_cast<long long>((n_t + 1) / 2) * BH * 2 >= 3ll * sms && (plain || (mod & fa::kModRef)) &&
                      (window == 0 || d == 128 || window > 512);
   a.p.n_units = pairs ? (n_t + 1) / 2 : n_t;
@@ -713,7 +713,7 @@ int fwd_mod(const void* q, const void* k, const void* v, void* o, float* lse, vo
   const int tight = d == 64 && mod == (fa::kModOn | fa::kModCap | fa::kModRef) && (short_walks || softcap < 25.0f)
                         ? fa::kModTight : 0;
   // (a window without sinks: the two-tile kernel has its intervals; the one-tile kernel with sinks skips the
-  // columns that none of a warp's rows sees, T16384 H12 d64 window 256 58.0 -> 54.6 µs)
+  // columns that none of a warp's rows sees, T16384 H12 d64 window 256 53.4 -> 49.5 µs)
   if (window > 0 && (sinks > 0 || !pairs)) {
     const cudaError_t e = pairs ? (d == 64 ? fa::launch_fwd_sink_pairs_d64(a, mod) : fa::launch_fwd_sink_pairs_d128(a, mod))
                                 : (d == 64 ? fa::launch_fwd_sink_d64(a, mod) : fa::launch_fwd_sink_d128(a, mod));
