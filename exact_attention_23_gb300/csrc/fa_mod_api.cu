@@ -143,6 +143,39 @@ __device__ __forceinline__ void doc_bits(const int* ids, int i0, int end, uint32
   *pads = pad;
 }
 
+// The same for a warp's stretches of seg ≤ 32 rows (`base`: its first row): ids side by side, 32 a load, as words
+// of bits, of which each lane takes its stretch. (From stretches of more than 8 rows on: documents of 700 with a window and sinks,
+// a thread reading its own rows -> side by side, T 32768 25.8 -> 14.2 µs, 16384 11.4 -> 9.6, 8192 7.6 -> 7.7, 4500 6.9 -> 7.8.)
+__device__ __forceinline__ void warp_doc_bits(const int* ids, int base, int seg, int T, uint32_t* starts, uint32_t* pads) {
+  const int lane = threadIdx.x & 31;
+  uint32_t st = 0u, pad = 0u;  // lane k's: of rows base + 32k …
+  int prev = base > 0 && base < T ? ids[base - 1] : 0;
+#pragma unroll 1
+  for (int k = 0; k < seg && base + 32 * k < T; k += 8) {
+    int id[8];
+#pragma unroll
+    for (int e = 0; e < 8; ++e) id[e] = ids[min(base + 32 * (k + e) + lane, T - 1)];
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      const int i = base + 32 * (k + e) + lane;
+      int before = __shfl_up_sync(0xffffffffu, id[e], 1);
+      if (lane == 0) before = prev;
+      prev = __shfl_sync(0xffffffffu, id[e], 31);
+      const uint32_t s = __ballot_sync(0xffffffffu, i < T && (i == 0 || id[e] != before));
+      const uint32_t p = __ballot_sync(0xffffffffu, i < T && id[e] < 0);
+      if (lane == k + e && k + e < seg) {
+        st = s;
+        pad = p;
+      }
+    }
+  }
+  const int at = lane * seg, word = at >> 5, next = min(word + 1, 31);
+  const uint32_t s0 = __shfl_sync(0xffffffffu, st, word), s1 = __shfl_sync(0xffffffffu, st, next);
+  const uint32_t p0 = __shfl_sync(0xffffffffu, pad, word), p1 = __shfl_sync(0xffffffffu, pad, next);
+  *starts = __funnelshift_r(s0, s1, at & 31) & bits_below(seg);
+  *pads = __funnelshift_r(p0, p1, at & 31) & bits_below(seg);
+}
+
 // One block a sequence. A document is a maximal run of equal ids, so a row's document starts at
 // the last change of id at or before it and ends at the next one after it: a running maximum and
 // a running minimum, each thread taking one stretch of rows (as bits, 32 rows at a time) and the
@@ -203,8 +236,11 @@ __global__ void __launch_bounds__(kVisThreads) fa_visible_kernel(const VisiblePa
   const int a1 = static_cast<int>(min(static_cast<long long>(T), (tid + 1) * seg));
   uint32_t starts = 0u, pads = 0u;
   int last = -1, first = T;  // this stretch's last and first document starts
+  const bool one = seg <= 32;  // a stretch is one group of bits
+  const bool side_by_side = one && seg > 8 && ids;
+  if (side_by_side) warp_doc_bits(ids, static_cast<int>(min(static_cast<long long>(T), warp * 32 * seg)), static_cast<int>(seg), T, &starts, &pads);
   for (int g0 = a0; g0 < a1; g0 += 32) {
-    doc_bits(ids, g0, a1, &starts, &pads);
+    if (!side_by_side) doc_bits(ids, g0, a1, &starts, &pads);
     if (starts) {
       last = g0 + 31 - __clz(starts);
       if (first == T) first = g0 + __ffs(starts) - 1;
@@ -253,7 +289,6 @@ __global__ void __launch_bounds__(kVisThreads) fa_visible_kernel(const VisiblePa
     }
     return r;
   };
-  const bool one = seg <= 32;  // a stretch is one group of bits
   if (one) {
     s_four[tid] = make_int4(static_cast<int>(starts), static_cast<int>(pads), cur, end);
   } else {
@@ -597,7 +632,7 @@ int make_visible(const int* doc_ids, const int* prefix_len, int prefix_per_token
   // A cluster a sequence from 4097 to 32768 tokens, of as many CTAs as leave every cluster a place (sms SMs: pairs
   // find them all, fours 144 of 152, eights 120; 16 eights 6.8 -> 13 µs). One CTA -> eight, µs: causal T8192 7.6 ->
   // 5.3, T16384 12.5 -> 5.6, T32768 24.7 -> 7.0; a window and sinks 10.0 -> 6.3, 17.1 -> 6.8, 34.9 -> 8.8; documents of
-  // 700 9.2 -> 6.9, 17.3 -> 10.3, 41.6 -> 24.1 (which all CTAs look for).
+  // 700 (which all CTAs look for) 9.2 -> 6.9, 17.3 -> 10.3, now 8.5, 41.6 -> 24.1, now 12.5.
   unsigned ctas = 1;
   if (seg <= 32 && p.n_t > 32)
     for (const unsigned c : {2u, 4u, 8u})

@@ -130,6 +130,15 @@ def _check_window(window, sinks, most):
         raise ValueError(f"window must be below 2**31, sinks at most {most}")
 
 
+@functools.lru_cache(maxsize=256)
+def _visible_bytes(B, T, window, sinks):
+    """fa_visible_size or fa_visible_window_size, functions of their arguments alone."""
+    n = fa_visible_window_size(B, T, window, sinks) if window else fa_visible_size(B, T)
+    if n == 0:
+        raise FAError(FA_ERR_INVALID_ARG, "fa_visible_size")
+    return n
+
+
 def visible(B: int, T: int, causal: bool = True, doc_ids=None, prefix_len=None, device=None,
             buffer=None, window: int = 0, sinks: int = 0) -> Visible:
     """The visibility of a batch of B sequences of T tokens, for every layer's ``fwd_mod`` and
@@ -157,9 +166,7 @@ def visible(B: int, T: int, causal: bool = True, doc_ids=None, prefix_len=None, 
         _check_int32(doc_ids, ((B, T),), device, "doc_ids")
     if prefix_len is not None:
         _check_int32(prefix_len, ((B,), (B, T)), device, "prefix_len")
-    need = fa_visible_window_size(B, T, window, sinks) if window else fa_visible_size(B, T)
-    if need == 0:
-        raise FAError(FA_ERR_INVALID_ARG, "fa_visible_size")
+    need = _visible_bytes(B, T, window, sinks)
     if buffer is None:
         buffer = torch.empty(need, dtype=_U8, device=device)
     elif not isinstance(buffer, torch.Tensor) or buffer.dtype is not _U8 or not buffer.is_contiguous():
@@ -244,11 +251,18 @@ def bwd_mod_workspace(B: int, H: int, Hkv: int, T: int, d: int, device=None, win
                       sinks: int = 0):
     """A uint8 CUDA tensor large enough to serve as ``bwd_mod``'s workspace (with a visibility that has
     this window and these sinks)."""
+    return torch.empty(_bwd_bytes(B, H, Hkv, T, d, window, sinks), dtype=_U8,
+                       device="cuda" if device is None else device)
+
+
+@functools.lru_cache(maxsize=256)
+def _bwd_bytes(B, H, Hkv, T, d, window, sinks):
+    """fa_bwd_mod_workspace_size or fa_bwd_window_workspace_size, functions of their arguments alone."""
     n = (fa_bwd_window_workspace_size(B, H, Hkv, T, d, window, sinks) if window
          else fa_bwd_mod_workspace_size(B, H, Hkv, T, d))
     if n == 0:
         raise FAError(FA_ERR_INVALID_ARG, "fa_bwd_mod_workspace_size")
-    return torch.empty(n, dtype=_U8, device="cuda" if device is None else device)
+    return n
 
 
 def bwd_mod(q, k, v, o, lse, do, visible=None, causal: bool | None = None, softcap: float = 0.0,
