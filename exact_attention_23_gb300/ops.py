@@ -805,7 +805,8 @@ def fwd_tree4(q, cache, ctx_len, tree=None, depths=None, softcap: float = 0.0, s
     """``fwd_tree`` over a 4-bit cache, through fa_fwd_tree4: new tokens q [B, H, Tq, d] against the
     ctx_len[b] tokens of their sequence and one another, whose keys and values ``append4`` has written
     behind them. Every other argument, the window included, and the results as there; keys and values are
-    what the codes stand for (``read4``), exactly."""
+    what the codes stand for (``read4``), exactly. (More than 16 rows, H / Hkv · Tq, go in blocks of 16
+    that each read the cache.)"""
     _check(q, "q")
     device = q.device
     Bk, Hkv, Tmax, dk = _check_cache4(cache)

@@ -573,8 +573,9 @@ int fa_fwd_tree_window(const void* q, const void* k_cache, const void* v_cache, 
  * [B, Hkv, n, d]. Rows past Tmax, and all of a negative start, are zeros.
  *
  * fa_fwd_tree4 — fa_fwd_tree (window 0) or fa_fwd_tree_window over such a cache: q, o and lse and every
- * other argument as there, the keys and values being what the codes stand for, exactly. (More than 32
- * query rows a key head are taken in blocks of 32, each of which reads the cache.)
+ * other argument as there, the keys and values being what the codes stand for, exactly. (More than 16
+ * query rows a key head, H / Hkv · Tq, are taken in blocks of 16, each of which reads the cache: meant for
+ * decoding and drafts; a prompt's chunks take longer than against a cache in bf16.)
  * workspace: fa_fwd_tree4_workspace_size(...) bytes, as for fa_fwd_tree.
  * ---------------------------------------------------------------------------------------
  */
