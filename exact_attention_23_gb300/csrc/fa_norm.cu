@@ -343,7 +343,17 @@ __global__ void __launch_bounds__(kNormThreads, kNormBackPerSm) fa_norm_bwd_kern
       f2_unpack(sd, d0, d1);
       const float sum_x = row_sum<D>(s0 + s1), sum_d = row_sum<D>(d0 + d1);
       const float r = rsqrtf(fmaf(sum_x, 1.0f / D, p.eps));
-      const uint64_t r2 = f2_pack(r, r), back = f2_splat(-r * (1.0f / D) * (r * sum_d));  // (r² may overflow)
+      float along = r * sum_d;  // Σ h·w·n  (r² may overflow)
+      if (__any_sync(0xffffffffu, !(fabsf(along) < INFINITY))) {
+        // Σ h·w·x passes fp32's range, or there is a NaN: the sum from n itself. (0 where Σ x² passes it too, as n is.)
+        uint64_t sn2 = f2_pack(0.f, 0.f);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) sn2 = f2_fma(yw[e], f2_mul(x2[e], f2_splat(r)), sn2);
+        f2_unpack(sn2, d0, d1);
+        const float sum_n = row_sum<D>(d0 + d1);
+        if (!(fabsf(along) < INFINITY)) along = sum_n;
+      }
+      const uint64_t r2 = f2_pack(r, r), back = f2_splat(-r * (1.0f / D) * along);
 #pragma unroll
       for (int e = 0; e < 8; ++e) {
         acc[e] = f2_fma(y2[e], f2_mul(x2[e], r2), acc[e]);

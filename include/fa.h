@@ -462,7 +462,7 @@ int fa_rope_append(const void* q, long long q_sb, long long q_sh, long long q_st
  *   eps                : finite and > 0
  *   everything else as for fa_rope and fa_rope_append (Hkv 0: k, k_out and k_weight NULL)
  *
- * The sums are taken in fp32 (a row whose squares' mean passes its range, magnitudes of 2⁶¹ and more, is
+ * The sums are taken in fp32 (a row whose sum of squares passes its range, as at magnitudes of 2⁶¹ and more, is
  * zeros) and a result is rounded once.
  * ---------------------------------------------------------------------------------------
  */
@@ -483,6 +483,8 @@ int fa_norm_rope_append(const void* q, long long q_sb, long long q_sh, long long
  * fa_norm_rope_bwd — the gradients of fa_norm_rope, from those of its results (gq, gk; strided as its
  * inputs) and its inputs q, k: with h = g turned back,
  *   dx = (h ∘ w − n · mean(h ∘ w ∘ n)) / √(mean(x²) + eps),   dw = Σ_rows h ∘ n
+ * Rows that fa_norm_rope gives as zeros (sum of squares past fp32's range) have gradients of zeros and add nothing
+ * to dw. Every row counts in dw, padding among them: a NaN or an infinity in a row shows there even where its g is 0.
  * dq, dk: contiguous bf16 (they may be the contiguous gq, gk); dq_weight, dk_weight: DEVICE float [d],
  * written, summed in a fixed order. workspace: fa_norm_rope_bwd_workspace_size(d) bytes (0: unsupported
  * d), 256-byte aligned, contents immaterial, not shared with a call that may run at the same time.
