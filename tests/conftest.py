@@ -12,6 +12,15 @@ def pytest_configure(config):
     config.addinivalue_line("markers", "gpu: needs a CUDA GPU (sm_103a) and the built library")
 
 
+def _valid_on_a_gpu(item):
+    """Refusals that hold without a device alone, where work is shared out as for one SM: a GPU's 152 take these
+    entries whole and need no workspace, so the call would go ahead on addresses that name no memory."""
+    if getattr(item, "originalname", None) != "test_tree_refusals" or not item.nodeid.split("::")[0].endswith("test_window.py"):
+        return False
+    kw = item.callspec.params["kw"]
+    return "ws" in kw or "ws_bytes" in kw
+
+
 def pytest_collection_modifyitems(config, items):
     # A test marked gpu must never silently pass on a machine without a GPU.
     try:
@@ -20,6 +29,10 @@ def pytest_collection_modifyitems(config, items):
     except Exception:  # pragma: no cover
         has_gpu = False
     if has_gpu:
+        skip = pytest.mark.skip(reason="a valid call on a GPU, and its addresses are made up")
+        for item in items:
+            if _valid_on_a_gpu(item):
+                item.add_marker(skip)
         return
     skip = pytest.mark.skip(reason="no CUDA GPU on this machine")
     for item in items:
