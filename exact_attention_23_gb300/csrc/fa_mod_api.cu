@@ -113,6 +113,7 @@ struct VisibleParams {
 
 constexpr int kVisThreads = 1024;
 constexpr int kVisTiles = 1024;
+constexpr int kVisFew = 32;
 
 // The document starts and the paddings among 32 rows from i0 on, as bits (rows past `end`: 0).
 // Eight loads stand together, so a group costs four round trips.
@@ -188,33 +189,37 @@ __device__ __forceinline__ void warp_doc_bits(const int* ids, int base, int seg,
 // `window` keys at most; SINK: and the first `sinks` of their document (fa_visible_window).
 // Long sequences of a small batch go to a cluster of CTAs a sequence, each with every `ctas`-th tile: all find the
 // documents, and tell one another of their tiles through shared memory.
-template <bool WINDOW, bool SINK>
+// FEW: at most 32 tiles on one CTA, a warp each, without what more tiles and clusters need. (One instantiation for all ->
+// this, causal, documents of 700, and with a window and sinks: B4 T1024 4.2 -> 3.6 µs, 4.8 -> 4.3, 5.4 -> 4.8; B1 T4096 5.0
+// -> 4.3, 5.9 -> 5.3, 7.5 -> 6.9; and with the forward behind it B4 H16 Hkv4 T62 d128 11.2 -> 9.9.)
+template <bool WINDOW, bool SINK, bool FEW>
 __global__ void __launch_bounds__(kVisThreads) fa_visible_kernel(const VisibleParams p) {
+  constexpr int kTiles = FEW ? kVisFew : kVisTiles;
   __shared__ int s_last[kVisThreads / 32], s_first[kVisThreads / 32];
   __shared__ int s_pad;
-  __shared__ int2 s_span[kVisTiles], s_seen[kVisTiles];
-  __shared__ int s_far[SINK ? kVisTiles : 1];   // past the last query tile that sees a key tile's sinks, 0: none beyond a window
-  __shared__ int2 s_near[SINK ? kVisTiles : 1]; // a query tile's K tiles with sinks, before its first
+  __shared__ int2 s_span[kTiles], s_seen[kTiles];
+  __shared__ int s_far[SINK ? kTiles : 1];   // past the last query tile that sees a key tile's sinks, 0: none beyond a window
+  __shared__ int2 s_near[SINK ? kTiles : 1]; // a query tile's K tiles with sinks, before its first
   // A stretch's document starts and paddings as bits, the document it starts in and the next one's start; then
   // a tile's steps in the forward, those of a piece of its walk in the backward and the pieces, and a pair's steps.
   static_assert(kVisThreads == kVisTiles, "one array for both");
   __shared__ int4 s_four[kVisThreads];
   pdl_wait();
   pdl_launch_dependents();
-  const int ctas = static_cast<int>(cluster_ctas()), rank = static_cast<int>(cluster_ctarank());
-  const int b = static_cast<int>(cluster_id()), tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int ctas = FEW ? 1 : static_cast<int>(cluster_ctas()), rank = FEW ? 0 : static_cast<int>(cluster_ctarank());
+  const int b = static_cast<int>(FEW ? blockIdx.x : cluster_id()), tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int step = ctas * (kVisThreads / 32), tile0 = rank + ctas * warp;  // a warp's tiles
   const int T = p.T, n_t = p.n_t;
   const long long T_pad = static_cast<long long>(n_t) * 128;
   const int* ids = p.ids ? p.ids + static_cast<size_t>(b) * T : nullptr;
   int2* rows = p.rows + static_cast<size_t>(b) * T_pad;
-  int2* span = n_t <= kVisTiles ? s_span : p.span + static_cast<size_t>(b) * n_t;
-  int2* seen = n_t <= kVisTiles ? s_seen : p.seen + static_cast<size_t>(b) * n_t;
+  int2* span = FEW || n_t <= kVisTiles ? s_span : p.span + static_cast<size_t>(b) * n_t;
+  int2* seen = FEW || n_t <= kVisTiles ? s_seen : p.seen + static_cast<size_t>(b) * n_t;
   int* far = nullptr;
   int2 *near = nullptr, *sink_rows = nullptr;
   if constexpr (SINK) {
-    far = n_t <= kVisTiles ? s_far : p.far + static_cast<size_t>(b) * n_t;
-    near = n_t <= kVisTiles ? s_near : p.near + static_cast<size_t>(b) * n_t;
+    far = FEW || n_t <= kVisTiles ? s_far : p.far + static_cast<size_t>(b) * n_t;
+    near = FEW || n_t <= kVisTiles ? s_near : p.near + static_cast<size_t>(b) * n_t;
     sink_rows = p.sink_rows + static_cast<size_t>(b) * T_pad;
     for (int t = rank + ctas * tid; t < n_t; t += ctas * kVisThreads) far[t] = 0;
   }
@@ -236,8 +241,8 @@ __global__ void __launch_bounds__(kVisThreads) fa_visible_kernel(const VisiblePa
   const int a1 = static_cast<int>(min(static_cast<long long>(T), (tid + 1) * seg));
   uint32_t starts = 0u, pads = 0u;
   int last = -1, first = T;  // this stretch's last and first document starts
-  const bool one = seg <= 32;  // a stretch is one group of bits
-  const bool side_by_side = one && seg > 8 && ids;
+  const bool one = FEW || seg <= 32;  // a stretch is one group of bits
+  const bool side_by_side = !FEW && one && seg > 8 && ids;
   if (side_by_side) warp_doc_bits(ids, static_cast<int>(min(static_cast<long long>(T), warp * 32 * seg)), static_cast<int>(seg), T, &starts, &pads);
   for (int g0 = a0; g0 < a1; g0 += 32) {
     if (!side_by_side) doc_bits(ids, g0, a1, &starts, &pads);
@@ -436,7 +441,7 @@ __global__ void __launch_bounds__(kVisThreads) fa_visible_kernel(const VisiblePa
     }
     return x;
   };
-  const bool kept = n_t > 32 && n_t <= kVisTiles;  // (few: made where they are looked at, one a lane)
+  const bool kept = !FEW && n_t > kVisFew && n_t <= kVisTiles;  // (few: made where they are looked at, one a lane)
   if (kept) {
     const int t = rank + ctas * tid;
     if (t < n_t) {
@@ -609,11 +614,12 @@ int make_visible(const int* doc_ids, const int* prefix_len, int prefix_per_token
   p.whole = reinterpret_cast<int2*>(base + l.whole);
   p.span = reinterpret_cast<int2*>(base + l.span);
   p.seen = reinterpret_cast<int2*>(base + l.seen);
-  auto* fn = &fa::fa_visible_kernel<false, false>;
+  const bool few = p.n_t <= fa::kVisFew;
+  auto* fn = few ? &fa::fa_visible_kernel<false, false, true> : &fa::fa_visible_kernel<false, false, false>;
   if (window > 0) {
     p.window = window;
     p.sinks = sinks;
-    fn = &fa::fa_visible_kernel<true, false>;
+    fn = few ? &fa::fa_visible_kernel<true, false, true> : &fa::fa_visible_kernel<true, false, false>;
     if (sinks > 0) {
       const fa::WindowLayout wl = fa::window_layout(B, T, window, sinks);
       p.piece = wl.piece;
@@ -626,7 +632,7 @@ int make_visible(const int* doc_ids, const int* prefix_len, int prefix_per_token
       p.cuts = reinterpret_cast<int4*>(base + wl.cuts);
       p.far = reinterpret_cast<int*>(base + wl.far);
       p.near = reinterpret_cast<int2*>(base + wl.near);
-      fn = &fa::fa_visible_kernel<true, true>;
+      fn = few ? &fa::fa_visible_kernel<true, true, true> : &fa::fa_visible_kernel<true, true, false>;
     }
   }
   // A cluster a sequence from 4097 to 32768 tokens, of as many CTAs as leave every cluster a place (sms SMs: pairs
@@ -634,7 +640,7 @@ int make_visible(const int* doc_ids, const int* prefix_len, int prefix_per_token
   // 5.3, T16384 12.5 -> 5.6, T32768 24.7 -> 7.0; a window and sinks 10.0 -> 6.3, 17.1 -> 6.8, 34.9 -> 8.8; documents of
   // 700 (which all CTAs look for) 9.2 -> 6.9, 17.3 -> 10.3, now 8.5, 41.6 -> 24.1, now 12.5.
   unsigned ctas = 1;
-  if (seg <= 32 && p.n_t > 32)
+  if (seg <= 32 && !few)
     for (const unsigned c : {2u, 4u, 8u})
       if (B <= sms * (c == 2 ? 16 : c == 4 ? 15 : 12) / 16 / static_cast<int>(c)) ctas = c;
   const cudaError_t e = fa::launch_pdl_clusters(fn, static_cast<unsigned>(B) * ctas, ctas, fa::kVisThreads, 0,
