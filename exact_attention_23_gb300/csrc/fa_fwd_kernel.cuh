@@ -143,10 +143,10 @@ struct ModParams {
   TreeList list;        // TREE: new tokens against a cache (fa_tree_walk.cuh); T above is then R,
   TreeMask mask;        //   BH counts key heads, and o_part, lse_part are [slots][128][D], [slots][128]
   TreeReach reach;      // SINK with TREE
-  const int2* sink_rows;   // SINK: [B][T_pad] a row's visible sinks, an interval in front of its rows entry (these
-                           //   three null: a window without sinks)
+  const int2* sink_rows;   // SINK: [B][T_pad] a row's visible sinks, an interval in front of its rows entry (this and the
+                           //   next null: a window without sinks, which the one-tile kernel takes too)
   const int2* sink_units;  // SINK: [B][n_t] the sinks' K tiles of each of `units`, all before its first
-  const int4* sink_pairs;  // SINK: [B][ceil(n_t/2)] the same of both tiles of each of `pairs`
+  const int4* sink_pairs;  // SINK, two tiles: [B][ceil(n_t/2)] the same of both tiles of each of `pairs`
 };
 
 struct FwdParams {
@@ -266,7 +266,7 @@ __device__ __forceinline__ Unit pair_unit_of(const FwdParams& p, int L) {
     u.lo[1] = r1.x;
     u.last[1] = r1.y;
     if constexpr (SINK) {
-      const int4 k = p.mod.sink_pairs ? __ldg(p.mod.sink_pairs + static_cast<size_t>(b) * p.n_units + pos) : make_int4(0, 0, 0, 0);
+      const int4 k = __ldg(p.mod.sink_pairs + static_cast<size_t>(b) * p.n_units + pos);
       u.sb[0] = k.x;
       u.se[0] = k.y;
       u.sb[1] = k.z;
@@ -948,7 +948,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           vlo = r.x;
           vhi = r.y;
           if constexpr (kSink) {
-            const int2 k = p.mod.sink_rows ? __ldg(p.mod.sink_rows + static_cast<size_t>(b) * p.mod.T_pad + q_row) : make_int2(0, 0);
+            const int2 k = __ldg(p.mod.sink_rows + static_cast<size_t>(b) * p.mod.T_pad + q_row);
             slo = k.x;
             shi = k.y;
           }

@@ -65,6 +65,9 @@ struct WindowLayout {
 };
 
 constexpr int kMaxSinks = 1024;
+constexpr int kVisThreads = 1024;
+constexpr int kVisTiles = 1024;  // whose extremes a CTA keeps in shared memory
+constexpr int kVisFew = 32;
 
 static WindowLayout window_layout(int B, int T, int window, int sinks) {
   auto up = [](size_t x) { return (x + 255u) / 256u * 256u; };
@@ -91,8 +94,9 @@ static WindowLayout window_layout(int B, int T, int window, int sinks) {
   l.pieces = l.sink_pairs + up(b * ((n_t + 1) / 2) * 16);
   l.cuts = l.pieces + up(b * l.n_rec * 32);
   l.far = l.cuts + up(b * l.n_cut * 16);
-  l.near = l.far + up(b * n_t * 4);
-  l.bytes = l.near + up(b * n_t * 8);
+  const size_t apart = n_t > kVisTiles ? b * n_t : 0;
+  l.near = l.far + up(apart * 4);
+  l.bytes = l.near + up(apart * 8);
   return l;
 }
 
@@ -111,9 +115,6 @@ struct VisibleParams {
   int* far;
 };
 
-constexpr int kVisThreads = 1024;
-constexpr int kVisTiles = 1024;
-constexpr int kVisFew = 32;
 
 // The document starts and the paddings among 32 rows from i0 on, as bits (rows past `end`: 0).
 // Eight loads stand together, so a group costs four round trips.
