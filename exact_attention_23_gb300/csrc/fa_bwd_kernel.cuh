@@ -40,6 +40,9 @@
 // and a single issuer blocked on one barrier would hold back independent work: the score
 // issuer starts Sᵀ of the next tile as soon as the compute warps have read the current
 // one into registers, while the gradient issuer is still waiting for this tile's Pᵀ/dSᵀ.
+// Pᵀ and dSᵀ are rounded to bf16, as operands beside dO, Q and K must be; P and dP − D are fp32 until then (windows of
+// 200 on documents, d = 64: dq, dk, dv off by 2.40e-3, 2.37e-3 and 2.28e-3 of their norms, where 64 bits with these two
+// roundings and the results' are by 2.36e-3, 2.34e-3 and 2.28e-3, and with the results' alone by 1.65e-3).
 // Pᵀ goes to tensor memory (bf16 pairs, the A operand of the dV MMA). dSᵀ is written to
 // shared memory as bf16 in the 128-byte-swizzled layout a TMA load would produce
 // ([key row][64 query columns] boxes, double-buffered). The same bytes serve as the

@@ -1157,7 +1157,7 @@ __global__ void __launch_bounds__(Cfg1<D, (MOD & kModRef) != 0>::kThreads, 1)
         }
         FA1_TRACE(40, j);
 
-        // p = 2^(s·c − m_ref) on fp32 pairs; row sum in fp32; P kept as bf16 pairs. (A row
+        // p = 2^(s·c − m_ref) on fp32 pairs; row sum in fp32; P as bf16 pairs, an operand beside V. (A row
         // whose keys so far are all masked — the general form, or a half at the causal
         // diagonal — has m_ref = −∞ and all its p are 0.)
         const uint64_t c2 = f2_pack(c, c);

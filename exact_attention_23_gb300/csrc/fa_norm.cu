@@ -14,8 +14,10 @@
 // of a row exchange its sums in 2 or 3 shuffles, and nothing but the rows goes through memory: 4
 // bytes an element forward, 6 backward.
 //
-// What bounds them: on long batches the rows' way from memory, forward B4 H12+12 T16384 d64 (403 MB)
-// 81.8 µs, 4.9 TB/s, backward B1 H16+4 T16384 d128 (252 MB) 50.2 µs, 5.0 TB/s (copying: 6.8); on short ones the launch and one
+// What bounds them: on long batches the rows' way from memory and the wait in its middle, the lanes' sum and a root between
+// a row's loads and its stores: forward B4 H12+12 T16384 d64 (403 MB) 81.2 µs, B1 H16+4 T16384 d128 (168 MB) 34.7, 4.8 to 5.0
+// TB/s, where fa_rope.cu, without a sum, moves the same bytes in 67.4 and 29.6 (copying: 6.8 TB/s), and more heads in flight
+// cost blocks an SM (below); backward that size (252 MB) 50.1 µs, 5.0 TB/s. On short ones the launch and one
 // wave's latency, B4 H12+12 T1024 d64 7.0 µs, one token 2.5. Arithmetic is on pairs of neighbouring
 // dimensions (fp32x2), weights lie in shared memory in the order that lanes read them in, and rows are
 // numbered with 32 bits, whose divisions are multiplications (backward 65 -> 51 µs).

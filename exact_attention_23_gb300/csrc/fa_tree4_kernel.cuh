@@ -13,7 +13,11 @@
 // operands left unmade: shifts, masks and multiply-adds are what it spends on top of streaming); B4 12 heads,
 // 8 drafts, to 4000, d64 10.6 (in clusters of eight CTAs; 13.5 in stretches). With the query rows on the 16 side and 16 of them always: 36.4 and 17.4.
 // Three CTAs an SM, four at d = 64, and four tiles a ring for 8 rows (16384 keys to 60000: three 24.0 and 56.1, two
-// 23.5 and 59.2); two CTAs for 16, whose registers spill otherwise.
+// 23.5 and 59.2); two CTAs for 16. Five warps a CTA put three of two CTAs' ten on one quarter of the SM, so these have 168
+// registers a thread, and at d = 128 spill 280 to 312 bytes all the same (at d = 64 up to 20).
+//
+// P is rounded to bf16, as an operand beside V's values must be, and l sums it before that: o is off by 2.3e-3 of its norm
+// where its own rounding is 1.69e-3 (64 bits with P so rounded: 2.3e-3 too).
 //
 // A CTA's four compute warps take 32 keys each of a chunk of 128, with a running maximum, sum and O of
 // their own, behind a producer warp that copies the chunk's codes and scales, two contiguous pieces each

@@ -392,7 +392,8 @@ __global__ void __launch_bounds__(kTreeBlock, TreeCfg<D>::kCtasPerSm)
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
           const float p0 = ex2_approx(s[j][2 * i] - mu[i]), p1 = ex2_approx(s[j][2 * i + 1] - mu[i]);
-          l[i] += p0 + p1;
+          l[i] += p0 + p1;  // (in fp32; P goes on in bf16, as an operand beside V must: o is off by 2.3e-3 of its norm,
+                            // as 64 bits with P so rounded are; o's own rounding is 1.66e-3)
           pf[j / 2][(j & 1) * 2 + i] = pack_bf16x2(p0, p1);
         }
       }
