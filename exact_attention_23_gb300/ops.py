@@ -620,7 +620,8 @@ def norm_rope_bwd(gq, gk, q, k, q_weight, k_weight, inv_freq, positions=None, in
     """Gradients of ``norm_rope`` through fa_norm_rope_bwd, from those of its results, ``gq`` and
     ``gk`` (as ``bwd_mod`` returns them; any strides), and its inputs; the other arguments as there.
     Returns (dq, dk, dq_weight, dk_weight): contiguous rows in bf16 and float32 [d] sums over all rows
-    (added in a fixed order: the same bits every time). gk, k and k_weight may be None together.
+    (added in a fixed order: the same bits every time; every row counts, so those of padding must hold
+    numbers). gk, k and k_weight may be None together.
     ``dq``/``dk`` may be the (contiguous) ``gq``/``gk``; ``workspace``: see ``norm_rope_bwd_workspace``.
     """
     _check_four(q, "q", "H")
